@@ -299,6 +299,90 @@ tpmlp_status tpmlp_attn_backward(const tpmlp_attn_shape *shape, const void *dZ, 
                                  void *dX, void *dWqkv, void *dbqkv, void *dWo, void *dbo, void *workspace,
                                  void *stream);
 
+/* ---- vocabulary cross entropy: the language-model head's loss -----------------
+ * Logits S = X W^T of T tokens against the V rows of the embedding W[V,h] (rows of
+ * h, the layout of an embedding table; its row blocks are the vocabulary shards),
+ * never stored as a whole:
+ *   lse_i = log sum_v exp S_iv,   loss_i = lse_i - S_{i, target_i}   per token;
+ * backward, for the gradients dloss_i of the per-token losses (1/T each for their
+ * mean):
+ *   dS = (exp(S - lse) - onehot(target)) * dloss,   dX = dS W,   dW = dS^T X.
+ * The forward pass keeps one (maximum, sum of exponentials) pair per token and 128
+ * vocabulary rows, in fp32, and joins them in a fixed order; the backward pass
+ * recomputes the logits of one piece of the vocabulary at a time and holds that
+ * piece's dS. */
+typedef struct {
+    int64_t tokens;       /* T >= 0 */
+    int64_t hidden;       /* h > 0 */
+    int64_t vocab;        /* V > 0, any number */
+    int64_t ignore_index; /* a token with this target has loss 0 and no gradient */
+    int64_t piece;        /* vocabulary rows per piece, a multiple of 8; 0: the library's choice */
+    int32_t dtype;        /* tpmlp_dtype of X, W, dX, dW */
+    int32_t algo;         /* tpmlp_algo */
+} tpmlp_xent_shape;
+
+/* Bytes of device workspace of both passes: status word, statistics (8 bytes per
+ * token and 128 vocabulary rows), dS of one piece (T * piece elements; FFMA path also
+ * its fp32 logits) and, for bf16 and several pieces, dX in fp32.  256-byte aligned,
+ * first 8 bytes zero before first use; 0 for an invalid shape. */
+size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
+
+/* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
+ * written for every token, ignored ones too.  bf16 runs on the tensor cores with
+ * fp32 accumulation and statistics; the logits are not rounded.  A logit of NaN or
+ * +inf makes its token's loss and lse non-finite, no other token's.  A target that
+ * is neither ignore_index nor in [0, V) is reported as TPMLP_ERR_INVALID_ARG in the
+ * status word (detail: the token) and treated as ignored.
+ * Errors: INVALID_ARG for a bad shape or a NULL pointer (token arrays may be NULL
+ * with T = 0); UNSUPPORTED for bf16 with h not a multiple of 8 or X or W not on 16
+ * bytes, and beyond 65535 * 64 tokens or vocabulary rows on the FFMA path; CUDA when
+ * a launch fails. */
+tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
+                                float *loss, float *lse, void *workspace, void *stream);
+
+/* Backward: dX[T,h] and dW[V,h] from the forward pass's inputs and lse, and dloss[T]
+ * (fp32).  Either output may be NULL and is then not computed (a frozen head, a
+ * frozen body).  dS is rounded to the shape's dtype before the two products; dX is
+ * summed over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
+ * Results are bit-identical from call to call.  Errors as the forward. */
+tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
+                                 const float *lse, const float *dloss, void *dX, void *dW, void *workspace,
+                                 void *stream);
+
+/* ---- orthogonalised updates ------------------------------------------------------
+ * Newton-Schulz orthogonalisation of gradient (or momentum) matrices G[batch][rows]
+ * [cols], each by itself:
+ *   X = G / (|G|_F + eps);   `steps` times:  A = X X^T,  X <- a X + (b A + c A^2) X
+ * (for rows > cols the same on the transpose, without transposing).  Each step maps
+ * every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.
+ * The output is bf16.
+ * Precision: the products' operands are fp16 (11 bits) with fp32 accumulation; X
+ * itself is carried as a sum of two fp16 numbers (about 22 bits), so that the
+ * directions of small singular values, which only the term a X moves, keep their
+ * precision whatever the matrix's condition.  The norm is exact to fp32 over the
+ * whole range of the input's type. */
+typedef struct {
+    int64_t batch; /* matrices, 0..65535 */
+    int64_t rows, cols; /* > 0, any number up to 2^20 */
+    int32_t steps; /* 1..32 */
+    int32_t dtype; /* tpmlp_dtype of G */
+    float a, b, c; /* the step's polynomial; its iterates must stay below 1.9 in norm */
+    float eps;     /* >= 0 */
+} tpmlp_ortho_shape;
+
+/* Bytes of device workspace (status word, block sums, two copies of X in 4 bytes per
+ * element, A and C in fp16, sizes rounded up to 64); 256-byte aligned, first 8 bytes
+ * zero before first use; 0 for an invalid shape. */
+size_t tpmlp_ortho_workspace_bytes(const tpmlp_ortho_shape *shape);
+
+/* O[batch][rows][cols] (bf16) from G (contiguous, of shape->dtype).  A zero matrix
+ * gives zeros; a matrix with NaN or infinity gives non-finite values in its own
+ * output only.  Errors: INVALID_ARG for a bad shape or NULL pointer; UNSUPPORTED
+ * where O is not on 16 bytes although cols is a multiple of 8, or the coefficients
+ * let the iterates grow past what the fp16 products hold; CUDA when a launch fails. */
+tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *shape, const void *G, void *O, void *workspace,
+                                 void *stream);
+
 /* Synchronises the stream, reads the workspace status word, clears it and
  * returns it (TPMLP_OK when no device-side error was recorded). */
 tpmlp_status tpmlp_check_device_status(void *workspace, void *stream);

@@ -3,6 +3,7 @@
 // device status word and per-kernel timing.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -1064,6 +1065,455 @@ tpmlp_status tpmlp_attn_backward(const tpmlp_attn_shape *s, const void *dZ, cons
     g8.out0 = dX;
     pick_raster(g8);
     e = gemm(&ms, "attn_bwd_dX_shard_fold", tpmlp::EPI_FOLD, g8, sms, st);
+    return from_cuda(e);
+}
+
+}  // extern "C"
+
+// ---- vocabulary cross entropy -------------------------------------------------------
+
+namespace {
+
+bool xent_valid(const tpmlp_xent_shape *s) {
+    if (!s) return false;
+    if (s->tokens < 0 || s->hidden <= 0 || s->vocab <= 0 || s->piece < 0) return false;
+    if (s->dtype != TPMLP_F32 && s->dtype != TPMLP_BF16) return false;
+    if (s->algo != TPMLP_ALGO_DEFAULT && s->algo != TPMLP_ALGO_SIMT) return false;
+    if (s->piece % 8 != 0) return false;
+    if (s->tokens > (1LL << 30) || s->hidden > (1LL << 30) || s->vocab > (1LL << 30)) return false;
+    const int64_t T = s->tokens, h = s->hidden, V = s->vocab;
+    return tiles_fit(T, V) && tiles_fit(T, h) && tiles_fit(V + 256, h);
+}
+
+bool xent_tc(const tpmlp_xent_shape *s) { return s->dtype == TPMLP_BF16 && s->algo == TPMLP_ALGO_DEFAULT; }
+
+// Vocabulary rows per piece.  The backward pass holds one piece of dS [T, piece] (and the
+// FFMA path its fp32 logits).  Each further piece costs one more addition to the fp32
+// dX [T, h], so pieces are as large as 256 MiB allow, equal in size, in whole wide
+// tiles (512 columns).
+int64_t xent_piece(const tpmlp_xent_shape *s) {
+    const int64_t V = s->vocab, T = s->tokens < 1 ? 1 : s->tokens;
+    if (s->piece > 0) return s->piece < V ? s->piece : (V + 7) / 8 * 8;
+    const int64_t esz = xent_tc(s) ? 2 : 4;
+    int64_t most = (int64_t{256} << 20) / (T * esz) / 512 * 512;
+    if (most < 2048) most = 2048;
+    const int64_t n = (V + most - 1) / most;
+    const int64_t even = ((V + n - 1) / n + 511) / 512 * 512;
+    return even < V ? even : (V + 7) / 8 * 8;
+}
+
+struct XentLayout {
+    int64_t piece, pieces, groups;
+    size_t part, target_logit, row_g, ds, logits, acc, total;
+};
+
+// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | g per
+// token | dS of one piece | fp32 logits of one piece (FFMA path, bf16) | fp32 dX.
+XentLayout xent_layout(const tpmlp_xent_shape *s) {
+    XentLayout L;
+    const size_t T = static_cast<size_t>(s->tokens), h = static_cast<size_t>(s->hidden);
+    const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
+    L.piece = xent_piece(s);
+    L.pieces = (s->vocab + L.piece - 1) / L.piece;
+    L.groups = tc ? (s->vocab + tpmlp::XENT_GROUP - 1) / tpmlp::XENT_GROUP : L.pieces;
+    size_t off = STATUS_BYTES;
+    auto region = [&](size_t bytes) {
+        const size_t at = off;
+        off += align_up(bytes, 1024);
+        return at;
+    };
+    const size_t groups_stored = static_cast<size_t>(tc ? tpmlp::xent_groups(s->vocab) : L.pieces);
+    L.part = region(groups_stored * T * sizeof(float2));
+    L.target_logit = region(T * 4);
+    L.row_g = region(T * 4);
+    L.ds = region(T * static_cast<size_t>(L.piece) * (f32 ? 4 : 2));
+    // in fp32 dS takes the place of the logits
+    L.logits = f32 ? L.ds : region(tc ? 0 : T * static_cast<size_t>(L.piece) * 4);
+    L.acc = region(!f32 && L.pieces > 1 ? T * h * 4 : 0);
+    L.total = off;
+    return L;
+}
+
+tpmlp_status xent_check(const tpmlp_xent_shape *s, const char *who, std::initializer_list<const void *> token_ptrs,
+                        std::initializer_list<const void *> matrices, std::initializer_list<const void *> rows,
+                        const void *workspace) {
+    if (!xent_valid(s)) {
+        tpmlp::set_last_error("%s: invalid shape", who);
+        return TPMLP_ERR_INVALID_ARG;
+    }
+    bool null = !workspace;
+    for (const void *p : token_ptrs) null = null || (!p && s->tokens > 0);
+    for (const void *p : rows) null = null || (!p && s->tokens > 0);
+    if (null) {
+        tpmlp::set_last_error("%s: NULL pointer", who);
+        return TPMLP_ERR_INVALID_ARG;
+    }
+    // bf16: TMA bases and row pitches on 16 bytes; fp32: elements
+    const size_t al = s->dtype == TPMLP_BF16 ? 16 : 4;
+    bool bad = !aligned16(workspace) || (s->dtype == TPMLP_BF16 && s->hidden % 8 != 0);
+    for (const void *p : matrices) bad = bad || (p && !aligned_elt(p, al));
+    for (const void *p : rows) bad = bad || (p && !aligned_elt(p, 4));
+    if (bad) {
+        tpmlp::set_last_error("%s: bf16 needs h a multiple of 8 and 16-byte aligned matrices, the workspace 16 bytes",
+                              who);
+        return TPMLP_ERR_UNSUPPORTED;
+    }
+    if (!xent_tc(s) && (s->tokens > 65535LL * 64 || s->vocab > 65535LL * 64)) {
+        tpmlp::set_last_error("%s: the FFMA path takes at most 65535 * 64 tokens and vocabulary rows", who);
+        return TPMLP_ERR_UNSUPPORTED;
+    }
+    return TPMLP_OK;
+}
+
+// SMs of the current device, or the error to return.
+tpmlp_status device_ready(int &sms) {
+    sms = num_sms_current();
+    return sms == 0 ? TPMLP_ERR_CUDA : (sms < 0 ? TPMLP_ERR_DEVICE : TPMLP_OK);
+}
+
+struct XentCall {
+    const tpmlp_xent_shape *s;
+    XentLayout L;
+    uint8_t *ws;
+    int sms;
+    cudaStream_t st;
+    tpmlp::RowArgs rows;
+    XentCall(const tpmlp_xent_shape *s_, const int64_t *target, void *workspace, int sms_, void *stream)
+        : s(s_), L(xent_layout(s_)), ws(static_cast<uint8_t *>(workspace)), sms(sms_),
+          st(static_cast<cudaStream_t>(stream)) {
+        rows.tokens = s->tokens, rows.vocab = s->vocab, rows.ignore_index = s->ignore_index;
+        rows.target = target;
+        rows.part = reinterpret_cast<float2 *>(ws + L.part);
+        rows.groups = L.groups;
+        rows.target_logit = reinterpret_cast<float *>(ws + L.target_logit);
+        rows.status = reinterpret_cast<uint32_t *>(ws);
+    }
+    size_t esz() const { return s->dtype == TPMLP_BF16 ? 2 : 4; }
+    const void *w_rows(const void *W, int64_t v0) const {
+        return static_cast<const uint8_t *>(W) + static_cast<size_t>(v0) * s->hidden * esz();
+    }
+    // X W_p^T over vocabulary rows v0 .. v0 + n - 1.
+    GemmArgs logits(const void *X, const void *W, int64_t v0, int64_t n) const {
+        GemmArgs g = base_args(rows.status);
+        g.a = X, g.a_mn = false;
+        g.b = w_rows(W, v0), g.b_mn = false;
+        g.M = s->tokens, g.N = n, g.K = s->hidden, g.kshard = s->hidden;
+        g.target = rows.target, g.ignore_index = s->ignore_index, g.col0 = v0;
+        return g;
+    }
+    cudaError_t launch(const char *name, Epi epi, GemmArgs &g) const {
+        const bool tc = xent_tc(s);
+        if (tc) pick_raster(g, epi);
+        Timed timed(name, st);
+        const cudaError_t e = tc ? tpmlp::launch_tc_gemm(epi, g, sms, st)
+                                 : tpmlp::launch_simt_gemm(epi, s->dtype == TPMLP_BF16, g, st);
+        if (e == cudaSuccess) g_launches.fetch_add(1);
+        return e;
+    }
+    template <typename F>
+    cudaError_t kernel(const char *name, F f) const {
+        Timed timed(name, st);
+        const cudaError_t e = f();
+        if (e == cudaSuccess) g_launches.fetch_add(1);
+        return e;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *s) { return xent_valid(s) ? xent_layout(s).total : 0; }
+
+tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const void *W, const int64_t *target,
+                                float *loss, float *lse, void *workspace, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    tpmlp_status rc = xent_check(s, "tpmlp_xent_forward", {X}, {X, W}, {loss, lse}, workspace);
+    if (rc != TPMLP_OK) return rc;
+    if (!W || (!target && s->tokens > 0)) return invalid("tpmlp_xent_forward: NULL pointer");
+    if (!aligned_elt(target, 8)) return TPMLP_ERR_UNSUPPORTED;
+    if (s->tokens == 0) return TPMLP_OK;
+    int sms;
+    if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
+    const XentCall c(s, target, workspace, sms, stream);
+    cudaError_t e;
+    if (xent_tc(s)) {
+        GemmArgs g = c.logits(X, W, 0, s->vocab);
+        g.part = reinterpret_cast<float2 *>(c.ws + c.L.part);
+        g.target_logit = c.rows.target_logit;
+        e = c.launch("xent_stats", tpmlp::EPI_XENT_STATS, g);
+        if (e != cudaSuccess) return from_cuda(e);
+    } else {
+        float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
+        for (int64_t k = 0; k < c.L.pieces; ++k) {
+            const int64_t v0 = k * c.L.piece, n = std::min(c.L.piece, s->vocab - v0);
+            GemmArgs g = c.logits(X, W, v0, n);
+            g.out0 = logits;
+            e = c.launch("xent_logits", tpmlp::EPI_ACC32, g);
+            if (e != cudaSuccess) return from_cuda(e);
+            float2 *part = reinterpret_cast<float2 *>(c.ws + c.L.part) + k * s->tokens;
+            e = c.kernel("xent_piece_stats",
+                         [&] { return tpmlp::launch_xent_piece_stats(c.rows, logits, n, v0, part, c.st); });
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+    }
+    return from_cuda(c.kernel("xent_combine", [&] { return tpmlp::launch_xent_combine(c.rows, loss, lse, c.st); }));
+}
+
+tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const void *W, const int64_t *target,
+                                 const float *lse, const float *dloss, void *dX, void *dW, void *workspace,
+                                 void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    tpmlp_status rc = xent_check(s, "tpmlp_xent_backward", {X}, {X, W, dX, dW}, {lse, dloss}, workspace);
+    if (rc != TPMLP_OK) return rc;
+    if (!W || (!target && s->tokens > 0)) return invalid("tpmlp_xent_backward: NULL pointer");
+    if (!aligned_elt(target, 8)) return TPMLP_ERR_UNSUPPORTED;
+    if (!dX && !dW) return TPMLP_OK;
+    int sms;
+    if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
+    cudaError_t e;
+    if (s->tokens == 0) {
+        if (!dW) return TPMLP_OK;
+        const size_t bytes = static_cast<size_t>(s->vocab) * s->hidden * (s->dtype == TPMLP_BF16 ? 2 : 4);
+        return from_cuda(cudaMemsetAsync(dW, 0, bytes, static_cast<cudaStream_t>(stream)));
+    }
+    const XentCall c(s, target, workspace, sms, stream);
+    const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
+    float *row_g = reinterpret_cast<float *>(c.ws + c.L.row_g);
+    e = c.kernel("xent_row_g", [&] { return tpmlp::launch_xent_row_g(c.rows, dloss, row_g, c.st); });
+    if (e != cudaSuccess) return from_cuda(e);
+    void *ds = c.ws + c.L.ds;
+    // dX is summed over the pieces in fp32: in place for fp32, in the workspace for
+    // bf16, and not at all when one piece holds the whole vocabulary.
+    float *acc = f32 ? static_cast<float *>(dX) : reinterpret_cast<float *>(c.ws + c.L.acc);
+    const bool direct = !f32 && c.L.pieces == 1;
+    for (int64_t k = 0; k < c.L.pieces; ++k) {
+        const int64_t v0 = k * c.L.piece, n = std::min(c.L.piece, s->vocab - v0);
+        GemmArgs g = c.logits(X, W, v0, n);
+        int64_t ld = n;  // row pitch of dS
+        if (tc) {
+            ld = c.L.piece;
+            g.out0 = ds, g.ldo = ld;
+            g.row_lse = lse, g.row_g = row_g;
+            e = c.launch("xent_ds", tpmlp::EPI_XENT_GRAD, g);
+        } else {
+            float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
+            g.out0 = logits;
+            e = c.launch("xent_logits", tpmlp::EPI_ACC32, g);
+            if (e == cudaSuccess)
+                e = c.kernel("xent_piece_grad", [&] {
+                    return tpmlp::launch_xent_piece_grad(!f32, c.rows, logits, n, v0, lse, row_g, ds, c.st);
+                });
+        }
+        if (e != cudaSuccess) return from_cuda(e);
+        if (dW) {  // rows v0 .. of dW = dS_p^T X
+            GemmArgs w = base_args(c.rows.status);
+            w.a = ds, w.a_mn = true, w.lda = ld;
+            w.b = X, w.b_mn = true;
+            w.M = n, w.N = s->hidden, w.K = s->tokens, w.kshard = s->tokens;
+            w.out0 = const_cast<void *>(c.w_rows(dW, v0));
+            e = c.launch("xent_dw", tpmlp::EPI_STORE, w);
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+        if (dX) {  // dX (+)= dS_p W_p
+            GemmArgs x = base_args(c.rows.status);
+            x.a = ds, x.a_mn = false, x.lda = ld;
+            x.b = c.w_rows(W, v0), x.b_mn = true;
+            x.M = s->tokens, x.N = s->hidden, x.K = n, x.kshard = n;
+            x.out0 = direct ? dX : static_cast<void *>(acc);
+            x.accumulate = k > 0;
+            e = c.launch("xent_dx", direct ? tpmlp::EPI_STORE : tpmlp::EPI_ACC32, x);
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+    }
+    if (dX && !direct && !f32)
+        e = c.kernel("xent_dx_round",
+                     [&] { return tpmlp::launch_to_bf16(acc, dX, s->tokens * s->hidden, c.st); });
+    return from_cuda(e);
+}
+
+}  // extern "C"
+
+// ---- Newton-Schulz orthogonalisation ------------------------------------------------
+
+namespace {
+
+// Powers of two that the fp16 iterates are stored with, so that both their largest
+// values (|X| < 2, |A| < 3.6, |C| < 7.5, see ortho_range_ok) and the small entries of
+// a large matrix's first step (about 1/(p sqrt(p)) off A's diagonal) are normal
+// fp16 numbers.
+constexpr float kScaleX = 8192.0f, kScaleA = 16384.0f, kScaleC = 8192.0f;
+
+// X' = aX + CX with C = bA + cA^2 is computed as (a - d) X + (C + dI) X: near the end A is
+// close to I and C to (b + c) I, about -2.7, so that d = 2 leaves C + dI small and its
+// rounding with it.  d is the power of two next to a/2.
+float ortho_shift(float a) { return a > 0.0f ? std::exp2(std::round(std::log2(0.5f * a))) : 0.0f; }
+
+// Follows the largest singular value through the steps: starting from the interval
+// [0, 1] (the Frobenius norm bounds it), the image of [0, r] under s -> a s + b s^3 +
+// c s^5 is sampled; every iterate must stay inside the fp16 scales above.
+bool ortho_range_ok(const tpmlp_ortho_shape *s) {
+    const double a = s->a, b = s->b, c = s->c, d = ortho_shift(s->a);
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    if (std::fabs(a - d) > 64.0) return false;
+    double r = 1.0;
+    for (int k = 0; k < s->steps; ++k) {
+        double next = 0.0;
+        for (int i = 0; i <= 1024; ++i) {
+            const double x = r * i / 1024.0, l = x * x;
+            if (std::fabs(d + b * l + c * l * l) > 7.5) return false;
+            next = std::max(next, std::fabs(x * (a + b * l + c * l * l)));
+        }
+        r = next * 1.01;  // rounding, and what lies between the samples
+        if (r > 1.9) return false;
+    }
+    return true;
+}
+
+bool ortho_valid(const tpmlp_ortho_shape *s) {
+    if (!s) return false;
+    if (s->batch < 0 || s->batch > 65535 || s->rows <= 0 || s->cols <= 0) return false;
+    if (s->rows > (1LL << 20) || s->cols > (1LL << 20)) return false;
+    if (s->steps < 1 || s->steps > 32) return false;
+    if (s->dtype != TPMLP_F32 && s->dtype != TPMLP_BF16) return false;
+    if (!(s->eps >= 0.0f) || !std::isfinite(s->eps)) return false;
+    return tiles_fit(s->rows + 64, s->cols + 64, s->batch);
+}
+
+struct OrthoLayout {
+    int64_t P, Q, p;
+    bool wide;  // rows <= cols: A = X X^T, else A = X^T X
+    size_t norm, hi[2], lo[2], A, C, total;
+};
+
+// Workspace, 1 KB-aligned regions: status | block sums of the norm | two of X's high
+// and low parts, used in turn | A | C.
+OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
+    OrthoLayout L;
+    L.P = (s->rows + 63) / 64 * 64, L.Q = (s->cols + 63) / 64 * 64;
+    L.wide = s->rows <= s->cols;
+    L.p = L.wide ? L.P : L.Q;
+    size_t off = STATUS_BYTES;
+    auto region = [&](size_t bytes) {
+        const size_t at = off;
+        off += align_up(bytes, 1024);
+        return at;
+    };
+    const size_t n = static_cast<size_t>(s->batch);
+    L.norm = region(n * static_cast<size_t>(tpmlp::ortho_norm_blocks(s->batch, s->rows * s->cols)) * 12);
+    const size_t x = n * static_cast<size_t>(L.P) * L.Q * 2, a = n * static_cast<size_t>(L.p) * L.p * 2;
+    for (int i = 0; i < 2; ++i) L.hi[i] = region(x), L.lo[i] = region(x);
+    L.A = region(a);
+    L.C = region(a);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tpmlp_ortho_workspace_bytes(const tpmlp_ortho_shape *s) {
+    return ortho_valid(s) && s->batch >= 0 ? ortho_layout(s).total : 0;
+}
+
+tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void *O, void *workspace, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!ortho_valid(s)) return invalid("tpmlp_orthogonalize: invalid shape");
+    if (!workspace || (s->batch > 0 && (!G || !O))) return invalid("tpmlp_orthogonalize: NULL pointer");
+    const size_t e_in = s->dtype == TPMLP_BF16 ? 2 : 4;
+    // whole rows of 16 bytes are stored by TMA, which wants the base on 16 bytes too
+    const bool tma_out = s->cols % 8 == 0;
+    if (!aligned16(workspace) || !aligned_elt(G, e_in) || !aligned_elt(O, tma_out ? 16 : 2)) {
+        tpmlp::set_last_error("tpmlp_orthogonalize: misaligned pointer (workspace 16 bytes, O 16 where cols is a "
+                              "multiple of 8, else 2)");
+        return TPMLP_ERR_UNSUPPORTED;
+    }
+    if (!ortho_range_ok(s)) {
+        tpmlp::set_last_error("tpmlp_orthogonalize: the coefficients let the iterates leave the fp16 range");
+        return TPMLP_ERR_UNSUPPORTED;
+    }
+    if (s->batch == 0) return TPMLP_OK;
+    int sms;
+    const tpmlp_status rc = device_ready(sms);
+    if (rc != TPMLP_OK) return rc;
+    const OrthoLayout L = ortho_layout(s);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint32_t *status = reinterpret_cast<uint32_t *>(ws);
+
+    tpmlp::OrthoStart a;
+    a.G = G;
+    a.batch = s->batch, a.rows = s->rows, a.cols = s->cols, a.P = L.P, a.Q = L.Q;
+    a.eps = s->eps, a.scale = kScaleX;
+    a.part = ws + L.norm;
+    a.hi = ws + L.hi[0], a.lo = ws + L.lo[0];
+    cudaError_t e;
+    {
+        Timed timed("ortho_start", st);
+        e = tpmlp::launch_ortho_start(s->dtype == TPMLP_BF16, a, st);
+        if (e == cudaSuccess) g_launches.fetch_add(2);
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+
+    auto product = [&](const void *x, bool x_mn, const void *y, bool y_mn, int64_t M,
+                       int64_t N, int64_t K, void *out) {
+        GemmArgs g = base_args(status);
+        g.cta_pair = true;
+        g.a = x, g.a_mn = x_mn;
+        g.b = y, g.b_mn = y_mn;
+        g.M = M, g.N = N, g.K = K, g.kshard = K;
+        g.batch = s->batch;
+        g.out0 = out;
+        return g;
+    };
+    auto launch = [&](const char *name, Epi epi, GemmArgs &g) {
+        pick_raster(g, epi);
+        Timed timed(name, st);
+        const cudaError_t r = tpmlp::launch_tc_gemm(epi, g, sms, st);
+        if (r == cudaSuccess) g_launches.fetch_add(1);
+        return r;
+    };
+    const float shift = ortho_shift(s->a);
+    void *A = ws + L.A, *C = ws + L.C;
+    for (int k = 0; k < s->steps; ++k) {
+        const bool last = k == s->steps - 1;
+        void *hi = ws + L.hi[k & 1], *lo = ws + L.lo[k & 1];
+        const int64_t inner = L.wide ? L.Q : L.P;
+        GemmArgs g = product(hi, !L.wide, hi, !L.wide, L.p, L.p, inner, A);
+        g.scale = kScaleA / (kScaleX * kScaleX);
+        e = launch("ortho_gram", tpmlp::EPI_NS_GRAM, g);
+        if (e != cudaSuccess) return from_cuda(e);
+
+        GemmArgs c = product(A, false, A, false, L.p, L.p, L.p, C);
+        c.aux = A;
+        c.alpha = s->b * (kScaleC / kScaleA);
+        c.scale = s->c * (kScaleC / (kScaleA * kScaleA));
+        c.diag = shift * kScaleC;
+        e = launch("ortho_poly", tpmlp::EPI_NS_POLY, c);
+        if (e != cudaSuccess) return from_cuda(e);
+
+        // X' = (a - d) hi + a lo + (C + dI) hi, hi and lo as stored (scale kScaleX, lo 2^11 times too large)
+        const Epi epi = last ? tpmlp::EPI_NS_LAST : tpmlp::EPI_NS_UPDATE;
+        void *hi2 = ws + L.hi[~k & 1], *lo2 = ws + L.lo[~k & 1];
+        void *out = last && tma_out ? O : hi2;
+        GemmArgs u = L.wide ? product(C, false, hi, true, L.P, L.Q, L.p, out)
+                            : product(hi, false, C, false, L.P, L.Q, L.p, out);
+        const float unit = last ? 1.0f / kScaleX : 1.0f;
+        u.aux = hi, u.aux2 = lo;
+        u.alpha = (s->a - shift) * unit;
+        u.beta = s->a / 2048.0f * unit;
+        u.scale = unit / kScaleC;
+        u.out1 = lo2;
+        u.out_rows = tma_out ? s->rows : L.P, u.out_cols = tma_out ? s->cols : L.Q;
+        e = launch(last ? "ortho_last" : "ortho_update", epi, u);
+        if (e != cudaSuccess) return from_cuda(e);
+        if (last && !tma_out) {
+            Timed timed("ortho_unpad", st);
+            e = tpmlp::launch_ortho_unpad(hi2, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
+            if (e == cudaSuccess) g_launches.fetch_add(1);
+        }
+    }
     return from_cuda(e);
 }
 

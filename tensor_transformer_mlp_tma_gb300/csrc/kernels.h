@@ -15,6 +15,13 @@ enum Epi : int {
     EPI_FOLD = 4,       // dX = ((P_1 + P_2) + ...)                        -- dY A^T
     EPI_ATTN_SCORE = 5, // S = scale * acc, -inf above the diagonal (causal), fp16 out -- Q K^T
     EPI_ATTN_DS = 6,    // dS = P * (acc - D[row]) * scale                  -- dO V^T -> dS
+    EPI_XENT_STATS = 7, // per row: max and sum of exponentials per 128 columns, the target's logit -- X W^T
+    EPI_XENT_GRAD = 8,  // dS = (exp(acc - lse[row]) - [col = target]) * g[row]  -- X W^T -> dS
+    EPI_ACC32 = 9,      // out (fp32) = acc, or out += acc                  -- dX, piece by piece
+    EPI_NS_GRAM = 10,   // A = scale * acc, symmetric, fp16                 -- X X^T
+    EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
+    EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
+    EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
 };
 
 // A per-head operand or output read or written in place inside a token-major
@@ -73,7 +80,29 @@ struct GemmArgs {
     // plain [batch][rows][cols] block.
     bool heads_layout;
     HeadView a_view, b_view, o_view;
+    // Row pitches in elements of operand A and B and of the output (0: contiguous),
+    // multiples of 8; batch must be 1 where one is set.
+    int64_t lda, ldb, ldo;
+    // EPI_XENT_STATS, EPI_XENT_GRAD: rows are tokens, columns vocabulary rows
+    // col0 .. col0 + N - 1 of W.
+    const int64_t *target;   // [M]
+    int64_t ignore_index, col0;
+    float2 *part;            // STATS: (max, sum) of 128-column group k, row m, at part[k * M + m]
+    float *target_logit;     // STATS: [M], written where the target is one of the columns
+    const float *row_lse;    // GRAD: [M]
+    const float *row_g;      // GRAD: [M]
+    bool accumulate;         // EPI_ACC32: add to what out0 holds
+    // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
+    // two parts of X through aux (high) and aux2 (low).  out0 / out1: X' high, low.
+    // LAST writes an [batch][out_rows][out_cols] array, the rest of the tile is dropped.
+    const void *aux2;
+    float alpha, beta, diag;
+    int64_t out_rows, out_cols;
 };
+
+// Columns per group of the EPI_XENT_STATS partials, and the groups that N columns make.
+constexpr int64_t XENT_GROUP = 128;
+inline int64_t xent_groups(int64_t N) { return (N + 511) / 512 * 4; }
 
 // Tensor-core path: bf16 operands, fp32 accumulation in TMEM (tcgen05).
 cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t st);
@@ -132,6 +161,38 @@ cudaError_t launch_softmax(const void *S, void *P, int64_t rows, int64_t cols, b
 // `ones` (optional): an 8 KiB block the kernel also fills with bf16 ones.
 cudaError_t launch_rowdot(const HeadLayout &L, const void *dO, const void *O, float *D, cudaStream_t st,
                           void *ones = nullptr);
+
+// Vocabulary cross entropy: the kernels over token rows (xent.cu).
+struct RowArgs {
+    int64_t tokens, vocab, ignore_index;
+    const int64_t *target;  // [tokens]
+    const float2 *part;     // [groups][tokens]: (max, sum of exponentials)
+    int64_t groups;
+    float *target_logit;    // [tokens]
+    uint32_t *status;
+};
+cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st);
+cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st);
+// n a multiple of 4, both 16-byte aligned.
+cudaError_t launch_to_bf16(const float *in, void *out, int64_t n, cudaStream_t st);
+// FFMA path: logits [tokens, n] of vocabulary rows col0 .. col0 + n - 1.
+cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,
+                                    cudaStream_t st);
+cudaError_t launch_xent_piece_grad(bool is_bf16, const RowArgs &a, const float *logits, int64_t n, int64_t col0,
+                                   const float *lse, const float *row_g, void *out, cudaStream_t st);
+
+// Newton-Schulz orthogonalisation (ortho.cu): X = G scale / (|G| + eps) as hi + lo / 2^11.
+struct OrthoStart {
+    const void *G;  // [batch][rows][cols]
+    int64_t batch, rows, cols, P, Q;
+    float eps, scale;
+    void *part;     // ortho_norm_blocks(batch, rows * cols) * batch * 12 bytes
+    void *hi, *lo;  // fp16 [batch][P][Q]
+};
+int64_t ortho_norm_blocks(int64_t batch, int64_t n);
+cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t st);
+cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
+                               void *out, cudaStream_t st);
 
 // Records a description of the last failure of this host thread (read back by
 // tpmlp_last_error()).

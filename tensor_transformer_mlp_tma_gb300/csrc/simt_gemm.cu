@@ -70,6 +70,7 @@ struct Params {
     void *out1;
     const void *aux;
     const void *bias;
+    int accumulate;  // EPI_ACC32: add to the fp32 output
 };
 
 template <typename T, int EPI>
@@ -168,6 +169,9 @@ __global__ void __launch_bounds__(256) gemm_kernel(const Params p) {
                 const float hv = ld<T>(static_cast<const T *>(p.aux), o);
                 st<T>(static_cast<T *>(p.out0), o, v * gelu_prime_exact_tanh(hv));
                 if (p.out1) st<T>(static_cast<T *>(p.out1), o, gelu_exact_tanh(hv));  // Y rebuilt from H
+            } else if constexpr (EPI == EPI_ACC32) {
+                float *out = static_cast<float *>(p.out0) + o;
+                *out = p.accumulate ? *out + v : v;
             } else {
                 st<T>(static_cast<T *>(p.out0), o, v);
             }
@@ -184,6 +188,7 @@ static cudaError_t launch_t(Epi epi, const Params &p, cudaStream_t st) {
         case EPI_DGELU: gemm_kernel<T, EPI_DGELU><<<grid, 256, 0, st>>>(p); break;
         case EPI_STORE: gemm_kernel<T, EPI_STORE><<<grid, 256, 0, st>>>(p); break;
         case EPI_FOLD: gemm_kernel<T, EPI_FOLD><<<grid, 256, 0, st>>>(p); break;
+        case EPI_ACC32: gemm_kernel<T, EPI_ACC32><<<grid, 256, 0, st>>>(p); break;
         default: return cudaErrorNotSupported;
     }
     return cudaGetLastError();
@@ -221,6 +226,7 @@ cudaError_t launch_simt_gemm(Epi epi, bool is_bf16, const GemmArgs &g, cudaStrea
     p.out1 = g.out1;
     p.aux = g.aux;
     p.bias = g.bias;
+    p.accumulate = g.accumulate ? 1 : 0;
     return is_bf16 ? simt::launch_t<__nv_bfloat16>(epi, p, st) : simt::launch_t<float>(epi, p, st);
 }
 

@@ -33,6 +33,7 @@
 // drains its own copies and MMAs and frees its tensor memory before returning.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
@@ -156,7 +157,26 @@ struct Params {
     // last k-block down to the first, so that a unit's next tile starts on the
     // k-blocks its wave read last, while they are still in L2.
     int serpentine;
+    // Vocabulary cross entropy (EPI_XENT_*), see GemmArgs.
+    const int64_t *target;
+    long long ignore_index, col0;
+    float2 *part;
+    float *target_logit;
+    const float *row_lse, *row_g;
+    int accumulate;  // EPI_ACC32
+    // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
+    const void *aux2;
+    float alpha, beta, diag;
+    int out_M, out_N;
 };
+
+// The Newton-Schulz products: fp16 operands; A and C = f(A) are symmetric, so only
+// the tiles on and below the diagonal are computed and each is stored twice.
+__host__ __device__ constexpr bool is_ns(int epi) {
+    return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
+}
+__host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY; }
+__host__ __device__ constexpr bool is_xent(int epi) { return epi == EPI_XENT_STATS || epi == EPI_XENT_GRAD; }
 
 // Coordinates after (x, y) of problem z in a map of the given rank.
 __device__ __forceinline__ void head_coords(int rank, int z, int heads, int hpt, int &c2, int &c3, int &c4) {
@@ -279,6 +299,29 @@ __device__ __forceinline__ void tile_coords(int tile, const Params &p, int &mb, 
     // every odd problem backwards gives each unit a mix of heavy and light
     // tiles, and the tiles of one problem stay adjacent (sharing operands in L2).
     if (p.flip_odd && (zb & 1)) mb = p.m_tiles - 1 - mb;
+}
+
+// Output tiles of one launch (whole tiles), and the coordinates of one of them.  A
+// symmetric output of n x n tiles has n (n + 1) / 2: tile i of a problem is row
+// mb of the lower triangle, mb (mb + 1) / 2 <= i < (mb + 1)(mb + 2) / 2.
+template <int EPI>
+__device__ __forceinline__ int tile_count(const Params &p) {
+    if constexpr (is_sym(EPI)) return p.m_tiles * (p.m_tiles + 1) / 2 * p.batch;
+    return p.m_tiles * p.n_tiles * p.batch;
+}
+template <int EPI>
+__device__ __forceinline__ void coords_of(int tile, const Params &p, int &mb, int &nb, int &zb) {
+    if constexpr (is_sym(EPI)) {
+        const int per = p.m_tiles * (p.m_tiles + 1) / 2;
+        zb = tile / per;
+        const int i = tile - zb * per;
+        mb = static_cast<int>((sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
+        while (mb * (mb + 1) / 2 > i) --mb;
+        while ((mb + 1) * (mb + 2) / 2 <= i) ++mb;
+        nb = i - mb * (mb + 1) / 2;
+    } else {
+        tile_coords(tile, p, mb, nb, zb);
+    }
 }
 
 // Wide tiles: the tile order is that of tile_coords over the 256 x 512 tiles,
@@ -536,13 +579,223 @@ __device__ __forceinline__ void gelu_of_packed(const uint32_t (&h)[16], uint32_t
     }
 }
 
+// ---- vocabulary cross entropy --------------------------------------------------
+// Row data of one thread's token (one accumulator row) and its running statistics.
+constexpr float kLog2e = 1.4426950408889634f;
+struct XentRow {
+    int tcol;      // the target's column of this launch, -1: none (ignored, or in another piece)
+    float lse2;    // GRAD: log-sum-exp times log2(e)
+    float g;       // GRAD: the loss's gradient, 0 for an ignored token
+    float m, s;    // STATS: running maximum, sum of exp(logit - m)
+};
+template <int EPI>
+__device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, XentRow &x) {
+    x.tcol = -1, x.lse2 = 0.0f, x.g = 0.0f;
+    x.m = -INFINITY, x.s = 0.0f;
+    if (row >= p.M) return;
+    const long long t = p.target[row];
+    const bool valid = t != p.ignore_index;
+    const long long c = t - p.col0;
+    if (valid && c >= 0 && c < p.N) x.tcol = static_cast<int>(c);
+    if constexpr (EPI == EPI_XENT_GRAD) {
+        x.lse2 = p.row_lse[row] * kLog2e;
+        x.g = p.row_g[row];  // zero where the target is ignored
+    }
+}
+
+// One pass of the online softmax over 32 logits: the running maximum moves to m',
+// the running sum is scaled by exp(m - m') and the 32 exponentials are added, all
+// in fp32.  Columns past N count as -inf.
+__device__ __forceinline__ void xent_stats_chunk(const Params &p, float (&v)[32], int64_t row, int col, XentRow &x) {
+    if (col >= p.N) return;
+    if (col + 32 > p.N) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (col + i >= p.N) v[i] = -INFINITY;
+    }
+    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+    const float m = fmaxf(x.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+    // all logits so far -inf: exp(-inf - 0) = 0 instead of exp(-inf + inf)
+    const float base = m == -INFINITY ? 0.0f : m * kLog2e;
+    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], kLog2e, -base));
+    x.m = m;
+    x.s = (s[0] + s[1]) + (s[2] + s[3]);
+    // the target's logit, where it is one of these columns (few warps at a time)
+    const int at = x.tcol - col;
+    const bool here = at >= 0 && at < 32;
+    if (__any_sync(0xffffffffu, here)) {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (at == i) z = v[i];
+        if (here && row < p.M) p.target_logit[row] = z;
+    }
+}
+__device__ __forceinline__ void xent_stats_flush(const Params &p, int64_t row, int group, XentRow &x) {
+    if (row < p.M) p.part[static_cast<int64_t>(group) * p.M + row] = make_float2(x.m, x.s);
+    x.m = -INFINITY, x.s = 0.0f;
+}
+
+// dS = (softmax - one-hot) g of 32 logits.  The one-hot term is subtracted before
+// the single rounding to bf16.  g = 0 gives exact zeros, whatever the logits.
+__device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const XentRow &x) {
+    const int at = x.tcol - col;
+    if (x.g == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float pr = ptx::ex2_approx(fmaf(v[i], kLog2e, -x.lse2));
+            v[i] = (at == i ? pr - 1.0f : pr) * x.g;
+        }
+    }
+}
+
+// ---- Newton-Schulz products -----------------------------------------------------
+// 32 consecutive fp16 values of a row-major matrix of pitch N (a multiple of 64)
+// fetched ahead of the chunk that uses them; rows past the end read as zero.
+struct HalfPre {
+    uint4 w[4];
+};
+__device__ __forceinline__ void half_fetch(const void *in, const Params &p, int z, int64_t row, int col, HalfPre &h) {
+    const bool ok = row < p.M && col < p.N;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __half *>(in) +
+                                                       (static_cast<int64_t>(z) * p.M + row) * p.N + col);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) h.w[g] = ok ? src[g] : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void unpack_f16(uint32_t u, float &lo, float &hi) {
+    const __half2 v = *reinterpret_cast<__half2 *>(&u);
+    lo = __low2float(v);
+    hi = __high2float(v);
+}
+// v = scale * v + k * h for the 32 fetched values.
+__device__ __forceinline__ void half_axpy(const HalfPre &h, float k, float (&v)[32]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const uint32_t u[4] = {h.w[g].x, h.w[g].y, h.w[g].z, h.w[g].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpack_f16(u[i], a, b);
+            v[8 * g + 2 * i] = fmaf(k, a, v[8 * g + 2 * i]);
+            v[8 * g + 2 * i + 1] = fmaf(k, b, v[8 * g + 2 * i + 1]);
+        }
+    }
+}
+
+// The transpose of a 32 x 32 box of 16-bit values, lane r holding row r as 16
+// packed pairs, written to a 64-byte-swizzled staging box: one exchange with the
+// neighbouring lane per pair gives the even lane the two rows' column 2i and the
+// odd lane their column 2i + 1, so that each stores whole 32-bit words; the 32
+// lanes of a store write 32 different words of two rows (no bank conflict).
+__device__ __forceinline__ void stage_transposed(uint32_t box, int lane, const uint32_t (&w)[16]) {
+    const bool odd = lane & 1;
+    const int word = lane >> 1;  // the pair of rows (2 word, 2 word + 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, w[i], 1);
+        const uint32_t t = odd ? __byte_perm(other, w[i], 0x7632) : __byte_perm(w[i], other, 0x5410);
+        const int r = 2 * i + (odd ? 1 : 0);  // row of the transposed box
+        ptx::st_shared_u32(box + static_cast<uint32_t>(r) * 64u +
+                               (static_cast<uint32_t>((word >> 2) ^ ((r >> 1) & 3)) << 4) +
+                               (static_cast<uint32_t>(word & 3) << 2),
+                           t);
+    }
+}
+
+// Finishes one 32-column chunk of a Newton-Schulz product.  All arithmetic is
+// fp32; every stored value is rounded once (high and low part of X' together hold
+// about 22 bits).
+template <int EPI>
+__device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0, const CUtensorMap *tm1,
+                                         float (&v)[32], const HalfPre &h0, const HalfPre &h1, int64_t row, int row0,
+                                         int col, int z, bool mirror, int lane, uint32_t stg) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= p.scale;
+    if constexpr (EPI == EPI_NS_POLY) {
+        half_axpy(h0, p.alpha, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (row == col + i) v[i] += p.diag;
+    } else if constexpr (EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST) {
+        half_axpy(h0, p.alpha, v);
+        half_axpy(h1, p.beta, v);
+    }
+    uint32_t w0[16], w1[16];
+    if constexpr (EPI == EPI_NS_LAST) {
+        pack32(v, w0);
+    } else {
+        // finite values saturate at the fp16 range (the scales keep them inside);
+        // NaN stays NaN
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w0[i] = ptx::f16x2_satfinite(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (EPI == EPI_NS_UPDATE) {
+        // the low part, 2^11 times larger than it is, so that it is a normal fp16
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack_f16(w0[i], a, b);
+            w1[i] = ptx::f16x2_satfinite((v[2 * i] - a) * 2048.0f, (v[2 * i + 1] - b) * 2048.0f);
+        }
+    }
+    if (lane == 0) ptx::bulk_wait_read0();
+    __syncwarp();
+    stage_row(stg, lane, w0);
+    if constexpr (EPI == EPI_NS_UPDATE) stage_row(stg + STG_BOX, lane, w1);
+    if constexpr (is_sym(EPI)) {
+        if (mirror) stage_transposed(stg + STG_BOX, lane, w0);
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    const int M = EPI == EPI_NS_LAST ? p.out_M : p.M, N = EPI == EPI_NS_LAST ? p.out_N : p.N;
+    if (lane == 0 && row0 < M && col < N) {
+        ptx::tma_store_3d(tm0, stg, col, row0, z);
+        if constexpr (EPI == EPI_NS_UPDATE) ptx::tma_store_3d(tm1, stg + STG_BOX, col, row0, z);
+        if constexpr (is_sym(EPI)) {
+            if (mirror) ptx::tma_store_3d(tm0, stg + STG_BOX, row0, col, z);
+        }
+        ptx::bulk_commit();
+    }
+}
+
 template <int EPI, bool HEADS = false>
 __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap *tm0, const CUtensorMap *tm1,
                                              const CUtensorMap *tm2, float (&v)[32], int64_t row, int row0,
                                              int col, int z, int lane, uint32_t stg, AuxLoad *aux = nullptr,
                                              int next_col = -1, int next_row0 = 0,
                                              volatile int *abort_flag = nullptr,
-                                             const BiasPre *bias_pre = nullptr) {
+                                             const BiasPre *bias_pre = nullptr, const XentRow *xr = nullptr) {
+    if constexpr (EPI == EPI_ACC32) {
+        // 32 x 32 fp32 box (128-byte rows, 128-byte swizzle), stored or added to
+        // the output.  One launch adds to an element once, and launches follow one
+        // another on their stream, so the order of the additions is fixed.
+        if (lane == 0) ptx::bulk_wait_read0();
+        __syncwarp();
+        const uint32_t r = stg + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            ptx::st_shared_v4(r + (static_cast<uint32_t>(j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
+                              __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                              __float_as_uint(v[4 * j + 3]));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < p.M && col < p.N) {
+            if (p.accumulate)
+                ptx::tma_reduce_add_3d(tm0, stg, col, row0, z);
+            else
+                ptx::tma_store_3d(tm0, stg, col, row0, z);
+            ptx::bulk_commit();
+        }
+        return;
+    }
+    if constexpr (EPI == EPI_XENT_GRAD) xent_grad_chunk(v, col, *xr);
     if constexpr (EPI == EPI_ATTN_SCORE) {
         // S = scale * Q K^T with the causal mask, stored in fp16 for the softmax
         // (11 significant bits; finite values saturate at the fp16 range, the
@@ -684,13 +937,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD);
     constexpr bool WIDE = TILE_N == 512;
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
-    constexpr uint32_t IDESC = ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
+    constexpr uint32_t IDESC = is_ns(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
+                                          : ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE),
                   "narrow tile: CTA pairs, plain store");
-    static_assert(!WIDE || (CG == 2 && !HEADS && (EPI == EPI_STORE || EPI == EPI_BIAS_GELU || EPI == EPI_DGELU)),
-                  "wide tile: CTA pairs, one shard, store / bias+GeLU / GeLU' epilogues");
+    static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
+                  "wide tile: CTA pairs, one shard");
+    static_assert(!is_sym(EPI) || C::TILE_M == TILE_N, "symmetric outputs: square tiles");
     constexpr int STAGES = C::STAGES;
 
     extern __shared__ uint8_t smem_raw[];
@@ -768,7 +1023,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                   p, &abort_sh, 0x0100u);
     (void)ring_end, (void)stg_end;
 
-    const int num_tiles = p.m_tiles * p.n_tiles * p.batch + (WIDE ? p.wide_tail : 0);
+    const int num_tiles = tile_count<EPI>(p) + (WIDE ? p.wide_tail : 0);
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -856,7 +1111,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             } else {
             for (int tile = unit_id; tile < num_tiles && ok; tile += num_units) {
                 int mb, nb, zb;
-                tile_coords(tile, p, mb, nb, zb);
+                coords_of<EPI>(tile, p, mb, nb, zb);
                 if (!tile_active<C::TILE_M, C::TILE_N>(p, mb, nb)) continue;
                 const int m0 = mb * C::TILE_M + BM * static_cast<int>(rank);
                 const int n0 = nb * TILE_N + C::B_ROWS * static_cast<int>(rank);
@@ -1129,7 +1384,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             } else {
             for (int tile = unit_id; tile < num_tiles && ok; tile += num_units) {
                 int mb, nb, zb;
-                tile_coords(tile, p, mb, nb, zb);
+                coords_of<EPI>(tile, p, mb, nb, zb);
                 if (!tile_active<C::TILE_M, C::TILE_N>(p, mb, nb)) continue;
                 int kb0, kb1;
                 k_range<C::TILE_M>(p, mb, kb0, kb1);
@@ -1261,6 +1516,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // the accumulator is still being computed).
             BiasPre bias_next;
             if constexpr (EPI == EPI_BIAS_GELU) bias_fetch(p.bias, col0 + 32 * qa, p.N, bias_next);
+            XentRow xr;
+            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, xr);
             bool got = ptx::mbar_wait_scoped<false>(ptx::smem_u32(&bar_tfull[0]), tcount & 1u, p.wait_ns, &abort_sh);
             ++tcount;
             got = __all_sync(0xffffffffu, got);
@@ -1295,9 +1552,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (rank == 0 && quarter == 0 && lane == 0) store_bias_grad(p, col0 + 32 * q, v);
                     continue;
                 }
+                if constexpr (EPI == EPI_XENT_STATS) {
+                    xent_stats_chunk(p, v, row, col0 + 32 * q, xr);
+                    if ((q & 3) == 3) xent_stats_flush(p, row, (col0 + 32 * q) >> 7, xr);
+                    continue;
+                }
                 finish_chunk<EPI, false>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + 32 * q, zb, lane, stg, &aux,
                                          q + 1 < qb ? col0 + 32 * (q + 1) : -1, row0, &abort_sh,
-                                         EPI == EPI_BIAS_GELU ? &bias_cur : nullptr);
+                                         EPI == EPI_BIAS_GELU ? &bias_cur : nullptr, is_xent(EPI) ? &xr : nullptr);
             }
         }
         } else {
@@ -1308,13 +1570,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // hold SMs that a CTA of this grid still waits for.
             if (tile + num_units >= num_tiles) ptx::griddep_launch_dependents();
             int mb, nb, zb;
-            tile_coords(tile, p, mb, nb, zb);
+            coords_of<EPI>(tile, p, mb, nb, zb);
             if (!tile_active<C::TILE_M, C::TILE_N>(p, mb, nb)) continue;
             const int row0 = mb * C::TILE_M + BM * static_cast<int>(rank) + quarter * 32;
             const int64_t row = static_cast<int64_t>(row0) + lane;
             const int col0 = nb * TILE_N + half * (TILE_N / 2);
             if constexpr (EPI == EPI_DGELU) aux_issue(&tmO1, aux, stg + STG_BOX, col0, row0, zb, lane);
             if constexpr (EPI == EPI_ATTN_DS) aux_issue(&tmO1, aux, stg + STG_BOX_WIDE, col0, row0, zb, lane, STG_BOX_WIDE);
+            XentRow xr;
+            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, xr);
+            (void)xr;
+            HalfPre h0, h1;  // the Newton-Schulz epilogues' inputs, one chunk ahead
+            auto ns_fetch = [&](int col) {
+                if constexpr (EPI == EPI_NS_POLY || EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST)
+                    half_fetch(p.aux, p, zb, row, col, h0);
+                if constexpr (EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST) half_fetch(p.aux2, p, zb, row, col, h1);
+            };
+            ns_fetch(col0);
+            (void)h0, (void)h1;
             for (int s = 0; s < p.nshards; ++s, ++unit) {
                 const uint32_t buf = unit & 1u, use = unit >> 1;
                 bool got = ptx::mbar_wait_scoped<false>(ptx::smem_u32(&bar_tfull[buf]), use & 1u, p.wait_ns,
@@ -1421,8 +1694,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        if constexpr (is_ns(EPI)) {
+                            const HalfPre c0 = h0, c1 = h1;
+                            if (c < CHUNKS - 1) ns_fetch(col0 + (c + 1) * 32);
+                            ns_chunk<EPI>(p, &tmO0, &tmO1, v, c0, c1, row, row0, col0 + c * 32, zb, mb != nb, lane, stg);
+                        } else if constexpr (EPI == EPI_XENT_STATS) {
+                            xent_stats_chunk(p, v, row, col0 + c * 32, xr);
+                            if ((c & 3) == 3) xent_stats_flush(p, row, (col0 + c * 32) >> 7, xr);
+                        } else {
                         finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg, &aux,
-                                          c < CHUNKS - 1 ? col0 + (c + 1) * 32 : -1, row0, &abort_sh);
+                                          c < CHUNKS - 1 ? col0 + (c + 1) * 32 : -1, row0, &abort_sh, nullptr,
+                                          is_xent(EPI) ? &xr : nullptr);
+                        }
                     }
                     }
                 }
@@ -1476,7 +1759,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // (cols, rows, batch); a plain matrix has batch 1.
 static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, uint32_t box_cols,
                      uint32_t box_rows, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int64_t batch = 1,
-                     CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+                     CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int64_t ld = 0) {
     auto fn = encode_fn();
     if (!fn) {
         set_last_error("cuTensorMapEncodeTiled is not available from the driver");
@@ -1485,8 +1768,9 @@ static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
     const cuuint64_t esz = dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(batch)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * esz,
-                             static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(rows) * esz};
+    if (ld == 0) ld = cols;  // row pitch in elements
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * esz,
+                             static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * esz};
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(m, dt, 3,
@@ -1506,13 +1790,14 @@ static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
 // row pitch of the second; returns false if the driver does not take the map
 // (the caller then keeps the per-block 3-D map).
 static bool make_map_mn4(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, uint32_t box_k,
-                         uint32_t nblk, int64_t batch) {
+                         uint32_t nblk, int64_t batch, int64_t ld = 0) {
     auto fn = encode_fn();
     if (!fn || cols % 64 != 0) return false;
     cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
                           static_cast<cuuint64_t>(batch)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(cols) * 2, 128,
-                             static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(rows) * 2};
+    if (ld == 0) ld = cols;
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128,
+                             static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * 2};
     cuuint32_t box[4] = {64, box_k, nblk, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
@@ -1620,6 +1905,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // B operand: this CTA's B_ROWS columns, K-major in one box or MN-major in 64-wide boxes.
     const int64_t nb = g.batch < 1 ? 1 : g.batch;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;  // the copies move 16-bit words: fp16 too
     // MN-major operands whose MN extent is a multiple of 64 take the 4-D map
     // (one copy per stage instead of one per 64-wide block); TPMLP_MN4=0 keeps
     // the per-block maps (a tuning knob, read per call).
@@ -1633,21 +1919,22 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // (HEADS kernels always copy MN-major operands block by block.)
     constexpr bool WIDE = TILE_N == 512;
     CUtensorMap mb2;  // wide tiles: B of one 256-column half of the tile (half the box)
-    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, nb);
+    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, nb, g.lda);
     const bool b4 = !HEADS && B_MN && mn4 && g.N % 64 == 0 &&
-                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, nb) &&
-                    (!WIDE || make_map_mn4(&mb2, g.b, g.K, g.N, BK, C::B_ROWS / 128, nb));
+                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, nb, g.ldb) &&
+                    (!WIDE || make_map_mn4(&mb2, g.b, g.K, g.N, BK, C::B_ROWS / 128, nb, g.ldb));
     bool oka, okb;
     if (a_rank > 3)
         oka = make_map_view(&ma, g.a, g.a_view, 64, A_MN ? BK : BM, sw);
     else
-        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, nb) : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, nb));
+        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, nb, bf, g.lda)
+                          : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, nb, bf, g.lda));
     if (b_rank > 3)
         okb = make_map_view(&mb, g.b, g.b_view, 64, B_MN ? BK : C::B_ROWS, sw);
     else
-        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, nb)
-                          : make_map(&mb, g.b, g.N, g.K, BK, C::B_ROWS, sw, nb));
-    if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, nb);
+        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, nb, bf, g.ldb)
+                          : make_map(&mb, g.b, g.N, g.K, BK, C::B_ROWS, sw, nb, bf, g.ldb));
+    if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, nb, bf, g.ldb);
     if (!WIDE || (B_MN && !b4)) mb2 = mb;  // unused, or the per-block maps serve both widths
     if (!oka || !okb) return cudaErrorInvalidValue;
     // Output maps: [M, N] row-major, 32 x 32 boxes, 64-byte swizzle (matches stage_row).
@@ -1655,18 +1942,24 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // the others write out0 only.
     // The GeLU' epilogue can also write Y rebuilt from H (third map).
     CUtensorMap mo0, mo1, mo2;
-    const void *o0 = g.out0 ? g.out0 : g.out1;
+    const void *o0 = EPI == EPI_XENT_STATS ? g.a : (g.out0 ? g.out0 : g.out1);  // STATS stores no matrix
     // The attention scores are fp16 (32 x 32 box, 64-byte swizzle, as the bf16
     // outputs); dS reads P through the second map; both of its maps have 32 x 64
     // boxes with 128-byte swizzle (see stage_half_row128).
     const void *o1 = (EPI == EPI_BIAS_GELU) ? (g.out1 ? g.out1 : o0)
-                                            : ((EPI == EPI_DGELU || EPI == EPI_ATTN_DS) ? g.aux : o0);
+                                            : ((EPI == EPI_DGELU || EPI == EPI_ATTN_DS) ? g.aux
+                                               : (EPI == EPI_NS_UPDATE ? g.out1 : o0));
     const void *o2 = (EPI == EPI_DGELU && g.out1) ? g.out1 : o0;
     const CUtensorMapDataType odt =
-        EPI == EPI_ATTN_SCORE ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        EPI == EPI_ATTN_SCORE ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                              : (EPI == EPI_ACC32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
     const bool wide = EPI == EPI_ATTN_DS;
     const uint32_t obox = wide ? 64 : 32;
-    const CUtensorMapSwizzle so = wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle so = wide || EPI == EPI_ACC32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    // What the output map covers: STATS stores no matrix (any valid map will do);
+    // LAST stores the unpadded part of the tiles.
+    const int64_t orows = EPI == EPI_NS_LAST ? g.out_rows : g.M;
+    const int64_t ocols = EPI == EPI_XENT_STATS ? g.K : (EPI == EPI_NS_LAST ? g.out_cols : g.N);
     if (wide && (o_rank > 3 || g.nshards != 1)) {
         set_last_error("dS epilogue: a plain [problems][M][N] output and one shard only");
         return cudaErrorInvalidValue;
@@ -1678,10 +1971,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         return cudaErrorInvalidValue;
     }
     if (!(o_rank > 3 ? make_map_view(&mo0, o0, g.o_view, 32, 32, so)
-                     : make_map(&mo0, o0, g.M, g.N, obox, 32, so, nb, odt)) ||
-        !make_map(&mo1, o1, g.M, g.N, obox, 32, so, nb, odt) ||
+                     : make_map(&mo0, o0, orows, ocols, obox, 32, so, nb, odt, g.ldo)) ||
+        !make_map(&mo1, o1, orows, ocols, obox, 32, so, nb, odt, g.ldo) ||
         !(bias_tile ? make_map(&mo2, g.ones, 64, 64, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, 1)
-                    : make_map(&mo2, o2, g.M, g.N, 32, 32, so, nb, odt)))
+                    : make_map(&mo2, o2, orows, ocols, 32, 32, so, nb, odt, g.ldo)))
         return cudaErrorInvalidValue;
 
     Params p;
@@ -1722,6 +2015,20 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.bias_grad = g.bias_grad;
     if (bias_tile) p.m_tiles += 1;  // the ones tile, after every row of the output
     p.skip_upper = g.skip_upper ? 1 : 0;
+    p.target = g.target;
+    p.ignore_index = g.ignore_index;
+    p.col0 = g.col0;
+    p.part = g.part;
+    p.target_logit = g.target_logit;
+    p.row_lse = g.row_lse;
+    p.row_g = g.row_g;
+    p.accumulate = g.accumulate ? 1 : 0;
+    p.aux2 = g.aux2;
+    p.alpha = g.alpha;
+    p.beta = g.beta;
+    p.diag = g.diag;
+    p.out_M = static_cast<int>(g.out_rows);
+    p.out_N = static_cast<int>(g.out_cols);
     // TPMLP_FLIP_ODD=0 keeps every problem's M-tiles in order (a tuning knob, read per call).
     {
         const char *flip = std::getenv("TPMLP_FLIP_ODD");
@@ -1739,7 +2046,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
                        static_cast<long long>(g.M), static_cast<long long>(g.K), g.nshards);
         return cudaErrorInvalidValue;
     }
-    int tiles = p.m_tiles * p.n_tiles * p.batch;
+    int tiles = is_sym(EPI) ? p.m_tiles * (p.m_tiles + 1) / 2 * p.batch : p.m_tiles * p.n_tiles * p.batch;
     int resident = max_clusters[dev];
     if (const char *o = std::getenv("TPMLP_MAX_UNITS")) resident = std::atoi(o) > 0 ? std::atoi(o) : resident;
     // Wide tiles: a last partial wave of r tiles is run as 2r half-width tiles
@@ -1791,7 +2098,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 template <int EPI, bool A_MN, bool B_MN>
 static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
-    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || (EPI == EPI_STORE && A_MN == B_MN)) {
+    if constexpr (is_ns(EPI)) {
+        return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
+    } else {
+    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || EPI == EPI_ACC32 || is_xent(EPI)) {
         if (tc_wide_tile(static_cast<Epi>(EPI), g)) return launch_t<EPI, A_MN, B_MN, 2, false, 512>(g, num_sms, st);
     }
     if constexpr (EPI == EPI_STORE && !A_MN && !B_MN) {
@@ -1814,13 +2124,14 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
     }
     return g.cta_pair ? launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st) : launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
     }
+    }
 }
 
 }  // namespace tc
 
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
-    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || (epi == EPI_STORE && g.a_mn == g.b_mn))) return false;
+    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || epi == EPI_ACC32 || tc::is_xent(epi))) return false;
     const char *w = std::getenv("TPMLP_WIDE");
     return !(w && w[0] == '0');
 }
@@ -1849,6 +2160,30 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
             break;
         case EPI_ATTN_DS:  // dO[S,d] (K-major) . V[S,d]^T (K-major), per head
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_ATTN_DS, false, false>(g, num_sms, st);
+            break;
+        case EPI_XENT_STATS:  // X[T,h] (K-major) . W[V,h]^T (K-major)
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_STATS, false, false>(g, num_sms, st);
+            break;
+        case EPI_XENT_GRAD:
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_GRAD, false, false>(g, num_sms, st);
+            break;
+        case EPI_ACC32:  // dS[T,V'] (K-major) . W[V',h] (MN-major)
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, false, true>(g, num_sms, st);
+            break;
+        case EPI_NS_GRAM:  // X X^T of a wide X (K-major), X^T X of a tall one (MN-major)
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAM, false, false>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_NS_GRAM, true, true>(g, num_sms, st);
+            break;
+        case EPI_NS_POLY:  // A A (symmetric: both K-major)
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_POLY, false, false>(g, num_sms, st);
+            break;
+        case EPI_NS_UPDATE:  // C X of a wide X (MN-major), X C of a tall one (C symmetric: K-major)
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_NS_UPDATE, false, true>(g, num_sms, st);
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_UPDATE, false, false>(g, num_sms, st);
+            break;
+        case EPI_NS_LAST:
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_NS_LAST, false, true>(g, num_sms, st);
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_LAST, false, false>(g, num_sms, st);
             break;
         case EPI_FOLD:  // dY[T,F] (K-major) . A[h,F]^T (K-major)
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_FOLD, false, false>(g, num_sms, st);

@@ -56,6 +56,18 @@ class AttnSaved(ctypes.Structure):
                 ("QKV", ctypes.c_void_p), ("P", ctypes.c_void_p), ("O", ctypes.c_void_p)]
 
 
+class XentShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("piece", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("algo", ctypes.c_int32)]
+
+
+class OrthoShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("steps", ctypes.c_int32), ("dtype", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class TpmlpError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -90,6 +102,11 @@ def _load():
         "tpmlp_attn_workspace_bytes": (sz, [ctypes.POINTER(AttnShape)]),
         "tpmlp_attn_forward": (i32, [ctypes.POINTER(AttnShape)] + [vp] * 6 + [ctypes.POINTER(AttnSaved), vp, vp]),
         "tpmlp_attn_backward": (i32, [ctypes.POINTER(AttnShape), vp, ctypes.POINTER(AttnSaved)] + [vp] * 7),
+        "tpmlp_xent_workspace_bytes": (sz, [ctypes.POINTER(XentShape)]),
+        "tpmlp_xent_forward": (i32, [ctypes.POINTER(XentShape)] + [vp] * 7),
+        "tpmlp_xent_backward": (i32, [ctypes.POINTER(XentShape)] + [vp] * 9),
+        "tpmlp_ortho_workspace_bytes": (sz, [ctypes.POINTER(OrthoShape)]),
+        "tpmlp_orthogonalize": (i32, [ctypes.POINTER(OrthoShape)] + [vp] * 4),
         "tpmlp_check_device_status": (i32, [vp, vp]),
         "tpmlp_set_wait_limit_ns": (None, [u64]),
         "tpmlp_debug_timeout_probe": (i32, [vp, u64, vp]),
@@ -399,8 +416,130 @@ def attn_backward(ctx: AttnContext, dZ, stream=None, **outs):
     return out
 
 
+def _status_workspace(nbytes, device):
+    """A workspace whose status word is zero; the rest is written before it is read."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    ws[:1024].zero_()
+    return ws
+
+
+def _same_device(ctx, *tensors):
+    for x in tensors:
+        if x is not None and x.device != ctx.workspace.device:
+            raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
+
+
+class XentContext:
+    """Buffers of the vocabulary cross entropy between forward and backward: lse [T]
+    (fp32) and the workspace.  W is [vocab, hidden], targets are int64; a target equal
+    to ignore_index takes no part.  `piece` sets the vocabulary rows per piece of the
+    backward pass (a multiple of 8; 0: the library's choice).
+
+    One context serves one call at a time: its workspace is scratch of every call,
+    also of captured graphs replayed at the same time."""
+
+    def __init__(self, tokens, hidden, vocab, dtype, ignore_index=-100, piece=0, algo=ALGO_DEFAULT, device=None):
+        if dtype not in _DTYPES:
+            raise ValueError("dtype %s: float32 or bfloat16" % (dtype,))
+        self.shape = XentShape(int(tokens), int(hidden), int(vocab), int(ignore_index), int(piece), _DTYPES[dtype],
+                               int(algo))
+        n = int(lib.tpmlp_xent_workspace_bytes(ctypes.byref(self.shape)))
+        if n == 0:
+            raise ValueError("invalid cross entropy shape (tokens=%d hidden=%d vocab=%d piece=%d)"
+                             % (tokens, hidden, vocab, piece))
+        self.dtype = dtype
+        self.workspace = _status_workspace(n, device)
+        self.lse = torch.empty((int(tokens),), dtype=torch.float32, device=self.workspace.device)
+        self._saved = None
+
+
+def xent_forward(ctx: XentContext, X, W, target, loss=None, stream=None):
+    """loss[T] = log sum_v exp(X W^T)_v - (X W^T)_target, 0 for an ignored target; fills
+    ctx.lse.  X and W are kept for xent_backward."""
+    s = ctx.shape
+    T, h, V = s.tokens, s.hidden, s.vocab
+    _need(X, "X", ctx.dtype, (T, h))
+    _need(W, "W", ctx.dtype, (V, h))
+    _need(target, "target", torch.int64, (T,))
+    if loss is None:
+        loss = torch.empty((T,), dtype=torch.float32, device=X.device)
+    _need(loss, "loss", torch.float32, (T,))
+    _same_device(ctx, X, W, target, loss)
+    with torch.cuda.device(X.device):
+        st = lib.tpmlp_xent_forward(ctypes.byref(s), _ptr(X), _ptr(W), _ptr(target), _ptr(loss), _ptr(ctx.lse),
+                                    _ptr(ctx.workspace), _stream(stream))
+    _check(st, "tpmlp_xent_forward")
+    ctx._saved = (X, W, target)
+    return loss
+
+
+def xent_backward(ctx: XentContext, dloss, dX=None, dW=None, need_dX=True, need_dW=True, stream=None):
+    """dX[T,h] and dW[V,h] for the gradients dloss[T] (fp32) of the losses that the
+    last xent_forward of this context returned; need_dX=False or need_dW=False leaves
+    one out (its entry is None)."""
+    if ctx._saved is None:
+        raise ValueError("xent_backward needs an xent_forward of the same context before it")
+    X, W, target = ctx._saved
+    s = ctx.shape
+    T, h, V = s.tokens, s.hidden, s.vocab
+    _need(dloss, "dloss", torch.float32, (T,))
+    if need_dX and dX is None:
+        dX = torch.empty((T, h), dtype=ctx.dtype, device=X.device)
+    if need_dW and dW is None:
+        dW = torch.empty((V, h), dtype=ctx.dtype, device=X.device)
+    dX, dW = dX if need_dX else None, dW if need_dW else None
+    for x, n, shp in ((dX, "dX", (T, h)), (dW, "dW", (V, h))):
+        if x is not None:
+            _need(x, n, ctx.dtype, shp)
+    _same_device(ctx, dloss, dX, dW)
+    with torch.cuda.device(X.device):
+        st = lib.tpmlp_xent_backward(ctypes.byref(s), _ptr(X), _ptr(W), _ptr(target), _ptr(ctx.lse), _ptr(dloss),
+                                     _ptr(dX), _ptr(dW), _ptr(ctx.workspace), _stream(stream))
+    _check(st, "tpmlp_xent_backward")
+    return {"dX": dX, "dW": dW}
+
+
+class OrthoContext:
+    """Workspace of the Newton-Schulz orthogonalisation of `batch` matrices [rows, cols]
+    of the given dtype (float32 or bfloat16; the output is bfloat16): `steps` steps of
+    X <- a X + (b A + c A^2) X with A = X X^T, from X = G / (|G| + eps).
+
+    One context serves one call at a time (see XentContext)."""
+
+    def __init__(self, rows, cols, batch=1, dtype=torch.bfloat16, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
+                 eps=1e-7, device=None):
+        if dtype not in _DTYPES:
+            raise ValueError("dtype %s: float32 or bfloat16" % (dtype,))
+        a, b, c = coefficients
+        self.shape = OrthoShape(int(batch), int(rows), int(cols), int(steps), _DTYPES[dtype], a, b, c, eps)
+        n = int(lib.tpmlp_ortho_workspace_bytes(ctypes.byref(self.shape)))
+        if n == 0:
+            raise ValueError("invalid orthogonalisation shape (batch=%d rows=%d cols=%d steps=%d eps=%g)"
+                             % (batch, rows, cols, steps, eps))
+        self.dtype = dtype
+        self.workspace = _status_workspace(n, device)
+
+
+def orthogonalize(ctx: OrthoContext, G, O=None, stream=None):
+    """O (bfloat16) from G, both [batch, rows, cols], or [rows, cols] where batch is 1."""
+    s = ctx.shape
+    shape = (s.batch, s.rows, s.cols)
+    if s.batch == 1 and G.dim() == 2:
+        shape = shape[1:]
+    _need(G, "G", ctx.dtype, shape)
+    if O is None:
+        O = torch.empty(shape, dtype=torch.bfloat16, device=G.device)
+    _need(O, "O", torch.bfloat16, shape)
+    _same_device(ctx, G, O)
+    with torch.cuda.device(G.device):
+        st = lib.tpmlp_orthogonalize(ctypes.byref(s), _ptr(G), _ptr(O), _ptr(ctx.workspace), _stream(stream))
+    _check(st, "tpmlp_orthogonalize")
+    return O
+
+
 def check_device_status(ctx_or_ws, stream=None) -> int:
-    ws = ctx_or_ws.workspace if isinstance(ctx_or_ws, (Context, AttnContext)) else ctx_or_ws
+    known = (Context, AttnContext, XentContext, OrthoContext)
+    ws = ctx_or_ws.workspace if isinstance(ctx_or_ws, known) else ctx_or_ws
     return int(lib.tpmlp_check_device_status(_ptr(ws), _stream(stream)))
 
 

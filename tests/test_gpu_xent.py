@@ -1,0 +1,256 @@
+"""The vocabulary cross entropy on the GPU against a plain implementation in 64 bits.
+
+Tolerances, per element and derived from the arithmetic:
+- a logit is a sum of h exact products, accumulated in fp32 with an error of at most
+  (h + 8) 2^-23 sum_k |x_k w_k| (2^-23, not 2^-24, allows an accumulator that truncates);
+  call the largest of a token e.  loss and lse move by at most 2e and e, plus 2^-20 of
+  their terms for the exponentials, the join and the logarithm;
+- dS = (p - 1[y]) g: p moves by a factor of at most exp(2e) (1 + 2^-20), then one rounding
+  to the dtype, u = eps/2 relative;
+- a probability below 2^-126, the smallest normal fp32 number, comes out of the exponential
+  as zero, and so may a dS or a sum below it: 2^-126 absolute, three times;
+- dX and dW are sums of n products of dS: the errors of dS times |W| or |X|, the
+  accumulation n 2^-23, and one rounding of the result.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+IGN = -100
+
+
+@pytest.fixture(scope="module")
+def tp():
+    from tensor_transformer_mlp_tma_gb300 import tpmlp
+    return tpmlp
+
+
+def make(T, h, V, dtype=torch.bfloat16, seed=0, ignored=0.0, scale=1.0, ignore_index=IGN):
+    g = torch.Generator(device="cpu")
+    g.manual_seed(seed)
+    X = torch.randn(T, h, generator=g) * scale
+    W = torch.randn(V, h, generator=g) * (1.3 / math.sqrt(h))
+    y = torch.randint(0, V, (T,), generator=g)
+    drop = torch.rand(T, generator=g) < ignored
+    y = torch.where(drop, torch.full_like(y, ignore_index), y)
+    dl = torch.rand(T, generator=g) * 2 / max(T, 1)
+    return X.to(dtype).cuda(), W.to(dtype).cuda(), y.cuda(), dl.cuda()
+
+
+def reference(X, W, y, dl, ignore_index=IGN):
+    X, W, dl = X.double(), W.double(), dl.double()
+    S = X @ W.t()
+    lse = torch.logsumexp(S, 1)
+    ok = y != ignore_index
+    at = torch.where(ok, y, 0)[:, None]
+    loss = torch.where(ok, lse - S.gather(1, at)[:, 0], 0.0)
+    P = torch.exp(S - lse[:, None])
+    P.scatter_add_(1, at, -ok.double()[:, None])
+    g = torch.where(ok, dl, 0.0)[:, None]
+    dS = torch.where(g != 0, P * g, 0.0)
+    return {"S": S, "lse": lse, "loss": loss, "dS": dS, "dX": dS @ W, "dW": dS.t() @ X}
+
+
+def check(X, W, y, dl, loss, lse, grads, ref):
+    T, h = X.shape
+    V = W.shape[0]
+    dt = X.dtype
+    u = torch.finfo(dt).eps / 2
+    Xa, Wa = X.double().abs(), W.double().abs()
+    e = (h + 8) * 2.0 ** -23 * (Xa @ Wa.t()).amax(1)
+    small = 2.0 ** -20 * (ref["S"].abs().amax(1) + math.log(V) + 1)
+    assert bool(((lse.double() - ref["lse"]).abs() <= e + small).all())
+    assert bool(((loss.double() - ref["loss"]).abs() <= 2 * e + 2 * small).all())
+    if grads is None:
+        return
+    # p's own error: relative on p, also where p - 1 cancels
+    P = torch.exp(ref["S"] - ref["lse"][:, None]) * (ref["dS"].abs().amax(1, keepdim=True) > 0)
+    g = torch.where(y != IGN, dl.double(), 0.0)[:, None]
+    dp = torch.expm1(2 * e + small)[:, None] * P * g.abs()
+    err_s = dp + (u + 2.0 ** -22) * (ref["dS"].abs() + dp) + 2 * 2.0 ** -126
+    for name, other, left in (("dX", Wa, False), ("dW", Xa, True)):
+        if grads[name] is None:
+            continue
+        a = ref["dS"].abs().t() if left else ref["dS"].abs()
+        s = err_s.t() if left else err_s
+        n = a.shape[1]
+        tol = (s @ other) + (n + 64) * 2.0 ** -23 * (a @ other)
+        tol = tol + u * (ref[name].abs() + tol) + 2.0 ** -126
+        bad = (grads[name].double() - ref[name]).abs() > tol
+        assert not bool(bad.any()), (name, int(bad.sum()))
+
+
+def run(tp, X, W, y, dl, **kw):
+    ctx = tp.XentContext(X.shape[0], X.shape[1], W.shape[0], X.dtype, **kw)
+    loss = tp.xent_forward(ctx, X, W, y)
+    grads = tp.xent_backward(ctx, dl)
+    assert tp.check_device_status(ctx) == tp.OK
+    return ctx, loss, grads
+
+
+SHAPES = [  # T, h, V: one token, ragged tiles in every dimension, vocabulary of one row, long rows
+    (1, 8, 1), (1, 64, 17), (3, 72, 513), (31, 128, 255), (128, 256, 512), (129, 264, 1025), (256, 512, 4096),
+    (300, 200, 3001), (257, 1000, 777), (1000, 96, 2049), (5, 4096, 8191), (2, 8192, 130),
+]
+
+
+@pytest.mark.parametrize("T,h,V", SHAPES)
+def test_bf16_against_64_bits(tp, T, h, V):
+    X, W, y, dl = make(T, h, V, seed=T + h + V, ignored=0.2)
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
+
+
+@pytest.mark.parametrize("T,h,V", [(1, 1, 1), (3, 5, 7), (64, 33, 1000), (130, 256, 777)])
+def test_f32_against_64_bits(tp, T, h, V):
+    X, W, y, dl = make(T, h, V, torch.float32, seed=T + h + V, ignored=0.2)
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("piece", [8, 64, 520, 1024, 4096])
+def test_pieces(tp, piece, dtype):
+    """Any division of the vocabulary gives the same loss and, within tolerance, gradients."""
+    X, W, y, dl = make(70, 128, 1300, dtype, seed=piece, ignored=0.3)
+    ref = reference(X, W, y, dl)
+    ctx, loss, grads = run(tp, X, W, y, dl, piece=piece)
+    check(X, W, y, dl, loss, ctx.lse, grads, ref)
+
+
+def test_ffma_path_on_bf16(tp):
+    X, W, y, dl = make(100, 192, 1111, seed=3, ignored=0.1)
+    ref = reference(X, W, y, dl)
+    for piece in (0, 512):
+        ctx, loss, grads = run(tp, X, W, y, dl, algo=tp.ALGO_SIMT, piece=piece)
+        check(X, W, y, dl, loss, ctx.lse, grads, ref)
+
+
+def test_every_token_ignored_and_ignore_index_inside_the_vocabulary(tp):
+    X, W, y, dl = make(40, 64, 300, seed=1)
+    ctx, loss, grads = run(tp, X, W, torch.full_like(y, IGN), dl)
+    assert not bool(loss.any()) and not bool(grads["dX"].any()) and not bool(grads["dW"].any())
+    y[::3] = 7
+    ctx, loss, grads = run(tp, X, W, y, dl, ignore_index=7)
+    ref = reference(X, W, y, dl, 7)
+    assert not bool(loss[::3].any())
+    assert torch.allclose(loss.double(), ref["loss"], atol=1e-4)
+    u = 2.0 ** -8  # coarse: the sharp bounds are checked above
+    assert float((grads["dX"].double() - ref["dX"]).norm() / ref["dX"].norm()) < 2 * u
+
+
+def test_large_logits_and_small_probabilities(tp):
+    """Logits of several hundred: the maximum is subtracted before any exponential."""
+    X, W, y, dl = make(64, 128, 1000, seed=2, scale=100.0)
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    ref = reference(X, W, y, dl)
+    assert float(ref["S"].abs().max()) > 300
+    check(X, W, y, dl, loss, ctx.lse, grads, ref)
+
+
+def test_non_finite_tokens_stay_alone(tp):
+    X, W, y, dl = make(300, 64, 700, seed=4)
+    X[5, 3] = float("nan")
+    X[290, 1] = float("inf")
+    y[7] = IGN
+    X[7] = float("nan")  # an ignored token's logits reach neither its loss nor dW
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[[5, 7, 290]] = False
+    assert not bool(torch.isfinite(loss[[5, 290]]).any())
+    assert float(loss[7]) == 0.0 and not bool(grads["dX"][7].any())
+    ref = reference(X[keep], W, y[keep], dl[keep])
+    assert torch.allclose(loss[keep].double(), ref["loss"], atol=1e-4)
+    assert bool(torch.isfinite(grads["dX"][keep]).all())
+
+
+def test_a_target_outside_the_vocabulary_is_reported(tp):
+    X, W, y, dl = make(50, 64, 100, seed=5)
+    for bad in (100, -1, 2 ** 40):
+        y2 = y.clone()
+        y2[11] = bad
+        ctx = tp.XentContext(50, 64, 100, X.dtype)
+        loss = tp.xent_forward(ctx, X, W, y2)
+        assert tp.check_device_status(ctx) == tp.ERR_INVALID_ARG
+        y3 = y.clone()
+        y3[11] = IGN
+        want = tp.xent_forward(ctx, X, W, y3)
+        assert tp.check_device_status(ctx) == tp.OK
+        assert torch.equal(loss, want)
+
+
+def test_outputs_left_out_and_guards_kept(tp):
+    """A frozen head or body: the other gradient has the same bits; nothing outside an output is written."""
+    X, W, y, dl = make(130, 136, 1001, seed=6, ignored=0.1)
+    ctx, loss, grads = run(tp, X, W, y, dl, piece=512)
+    only = tp.xent_backward(ctx, dl, need_dW=False)
+    assert only["dW"] is None and torch.equal(only["dX"], grads["dX"])
+    only = tp.xent_backward(ctx, dl, need_dX=False)
+    assert only["dX"] is None and torch.equal(only["dW"], grads["dW"])
+    room_x = torch.full((132, 136), 7.0, dtype=X.dtype, device="cuda")
+    room_w = torch.full((1003, 136), 7.0, dtype=X.dtype, device="cuda")
+    tp.xent_backward(ctx, dl, dX=room_x[1:131], dW=room_w[1:1002])
+    assert torch.equal(room_x[1:131], grads["dX"]) and torch.equal(room_w[1:1002], grads["dW"])
+    assert bool((room_x[[0, 131]] == 7).all()) and bool((room_w[[0, 1002]] == 7).all())
+
+
+def test_same_bits_again_and_on_another_stream(tp):
+    X, W, y, dl = make(513, 256, 5000, seed=7)
+    ctx, loss, grads = run(tp, X, W, y, dl, piece=1536)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ctx2, loss2, grads2 = run(tp, X, W, y, dl, piece=1536)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(loss, loss2) and torch.equal(ctx.lse, ctx2.lse)
+    assert torch.equal(grads["dX"], grads2["dX"]) and torch.equal(grads["dW"], grads2["dW"])
+
+
+def test_captured_and_replayed(tp):
+    X, W, y, dl = make(200, 128, 3000, seed=8)
+    ctx, loss, grads = run(tp, X, W, y, dl, piece=1024)
+    out = torch.empty_like(loss)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tp.xent_forward(ctx, X, W, y, out)
+        tp.xent_backward(ctx, dl, dX, dW)
+    X2, _, y2, _ = make(200, 128, 3000, seed=9)
+    X.copy_(X2)
+    y.copy_(y2)
+    g.replay()
+    torch.cuda.synchronize()
+    check(X, W, y, dl, out, ctx.lse, {"dX": dX, "dW": dW}, reference(X, W, y, dl))
+
+
+def test_no_tokens(tp):
+    W = torch.randn(100, 64, device="cuda").bfloat16()
+    X = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    ctx = tp.XentContext(0, 64, 100, torch.bfloat16)
+    loss = tp.xent_forward(ctx, X, W, torch.empty(0, dtype=torch.int64, device="cuda"))
+    assert loss.shape == (0,)
+    grads = tp.xent_backward(ctx, loss)
+    assert grads["dX"].shape == (0, 64) and not bool(grads["dW"].any())
+
+
+def test_gradient_against_differences(tp):
+    """dX in fp32 against central differences of the 64-bit loss along random directions: the
+    third-order term is far below, the loss is exact to 64 bits."""
+    X, W, y, dl = make(20, 48, 90, torch.float32, seed=10)
+    _, _, grads = run(tp, X, W, y, dl)
+
+    def total(Xd, Wd):
+        S = Xd @ Wd.t()
+        return float((dl.double() * (torch.logsumexp(S, 1) - S.gather(1, y[:, None])[:, 0])).sum())
+
+    for k in range(3):
+        dx, dw = torch.randn_like(X).double(), torch.randn_like(W).double()
+        eps = 1e-5
+        num = (total(X.double() + eps * dx, W.double() + eps * dw)
+               - total(X.double() - eps * dx, W.double() - eps * dw)) / (2 * eps)
+        ana = float((grads["dX"].double() * dx).sum() + (grads["dW"].double() * dw).sum())
+        scale = float((grads["dX"].double() * dx).abs().sum() + (grads["dW"].double() * dw).abs().sum())
+        assert abs(num - ana) <= 1e-5 * scale + 1e-9
