@@ -1085,7 +1085,8 @@ bool xent_valid(const tpmlp_xent_shape *s) {
     return tiles_fit(T, V) && tiles_fit(T, h) && tiles_fit(V + 256, h);
 }
 
-bool xent_tc(const tpmlp_xent_shape *s) { return s->dtype == TPMLP_BF16 && s->algo == TPMLP_ALGO_DEFAULT; }
+// Tensor cores for both types: fp32 operands as the sum of three bf16 matrices each.
+bool xent_tc(const tpmlp_xent_shape *s) { return s->algo == TPMLP_ALGO_DEFAULT; }
 
 // Vocabulary rows per piece.  The backward pass holds one piece of dS [T, piece] (and the
 // FFMA path its fp32 logits).  Each further piece costs one more addition to the fp32
@@ -1094,7 +1095,7 @@ bool xent_tc(const tpmlp_xent_shape *s) { return s->dtype == TPMLP_BF16 && s->al
 int64_t xent_piece(const tpmlp_xent_shape *s) {
     const int64_t V = s->vocab, T = s->tokens < 1 ? 1 : s->tokens;
     if (s->piece > 0) return s->piece < V ? s->piece : (V + 7) / 8 * 8;
-    const int64_t esz = xent_tc(s) ? 2 : 4;
+    const int64_t esz = s->dtype == TPMLP_F32 && xent_tc(s) ? 6 : (xent_tc(s) ? 2 : 4);
     int64_t most = (int64_t{256} << 20) / (T * esz) / 512 * 512;
     if (most < 2048) most = 2048;
     const int64_t n = (V + most - 1) / most;
@@ -1102,20 +1103,60 @@ int64_t xent_piece(const tpmlp_xent_shape *s) {
     return even < V ? even : (V + 7) / 8 * 8;
 }
 
+// How many K ranges a product of M x N outputs is split into, and their length.  An
+// output of few tiles leaves most CTA pairs idle (76 of them take 256 x 512 tiles or
+// halves of such): S ranges run at once, each into an fp32 matrix of its own, which
+// sum_splits adds up.  The model counts waves of half tiles at the rate of a pair's
+// share of the tensor rate, and 8 bytes written and read per split output at the copy
+// rate.  fp32 operands also bound the range to 2048: the tensor core cuts off
+// (does not round) the accumulator at every 16-element step, 2^-24 on average,
+// and 128 such steps stay below the fp32 result's own 1e-6.
+// Measured at T = 1001, h = 1000, V = 30011 (dX): see the table of results.
+struct Split {
+    int n;
+    int64_t len;
+};
+Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
+    const double pair_rate = 24e12 / (f32 ? 6 : 1), bytes_rate = 6e12;
+    const int64_t halves = (M + 255) / 256 * ((N + 255) / 256), units = 76;
+    Split best{1, (K + 63) / 64 * 64};
+    double best_t = 0.0;
+    const int64_t fewest = f32 ? std::min<int64_t>(64, (K + 2047) / 2048) : 1;
+    for (int64_t n = fewest; n < fewest + 16; ++n) {
+        const int64_t len = ((K + n - 1) / n + 63) / 64 * 64;
+        if (n > fewest && len < 256) break;
+        const double waves = static_cast<double>((halves * n + units - 1) / units);
+        const double t = waves * (static_cast<double>(len) * 2 * 256 * 256 / pair_rate + 1e-6) +
+                         (n > 1 ? static_cast<double>(n) * M * N * 8 / bytes_rate + 4e-6 : 0.0);
+        if (best_t == 0.0 || t < best_t) best_t = t, best = {static_cast<int>((K + len - 1) / len), len};
+    }
+    return best;
+}
+
 struct XentLayout {
-    int64_t piece, pieces, groups;
-    size_t part, target_logit, row_g, ds, logits, acc, total;
+    int64_t piece, pieces, groups, hp, ldo;
+    Split dx, dw;
+    size_t part, target_logit, row_g, xp, wp, ds, logits, acc, dwacc, total;
 };
 
 // Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | g per
-// token | dS of one piece | fp32 logits of one piece (FFMA path, bf16) | fp32 dX.
+// token | three bf16 parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA
+// path) | fp32 dX, per split | fp32 dW of one piece, per split.
 XentLayout xent_layout(const tpmlp_xent_shape *s) {
     XentLayout L;
     const size_t T = static_cast<size_t>(s->tokens), h = static_cast<size_t>(s->hidden);
+    const size_t V = static_cast<size_t>(s->vocab);
     const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
     L.piece = xent_piece(s);
     L.pieces = (s->vocab + L.piece - 1) / L.piece;
     L.groups = tc ? (s->vocab + tpmlp::XENT_GROUP - 1) / tpmlp::XENT_GROUP : L.pieces;
+    L.hp = (s->hidden + 63) / 64 * 64;
+    L.ldo = (s->hidden + 3) / 4 * 4;
+    L.dx = L.dw = {1, 0};
+    if (tc && s->tokens > 0) {
+        L.dx = xent_split(s->tokens, s->hidden, L.piece, f32);
+        L.dw = xent_split(L.piece, s->hidden, s->tokens, f32);
+    }
     size_t off = STATUS_BYTES;
     auto region = [&](size_t bytes) {
         const size_t at = off;
@@ -1123,13 +1164,21 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
         return at;
     };
     const size_t groups_stored = static_cast<size_t>(tc ? tpmlp::xent_groups(s->vocab) : L.pieces);
+    const size_t piece = static_cast<size_t>(L.piece), hp = static_cast<size_t>(L.hp), ldo = static_cast<size_t>(L.ldo);
     L.part = region(groups_stored * T * sizeof(float2));
     L.target_logit = region(T * 4);
     L.row_g = region(T * 4);
-    L.ds = region(T * static_cast<size_t>(L.piece) * (f32 ? 4 : 2));
-    // in fp32 dS takes the place of the logits
-    L.logits = f32 ? L.ds : region(tc ? 0 : T * static_cast<size_t>(L.piece) * 4);
-    L.acc = region(!f32 && L.pieces > 1 ? T * h * 4 : 0);
+    L.xp = region(tc && f32 ? 3 * T * hp * 2 : 0);
+    L.wp = region(tc && f32 ? 3 * V * hp * 2 : 0);
+    L.ds = region(T * piece * (tc ? (f32 ? 6 : 2) : (f32 ? 4 : 2)));
+    // FFMA path: in fp32 dS takes the place of the logits
+    L.logits = tc || f32 ? L.ds : region(T * piece * 4);
+    // dX and dW pass through fp32 where they are summed, or (fp32) cannot be stored by TMA
+    const bool odd = f32 && s->hidden % 4 != 0;
+    const bool dx_direct = tc ? L.dx.n == 1 && (f32 ? !odd : L.pieces == 1) : f32 || L.pieces == 1;
+    L.acc = region(dx_direct && !f32 ? 0 : static_cast<size_t>(L.dx.n) * T * ldo * 4);
+    L.dwacc = region(tc && (L.dw.n > 1 || f32) ? static_cast<size_t>(L.dw.n) * piece * ldo * 4 : 0);
+    (void)h;
     L.total = off;
     return L;
 }
@@ -1158,7 +1207,7 @@ tpmlp_status xent_check(const tpmlp_xent_shape *s, const char *who, std::initial
                               who);
         return TPMLP_ERR_UNSUPPORTED;
     }
-    if (!xent_tc(s) && (s->tokens > 65535LL * 64 || s->vocab > 65535LL * 64)) {
+    if (s->algo == TPMLP_ALGO_SIMT && (s->tokens > 65535LL * 64 || s->vocab > 65535LL * 64)) {
         tpmlp::set_last_error("%s: the FFMA path takes at most 65535 * 64 tokens and vocabulary rows", who);
         return TPMLP_ERR_UNSUPPORTED;
     }
@@ -1189,6 +1238,24 @@ struct XentCall {
         rows.status = reinterpret_cast<uint32_t *>(ws);
     }
     size_t esz() const { return s->dtype == TPMLP_BF16 ? 2 : 4; }
+    // fp32 on tensor cores: the three bf16 parts of X [3][T][hp] and W [3][V][hp].
+    bool parts() const { return xent_tc(s) && s->dtype == TPMLP_F32; }
+    const uint16_t *xp() const { return reinterpret_cast<const uint16_t *>(ws + L.xp); }
+    const uint16_t *wp(int64_t v0) const { return reinterpret_cast<const uint16_t *>(ws + L.wp) + v0 * L.hp; }
+    static void set_parts(GemmArgs &g, int64_t a_part, int64_t b_part) {
+        g.parts = 3, g.a_part = a_part, g.b_part = b_part;
+    }
+    cudaError_t split_operands(const void *X, const void *W) const {
+        if (!parts()) return cudaSuccess;
+        cudaError_t e = kernel("xent_split_x", [&] {
+            return tpmlp::launch_split3(static_cast<const float *>(X), s->tokens, s->hidden, L.hp, ws + L.xp, st);
+        });
+        if (e == cudaSuccess)
+            e = kernel("xent_split_w", [&] {
+                return tpmlp::launch_split3(static_cast<const float *>(W), s->vocab, s->hidden, L.hp, ws + L.wp, st);
+            });
+        return e;
+    }
     const void *w_rows(const void *W, int64_t v0) const {
         return static_cast<const uint8_t *>(W) + static_cast<size_t>(v0) * s->hidden * esz();
     }
@@ -1198,6 +1265,11 @@ struct XentCall {
         g.a = X, g.a_mn = false;
         g.b = w_rows(W, v0), g.b_mn = false;
         g.M = s->tokens, g.N = n, g.K = s->hidden, g.kshard = s->hidden;
+        if (parts()) {
+            g.a = xp(), g.lda = L.hp;
+            g.b = wp(v0), g.ldb = L.hp;
+            set_parts(g, s->tokens * L.hp, s->vocab * L.hp);
+        }
         g.target = rows.target, g.ignore_index = s->ignore_index, g.col0 = v0;
         return g;
     }
@@ -1236,7 +1308,8 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
     int sms;
     if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
     const XentCall c(s, target, workspace, sms, stream);
-    cudaError_t e;
+    cudaError_t e = c.split_operands(X, W);
+    if (e != cudaSuccess) return from_cuda(e);
     if (xent_tc(s)) {
         GemmArgs g = c.logits(X, W, 0, s->vocab);
         g.part = reinterpret_cast<float2 *>(c.ws + c.L.part);
@@ -1282,20 +1355,24 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     float *row_g = reinterpret_cast<float *>(c.ws + c.L.row_g);
     e = c.kernel("xent_row_g", [&] { return tpmlp::launch_xent_row_g(c.rows, dloss, row_g, c.st); });
     if (e != cudaSuccess) return from_cuda(e);
-    void *ds = c.ws + c.L.ds;
-    // dX is summed over the pieces in fp32: in place for fp32, in the workspace for
-    // bf16, and not at all when one piece holds the whole vocabulary.
-    float *acc = f32 ? static_cast<float *>(dX) : reinterpret_cast<float *>(c.ws + c.L.acc);
-    const bool direct = !f32 && c.L.pieces == 1;
+    if ((e = c.split_operands(X, W)) != cudaSuccess) return from_cuda(e);
+    uint8_t *ds = c.ws + c.L.ds;
+    const int64_t T = s->tokens, h = s->hidden;
+    // dX is summed over the pieces (and the splits of each) in fp32: in place for fp32,
+    // in the workspace for bf16, and not at all when one piece and one range hold it all.
+    const bool stores = !f32 || (h % 4 == 0 && aligned16(dX));  // fp32 rows that TMA can store
+    const bool one = !f32 && c.L.pieces == 1 && c.L.dx.n == 1;
+    const bool dx_in_place = tc ? (f32 ? c.L.dx.n == 1 && stores : one) : f32 || c.L.pieces == 1;
+    float *acc = reinterpret_cast<float *>(c.ws + c.L.acc);
     for (int64_t k = 0; k < c.L.pieces; ++k) {
         const int64_t v0 = k * c.L.piece, n = std::min(c.L.piece, s->vocab - v0);
         GemmArgs g = c.logits(X, W, v0, n);
-        int64_t ld = n;  // row pitch of dS
+        const int64_t ld = tc ? c.L.piece : n;  // row pitch of dS, and between its parts
+        const int64_t ds_part = T * ld;
         if (tc) {
-            ld = c.L.piece;
             g.out0 = ds, g.ldo = ld;
             g.row_lse = lse, g.row_g = row_g;
-            e = c.launch("xent_ds", tpmlp::EPI_XENT_GRAD, g);
+            e = c.launch("xent_ds", f32 ? tpmlp::EPI_XENT_GRAD3 : tpmlp::EPI_XENT_GRAD, g);
         } else {
             float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
             g.out0 = logits;
@@ -1307,28 +1384,54 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
         }
         if (e != cudaSuccess) return from_cuda(e);
         if (dW) {  // rows v0 .. of dW = dS_p^T X
+            void *out = const_cast<void *>(c.w_rows(dW, v0));
             GemmArgs w = base_args(c.rows.status);
             w.a = ds, w.a_mn = true, w.lda = ld;
             w.b = X, w.b_mn = true;
-            w.M = n, w.N = s->hidden, w.K = s->tokens, w.kshard = s->tokens;
-            w.out0 = const_cast<void *>(c.w_rows(dW, v0));
-            e = c.launch("xent_dw", tpmlp::EPI_STORE, w);
+            w.M = n, w.N = h, w.K = T, w.kshard = T;
+            w.out0 = out;
+            bool in_place = true;
+            if (tc) {
+                in_place = c.L.dw.n == 1 && (!f32 || (h % 4 == 0 && aligned16(out)));
+                if (c.L.dw.n > 1) w.ksplit = c.L.dw.n, w.kshard = c.L.dw.len;
+                if (!in_place) w.out0 = c.ws + c.L.dwacc, w.ldo = c.L.ldo;
+                if (f32) {
+                    w.b = c.xp(), w.ldb = c.L.hp;
+                    XentCall::set_parts(w, ds_part, T * c.L.hp);
+                }
+            }
+            e = c.launch("xent_dw", tc && (f32 || !in_place) ? tpmlp::EPI_ACC32 : tpmlp::EPI_STORE, w);
+            if (e == cudaSuccess && !in_place)
+                e = c.kernel("xent_dw_sum", [&] {
+                    return tpmlp::launch_sum_splits(!f32, reinterpret_cast<float *>(c.ws + c.L.dwacc), c.L.dw.n, n, h,
+                                                    c.L.ldo, out, c.st);
+                });
             if (e != cudaSuccess) return from_cuda(e);
         }
         if (dX) {  // dX (+)= dS_p W_p
             GemmArgs x = base_args(c.rows.status);
             x.a = ds, x.a_mn = false, x.lda = ld;
             x.b = c.w_rows(W, v0), x.b_mn = true;
-            x.M = s->tokens, x.N = s->hidden, x.K = n, x.kshard = n;
-            x.out0 = direct ? dX : static_cast<void *>(acc);
+            x.M = T, x.N = h, x.K = n, x.kshard = n;
+            x.out0 = dx_in_place ? dX : static_cast<void *>(acc);
             x.accumulate = k > 0;
-            e = c.launch("xent_dx", direct ? tpmlp::EPI_STORE : tpmlp::EPI_ACC32, x);
+            if (tc) {
+                if (c.L.dx.n > 1) x.ksplit = c.L.dx.n, x.kshard = c.L.dx.len;
+                if (!dx_in_place) x.ldo = c.L.ldo;
+                if (f32) {
+                    x.b = c.wp(v0), x.ldb = c.L.hp;
+                    XentCall::set_parts(x, ds_part, s->vocab * c.L.hp);
+                }
+            }
+            const bool rounds = dx_in_place && !f32;  // one product gives the bf16 result
+            e = c.launch("xent_dx", rounds ? tpmlp::EPI_STORE : tpmlp::EPI_ACC32, x);
             if (e != cudaSuccess) return from_cuda(e);
         }
     }
-    if (dX && !direct && !f32)
-        e = c.kernel("xent_dx_round",
-                     [&] { return tpmlp::launch_to_bf16(acc, dX, s->tokens * s->hidden, c.st); });
+    if (dX && !dx_in_place)
+        e = c.kernel("xent_dx_sum", [&] {
+            return tpmlp::launch_sum_splits(!f32, acc, tc ? c.L.dx.n : 1, T, h, tc ? c.L.ldo : h, dX, c.st);
+        });
     return from_cuda(e);
 }
 

@@ -17,11 +17,12 @@ enum Epi : int {
     EPI_ATTN_DS = 6,    // dS = P * (acc - D[row]) * scale                  -- dO V^T -> dS
     EPI_XENT_STATS = 7, // per row: max and sum of exponentials per 128 columns, the target's logit -- X W^T
     EPI_XENT_GRAD = 8,  // dS = (exp(acc - lse[row]) - [col = target]) * g[row]  -- X W^T -> dS
-    EPI_ACC32 = 9,      // out (fp32) = acc, or out += acc                  -- dX, piece by piece
+    EPI_ACC32 = 9,      // out (fp32) = acc, or out += acc                  -- dX and dW, piece by piece
     EPI_NS_GRAM = 10,   // A = scale * acc, symmetric, fp16                 -- X X^T
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
+    EPI_XENT_GRAD3 = 14, // XENT_GRAD for fp32: dS as three bf16 parts      -- X W^T -> dS
 };
 
 // A per-head operand or output read or written in place inside a token-major
@@ -83,6 +84,14 @@ struct GemmArgs {
     // Row pitches in elements of operand A and B and of the output (0: contiguous),
     // multiples of 8; batch must be 1 where one is set.
     int64_t lda, ldb, ldo;
+    // EPI_XENT_*, EPI_ACC32.  parts = 3: the operands are fp32 numbers given as the sum of
+    // three bf16 matrices, a_part / b_part elements apart, and each k-block is
+    // multiplied six times (every pair of parts but those below 2^-24).  ksplit > 1 (ACC32):
+    // the K range in ksplit parts of kshard elements, each an output [M, N] of its
+    // own, one after the other in out0.
+    int parts;
+    int64_t a_part, b_part;
+    int ksplit;
     // EPI_XENT_STATS, EPI_XENT_GRAD: rows are tokens, columns vocabulary rows
     // col0 .. col0 + N - 1 of W.
     const int64_t *target;   // [M]
@@ -173,8 +182,11 @@ struct RowArgs {
 };
 cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st);
 cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st);
-// n a multiple of 4, both 16-byte aligned.
-cudaError_t launch_to_bf16(const float *in, void *out, int64_t n, cudaStream_t st);
+// out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
+cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
+                              void *out, cudaStream_t st);
+// fp32 [rows][cols] as three bf16 matrices [rows][ld], ld >= cols, the rest zero.
+cudaError_t launch_split3(const float *in, int64_t rows, int64_t cols, int64_t ld, void *out, cudaStream_t st);
 // FFMA path: logits [tokens, n] of vocabulary rows col0 .. col0 + n - 1.
 cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,
                                     cudaStream_t st);

@@ -164,6 +164,10 @@ struct Params {
     float *target_logit;
     const float *row_lse, *row_g;
     int accumulate;  // EPI_ACC32
+    // K of the cross entropy's products: kb_seg k-blocks per pair of operand parts (one
+    // pair, or six for fp32 operands in three parts); problem z starts at k-block
+    // z * kb_seg (split K) and reads the operands of problem 0.
+    int kb_seg;
     // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
     const void *aux2;
     float alpha, beta, diag;
@@ -176,7 +180,31 @@ __host__ __device__ constexpr bool is_ns(int epi) {
     return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
 }
 __host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY; }
-__host__ __device__ constexpr bool is_xent(int epi) { return epi == EPI_XENT_STATS || epi == EPI_XENT_GRAD; }
+__host__ __device__ constexpr bool is_grad(int epi) { return epi == EPI_XENT_GRAD || epi == EPI_XENT_GRAD3; }
+__host__ __device__ constexpr bool is_xent(int epi) { return epi == EPI_XENT_STATS || is_grad(epi); }
+// Products whose K range can run over pairs of operand parts, or be split.
+__host__ __device__ constexpr bool has_segments(int epi) { return is_xent(epi) || epi == EPI_ACC32; }
+
+// The pairs of parts (a, b) of an fp32 product, two bits each, from the smallest:
+// (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).  Part i holds bits 8i .. 8i + 7 of the
+// significand, so what is left out is below 2^-23 of |a| |b|.  A plain product takes
+// the last pair only.
+constexpr uint32_t kSegA = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
+constexpr uint32_t kSegB = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
+struct KCoord {
+    int k0, za, zb;
+};
+template <int EPI>
+__device__ __forceinline__ KCoord k_coord(const Params &p, int kb, int z) {
+    if constexpr (has_segments(EPI)) {
+        const int seg = kb / p.kb_seg;
+        const int pair = p.kb_per_shard == p.kb_seg ? 5 : seg;
+        return {(kb - seg * p.kb_seg + z * p.kb_seg) * BK, static_cast<int>((kSegA >> (2 * pair)) & 3u),
+                static_cast<int>((kSegB >> (2 * pair)) & 3u)};
+    } else {
+        return {kb * BK, z, z};
+    }
+}
 
 // Coordinates after (x, y) of problem z in a map of the given rank.
 __device__ __forceinline__ void head_coords(int rank, int z, int heads, int hpt, int &c2, int &c3, int &c4) {
@@ -584,21 +612,21 @@ __device__ __forceinline__ void gelu_of_packed(const uint32_t (&h)[16], uint32_t
 constexpr float kLog2e = 1.4426950408889634f;
 struct XentRow {
     int tcol;      // the target's column of this launch, -1: none (ignored, or in another piece)
-    float lse2;    // GRAD: log-sum-exp times log2(e)
+    float lse;     // GRAD: log-sum-exp
     float g;       // GRAD: the loss's gradient, 0 for an ignored token
     float m, s;    // STATS: running maximum, sum of exp(logit - m)
 };
 template <int EPI>
 __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, XentRow &x) {
-    x.tcol = -1, x.lse2 = 0.0f, x.g = 0.0f;
+    x.tcol = -1, x.lse = 0.0f, x.g = 0.0f;
     x.m = -INFINITY, x.s = 0.0f;
     if (row >= p.M) return;
     const long long t = p.target[row];
     const bool valid = t != p.ignore_index;
     const long long c = t - p.col0;
     if (valid && c >= 0 && c < p.N) x.tcol = static_cast<int>(c);
-    if constexpr (EPI == EPI_XENT_GRAD) {
-        x.lse2 = p.row_lse[row] * kLog2e;
+    if constexpr (is_grad(EPI)) {
+        x.lse = p.row_lse[row];
         x.g = p.row_g[row];  // zero where the target is ignored
     }
 }
@@ -641,7 +669,9 @@ __device__ __forceinline__ void xent_stats_flush(const Params &p, int64_t row, i
 }
 
 // dS = (softmax - one-hot) g of 32 logits.  The one-hot term is subtracted before
-// the single rounding to bf16.  g = 0 gives exact zeros, whatever the logits.
+// the single rounding to bf16.  g = 0 gives exact zeros, whatever the logits.  The
+// difference S - lse is taken before the factor log2(e): where p is large it is
+// small, and its rounding too.
 __device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const XentRow &x) {
     const int at = x.tcol - col;
     if (x.g == 0.0f) {
@@ -650,7 +680,7 @@ __device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const X
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float pr = ptx::ex2_approx(fmaf(v[i], kLog2e, -x.lse2));
+            const float pr = ptx::ex2_approx((v[i] - x.lse) * kLog2e);
             v[i] = (at == i ? pr - 1.0f : pr) * x.g;
         }
     }
@@ -796,6 +826,36 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
         return;
     }
     if constexpr (EPI == EPI_XENT_GRAD) xent_grad_chunk(v, col, *xr);
+    if constexpr (EPI == EPI_XENT_GRAD3) {
+        // dS = d0 + d1 + d2, the first two cut (not rounded) to bf16, so that each holds
+        // the next eight bits of the significand.
+        xent_grad_chunk(v, col, *xr);
+        const bool inside = row0 < p.M && col < p.N;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float hi = part < 2 ? __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u) : v[i];
+                if (i & 1)
+                    w[i >> 1] = pack_bf16(__uint_as_float(w[i >> 1]), hi);
+                else
+                    w[i >> 1] = __float_as_uint(hi);
+                if (part < 2) v[i] -= hi;
+            }
+            if (lane == 0 && part != 1) ptx::bulk_wait_read0();  // parts 0 and 2 share a box
+            __syncwarp();
+            const uint32_t box = stg + (part == 1 ? STG_BOX : 0);
+            stage_row(box, lane, w);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && inside) {
+                ptx::tma_store_3d(tm0, box, col, row0, part);
+                ptx::bulk_commit();
+            }
+        }
+        return;
+    }
     if constexpr (EPI == EPI_ATTN_SCORE) {
         // S = scale * Q K^T with the causal mask, stored in fp16 for the softmax
         // (11 significant bits; finite values saturate at the fp16 range, the
@@ -1065,9 +1125,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t full = ptx::mapa_shared(full_local, 0);
                     const uint32_t sa = smem_base + stage * C::STAGE_BYTES;
                     const uint32_t sb = sa + C::A_STAGE + hs * (C::B_STAGE / 2);
-                    const int k0 = (down ? nkb - 1 - kb : kb) * BK;
+                    const KCoord kc = k_coord<EPI>(p, down ? nkb - 1 - kb : kb, zb);
+                    const int k0 = kc.k0, za = kc.za, zw = kc.zb;
                     if (!dbg_ok(stage >= 0 && stage < STAGES && sb + b_blocks * MN_BLOCK_BYTES <= ring_end &&
-                                    k0 >= 0 && k0 < nkb * BK,
+                                    k0 >= 0 && k0 < nkb * BK * p.batch,
                                 p, &abort_sh, 0x0301u)) {
                         ok = false;
                         break;
@@ -1081,24 +1142,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             ptx::tma_load_3d_pair(sa + j * MN_BLOCK_BYTES, &tmO2, full,
                                                   BM * static_cast<int>(rank) + 64 * j, 0, 0);
                     } else if constexpr (!A_MN) {
-                        ptx::tma_load_3d_pair(sa, &tmA, full, k0, m0, zb);
+                        ptx::tma_load_3d_pair(sa, &tmA, full, k0, m0, za);
                     } else {
                         if (p.a_mn4) {
-                            ptx::tma_load_4d_pair(sa, &tmA, full, 0, k0, m0 / 64, zb);
+                            ptx::tma_load_4d_pair(sa, &tmA, full, 0, k0, m0 / 64, za);
                         } else {
 #pragma unroll
                             for (int j = 0; j < BM / 64; ++j)
-                                ptx::tma_load_3d_pair(sa + j * MN_BLOCK_BYTES, &tmA, full, m0 + 64 * j, k0, zb);
+                                ptx::tma_load_3d_pair(sa + j * MN_BLOCK_BYTES, &tmA, full, m0 + 64 * j, k0, za);
                         }
                     }
                     if constexpr (!B_MN) {
-                        ptx::tma_load_3d_pair(sb, bmap, full, k0, n0, zb);
+                        ptx::tma_load_3d_pair(sb, bmap, full, k0, n0, zw);
                     } else {
                         if (p.b_mn4) {
-                            ptx::tma_load_4d_pair(sb, bmap, full, 0, k0, n0 / 64, zb);
+                            ptx::tma_load_4d_pair(sb, bmap, full, 0, k0, n0 / 64, zw);
                         } else {
                             for (int j = 0; j < b_blocks; ++j)
-                                ptx::tma_load_3d_pair(sb + j * MN_BLOCK_BYTES, &tmB, full, n0 + 64 * j, k0, zb);
+                                ptx::tma_load_3d_pair(sb + j * MN_BLOCK_BYTES, &tmB, full, n0 + 64 * j, k0, zw);
                         }
                     }
                     ++issued;
@@ -1188,23 +1249,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t full = PAIR ? ptx::mapa_shared(full_local, 0) : full_local;
                     const uint32_t sa = smem_base + stage * C::STAGE_BYTES;
                     const uint32_t sb = sa + C::A_STAGE;
-                    const int k0 = (down ? kb0 + kb1 - 1 - kb : kb) * BK;
+                    const KCoord kc = k_coord<EPI>(p, down ? kb0 + kb1 - 1 - kb : kb, zb);
+                    const int k0 = kc.k0, za = kc.za, zw = kc.zb;
                     if (!dbg_ok(stage >= 0 && stage < STAGES && sb + C::B_STAGE <= ring_end, p, &abort_sh, 0x0501u)) {
                         ok = false;
                         break;
                     }
-                    auto load = [&](uint32_t dst, const CUtensorMap *map, int x, int y) {
+                    auto load = [&](uint32_t dst, const CUtensorMap *map, int x, int y, int z) {
                         if constexpr (PAIR)
-                            ptx::tma_load_3d_pair(dst, map, full, x, y, zb);
+                            ptx::tma_load_3d_pair(dst, map, full, x, y, z);
                         else
-                            ptx::tma_load_3d(dst, map, full, x, y, zb);
+                            ptx::tma_load_3d(dst, map, full, x, y, z);
                     };
                     // one copy of every 64-wide MN block of the stage: (0, k, block, problem)
-                    auto load4 = [&](uint32_t dst, const CUtensorMap *map, int k, int blk) {
+                    auto load4 = [&](uint32_t dst, const CUtensorMap *map, int k, int blk, int z) {
                         if constexpr (PAIR)
-                            ptx::tma_load_4d_pair(dst, map, full, 0, k, blk, zb);
+                            ptx::tma_load_4d_pair(dst, map, full, 0, k, blk, z);
                         else
-                            ptx::tma_load_4d(dst, map, full, 0, k, blk, zb);
+                            ptx::tma_load_4d(dst, map, full, 0, k, blk, z);
                     };
                     // The leader announces the bytes of both CTAs' copies; the peer's
                     // copies only complete bytes on the leader's barrier (they can land
@@ -1233,21 +1295,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                     } else {
                     if constexpr (!A_MN) {
-                        load(sa, &tmA, k0, m0);
+                        load(sa, &tmA, k0, m0, za);
                     } else if (p.a_mn4) {
-                        load4(sa, &tmA, k0, m0 / 64);
+                        load4(sa, &tmA, k0, m0 / 64, za);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK_BYTES, &tmA, m0 + 64 * j, k0);
+                        for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK_BYTES, &tmA, m0 + 64 * j, k0, za);
                     }
                     if constexpr (!B_MN) {
-                        load(sb, &tmB, k0, n0);
+                        load(sb, &tmB, k0, n0, zw);
                     } else if (p.b_mn4) {
-                        load4(sb, &tmB, k0, n0 / 64);
+                        load4(sb, &tmB, k0, n0 / 64, zw);
                     } else {
 #pragma unroll
                         for (int j = 0; j < C::B_ROWS / 64; ++j)
-                            load(sb + j * MN_BLOCK_BYTES, &tmB, n0 + 64 * j, k0);
+                            load(sb + j * MN_BLOCK_BYTES, &tmB, n0 + 64 * j, k0, zw);
                     }
                     }
                     ++issued;
@@ -1759,7 +1821,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // (cols, rows, batch); a plain matrix has batch 1.
 static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, uint32_t box_cols,
                      uint32_t box_rows, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int64_t batch = 1,
-                     CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int64_t ld = 0) {
+                     CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int64_t ld = 0,
+                     int64_t batch_step = 0) {
     auto fn = encode_fn();
     if (!fn) {
         set_last_error("cuTensorMapEncodeTiled is not available from the driver");
@@ -1769,8 +1832,8 @@ static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(batch)};
     if (ld == 0) ld = cols;  // row pitch in elements
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * esz,
-                             static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * esz};
+    if (batch_step == 0) batch_step = ld * rows;
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * esz, static_cast<cuuint64_t>(batch_step) * esz};
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(m, dt, 3,
@@ -1790,14 +1853,14 @@ static bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
 // row pitch of the second; returns false if the driver does not take the map
 // (the caller then keeps the per-block 3-D map).
 static bool make_map_mn4(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, uint32_t box_k,
-                         uint32_t nblk, int64_t batch, int64_t ld = 0) {
+                         uint32_t nblk, int64_t batch, int64_t ld = 0, int64_t batch_step = 0) {
     auto fn = encode_fn();
     if (!fn || cols % 64 != 0) return false;
     cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
                           static_cast<cuuint64_t>(batch)};
     if (ld == 0) ld = cols;
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128,
-                             static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * 2};
+    if (batch_step == 0) batch_step = ld * rows;
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(batch_step) * 2};
     cuuint32_t box[4] = {64, box_k, nblk, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
@@ -1904,6 +1967,9 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // A operand: K-major [M,K] with a 64 x 128 box, or MN-major [K,M] with 64 x 64 boxes.
     // B operand: this CTA's B_ROWS columns, K-major in one box or MN-major in 64-wide boxes.
     const int64_t nb = g.batch < 1 ? 1 : g.batch;
+    constexpr bool SEG = has_segments(EPI);
+    const int64_t ni = SEG ? (g.parts > 1 ? g.parts : 1) : nb;  // matrices per operand
+    const int64_t no = EPI == EPI_XENT_GRAD3 ? 3 : (SEG && g.ksplit > 1 ? g.ksplit : nb);  // and of the output
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;  // the copies move 16-bit words: fp16 too
     // MN-major operands whose MN extent is a multiple of 64 take the 4-D map
@@ -1919,22 +1985,22 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // (HEADS kernels always copy MN-major operands block by block.)
     constexpr bool WIDE = TILE_N == 512;
     CUtensorMap mb2;  // wide tiles: B of one 256-column half of the tile (half the box)
-    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, nb, g.lda);
+    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, ni, g.lda, g.a_part);
     const bool b4 = !HEADS && B_MN && mn4 && g.N % 64 == 0 &&
-                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, nb, g.ldb) &&
-                    (!WIDE || make_map_mn4(&mb2, g.b, g.K, g.N, BK, C::B_ROWS / 128, nb, g.ldb));
+                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, ni, g.ldb, g.b_part) &&
+                    (!WIDE || make_map_mn4(&mb2, g.b, g.K, g.N, BK, C::B_ROWS / 128, ni, g.ldb, g.b_part));
     bool oka, okb;
     if (a_rank > 3)
         oka = make_map_view(&ma, g.a, g.a_view, 64, A_MN ? BK : BM, sw);
     else
-        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, nb, bf, g.lda)
-                          : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, nb, bf, g.lda));
+        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, ni, bf, g.lda, g.a_part)
+                          : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, ni, bf, g.lda, g.a_part));
     if (b_rank > 3)
         okb = make_map_view(&mb, g.b, g.b_view, 64, B_MN ? BK : C::B_ROWS, sw);
     else
-        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, nb, bf, g.ldb)
-                          : make_map(&mb, g.b, g.N, g.K, BK, C::B_ROWS, sw, nb, bf, g.ldb));
-    if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, nb, bf, g.ldb);
+        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, ni, bf, g.ldb, g.b_part)
+                          : make_map(&mb, g.b, g.N, g.K, BK, C::B_ROWS, sw, ni, bf, g.ldb, g.b_part));
+    if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, ni, bf, g.ldb, g.b_part);
     if (!WIDE || (B_MN && !b4)) mb2 = mb;  // unused, or the per-block maps serve both widths
     if (!oka || !okb) return cudaErrorInvalidValue;
     // Output maps: [M, N] row-major, 32 x 32 boxes, 64-byte swizzle (matches stage_row).
@@ -1942,7 +2008,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // the others write out0 only.
     // The GeLU' epilogue can also write Y rebuilt from H (third map).
     CUtensorMap mo0, mo1, mo2;
-    const void *o0 = EPI == EPI_XENT_STATS ? g.a : (g.out0 ? g.out0 : g.out1);  // STATS stores no matrix
+    const void *o0 = g.out0 ? g.out0 : g.out1;
     // The attention scores are fp16 (32 x 32 box, 64-byte swizzle, as the bf16
     // outputs); dS reads P through the second map; both of its maps have 32 x 64
     // boxes with 128-byte swizzle (see stage_half_row128).
@@ -1956,10 +2022,9 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     const bool wide = EPI == EPI_ATTN_DS;
     const uint32_t obox = wide ? 64 : 32;
     const CUtensorMapSwizzle so = wide || EPI == EPI_ACC32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    // What the output map covers: STATS stores no matrix (any valid map will do);
-    // LAST stores the unpadded part of the tiles.
+    // What the output map covers: LAST stores the unpadded part of the tiles.
     const int64_t orows = EPI == EPI_NS_LAST ? g.out_rows : g.M;
-    const int64_t ocols = EPI == EPI_XENT_STATS ? g.K : (EPI == EPI_NS_LAST ? g.out_cols : g.N);
+    const int64_t ocols = EPI == EPI_NS_LAST ? g.out_cols : g.N;
     if (wide && (o_rank > 3 || g.nshards != 1)) {
         set_last_error("dS epilogue: a plain [problems][M][N] output and one shard only");
         return cudaErrorInvalidValue;
@@ -1970,12 +2035,21 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         set_last_error("bias-gradient tile: needs the ones block, one problem, one shard, no causal ranges");
         return cudaErrorInvalidValue;
     }
-    if (!(o_rank > 3 ? make_map_view(&mo0, o0, g.o_view, 32, 32, so)
-                     : make_map(&mo0, o0, orows, ocols, obox, 32, so, nb, odt, g.ldo)) ||
-        !make_map(&mo1, o1, orows, ocols, obox, 32, so, nb, odt, g.ldo) ||
-        !(bias_tile ? make_map(&mo2, g.ones, 64, 64, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, 1)
-                    : make_map(&mo2, o2, orows, ocols, 32, 32, so, nb, odt, g.ldo)))
-        return cudaErrorInvalidValue;
+    // A map that no epilogue uses is a copy of one that exists (encoding takes host time).
+    if constexpr (EPI == EPI_XENT_STATS) {
+        mo0 = mo1 = mo2 = ma;
+    } else {
+        if (!(o_rank > 3 ? make_map_view(&mo0, o0, g.o_view, 32, 32, so)
+                         : make_map(&mo0, o0, orows, ocols, obox, 32, so, no, odt, g.ldo)))
+            return cudaErrorInvalidValue;
+        mo1 = mo2 = mo0;
+        if (o1 != o0 && !make_map(&mo1, o1, orows, ocols, obox, 32, so, no, odt, g.ldo)) return cudaErrorInvalidValue;
+        if (bias_tile) {
+            if (!make_map(&mo2, g.ones, 64, 64, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, 1)) return cudaErrorInvalidValue;
+        } else if (o2 != o0 && !make_map(&mo2, o2, orows, ocols, obox, 32, so, no, odt, g.ldo)) {
+            return cudaErrorInvalidValue;
+        }
+    }
 
     Params p;
     p.M = static_cast<int>(g.M);
@@ -1996,7 +2070,9 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.status = g.status;
     p.wait_ns = g.wait_ns;
     p.colsum_part = g.colsum_part;
-    p.batch = static_cast<int>(nb);
+    p.batch = static_cast<int>(SEG && g.ksplit > 1 ? g.ksplit : nb);
+    p.kb_seg = p.kb_per_shard;
+    if (SEG && g.parts > 1) p.kb_per_shard *= 6;
     p.scale = g.scale;
     p.causal = g.causal ? 1 : 0;
     p.rowvec = g.rowvec;
@@ -2101,7 +2177,7 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
     if constexpr (is_ns(EPI)) {
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
-    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || EPI == EPI_ACC32 || is_xent(EPI)) {
+    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || has_segments(EPI)) {
         if (tc_wide_tile(static_cast<Epi>(EPI), g)) return launch_t<EPI, A_MN, B_MN, 2, false, 512>(g, num_sms, st);
     }
     if constexpr (EPI == EPI_STORE && !A_MN && !B_MN) {
@@ -2131,7 +2207,7 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
-    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || epi == EPI_ACC32 || tc::is_xent(epi))) return false;
+    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || tc::has_segments(epi))) return false;
     const char *w = std::getenv("TPMLP_WIDE");
     return !(w && w[0] == '0');
 }
@@ -2167,8 +2243,12 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
         case EPI_XENT_GRAD:
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_GRAD, false, false>(g, num_sms, st);
             break;
-        case EPI_ACC32:  // dS[T,V'] (K-major) . W[V',h] (MN-major)
+        case EPI_XENT_GRAD3:
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_GRAD3, false, false>(g, num_sms, st);
+            break;
+        case EPI_ACC32:  // dS[T,V'] (K-major) . W[V',h] (MN-major); dS^T . X[T,h] (both MN-major)
             if (!g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, false, true>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, true, true>(g, num_sms, st);
             break;
         case EPI_NS_GRAM:  // X X^T of a wide X (K-major), X^T X of a tall one (MN-major)
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAM, false, false>(g, num_sms, st);

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace tpmlp {
 namespace xent {
@@ -40,6 +41,8 @@ __device__ __forceinline__ bool target_ok(const RowArgs &a, int64_t row) {
 constexpr int COMBINE_WARPS = 32;
 __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowArgs a, float *loss, float *lse) {
     __shared__ float2 sh[COMBINE_WARPS][32];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float m = -INFINITY, s = 0.0f;
@@ -70,17 +73,76 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowAr
 
 // g of every token for the backward pass: 0 where the target does not take part.
 __global__ void row_g_kernel(const RowArgs a, const float *dloss, float *row_g) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (row < a.tokens) row_g[row] = target_ok(a, row) ? dloss[row] : 0.0f;
 }
 
-// The fp32 sum of the pieces' dX, rounded once.  Memory bound: 6 bytes per element.
-__global__ void to_bf16_kernel(const float4 *in, uint2 *out, int64_t n4) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const float4 v = in[i];
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        out[i] = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+// Fixed-order sum of the fp32 matrices that split products left, rounded once to the
+// output's type.  V columns per thread.  Memory bound: 4 bytes per split and element.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int splits, int64_t rows, int64_t cols,
+                                                         int64_t ld, T *out) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int64_t per_row = cols / V, n = rows * per_row, step = rows * ld;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * V;
+        const float *src = in + r * ld + c;
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 0.0f;
+        for (int k = 0; k < splits; ++k, src += step) {
+            if constexpr (V == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(src);
+                v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+            } else {
+                v[0] += *src;
+            }
+        }
+        T *dst = out + r * cols + c;
+        if constexpr (sizeof(T) == 4 && V == 4) {
+            *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if constexpr (sizeof(T) == 4) {
+            dst[0] = v[0];
+        } else if constexpr (V == 4) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2 *>(dst) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        } else {
+            dst[0] = __float2bfloat16_rn(v[0]);
+        }
+    }
+}
+
+// x = p0 + p1 + p2 in bf16: the first two cut off after eight bits of the significand, so
+// that the three together hold its 24 bits (a value too large to round to bf16 does not
+// become infinite; an infinite one has parts inf, 0, 0).  Four columns per thread.
+// Memory bound: 4 bytes read, 6 written per element.
+__global__ void __launch_bounds__(256) split3_kernel(const float *in, int64_t rows, int64_t cols, int64_t ld,
+                                                     __nv_bfloat16 *out) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int64_t n = rows * ld;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 1024) {
+        const int64_t r = i / ld, c = i - r * ld;
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = c + j < cols ? in[r * cols + c + j] : 0.0f;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            __nv_bfloat16 h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float hi = part < 2 ? __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u) : v[j];
+                h[j] = __float2bfloat16_rn(hi);
+                v[j] = isinf(v[j]) ? 0.0f : v[j] - hi;
+            }
+            *reinterpret_cast<uint2 *>(out + part * n + i) = *reinterpret_cast<const uint2 *>(h);
+        }
     }
 }
 
@@ -133,23 +195,56 @@ __global__ void __launch_bounds__(ROW_THREADS) piece_grad_kernel(const RowArgs a
     }
 }
 
+// Launches with programmatic stream serialisation: the kernel waits for the one before it
+// itself (griddep_wait), so that its launch overlaps that kernel's tail.
+template <typename... P, typename... A>
+static cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Blocks of 256 threads for n units of work, as many as stay resident.
+static int64_t blocks_for(int64_t n) {
+    const int64_t b = (n + 255) / 256;
+    return b < 152 * 8 ? b : 152 * 8;
+}
+
 }  // namespace xent
 
 cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st) {
-    xent::combine_kernel<<<static_cast<unsigned>((a.tokens + 31) / 32), 32 * xent::COMBINE_WARPS, 0, st>>>(a, loss, lse);
-    return cudaGetLastError();
+    return xent::launch(xent::combine_kernel, (a.tokens + 31) / 32, 32 * xent::COMBINE_WARPS, st, a, loss, lse);
 }
 
 cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st) {
-    xent::row_g_kernel<<<static_cast<unsigned>((a.tokens + 255) / 256), 256, 0, st>>>(a, dloss, row_g);
-    return cudaGetLastError();
+    return xent::launch(xent::row_g_kernel, (a.tokens + 255) / 256, 256, st, a, dloss, row_g);
 }
 
-cudaError_t launch_to_bf16(const float *in, void *out, int64_t n, cudaStream_t st) {
-    const int64_t n4 = n / 4, blocks = (n4 + 255) / 256;
-    xent::to_bf16_kernel<<<static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(
-        reinterpret_cast<const float4 *>(in), static_cast<uint2 *>(out), n4);
-    return cudaGetLastError();
+cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
+                              void *out, cudaStream_t st) {
+    const bool vec = cols % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const int64_t blocks = xent::blocks_for(rows * cols / (vec ? 4 : 1));
+    if (is_bf16) {
+        auto o = static_cast<__nv_bfloat16 *>(out);
+        return vec ? xent::launch(xent::sum_splits_kernel<__nv_bfloat16, 4>, blocks, 256, st, in, splits, rows, cols, ld, o)
+                   : xent::launch(xent::sum_splits_kernel<__nv_bfloat16, 1>, blocks, 256, st, in, splits, rows, cols, ld, o);
+    }
+    auto o = static_cast<float *>(out);
+    return vec ? xent::launch(xent::sum_splits_kernel<float, 4>, blocks, 256, st, in, splits, rows, cols, ld, o)
+               : xent::launch(xent::sum_splits_kernel<float, 1>, blocks, 256, st, in, splits, rows, cols, ld, o);
+}
+
+cudaError_t launch_split3(const float *in, int64_t rows, int64_t cols, int64_t ld, void *out, cudaStream_t st) {
+    return xent::launch(xent::split3_kernel, xent::blocks_for(rows * ld / 4), 256, st, in, rows, cols, ld,
+                        static_cast<__nv_bfloat16 *>(out));
 }
 
 cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,

@@ -94,6 +94,7 @@ def run(tp, X, W, y, dl, **kw):
 SHAPES = [  # T, h, V: one token, ragged tiles in every dimension, vocabulary of one row, long rows
     (1, 8, 1), (1, 64, 17), (3, 72, 513), (31, 128, 255), (128, 256, 512), (129, 264, 1025), (256, 512, 4096),
     (300, 200, 3001), (257, 1000, 777), (1000, 96, 2049), (5, 4096, 8191), (2, 8192, 130),
+    (40, 64, 30011), (6000, 72, 100),  # K of dX and of dW long, few tiles: split
 ]
 
 
@@ -104,7 +105,8 @@ def test_bf16_against_64_bits(tp, T, h, V):
     check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
 
 
-@pytest.mark.parametrize("T,h,V", [(1, 1, 1), (3, 5, 7), (64, 33, 1000), (130, 256, 777)])
+@pytest.mark.parametrize("T,h,V", [(1, 1, 1), (3, 5, 7), (64, 33, 1000), (130, 256, 777), (300, 770, 2500),
+                                   (17, 40, 20011), (5000, 36, 90), (4100, 9, 33)])
 def test_f32_against_64_bits(tp, T, h, V):
     X, W, y, dl = make(T, h, V, torch.float32, seed=T + h + V, ignored=0.2)
     ctx, loss, grads = run(tp, X, W, y, dl)
@@ -121,8 +123,9 @@ def test_pieces(tp, piece, dtype):
     check(X, W, y, dl, loss, ctx.lse, grads, ref)
 
 
-def test_ffma_path_on_bf16(tp):
-    X, W, y, dl = make(100, 192, 1111, seed=3, ignored=0.1)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_ffma_path(tp, dtype):
+    X, W, y, dl = make(100, 192, 1111, dtype, seed=3, ignored=0.1)
     ref = reference(X, W, y, dl)
     for piece in (0, 512):
         ctx, loss, grads = run(tp, X, W, y, dl, algo=tp.ALGO_SIMT, piece=piece)
