@@ -1455,18 +1455,22 @@ float ortho_shift(float a) { return a > 0.0f ? std::exp2(std::round(std::log2(0.
 // Follows the largest singular value through the steps: starting from the interval
 // [0, 1] (the Frobenius norm bounds it), the image of [0, r] under s -> a s + b s^3 +
 // c s^5 is sampled; every iterate must stay inside the fp16 scales above.
-bool ortho_range_ok(const tpmlp_ortho_shape *s) {
+// q_bound: a bound of the product of the steps' factors a + b l + c l^2.
+bool ortho_range_ok(const tpmlp_ortho_shape *s, double &q_bound) {
     const double a = s->a, b = s->b, c = s->c, d = ortho_shift(s->a);
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     if (std::fabs(a - d) > 64.0) return false;
     double r = 1.0;
+    q_bound = 1.0;
     for (int k = 0; k < s->steps; ++k) {
-        double next = 0.0;
+        double next = 0.0, factor = 0.0;
         for (int i = 0; i <= 1024; ++i) {
             const double x = r * i / 1024.0, l = x * x;
-            if (std::fabs(d + b * l + c * l * l) > 7.5) return false;
+            if (std::fabs(d + b * l + c * l * l) > 7.5 || std::fabs(a + b * l + c * l * l) > 7.5) return false;
+            factor = std::max(factor, std::fabs(a + b * l + c * l * l));
             next = std::max(next, std::fabs(x * (a + b * l + c * l * l)));
         }
+        q_bound *= factor * 1.01;
         r = next * 1.01;  // rounding, and what lies between the samples
         if (r > 1.9) return false;
     }
@@ -1485,17 +1489,26 @@ bool ortho_valid(const tpmlp_ortho_shape *s) {
 
 struct OrthoLayout {
     int64_t P, Q, p;
-    bool wide;  // rows <= cols: A = X X^T, else A = X^T X
+    bool wide;   // rows <= cols: A = X X^T, else A = X^T X
+    bool chain;  // the steps on the Gram matrix alone (ns_chain.cu)
+    int splits;  // chain: K ranges of the Gram product, and their length
+    int64_t split_len;
+    float q_scale;
     size_t norm, hi[2], lo[2], A, C, total;
 };
 
-// Workspace, 1 KB-aligned regions: status | block sums of the norm | two of X's high
-// and low parts, used in turn | A | C.
+// Workspace, 1 KB-aligned regions: status | block sums of the norm | X's high and low parts
+// (without the chain two of each, used in turn; with it only once, and a padded output
+// where TMA cannot store the unpadded one) | A | C (chain: the splits' A in fp32 | Q).
 OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
     OrthoLayout L;
     L.P = (s->rows + 63) / 64 * 64, L.Q = (s->cols + 63) / 64 * 64;
     L.wide = s->rows <= s->cols;
     L.p = L.wide ? L.P : L.Q;
+    // The chain wants Q in fp16's range with room for its low part.
+    double q_bound = 0.0;
+    L.chain = L.p <= tpmlp::NS_CHAIN_P && ortho_range_ok(s, q_bound) && q_bound < 32768.0;
+    L.q_scale = L.chain ? static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(q_bound, 1.0))))) : 1.0f;
     size_t off = STATUS_BYTES;
     auto region = [&](size_t bytes) {
         const size_t at = off;
@@ -1505,9 +1518,24 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
     const size_t n = static_cast<size_t>(s->batch);
     L.norm = region(n * static_cast<size_t>(tpmlp::ortho_norm_blocks(s->batch, s->rows * s->cols)) * 12);
     const size_t x = n * static_cast<size_t>(L.P) * L.Q * 2, a = n * static_cast<size_t>(L.p) * L.p * 2;
-    for (int i = 0; i < 2; ++i) L.hi[i] = region(x), L.lo[i] = region(x);
-    L.A = region(a);
-    L.C = region(a);
+    if (L.chain) {
+        // one tile per matrix: split K until the SMs have one each, 256 or more at a time
+        const int64_t K = L.wide ? L.Q : L.P;
+        const int64_t want = std::min<int64_t>(152 / std::max<int64_t>(1, s->batch), (K + 255) / 256);
+        L.split_len = (K / std::max<int64_t>(1, want) + 63) / 64 * 64;
+        L.splits = static_cast<int>((K + L.split_len - 1) / L.split_len);
+        L.hi[0] = region(2 * x);
+        L.lo[0] = L.hi[0] + x;
+        L.hi[1] = region(s->cols % 8 ? x : 0);
+        L.lo[1] = 0;
+        L.A = region(2 * a * static_cast<size_t>(L.splits));
+        L.C = region(2 * a);
+    } else {
+        L.splits = 0, L.split_len = 0;
+        for (int i = 0; i < 2; ++i) L.hi[i] = region(x), L.lo[i] = region(x);
+        L.A = region(a);
+        L.C = region(a);
+    }
     L.total = off;
     return L;
 }
@@ -1532,7 +1560,8 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
                               "multiple of 8, else 2)");
         return TPMLP_ERR_UNSUPPORTED;
     }
-    if (!ortho_range_ok(s)) {
+    double q_bound;
+    if (!ortho_range_ok(s, q_bound)) {
         tpmlp::set_last_error("tpmlp_orthogonalize: the coefficients let the iterates leave the fp16 range");
         return TPMLP_ERR_UNSUPPORTED;
     }
@@ -1551,6 +1580,7 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
     a.eps = s->eps, a.scale = kScaleX;
     a.part = ws + L.norm;
     a.hi = ws + L.hi[0], a.lo = ws + L.lo[0];
+    a.lo_scale = L.chain ? 1.0f : 2048.0f;
     cudaError_t e;
     {
         Timed timed("ortho_start", st);
@@ -1577,6 +1607,39 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         if (r == cudaSuccess) g_launches.fetch_add(1);
         return r;
     };
+    if (L.chain) {
+        GemmArgs g = product(ws + L.hi[0], !L.wide, ws + L.hi[0], !L.wide, L.p, L.p, L.wide ? L.Q : L.P, ws + L.A);
+        g.ksplit = L.splits, g.kshard = L.split_len;
+        e = launch("ortho_gram32", tpmlp::EPI_NS_GRAM32, g);
+        if (e != cudaSuccess) return from_cuda(e);
+        tpmlp::NsChain c;
+        c.matrices = s->batch, c.P = L.p;
+        c.gram = reinterpret_cast<const float *>(ws + L.A), c.splits = L.splits;
+        c.unit = 1.0f / (kScaleX * kScaleX);
+        c.steps = s->steps, c.a = s->a, c.b = s->b, c.c = s->c, c.q_scale = L.q_scale;
+        c.Q = ws + L.C;
+        c.status = status, c.wait_ns = g_wait_ns.load();
+        {
+            Timed timed("ortho_chain", st);
+            e = tpmlp::launch_ns_chain(c, st);
+            if (e == cudaSuccess) g_launches.fetch_add(1);
+        }
+        if (e != cudaSuccess) return from_cuda(e);
+        void *out = tma_out ? O : ws + L.hi[1];
+        GemmArgs u = L.wide ? product(c.Q, false, ws + L.hi[0], true, L.P, L.Q, L.p, out)
+                            : product(ws + L.hi[0], false, c.Q, false, L.P, L.Q, L.p, out);
+        u.cta_pair = false;  // 128 rows hold all of a wide matrix
+        u.scale = 1.0f / (kScaleX * L.q_scale);
+        u.out_rows = tma_out ? s->rows : L.P, u.out_cols = tma_out ? s->cols : L.Q;
+        e = launch("ortho_final", tpmlp::EPI_NS_FINAL, u);
+        if (e == cudaSuccess && !tma_out) {
+            Timed timed("ortho_unpad", st);
+            e = tpmlp::launch_ortho_unpad(out, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
+            if (e == cudaSuccess) g_launches.fetch_add(1);
+        }
+        return from_cuda(e);
+    }
+
     const float shift = ortho_shift(s->a);
     void *A = ws + L.A, *C = ws + L.C;
     for (int k = 0; k < s->steps; ++k) {

@@ -22,6 +22,8 @@ enum Epi : int {
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
+    EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts               -- X X^T
+    EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
     EPI_XENT_GRAD3 = 14, // XENT_GRAD for fp32: dS as three bf16 parts      -- X W^T -> dS
 };
 
@@ -200,9 +202,24 @@ struct OrthoStart {
     float eps, scale;
     void *part;     // ortho_norm_blocks(batch, rows * cols) * batch * 12 bytes
     void *hi, *lo;  // fp16 [batch][P][Q]
+    float lo_scale; // lo holds the remainder times this
 };
 int64_t ortho_norm_blocks(int64_t batch, int64_t n);
 cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t st);
+// The steps on p x p Gram matrices, p <= 128 (ns_chain.cu).
+constexpr int NS_CHAIN_P = 128;
+struct NsChain {
+    int64_t matrices, P;  // P: 64 or 128
+    const float *gram;    // [splits][matrices][P][P]
+    int splits;
+    float unit;           // A_0 = unit * the sum of the splits
+    int steps;
+    float a, b, c, q_scale;
+    void *Q;              // fp16 [2][matrices][P][P]: high and low part of q_scale * Q
+    uint32_t *status;
+    uint64_t wait_ns;
+};
+cudaError_t launch_ns_chain(const NsChain &c, cudaStream_t st);
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                void *out, cudaStream_t st);
 

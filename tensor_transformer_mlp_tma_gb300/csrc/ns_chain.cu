@@ -1,0 +1,258 @@
+// Newton-Schulz steps on the Gram matrix alone.  With A_k = X_k X_k^T and
+// B_k = a I + b A_k + c A_k^2, the step X_{k+1} = B_k X_k gives
+//   A_{k+1} = B_k A_k B_k,   X_n = Q X_0,  Q = B_{n-1} ... B_1 B_0,
+// so that n steps on a p x q matrix need X_0 twice, once for A_0 and once for Q X_0, and
+// everything between is p x p.  For p <= 128 one CTA per matrix holds A, B and Q in
+// shared memory and runs all steps without leaving the SM.
+//
+// Precision: A holds the squares of X's singular values and Q grows to a^n on the
+// small ones, so 11-bit operands would not do.  Every matrix is the sum of two fp16
+// matrices (22 bits) and a product is three: hi hi + hi lo + lo hi, in one fp32
+// accumulator.  Against 64 bits that leaves errors of 1e-6 (Gaussian matrices) to
+// 6e-4 (one singular value 1000 times the others), below the bf16 output's own.
+// All factors are polynomials of A_0 and commute, but their roundings do not: an error
+// that couples a large singular value i and a small one j is multiplied by
+// B_i B_j (at most about 2.4) in B A B and by B_j^2 (up to 11.8 a step) in A B B, and by
+// B_i (below 1) or B_j (3.4) in B Q or Q B.  The other forms lose three digits in
+// five steps.
+//
+// Bound by latency: a step is three dependent rounds of MMAs (24 of 128 x 128 x 16 each)
+// with a trip through tensor memory, registers and shared memory between them.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace tpmlp {
+namespace chain {
+
+constexpr int PT = NS_CHAIN_P;           // rows and columns of the tile, 128
+constexpr int THREADS = 256;             // warp w: TMEM lanes 32 (w % 4).., columns 64 (w / 4)..
+constexpr uint32_t PART = PT * PT * 2;   // one fp16 matrix: two blocks of 64 columns, 128-byte swizzled
+constexpr uint32_t MAT = 2 * PART;       // high and low part
+constexpr size_t SMEM = 3 * MAT + 1024;  // A, B, Q, and alignment
+constexpr uint32_t TMEM_COLS = 256;      // two accumulators of 128 columns
+constexpr uint32_t STATUS_TIMEOUT = 4;   // TPMLP_ERR_TIMEOUT
+
+// The scales that A and B are stored with (powers of two; see kScaleX in api.cu for why).
+constexpr float SA = 8192.0f, SB = 8192.0f;
+
+// 32 values of one row, columns col .. col + 31, split into the two parts of the matrix at
+// `mat`: 16-byte chunk j of a 128-byte row r sits at chunk j ^ (r & 7).
+__device__ __forceinline__ void put(uint32_t mat, int row, int col, const float (&v)[32]) {
+    const uint32_t base = mat + static_cast<uint32_t>(col >> 6) * (PART / 2) + static_cast<uint32_t>(row) * 128u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = v[8 * j + 2 * i], b = v[8 * j + 2 * i + 1];
+            h[i] = ptx::f16x2_satfinite(a, b);
+            const __half2 hh = *reinterpret_cast<__half2 *>(&h[i]);
+            l[i] = ptx::f16x2_satfinite(a - __low2float(hh), b - __high2float(hh));
+        }
+        const uint32_t at = base + (static_cast<uint32_t>((((col & 63) >> 3) + j) ^ (row & 7)) << 4);
+        ptx::st_shared_v4(at, h[0], h[1], h[2], h[3]);
+        ptx::st_shared_v4(at + PART, l[0], l[1], l[2], l[3]);
+    }
+}
+
+// D = X Y^T for two matrices in shared memory, issued by one thread.
+__device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y) {
+    constexpr uint32_t IDESC = ptx::idesc_f16_f32(PT, PT, false, false);
+    constexpr uint32_t px[3] = {0, PART, 0}, py[3] = {PART, 0, 0};  // the small products first
+    uint32_t acc = 0;
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int k = 0; k < PT / 16; ++k) {
+            const uint32_t off = static_cast<uint32_t>(k >> 2) * (PART / 2) + static_cast<uint32_t>(k & 3) * 32u;
+            ptx::umma_f16_ss(d, ptx::sdesc_sw128(x + px[s] + off, 16, 1024),
+                             ptx::sdesc_sw128(y + py[s] + off, 16, 1024), IDESC, acc);
+            acc = 1;
+        }
+}
+
+__global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ uint32_t tmem_sh;
+    __shared__ volatile int abort_sh;
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t mA = base, mB = base + MAT, mQ = base + 2 * MAT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = 32 * (warp & 3) + lane, col0 = 64 * (warp >> 2);
+    const uint32_t bar_a = ptx::smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar_a, 1);
+        abort_sh = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(&tmem_sh), TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + static_cast<uint32_t>(col0);
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    // A_0: the sum of the splits' Gram matrices.  They are symmetric, so a thread reads its
+    // row as a column and a warp's loads are contiguous.
+    const int64_t z = blockIdx.x, P = c.P;
+    float A[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) A[i] = 0.0f;
+    if (row < P && col0 < P) {
+        const float *src = c.gram + z * P * P + col0 * P + row;
+        for (int s = 0; s < c.splits; ++s, src += c.matrices * P * P)
+#pragma unroll
+            for (int i = 0; i < 64; ++i) A[i] += src[i * P];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) A[i] *= c.unit;
+    }
+
+    // All shared-memory writes of a round are made, then one thread issues the next
+    // round's products; every thread waits for them.
+    uint32_t phase = 0;
+    bool ok = true;
+    auto round = [&](auto issue) {
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            ptx::tc_fence_after();
+            issue();
+            ptx::umma_commit(bar_a);
+        }
+        if (!ptx::mbar_wait(bar_a, phase, c.wait_ns, &abort_sh)) {
+            ok = false;
+            abort_sh = 1;
+        }
+        phase ^= 1u;
+        ptx::tc_fence_after();
+        ok = !__syncthreads_or(!ok);
+    };
+    auto load = [&](int acc, int half, float (&v)[32]) {
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * PT + 32 * half), r);
+        ptx::tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    };
+    auto put_A = [&]() {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = A[32 * half + i] * SA;
+            put(mA, row, col0 + 32 * half, v);
+        }
+    };
+    put_A();
+    for (int k = 0; k < c.steps && ok; ++k) {
+        const bool last = k == c.steps - 1;
+        round([&] { multiply(tmem, mA, mA); });
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            load(0, half, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int col = col0 + 32 * half + i;
+                v[i] = fmaf(c.c * (SB / (SA * SA)), v[i], (c.b * SB) * A[32 * half + i]);
+                if (row == col) v[i] += c.a * SB;
+            }
+            put(mB, row, col0 + 32 * half, v);
+            if (k == 0) {  // Q^T = B_0
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= c.q_scale / SB;
+                put(mQ, row, col0 + 32 * half, v);
+            }
+        }
+        if (k == 0 && last) break;
+        round([&] {
+            if (k > 0) multiply(tmem, mQ, mB);         // Q^T B = (B Q)^T
+            if (!last) multiply(tmem + PT, mB, mA);  // B A
+        });
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            if (k > 0) {
+                load(0, half, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
+                put(mQ, row, col0 + 32 * half, v);
+            }
+            if (!last) {  // B A takes A's place
+                load(1, half, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
+                put(mA, row, col0 + 32 * half, v);
+            }
+        }
+        if (last) break;
+        round([&] { multiply(tmem, mB, mA); });  // B (B A)^T = B A B
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            load(0, half, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) A[32 * half + i] = v[i] * (1.0f / (SA * SB));
+        }
+        put_A();
+    }
+    // Given up: once more for the products in flight, so that they do not outlive the
+    // shared and tensor memory that they use.
+    if (!ok) ptx::mbar_wait(bar_a, phase ^ 1u, c.wait_ns, nullptr);
+    if (!ok && threadIdx.x == 0 && c.status && atomicCAS(c.status, 0u, STATUS_TIMEOUT) == 0u)
+        atomicExch(c.status + 1, 8u);
+
+    // Q from Q^T in shared memory, every thread what it wrote itself: element (row, col) of
+    // Q^T to row col of Q, where a warp's 32 rows are neighbours.
+    if (row < P && col0 < P) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            __half *out = static_cast<__half *>(c.Q) + ((part * c.matrices + z) * P + col0) * P + row;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t w[4];
+                ptx::ld_shared_v4(mQ + part * PART + static_cast<uint32_t>(col0 >> 6) * (PART / 2) +
+                                      static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(j ^ (row & 7)) << 4),
+                                  w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 v = *reinterpret_cast<const __half2 *>(&w[i]);
+                    out[(8 * j + 2 * i) * P] = __low2half(v);
+                    out[(8 * j + 2 * i + 1) * P] = __high2half(v);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+}  // namespace chain
+
+cudaError_t launch_ns_chain(const NsChain &c, cudaStream_t st) {
+    // per call: the attribute belongs to the current device
+    const cudaError_t e = cudaFuncSetAttribute(chain::chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(chain::SMEM));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(chain::chain_kernel, dim3(static_cast<unsigned>(c.matrices)), chain::THREADS, chain::SMEM, st, c);
+}
+
+}  // namespace tpmlp

@@ -1,12 +1,14 @@
 // Norm, scaling and padding of the Newton-Schulz orthogonalisation (the products run
 // in tc_gemm.cu).  Each matrix G [rows, cols] becomes X = G / (|G|_F + eps), held as
-// the sum of two fp16 matrices, hi + lo / 2^11, of size [P, Q] (rows and cols rounded
+// the sum of two fp16 matrices, hi + lo / lo_scale, of size [P, Q] (rows and cols rounded
 // up to 64, the rest zero: zero rows and columns stay zero through every product).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace tpmlp {
 namespace ortho {
@@ -51,6 +53,8 @@ __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 x) {
 // Memory bound: one read of G.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, int64_t per_block, Blue *part) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const T *g = G + static_cast<int64_t>(blockIdx.y) * n;
     const int64_t beg = static_cast<int64_t>(blockIdx.x) * per_block, end = min(beg + per_block, n);
     Blue b{0.0f, 0.0f, 0.0f};
@@ -111,7 +115,9 @@ __device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                                         const Blue *part, int nparts, float eps, float scale,
-                                                        __half *hi, __half *lo) {
+                                                        __half *hi, __half *lo, float lo_scale) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int64_t z = blockIdx.y;
     const float f = inverse_norm(part + z * nparts, nparts, eps, scale);
     const T *g = G + z * rows * cols;
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
         for (int j = 0; j < 8; ++j) {
             const float x = v[j] * f;
             h[j] = __float2half_rn(x);
-            l[j] = __float2half_rn((x - __half2float(h[j])) * 2048.0f);
+            l[j] = __float2half_rn((x - __half2float(h[j])) * lo_scale);
         }
         const int64_t o = z * P * Q + r * Q + c;
         *reinterpret_cast<uint4 *>(hi + o) = *reinterpret_cast<const uint4 *>(h);
@@ -148,6 +154,8 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
 // multiples of 16 bytes (a TMA store cannot write them).
 __global__ void __launch_bounds__(THREADS) unpad_kernel(const __nv_bfloat16 *in, int64_t rows, int64_t cols, int64_t P,
                                                         int64_t Q, __nv_bfloat16 *out) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int64_t z = blockIdx.y;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < rows * cols;
          i += static_cast<int64_t>(gridDim.x) * THREADS) {
@@ -173,21 +181,12 @@ static cudaError_t launch_start(const OrthoStart &a, cudaStream_t st) {
     const int64_t per = ((n + nb - 1) / nb + 15) / 16 * 16;
     const dim3 gn(static_cast<unsigned>(nb), static_cast<unsigned>(a.batch));
     Blue *part = static_cast<Blue *>(a.part);
-    if (vec_all)
-        norm_kernel<T, true><<<gn, THREADS, 0, st>>>(G, n, per, part);
-    else
-        norm_kernel<T, false><<<gn, THREADS, 0, st>>>(G, n, per, part);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_pdl(vec_all ? norm_kernel<T, true> : norm_kernel<T, false>, gn, THREADS, 0, st, G, n, per, part);
     if (e != cudaSuccess) return e;
     const dim3 gs(grid_x(a.P * a.Q / 8, a.batch), static_cast<unsigned>(a.batch));
     __half *hi = static_cast<__half *>(a.hi), *lo = static_cast<__half *>(a.lo);
-    if (vec_rows)
-        scale_kernel<T, true><<<gs, THREADS, 0, st>>>(G, a.rows, a.cols, a.P, a.Q, part, static_cast<int>(nb), a.eps,
-                                                      a.scale, hi, lo);
-    else
-        scale_kernel<T, false><<<gs, THREADS, 0, st>>>(G, a.rows, a.cols, a.P, a.Q, part, static_cast<int>(nb), a.eps,
-                                                       a.scale, hi, lo);
-    return cudaGetLastError();
+    return launch_pdl(vec_rows ? scale_kernel<T, true> : scale_kernel<T, false>, gs, THREADS, 0, st, G, a.rows, a.cols,
+                      a.P, a.Q, part, static_cast<int>(nb), a.eps, a.scale, hi, lo, a.lo_scale);
 }
 
 }  // namespace ortho
@@ -204,9 +203,8 @@ cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t s
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                void *out, cudaStream_t st) {
     const dim3 g(ortho::grid_x(rows * cols, batch), static_cast<unsigned>(batch));
-    ortho::unpad_kernel<<<g, ortho::THREADS, 0, st>>>(static_cast<const __nv_bfloat16 *>(in), rows, cols, P, Q,
-                                                      static_cast<__nv_bfloat16 *>(out));
-    return cudaGetLastError();
+    return launch_pdl(ortho::unpad_kernel, g, ortho::THREADS, 0, st, static_cast<const __nv_bfloat16 *>(in), rows, cols,
+                      P, Q, static_cast<__nv_bfloat16 *>(out));
 }
 
 }  // namespace tpmlp

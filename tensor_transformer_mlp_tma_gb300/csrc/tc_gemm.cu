@@ -92,7 +92,7 @@ struct Cfg {
     static constexpr int STG_PER_WARP = DS ? 2 * STG_BOX_WIDE : 2 * STG_BOX;
     // dS: the K extent is one head dimension (two K blocks per tile), so fewer
     // stages make room for its wider staging boxes
-    static constexpr int STAGES = CG == 1 ? (DS ? 3 : 4) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
+    static constexpr int STAGES = CG == 1 ? (DS ? 3 : (TILE_N == 128 ? 6 : 4)) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
     static constexpr int SMEM_DYN = STAGES * STAGE_BYTES + (EPI_THREADS / 32) * STG_PER_WARP + 1024;
 };
 constexpr int MAX_STAGES = 8;
@@ -168,6 +168,7 @@ struct Params {
     // pair, or six for fp32 operands in three parts); problem z starts at k-block
     // z * kb_seg (split K) and reads the operands of problem 0.
     int kb_seg;
+    int matrices;  // EPI_NS_GRAM32, EPI_NS_FINAL: problem z is matrix z % matrices, K range z / matrices
     // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
     const void *aux2;
     float alpha, beta, diag;
@@ -177,8 +178,13 @@ struct Params {
 // The Newton-Schulz products: fp16 operands; A and C = f(A) are symmetric, so only
 // the tiles on and below the diagonal are computed and each is stored twice.
 __host__ __device__ constexpr bool is_ns(int epi) {
-    return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
+    return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST ||
+           epi == EPI_NS_FINAL;
 }
+// Both operands as two fp16 parts (22 bits), three products per k-block.
+__host__ __device__ constexpr bool is_ns2(int epi) { return epi == EPI_NS_GRAM32 || epi == EPI_NS_FINAL; }
+__host__ __device__ constexpr bool is_f16(int epi) { return is_ns(epi) || is_ns2(epi); }
+__host__ __device__ constexpr bool is_out32(int epi) { return epi == EPI_ACC32 || epi == EPI_NS_GRAM32; }
 __host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY; }
 __host__ __device__ constexpr bool is_grad(int epi) { return epi == EPI_XENT_GRAD || epi == EPI_XENT_GRAD3; }
 __host__ __device__ constexpr bool is_xent(int epi) { return epi == EPI_XENT_STATS || is_grad(epi); }
@@ -201,6 +207,11 @@ __device__ __forceinline__ KCoord k_coord(const Params &p, int kb, int z) {
         const int pair = p.kb_per_shard == p.kb_seg ? 5 : seg;
         return {(kb - seg * p.kb_seg + z * p.kb_seg) * BK, static_cast<int>((kSegA >> (2 * pair)) & 3u),
                 static_cast<int>((kSegB >> (2 * pair)) & 3u)};
+    } else if constexpr (is_ns2(EPI)) {
+        // (high, low), (low, high), (high, high); the low parts follow the high ones
+        const int seg = kb / p.kb_seg, split = z / p.matrices, m = z - split * p.matrices;
+        return {(kb - seg * p.kb_seg + split * p.kb_seg) * BK, m + (seg == 1 ? p.matrices : 0),
+                m + (seg == 0 ? p.matrices : 0)};
     } else {
         return {kb * BK, z, z};
     }
@@ -758,7 +769,8 @@ __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0
         half_axpy(h1, p.beta, v);
     }
     uint32_t w0[16], w1[16];
-    if constexpr (EPI == EPI_NS_LAST) {
+    constexpr bool OUT = EPI == EPI_NS_LAST || EPI == EPI_NS_FINAL;  // the bf16 result
+    if constexpr (OUT) {
         pack32(v, w0);
     } else {
         // finite values saturate at the fp16 range (the scales keep them inside);
@@ -784,7 +796,7 @@ __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    const int M = EPI == EPI_NS_LAST ? p.out_M : p.M, N = EPI == EPI_NS_LAST ? p.out_N : p.N;
+    const int M = OUT ? p.out_M : p.M, N = OUT ? p.out_N : p.N;
     if (lane == 0 && row0 < M && col < N) {
         ptx::tma_store_3d(tm0, stg, col, row0, z);
         if constexpr (EPI == EPI_NS_UPDATE) ptx::tma_store_3d(tm1, stg + STG_BOX, col, row0, z);
@@ -802,7 +814,7 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
                                              int next_col = -1, int next_row0 = 0,
                                              volatile int *abort_flag = nullptr,
                                              const BiasPre *bias_pre = nullptr, const XentRow *xr = nullptr) {
-    if constexpr (EPI == EPI_ACC32) {
+    if constexpr (is_out32(EPI)) {
         // 32 x 32 fp32 box (128-byte rows, 128-byte swizzle), stored or added to
         // the output.  One launch adds to an element once, and launches follow one
         // another on their stream, so the order of the additions is fixed.
@@ -997,12 +1009,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD);
     constexpr bool WIDE = TILE_N == 512;
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
-    constexpr uint32_t IDESC = is_ns(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
+    constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
                                           : ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
-    static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE),
-                  "narrow tile: CTA pairs, plain store");
+    static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
+                      (TILE_N == 128 && CG == 1 && EPI == EPI_NS_GRAM32),
+                  "narrow tile: CTA pairs and plain store, or single CTAs and the small Gram matrices");
     static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
                   "wide tile: CTA pairs, one shard");
     static_assert(!is_sym(EPI) || C::TILE_M == TILE_N, "symmetric outputs: square tiles");
@@ -1968,8 +1981,9 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // B operand: this CTA's B_ROWS columns, K-major in one box or MN-major in 64-wide boxes.
     const int64_t nb = g.batch < 1 ? 1 : g.batch;
     constexpr bool SEG = has_segments(EPI);
-    const int64_t ni = SEG ? (g.parts > 1 ? g.parts : 1) : nb;  // matrices per operand
-    const int64_t no = EPI == EPI_XENT_GRAD3 ? 3 : (SEG && g.ksplit > 1 ? g.ksplit : nb);  // and of the output
+    const int64_t splits = g.ksplit > 1 ? g.ksplit : 1;
+    const int64_t ni = SEG ? (g.parts > 1 ? g.parts : 1) : (is_ns2(EPI) ? 2 * nb : nb);  // matrices per operand
+    const int64_t no = EPI == EPI_XENT_GRAD3 ? 3 : (SEG ? splits : nb * splits);         // and of the output
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;  // the copies move 16-bit words: fp16 too
     // MN-major operands whose MN extent is a multiple of 64 take the 4-D map
@@ -2018,13 +2032,14 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     const void *o2 = (EPI == EPI_DGELU && g.out1) ? g.out1 : o0;
     const CUtensorMapDataType odt =
         EPI == EPI_ATTN_SCORE ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                              : (EPI == EPI_ACC32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+                              : (is_out32(EPI) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
     const bool wide = EPI == EPI_ATTN_DS;
     const uint32_t obox = wide ? 64 : 32;
-    const CUtensorMapSwizzle so = wide || EPI == EPI_ACC32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    // What the output map covers: LAST stores the unpadded part of the tiles.
-    const int64_t orows = EPI == EPI_NS_LAST ? g.out_rows : g.M;
-    const int64_t ocols = EPI == EPI_NS_LAST ? g.out_cols : g.N;
+    const CUtensorMapSwizzle so = wide || is_out32(EPI) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    // What the output map covers: LAST and FINAL store the unpadded part of the tiles.
+    const bool unpadded = EPI == EPI_NS_LAST || EPI == EPI_NS_FINAL;
+    const int64_t orows = unpadded ? g.out_rows : g.M;
+    const int64_t ocols = unpadded ? g.out_cols : g.N;
     if (wide && (o_rank > 3 || g.nshards != 1)) {
         set_last_error("dS epilogue: a plain [problems][M][N] output and one shard only");
         return cudaErrorInvalidValue;
@@ -2070,9 +2085,11 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.status = g.status;
     p.wait_ns = g.wait_ns;
     p.colsum_part = g.colsum_part;
-    p.batch = static_cast<int>(SEG && g.ksplit > 1 ? g.ksplit : nb);
+    p.batch = static_cast<int>(nb * splits);
+    p.matrices = static_cast<int>(nb);
     p.kb_seg = p.kb_per_shard;
     if (SEG && g.parts > 1) p.kb_per_shard *= 6;
+    if (is_ns2(EPI)) p.kb_per_shard *= 3;
     p.scale = g.scale;
     p.causal = g.causal ? 1 : 0;
     p.rowvec = g.rowvec;
@@ -2174,7 +2191,11 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 template <int EPI, bool A_MN, bool B_MN>
 static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
-    if constexpr (is_ns(EPI)) {
+    if constexpr (EPI == EPI_NS_GRAM32) {
+        return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);  // outputs of at most 128 x 128
+    } else if constexpr (EPI == EPI_NS_FINAL) {
+        return launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
+    } else if constexpr (is_ns(EPI)) {
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
     if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || has_segments(EPI)) {
@@ -2264,6 +2285,14 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
         case EPI_NS_LAST:
             if (!g.a_mn && g.b_mn) return launch_cg<EPI_NS_LAST, false, true>(g, num_sms, st);
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_LAST, false, false>(g, num_sms, st);
+            break;
+        case EPI_NS_GRAM32:
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAM32, false, false>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_NS_GRAM32, true, true>(g, num_sms, st);
+            break;
+        case EPI_NS_FINAL:  // Q X of a wide X (MN-major), X Q of a tall one
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_NS_FINAL, false, true>(g, num_sms, st);
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_FINAL, false, false>(g, num_sms, st);
             break;
         case EPI_FOLD:  // dY[T,F] (K-major) . A[h,F]^T (K-major)
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_FOLD, false, false>(g, num_sms, st);

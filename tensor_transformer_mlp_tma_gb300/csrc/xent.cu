@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace tpmlp {
@@ -195,23 +196,6 @@ __global__ void __launch_bounds__(ROW_THREADS) piece_grad_kernel(const RowArgs a
     }
 }
 
-// Launches with programmatic stream serialisation: the kernel waits for the one before it
-// itself (griddep_wait), so that its launch overlaps that kernel's tail.
-template <typename... P, typename... A>
-static cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, cudaStream_t st, A... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-    return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
 // Blocks of 256 threads for n units of work, as many as stay resident.
 static int64_t blocks_for(int64_t n) {
     const int64_t b = (n + 255) / 256;
@@ -221,11 +205,11 @@ static int64_t blocks_for(int64_t n) {
 }  // namespace xent
 
 cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st) {
-    return xent::launch(xent::combine_kernel, (a.tokens + 31) / 32, 32 * xent::COMBINE_WARPS, st, a, loss, lse);
+    return launch_pdl(xent::combine_kernel, dim3(static_cast<unsigned>((a.tokens + 31) / 32)), 32 * xent::COMBINE_WARPS, 0, st, a, loss, lse);
 }
 
 cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st) {
-    return xent::launch(xent::row_g_kernel, (a.tokens + 255) / 256, 256, st, a, dloss, row_g);
+    return launch_pdl(xent::row_g_kernel, dim3(static_cast<unsigned>((a.tokens + 255) / 256)), 256, 0, st, a, dloss, row_g);
 }
 
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
@@ -234,16 +218,16 @@ cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t
     const int64_t blocks = xent::blocks_for(rows * cols / (vec ? 4 : 1));
     if (is_bf16) {
         auto o = static_cast<__nv_bfloat16 *>(out);
-        return vec ? xent::launch(xent::sum_splits_kernel<__nv_bfloat16, 4>, blocks, 256, st, in, splits, rows, cols, ld, o)
-                   : xent::launch(xent::sum_splits_kernel<__nv_bfloat16, 1>, blocks, 256, st, in, splits, rows, cols, ld, o);
+        return vec ? launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o)
+                   : launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o);
     }
     auto o = static_cast<float *>(out);
-    return vec ? xent::launch(xent::sum_splits_kernel<float, 4>, blocks, 256, st, in, splits, rows, cols, ld, o)
-               : xent::launch(xent::sum_splits_kernel<float, 1>, blocks, 256, st, in, splits, rows, cols, ld, o);
+    return vec ? launch_pdl(xent::sum_splits_kernel<float, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o)
+               : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o);
 }
 
 cudaError_t launch_split3(const float *in, int64_t rows, int64_t cols, int64_t ld, void *out, cudaStream_t st) {
-    return xent::launch(xent::split3_kernel, xent::blocks_for(rows * ld / 4), 256, st, in, rows, cols, ld,
+    return launch_pdl(xent::split3_kernel, dim3(static_cast<unsigned>(xent::blocks_for(rows * ld / 4))), 256, 0, st, in, rows, cols, ld,
                         static_cast<__nv_bfloat16 *>(out));
 }
 
