@@ -24,6 +24,7 @@ enum Epi : int {
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
     EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts               -- X X^T
     EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
+    EPI_XENT_FOLD = 17, // XENT_STATS over K in nshards ranges, added up in fp32
     EPI_XENT_GRAD3 = 14, // XENT_GRAD for fp32: dS as three bf16 parts      -- X W^T -> dS
 };
 
@@ -209,7 +210,8 @@ cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t s
 // The steps on p x p Gram matrices, p <= 128 (ns_chain.cu).
 constexpr int NS_CHAIN_P = 128;
 struct NsChain {
-    int64_t matrices, P;  // P: 64 or 128
+    int64_t matrices, P;  // P: 64 or 128, the row pitch and size in memory
+    int size;             // rows and columns in use, a multiple of 16
     const float *gram;    // [splits][matrices][P][P]
     int splits;
     float unit;           // A_0 = unit * the sum of the splits

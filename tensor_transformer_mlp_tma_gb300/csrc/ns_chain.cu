@@ -29,11 +29,11 @@ namespace tpmlp {
 namespace chain {
 
 constexpr int PT = NS_CHAIN_P;           // rows and columns of the tile, 128
-constexpr int THREADS = 256;             // warp w: TMEM lanes 32 (w % 4).., columns 64 (w / 4)..
+constexpr int THREADS = 512;             // warp w: TMEM lanes 32 (w % 4).., columns 32 (w / 4)..
 constexpr uint32_t PART = PT * PT * 2;   // one fp16 matrix: two blocks of 64 columns, 128-byte swizzled
 constexpr uint32_t MAT = 2 * PART;       // high and low part
 constexpr size_t SMEM = 3 * MAT + 1024;  // A, B, Q, and alignment
-constexpr uint32_t TMEM_COLS = 256;      // two accumulators of 128 columns
+constexpr uint32_t TMEM_COLS = 512;      // three accumulators of 128 columns
 constexpr uint32_t STATUS_TIMEOUT = 4;   // TPMLP_ERR_TIMEOUT
 
 // The scales that A and B are stored with (powers of two; see kScaleX in api.cu for why).
@@ -59,34 +59,38 @@ __device__ __forceinline__ void put(uint32_t mat, int row, int col, const float 
     }
 }
 
-// D = X Y^T for two matrices in shared memory, issued by one thread.
-__device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y) {
-    constexpr uint32_t IDESC = ptx::idesc_f16_f32(PT, PT, false, false);
-    constexpr uint32_t px[3] = {0, PART, 0}, py[3] = {PART, 0, 0};  // the small products first
+// D = X Y^T for two matrices in shared memory of n columns each (n a multiple of 16),
+// issued by one thread.
+__device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y, int n, uint32_t idesc) {
     uint32_t acc = 0;
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
-#pragma unroll
-        for (int k = 0; k < PT / 16; ++k) {
+    for (int s = 0; s < 3; ++s) {  // the small products first
+        const uint32_t px = x + (s == 1 ? PART : 0), py = y + (s == 0 ? PART : 0);
+        for (int k = 0; k < n / 16; ++k) {
             const uint32_t off = static_cast<uint32_t>(k >> 2) * (PART / 2) + static_cast<uint32_t>(k & 3) * 32u;
-            ptx::umma_f16_ss(d, ptx::sdesc_sw128(x + px[s] + off, 16, 1024),
-                             ptx::sdesc_sw128(y + py[s] + off, 16, 1024), IDESC, acc);
+            ptx::umma_f16_ss(d, ptx::sdesc_sw128(px + off, 16, 1024), ptx::sdesc_sw128(py + off, 16, 1024), idesc, acc);
             acc = 1;
         }
+    }
 }
 
 __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bar;
+    __shared__ __align__(8) uint64_t bars[3];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_sh;
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t mA = base, mB = base + MAT, mQ = base + 2 * MAT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = 32 * (warp & 3) + lane, col0 = 64 * (warp >> 2);
-    const uint32_t bar_a = ptx::smem_u32(&bar);
+    const int row = 32 * (warp & 3) + lane, col0 = 32 * (warp >> 2);
+    const int n = c.size;
+    const bool mine_in = col0 < n;  // warps whose columns are all padding only keep step
+    const uint32_t idesc = ptx::idesc_f16_f32(PT, n, false, false);
+    const uint32_t bar[2] = {ptx::smem_u32(&bars[0]), ptx::smem_u32(&bars[1])};
     if (threadIdx.x == 0) {
-        ptx::mbar_init(bar_a, 1);
+        ptx::mbar_init(bar[0], 1);
+        ptx::mbar_init(bar[1], 1);
+        ptx::mbar_init(ptx::smem_u32(&bars[2]), 1);
         abort_sh = 0;
         ptx::fence_mbar_init();
     }
@@ -105,134 +109,154 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     // A_0: the sum of the splits' Gram matrices.  They are symmetric, so a thread reads its
     // row as a column and a warp's loads are contiguous.
     const int64_t z = blockIdx.x, P = c.P;
-    float A[64];
+    float A[32];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) A[i] = 0.0f;
+    for (int i = 0; i < 32; ++i) A[i] = 0.0f;
     if (row < P && col0 < P) {
         const float *src = c.gram + z * P * P + col0 * P + row;
         for (int s = 0; s < c.splits; ++s, src += c.matrices * P * P)
 #pragma unroll
-            for (int i = 0; i < 64; ++i) A[i] += src[i * P];
+            for (int i = 0; i < 32; ++i) A[i] += src[i * P];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) A[i] *= c.unit;
+        for (int i = 0; i < 32; ++i) A[i] *= c.unit;
     }
 
-    // All shared-memory writes of a round are made, then one thread issues the next
-    // round's products; every thread waits for them.
-    uint32_t phase = 0;
+    // Each product belongs to one of two barriers; `start` runs once every thread's
+    // shared-memory writes and tensor-memory reads before it are done.
+    uint32_t phase[2] = {0u, 0u};
     bool ok = true;
-    auto round = [&](auto issue) {
+    auto start = [&](auto issue) {
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
         if (threadIdx.x == 0) {
             ptx::tc_fence_after();
             issue();
-            ptx::umma_commit(bar_a);
         }
-        if (!ptx::mbar_wait(bar_a, phase, c.wait_ns, &abort_sh)) {
+    };
+    auto wait = [&](int b) {
+        if (!ptx::mbar_wait(bar[b], phase[b], c.wait_ns, &abort_sh)) {
             ok = false;
             abort_sh = 1;
         }
-        phase ^= 1u;
+        phase[b] ^= 1u;
         ptx::tc_fence_after();
-        ok = !__syncthreads_or(!ok);
     };
-    auto load = [&](int acc, int half, float (&v)[32]) {
+    auto load = [&](int acc, float (&v)[32]) {
         uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * PT + 32 * half), r);
+        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * PT), r);
         ptx::tmem_ld_wait(r);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
     };
+    float v[32];
     auto put_A = [&]() {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = A[32 * half + i] * SA;
-            put(mA, row, col0 + 32 * half, v);
-        }
+        for (int i = 0; i < 32; ++i) v[i] = A[i] * SA;
+        put(mA, row, col0, v);
     };
     put_A();
-    for (int k = 0; k < c.steps && ok; ++k) {
+    // A wait that runs out leaves `ok` false in at least one thread and raises the
+    // flag that ends every other wait at once; the steps are then gone through without
+    // waiting, so that all threads meet at the same barriers.
+    for (int k = 0; k < c.steps; ++k) {
         const bool last = k == c.steps - 1;
-        round([&] { multiply(tmem, mA, mA); });
-        if (!ok) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            load(0, half, v);
+        start([&] {
+            multiply(tmem, mA, mA, n, idesc);
+            ptx::umma_commit(bar[0]);
+        });
+        wait(0);
+        if (mine_in) {
+            load(0, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const int col = col0 + 32 * half + i;
-                v[i] = fmaf(c.c * (SB / (SA * SA)), v[i], (c.b * SB) * A[32 * half + i]);
-                if (row == col) v[i] += c.a * SB;
+                v[i] = fmaf(c.c * (SB / (SA * SA)), v[i], (c.b * SB) * A[i]);
+                if (row == col0 + i) v[i] += c.a * SB;
             }
-            put(mB, row, col0 + 32 * half, v);
+            put(mB, row, col0, v);
             if (k == 0) {  // Q^T = B_0
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= c.q_scale / SB;
-                put(mQ, row, col0 + 32 * half, v);
+                put(mQ, row, col0, v);
             }
         }
         if (k == 0 && last) break;
-        round([&] {
-            if (k > 0) multiply(tmem, mQ, mB);         // Q^T B = (B Q)^T
-            if (!last) multiply(tmem + PT, mB, mA);  // B A
-        });
-        if (!ok) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            if (k > 0) {
-                load(0, half, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
-                put(mQ, row, col0 + 32 * half, v);
+        // B A first: the chain goes on with it, while Q^T B = (B Q)^T has time until the step's end.
+        start([&] {
+            if (!last) {
+                multiply(tmem + PT, mB, mA, n, idesc);
+                ptx::umma_commit(bar[0]);
             }
-            if (!last) {  // B A takes A's place
-                load(1, half, v);
+            if (k > 0) {
+                multiply(tmem + 2 * PT, mQ, mB, n, idesc);
+                ptx::umma_commit(bar[1]);
+            }
+        });
+        if (!last) {
+            wait(0);
+            if (mine_in) {  // B A takes A's place
+                load(1, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
-                put(mA, row, col0 + 32 * half, v);
+                put(mA, row, col0, v);
+            }
+            start([&] {
+                multiply(tmem, mB, mA, n, idesc);  // B (B A)^T = B A B
+                ptx::umma_commit(bar[0]);
+            });
+        }
+        if (k > 0) {
+            wait(1);
+            if (mine_in) {
+                load(2, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
+                put(mQ, row, col0, v);
             }
         }
         if (last) break;
-        round([&] { multiply(tmem, mB, mA); });  // B (B A)^T = B A B
-        if (!ok) break;
+        wait(0);
+        if (mine_in) {
+            load(0, v);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            load(0, half, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) A[32 * half + i] = v[i] * (1.0f / (SA * SB));
+            for (int i = 0; i < 32; ++i) A[i] = v[i] * (1.0f / (SA * SB));
+            put_A();
         }
-        put_A();
     }
     // Given up: once more for the products in flight, so that they do not outlive the
     // shared and tensor memory that they use.
-    if (!ok) ptx::mbar_wait(bar_a, phase ^ 1u, c.wait_ns, nullptr);
-    if (!ok && threadIdx.x == 0 && c.status && atomicCAS(c.status, 0u, STATUS_TIMEOUT) == 0u)
-        atomicExch(c.status + 1, 8u);
+    ok = !__syncthreads_or(!ok);
+    if (!ok) {
+        if (threadIdx.x == 0) {
+            ptx::umma_commit(ptx::smem_u32(&bars[2]));
+            ptx::mbar_wait(ptx::smem_u32(&bars[2]), 0, c.wait_ns, nullptr);
+            if (c.status && atomicCAS(c.status, 0u, STATUS_TIMEOUT) == 0u) atomicExch(c.status + 1, 8u);
+        }
+        __syncthreads();
+    }
 
     // Q from Q^T in shared memory, every thread what it wrote itself: element (row, col) of
-    // Q^T to row col of Q, where a warp's 32 rows are neighbours.
+    // Q^T to row col of Q, where a warp's 32 rows are neighbours.  Past the rows and columns
+    // in use the tile holds anything; there Q is zero, since the product Q X runs over them.
     if (row < P && col0 < P) {
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             __half *out = static_cast<__half *>(c.Q) + ((part * c.matrices + z) * P + col0) * P + row;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t w[4];
-                ptx::ld_shared_v4(mQ + part * PART + static_cast<uint32_t>(col0 >> 6) * (PART / 2) +
-                                      static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(j ^ (row & 7)) << 4),
-                                  w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (mine_in && row < n)
+                    ptx::ld_shared_v4(mQ + part * PART + static_cast<uint32_t>(col0 >> 6) * (PART / 2) +
+                                          static_cast<uint32_t>(row) * 128u +
+                                          (static_cast<uint32_t>((((col0 & 63) >> 3) + j) ^ (row & 7)) << 4),
+                                      w[0], w[1], w[2], w[3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const __half2 v = *reinterpret_cast<const __half2 *>(&w[i]);
-                    out[(8 * j + 2 * i) * P] = __low2half(v);
-                    out[(8 * j + 2 * i + 1) * P] = __high2half(v);
+                    const __half2 h = *reinterpret_cast<const __half2 *>(&w[i]);
+                    const int col = 8 * j + 2 * i;
+                    const bool in = col0 + col < n;  // n is even
+                    out[col * P] = in ? __low2half(h) : __half(0.0f);
+                    out[(col + 1) * P] = in ? __high2half(h) : __half(0.0f);
                 }
             }
         }

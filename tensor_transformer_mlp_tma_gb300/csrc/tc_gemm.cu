@@ -167,7 +167,7 @@ struct Params {
     // K of the cross entropy's products: kb_seg k-blocks per pair of operand parts (one
     // pair, or six for fp32 operands in three parts); problem z starts at k-block
     // z * kb_seg (split K) and reads the operands of problem 0.
-    int kb_seg;
+    int kb_seg, pairs;
     int matrices;  // EPI_NS_GRAM32, EPI_NS_FINAL: problem z is matrix z % matrices, K range z / matrices
     // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
     const void *aux2;
@@ -187,7 +187,8 @@ __host__ __device__ constexpr bool is_f16(int epi) { return is_ns(epi) || is_ns2
 __host__ __device__ constexpr bool is_out32(int epi) { return epi == EPI_ACC32 || epi == EPI_NS_GRAM32; }
 __host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY; }
 __host__ __device__ constexpr bool is_grad(int epi) { return epi == EPI_XENT_GRAD || epi == EPI_XENT_GRAD3; }
-__host__ __device__ constexpr bool is_xent(int epi) { return epi == EPI_XENT_STATS || is_grad(epi); }
+__host__ __device__ constexpr bool is_stats(int epi) { return epi == EPI_XENT_STATS || epi == EPI_XENT_FOLD; }
+__host__ __device__ constexpr bool is_xent(int epi) { return is_stats(epi) || is_grad(epi); }
 // Products whose K range can run over pairs of operand parts, or be split.
 __host__ __device__ constexpr bool has_segments(int epi) { return is_xent(epi) || epi == EPI_ACC32; }
 
@@ -204,10 +205,16 @@ template <int EPI>
 __device__ __forceinline__ KCoord k_coord(const Params &p, int kb, int z) {
     if constexpr (has_segments(EPI)) {
         const int seg = kb / p.kb_seg;
-        const int pair = p.kb_per_shard == p.kb_seg ? 5 : seg;
+        const int pair = p.pairs == 1 ? 5 : seg;
         return {(kb - seg * p.kb_seg + z * p.kb_seg) * BK, static_cast<int>((kSegA >> (2 * pair)) & 3u),
                 static_cast<int>((kSegB >> (2 * pair)) & 3u)};
     } else if constexpr (is_ns2(EPI)) {
+        if constexpr (EPI == EPI_NS_GRAM32) {
+            // the high part through A's map and the low part through B's: one copy of each
+            // serves all three products (see the MMA issuer)
+            const int split = z / p.matrices, m = z - split * p.matrices;
+            return {(kb + split * p.kb_seg) * BK, m, m + p.matrices};
+        }
         // (high, low), (low, high), (high, high); the low parts follow the high ones
         const int seg = kb / p.kb_seg, split = z / p.matrices, m = z - split * p.matrices;
         return {(kb - seg * p.kb_seg + split * p.kb_seg) * BK, m + (seg == 1 ? p.matrices : 0),
@@ -1006,7 +1013,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const Params p) {
     using C = Cfg<CG, TILE_N, EPI>;
     constexpr bool PAIR = CG == 2;
-    constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD);
+    constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD);
     constexpr bool WIDE = TILE_N == 512;
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
     constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
@@ -1511,7 +1518,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 const uint64_t bd = B_MN ? ptx::sdesc_sw128(sb + k * 2048, MN_BLOCK_BYTES, 1024)
                                                          : ptx::sdesc_sw128(sb + k * 32, 16, 1024);
                                 const uint32_t acc = (kk != kb0 || k != 0) ? 1u : 0u;
-                                if constexpr (PAIR)
+                                if constexpr (EPI == EPI_NS_GRAM32) {
+                                    // hi lo^T + lo hi^T + hi hi^T (both tiles are 128 x 64 in the
+                                    // same layout, the high part in A's place)
+                                    ptx::umma_f16_ss(d_tmem, ad, bd, IDESC, acc);
+                                    ptx::umma_f16_ss(d_tmem, bd, ad, IDESC, 1u);
+                                    ptx::umma_f16_ss(d_tmem, ad, ad, IDESC, 1u);
+                                } else if constexpr (PAIR)
                                     ptx::umma_f16_ss_pair(d_tmem, ad, bd, IDESC, acc);
                                 else
                                     ptx::umma_f16_ss(d_tmem, ad, bd, IDESC, acc);
@@ -1700,6 +1713,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             float v[32];
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = sum[c * 32 + i];
+                            if constexpr (EPI == EPI_XENT_FOLD) {
+                                xent_stats_chunk(p, v, row, col0 + c * 32, xr);
+                                if (c == CHUNKS - 1) xent_stats_flush(p, row, (col0 + c * 32) >> 7, xr);
+                                continue;
+                            }
                             finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg);
                         }
                     }
@@ -2051,7 +2069,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         return cudaErrorInvalidValue;
     }
     // A map that no epilogue uses is a copy of one that exists (encoding takes host time).
-    if constexpr (EPI == EPI_XENT_STATS) {
+    if constexpr (is_stats(EPI)) {
         mo0 = mo1 = mo2 = ma;
     } else {
         if (!(o_rank > 3 ? make_map_view(&mo0, o0, g.o_view, 32, 32, so)
@@ -2088,8 +2106,12 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.batch = static_cast<int>(nb * splits);
     p.matrices = static_cast<int>(nb);
     p.kb_seg = p.kb_per_shard;
-    if (SEG && g.parts > 1) p.kb_per_shard *= 6;
-    if (is_ns2(EPI)) p.kb_per_shard *= 3;
+    p.pairs = SEG && g.parts > 1 ? 6 : 1;
+    if (EPI == EPI_XENT_FOLD)
+        p.kb_seg = p.nshards * p.kb_per_shard / p.pairs;
+    else
+        p.kb_per_shard *= p.pairs;
+    if (EPI == EPI_NS_FINAL) p.kb_per_shard *= 3;
     p.scale = g.scale;
     p.causal = g.causal ? 1 : 0;
     p.rowvec = g.rowvec;
@@ -2191,7 +2213,9 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 template <int EPI, bool A_MN, bool B_MN>
 static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
-    if constexpr (EPI == EPI_NS_GRAM32) {
+    if constexpr (EPI == EPI_XENT_FOLD) {
+        return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
+    } else if constexpr (EPI == EPI_NS_GRAM32) {
         return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);  // outputs of at most 128 x 128
     } else if constexpr (EPI == EPI_NS_FINAL) {
         return launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
@@ -2228,7 +2252,7 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
-    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || tc::has_segments(epi))) return false;
+    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || (tc::has_segments(epi) && epi != EPI_XENT_FOLD))) return false;
     const char *w = std::getenv("TPMLP_WIDE");
     return !(w && w[0] == '0');
 }
@@ -2260,6 +2284,9 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
             break;
         case EPI_XENT_STATS:  // X[T,h] (K-major) . W[V,h]^T (K-major)
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_STATS, false, false>(g, num_sms, st);
+            break;
+        case EPI_XENT_FOLD:
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_FOLD, false, false>(g, num_sms, st);
             break;
         case EPI_XENT_GRAD:
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_GRAD, false, false>(g, num_sms, st);

@@ -175,6 +175,8 @@ def _check(status: int, what: str):
 
 
 def _need(x, name, dtype, shape):
+    if x.is_cuda and x.dtype is dtype and x.shape == shape and x.is_contiguous():
+        return
     if not (x.is_cuda and x.is_contiguous()):
         raise ValueError("%s must be a contiguous CUDA tensor" % name)
     if x.dtype != dtype:
@@ -424,9 +426,20 @@ def _status_workspace(nbytes, device):
 
 
 def _same_device(ctx, *tensors):
+    device = ctx.workspace.device
     for x in tensors:
-        if x is not None and x.device != ctx.workspace.device:
-            raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
+        if x is not None and x.device != device:
+            raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, device))
+
+
+def _call(ctx, fn, name, args, stream):
+    """fn(*args, stream) with the context's device as the current one."""
+    device = ctx.workspace.device
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), name)
 
 
 class XentContext:
@@ -465,10 +478,9 @@ def xent_forward(ctx: XentContext, X, W, target, loss=None, stream=None):
         loss = torch.empty((T,), dtype=torch.float32, device=X.device)
     _need(loss, "loss", torch.float32, (T,))
     _same_device(ctx, X, W, target, loss)
-    with torch.cuda.device(X.device):
-        st = lib.tpmlp_xent_forward(ctypes.byref(s), _ptr(X), _ptr(W), _ptr(target), _ptr(loss), _ptr(ctx.lse),
-                                    _ptr(ctx.workspace), _stream(stream))
-    _check(st, "tpmlp_xent_forward")
+    _call(ctx, lib.tpmlp_xent_forward, "tpmlp_xent_forward",
+          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(), ctx.lse.data_ptr(),
+           ctx.workspace.data_ptr()), stream)
     ctx._saved = (X, W, target)
     return loss
 
@@ -492,10 +504,9 @@ def xent_backward(ctx: XentContext, dloss, dX=None, dW=None, need_dX=True, need_
         if x is not None:
             _need(x, n, ctx.dtype, shp)
     _same_device(ctx, dloss, dX, dW)
-    with torch.cuda.device(X.device):
-        st = lib.tpmlp_xent_backward(ctypes.byref(s), _ptr(X), _ptr(W), _ptr(target), _ptr(ctx.lse), _ptr(dloss),
-                                     _ptr(dX), _ptr(dW), _ptr(ctx.workspace), _stream(stream))
-    _check(st, "tpmlp_xent_backward")
+    _call(ctx, lib.tpmlp_xent_backward, "tpmlp_xent_backward",
+          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), ctx.lse.data_ptr(), dloss.data_ptr(),
+           _ptr(dX), _ptr(dW), ctx.workspace.data_ptr()), stream)
     return {"dX": dX, "dW": dW}
 
 
@@ -531,9 +542,8 @@ def orthogonalize(ctx: OrthoContext, G, O=None, stream=None):
         O = torch.empty(shape, dtype=torch.bfloat16, device=G.device)
     _need(O, "O", torch.bfloat16, shape)
     _same_device(ctx, G, O)
-    with torch.cuda.device(G.device):
-        st = lib.tpmlp_orthogonalize(ctypes.byref(s), _ptr(G), _ptr(O), _ptr(ctx.workspace), _stream(stream))
-    _check(st, "tpmlp_orthogonalize")
+    _call(ctx, lib.tpmlp_orthogonalize, "tpmlp_orthogonalize",
+          (ctypes.byref(s), G.data_ptr(), O.data_ptr(), ctx.workspace.data_ptr()), stream)
     return O
 
 
