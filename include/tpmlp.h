@@ -307,8 +307,8 @@ tpmlp_status tpmlp_attn_backward(const tpmlp_attn_shape *shape, const void *dZ, 
  * backward, for the gradients dloss_i of the per-token losses (1/T each for their
  * mean):
  *   dS = (exp(S - lse) - onehot(target)) * dloss,   dX = dS W,   dW = dS^T X.
- * The forward pass keeps one (maximum, sum of exponentials) pair per token and 128
- * vocabulary rows, in fp32, and joins them in a fixed order; the backward pass
+ * The forward pass keeps one (maximum, sum of exponentials) pair per token and 16 to
+ * 128 vocabulary rows, in fp32, and joins them in a fixed order; the backward pass
  * recomputes the logits of one piece of the vocabulary at a time and holds that
  * piece's dS. */
 typedef struct {
@@ -322,7 +322,7 @@ typedef struct {
 } tpmlp_xent_shape;
 
 /* Bytes of device workspace of both passes: status word, statistics (8 bytes per
- * token and 128 vocabulary rows), dS of one piece (T * piece elements; FFMA path also
+ * token and 128 vocabulary rows, or per 16 at the fewest where there are few tokens), dS of one piece (T * piece elements; FFMA path also
  * its fp32 logits) and, for bf16 and several pieces, dX in fp32.  256-byte aligned,
  * first 8 bytes zero before first use; 0 for an invalid shape. */
 size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);

@@ -1133,8 +1133,38 @@ Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
     return best;
 }
 
+// The forward product's tiles.  512: 256 x 512 with the whole K in one accumulator.
+// Otherwise 256 x tile_n with K in ranges that the epilogue adds up in fp32: the tensor
+// core cuts the accumulator off (does not round) at every step of 16 products, an error of
+// about 2.5e-10 h of the loss, so that beyond 4096 products it would pass 1e-6.
+// On 256 x 256 tiles and in ranges the product is 8 to 12% slower (T = 8192, h = 4096,
+// V = 65536: 2.10 against 2.27 ms).  Where there are few tiles the ranges cost nothing,
+// and narrower tiles divide the vocabulary evenly among the 76 units; fp32 operands
+// want the precision and take short ranges always.
+struct StatsTile {
+    int tile_n;  // 0: a pass over W without tiles, for few tokens
+    int64_t ranges, range;
+};
+StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
+    const int64_t T = s->tokens, V = s->vocab, h = s->hidden, units = 76;
+    const bool f32 = s->dtype == TPMLP_F32;
+    const int64_t m = (T + 255) / 256, tiles = m * ((V + 255) / 256);
+    if (tpmlp::xent_few(!f32, T, h)) return {0, 1, h};
+    const bool few = m == 1 || tiles <= 4 * units;
+    if (!f32 && !few && h <= 4096) return {512, 1, h};
+    int64_t tile_n = 256;
+    if (few) {  // as many waves as 256-wide tiles need, evenly filled
+        const int64_t waves = (tiles + units - 1) / units, per = std::max<int64_t>(1, waves * units / m);
+        tile_n = std::min<int64_t>(256, ((V + per - 1) / per + 31) / 32 * 32);
+    }
+    const int64_t longest = f32 ? 512 : (few ? 1024 : 2816);
+    const int64_t ranges = (h + longest - 1) / longest;
+    return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64};
+}
+
 struct XentLayout {
     int64_t piece, pieces, groups, hp, ldo;
+    StatsTile stats;
     Split dx, dw;
     size_t part, target_logit, row_g, xp, wp, ds, logits, acc, dwacc, total;
 };
@@ -1149,7 +1179,12 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
     const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
     L.piece = xent_piece(s);
     L.pieces = (s->vocab + L.piece - 1) / L.piece;
-    L.groups = tc ? (s->vocab + tpmlp::XENT_GROUP - 1) / tpmlp::XENT_GROUP : L.pieces;
+    L.stats = xent_stats_tile(s);
+    // stored groups, and those of them that hold columns
+    const size_t stored = static_cast<size_t>(!tc                     ? L.pieces
+                                              : L.stats.tile_n == 0 ? tpmlp::xent_few_groups(s->vocab)
+                                                                    : tpmlp::xent_groups(s->vocab, L.stats.tile_n));
+    L.groups = tc && L.stats.tile_n == 512 ? (s->vocab + 127) / 128 : static_cast<int64_t>(stored);
     L.hp = (s->hidden + 63) / 64 * 64;
     L.ldo = (s->hidden + 3) / 4 * 4;
     L.dx = L.dw = {1, 0};
@@ -1163,9 +1198,8 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
         off += align_up(bytes, 1024);
         return at;
     };
-    const size_t groups_stored = static_cast<size_t>(tc ? tpmlp::xent_groups(s->vocab) : L.pieces);
     const size_t piece = static_cast<size_t>(L.piece), hp = static_cast<size_t>(L.hp), ldo = static_cast<size_t>(L.ldo);
-    L.part = region(groups_stored * T * sizeof(float2));
+    L.part = region(stored * T * sizeof(float2));
     L.target_logit = region(T * 4);
     L.row_g = region(T * 4);
     L.xp = region(tc && f32 ? 3 * T * hp * 2 : 0);
@@ -1308,27 +1342,26 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
     int sms;
     if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
     const XentCall c(s, target, workspace, sms, stream);
-    cudaError_t e = c.split_operands(X, W);
-    if (e != cudaSuccess) return from_cuda(e);
-    if (xent_tc(s)) {
+    cudaError_t e = cudaSuccess;
+    if (xent_tc(s) && c.L.stats.tile_n == 0) {
+        float2 *part = reinterpret_cast<float2 *>(c.ws + c.L.part);
+        e = c.kernel("xent_few", [&] {
+            return tpmlp::launch_xent_few(s->dtype == TPMLP_BF16, c.rows, X, W, s->hidden, part, c.st);
+        });
+        if (e != cudaSuccess) return from_cuda(e);
+    } else if (xent_tc(s)) {
+        e = c.split_operands(X, W);
+        if (e != cudaSuccess) return from_cuda(e);
         GemmArgs g = c.logits(X, W, 0, s->vocab);
         g.part = reinterpret_cast<float2 *>(c.ws + c.L.part);
         g.target_logit = c.rows.target_logit;
-        // The tensor core cuts the accumulator off at every step of 16 products, an error of
-        // about 2.5e-10 h of the logit.  Beyond 4096 products (1e-6) the sums are taken in
-        // ranges that the epilogue adds up in fp32, on 256 x 256 tiles; the 256 x 512 tiles
-        // are 8% faster (T = 8192, h = 4096, V = 65536: 2.10 against 2.27 ms).  Few tokens are
-        // bound by W's bytes, and fp32 operands want the precision: both take the
-        // ranges always, short ones.
-        const bool f32 = s->dtype == TPMLP_F32, few = s->tokens <= 256;
-        if (f32 || few || s->hidden > 4096) {
-            const int64_t range = f32 ? 512 : (few ? 1024 : 2048), ranges = (s->hidden + range - 1) / range;
-            g.nshards = static_cast<int>(ranges * (f32 ? 6 : 1));
-            g.kshard = ((s->hidden + ranges - 1) / ranges + 63) / 64 * 64;
-            e = c.launch("xent_stats", tpmlp::EPI_XENT_FOLD, g);
-        } else {
-            e = c.launch("xent_stats", tpmlp::EPI_XENT_STATS, g);
+        const StatsTile &t = c.L.stats;
+        if (t.tile_n < 512) {
+            g.tile_n = t.tile_n;
+            g.nshards = static_cast<int>(t.ranges * (c.parts() ? 6 : 1));
+            g.kshard = t.range;
         }
+        e = c.launch("xent_stats", t.tile_n < 512 ? tpmlp::EPI_XENT_FOLD : tpmlp::EPI_XENT_STATS, g);
         if (e != cudaSuccess) return from_cuda(e);
     } else {
         float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
@@ -1507,6 +1540,8 @@ bool ortho_valid(const tpmlp_ortho_shape *s) {
     if (s->steps < 1 || s->steps > 32) return false;
     if (s->dtype != TPMLP_F32 && s->dtype != TPMLP_BF16) return false;
     if (!(s->eps >= 0.0f) || !std::isfinite(s->eps)) return false;
+    // 32-bit counts of 16-byte pieces
+    if ((s->rows + 64) * (s->cols + 64) >= (1LL << 34)) return false;
     return tiles_fit(s->rows + 64, s->cols + 64, s->batch);
 }
 
@@ -1615,7 +1650,6 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
     auto product = [&](const void *x, bool x_mn, const void *y, bool y_mn, int64_t M,
                        int64_t N, int64_t K, void *out) {
         GemmArgs g = base_args(status);
-        g.cta_pair = true;
         g.a = x, g.a_mn = x_mn;
         g.b = y, g.b_mn = y_mn;
         g.M = M, g.N = N, g.K = K, g.kshard = K;
@@ -1624,6 +1658,13 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         return g;
     };
     auto launch = [&](const char *name, Epi epi, GemmArgs &g) {
+        // Products of few tiles are bound by their latency, which 128 x 128 tiles on single CTAs
+        // keep shorter than 256 x 256 tiles on CTA pairs, up to about two waves of them
+        // (256 x 1024: 148 against 109 us, 700 x 8000: 393 against 365 us, six of 515 x 1003: 204
+        // against 183 us; 4096 x 4096, beyond it, the same with either).
+        const int64_t mt = (g.M + 127) / 128, nt = (g.N + 127) / 128;
+        const bool sym = epi == tpmlp::EPI_NS_GRAM || epi == tpmlp::EPI_NS_POLY;
+        g.cta_pair = (sym ? mt * (mt + 1) / 2 : mt * nt) * s->batch > 400;
         pick_raster(g, epi);
         Timed timed(name, st);
         const cudaError_t r = tpmlp::launch_tc_gemm(epi, g, sms, st);
@@ -1652,7 +1693,6 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         void *out = tma_out ? O : ws + L.hi[1];
         GemmArgs u = L.wide ? product(c.Q, false, ws + L.hi[0], true, L.P, L.Q, L.p, out)
                             : product(ws + L.hi[0], false, c.Q, false, L.P, L.Q, L.p, out);
-        u.cta_pair = false;  // 128 rows hold all of a wide matrix
         u.scale = 1.0f / (kScaleX * L.q_scale);
         u.out_rows = tma_out ? s->rows : L.P, u.out_cols = tma_out ? s->cols : L.Q;
         e = launch("ortho_final", tpmlp::EPI_NS_FINAL, u);

@@ -99,11 +99,12 @@ struct GemmArgs {
     // col0 .. col0 + N - 1 of W.
     const int64_t *target;   // [M]
     int64_t ignore_index, col0;
-    float2 *part;            // STATS: (max, sum) of 128-column group k, row m, at part[k * M + m]
+    float2 *part;            // STATS: (max, sum) of column group k, row m, at part[k * M + m]
     float *target_logit;     // STATS: [M], written where the target is one of the columns
     const float *row_lse;    // GRAD: [M]
     const float *row_g;      // GRAD: [M]
     bool accumulate;         // EPI_ACC32: add to what out0 holds
+    int tile_n;              // EPI_XENT_FOLD: columns per tile, a multiple of 32 up to 256 (0: 256)
     // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
     // two parts of X through aux (high) and aux2 (low).  out0 / out1: X' high, low.
     // LAST writes an [batch][out_rows][out_cols] array, the rest of the tile is dropped.
@@ -112,9 +113,11 @@ struct GemmArgs {
     int64_t out_rows, out_cols;
 };
 
-// Columns per group of the EPI_XENT_STATS partials, and the groups that N columns make.
-constexpr int64_t XENT_GROUP = 128;
-inline int64_t xent_groups(int64_t N) { return (N + 511) / 512 * 4; }
+// Column groups of the EPI_XENT_STATS partials: four per 512-wide tile (128 columns each), or
+// two per tile of EPI_XENT_FOLD.
+inline int64_t xent_groups(int64_t N, int tile_n) {
+    return tile_n == 512 ? (N + 511) / 512 * 4 : (N + tile_n - 1) / tile_n * 2;
+}
 
 // Tensor-core path: bf16 operands, fp32 accumulation in TMEM (tcgen05).
 cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t st);
@@ -184,6 +187,12 @@ struct RowArgs {
     uint32_t *status;
 };
 cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st);
+// Statistics of few tokens in one pass over W (xent_few says whether these are); partials in `groups` = xent_few_groups(vocab) groups.
+constexpr int64_t XENT_FEW_SMEM = 192 * 1024;
+bool xent_few(bool is_bf16, int64_t tokens, int64_t hidden);
+int64_t xent_few_groups(int64_t vocab);
+cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden, float2 *part,
+                            cudaStream_t st);
 cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st);
 // out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,

@@ -121,32 +121,45 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
     const int64_t z = blockIdx.y;
     const float f = inverse_norm(part + z * nparts, nparts, eps, scale);
     const T *g = G + z * rows * cols;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < P * Q / 8;
-         i += static_cast<int64_t>(gridDim.x) * THREADS) {
-        const int64_t r = i / (Q / 8), c = (i - r * (Q / 8)) * 8;
-        float v[8];
-        if (VEC && r < rows && c + 8 <= cols) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(g + r * cols + c);
-            alignas(16) T t[8];
-            *reinterpret_cast<uint4 *>(t) = __ldg(src);
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t + 4) = __ldg(src + 1);
+    // UN loads in flight per thread before the first is used
+    constexpr int UN = 4;
+    const uint32_t per_row = static_cast<uint32_t>(Q / 8), total = static_cast<uint32_t>(P * Q / 8);
+    const uint32_t stride = gridDim.x * THREADS;
+    for (uint32_t i0 = blockIdx.x * THREADS + threadIdx.x; i0 < total; i0 += UN * stride) {
+        float v[UN][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = value<T>(t[j]);
-        } else {
+        for (int u = 0; u < UN; ++u) {
+            const uint32_t i = i0 + u * stride;
+            if (i >= total) break;
+            const int64_t r = i / per_row, c = (i - static_cast<uint32_t>(r) * per_row) * 8;
+            if (VEC && r < rows && c + 8 <= cols) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(g + r * cols + c);
+                alignas(16) T t[8];
+                *reinterpret_cast<uint4 *>(t) = __ldg(src);
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t + 4) = __ldg(src + 1);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = r < rows && c + j < cols ? value<T>(g[r * cols + c + j]) : 0.0f;
+                for (int j = 0; j < 8; ++j) v[u][j] = value<T>(t[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[u][j] = r < rows && c + j < cols ? value<T>(g[r * cols + c + j]) : 0.0f;
+            }
         }
-        alignas(16) __half h[8];
-        alignas(16) __half l[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x = v[j] * f;
-            h[j] = __float2half_rn(x);
-            l[j] = __float2half_rn((x - __half2float(h[j])) * lo_scale);
+        for (int u = 0; u < UN; ++u) {
+            const uint32_t i = i0 + u * stride;
+            if (i >= total) break;
+            alignas(16) __half h[8];
+            alignas(16) __half l[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = v[u][j] * f;
+                h[j] = __float2half_rn(x);
+                l[j] = __float2half_rn((x - __half2float(h[j])) * lo_scale);
+            }
+            const int64_t o = z * P * Q + static_cast<int64_t>(i) * 8;
+            *reinterpret_cast<uint4 *>(hi + o) = *reinterpret_cast<const uint4 *>(h);
+            *reinterpret_cast<uint4 *>(lo + o) = *reinterpret_cast<const uint4 *>(l);
         }
-        const int64_t o = z * P * Q + r * Q + c;
-        *reinterpret_cast<uint4 *>(hi + o) = *reinterpret_cast<const uint4 *>(h);
-        *reinterpret_cast<uint4 *>(lo + o) = *reinterpret_cast<const uint4 *>(l);
     }
 }
 
@@ -156,11 +169,13 @@ __global__ void __launch_bounds__(THREADS) unpad_kernel(const __nv_bfloat16 *in,
                                                         int64_t Q, __nv_bfloat16 *out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t z = blockIdx.y;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < rows * cols;
-         i += static_cast<int64_t>(gridDim.x) * THREADS) {
-        const int64_t r = i / cols;
-        out[z * rows * cols + i] = in[z * P * Q + r * Q + (i - r * cols)];
+    // a warp per row: its loads and stores of consecutive columns coalesce
+    const int64_t z = blockIdx.y, warps = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+        const __nv_bfloat16 *src = in + (z * P + r) * Q;
+        __nv_bfloat16 *dst = out + (z * rows + r) * cols;
+#pragma unroll 4
+        for (int64_t c = threadIdx.x & 31; c < cols; c += 32) dst[c] = src[c];
     }
 }
 
@@ -183,7 +198,7 @@ static cudaError_t launch_start(const OrthoStart &a, cudaStream_t st) {
     Blue *part = static_cast<Blue *>(a.part);
     cudaError_t e = launch_pdl(vec_all ? norm_kernel<T, true> : norm_kernel<T, false>, gn, THREADS, 0, st, G, n, per, part);
     if (e != cudaSuccess) return e;
-    const dim3 gs(grid_x(a.P * a.Q / 8, a.batch), static_cast<unsigned>(a.batch));
+    const dim3 gs(grid_x(a.P * a.Q / 32, a.batch), static_cast<unsigned>(a.batch));
     __half *hi = static_cast<__half *>(a.hi), *lo = static_cast<__half *>(a.lo);
     return launch_pdl(vec_rows ? scale_kernel<T, true> : scale_kernel<T, false>, gs, THREADS, 0, st, G, a.rows, a.cols,
                       a.P, a.Q, part, static_cast<int>(nb), a.eps, a.scale, hi, lo, a.lo_scale);
@@ -202,7 +217,7 @@ cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t s
 
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                void *out, cudaStream_t st) {
-    const dim3 g(ortho::grid_x(rows * cols, batch), static_cast<unsigned>(batch));
+    const dim3 g(ortho::grid_x(rows * 32, batch), static_cast<unsigned>(batch));
     return launch_pdl(ortho::unpad_kernel, g, ortho::THREADS, 0, st, static_cast<const __nv_bfloat16 *>(in), rows, cols,
                       P, Q, static_cast<__nv_bfloat16 *>(out));
 }

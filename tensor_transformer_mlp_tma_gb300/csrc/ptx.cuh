@@ -434,6 +434,28 @@ __device__ __forceinline__ uint32_t f16x2_satfinite(float lo, float hi) {
     return r;
 }
 
+// D += A B for one warp: A 16 x 16 (row r = lane / 4 in a[0], a[2], row r + 8 in a[1], a[3]), B
+// 16 x 8 (column lane / 4), bf16, D 16 x 8 in fp32.  For products that are bound by
+// memory and too narrow for a tcgen05 tile.
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fused multiply-adds of one instruction: (a.x b.x + c.x, a.y b.y + c.y).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // 2^x via the MUFU approximation (relative error about 2^-22; 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;

@@ -62,6 +62,10 @@ constexpr int MN_BLOCK_BYTES = 64 * BK * 2;             // one 64(MN) x 64(K) TM
 constexpr int STG_BOX = 32 * 32 * 2;
 constexpr int STG_BOX_WIDE = 32 * 64 * 2;
 
+__host__ __device__ constexpr bool is_ns_tile(int epi) {
+    return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
+}
+
 // Per-CTA pipeline geometry.  CG = 1: one CTA computes a 128 x 256 tile and loads
 // all of B's 256 columns.  CG = 2: a CTA pair computes a 256 x 256 tile with
 // CTA-pair MMAs; each CTA loads its own 128 rows of A and 128 of B's columns, so
@@ -89,10 +93,13 @@ struct Cfg {
     static constexpr int B_STAGE = B_ROWS * BK * 2;
     static constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
     static constexpr bool DS = EPI_ == EPI_ATTN_DS;
-    static constexpr int STG_PER_WARP = DS ? 2 * STG_BOX_WIDE : 2 * STG_BOX;
+    // The Newton-Schulz products on single CTAs (few, small tiles) have two pairs of boxes,
+    // one for each of a warp's two chunks, so that no chunk waits for a store.
+    static constexpr bool SMALL = CG == 1 && TILE_N == 128 && is_ns_tile(EPI_);
+    static constexpr int STG_PER_WARP = DS ? 2 * STG_BOX_WIDE : (SMALL ? 4 * STG_BOX : 2 * STG_BOX);
     // dS: the K extent is one head dimension (two K blocks per tile), so fewer
     // stages make room for its wider staging boxes
-    static constexpr int STAGES = CG == 1 ? (DS ? 3 : (TILE_N == 128 ? 6 : 4)) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
+    static constexpr int STAGES = CG == 1 ? (DS ? 3 : (TILE_N == 128 ? (SMALL ? 5 : 6) : 4)) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
     static constexpr int SMEM_DYN = STAGES * STAGE_BYTES + (EPI_THREADS / 32) * STG_PER_WARP + 1024;
 };
 constexpr int MAX_STAGES = 8;
@@ -168,6 +175,10 @@ struct Params {
     // pair, or six for fp32 operands in three parts); problem z starts at k-block
     // z * kb_seg (split K) and reads the operands of problem 0.
     int kb_seg, pairs;
+    // EPI_XENT_FOLD: the tile's columns (a multiple of 32, up to TILE_N), the MMA's descriptor and
+    // the stage's bytes for them.
+    int tile_n;
+    uint32_t idesc, stage_bytes;
     int matrices;  // EPI_NS_GRAM32, EPI_NS_FINAL: problem z is matrix z % matrices, K range z / matrices
     // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
     const void *aux2;
@@ -651,13 +662,14 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, Xent
 
 // One pass of the online softmax over 32 logits: the running maximum moves to m',
 // the running sum is scaled by exp(m - m') and the 32 exponentials are added, all
-// in fp32.  Columns past N count as -inf.
-__device__ __forceinline__ void xent_stats_chunk(const Params &p, float (&v)[32], int64_t row, int col, XentRow &x) {
-    if (col >= p.N) return;
-    if (col + 32 > p.N) {
+// in fp32.  Columns from `end` on count as -inf.
+__device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, int col, int end, const Params &p,
+                                                 XentRow &x) {
+    if (col >= end) return;
+    if (col + 32 > end) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (col + i >= p.N) v[i] = -INFINITY;
+            if (col + i >= end) v[i] = -INFINITY;
     }
     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -672,7 +684,7 @@ __device__ __forceinline__ void xent_stats_chunk(const Params &p, float (&v)[32]
     x.s = (s[0] + s[1]) + (s[2] + s[3]);
     // the target's logit, where it is one of these columns (few warps at a time)
     const int at = x.tcol - col;
-    const bool here = at >= 0 && at < 32;
+    const bool here = at >= 0 && at < 32 && x.tcol < end;
     if (__any_sync(0xffffffffu, here)) {
         float z = 0.0f;
 #pragma unroll
@@ -763,7 +775,7 @@ __device__ __forceinline__ void stage_transposed(uint32_t box, int lane, const u
 template <int EPI>
 __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0, const CUtensorMap *tm1,
                                          float (&v)[32], const HalfPre &h0, const HalfPre &h1, int64_t row, int row0,
-                                         int col, int z, bool mirror, int lane, uint32_t stg) {
+                                         int col, int z, bool mirror, int lane, uint32_t stg, bool fresh) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= p.scale;
     if constexpr (EPI == EPI_NS_POLY) {
@@ -794,7 +806,8 @@ __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0
             w1[i] = ptx::f16x2_satfinite((v[2 * i] - a) * 2048.0f, (v[2 * i + 1] - b) * 2048.0f);
         }
     }
-    if (lane == 0) ptx::bulk_wait_read0();
+    // `fresh`: the first chunk of the tile has waited for the boxes of the second too
+    if (!fresh && lane == 0) ptx::bulk_wait_read0();
     __syncwarp();
     stage_row(stg, lane, w0);
     if constexpr (EPI == EPI_NS_UPDATE) stage_row(stg + STG_BOX, lane, w1);
@@ -1018,11 +1031,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
     constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
                                           : ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
+    // The few-token statistics take narrower tiles, so that the vocabulary divides evenly
+    // among the units.
+    constexpr bool ANY_N = EPI == EPI_XENT_FOLD;
+    const int tile_n = ANY_N ? p.tile_n : TILE_N;
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
-                      (TILE_N == 128 && CG == 1 && EPI == EPI_NS_GRAM32),
-                  "narrow tile: CTA pairs and plain store, or single CTAs and the small Gram matrices");
+                      (TILE_N == 128 && CG == 1 && (EPI == EPI_NS_GRAM32 || is_ns_tile(EPI))),
+                  "narrow tile: CTA pairs and plain store, or single CTAs and Newton-Schulz products");
     static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
                   "wide tile: CTA pairs, one shard");
     static_assert(!is_sym(EPI) || C::TILE_M == TILE_N, "symmetric outputs: square tiles");
@@ -1195,11 +1212,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 coords_of<EPI>(tile, p, mb, nb, zb);
                 if (!tile_active<C::TILE_M, C::TILE_N>(p, mb, nb)) continue;
                 const int m0 = mb * C::TILE_M + BM * static_cast<int>(rank);
-                const int n0 = nb * TILE_N + C::B_ROWS * static_cast<int>(rank);
+                const int n0 = ANY_N ? nb * tile_n + tile_n / CG * static_cast<int>(rank)
+                                     : nb * TILE_N + C::B_ROWS * static_cast<int>(rank);
                 int kb0, kb1;
                 k_range<C::TILE_M>(p, mb, kb0, kb1);
                 if (!dbg_ok(mb >= 0 && mb < p.m_tiles && nb >= 0 && nb < p.n_tiles && zb >= 0 && zb < p.batch &&
-                                kb0 >= 0 && kb0 <= kb1 && kb1 <= p.nshards * p.kb_per_shard && n0 % 64 == 0,
+                                kb0 >= 0 && kb0 <= kb1 && kb1 <= p.nshards * p.kb_per_shard && (ANY_N || n0 % 64 == 0),
                             p, &abort_sh, 0x0401u)) {
                     ok = false;
                     break;
@@ -1291,7 +1309,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     // The leader announces the bytes of both CTAs' copies; the peer's
                     // copies only complete bytes on the leader's barrier (they can land
                     // before the announcement: the phase still needs the arrival).
-                    if (leader) ptx::mbar_arrive_expect_tx(full_local, CG * C::STAGE_BYTES);
+                    if (leader)
+                        ptx::mbar_arrive_expect_tx(full_local, CG * (ANY_N ? p.stage_bytes : C::STAGE_BYTES));
                     if constexpr (HEADS) {
                         // per-head operands addressed in place (rank-3/4/5 maps)
                         int a2, a3, a4, b2, b3, b4;
@@ -1518,7 +1537,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 const uint64_t bd = B_MN ? ptx::sdesc_sw128(sb + k * 2048, MN_BLOCK_BYTES, 1024)
                                                          : ptx::sdesc_sw128(sb + k * 32, 16, 1024);
                                 const uint32_t acc = (kk != kb0 || k != 0) ? 1u : 0u;
-                                if constexpr (EPI == EPI_NS_GRAM32) {
+                                if constexpr (ANY_N) {
+                                    if constexpr (PAIR)
+                                        ptx::umma_f16_ss_pair(d_tmem, ad, bd, p.idesc, acc);
+                                } else if constexpr (EPI == EPI_NS_GRAM32) {
                                     // hi lo^T + lo hi^T + hi hi^T (both tiles are 128 x 64 in the
                                     // same layout, the high part in A's place)
                                     ptx::umma_f16_ss(d_tmem, ad, bd, IDESC, acc);
@@ -1641,7 +1663,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     continue;
                 }
                 if constexpr (EPI == EPI_XENT_STATS) {
-                    xent_stats_chunk(p, v, row, col0 + 32 * q, xr);
+                    xent_stats_chunk(v, row, col0 + 32 * q, p.N, p, xr);
                     if ((q & 3) == 3) xent_stats_flush(p, row, (col0 + 32 * q) >> 7, xr);
                     continue;
                 }
@@ -1662,7 +1684,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!tile_active<C::TILE_M, C::TILE_N>(p, mb, nb)) continue;
             const int row0 = mb * C::TILE_M + BM * static_cast<int>(rank) + quarter * 32;
             const int64_t row = static_cast<int64_t>(row0) + lane;
-            const int col0 = nb * TILE_N + half * (TILE_N / 2);
+            const int col0 = nb * tile_n + half * (tile_n / 2);
             if constexpr (EPI == EPI_DGELU) aux_issue(&tmO1, aux, stg + STG_BOX, col0, row0, zb, lane);
             if constexpr (EPI == EPI_ATTN_DS) aux_issue(&tmO1, aux, stg + STG_BOX_WIDE, col0, row0, zb, lane, STG_BOX_WIDE);
             XentRow xr;
@@ -1686,9 +1708,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = tmem_base + lane_off + buf * TILE_N + half * (TILE_N / 2);
+                const uint32_t taddr = tmem_base + lane_off + buf * TILE_N + half * (tile_n / 2);
                 if (!dbg_ok(buf * TILE_N + TILE_N <= TMEM_COLS && stg + C::STG_PER_WARP <= stg_end &&
-                                col0 % 32 == 0 && row0 % 32 == 0 && mb >= 0 && mb < p.m_tiles && nb >= 0 &&
+                                (ANY_N || col0 % 32 == 0) && row0 % 32 == 0 && mb >= 0 && mb < p.m_tiles && nb >= 0 &&
                                 nb < p.n_tiles && zb >= 0 && zb < p.batch,
                             p, &abort_sh, 0x0903u)) {
                     ok = false;
@@ -1714,8 +1736,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = sum[c * 32 + i];
                             if constexpr (EPI == EPI_XENT_FOLD) {
-                                xent_stats_chunk(p, v, row, col0 + c * 32, xr);
-                                if (c == CHUNKS - 1) xent_stats_flush(p, row, (col0 + c * 32) >> 7, xr);
+                                // the half's columns end at tile_n / 2, inside a chunk or before it
+                                xent_stats_chunk(v, row, col0 + c * 32, min(p.N, col0 + tile_n / 2), p, xr);
+                                if (c == CHUNKS - 1) xent_stats_flush(p, row, 2 * nb + half, xr);
                                 continue;
                             }
                             finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg);
@@ -1790,9 +1813,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         if constexpr (is_ns(EPI)) {
                             const HalfPre c0 = h0, c1 = h1;
                             if (c < CHUNKS - 1) ns_fetch(col0 + (c + 1) * 32);
-                            ns_chunk<EPI>(p, &tmO0, &tmO1, v, c0, c1, row, row0, col0 + c * 32, zb, mb != nb, lane, stg);
+                            ns_chunk<EPI>(p, &tmO0, &tmO1, v, c0, c1, row, row0, col0 + c * 32, zb, mb != nb, lane,
+                                          stg + (C::SMALL ? (c & 1) * 2 * STG_BOX : 0), C::SMALL && (c & 1));
                         } else if constexpr (EPI == EPI_XENT_STATS) {
-                            xent_stats_chunk(p, v, row, col0 + c * 32, xr);
+                            xent_stats_chunk(v, row, col0 + c * 32, p.N, p, xr);
                             if ((c & 3) == 3) xent_stats_flush(p, row, (col0 + c * 32) >> 7, xr);
                         } else {
                         finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg, &aux,
@@ -1999,6 +2023,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // B operand: this CTA's B_ROWS columns, K-major in one box or MN-major in 64-wide boxes.
     const int64_t nb = g.batch < 1 ? 1 : g.batch;
     constexpr bool SEG = has_segments(EPI);
+    const int any_n = EPI == EPI_XENT_FOLD ? (g.tile_n > 0 ? g.tile_n : TILE_N) : 0;
     const int64_t splits = g.ksplit > 1 ? g.ksplit : 1;
     const int64_t ni = SEG ? (g.parts > 1 ? g.parts : 1) : (is_ns2(EPI) ? 2 * nb : nb);  // matrices per operand
     const int64_t no = EPI == EPI_XENT_GRAD3 ? 3 : (SEG ? splits : nb * splits);         // and of the output
@@ -2031,7 +2056,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         okb = make_map_view(&mb, g.b, g.b_view, 64, B_MN ? BK : C::B_ROWS, sw);
     else
         okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, ni, bf, g.ldb, g.b_part)
-                          : make_map(&mb, g.b, g.N, g.K, BK, C::B_ROWS, sw, ni, bf, g.ldb, g.b_part));
+                          : make_map(&mb, g.b, g.N, g.K, BK, any_n ? any_n / CG : C::B_ROWS, sw, ni, bf, g.ldb, g.b_part));
     if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, ni, bf, g.ldb, g.b_part);
     if (!WIDE || (B_MN && !b4)) mb2 = mb;  // unused, or the per-block maps serve both widths
     if (!oka || !okb) return cudaErrorInvalidValue;
@@ -2089,6 +2114,12 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.N = static_cast<int>(g.N);
     p.m_tiles = static_cast<int>((g.M + C::TILE_M - 1) / C::TILE_M);
     p.n_tiles = static_cast<int>((g.N + TILE_N - 1) / TILE_N);
+    if (any_n) {
+        p.tile_n = any_n;
+        p.n_tiles = static_cast<int>((g.N + any_n - 1) / any_n);
+        p.idesc = ptx::idesc_bf16_f32(C::TILE_M, any_n, false, false);
+        p.stage_bytes = static_cast<uint32_t>(C::A_STAGE + any_n / CG * BK * 2);
+    }
     p.raster_n = g.raster_n ? 1 : 0;
     {
         const int fast_tiles = p.raster_n ? p.n_tiles : p.m_tiles;
@@ -2220,6 +2251,7 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
     } else if constexpr (EPI == EPI_NS_FINAL) {
         return launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
     } else if constexpr (is_ns(EPI)) {
+        if (!g.cta_pair) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
     if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || has_segments(EPI)) {

@@ -21,7 +21,7 @@ constexpr uint32_t STATUS_INVALID_ARG = 1;  // TPMLP_ERR_INVALID_ARG
 __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     const float mx = fmaxf(m, m2);
     const float base = mx == -INFINITY ? 0.0f : mx;
-    s = s * expf(m - base) + s2 * expf(m2 - base);
+    s = s * __expf(m - base) + s2 * __expf(m2 - base);
     m = mx;
 }
 
@@ -78,6 +78,242 @@ __global__ void row_g_kernel(const RowArgs a, const float *dloss, float *row_g) 
     ptx::griddep_launch_dependents();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (row < a.tokens) row_g[row] = target_ok(a, row) ? dloss[row] : 0.0f;
+}
+
+// ---- few tokens ------------------------------------------------------------------
+// Statistics of up to T tokens (one in bf16, up to eight in fp32) in one pass over W: X sits in shared memory, every warp
+// streams its share of W's rows, FEW_ROWS at a time, 512 bytes of each per load, and keeps its
+// own online softmax.  A product of so few rows would waste the tensor core's tile, and
+// its copies of 128-byte pieces of many rows read W at 3.2 to 3.6 TB/s (T = 1 to 8).
+// Bound by W's bytes.
+constexpr int FEW_THREADS = 512, FEW_ROWS = 4;
+
+// EC consecutive elements as fp32 pairs.
+template <typename E, int EC>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16, 8> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void stream(const __nv_bfloat16 *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float2 pair(int i) const {
+        const uint32_t u = i == 0 ? w.x : (i == 1 ? w.y : (i == 2 ? w.z : w.w));
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    }
+};
+template <>
+struct Chunk<float, 4> {
+    float4 w;
+    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void stream(const float *p) { w = __ldcs(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void zero() { w = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float2 pair(int i) const {
+        return i == 0 ? make_float2(w.x, w.y) : make_float2(w.z, w.w);
+    }
+};
+template <>
+struct Chunk<float, 1> {  // rows that do not start on 16 bytes
+    float w;
+    __device__ __forceinline__ void load(const float *p) { w = *p; }
+    __device__ __forceinline__ void stream(const float *p) { w = __ldcs(p); }
+    __device__ __forceinline__ void zero() { w = 0.0f; }
+    __device__ __forceinline__ float2 pair(int) const { return make_float2(w, 0.0f); }
+};
+
+template <typename E, int EC, int T>
+__global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, const E *X, const E *W, int64_t h,
+                                                            float2 *part) {
+    extern __shared__ __align__(16) uint8_t few_smem[];
+    E *xs = reinterpret_cast<E *>(few_smem);  // [T][h]
+    __shared__ float2 sh[FEW_THREADS / 32][T];
+    constexpr int N = FEW_ROWS * T, LOG = N == 4 ? 2 : (N == 8 ? 3 : (N == 16 ? 4 : 5)), PAIRS = EC == 1 ? 1 : EC / 2;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    for (int64_t i = static_cast<int64_t>(threadIdx.x) * EC; i < T * h; i += FEW_THREADS * EC) {
+        Chunk<E, EC> c;
+        if (i < a.tokens * h)
+            c.load(X + i);
+        else
+            c.zero();
+        *reinterpret_cast<Chunk<E, EC> *>(xs + i) = c;
+    }
+    __syncthreads();
+    // This warp's rows of W, a contiguous share.
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (FEW_THREADS / 32);
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * (FEW_THREADS / 32) + w;
+    const int64_t beg = a.vocab * id / warps, end = a.vocab * (id + 1) / warps;
+    // After the reduction below lane l holds sum number l >> (5 - LOG): row / T, token % T.
+    const int mine = lane >> (5 - LOG), my_row = mine / T, my_t = mine % T;
+    int64_t target = -1;
+    if (my_t < a.tokens) {
+        target = a.target[my_t];
+        if (target == a.ignore_index) target = -1;
+    }
+    float m = -INFINITY, s = 0.0f;
+    for (int64_t r0 = beg; r0 < end; r0 += FEW_ROWS) {
+        float2 acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        const E *rows = W + r0 * h;
+        const int n = static_cast<int>(min(static_cast<int64_t>(FEW_ROWS), end - r0));
+#pragma unroll 2
+        for (int64_t c = lane * EC; c < h; c += 32 * EC) {
+            Chunk<E, EC> b[FEW_ROWS];
+#pragma unroll
+            for (int i = 0; i < FEW_ROWS; ++i) {
+                if (i < n)
+                    b[i].stream(rows + i * h + c);
+                else
+                    b[i].zero();
+            }
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                Chunk<E, EC> x;
+                x.load(xs + t * h + c);
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float2 xv = x.pair(j);
+#pragma unroll
+                    for (int i = 0; i < FEW_ROWS; ++i)
+                        acc[i * T + t] = ptx::fma2(b[i].pair(j), xv, acc[i * T + t]);
+                }
+            }
+        }
+        // Every lane has a share of all N sums; each exchange halves how many sums a lane
+        // is concerned with.
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = acc[i].x + acc[i].y;
+#pragma unroll
+        for (int q = 0; q < 5; ++q) {
+            const int off = 16 >> q;
+            if (q < LOG) {
+                const int half = N >> (q + 1);
+#pragma unroll
+                for (int i = 0; i < half; ++i) {
+                    const float send = (lane & off) ? v[i] : v[i + half];
+                    const float keep = (lane & off) ? v[i + half] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+                }
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+            }
+        }
+        if (my_row < n) {
+            join(m, s, v[0], 1.0f);
+            if (target == r0 + my_row) a.target_logit[my_t] = v[0];
+        }
+    }
+    // the rows of one token sit in lanes that differ in bits 4 and 3
+#pragma unroll
+    for (int off = 16; off >= 8; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, off), s2 = __shfl_xor_sync(0xffffffffu, s, off);
+        join(m, s, m2, s2);
+    }
+    if (mine < T) sh[w][mine] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x < a.tokens) {
+        float2 p = sh[0][threadIdx.x];
+        for (int i = 1; i < FEW_THREADS / 32; ++i) join(p.x, p.y, sh[i][threadIdx.x].x, sh[i][threadIdx.x].y);
+        part[static_cast<int64_t>(blockIdx.x) * a.tokens + threadIdx.x] = p;
+    }
+}
+
+// The same for 2 to 8 bf16 tokens, where one FMA per weight and token would cost more than
+// W's bytes: warp products of 16 rows of W with 8 tokens.  A dot product does not
+// care in which order k comes, so each lane loads 16 contiguous bytes of two rows and
+// takes them as its share of two 16-deep products, with the tokens' values at the same
+// places; no shuffling, no staging of W.  The warps of a block share a group of 16
+// rows by slices of k and add their sums in order through shared memory, so that the
+// blocks' shares of the vocabulary stay even; two buffers let one barrier per group do.
+constexpr int SLIM_ROWS = 16;
+
+template <int SLIM_WARPS>
+__global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(const RowArgs a, const __nv_bfloat16 *X,
+                                                              const __nv_bfloat16 *W, int64_t h, int hp,
+                                                              float2 *part) {
+    extern __shared__ __align__(16) uint8_t slim_smem[];
+    // [8][hp], hp = h rounded up to 32, and 8 more: a row's 16-byte pieces then start 4
+    // banks after the row before, and the eight tokens that a load touches do not collide
+    __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(slim_smem);
+    __shared__ float4 sums[2][SLIM_WARPS][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, q = lane & 3, r = lane >> 2;
+    const int ld = hp + 8;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    for (int i = threadIdx.x * 8; i < 8 * hp; i += 256 * SLIM_WARPS) {
+        const int t = i / hp, c = i - t * hp;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (t < a.tokens && c < h) v = *reinterpret_cast<const uint4 *>(X + t * h + c);
+        *reinterpret_cast<uint4 *>(xs + t * ld + c) = v;
+    }
+    __syncthreads();
+    int64_t target[2];
+    float m[2], s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = 2 * q + j;
+        target[j] = -1;
+        if (t < a.tokens && a.target[t] != a.ignore_index) target[j] = a.target[t];
+        m[j] = -INFINITY, s[j] = 0.0f;
+    }
+    int it = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * SLIM_ROWS; r0 < a.vocab;
+         r0 += static_cast<int64_t>(gridDim.x) * SLIM_ROWS, ++it) {
+        const int rows = static_cast<int>(min(static_cast<int64_t>(SLIM_ROWS), a.vocab - r0));
+        const __nv_bfloat16 *row0 = W + (r0 + r) * h + 8 * q, *row1 = row0 + 8 * h;
+        const bool in0 = r < rows, in1 = r + 8 < rows;
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int c = 32 * w; c < hp; c += 32 * SLIM_WARPS) {
+            const bool in = c + 8 * q < h;
+            uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
+            if (in && in0) u = __ldcs(reinterpret_cast<const uint4 *>(row0 + c));
+            if (in && in1) v = __ldcs(reinterpret_cast<const uint4 *>(row1 + c));
+            const uint4 x = *reinterpret_cast<const uint4 *>(xs + r * ld + c + 8 * q);
+            ptx::mma_bf16_16x8x16(d, u.x, v.x, u.y, v.y, x.x, x.y);
+            ptx::mma_bf16_16x8x16(d, u.z, v.z, u.w, v.w, x.z, x.w);
+        }
+        const int buf = it & 1;
+        sums[buf][w][lane] = make_float4(d[0], d[1], d[2], d[3]);
+        __syncthreads();
+        if (it % SLIM_WARPS == w) {  // the warps take turns
+            float4 v = sums[buf][0][lane];
+            for (int k = 1; k < SLIM_WARPS; ++k) {
+                const float4 o = sums[buf][k][lane];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            const float z[4] = {v.x, v.y, v.z, v.w};  // (row r, tokens 2q, 2q + 1), (row r + 8, the same)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = r + 8 * (j >> 1);
+                if (row < rows) {
+                    join(m[j & 1], s[j & 1], z[j], 1.0f);
+                    if (target[j & 1] == r0 + row) a.target_logit[2 * q + (j & 1)] = z[j];
+                }
+            }
+        }
+    }
+    // One token's rows: 8 lanes of every warp.
+    float2 *all = reinterpret_cast<float2 *>(&sums[0][0][0]);  // [SLIM_WARPS][8]
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[j], off), s2 = __shfl_xor_sync(0xffffffffu, s[j], off);
+            join(m[j], s[j], m2, s2);
+        }
+        if (r == 0) all[w * 8 + 2 * q + j] = make_float2(m[j], s[j]);
+    }
+    __syncthreads();
+    if (threadIdx.x < a.tokens) {
+        float2 p = all[threadIdx.x];
+        for (int k = 1; k < SLIM_WARPS; ++k) join(p.x, p.y, all[k * 8 + threadIdx.x].x, all[k * 8 + threadIdx.x].y);
+        part[static_cast<int64_t>(blockIdx.x) * a.tokens + threadIdx.x] = p;
+    }
 }
 
 // Fixed-order sum of the fp32 matrices that split products left, rounded once to the
@@ -206,6 +442,69 @@ static int64_t blocks_for(int64_t n) {
 
 cudaError_t launch_xent_combine(const RowArgs &a, float *loss, float *lse, cudaStream_t st) {
     return launch_pdl(xent::combine_kernel, dim3(static_cast<unsigned>((a.tokens + 31) / 32)), 32 * xent::COMBINE_WARPS, 0, st, a, loss, lse);
+}
+
+// Shared memory of the kernel that takes these tokens: X, for as many tokens as it is built for.
+static int64_t few_smem(bool is_bf16, int64_t tokens, int64_t hidden) {
+    if (is_bf16) return tokens <= 1 ? hidden * 2 : 8 * ((hidden + 31) / 32 * 32 + 8) * 2;
+    return (tokens <= 2 ? tokens : (tokens <= 4 ? 4 : 8)) * hidden * 4;
+}
+
+bool xent_few(bool is_bf16, int64_t tokens, int64_t hidden) {
+    if (tokens > 8) return false;
+    return few_smem(is_bf16, tokens, hidden) <= XENT_FEW_SMEM;
+}
+
+int64_t xent_few_groups(int64_t vocab) {
+    const int64_t b = (vocab + 15) / 16;
+    return b < 304 ? b : 304;
+}
+
+template <int WARPS>
+static cudaError_t launch_slim(const RowArgs &a, const void *X, const void *W, int64_t h, int64_t smem, float2 *part,
+                               cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(xent::slim_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(XENT_FEW_SMEM));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(xent::slim_kernel<WARPS>, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), 32 * WARPS,
+                      static_cast<size_t>(smem), st, a, static_cast<const __nv_bfloat16 *>(X),
+                      static_cast<const __nv_bfloat16 *>(W), h, static_cast<int>((h + 31) / 32 * 32), part);
+}
+
+template <typename E, int EC, int T>
+static cudaError_t launch_few(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part, cudaStream_t st) {
+    auto kernel = xent::few_kernel<E, EC, T>;
+    const size_t smem = static_cast<size_t>(T) * h * sizeof(E);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(XENT_FEW_SMEM));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), xent::FEW_THREADS, smem, st, a,
+                      static_cast<const E *>(X), static_cast<const E *>(W), h, part);
+}
+
+template <typename E, int EC>
+static cudaError_t launch_few_t(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
+                                cudaStream_t st) {
+    if (a.tokens <= 1) return launch_few<E, EC, 1>(a, X, W, h, part, st);
+    if (a.tokens <= 2) return launch_few<E, EC, 2>(a, X, W, h, part, st);
+    if (a.tokens <= 4) return launch_few<E, EC, 4>(a, X, W, h, part, st);
+    return launch_few<E, EC, 8>(a, X, W, h, part, st);
+}
+
+cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
+                            cudaStream_t st) {
+    if (is_bf16) {
+        if (a.tokens <= 1) return launch_few<__nv_bfloat16, 8, 1>(a, X, W, h, part, st);
+        // 16 warps per SM: two blocks, of which one computes while the other is at its barrier,
+        // where two copies of X leave room for the loads in L1; one block of all 16 warps where
+        // they do not (T = 4, V = 50000: h = 6144 4.4 TB/s with two blocks, h = 8192 5.8 with one).
+        const int64_t smem = few_smem(true, a.tokens, h);
+        return smem <= 72 * 1024 ? launch_slim<8>(a, X, W, h, smem, part, st)
+                                  : launch_slim<16>(a, X, W, h, smem, part, st);
+    }
+    const uintptr_t both = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W);
+    if (h % 4 == 0 && (both & 15) == 0) return launch_few_t<float, 4>(a, X, W, h, part, st);
+    return launch_few_t<float, 1>(a, X, W, h, part, st);
 }
 
 cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st) {

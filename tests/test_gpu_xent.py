@@ -94,6 +94,8 @@ def run(tp, X, W, y, dl, **kw):
 SHAPES = [  # T, h, V: one token, ragged tiles in every dimension, vocabulary of one row, long rows
     (1, 8, 1), (1, 64, 17), (3, 72, 513), (31, 128, 255), (128, 256, 512), (129, 264, 1025), (256, 512, 4096),
     (300, 200, 3001), (257, 1000, 777), (1000, 96, 2049), (5, 4096, 8191), (2, 8192, 130),
+    (1, 24, 5000), (2, 1000, 333), (4, 264, 20000), (7, 40, 61), (8, 8192, 700), (8, 64, 3), (9, 200, 999), (16, 4096, 300),
+    (20, 104, 5003), (32, 1024, 77), (32, 24, 6000), (33, 64, 500),  # a pass over W
     (40, 64, 30011), (6000, 72, 100),  # K of dX and of dW long, few tiles: split
 ]
 
@@ -106,7 +108,8 @@ def test_bf16_against_64_bits(tp, T, h, V):
 
 
 @pytest.mark.parametrize("T,h,V", [(1, 1, 1), (3, 5, 7), (64, 33, 1000), (130, 256, 777), (300, 770, 2500),
-                                   (17, 40, 20011), (5000, 36, 90), (4100, 9, 33)])
+                                   (17, 40, 20011), (5000, 36, 90), (4100, 9, 33),
+                                   (1, 4100, 700), (5, 130, 3000), (8, 8192, 50)])
 def test_f32_against_64_bits(tp, T, h, V):
     X, W, y, dl = make(T, h, V, torch.float32, seed=T + h + V, ignored=0.2)
     ctx, loss, grads = run(tp, X, W, y, dl)
