@@ -1552,7 +1552,7 @@ struct OrthoLayout {
     int splits;  // chain: K ranges of the Gram product, and their length
     int64_t split_len;
     float q_scale;
-    size_t norm, hi[2], lo[2], A, C, total;
+    size_t norm, hi[2], lo[2], rest, A, C, total;
 };
 
 // Workspace, 1 KB-aligned regions: status | block sums of the norm | X's high and low parts
@@ -1563,10 +1563,10 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
     L.P = (s->rows + 63) / 64 * 64, L.Q = (s->cols + 63) / 64 * 64;
     L.wide = s->rows <= s->cols;
     L.p = L.wide ? L.P : L.Q;
-    // The chain wants Q in fp16's range with room for its low part.
+    // The chain wants Q (times a factor of up to 2) in fp16's range.
     double q_bound = 0.0;
     L.chain = L.p <= tpmlp::NS_CHAIN_P && ortho_range_ok(s, q_bound) && q_bound < 32768.0;
-    L.q_scale = L.chain ? static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(q_bound, 1.0))))) : 1.0f;
+    L.q_scale = L.chain ? static_cast<float>(std::exp2(std::floor(std::log2(30000.0 / std::max(q_bound, 1.0))))) : 1.0f;
     size_t off = STATUS_BYTES;
     auto region = [&](size_t bytes) {
         const size_t at = off;
@@ -1582,8 +1582,10 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
         const int64_t want = std::min<int64_t>(152 / std::max<int64_t>(1, s->batch), (K + 255) / 256);
         L.split_len = (K / std::max<int64_t>(1, want) + 63) / 64 * 64;
         L.splits = static_cast<int>((K + L.split_len - 1) / L.split_len);
-        L.hi[0] = region(2 * x);
-        L.lo[0] = L.hi[0] + x;
+        const bool f32 = s->dtype == TPMLP_F32;  // bf16 values need no low part (see OrthoStart::rest)
+        L.hi[0] = region(f32 ? 2 * x : x);
+        L.lo[0] = f32 ? L.hi[0] + x : 0;
+        L.rest = region(n * 4);
         L.hi[1] = region(s->cols % 8 ? x : 0);
         L.lo[1] = 0;
         L.A = region(2 * a * static_cast<size_t>(L.splits));
@@ -1639,12 +1641,20 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
     a.part = ws + L.norm;
     a.hi = ws + L.hi[0], a.lo = ws + L.lo[0];
     a.lo_scale = L.chain ? 1.0f : 2048.0f;
-    cudaError_t e;
-    {
-        Timed timed("ortho_start", st);
-        e = tpmlp::launch_ortho_start(s->dtype == TPMLP_BF16, a, st);
-        if (e == cudaSuccess) g_launches.fetch_add(2);
-    }
+    a.rest = nullptr;
+    const bool single = L.chain && s->dtype == TPMLP_BF16;
+    if (L.chain) a.rest = reinterpret_cast<float *>(ws + L.rest);
+    if (single) a.lo = nullptr;
+    auto timed_launch = [&](const char *name, auto f) {
+        Timed timed(name, st);
+        const cudaError_t r = f();
+        if (r == cudaSuccess) g_launches.fetch_add(1);
+        return r;
+    };
+    const bool bf16 = s->dtype == TPMLP_BF16;
+    cudaError_t e = timed_launch("ortho_norm", [&] { return tpmlp::launch_ortho_norm(bf16, a, st); });
+    if (e != cudaSuccess) return from_cuda(e);
+    e = timed_launch("ortho_scale", [&] { return tpmlp::launch_ortho_scale(bf16, a, st); });
     if (e != cudaSuccess) return from_cuda(e);
 
     auto product = [&](const void *x, bool x_mn, const void *y, bool y_mn, int64_t M,
@@ -1666,41 +1676,35 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         const bool sym = epi == tpmlp::EPI_NS_GRAM || epi == tpmlp::EPI_NS_POLY;
         g.cta_pair = (sym ? mt * (mt + 1) / 2 : mt * nt) * s->batch > 400;
         pick_raster(g, epi);
-        Timed timed(name, st);
-        const cudaError_t r = tpmlp::launch_tc_gemm(epi, g, sms, st);
-        if (r == cudaSuccess) g_launches.fetch_add(1);
-        return r;
+        return timed_launch(name, [&] { return tpmlp::launch_tc_gemm(epi, g, sms, st); });
     };
     if (L.chain) {
         GemmArgs g = product(ws + L.hi[0], !L.wide, ws + L.hi[0], !L.wide, L.p, L.p, L.wide ? L.Q : L.P, ws + L.A);
         g.ksplit = L.splits, g.kshard = L.split_len;
+        g.x_single = single;
         e = launch("ortho_gram32", tpmlp::EPI_NS_GRAM32, g);
         if (e != cudaSuccess) return from_cuda(e);
         tpmlp::NsChain c;
         c.matrices = s->batch, c.P = L.p;
         c.size = static_cast<int>(std::min(s->rows, s->cols) + 15) / 16 * 16;
         c.gram = reinterpret_cast<const float *>(ws + L.A), c.splits = L.splits;
-        c.unit = 1.0f / (kScaleX * kScaleX);
+        c.unit = 1.0f / (kScaleX * kScaleX), c.rest = a.rest;
         c.steps = s->steps, c.a = s->a, c.b = s->b, c.c = s->c, c.q_scale = L.q_scale;
         c.Q = ws + L.C;
         c.status = status, c.wait_ns = g_wait_ns.load();
-        {
-            Timed timed("ortho_chain", st);
-            e = tpmlp::launch_ns_chain(c, st);
-            if (e == cudaSuccess) g_launches.fetch_add(1);
-        }
+        e = timed_launch("ortho_chain", [&] { return tpmlp::launch_ns_chain(c, st); });
         if (e != cudaSuccess) return from_cuda(e);
         void *out = tma_out ? O : ws + L.hi[1];
         GemmArgs u = L.wide ? product(c.Q, false, ws + L.hi[0], true, L.P, L.Q, L.p, out)
                             : product(ws + L.hi[0], false, c.Q, false, L.P, L.Q, L.p, out);
         u.scale = 1.0f / (kScaleX * L.q_scale);
+        u.x_single = single;
         u.out_rows = tma_out ? s->rows : L.P, u.out_cols = tma_out ? s->cols : L.Q;
         e = launch("ortho_final", tpmlp::EPI_NS_FINAL, u);
-        if (e == cudaSuccess && !tma_out) {
-            Timed timed("ortho_unpad", st);
-            e = tpmlp::launch_ortho_unpad(out, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
-            if (e == cudaSuccess) g_launches.fetch_add(1);
-        }
+        if (e == cudaSuccess && !tma_out)
+            e = timed_launch("ortho_unpad", [&] {
+                return tpmlp::launch_ortho_unpad(out, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
+            });
         return from_cuda(e);
     }
 
@@ -1738,11 +1742,10 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         u.out_rows = tma_out ? s->rows : L.P, u.out_cols = tma_out ? s->cols : L.Q;
         e = launch(last ? "ortho_last" : "ortho_update", epi, u);
         if (e != cudaSuccess) return from_cuda(e);
-        if (last && !tma_out) {
-            Timed timed("ortho_unpad", st);
-            e = tpmlp::launch_ortho_unpad(hi2, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
-            if (e == cudaSuccess) g_launches.fetch_add(1);
-        }
+        if (last && !tma_out)
+            e = timed_launch("ortho_unpad", [&] {
+                return tpmlp::launch_ortho_unpad(hi2, s->batch, s->rows, s->cols, L.P, L.Q, O, st);
+            });
     }
     return from_cuda(e);
 }

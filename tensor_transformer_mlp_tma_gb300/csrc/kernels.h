@@ -108,6 +108,8 @@ struct GemmArgs {
     // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
     // two parts of X through aux (high) and aux2 (low).  out0 / out1: X' high, low.
     // LAST writes an [batch][out_rows][out_cols] array, the rest of the tile is dropped.
+    // GRAM32 and FINAL: X as two parts, or with x_single the high one alone.
+    bool x_single;
     const void *aux2;
     float alpha, beta, diag;
     int64_t out_rows, out_cols;
@@ -213,9 +215,12 @@ struct OrthoStart {
     void *part;     // ortho_norm_blocks(batch, rows * cols) * batch * 12 bytes
     void *hi, *lo;  // fp16 [batch][P][Q]
     float lo_scale; // lo holds the remainder times this
+    float *rest;    // null: X scaled by the whole factor; else by the power of two below it, and the rest here
 };
 int64_t ortho_norm_blocks(int64_t batch, int64_t n);
-cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t st);
+// The block sums of the norms, then the scaled parts.
+cudaError_t launch_ortho_norm(bool is_bf16, const OrthoStart &a, cudaStream_t st);
+cudaError_t launch_ortho_scale(bool is_bf16, const OrthoStart &a, cudaStream_t st);
 // The steps on p x p Gram matrices, p <= 128 (ns_chain.cu).
 constexpr int NS_CHAIN_P = 128;
 struct NsChain {
@@ -223,7 +228,8 @@ struct NsChain {
     int size;             // rows and columns in use, a multiple of 16
     const float *gram;    // [splits][matrices][P][P]
     int splits;
-    float unit;           // A_0 = unit * the sum of the splits
+    float unit;           // A_0 = unit * rest^2 * the sum of the splits
+    const float *rest;    // [matrices]; Q is multiplied by it
     int steps;
     float a, b, c, q_scale;
     void *Q;              // fp16 [2][matrices][P][P]: high and low part of q_scale * Q

@@ -30,10 +30,14 @@ namespace chain {
 
 constexpr int PT = NS_CHAIN_P;           // rows and columns of the tile, 128
 constexpr int THREADS = 512;             // warp w: TMEM lanes 32 (w % 4).., columns 32 (w / 4)..
-constexpr uint32_t PART = PT * PT * 2;   // one fp16 matrix: two blocks of 64 columns, 128-byte swizzled
-constexpr uint32_t MAT = 2 * PART;       // high and low part
+// A matrix: two blocks of 64 columns, each 128 rows of the high part and then 128 rows of
+// the low part, 128-byte swizzled.  As the second operand of a product the 256 rows of a
+// block give hi and lo in one MMA.
+constexpr uint32_t PART = PT * 128;      // from the high to the low part
+constexpr uint32_t BLOCK = 2 * PART;     // from one block to the next
+constexpr uint32_t MAT = 2 * BLOCK;
 constexpr size_t SMEM = 3 * MAT + 1024;  // A, B, Q, and alignment
-constexpr uint32_t TMEM_COLS = 512;      // three accumulators of 128 columns
+constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 2 x 128 columns
 constexpr uint32_t STATUS_TIMEOUT = 4;   // TPMLP_ERR_TIMEOUT
 
 // The scales that A and B are stored with (powers of two; see kScaleX in api.cu for why).
@@ -42,7 +46,7 @@ constexpr float SA = 8192.0f, SB = 8192.0f;
 // 32 values of one row, columns col .. col + 31, split into the two parts of the matrix at
 // `mat`: 16-byte chunk j of a 128-byte row r sits at chunk j ^ (r & 7).
 __device__ __forceinline__ void put(uint32_t mat, int row, int col, const float (&v)[32]) {
-    const uint32_t base = mat + static_cast<uint32_t>(col >> 6) * (PART / 2) + static_cast<uint32_t>(row) * 128u;
+    const uint32_t base = mat + static_cast<uint32_t>(col >> 6) * BLOCK + static_cast<uint32_t>(row) * 128u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t h[4], l[4];
@@ -59,18 +63,22 @@ __device__ __forceinline__ void put(uint32_t mat, int row, int col, const float 
     }
 }
 
-// D = X Y^T for two matrices in shared memory of n columns each (n a multiple of 16),
-// issued by one thread.
-__device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y, int n, uint32_t idesc) {
-    uint32_t acc = 0;
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {  // the small products first
-        const uint32_t px = x + (s == 1 ? PART : 0), py = y + (s == 0 ? PART : 0);
-        for (int k = 0; k < n / 16; ++k) {
-            const uint32_t off = static_cast<uint32_t>(k >> 2) * (PART / 2) + static_cast<uint32_t>(k & 3) * 32u;
-            ptx::umma_f16_ss(d, ptx::sdesc_sw128(px + off, 16, 1024), ptx::sdesc_sw128(py + off, 16, 1024), idesc, acc);
-            acc = 1;
-        }
+// X Y^T for two matrices in shared memory of n columns each (n a multiple of 16), issued by one
+// thread: D[0, 128) = X_hi Y_hi^T and D[128, 256) = X_hi Y_lo^T by MMAs of 256 columns, then
+// D[128, 256) += X_lo Y_hi^T.  Their sum is the product.  (Three MMAs of 128 columns in the
+// place of one of 256 and one of 128 read the operands from shared memory more often
+// than the tensor core can take them: 12% of the kernel's time.)
+__device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y, int n) {
+    constexpr uint32_t WIDE = ptx::idesc_f16_f32(PT, 2 * PT, false, false);
+    const uint32_t narrow = ptx::idesc_f16_f32(PT, n, false, false);
+    for (int k = 0; k < n / 16; ++k) {
+        const uint32_t off = static_cast<uint32_t>(k >> 2) * BLOCK + static_cast<uint32_t>(k & 3) * 32u;
+        ptx::umma_f16_ss(d, ptx::sdesc_sw128(x + off, 16, 1024), ptx::sdesc_sw128(y + off, 16, 1024), WIDE, k > 0);
+    }
+    for (int k = 0; k < n / 16; ++k) {
+        const uint32_t off = static_cast<uint32_t>(k >> 2) * BLOCK + static_cast<uint32_t>(k & 3) * 32u;
+        ptx::umma_f16_ss(d + PT, ptx::sdesc_sw128(x + PART + off, 16, 1024), ptx::sdesc_sw128(y + off, 16, 1024), narrow,
+                         1u);
     }
 }
 
@@ -85,7 +93,6 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     const int row = 32 * (warp & 3) + lane, col0 = 32 * (warp >> 2);
     const int n = c.size;
     const bool mine_in = col0 < n;  // warps whose columns are all padding only keep step
-    const uint32_t idesc = ptx::idesc_f16_f32(PT, n, false, false);
     const uint32_t bar[2] = {ptx::smem_u32(&bars[0]), ptx::smem_u32(&bars[1])};
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar[0], 1);
@@ -112,13 +119,14 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     float A[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) A[i] = 0.0f;
-    if (row < P && col0 < P) {
+    const float rest = c.rest ? c.rest[z] : 1.0f;
+    if (row < n && col0 < n) {
         const float *src = c.gram + z * P * P + col0 * P + row;
         for (int s = 0; s < c.splits; ++s, src += c.matrices * P * P)
 #pragma unroll
             for (int i = 0; i < 32; ++i) A[i] += src[i * P];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) A[i] *= c.unit;
+        for (int i = 0; i < 32; ++i) A[i] = col0 + i < n ? A[i] * (c.unit * rest * rest) : 0.0f;
     }
 
     // Each product belongs to one of two barriers; `start` runs once every thread's
@@ -143,11 +151,13 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
         ptx::tc_fence_after();
     };
     auto load = [&](int acc, float (&v)[32]) {
-        uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * PT), r);
+        uint32_t r[32], l[32];
+        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * 2 * PT), r);
+        ptx::tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(acc * 2 * PT + PT), l);
         ptx::tmem_ld_wait(r);
+        ptx::tmem_ld_wait(l);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(l[i]);
     };
     float v[32];
     auto put_A = [&]() {
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     for (int k = 0; k < c.steps; ++k) {
         const bool last = k == c.steps - 1;
         start([&] {
-            multiply(tmem, mA, mA, n, idesc);
+            multiply(tmem, mA, mA, n);
             ptx::umma_commit(bar[0]);
         });
         wait(0);
@@ -176,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
             put(mB, row, col0, v);
             if (k == 0) {  // Q^T = B_0
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= c.q_scale / SB;
+                for (int i = 0; i < 32; ++i) v[i] *= c.q_scale * rest / SB;
                 put(mQ, row, col0, v);
             }
         }
@@ -184,31 +194,31 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
         // B A first: the chain goes on with it, while Q^T B = (B Q)^T has time until the step's end.
         start([&] {
             if (!last) {
-                multiply(tmem + PT, mB, mA, n, idesc);
+                multiply(tmem, mB, mA, n);
                 ptx::umma_commit(bar[0]);
             }
             if (k > 0) {
-                multiply(tmem + 2 * PT, mQ, mB, n, idesc);
+                multiply(tmem + 2 * PT, mQ, mB, n);
                 ptx::umma_commit(bar[1]);
             }
         });
         if (!last) {
             wait(0);
             if (mine_in) {  // B A takes A's place
-                load(1, v);
+                load(0, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
                 put(mA, row, col0, v);
             }
             start([&] {
-                multiply(tmem, mB, mA, n, idesc);  // B (B A)^T = B A B
+                multiply(tmem, mB, mA, n);  // B (B A)^T = B A B
                 ptx::umma_commit(bar[0]);
             });
         }
         if (k > 0) {
             wait(1);
             if (mine_in) {
-                load(2, v);
+                load(1, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
                 put(mQ, row, col0, v);
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
             for (int j = 0; j < 4; ++j) {
                 uint32_t w[4] = {0u, 0u, 0u, 0u};
                 if (mine_in && row < n)
-                    ptx::ld_shared_v4(mQ + part * PART + static_cast<uint32_t>(col0 >> 6) * (PART / 2) +
+                    ptx::ld_shared_v4(mQ + part * PART + static_cast<uint32_t>(col0 >> 6) * BLOCK +
                                           static_cast<uint32_t>(row) * 128u +
                                           (static_cast<uint32_t>((((col0 & 63) >> 3) + j) ^ (row & 7)) << 4),
                                       w[0], w[1], w[2], w[3]);

@@ -24,16 +24,23 @@ struct Blue {
 };
 constexpr float kBig = 0x1p48f, kSmall = 0x1p-48f;      // limits of the ordinary values
 constexpr float kBigScale = 0x1p-72f, kSmallScale = 0x1p72f;
-__device__ __forceinline__ void add(Blue &b, float x) {
-    const float ax = fabsf(x);
-    if (ax > kBig) {  // also +-inf
-        const float y = x * kBigScale;
-        b.big = fmaf(y, y, b.big);
-    } else if (ax < kSmall) {
-        const float y = x * kSmallScale;
-        b.small = fmaf(y, y, b.small);
-    } else {  // also NaN
-        b.mid = fmaf(x, x, b.mid);
+// N values at once, all into the sum that the largest of them belongs to: beside a value of
+// 2^-48 or more, what underflows (below 2^-74) is too small to count.
+template <int N>
+__device__ __forceinline__ void add(Blue &b, const float (&x)[N]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(x[j]));
+    if (m <= kBig && m >= kSmall) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) b.mid = fmaf(x[j], x[j], b.mid);
+    } else {
+        const bool big = m > kBig;  // also +-inf; a NaN beside small values goes with them
+        const float f = big ? kBigScale : kSmallScale;
+        float s = big ? b.big : b.small;
+#pragma unroll
+        for (int j = 0; j < N; ++j) s = fmaf(x[j] * f, x[j] * f, s);
+        (big ? b.big : b.small) = s;
     }
 }
 
@@ -64,12 +71,17 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, in
         for (int64_t i = beg + threadIdx.x * E; i < end; i += THREADS * E) {
             const uint4 w = __ldg(reinterpret_cast<const uint4 *>(g + i));
             const T *v = reinterpret_cast<const T *>(&w);
+            float x[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) add(b, value<T>(v[j]));
+            for (int j = 0; j < E; ++j) x[j] = value<T>(v[j]);
+            add(b, x);
         }
     } else {
 #pragma unroll 4
-        for (int64_t i = beg + threadIdx.x; i < end; i += THREADS) add(b, value<T>(g[i]));
+        for (int64_t i = beg + threadIdx.x; i < end; i += THREADS) {
+            const float x[1] = {value<T>(g[i])};
+            add(b, x);
+        }
     }
     __shared__ Blue sh[THREADS / 32];
 #pragma unroll
@@ -86,11 +98,21 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, in
     }
 }
 
+// 2^e as a double, e within its normal range.
+__device__ __forceinline__ double pow2(int e) { return __longlong_as_double(static_cast<long long>(1023 + e) << 52); }
+__device__ __forceinline__ int exponent(double x) {
+    return static_cast<int>((__double_as_longlong(x) >> 52) & 2047) - 1023;
+}
+
 // scale / (|G| + eps) of one matrix from its block sums, in the same order in every
-// block that asks.  The three sums meet in 64 bits, where none of them can overflow.
-__device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps, float scale) {
+// block that asks.  The three sums meet in 64 bits, where none of them can overflow; root
+// and quotient are taken of the fp32 significands (64-bit ones would take longer than a
+// block's share of the matrix) and their exponents apart.
+// With `power` the result is the power of two below it, and `rest` (1 to 2) is what is left.
+template <bool POW2>
+__device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps, float scale, float &rest) {
     __shared__ double sh[THREADS / 32];
-    __shared__ float result;
+    __shared__ float result, left;
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += THREADS) {
         const Blue b = part[i];
@@ -102,24 +124,46 @@ __device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < THREADS / 32; ++w) s += sh[w];
-        // beyond the fp32 range (|G| < 2^-113 with eps = 0) the factor saturates
-        result = static_cast<float>(fmin(static_cast<double>(scale) / (sqrt(s) + static_cast<double>(eps)), 0x1p127));
-        if (s != s) result = nanf("");
+        double norm = s;  // 0, inf and NaN stay what they are
+        if (s > 0.0 && s < 0x1p1000) {
+            const int e = exponent(s) & ~1;
+            norm = static_cast<double>(sqrtf(static_cast<float>(s * pow2(-e)))) * pow2(e / 2);
+        }
+        norm += static_cast<double>(eps);
+        if (norm > 0.0 && norm < 0x1p1000) {
+            const int e = exponent(norm);
+            // beyond the fp32 range (|G| < 2^-113 with eps = 0) the factor saturates
+            result = static_cast<float>(static_cast<double>(scale / static_cast<float>(norm * pow2(-e))) *
+                                        pow2(min(-e, 113)));
+        } else {
+            result = norm > 0.0 ? 0.0f : (norm == 0.0 ? 0x1p127f : nanf(""));
+        }
+        left = 1.0f;
+        if (POW2 && result > 0x1p-126f && result <= 0x1p127f) {
+            const float p = __uint_as_float(__float_as_uint(result) & 0x7F800000u);
+            left = result / p;
+            result = p;
+        }
     }
     __syncthreads();
+    rest = left;
     return result;
 }
 
-// hi and lo of 8 consecutive columns per thread; grid.x covers P * Q / 8, grid.y the
-// matrices.  Memory bound: G read once more, 4 bytes written per element.
-template <typename T, bool VEC>
+// hi and lo of 8 consecutive columns per thread; grid.y is the matrix.  Memory bound: G read
+// once more, 4 bytes written per element, or 2: with POW2 (lo may then be null) X is scaled by the
+// power of two below the factor, which leaves bf16 values exact in fp16 and their
+// low part zero, and the rest of the factor goes to rest[matrix].
+template <typename T, bool VEC, bool POW2>
 __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                                         const Blue *part, int nparts, float eps, float scale,
-                                                        __half *hi, __half *lo, float lo_scale) {
+                                                        __half *hi, __half *lo, float lo_scale, float *rest) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t z = blockIdx.y;
-    const float f = inverse_norm(part + z * nparts, nparts, eps, scale);
+    float left;
+    const float f = inverse_norm<POW2>(part + z * nparts, nparts, eps, scale, left);
+    if (POW2 && blockIdx.x == 0 && threadIdx.x == 0) rest[z] = left;
     const T *g = G + z * rows * cols;
     // UN loads in flight per thread before the first is used
     constexpr int UN = 4;
@@ -158,7 +202,7 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
             }
             const int64_t o = z * P * Q + static_cast<int64_t>(i) * 8;
             *reinterpret_cast<uint4 *>(hi + o) = *reinterpret_cast<const uint4 *>(h);
-            *reinterpret_cast<uint4 *>(lo + o) = *reinterpret_cast<const uint4 *>(l);
+            if (!POW2 || lo) *reinterpret_cast<uint4 *>(lo + o) = *reinterpret_cast<const uint4 *>(l);
         }
     }
 }
@@ -169,13 +213,21 @@ __global__ void __launch_bounds__(THREADS) unpad_kernel(const __nv_bfloat16 *in,
                                                         int64_t Q, __nv_bfloat16 *out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    // a warp per row: its loads and stores of consecutive columns coalesce
-    const int64_t z = blockIdx.y, warps = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+    // a warp per 128 columns of a row: consecutive columns coalesce, four loads at once
+    const int64_t z = blockIdx.y;
+    const uint32_t segs = static_cast<uint32_t>((cols + 127) / 128), total = static_cast<uint32_t>(rows) * segs;
+    const int lane = threadIdx.x & 31;
+    for (uint32_t i = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); i < total; i += gridDim.x * (THREADS / 32)) {
+        const int64_t r = i / segs, c0 = static_cast<int64_t>(i - static_cast<uint32_t>(r) * segs) * 128 + lane;
         const __nv_bfloat16 *src = in + (z * P + r) * Q;
         __nv_bfloat16 *dst = out + (z * rows + r) * cols;
-#pragma unroll 4
-        for (int64_t c = threadIdx.x & 31; c < cols; c += 32) dst[c] = src[c];
+        __nv_bfloat16 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + 32 * j < cols) v[j] = src[c0 + 32 * j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + 32 * j < cols) dst[c0 + 32 * j] = v[j];
     }
 }
 
@@ -186,7 +238,7 @@ static unsigned grid_x(int64_t work, int64_t batch) {
 }
 
 template <typename T>
-static cudaError_t launch_start(const OrthoStart &a, cudaStream_t st) {
+static cudaError_t launch_start(const OrthoStart &a, bool norm, cudaStream_t st) {
     const int64_t n = a.rows * a.cols;
     const T *G = static_cast<const T *>(a.G);
     const bool aligned = (reinterpret_cast<uintptr_t>(G) & 15) == 0;
@@ -196,12 +248,14 @@ static cudaError_t launch_start(const OrthoStart &a, cudaStream_t st) {
     const int64_t per = ((n + nb - 1) / nb + 15) / 16 * 16;
     const dim3 gn(static_cast<unsigned>(nb), static_cast<unsigned>(a.batch));
     Blue *part = static_cast<Blue *>(a.part);
-    cudaError_t e = launch_pdl(vec_all ? norm_kernel<T, true> : norm_kernel<T, false>, gn, THREADS, 0, st, G, n, per, part);
-    if (e != cudaSuccess) return e;
+    if (norm)
+        return launch_pdl(vec_all ? norm_kernel<T, true> : norm_kernel<T, false>, gn, THREADS, 0, st, G, n, per, part);
     const dim3 gs(grid_x(a.P * a.Q / 32, a.batch), static_cast<unsigned>(a.batch));
     __half *hi = static_cast<__half *>(a.hi), *lo = static_cast<__half *>(a.lo);
-    return launch_pdl(vec_rows ? scale_kernel<T, true> : scale_kernel<T, false>, gs, THREADS, 0, st, G, a.rows, a.cols,
-                      a.P, a.Q, part, static_cast<int>(nb), a.eps, a.scale, hi, lo, a.lo_scale);
+    auto kernel = a.rest ? (vec_rows ? scale_kernel<T, true, true> : scale_kernel<T, false, true>)
+                         : (vec_rows ? scale_kernel<T, true, false> : scale_kernel<T, false, false>);
+    return launch_pdl(kernel, gs, THREADS, 0, st, G, a.rows, a.cols, a.P, a.Q, part, static_cast<int>(nb), a.eps,
+                      a.scale, hi, lo, a.lo_scale, a.rest);
 }
 
 }  // namespace ortho
@@ -211,13 +265,16 @@ int64_t ortho_norm_blocks(int64_t batch, int64_t n) {
     return want < most ? want : most;
 }
 
-cudaError_t launch_ortho_start(bool is_bf16, const OrthoStart &a, cudaStream_t st) {
-    return is_bf16 ? ortho::launch_start<__nv_bfloat16>(a, st) : ortho::launch_start<float>(a, st);
+cudaError_t launch_ortho_norm(bool is_bf16, const OrthoStart &a, cudaStream_t st) {
+    return is_bf16 ? ortho::launch_start<__nv_bfloat16>(a, true, st) : ortho::launch_start<float>(a, true, st);
+}
+cudaError_t launch_ortho_scale(bool is_bf16, const OrthoStart &a, cudaStream_t st) {
+    return is_bf16 ? ortho::launch_start<__nv_bfloat16>(a, false, st) : ortho::launch_start<float>(a, false, st);
 }
 
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                void *out, cudaStream_t st) {
-    const dim3 g(ortho::grid_x(rows * 32, batch), static_cast<unsigned>(batch));
+    const dim3 g(ortho::grid_x(rows * ((cols + 127) / 128) * 32, batch), static_cast<unsigned>(batch));
     return launch_pdl(ortho::unpad_kernel, g, ortho::THREADS, 0, st, static_cast<const __nv_bfloat16 *>(in), rows, cols,
                       P, Q, static_cast<__nv_bfloat16 *>(out));
 }

@@ -179,6 +179,8 @@ struct Params {
     // the stage's bytes for them.
     int tile_n;
     uint32_t idesc, stage_bytes;
+    uint32_t seg_codes;  // EPI_NS_FINAL: the products of a k-block, two bits each (see k_coord)
+    int x_single;        // EPI_NS_GRAM32: X is its high part alone
     int matrices;  // EPI_NS_GRAM32, EPI_NS_FINAL: problem z is matrix z % matrices, K range z / matrices
     // Newton-Schulz products (EPI_NS_*), see GemmArgs; out_M x out_N is what LAST stores.
     const void *aux2;
@@ -226,10 +228,10 @@ __device__ __forceinline__ KCoord k_coord(const Params &p, int kb, int z) {
             const int split = z / p.matrices, m = z - split * p.matrices;
             return {(kb + split * p.kb_seg) * BK, m, m + p.matrices};
         }
-        // (high, low), (low, high), (high, high); the low parts follow the high ones
-        const int seg = kb / p.kb_seg, split = z / p.matrices, m = z - split * p.matrices;
-        return {(kb - seg * p.kb_seg + split * p.kb_seg) * BK, m + (seg == 1 ? p.matrices : 0),
-                m + (seg == 0 ? p.matrices : 0)};
+        // products 0 (high, low), 1 (low, high), 2 (high, high); the low parts follow the high ones
+        const int seg = kb / p.kb_seg;
+        const uint32_t code = (p.seg_codes >> (2 * seg)) & 3u;
+        return {(kb - seg * p.kb_seg) * BK, z + (code == 1 ? p.matrices : 0), z + (code == 0 ? p.matrices : 0)};
     } else {
         return {kb * BK, z, z};
     }
@@ -1310,7 +1312,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     // copies only complete bytes on the leader's barrier (they can land
                     // before the announcement: the phase still needs the arrival).
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(full_local, CG * (ANY_N ? p.stage_bytes : C::STAGE_BYTES));
+                        ptx::mbar_arrive_expect_tx(
+                            full_local, CG * (ANY_N || EPI == EPI_NS_GRAM32 ? p.stage_bytes : C::STAGE_BYTES));
                     if constexpr (HEADS) {
                         // per-head operands addressed in place (rank-3/4/5 maps)
                         int a2, a3, a4, b2, b3, b4;
@@ -1341,7 +1344,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK_BYTES, &tmA, m0 + 64 * j, k0, za);
                     }
-                    if constexpr (!B_MN) {
+                    if (EPI == EPI_NS_GRAM32 && p.x_single) {
+                        // the one part is both operands
+                    } else if constexpr (!B_MN) {
                         load(sb, &tmB, k0, n0, zw);
                     } else if (p.b_mn4) {
                         load4(sb, &tmB, k0, n0 / 64, zw);
@@ -1543,9 +1548,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 } else if constexpr (EPI == EPI_NS_GRAM32) {
                                     // hi lo^T + lo hi^T + hi hi^T (both tiles are 128 x 64 in the
                                     // same layout, the high part in A's place)
-                                    ptx::umma_f16_ss(d_tmem, ad, bd, IDESC, acc);
-                                    ptx::umma_f16_ss(d_tmem, bd, ad, IDESC, 1u);
-                                    ptx::umma_f16_ss(d_tmem, ad, ad, IDESC, 1u);
+                                    if (p.x_single) {
+                                        ptx::umma_f16_ss(d_tmem, ad, ad, IDESC, acc);
+                                    } else {
+                                        ptx::umma_f16_ss(d_tmem, ad, bd, IDESC, acc);
+                                        ptx::umma_f16_ss(d_tmem, bd, ad, IDESC, 1u);
+                                        ptx::umma_f16_ss(d_tmem, ad, ad, IDESC, 1u);
+                                    }
                                 } else if constexpr (PAIR)
                                     ptx::umma_f16_ss_pair(d_tmem, ad, bd, IDESC, acc);
                                 else
@@ -2026,6 +2035,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     const int any_n = EPI == EPI_XENT_FOLD ? (g.tile_n > 0 ? g.tile_n : TILE_N) : 0;
     const int64_t splits = g.ksplit > 1 ? g.ksplit : 1;
     const int64_t ni = SEG ? (g.parts > 1 ? g.parts : 1) : (is_ns2(EPI) ? 2 * nb : nb);  // matrices per operand
+    // X's operand of the products in two parts may have its high part alone
+    const bool x_is_a = EPI == EPI_NS_GRAM32 || !B_MN;
+    const int64_t nia = g.x_single && x_is_a ? nb : ni;
+    const int64_t nib = g.x_single && (EPI == EPI_NS_GRAM32 || !x_is_a) ? nb : ni;
     const int64_t no = EPI == EPI_XENT_GRAD3 ? 3 : (SEG ? splits : nb * splits);         // and of the output
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;  // the copies move 16-bit words: fp16 too
@@ -2042,21 +2055,21 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // (HEADS kernels always copy MN-major operands block by block.)
     constexpr bool WIDE = TILE_N == 512;
     CUtensorMap mb2;  // wide tiles: B of one 256-column half of the tile (half the box)
-    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, ni, g.lda, g.a_part);
+    const bool a4 = !HEADS && A_MN && mn4 && g.M % 64 == 0 && make_map_mn4(&ma, g.a, g.K, g.M, BK, BM / 64, nia, g.lda, g.a_part);
     const bool b4 = !HEADS && B_MN && mn4 && g.N % 64 == 0 &&
-                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, ni, g.ldb, g.b_part) &&
+                    make_map_mn4(&mb, g.b, g.K, g.N, BK, C::B_ROWS / 64, nib, g.ldb, g.b_part) &&
                     (!WIDE || make_map_mn4(&mb2, g.b, g.K, g.N, BK, C::B_ROWS / 128, ni, g.ldb, g.b_part));
     bool oka, okb;
     if (a_rank > 3)
         oka = make_map_view(&ma, g.a, g.a_view, 64, A_MN ? BK : BM, sw);
     else
-        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, ni, bf, g.lda, g.a_part)
-                          : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, ni, bf, g.lda, g.a_part));
+        oka = a4 || (A_MN ? make_map(&ma, g.a, g.K, g.M, 64, BK, sw, nia, bf, g.lda, g.a_part)
+                          : make_map(&ma, g.a, g.M, g.K, BK, BM, sw, nia, bf, g.lda, g.a_part));
     if (b_rank > 3)
         okb = make_map_view(&mb, g.b, g.b_view, 64, B_MN ? BK : C::B_ROWS, sw);
     else
-        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, ni, bf, g.ldb, g.b_part)
-                          : make_map(&mb, g.b, g.N, g.K, BK, any_n ? any_n / CG : C::B_ROWS, sw, ni, bf, g.ldb, g.b_part));
+        okb = b4 || (B_MN ? make_map(&mb, g.b, g.K, g.N, 64, BK, sw, nib, bf, g.ldb, g.b_part)
+                          : make_map(&mb, g.b, g.N, g.K, BK, any_n ? any_n / CG : C::B_ROWS, sw, nib, bf, g.ldb, g.b_part));
     if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, ni, bf, g.ldb, g.b_part);
     if (!WIDE || (B_MN && !b4)) mb2 = mb;  // unused, or the per-block maps serve both widths
     if (!oka || !okb) return cudaErrorInvalidValue;
@@ -2142,7 +2155,14 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         p.kb_seg = p.nshards * p.kb_per_shard / p.pairs;
     else
         p.kb_per_shard *= p.pairs;
-    if (EPI == EPI_NS_FINAL) p.kb_per_shard *= 3;
+    if (EPI == EPI_NS_FINAL) {
+        // Q's low part times X, (X's low part times Q,) then the high parts; in a wide matrix's
+        // product Q is A, in a tall one's B
+        p.seg_codes = g.x_single ? (x_is_a ? 0u | 2u << 2 : 1u | 2u << 2) : (0u | 1u << 2 | 2u << 4);
+        p.kb_per_shard *= g.x_single ? 2 : 3;
+    }
+    p.x_single = g.x_single ? 1 : 0;
+    if (EPI == EPI_NS_GRAM32) p.stage_bytes = static_cast<uint32_t>(g.x_single ? C::A_STAGE : C::STAGE_BYTES);
     p.scale = g.scale;
     p.causal = g.causal ? 1 : 0;
     p.rowvec = g.rowvec;
