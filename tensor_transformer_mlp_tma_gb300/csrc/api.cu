@@ -1166,11 +1166,10 @@ struct XentLayout {
     int64_t piece, pieces, groups, hp, ldo;
     StatsTile stats;
     Split dx, dw;
-    size_t part, target_logit, row_g, xp, wp, ds, logits, acc, dwacc, total;
+    size_t part, target_logit, xp, wp, ds, logits, acc, dwacc, total;
 };
 
-// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | g per
-// token | three bf16 parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA
+// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | three bf16 parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA
 // path) | fp32 dX, per split | fp32 dW of one piece, per split.
 XentLayout xent_layout(const tpmlp_xent_shape *s) {
     XentLayout L;
@@ -1201,7 +1200,6 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
     const size_t piece = static_cast<size_t>(L.piece), hp = static_cast<size_t>(L.hp), ldo = static_cast<size_t>(L.ldo);
     L.part = region(stored * T * sizeof(float2));
     L.target_logit = region(T * 4);
-    L.row_g = region(T * 4);
     L.xp = region(tc && f32 ? 3 * T * hp * 2 : 0);
     L.wp = region(tc && f32 ? 3 * V * hp * 2 : 0);
     L.ds = region(T * piece * (tc ? (f32 ? 6 : 2) : (f32 ? 4 : 2)));
@@ -1281,14 +1279,9 @@ struct XentCall {
     }
     cudaError_t split_operands(const void *X, const void *W) const {
         if (!parts()) return cudaSuccess;
-        cudaError_t e = kernel("xent_split_x", [&] {
-            return tpmlp::launch_split3(static_cast<const float *>(X), s->tokens, s->hidden, L.hp, ws + L.xp, st);
-        });
-        if (e == cudaSuccess)
-            e = kernel("xent_split_w", [&] {
-                return tpmlp::launch_split3(static_cast<const float *>(W), s->vocab, s->hidden, L.hp, ws + L.wp, st);
-            });
-        return e;
+        const tpmlp::Split3 x = {static_cast<const float *>(X), s->tokens, s->hidden, L.hp, ws + L.xp};
+        const tpmlp::Split3 w = {static_cast<const float *>(W), s->vocab, s->hidden, L.hp, ws + L.wp};
+        return kernel("xent_split", [&] { return tpmlp::launch_split3(x, w, st); });
     }
     const void *w_rows(const void *W, int64_t v0) const {
         return static_cast<const uint8_t *>(W) + static_cast<size_t>(v0) * s->hidden * esz();
@@ -1399,9 +1392,6 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     }
     const XentCall c(s, target, workspace, sms, stream);
     const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
-    float *row_g = reinterpret_cast<float *>(c.ws + c.L.row_g);
-    e = c.kernel("xent_row_g", [&] { return tpmlp::launch_xent_row_g(c.rows, dloss, row_g, c.st); });
-    if (e != cudaSuccess) return from_cuda(e);
     if ((e = c.split_operands(X, W)) != cudaSuccess) return from_cuda(e);
     uint8_t *ds = c.ws + c.L.ds;
     const int64_t T = s->tokens, h = s->hidden;
@@ -1418,7 +1408,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
         const int64_t ds_part = T * ld;
         if (tc) {
             g.out0 = ds, g.ldo = ld;
-            g.row_lse = lse, g.row_g = row_g;
+            g.row_lse = lse, g.dloss = dloss, g.vocab = s->vocab;
             e = c.launch("xent_ds", f32 ? tpmlp::EPI_XENT_GRAD3 : tpmlp::EPI_XENT_GRAD, g);
         } else {
             float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
@@ -1426,7 +1416,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
             e = c.launch("xent_logits", tpmlp::EPI_ACC32, g);
             if (e == cudaSuccess)
                 e = c.kernel("xent_piece_grad", [&] {
-                    return tpmlp::launch_xent_piece_grad(!f32, c.rows, logits, n, v0, lse, row_g, ds, c.st);
+                    return tpmlp::launch_xent_piece_grad(!f32, c.rows, logits, n, v0, lse, dloss, ds, c.st);
                 });
         }
         if (e != cudaSuccess) return from_cuda(e);
@@ -1549,10 +1539,10 @@ struct OrthoLayout {
     int64_t P, Q, p;
     bool wide;   // rows <= cols: A = X X^T, else A = X^T X
     bool chain;  // the steps on the Gram matrix alone (ns_chain.cu)
-    int splits;  // chain: K ranges of the Gram product, and their length
+    int splits;  // K ranges of the Gram product, and their length
     int64_t split_len;
     float q_scale;
-    size_t norm, hi[2], lo[2], rest, A, C, total;
+    size_t norm, hi[2], lo[2], rest, gram, A, C, total;
 };
 
 // Workspace, 1 KB-aligned regions: status | block sums of the norm | X's high and low parts
@@ -1591,7 +1581,16 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
         L.A = region(2 * a * static_cast<size_t>(L.splits));
         L.C = region(2 * a);
     } else {
-        L.splits = 0, L.split_len = 0;
+        // A long K over few tiles: K ranges of 512 or more on the idle SMs, added up by a launch of
+        // their own (about 6 us against 0.3 us per 64 of K; 700 x 8000: A 42 us at 21 tiles).
+        const int64_t K = L.wide ? L.Q : L.P, t = (L.p + 127) / 128, tiles = t * (t + 1) / 2 * s->batch;
+        const int64_t want = std::min<int64_t>(152 / std::max<int64_t>(1, tiles), K / 512);
+        L.splits = 1, L.split_len = K;
+        if (want > 1 && K - K / want >= 2048) {
+            L.split_len = (K / want + 63) / 64 * 64;
+            L.splits = static_cast<int>((K + L.split_len - 1) / L.split_len);
+        }
+        L.gram = region(L.splits > 1 ? 2 * a * static_cast<size_t>(L.splits) : 0);
         for (int i = 0; i < 2; ++i) L.hi[i] = region(x), L.lo[i] = region(x);
         L.A = region(a);
         L.C = region(a);
@@ -1716,7 +1715,18 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
         const int64_t inner = L.wide ? L.Q : L.P;
         GemmArgs g = product(hi, !L.wide, hi, !L.wide, L.p, L.p, inner, A);
         g.scale = kScaleA / (kScaleX * kScaleX);
-        e = launch("ortho_gram", tpmlp::EPI_NS_GRAM, g);
+        if (L.splits > 1) {
+            g.out0 = ws + L.gram;
+            g.ksplit = L.splits, g.kshard = L.split_len;
+            e = launch("ortho_gram", tpmlp::EPI_NS_GRAMS, g);
+            if (e == cudaSuccess)
+                e = timed_launch("ortho_gram_sum", [&] {
+                    return tpmlp::launch_ortho_gram_sum(reinterpret_cast<const float *>(ws + L.gram), L.splits,
+                                                        s->batch, L.p, g.scale, A, st);
+                });
+        } else {
+            e = launch("ortho_gram", tpmlp::EPI_NS_GRAM, g);
+        }
         if (e != cudaSuccess) return from_cuda(e);
 
         GemmArgs c = product(A, false, A, false, L.p, L.p, L.p, C);

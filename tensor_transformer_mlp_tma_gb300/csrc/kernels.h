@@ -22,6 +22,7 @@ enum Epi : int {
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
+    EPI_NS_GRAMS = 18,  // A in fp32, lower triangle, over K in ksplit ranges -- X X^T
     EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts               -- X X^T
     EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
     EPI_XENT_FOLD = 17, // XENT_STATS over K in nshards ranges, added up in fp32
@@ -98,11 +99,11 @@ struct GemmArgs {
     // EPI_XENT_STATS, EPI_XENT_GRAD: rows are tokens, columns vocabulary rows
     // col0 .. col0 + N - 1 of W.
     const int64_t *target;   // [M]
-    int64_t ignore_index, col0;
+    int64_t ignore_index, col0, vocab;
     float2 *part;            // STATS: (max, sum) of column group k, row m, at part[k * M + m]
     float *target_logit;     // STATS: [M], written where the target is one of the columns
     const float *row_lse;    // GRAD: [M]
-    const float *row_g;      // GRAD: [M]
+    const float *dloss;      // GRAD: [M]; a target that is ignored or outside [0, vocab) has none
     bool accumulate;         // EPI_ACC32: add to what out0 holds
     int tile_n;              // EPI_XENT_FOLD: columns per tile, a multiple of 32 up to 256 (0: 256)
     // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
@@ -195,17 +196,26 @@ bool xent_few(bool is_bf16, int64_t tokens, int64_t hidden);
 int64_t xent_few_groups(int64_t vocab);
 cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden, float2 *part,
                             cudaStream_t st);
-cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st);
 // out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
                               void *out, cudaStream_t st);
-// fp32 [rows][cols] as three bf16 matrices [rows][ld], ld >= cols, the rest zero.
-cudaError_t launch_split3(const float *in, int64_t rows, int64_t cols, int64_t ld, void *out, cudaStream_t st);
+// fp32 [rows][cols] as three bf16 matrices [rows][ld], ld >= cols a multiple of 4, the rest zero.
+struct Split3 {
+    const float *in;
+    int64_t rows, cols, ld;
+    void *out;
+};
+cudaError_t launch_split3(const Split3 &a, const Split3 &b, cudaStream_t st);
 // FFMA path: logits [tokens, n] of vocabulary rows col0 .. col0 + n - 1.
 cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,
                                     cudaStream_t st);
 cudaError_t launch_xent_piece_grad(bool is_bf16, const RowArgs &a, const float *logits, int64_t n, int64_t col0,
-                                   const float *lse, const float *row_g, void *out, cudaStream_t st);
+                                   const float *lse, const float *dloss, void *out, cudaStream_t st);
+
+// A [matrices][p][p] (fp16, whole) = scale * the sum of the splits' lower triangles
+// [splits][matrices][p][p], in order.
+cudaError_t launch_ortho_gram_sum(const float *in, int splits, int64_t matrices, int64_t p, float scale, void *A,
+                                  cudaStream_t st);
 
 // Newton-Schulz orthogonalisation (ortho.cu): X = G scale / (|G| + eps) as hi + lo / 2^11.
 struct OrthoStart {

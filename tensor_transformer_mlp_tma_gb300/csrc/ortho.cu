@@ -67,14 +67,21 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, in
     Blue b{0.0f, 0.0f, 0.0f};
     if constexpr (VEC) {
         constexpr int E = 16 / sizeof(T);
-#pragma unroll 4
-        for (int64_t i = beg + threadIdx.x * E; i < end; i += THREADS * E) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(g + i));
-            const T *v = reinterpret_cast<const T *>(&w);
-            float x[E];
+        constexpr int UN = 4;  // loads in flight before the first is used
+        for (int64_t i = beg + threadIdx.x * E; i < end; i += UN * THREADS * E) {
+            uint4 w[UN];
 #pragma unroll
-            for (int j = 0; j < E; ++j) x[j] = value<T>(v[j]);
-            add(b, x);
+            for (int u = 0; u < UN; ++u)
+                w[u] = i + u * THREADS * E < end ? __ldg(reinterpret_cast<const uint4 *>(g + i + u * THREADS * E))
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const T *v = reinterpret_cast<const T *>(&w[u]);
+                float x[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[j] = value<T>(v[j]);
+                add(b, x);
+            }
         }
     } else {
 #pragma unroll 4
@@ -207,6 +214,32 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
     }
 }
 
+// The splits' sum of one 32 x 32 piece of A's lower triangle per block, stored where it is
+// and transposed.  Memory bound: 4 bytes per split and element of the triangle, 4 written.
+__global__ void __launch_bounds__(THREADS) gram_sum_kernel(const float *in, int splits, int64_t p, float scale,
+                                                           __half *A) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (blockIdx.x > blockIdx.y) return;  // above the diagonal
+    __shared__ float t[32][33];
+    const int64_t step = static_cast<int64_t>(gridDim.z) * p * p, at = blockIdx.z * p * p;
+    const int64_t r0 = blockIdx.y * 32, c0 = blockIdx.x * 32;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float *src = in + at + (r0 + y + 8 * k) * p + c0 + x;
+        float s = 0.0f;
+        for (int i = 0; i < splits; ++i) s += src[i * step];
+        s *= scale;
+        A[at + (r0 + y + 8 * k) * p + c0 + x] = __float2half_rn(s);
+        t[y + 8 * k][x] = s;
+    }
+    if (blockIdx.x == blockIdx.y) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A[at + (c0 + y + 8 * k) * p + r0 + x] = __float2half_rn(t[x][y + 8 * k]);
+}
+
 // The last step's result out of its padded array, where the output's rows are not
 // multiples of 16 bytes (a TMA store cannot write them).
 __global__ void __launch_bounds__(THREADS) unpad_kernel(const __nv_bfloat16 *in, int64_t rows, int64_t cols, int64_t P,
@@ -270,6 +303,12 @@ cudaError_t launch_ortho_norm(bool is_bf16, const OrthoStart &a, cudaStream_t st
 }
 cudaError_t launch_ortho_scale(bool is_bf16, const OrthoStart &a, cudaStream_t st) {
     return is_bf16 ? ortho::launch_start<__nv_bfloat16>(a, false, st) : ortho::launch_start<float>(a, false, st);
+}
+
+cudaError_t launch_ortho_gram_sum(const float *in, int splits, int64_t matrices, int64_t p, float scale, void *A,
+                                  cudaStream_t st) {
+    const dim3 g(static_cast<unsigned>(p / 32), static_cast<unsigned>(p / 32), static_cast<unsigned>(matrices));
+    return launch_pdl(ortho::gram_sum_kernel, g, ortho::THREADS, 0, st, in, splits, p, scale, static_cast<__half *>(A));
 }
 
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,

@@ -169,7 +169,8 @@ struct Params {
     long long ignore_index, col0;
     float2 *part;
     float *target_logit;
-    const float *row_lse, *row_g;
+    const float *row_lse, *dloss;
+    long long vocab;
     int accumulate;  // EPI_ACC32
     // K of the cross entropy's products: kb_seg k-blocks per pair of operand parts (one
     // pair, or six for fp32 operands in three parts); problem z starts at k-block
@@ -196,9 +197,11 @@ __host__ __device__ constexpr bool is_ns(int epi) {
 }
 // Both operands as two fp16 parts (22 bits), three products per k-block.
 __host__ __device__ constexpr bool is_ns2(int epi) { return epi == EPI_NS_GRAM32 || epi == EPI_NS_FINAL; }
-__host__ __device__ constexpr bool is_f16(int epi) { return is_ns(epi) || is_ns2(epi); }
-__host__ __device__ constexpr bool is_out32(int epi) { return epi == EPI_ACC32 || epi == EPI_NS_GRAM32; }
-__host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY; }
+__host__ __device__ constexpr bool is_f16(int epi) { return is_ns(epi) || is_ns2(epi) || epi == EPI_NS_GRAMS; }
+__host__ __device__ constexpr bool is_out32(int epi) {
+    return epi == EPI_ACC32 || epi == EPI_NS_GRAM32 || epi == EPI_NS_GRAMS;
+}
+__host__ __device__ constexpr bool is_sym(int epi) { return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_GRAMS; }
 __host__ __device__ constexpr bool is_grad(int epi) { return epi == EPI_XENT_GRAD || epi == EPI_XENT_GRAD3; }
 __host__ __device__ constexpr bool is_stats(int epi) { return epi == EPI_XENT_STATS || epi == EPI_XENT_FOLD; }
 __host__ __device__ constexpr bool is_xent(int epi) { return is_stats(epi) || is_grad(epi); }
@@ -221,6 +224,9 @@ __device__ __forceinline__ KCoord k_coord(const Params &p, int kb, int z) {
         const int pair = p.pairs == 1 ? 5 : seg;
         return {(kb - seg * p.kb_seg + z * p.kb_seg) * BK, static_cast<int>((kSegA >> (2 * pair)) & 3u),
                 static_cast<int>((kSegB >> (2 * pair)) & 3u)};
+    } else if constexpr (EPI == EPI_NS_GRAMS) {
+        const int split = z / p.matrices, m = z - split * p.matrices;
+        return {(kb + split * p.kb_seg) * BK, m, m};
     } else if constexpr (is_ns2(EPI)) {
         if constexpr (EPI == EPI_NS_GRAM32) {
             // the high part through A's map and the low part through B's: one copy of each
@@ -658,7 +664,7 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, Xent
     if (valid && c >= 0 && c < p.N) x.tcol = static_cast<int>(c);
     if constexpr (is_grad(EPI)) {
         x.lse = p.row_lse[row];
-        x.g = p.row_g[row];  // zero where the target is ignored
+        x.g = valid && t >= 0 && t < p.vocab ? p.dloss[row] : 0.0f;
     }
 }
 
@@ -1040,7 +1046,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
-                      (TILE_N == 128 && CG == 1 && (EPI == EPI_NS_GRAM32 || is_ns_tile(EPI))),
+                      (TILE_N == 128 && CG == 1 && (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS || is_ns_tile(EPI))),
                   "narrow tile: CTA pairs and plain store, or single CTAs and Newton-Schulz products");
     static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
                   "wide tile: CTA pairs, one shard");
@@ -2187,7 +2193,8 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.part = g.part;
     p.target_logit = g.target_logit;
     p.row_lse = g.row_lse;
-    p.row_g = g.row_g;
+    p.dloss = g.dloss;
+    p.vocab = g.vocab;
     p.accumulate = g.accumulate ? 1 : 0;
     p.aux2 = g.aux2;
     p.alpha = g.alpha;
@@ -2266,8 +2273,8 @@ template <int EPI, bool A_MN, bool B_MN>
 static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
     if constexpr (EPI == EPI_XENT_FOLD) {
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
-    } else if constexpr (EPI == EPI_NS_GRAM32) {
-        return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);  // outputs of at most 128 x 128
+    } else if constexpr (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS) {
+        return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);  // small or split outputs
     } else if constexpr (EPI == EPI_NS_FINAL) {
         return launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
     } else if constexpr (is_ns(EPI)) {
@@ -2364,6 +2371,10 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
         case EPI_NS_LAST:
             if (!g.a_mn && g.b_mn) return launch_cg<EPI_NS_LAST, false, true>(g, num_sms, st);
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_LAST, false, false>(g, num_sms, st);
+            break;
+        case EPI_NS_GRAMS:
+            if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAMS, false, false>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_NS_GRAMS, true, true>(g, num_sms, st);
             break;
         case EPI_NS_GRAM32:
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAM32, false, false>(g, num_sms, st);

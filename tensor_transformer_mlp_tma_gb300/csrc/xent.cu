@@ -72,14 +72,6 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowAr
     }
 }
 
-// g of every token for the backward pass: 0 where the target does not take part.
-__global__ void row_g_kernel(const RowArgs a, const float *dloss, float *row_g) {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (row < a.tokens) row_g[row] = target_ok(a, row) ? dloss[row] : 0.0f;
-}
-
 // ---- few tokens ------------------------------------------------------------------
 // Statistics of up to T tokens (one in bf16, up to eight in fp32) in one pass over W: X sits in shared memory, every warp
 // streams its share of W's rows, FEW_ROWS at a time, 512 bytes of each per load, and keeps its
@@ -356,19 +348,20 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int sp
 
 // x = p0 + p1 + p2 in bf16: the first two cut off after eight bits of the significand, so
 // that the three together hold its 24 bits (a value too large to round to bf16 does not
-// become infinite; an infinite one has parts inf, 0, 0).  Four columns per thread.
-// Memory bound: 4 bytes read, 6 written per element.
-__global__ void __launch_bounds__(256) split3_kernel(const float *in, int64_t rows, int64_t cols, int64_t ld,
-                                                     __nv_bfloat16 *out) {
+// become infinite; an infinite one has parts inf, 0, 0).  Two matrices in one launch, four
+// columns per thread.  Memory bound: 4 bytes read, 6 written per element.
+__global__ void __launch_bounds__(256) split3_kernel(const Split3 a, const Split3 b) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t n = rows * ld;
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
-         i += static_cast<int64_t>(gridDim.x) * 1024) {
-        const int64_t r = i / ld, c = i - r * ld;
+    const int64_t na = a.rows * a.ld, n = na + b.rows * b.ld;
+    for (int64_t k = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; k < n;
+         k += static_cast<int64_t>(gridDim.x) * 1024) {
+        const Split3 &m = k < na ? a : b;
+        const int64_t i = k < na ? k : k - na, all = m.rows * m.ld;
+        const int64_t r = i / m.ld, c = i - r * m.ld;
         float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = c + j < cols ? in[r * cols + c + j] : 0.0f;
+        for (int j = 0; j < 4; ++j) v[j] = c + j < m.cols ? m.in[r * m.cols + c + j] : 0.0f;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
             __nv_bfloat16 h[4];
@@ -378,7 +371,8 @@ __global__ void __launch_bounds__(256) split3_kernel(const float *in, int64_t ro
                 h[j] = __float2bfloat16_rn(hi);
                 v[j] = isinf(v[j]) ? 0.0f : v[j] - hi;
             }
-            *reinterpret_cast<uint2 *>(out + part * n + i) = *reinterpret_cast<const uint2 *>(h);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(m.out) + part * all + i) =
+                *reinterpret_cast<const uint2 *>(h);
         }
     }
 }
@@ -414,10 +408,11 @@ __global__ void __launch_bounds__(ROW_THREADS) piece_stats_kernel(const RowArgs 
 // dS of one token over this piece (fp32 in place, or bf16 beside the logits).
 template <typename T>
 __global__ void __launch_bounds__(ROW_THREADS) piece_grad_kernel(const RowArgs a, const float *logits, int64_t n,
-                                                                int64_t col0, const float *lse, const float *row_g,
+                                                                int64_t col0, const float *lse, const float *dloss,
                                                                 T *out) {
     const int64_t row = blockIdx.x;
-    const float g = row_g[row], l = lse[row];
+    const bool takes_part = a.target[row] != a.ignore_index && a.target[row] >= 0 && a.target[row] < a.vocab;
+    const float g = takes_part ? dloss[row] : 0.0f, l = lse[row];
     const int64_t t = a.target[row] - col0;
     for (int64_t i = threadIdx.x; i < n; i += ROW_THREADS) {
         float v = 0.0f;
@@ -507,10 +502,6 @@ cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const
     return launch_few_t<float, 1>(a, X, W, h, part, st);
 }
 
-cudaError_t launch_xent_row_g(const RowArgs &a, const float *dloss, float *row_g, cudaStream_t st) {
-    return launch_pdl(xent::row_g_kernel, dim3(static_cast<unsigned>((a.tokens + 255) / 256)), 256, 0, st, a, dloss, row_g);
-}
-
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
                               void *out, cudaStream_t st) {
     const bool vec = cols % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
@@ -525,9 +516,9 @@ cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t
                : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o);
 }
 
-cudaError_t launch_split3(const float *in, int64_t rows, int64_t cols, int64_t ld, void *out, cudaStream_t st) {
-    return launch_pdl(xent::split3_kernel, dim3(static_cast<unsigned>(xent::blocks_for(rows * ld / 4))), 256, 0, st, in, rows, cols, ld,
-                        static_cast<__nv_bfloat16 *>(out));
+cudaError_t launch_split3(const Split3 &a, const Split3 &b, cudaStream_t st) {
+    const int64_t n = a.rows * a.ld + b.rows * b.ld;
+    return launch_pdl(xent::split3_kernel, dim3(static_cast<unsigned>(xent::blocks_for(n / 4))), 256, 0, st, a, b);
 }
 
 cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,
@@ -537,13 +528,13 @@ cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64
 }
 
 cudaError_t launch_xent_piece_grad(bool is_bf16, const RowArgs &a, const float *logits, int64_t n, int64_t col0,
-                                   const float *lse, const float *row_g, void *out, cudaStream_t st) {
+                                   const float *lse, const float *dloss, void *out, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(a.tokens);
     if (is_bf16)
-        xent::piece_grad_kernel<<<grid, xent::ROW_THREADS, 0, st>>>(a, logits, n, col0, lse, row_g,
+        xent::piece_grad_kernel<<<grid, xent::ROW_THREADS, 0, st>>>(a, logits, n, col0, lse, dloss,
                                                                     static_cast<__nv_bfloat16 *>(out));
     else
-        xent::piece_grad_kernel<<<grid, xent::ROW_THREADS, 0, st>>>(a, logits, n, col0, lse, row_g,
+        xent::piece_grad_kernel<<<grid, xent::ROW_THREADS, 0, st>>>(a, logits, n, col0, lse, dloss,
                                                                     static_cast<float *>(out));
     return cudaGetLastError();
 }

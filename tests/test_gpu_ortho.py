@@ -74,6 +74,7 @@ SHAPES = [  # batch, rows, cols
     (1, 1, 1), (1, 1, 40), (2, 7, 5), (3, 16, 64), (1, 64, 64), (2, 65, 63), (1, 128, 512), (4, 200, 120),
     (1, 256, 256), (1, 257, 1024), (2, 1000, 264), (1, 515, 1003), (5, 300, 300), (1, 1024, 700), (33, 32, 130), (2, 48, 48),
     (3, 17, 300), (1, 90, 90), (2, 700, 112), (1, 128, 129), (1, 130, 127),
+    (1, 150, 6000), (2, 5003, 200),  # long and few tiles: the Gram product split
 ]
 
 
