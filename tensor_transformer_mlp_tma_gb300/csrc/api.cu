@@ -1302,6 +1302,12 @@ struct XentCall {
     }
     cudaError_t launch(const char *name, Epi epi, GemmArgs &g) const {
         const bool tc = xent_tc(s);
+        // Products of no more 128 x 128 tiles than there are SMs are bound by latency (T = 95, h = 840,
+        // V = 81: a step 35 against 31 us); with two waves of them the operands' bytes
+        // count again (T = 1001, h = 1000, V = 30011, dX: 90 against 55 us).
+        g.small_tile = epi != tpmlp::EPI_XENT_STATS && epi != tpmlp::EPI_XENT_FOLD &&
+                       (g.M + 127) / 128 * ((g.N + 127) / 128) * std::max(1, g.ksplit) <= 152;
+        if (g.small_tile) g.cta_pair = false;
         if (tc) pick_raster(g, epi);
         Timed timed(name, st);
         const cudaError_t e = tc ? tpmlp::launch_tc_gemm(epi, g, sms, st)

@@ -96,6 +96,7 @@ struct GemmArgs {
     int parts;
     int64_t a_part, b_part;
     int ksplit;
+    bool small_tile;  // 128 x 128 tiles on single CTAs (XENT_GRAD, XENT_GRAD3, ACC32, STORE)
     // EPI_XENT_STATS, EPI_XENT_GRAD: rows are tokens, columns vocabulary rows
     // col0 .. col0 + N - 1 of W.
     const int64_t *target;   // [M]

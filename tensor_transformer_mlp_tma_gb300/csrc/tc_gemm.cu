@@ -1046,8 +1046,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
-                      (TILE_N == 128 && CG == 1 && (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS || is_ns_tile(EPI))),
-                  "narrow tile: CTA pairs and plain store, or single CTAs and Newton-Schulz products");
+                      (TILE_N == 128 && CG == 1 && !HEADS && (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS || is_ns_tile(EPI) || is_grad(EPI) ||
+                                                  EPI == EPI_ACC32 || EPI == EPI_STORE)),
+                  "narrow tile: CTA pairs and plain store, or single CTAs and the small products");
     static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
                   "wide tile: CTA pairs, one shard");
     static_assert(!is_sym(EPI) || C::TILE_M == TILE_N, "symmetric outputs: square tiles");
@@ -2281,6 +2282,9 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
         if (!g.cta_pair) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
+    if constexpr (is_grad(EPI) || EPI == EPI_ACC32 || (EPI == EPI_STORE && B_MN)) {
+        if (g.small_tile) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
+    }
     if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || has_segments(EPI)) {
         if (tc_wide_tile(static_cast<Epi>(EPI), g)) return launch_t<EPI, A_MN, B_MN, 2, false, 512>(g, num_sms, st);
     }
@@ -2312,6 +2316,13 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
     if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || (tc::has_segments(epi) && epi != EPI_XENT_FOLD))) return false;
+    if (g.small_tile) return false;
+    if (tc::has_segments(epi) || (epi == EPI_STORE && !g.a_mn && g.b_mn)) {
+        // The cross entropy's products: where every wide tile would run as two half-width ones,
+        // the double-buffered 256 x 256 tiles do (T = 2048, h = 2048, V = 32768, dX: 187 against 171 us).
+        const int64_t tiles = (g.M + 255) / 256 * ((g.N + 511) / 512) * (g.ksplit > 1 ? g.ksplit : 1);
+        if (2 * tiles <= 76) return false;
+    }
     const char *w = std::getenv("TPMLP_WIDE");
     return !(w && w[0] == '0');
 }
