@@ -324,7 +324,7 @@ typedef struct {
 /* Bytes of device workspace of both passes: status word, statistics (8 bytes per
  * token and 128 vocabulary rows, or per 16 at the fewest where there are few tokens), dS of one piece (T * piece elements; FFMA path also
  * its fp32 logits) and, for bf16 and several pieces, dX in fp32.  256-byte aligned,
- * first 8 bytes zero before first use; 0 for an invalid shape. */
+ * first 16 bytes zero before first use; 0 for an invalid shape. */
 size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
 
 /* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
@@ -342,8 +342,9 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, co
 
 /* Backward: dX[T,h] and dW[V,h] from the forward pass's inputs and lse, and dloss[T]
  * (fp32).  Either output may be NULL and is then not computed (a frozen head, a
- * frozen body).  dS is rounded to the shape's dtype before the two products; dX is
- * summed over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
+ * frozen body).  In bf16 dS is rounded (in units of dloss[0] where that is a
+ * number of ordinary size) before the two products, in fp32 it is not; dX is summed
+ * over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
  * Results are bit-identical from call to call.  Errors as the forward. */
 tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
                                  const float *lse, const float *dloss, void *dX, void *dW, void *workspace,

@@ -1345,9 +1345,9 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
     if (xent_tc(s) && c.L.stats.tile_n == 0) {
         float2 *part = reinterpret_cast<float2 *>(c.ws + c.L.part);
         e = c.kernel("xent_few", [&] {
-            return tpmlp::launch_xent_few(s->dtype == TPMLP_BF16, c.rows, X, W, s->hidden, part, c.st);
+            return tpmlp::launch_xent_few(s->dtype == TPMLP_BF16, c.rows, X, W, s->hidden, part, loss, lse, c.st);
         });
-        if (e != cudaSuccess) return from_cuda(e);
+        return from_cuda(e);
     } else if (xent_tc(s)) {
         e = c.split_operands(X, W);
         if (e != cudaSuccess) return from_cuda(e);
@@ -1443,11 +1443,14 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
                     XentCall::set_parts(w, ds_part, T * c.L.hp);
                 }
             }
-            e = c.launch("xent_dw", tc && (f32 || !in_place) ? tpmlp::EPI_ACC32 : tpmlp::EPI_STORE, w);
+            w.dloss = dloss;
+            e = c.launch("xent_dw", !tc                 ? tpmlp::EPI_STORE
+                                    : f32 || !in_place ? tpmlp::EPI_ACC32
+                                                       : tpmlp::EPI_STORE_UNIT, w);
             if (e == cudaSuccess && !in_place)
                 e = c.kernel("xent_dw_sum", [&] {
                     return tpmlp::launch_sum_splits(!f32, reinterpret_cast<float *>(c.ws + c.L.dwacc), c.L.dw.n, n, h,
-                                                    c.L.ldo, out, c.st);
+                                                    c.L.ldo, f32 ? nullptr : dloss, out, c.st);
                 });
             if (e != cudaSuccess) return from_cuda(e);
         }
@@ -1467,13 +1470,15 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
                 }
             }
             const bool rounds = dx_in_place && !f32;  // one product gives the bf16 result
-            e = c.launch("xent_dx", rounds ? tpmlp::EPI_STORE : tpmlp::EPI_ACC32, x);
+            x.dloss = dloss;
+            e = c.launch("xent_dx", !rounds ? tpmlp::EPI_ACC32 : (tc ? tpmlp::EPI_STORE_UNIT : tpmlp::EPI_STORE), x);
             if (e != cudaSuccess) return from_cuda(e);
         }
     }
     if (dX && !dx_in_place)
         e = c.kernel("xent_dx_sum", [&] {
-            return tpmlp::launch_sum_splits(!f32, acc, tc ? c.L.dx.n : 1, T, h, tc ? c.L.ldo : h, dX, c.st);
+            return tpmlp::launch_sum_splits(!f32, acc, tc ? c.L.dx.n : 1, T, h, tc ? c.L.ldo : h,
+                                            tc && !f32 ? dloss : nullptr, dX, c.st);
         });
     return from_cuda(e);
 }

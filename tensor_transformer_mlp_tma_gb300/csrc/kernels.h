@@ -6,6 +6,19 @@
 
 namespace tpmlp {
 
+// The unit that dS of bf16 is taken in: dS / unit is rounded and multiplied, and the products
+// are multiplied by it in fp32.  The usual gradients of the losses are all the same (1 over
+// the tokens of a mean); in that unit dS at a target is p - 1, close to -1, where in the
+// plain unit it is the same rounding of 1/n in every token, up to 2^-9 of dX and dW that
+// does not average out.  The first token's gradient is as good as any where they differ;
+// one out of reach of fp32's middle range is not used.
+#ifdef __CUDACC__
+__device__ __forceinline__ float xent_unit(const float *dloss) {
+    const float g = fabsf(dloss[0]);
+    return g >= 0x1p-20f && g <= 0x1p20f ? g : 1.0f;
+}
+#endif
+
 // Epilogues of the GEMM kernels.  Each names the step of the MLP it finishes.
 enum Epi : int {
     EPI_BIAS_GELU = 0,  // H = acc + a (optional store), Y = GeLU(H) (optional) -- column-parallel GEMM
@@ -22,6 +35,7 @@ enum Epi : int {
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
+    EPI_STORE_UNIT = 19, // out = acc * unit (see xent_unit)                 -- dX and dW of bf16
     EPI_NS_GRAMS = 18,  // A in fp32, lower triangle, over K in ksplit ranges -- X X^T
     EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts               -- X X^T
     EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
@@ -196,10 +210,11 @@ constexpr int64_t XENT_FEW_SMEM = 192 * 1024;
 bool xent_few(bool is_bf16, int64_t tokens, int64_t hidden);
 int64_t xent_few_groups(int64_t vocab);
 cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden, float2 *part,
-                            cudaStream_t st);
+                            float *loss, float *lse, cudaStream_t st);
 // out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
+// With dloss the sums are multiplied by xent_unit(dloss).
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
-                              void *out, cudaStream_t st);
+                              const float *dloss, void *out, cudaStream_t st);
 // fp32 [rows][cols] as three bf16 matrices [rows][ld], ld >= cols a multiple of 4, the rest zero.
 struct Split3 {
     const float *in;

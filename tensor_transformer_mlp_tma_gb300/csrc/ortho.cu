@@ -294,6 +294,7 @@ static cudaError_t launch_start(const OrthoStart &a, bool norm, cudaStream_t st)
 }  // namespace ortho
 
 int64_t ortho_norm_blocks(int64_t batch, int64_t n) {
+    if (batch < 1) batch = 1;
     const int64_t most = (152 * 4 + batch - 1) / batch, want = (n + 8191) / 8192;
     return want < most ? want : most;
 }

@@ -209,9 +209,9 @@ __host__ __device__ constexpr bool is_xent(int epi) { return is_stats(epi) || is
 __host__ __device__ constexpr bool has_segments(int epi) { return is_xent(epi) || epi == EPI_ACC32; }
 
 // The pairs of parts (a, b) of an fp32 product, two bits each, from the smallest:
-// (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).  Part i holds bits 8i .. 8i + 7 of the
-// significand, so what is left out is below 2^-23 of |a| |b|.  A plain product takes
-// the last pair only.
+// (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).  Part i is at most 2^-8i of the number (each is
+// what the ones before it left, rounded), so what is left out, (1,2), (2,1) and (2,2), is
+// below 2^-22 of |a| |b|, of either sign.  A plain product takes the last pair only.
 constexpr uint32_t kSegA = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
 constexpr uint32_t kSegB = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
 struct KCoord {
@@ -665,6 +665,7 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, Xent
     if constexpr (is_grad(EPI)) {
         x.lse = p.row_lse[row];
         x.g = valid && t >= 0 && t < p.vocab ? p.dloss[row] : 0.0f;
+        if constexpr (EPI == EPI_XENT_GRAD) x.g = __fdiv_rn(x.g, xent_unit(p.dloss));
     }
 }
 
@@ -867,21 +868,18 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
     }
     if constexpr (EPI == EPI_XENT_GRAD) xent_grad_chunk(v, col, *xr);
     if constexpr (EPI == EPI_XENT_GRAD3) {
-        // dS = d0 + d1 + d2, the first two cut (not rounded) to bf16, so that each holds
-        // the next eight bits of the significand.
+        // dS = d0 + d1 + d2, each the rest before it rounded to bf16.
         xent_grad_chunk(v, col, *xr);
         const bool inside = row0 < p.M && col < p.N;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
             uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float hi = part < 2 ? __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u) : v[i];
-                if (i & 1)
-                    w[i >> 1] = pack_bf16(__uint_as_float(w[i >> 1]), hi);
-                else
-                    w[i >> 1] = __float_as_uint(hi);
-                if (part < 2) v[i] -= hi;
+            for (int i = 0; i < 16; ++i) {
+                w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                float a, b;
+                unpack_bf16(w[i], a, b);
+                v[2 * i] -= a, v[2 * i + 1] -= b;
             }
             if (lane == 0 && part != 1) ptx::bulk_wait_read0();  // parts 0 and 2 share a box
             __syncwarp();
@@ -974,7 +972,12 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += bias[i];
         pack32(v, w0);
-    } else {  // EPI_STORE, EPI_FOLD
+    } else {  // EPI_STORE, EPI_STORE_UNIT, EPI_FOLD
+        if constexpr (EPI == EPI_STORE_UNIT) {
+            const float unit = xent_unit(p.dloss);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= unit;
+        }
         pack32(v, w0);
     }
     // The previous chunk's stores must have finished reading the staging boxes.
@@ -1047,7 +1050,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int CHUNKS = TILE_N / 64;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
                       (TILE_N == 128 && CG == 1 && !HEADS && (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS || is_ns_tile(EPI) || is_grad(EPI) ||
-                                                  EPI == EPI_ACC32 || EPI == EPI_STORE)),
+                                                  EPI == EPI_ACC32 || EPI == EPI_STORE_UNIT)),
                   "narrow tile: CTA pairs and plain store, or single CTAs and the small products");
     static_assert(!WIDE || (CG == 2 && !HEADS && !FOLD && EPI != EPI_ATTN_SCORE && EPI != EPI_ATTN_DS && !is_ns(EPI)),
                   "wide tile: CTA pairs, one shard");
@@ -2282,10 +2285,11 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
         if (!g.cta_pair) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
-    if constexpr (is_grad(EPI) || EPI == EPI_ACC32 || (EPI == EPI_STORE && B_MN)) {
+    if constexpr (is_grad(EPI) || EPI == EPI_ACC32 || EPI == EPI_STORE_UNIT) {
         if (g.small_tile) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
     }
-    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || EPI == EPI_STORE || has_segments(EPI)) {
+    if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || (EPI == EPI_STORE && A_MN == B_MN) ||
+                  EPI == EPI_STORE_UNIT || has_segments(EPI)) {
         if (tc_wide_tile(static_cast<Epi>(EPI), g)) return launch_t<EPI, A_MN, B_MN, 2, false, 512>(g, num_sms, st);
     }
     if constexpr (EPI == EPI_STORE && !A_MN && !B_MN) {
@@ -2315,9 +2319,11 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
-    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || epi == EPI_STORE || (tc::has_segments(epi) && epi != EPI_XENT_FOLD))) return false;
+    if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || (epi == EPI_STORE && g.a_mn == g.b_mn) || epi == EPI_STORE_UNIT ||
+          (tc::has_segments(epi) && epi != EPI_XENT_FOLD)))
+        return false;
     if (g.small_tile) return false;
-    if (tc::has_segments(epi) || (epi == EPI_STORE && !g.a_mn && g.b_mn)) {
+    if (tc::has_segments(epi) || epi == EPI_STORE_UNIT) {
         // The cross entropy's products: where every wide tile would run as two half-width ones,
         // the double-buffered 256 x 256 tiles do (T = 2048, h = 2048, V = 32768, dX: 187 against 171 us).
         const int64_t tiles = (g.M + 255) / 256 * ((g.N + 511) / 512) * (g.ksplit > 1 ? g.ksplit : 1);
@@ -2363,6 +2369,10 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
             break;
         case EPI_XENT_GRAD3:
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_XENT_GRAD3, false, false>(g, num_sms, st);
+            break;
+        case EPI_STORE_UNIT:
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_STORE_UNIT, false, true>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_STORE_UNIT, true, true>(g, num_sms, st);
             break;
         case EPI_ACC32:  // dS[T,V'] (K-major) . W[V',h] (MN-major); dS^T . X[T,h] (both MN-major)
             if (!g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, false, true>(g, num_sms, st);

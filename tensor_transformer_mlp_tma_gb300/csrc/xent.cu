@@ -35,6 +35,39 @@ __device__ __forceinline__ bool target_ok(const RowArgs &a, int64_t row) {
     return false;
 }
 
+__device__ __forceinline__ void finish_row(const RowArgs &a, int64_t row, float m, float s, float *loss, float *lse) {
+    const float l = logf(s);
+    lse[row] = m + l;
+    // the difference of the two large terms first, then the small one
+    loss[row] = target_ok(a, row) ? (m - __ldcg(a.target_logit + row)) + l : 0.0f;
+}
+
+// The last block of a grid to get here joins the blocks' pairs of up to 8 tokens, in order, a
+// warp per token.  status[2] counts the blocks; the last one sets it back to zero.
+__device__ __forceinline__ void last_block_joins(const RowArgs &a, float *loss, float *lse) {
+    __shared__ bool last;
+    __threadfence();  // this thread's partials and target logits, before its block is counted
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.status + 2, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (threadIdx.x == 0) a.status[2] = 0u;
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    if (row >= a.tokens) return;
+    float m = -INFINITY, s = 0.0f;
+    for (int64_t g = lane; g < gridDim.x; g += 32) {
+        const float2 p = __ldcg(a.part + g * a.tokens + row);
+        join(m, s, p.x, p.y);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, off), s2 = __shfl_xor_sync(0xffffffffu, s, off);
+        join(m, s, m2, s2);
+    }
+    if (lane == 0) finish_row(a, row, m, s, loss, lse);
+}
+
 // loss and lse of 32 tokens per block: lane = token (the partials of one group are
 // contiguous over tokens), the warps take every 32nd group and join theirs through
 // shared memory, in a fixed order.  Reads 8 bytes per token and 128 vocabulary rows,
@@ -64,12 +97,7 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowAr
         }
         __syncthreads();
     }
-    if (w == 0 && row < a.tokens) {
-        const float l = logf(s);
-        lse[row] = m + l;
-        // the difference of the two large terms first, then the small one
-        loss[row] = target_ok(a, row) ? (m - a.target_logit[row]) + l : 0.0f;
-    }
+    if (w == 0 && row < a.tokens) finish_row(a, row, m, s, loss, lse);
 }
 
 // ---- few tokens ------------------------------------------------------------------
@@ -115,7 +143,7 @@ struct Chunk<float, 1> {  // rows that do not start on 16 bytes
 
 template <typename E, int EC, int T>
 __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, const E *X, const E *W, int64_t h,
-                                                            float2 *part) {
+                                                            float2 *part, float *loss, float *lse) {
     extern __shared__ __align__(16) uint8_t few_smem[];
     E *xs = reinterpret_cast<E *>(few_smem);  // [T][h]
     __shared__ float2 sh[FEW_THREADS / 32][T];
@@ -211,6 +239,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, co
         for (int i = 1; i < FEW_THREADS / 32; ++i) join(p.x, p.y, sh[i][threadIdx.x].x, sh[i][threadIdx.x].y);
         part[static_cast<int64_t>(blockIdx.x) * a.tokens + threadIdx.x] = p;
     }
+    last_block_joins(a, loss, lse);
 }
 
 // The same for 2 to 8 bf16 tokens, where one FMA per weight and token would cost more than
@@ -225,7 +254,7 @@ constexpr int SLIM_ROWS = 16;
 template <int SLIM_WARPS>
 __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(const RowArgs a, const __nv_bfloat16 *X,
                                                               const __nv_bfloat16 *W, int64_t h, int hp,
-                                                              float2 *part) {
+                                                              float2 *part, float *loss, float *lse) {
     extern __shared__ __align__(16) uint8_t slim_smem[];
     // [8][hp], hp = h rounded up to 32, and 8 more: a row's 16-byte pieces then start 4
     // banks after the row before, and the eight tokens that a load touches do not collide
@@ -306,15 +335,17 @@ __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(
         for (int k = 1; k < SLIM_WARPS; ++k) join(p.x, p.y, all[k * 8 + threadIdx.x].x, all[k * 8 + threadIdx.x].y);
         part[static_cast<int64_t>(blockIdx.x) * a.tokens + threadIdx.x] = p;
     }
+    last_block_joins(a, loss, lse);
 }
 
 // Fixed-order sum of the fp32 matrices that split products left, rounded once to the
 // output's type.  V columns per thread.  Memory bound: 4 bytes per split and element.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int splits, int64_t rows, int64_t cols,
-                                                         int64_t ld, T *out) {
+                                                         int64_t ld, const float *dloss, T *out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    const float unit = dloss ? xent_unit(dloss) : 1.0f;
     const int64_t per_row = cols / V, n = rows * per_row, step = rows * ld;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -332,6 +363,8 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int sp
             }
         }
         T *dst = out + r * cols + c;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] *= unit;
         if constexpr (sizeof(T) == 4 && V == 4) {
             *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
         } else if constexpr (sizeof(T) == 4) {
@@ -346,9 +379,9 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int sp
     }
 }
 
-// x = p0 + p1 + p2 in bf16: the first two cut off after eight bits of the significand, so
-// that the three together hold its 24 bits (a value too large to round to bf16 does not
-// become infinite; an infinite one has parts inf, 0, 0).  Two matrices in one launch, four
+// x = p0 + p1 + p2 in bf16, each the rest before it rounded to eight bits, so that the
+// three together hold all 24 (the largest fp32 numbers, which would round up to
+// infinity, are cut off instead; an infinite one has parts inf, 0, 0).  Two matrices in one launch, four
 // columns per thread.  Memory bound: 4 bytes read, 6 written per element.
 __global__ void __launch_bounds__(256) split3_kernel(const Split3 a, const Split3 b) {
     ptx::griddep_wait();
@@ -367,9 +400,9 @@ __global__ void __launch_bounds__(256) split3_kernel(const Split3 a, const Split
             __nv_bfloat16 h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float hi = part < 2 ? __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u) : v[j];
-                h[j] = __float2bfloat16_rn(hi);
-                v[j] = isinf(v[j]) ? 0.0f : v[j] - hi;
+                h[j] = __float2bfloat16_rn(v[j]);
+                if (__hisinf(h[j]) && !isinf(v[j])) h[j] = __float2bfloat16_rz(v[j]);
+                v[j] = isinf(v[j]) ? 0.0f : v[j] - __bfloat162float(h[j]);
             }
             *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(m.out) + part * all + i) =
                 *reinterpret_cast<const uint2 *>(h);
@@ -457,63 +490,64 @@ int64_t xent_few_groups(int64_t vocab) {
 
 template <int WARPS>
 static cudaError_t launch_slim(const RowArgs &a, const void *X, const void *W, int64_t h, int64_t smem, float2 *part,
-                               cudaStream_t st) {
+                               float *loss, float *lse, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(xent::slim_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(XENT_FEW_SMEM));
     if (e != cudaSuccess) return e;
     return launch_pdl(xent::slim_kernel<WARPS>, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), 32 * WARPS,
                       static_cast<size_t>(smem), st, a, static_cast<const __nv_bfloat16 *>(X),
-                      static_cast<const __nv_bfloat16 *>(W), h, static_cast<int>((h + 31) / 32 * 32), part);
+                      static_cast<const __nv_bfloat16 *>(W), h, static_cast<int>((h + 31) / 32 * 32), part, loss, lse);
 }
 
 template <typename E, int EC, int T>
-static cudaError_t launch_few(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part, cudaStream_t st) {
+static cudaError_t launch_few(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part, float *loss, float *lse,
+                              cudaStream_t st) {
     auto kernel = xent::few_kernel<E, EC, T>;
     const size_t smem = static_cast<size_t>(T) * h * sizeof(E);
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(XENT_FEW_SMEM));
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), xent::FEW_THREADS, smem, st, a,
-                      static_cast<const E *>(X), static_cast<const E *>(W), h, part);
+                      static_cast<const E *>(X), static_cast<const E *>(W), h, part, loss, lse);
 }
 
 template <typename E, int EC>
 static cudaError_t launch_few_t(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
-                                cudaStream_t st) {
-    if (a.tokens <= 1) return launch_few<E, EC, 1>(a, X, W, h, part, st);
-    if (a.tokens <= 2) return launch_few<E, EC, 2>(a, X, W, h, part, st);
-    if (a.tokens <= 4) return launch_few<E, EC, 4>(a, X, W, h, part, st);
-    return launch_few<E, EC, 8>(a, X, W, h, part, st);
+                                float *loss, float *lse, cudaStream_t st) {
+    if (a.tokens <= 1) return launch_few<E, EC, 1>(a, X, W, h, part, loss, lse, st);
+    if (a.tokens <= 2) return launch_few<E, EC, 2>(a, X, W, h, part, loss, lse, st);
+    if (a.tokens <= 4) return launch_few<E, EC, 4>(a, X, W, h, part, loss, lse, st);
+    return launch_few<E, EC, 8>(a, X, W, h, part, loss, lse, st);
 }
 
 cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
-                            cudaStream_t st) {
+                            float *loss, float *lse, cudaStream_t st) {
     if (is_bf16) {
-        if (a.tokens <= 1) return launch_few<__nv_bfloat16, 8, 1>(a, X, W, h, part, st);
+        if (a.tokens <= 1) return launch_few<__nv_bfloat16, 8, 1>(a, X, W, h, part, loss, lse, st);
         // 16 warps per SM: two blocks, of which one computes while the other is at its barrier,
         // where two copies of X leave room for the loads in L1; one block of all 16 warps where
         // they do not (T = 4, V = 50000: h = 6144 4.4 TB/s with two blocks, h = 8192 5.8 with one).
         const int64_t smem = few_smem(true, a.tokens, h);
-        return smem <= 72 * 1024 ? launch_slim<8>(a, X, W, h, smem, part, st)
-                                  : launch_slim<16>(a, X, W, h, smem, part, st);
+        return smem <= 72 * 1024 ? launch_slim<8>(a, X, W, h, smem, part, loss, lse, st)
+                                  : launch_slim<16>(a, X, W, h, smem, part, loss, lse, st);
     }
     const uintptr_t both = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W);
-    if (h % 4 == 0 && (both & 15) == 0) return launch_few_t<float, 4>(a, X, W, h, part, st);
-    return launch_few_t<float, 1>(a, X, W, h, part, st);
+    if (h % 4 == 0 && (both & 15) == 0) return launch_few_t<float, 4>(a, X, W, h, part, loss, lse, st);
+    return launch_few_t<float, 1>(a, X, W, h, part, loss, lse, st);
 }
 
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
-                              void *out, cudaStream_t st) {
+                              const float *dloss, void *out, cudaStream_t st) {
     const bool vec = cols % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     const int64_t blocks = xent::blocks_for(rows * cols / (vec ? 4 : 1));
     if (is_bf16) {
         auto o = static_cast<__nv_bfloat16 *>(out);
-        return vec ? launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o)
-                   : launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o);
+        return vec ? launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o)
+                   : launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o);
     }
     auto o = static_cast<float *>(out);
-    return vec ? launch_pdl(xent::sum_splits_kernel<float, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o)
-               : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, o);
+    return vec ? launch_pdl(xent::sum_splits_kernel<float, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o)
+               : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o);
 }
 
 cudaError_t launch_split3(const Split3 &a, const Split3 &b, cudaStream_t st) {

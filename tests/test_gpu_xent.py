@@ -232,6 +232,48 @@ def test_captured_and_replayed(tp):
     check(X, W, y, dl, out, ctx.lse, {"dX": dX, "dW": dW}, reference(X, W, y, dl))
 
 
+def test_equal_weights_leave_no_bias(tp):
+    """The same dloss for every token, half way between two bf16 numbers: rounding dS token by
+    token would move every target's term the same way, by 2^-9 to 2^-8 of it.  With T
+    terms rounded apart the mean error is at most 2^-8 / sqrt(3 T) in the mean of squares,
+    1e-4 for T = 512; 2^-10 is nine times that."""
+    X, W, y, _ = make(512, 256, 4000, seed=11)
+    dl = torch.full((512,), (1 + 2.0 ** -8) / 512, device="cuda")
+    for piece in (0, 2048):
+        ctx, loss, grads = run(tp, X, W, y, dl, piece=piece)
+        ref = reference(X, W, y, dl)
+        check(X, W, y, dl, loss, ctx.lse, grads, ref)
+        for n in ("dX", "dW"):
+            along = float((grads[n].double() * ref[n]).sum() / (ref[n] * ref[n]).sum())
+            assert abs(along - 1) < 2.0 ** -10, (n, along)
+
+
+def test_workspace_is_left_ready_for_the_next_call(tp):
+    """Calls of different kinds share one workspace, with other workspace contents between them."""
+    X, W, y, dl = make(4, 128, 700, seed=12)
+    ctx = tp.XentContext(4, 128, 700, X.dtype)
+    want = tp.xent_forward(ctx, X, W, y).clone()
+    for _ in range(3):
+        tp.xent_backward(ctx, dl)
+        ctx.workspace[1024:] = 255
+        assert torch.equal(tp.xent_forward(ctx, X, W, y), want)
+
+
+def test_a_context_on_its_tensors_device_only(tp):
+    X, W, y, dl = make(4, 64, 50, seed=13)
+    ctx = tp.XentContext(4, 64, 50, X.dtype)
+    with pytest.raises(ValueError):
+        tp.xent_forward(ctx, X.cpu(), W, y)
+    with pytest.raises(ValueError):
+        tp.xent_backward(ctx, dl)  # no forward yet
+    with pytest.raises(ValueError):
+        tp.xent_forward(ctx, X, W, y.int())
+    with pytest.raises(ValueError):
+        tp.xent_forward(ctx, X, W.t().contiguous().t(), y)
+    with pytest.raises(tp.TpmlpError):
+        tp.xent_forward(tp.XentContext(4, 60, 50, X.dtype), X[:, :60].contiguous(), W[:, :60].contiguous(), y)
+
+
 def test_no_tokens(tp):
     W = torch.randn(100, 64, device="cuda").bfloat16()
     X = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
