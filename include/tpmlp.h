@@ -345,7 +345,8 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, co
  * frozen body).  In bf16 dS is rounded (in units of dloss[0] where that is a
  * number of ordinary size) before the two products, in fp32 it is not; dX is summed
  * over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
- * Results are bit-identical from call to call.  Errors as the forward. */
+ * Results are bit-identical from call to call.  No output may overlap an input or the
+ * other output (the same pointer is refused).  Errors as the forward. */
 tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
                                  const float *lse, const float *dloss, void *dX, void *dW, void *workspace,
                                  void *stream);
@@ -376,10 +377,12 @@ typedef struct {
  * zero before first use; 0 for an invalid shape. */
 size_t tpmlp_ortho_workspace_bytes(const tpmlp_ortho_shape *shape);
 
-/* O[batch][rows][cols] (bf16) from G (contiguous, of shape->dtype).  A zero matrix
+/* O[batch][rows][cols] (bf16) from G (contiguous, of shape->dtype); O may be the buffer
+ * of a bf16 G.  A zero matrix
  * gives zeros; a matrix with NaN or infinity gives non-finite values in its own
- * output only.  Errors: INVALID_ARG for a bad shape or NULL pointer; UNSUPPORTED
- * where O is not on 16 bytes although cols is a multiple of 8, or the coefficients
+ * output only.  Calls with the same shape and inputs give the same bits; the same
+ * matrix in a batch of another size may round differently.  Errors: INVALID_ARG for a
+ * bad shape or NULL pointer; UNSUPPORTED where O is not on 16 bytes although cols is a multiple of 8, or the coefficients
  * let the iterates grow past what the fp16 products hold; CUDA when a launch fails. */
 tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *shape, const void *G, void *O, void *workspace,
                                  void *stream);

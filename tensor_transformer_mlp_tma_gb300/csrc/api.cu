@@ -1387,6 +1387,8 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     if (rc != TPMLP_OK) return rc;
     if (!W || (!target && s->tokens > 0)) return invalid("tpmlp_xent_backward: NULL pointer");
     if (!aligned_elt(target, 8)) return TPMLP_ERR_UNSUPPORTED;
+    if (s->tokens > 0 && ((dX && (dX == X || dX == W || dX == dW)) || (dW && (dW == W || dW == X))))
+        return invalid("tpmlp_xent_backward: an output is an input's buffer, or the other output's");
     if (!dX && !dW) return TPMLP_OK;
     int sms;
     if ((rc = device_ready(sms)) != TPMLP_OK) return rc;

@@ -97,14 +97,21 @@ def test_ill_conditioned(tp, rows, cols, kind):
 def test_any_magnitude(tp, scale):
     """The norm neither overflows nor underflows (with eps = 0 the scale cancels)."""
     for dtype in (torch.float32, torch.bfloat16):
-        G = (rand(1, 96, 160, torch.float32, seed=2) * scale).to(dtype)
-        check(run(tp, G, eps=0.0), reference(G, eps=0.0))
+        for rows, cols in ((96, 160), (300, 200)):
+            G = (rand(1, rows, cols, torch.float32, seed=2) * scale).to(dtype)
+            check(run(tp, G, eps=0.0), reference(G, eps=0.0))
+    # small and ordinary values side by side
+    G = rand(1, 160, 200, torch.float32, seed=2)
+    G[:, :80] *= scale
+    check(run(tp, G, eps=0.0), reference(G, eps=0.0))
 
 
-def test_zero_and_non_finite_matrices(tp):
-    G = rand(4, 80, 96, seed=3)
+@pytest.mark.parametrize("rows,cols", [(80, 96), (200, 264), (264, 200)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_zero_and_non_finite_matrices(tp, rows, cols, bad):
+    G = rand(4, rows, cols, seed=3)
     G[1] = 0
-    G[2, 3, 4] = float("nan")
+    G[2, 3, 4] = bad
     O = run(tp, G)
     ref = reference(G[[0, 3]])
     check(O[[0, 3]], ref)
@@ -114,16 +121,21 @@ def test_zero_and_non_finite_matrices(tp):
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
-def test_steps(tp, steps):
-    G = rand(2, 130, 200, seed=4)
+@pytest.mark.parametrize("rows,cols", [(130, 200), (100, 200), (200, 60)])
+def test_steps(tp, steps, rows, cols):
+    G = rand(2, rows, cols, seed=4)
     check(run(tp, G, steps=steps), reference(G, steps))
 
 
 def test_other_coefficients(tp):
     """The convergent cubic s (3 - s^2)/2 and a quintic that converges to 1."""
     G = rand(1, 100, 300, seed=5)
+    G2 = rand(1, 300, 160, seed=5)
     for coef in ((1.5, -0.5, 0.0), (1.875, -1.25, 0.375)):
         check(run(tp, G, steps=12, coefficients=coef), reference(G, 12, coef))
+        check(run(tp, G2, steps=12, coefficients=coef), reference(G2, 12, coef))
+    # too many steps for Q in fp16's range: the steps on X itself
+    check(run(tp, G, steps=20, coefficients=(1.875, -1.25, 0.375)), reference(G, 20, (1.875, -1.25, 0.375)))
 
 
 def test_same_bits_again_in_a_batch_and_on_another_stream(tp):
@@ -165,6 +177,29 @@ def test_captured_and_replayed(tp):
     g.replay()
     torch.cuda.synchronize()
     check(O, reference(G))
+
+
+@pytest.mark.parametrize("rows,cols", [(96, 200), (300, 200), (70, 33)])
+def test_in_place(tp, rows, cols):
+    G = rand(2, rows, cols, seed=10)
+    want = run(tp, G)
+    ctx = tp.OrthoContext(rows, cols, 2)
+    assert tp.orthogonalize(ctx, G, G) is G
+    assert torch.equal(G, want)
+
+
+def test_a_batch_past_32_bits(tp):
+    """65 matrices of 4096 x 8192, 2.2e9 elements: the last one like the first."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    n, r, c = 65, 4096, 8192
+    G = torch.empty(n, r, c, dtype=torch.bfloat16, device="cuda")
+    for i in range(n):
+        G[i] = torch.randn(r, c, device="cuda")
+    O = run(tp, G)
+    for i in (0, n - 1):  # (alone it may round differently: other tiles, other orders)
+        check(O[i:i + 1], reference(G[i:i + 1]))
 
 
 def test_empty_batch(tp):

@@ -215,8 +215,9 @@ def test_same_bits_again_and_on_another_stream(tp):
     assert torch.equal(grads["dX"], grads2["dX"]) and torch.equal(grads["dW"], grads2["dW"])
 
 
-def test_captured_and_replayed(tp):
-    X, W, y, dl = make(200, 128, 3000, seed=8)
+@pytest.mark.parametrize("T", [1, 5, 200])
+def test_captured_and_replayed(tp, T):
+    X, W, y, dl = make(T, 128, 3000, seed=8)
     ctx, loss, grads = run(tp, X, W, y, dl, piece=1024)
     out = torch.empty_like(loss)
     dX, dW = torch.empty_like(X), torch.empty_like(W)
@@ -224,12 +225,65 @@ def test_captured_and_replayed(tp):
     with torch.cuda.graph(g):
         tp.xent_forward(ctx, X, W, y, out)
         tp.xent_backward(ctx, dl, dX, dW)
-    X2, _, y2, _ = make(200, 128, 3000, seed=9)
+    X2, _, y2, _ = make(T, 128, 3000, seed=9)
     X.copy_(X2)
     y.copy_(y2)
-    g.replay()
+    for _ in range(3):
+        g.replay()
     torch.cuda.synchronize()
     check(X, W, y, dl, out, ctx.lse, {"dX": dX, "dW": dW}, reference(X, W, y, dl))
+
+
+@pytest.mark.parametrize("T,h,V", [(3, 36, 500), (50, 36, 500), (50, 33, 70)])
+def test_f32_on_any_element(tp, T, h, V):
+    """fp32 inputs and outputs that start on 4 bytes only."""
+    def shifted(x):
+        room = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+        room[1:] = x.reshape(-1)
+        return room[1:].view(x.shape)
+
+    X, W, y, dl = make(T, h, V, torch.float32, seed=T)
+    X, W = shifted(X), shifted(W)
+    ctx = tp.XentContext(T, h, V, X.dtype)
+    loss = tp.xent_forward(ctx, X, W, y)
+    dX, dW = shifted(torch.empty_like(X)), shifted(torch.empty_like(W))
+    grads = tp.xent_backward(ctx, dl, dX, dW)
+    check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
+
+
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_a_vocabulary_past_32_bits(tp, T):
+    """W and dW of 2.2e9 elements: rows at the far end count like the others."""
+    h, V = 8192, 270000
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    W = torch.empty(V, h, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, V, 30000):
+        W[i:i + 30000] = torch.randn(30000, h, generator=g, device="cuda") * 0.01
+    X = torch.randn(T, h, generator=g, device="cuda").bfloat16()
+    y = torch.full((T,), V - 1, device="cuda")
+    y[T // 2] = V - 4097
+    dl = torch.ones(T, device="cuda")
+    ctx = tp.XentContext(T, h, V, X.dtype)
+    loss = tp.xent_forward(ctx, X, W, y)
+    grads = tp.xent_backward(ctx, dl)
+    assert tp.check_device_status(ctx) == tp.OK
+    S = torch.cat([X.double() @ W[i:i + 30000].double().t() for i in range(0, V, 30000)], 1)
+    lse = torch.logsumexp(S, 1)
+    assert torch.allclose(loss.double(), lse - S.gather(1, y[:, None])[:, 0], rtol=0, atol=1e-3)
+    P = torch.exp(S - lse[:, None])
+    P.scatter_add_(1, y[:, None], -torch.ones_like(P[:, :1]))
+    u = 2.0 ** -8
+    for rows in (slice(0, 1000), slice(V - 5000, V)):
+        ref = P[:, rows].t() @ X.double()
+        # one rounding of dS and one of dW, and the logits' error of 1e-3 in p
+        tol = (2.1 * u + 2e-3) * (P[:, rows].abs().t() @ X.double().abs())
+        assert bool(((grads["dW"][rows].double() - ref).abs() <= tol + 1e-30).all())
+    dX = sum(P[:, i:i + 30000] @ W[i:i + 30000].double() for i in range(0, V, 30000))
+    assert float((grads["dX"].double() - dX).norm()) <= 2 * u * float(dX.norm())
 
 
 def test_equal_weights_leave_no_bias(tp):

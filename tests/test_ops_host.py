@@ -57,11 +57,14 @@ def test_xent_refusals(tp):
     for i in range(5):  # dX and dW (5, 6) may be NULL
         assert xbwd(tp, good, [None if k == i else FAKE for k in range(7)]) == tp.ERR_INVALID_ARG
     assert xbwd(tp, good, [FAKE] * 5 + [None, None]) == tp.OK  # nothing asked for
+    apart = [FAKE + 4096 * k for k in range(7)]
+    for i, j in ((5, 0), (5, 1), (6, 0), (6, 1), (6, 5)):  # outputs in the place of inputs, or of each other
+        assert xbwd(tp, good, [apart[j] if k == i else apart[k] for k in range(7)]) == tp.ERR_INVALID_ARG
     for i in (0, 1):  # X and W on 16 bytes
         assert xfwd(tp, good, [FAKE + 2 if k == i else FAKE for k in range(5)]) == tp.ERR_UNSUPPORTED
         assert "16-byte" in tp.last_error()
     for i in (5, 6):
-        assert xbwd(tp, good, [FAKE + 2 if k == i else FAKE for k in range(7)]) == tp.ERR_UNSUPPORTED
+        assert xbwd(tp, good, [apart[k] + (2 if k == i else 0) for k in range(7)]) == tp.ERR_UNSUPPORTED
     assert xfwd(tp, good, [FAKE, FAKE, FAKE + 4, FAKE, FAKE]) == tp.ERR_UNSUPPORTED  # int64 targets
     assert xfwd(tp, xshape(tp, h=250)) == tp.ERR_UNSUPPORTED
     assert xfwd(tp, xshape(tp, T=65535 * 64 + 1, h=8, V=8, algo=1)) == tp.ERR_UNSUPPORTED
