@@ -40,8 +40,10 @@ constexpr size_t SMEM = 3 * MAT + 1024;  // A, B, Q, and alignment
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 2 x 128 columns
 constexpr uint32_t STATUS_TIMEOUT = 4;   // TPMLP_ERR_TIMEOUT
 
-// The scales that A and B are stored with (powers of two; see kScaleX in api.cu for why).
-constexpr float SA = 8192.0f, SB = 8192.0f;
+// A is stored times 2^13: its entries are at most 3.6, and 2^-25 / 2^13 is what the two parts
+// can miss of the small ones.  B is stored as it is (at most 7.5, and 2^-25 of it is below
+// the 22 bits of its large entries), so that a product with B keeps its scale.
+constexpr float SA = 8192.0f;
 
 // 32 values of one row, columns col .. col + 31, split into the two parts of the matrix at
 // `mat`: 16-byte chunk j of a 128-byte row r sits at chunk j ^ (r & 7).
@@ -63,6 +65,9 @@ __device__ __forceinline__ void put(uint32_t mat, int row, int col, const float 
     }
 }
 
+// Descriptor of a 128-byte-swizzled K-major operand; 16 columns on are 32 bytes on.
+__device__ __forceinline__ uint64_t operand(uint32_t at) { return ptx::sdesc_sw128(at, 16, 1024); }
+
 // X Y^T for two matrices in shared memory of n columns each (n a multiple of 16), issued by one
 // thread: D[0, 128) = X_hi Y_hi^T and D[128, 256) = X_hi Y_lo^T by MMAs of 256 columns, then
 // D[128, 256) += X_lo Y_hi^T.  Their sum is the product.  (Three MMAs of 128 columns in the
@@ -71,15 +76,11 @@ __device__ __forceinline__ void put(uint32_t mat, int row, int col, const float 
 __device__ __forceinline__ void multiply(uint32_t d, uint32_t x, uint32_t y, int n) {
     constexpr uint32_t WIDE = ptx::idesc_f16_f32(PT, 2 * PT, false, false);
     const uint32_t narrow = ptx::idesc_f16_f32(PT, n, false, false);
-    for (int k = 0; k < n / 16; ++k) {
-        const uint32_t off = static_cast<uint32_t>(k >> 2) * BLOCK + static_cast<uint32_t>(k & 3) * 32u;
-        ptx::umma_f16_ss(d, ptx::sdesc_sw128(x + off, 16, 1024), ptx::sdesc_sw128(y + off, 16, 1024), WIDE, k > 0);
-    }
-    for (int k = 0; k < n / 16; ++k) {
-        const uint32_t off = static_cast<uint32_t>(k >> 2) * BLOCK + static_cast<uint32_t>(k & 3) * 32u;
-        ptx::umma_f16_ss(d + PT, ptx::sdesc_sw128(x + PART + off, 16, 1024), ptx::sdesc_sw128(y + off, 16, 1024), narrow,
-                         1u);
-    }
+    const uint64_t xh = operand(x), xl = operand(x + PART), yh = operand(y);
+    // the address field counts 16 bytes
+    const auto step = [](int k) { return static_cast<uint64_t>((k >> 2) * (BLOCK >> 4) + (k & 3) * 2); };
+    for (int k = 0; k < n / 16; ++k) ptx::umma_f16_ss(d, xh + step(k), yh + step(k), WIDE, k > 0);
+    for (int k = 0; k < n / 16; ++k) ptx::umma_f16_ss(d + PT, xl + step(k), yh + step(k), narrow, 1u);
 }
 
 __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
     // A_0: the sum of the splits' Gram matrices.  They are symmetric, so a thread reads its
     // row as a column and a warp's loads are contiguous.
     const int64_t z = blockIdx.x, P = c.P;
-    float A[32];
+    float A[32];  // times SA
 #pragma unroll
     for (int i = 0; i < 32; ++i) A[i] = 0.0f;
     const float rest = c.rest ? c.rest[z] : 1.0f;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) A[i] += src[i * P];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) A[i] = col0 + i < n ? A[i] * (c.unit * rest * rest) : 0.0f;
+        for (int i = 0; i < 32; ++i) A[i] = col0 + i < n ? A[i] * (c.unit * rest * rest * SA) : 0.0f;
     }
 
     // Each product belongs to one of two barriers; `start` runs once every thread's
@@ -160,12 +161,9 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(l[i]);
     };
     float v[32];
-    auto put_A = [&]() {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = A[i] * SA;
-        put(mA, row, col0, v);
-    };
-    put_A();
+    put(mA, row, col0, A);
+    const bool on_diagonal = (warp & 3) == (warp >> 2);  // this warp's block holds the diagonal
+    const float ca = c.b * (1.0f / SA), cs = c.c * (1.0f / (SA * SA));
     // A wait that runs out leaves `ok` false in at least one thread and raises the
     // flag that ends every other wait at once; the steps are then gone through without
     // waiting, so that all threads meet at the same barriers.
@@ -179,14 +177,16 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
         if (mine_in) {
             load(0, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = fmaf(c.c * (SB / (SA * SA)), v[i], (c.b * SB) * A[i]);
-                if (row == col0 + i) v[i] += c.a * SB;
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(cs, v[i], ca * A[i]);
+            if (on_diagonal) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (lane == i) v[i] += c.a;
             }
             put(mB, row, col0, v);
             if (k == 0) {  // Q^T = B_0
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= c.q_scale * rest / SB;
+                for (int i = 0; i < 32; ++i) v[i] *= c.q_scale * rest;
                 put(mQ, row, col0, v);
             }
         }
@@ -206,8 +206,6 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
             wait(0);
             if (mine_in) {  // B A takes A's place
                 load(0, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
                 put(mA, row, col0, v);
             }
             start([&] {
@@ -219,18 +217,14 @@ __global__ void __launch_bounds__(THREADS, 1) chain_kernel(const NsChain c) {
             wait(1);
             if (mine_in) {
                 load(1, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= 1.0f / SB;
                 put(mQ, row, col0, v);
             }
         }
         if (last) break;
         wait(0);
         if (mine_in) {
-            load(0, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) A[i] = v[i] * (1.0f / (SA * SB));
-            put_A();
+            load(0, A);
+            put(mA, row, col0, A);
         }
     }
     // Given up: once more for the products in flight, so that they do not outlive the

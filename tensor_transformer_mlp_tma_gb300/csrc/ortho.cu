@@ -55,15 +55,28 @@ __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 x) {
     return __bfloat162float(x);
 }
 
+// Sums over the block, in the same order in every block that asks.
+__device__ __forceinline__ Blue block_sum(Blue b) {
+    __shared__ Blue sh[THREADS / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        b.big += __shfl_xor_sync(0xffffffffu, b.big, o);
+        b.mid += __shfl_xor_sync(0xffffffffu, b.mid, o);
+        b.small += __shfl_xor_sync(0xffffffffu, b.small, o);
+    }
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = b;
+    __syncthreads();
+    b = sh[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) b.big += sh[w].big, b.mid += sh[w].mid, b.small += sh[w].small;
+    return b;
+}
+
 // Block sums of squares: blocks blockIdx.x = 0.. of matrix blockIdx.y, each over a
 // contiguous range.  VEC: 16-byte loads (the matrix starts and ends on 16 bytes).
 // Memory bound: one read of G.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, int64_t per_block, Blue *part) {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const T *g = G + static_cast<int64_t>(blockIdx.y) * n;
-    const int64_t beg = static_cast<int64_t>(blockIdx.x) * per_block, end = min(beg + per_block, n);
+__device__ __forceinline__ Blue sum_of_squares(const T *g, int64_t beg, int64_t end) {
     Blue b{0.0f, 0.0f, 0.0f};
     if constexpr (VEC) {
         constexpr int E = 16 / sizeof(T);
@@ -90,71 +103,45 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, in
             add(b, x);
         }
     }
-    __shared__ Blue sh[THREADS / 32];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        b.big += __shfl_xor_sync(0xffffffffu, b.big, o);
-        b.mid += __shfl_xor_sync(0xffffffffu, b.mid, o);
-        b.small += __shfl_xor_sync(0xffffffffu, b.small, o);
-    }
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = b;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < THREADS / 32; ++w) b.big += sh[w].big, b.mid += sh[w].mid, b.small += sh[w].small;
-        part[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = b;
-    }
+    return b;
 }
 
-// 2^e as a double, e within its normal range.
-__device__ __forceinline__ double pow2(int e) { return __longlong_as_double(static_cast<long long>(1023 + e) << 52); }
-__device__ __forceinline__ int exponent(double x) {
-    return static_cast<int>((__double_as_longlong(x) >> 52) & 2047) - 1023;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, int64_t per_block, Blue *part) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const T *g = G + static_cast<int64_t>(blockIdx.y) * n;
+    const int64_t beg = static_cast<int64_t>(blockIdx.x) * per_block, end = min(beg + per_block, n);
+    Blue b = sum_of_squares<T, VEC>(g, beg, end);
+    b = block_sum(b);
+    if (threadIdx.x == 0) part[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = b;
 }
 
-// scale / (|G| + eps) of one matrix from its block sums, in the same order in every
-// block that asks.  The three sums meet in 64 bits, where none of them can overflow; root
-// and quotient are taken of the fp32 significands (64-bit ones would take longer than a
-// block's share of the matrix) and their exponents apart.
-// With `power` the result is the power of two below it, and `rest` (1 to 2) is what is left.
+// scale / (|G| + eps) from the three sums.  The norm is sqrt(s) 2^h, s the sum in the
+// largest unit that has any (a sum two units down could not count): neither it nor the
+// factor then leaves fp32's range before the last step, where a factor beyond it
+// (|G| < 2^-113 with eps = 0) saturates.  fp32 throughout: 64-bit arithmetic here took
+// longer than a block's share of the matrix.
+// With POW2 the result is the power of two below it, and `rest` (1 to 2) is what is left.
 template <bool POW2>
-__device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps, float scale, float &rest) {
-    __shared__ double sh[THREADS / 32];
-    __shared__ float result, left;
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-        const Blue b = part[i];
-        s += static_cast<double>(b.mid) + static_cast<double>(b.big) * 0x1p144 + static_cast<double>(b.small) * 0x1p-144;
+__device__ __forceinline__ float inverse_norm(const Blue &b, float eps, float scale, float &rest) {
+    float s, down;  // 2^-h
+    if (b.big > 0.0f)
+        s = fmaf(b.mid, 0x1p-144f, b.big), down = 0x1p-72f;
+    else if (b.mid == 0.0f && b.small > 0.0f)
+        s = b.small, down = 0x1p72f;
+    else
+        s = fmaf(b.small, 0x1p-144f, b.mid), down = 1.0f;
+    if (b.big != b.big || b.mid != b.mid || b.small != b.small) s = nanf("");
+    float f = __fdiv_rn(scale, __fsqrt_rn(s) + eps * down) * down;
+    if (f > 0x1p127f) f = 0x1p127f;  // not NaN
+    rest = 1.0f;
+    if (POW2 && f >= 0x1p-126f) {
+        const float p = __uint_as_float(__float_as_uint(f) & 0x7F800000u);
+        rest = f / p;
+        f = p;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < THREADS / 32; ++w) s += sh[w];
-        double norm = s;  // 0, inf and NaN stay what they are
-        if (s > 0.0 && s < 0x1p1000) {
-            const int e = exponent(s) & ~1;
-            norm = static_cast<double>(sqrtf(static_cast<float>(s * pow2(-e)))) * pow2(e / 2);
-        }
-        norm += static_cast<double>(eps);
-        if (norm > 0.0 && norm < 0x1p1000) {
-            const int e = exponent(norm);
-            // beyond the fp32 range (|G| < 2^-113 with eps = 0) the factor saturates
-            result = static_cast<float>(static_cast<double>(scale / static_cast<float>(norm * pow2(-e))) *
-                                        pow2(min(-e, 113)));
-        } else {
-            result = norm > 0.0 ? 0.0f : (norm == 0.0 ? 0x1p127f : nanf(""));
-        }
-        left = 1.0f;
-        if (POW2 && result > 0x1p-126f && result <= 0x1p127f) {
-            const float p = __uint_as_float(__float_as_uint(result) & 0x7F800000u);
-            left = result / p;
-            result = p;
-        }
-    }
-    __syncthreads();
-    rest = left;
-    return result;
+    return f;
 }
 
 // hi and lo of 8 consecutive columns per thread; grid.y is the matrix.  Memory bound: G read
@@ -162,21 +149,13 @@ __device__ __forceinline__ float inverse_norm(const Blue *part, int n, float eps
 // power of two below the factor, which leaves bf16 values exact in fp16 and their
 // low part zero, and the rest of the factor goes to rest[matrix].
 template <typename T, bool VEC, bool POW2>
-__global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows, int64_t cols, int64_t P, int64_t Q,
-                                                        const Blue *part, int nparts, float eps, float scale,
-                                                        __half *hi, __half *lo, float lo_scale, float *rest) {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const int64_t z = blockIdx.y;
-    float left;
-    const float f = inverse_norm<POW2>(part + z * nparts, nparts, eps, scale, left);
-    if (POW2 && blockIdx.x == 0 && threadIdx.x == 0) rest[z] = left;
-    const T *g = G + z * rows * cols;
+__device__ __forceinline__ void scale_range(const T *g, int64_t z, int64_t rows, int64_t cols, int64_t P, int64_t Q,
+                                            float f, uint32_t first, uint32_t stride, __half *hi, __half *lo,
+                                            float lo_scale) {
     // UN loads in flight per thread before the first is used
     constexpr int UN = 4;
     const uint32_t per_row = static_cast<uint32_t>(Q / 8), total = static_cast<uint32_t>(P * Q / 8);
-    const uint32_t stride = gridDim.x * THREADS;
-    for (uint32_t i0 = blockIdx.x * THREADS + threadIdx.x; i0 < total; i0 += UN * stride) {
+    for (uint32_t i0 = first; i0 < total; i0 += UN * stride) {
         float v[UN][8];
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
@@ -212,6 +191,25 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
             if (!POW2 || lo) *reinterpret_cast<uint4 *>(lo + o) = *reinterpret_cast<const uint4 *>(l);
         }
     }
+}
+
+template <typename T, bool VEC, bool POW2>
+__global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows, int64_t cols, int64_t P, int64_t Q,
+                                                        const Blue *part, int nparts, float eps, float scale,
+                                                        __half *hi, __half *lo, float lo_scale, float *rest) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int64_t z = blockIdx.y;
+    Blue b{0.0f, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < nparts; i += THREADS) {
+        const Blue p = part[z * nparts + i];
+        b.big += p.big, b.mid += p.mid, b.small += p.small;
+    }
+    float left;
+    const float f = inverse_norm<POW2>(block_sum(b), eps, scale, left);
+    if (POW2 && blockIdx.x == 0 && threadIdx.x == 0) rest[z] = left;
+    scale_range<T, VEC, POW2>(G + z * rows * cols, z, rows, cols, P, Q, f, blockIdx.x * THREADS + threadIdx.x,
+                              gridDim.x * THREADS, hi, lo, lo_scale);
 }
 
 // The splits' sum of one 32 x 32 piece of A's lower triangle per block, stored where it is
