@@ -66,6 +66,11 @@ __host__ __device__ constexpr bool is_ns_tile(int epi) {
     return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
 }
 
+// Those of them whose epilogue reads matrices of the output's shape.
+__host__ __device__ constexpr bool is_ns_aux(int epi) {
+    return epi == EPI_NS_POLY || epi == EPI_NS_UPDATE || epi == EPI_NS_LAST;
+}
+
 // Per-CTA pipeline geometry.  CG = 1: one CTA computes a 128 x 256 tile and loads
 // all of B's 256 columns.  CG = 2: a CTA pair computes a 256 x 256 tile with
 // CTA-pair MMAs; each CTA loads its own 128 rows of A and 128 of B's columns, so
@@ -93,13 +98,15 @@ struct Cfg {
     static constexpr int B_STAGE = B_ROWS * BK * 2;
     static constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
     static constexpr bool DS = EPI_ == EPI_ATTN_DS;
-    // The Newton-Schulz products on single CTAs (few, small tiles) have two pairs of boxes,
-    // one for each of a warp's two chunks, so that no chunk waits for a store.
-    static constexpr bool SMALL = CG == 1 && TILE_N == 128 && is_ns_tile(EPI_);
-    static constexpr int STG_PER_WARP = DS ? 2 * STG_BOX_WIDE : (SMALL ? 4 * STG_BOX : 2 * STG_BOX);
+    // The Newton-Schulz products have two pairs of boxes, used in turn: a chunk's matrices are
+    // loaded into a pair ahead of it, and its results go into their place.  (On single
+    // CTAs, with two chunks per warp and tile, no chunk then waits for a store.)
+    static constexpr bool NS = is_ns_tile(EPI_) && CG == 1;
+    static constexpr int NS_SETS = CG == 1 ? 2 : 1;
+    static constexpr int STG_PER_WARP = DS ? 2 * STG_BOX_WIDE : (NS ? 4 * STG_BOX : 2 * STG_BOX);
     // dS: the K extent is one head dimension (two K blocks per tile), so fewer
     // stages make room for its wider staging boxes
-    static constexpr int STAGES = CG == 1 ? (DS ? 3 : (TILE_N == 128 ? (SMALL ? 5 : 6) : 4)) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
+    static constexpr int STAGES = CG == 1 ? (DS ? 3 : (TILE_N == 128 ? (NS ? 5 : 6) : 4)) : (TILE_N == BN ? (DS ? 5 : 6) : (TILE_N == 512 ? 4 : 8));
     static constexpr int SMEM_DYN = STAGES * STAGE_BYTES + (EPI_THREADS / 32) * STG_PER_WARP + 1024;
 };
 constexpr int MAX_STAGES = 8;
@@ -726,36 +733,47 @@ __device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const X
 }
 
 // ---- Newton-Schulz products -----------------------------------------------------
-// 32 consecutive fp16 values of a row-major matrix of pitch N (a multiple of 64)
-// fetched ahead of the chunk that uses them; rows past the end read as zero.
-struct HalfPre {
-    uint4 w[4];
-};
-__device__ __forceinline__ void half_fetch(const void *in, const Params &p, int z, int64_t row, int col, HalfPre &h) {
-    const bool ok = row < p.M && col < p.N;
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __half *>(in) +
-                                                       (static_cast<int64_t>(z) * p.M + row) * p.N + col);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) h.w[g] = ok ? src[g] : make_uint4(0u, 0u, 0u, 0u);
-}
 __device__ __forceinline__ void unpack_f16(uint32_t u, float &lo, float &hi) {
     const __half2 v = *reinterpret_cast<__half2 *>(&u);
     lo = __low2float(v);
     hi = __high2float(v);
 }
-// v = scale * v + k * h for the 32 fetched values.
-__device__ __forceinline__ void half_axpy(const HalfPre &h, float k, float (&v)[32]) {
+// v += k * (row r of a 64-byte-swizzled 32 x 32 fp16 box).
+__device__ __forceinline__ void box_axpy(uint32_t box, int r, float k, float (&v)[32]) {
+    const uint32_t row = box + static_cast<uint32_t>(r) * 64u;
+    const int x = (r >> 1) & 3;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const uint32_t u[4] = {h.w[g].x, h.w[g].y, h.w[g].z, h.w[g].w};
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+        ptx::ld_shared_v4(row + (static_cast<uint32_t>(j ^ x) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float a, b;
-            unpack_f16(u[i], a, b);
-            v[8 * g + 2 * i] = fmaf(k, a, v[8 * g + 2 * i]);
-            v[8 * g + 2 * i + 1] = fmaf(k, b, v[8 * g + 2 * i + 1]);
+            unpack_f16(w[i], a, b);
+            v[8 * j + 2 * i] = fmaf(k, a, v[8 * j + 2 * i]);
+            v[8 * j + 2 * i + 1] = fmaf(k, b, v[8 * j + 2 * i + 1]);
         }
     }
+}
+
+// Loads a chunk's matrices into a pair of boxes: A (POLY), or the high and low part of X (maps
+// tm0, tm1); parts outside the matrix read as zero.  Before that every store out of the
+// warp's boxes has been read, but the newest group's (NEWEST) out of the other pair.
+template <int EPI, bool NEWEST>
+__device__ __forceinline__ void ns_issue(const CUtensorMap *tm0, const CUtensorMap *tm1, AuxLoad &a, uint32_t box,
+                                         int col, int row0, int z, int lane) {
+    __syncwarp();
+    if (lane == 0) {
+        if constexpr (NEWEST)
+            ptx::bulk_wait_read1();
+        else
+            ptx::bulk_wait_read0();
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive_expect_tx(a.bar, EPI == EPI_NS_POLY ? STG_BOX : 2 * STG_BOX);
+        ptx::tma_load_3d(box, tm0, a.bar, col, row0, z);
+        if constexpr (EPI != EPI_NS_POLY) ptx::tma_load_3d(box + STG_BOX, tm1, a.bar, col, row0, z);
+    }
+    a.pending = true;
 }
 
 // The transpose of a 32 x 32 box of 16-bit values, lane r holding row r as 16
@@ -783,18 +801,20 @@ __device__ __forceinline__ void stage_transposed(uint32_t box, int lane, const u
 // about 22 bits).
 template <int EPI>
 __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0, const CUtensorMap *tm1,
-                                         float (&v)[32], const HalfPre &h0, const HalfPre &h1, int64_t row, int row0,
-                                         int col, int z, bool mirror, int lane, uint32_t stg, bool fresh) {
+                                         float (&v)[32], int64_t row, int row0, int col, int z, bool mirror, int lane,
+                                         uint32_t stg, bool fresh) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= p.scale;
     if constexpr (EPI == EPI_NS_POLY) {
-        half_axpy(h0, p.alpha, v);
+        box_axpy(stg, lane, p.alpha, v);
+        if (row0 == col) {  // a chunk on the diagonal (both are multiples of 32)
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (row == col + i) v[i] += p.diag;
+            for (int i = 0; i < 32; ++i)
+                if (lane == i) v[i] += p.diag;
+        }
     } else if constexpr (EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST) {
-        half_axpy(h0, p.alpha, v);
-        half_axpy(h1, p.beta, v);
+        box_axpy(stg, lane, p.alpha, v);
+        box_axpy(stg + STG_BOX, lane, p.beta, v);
     }
     uint32_t w0[16], w1[16];
     constexpr bool OUT = EPI == EPI_NS_LAST || EPI == EPI_NS_FINAL;  // the bf16 result
@@ -815,7 +835,8 @@ __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0
             w1[i] = ptx::f16x2_satfinite((v[2 * i] - a) * 2048.0f, (v[2 * i + 1] - b) * 2048.0f);
         }
     }
-    // `fresh`: the first chunk of the tile has waited for the boxes of the second too
+    // `fresh`: no store out of these boxes can be unread.  A lane reads and writes its own row
+    // of the boxes; only the transposed one is written across rows, and nothing is read there.
     if (!fresh && lane == 0) ptx::bulk_wait_read0();
     __syncwarp();
     stage_row(stg, lane, w0);
@@ -832,8 +853,8 @@ __device__ __forceinline__ void ns_chunk(const Params &p, const CUtensorMap *tm0
         if constexpr (is_sym(EPI)) {
             if (mirror) ptx::tma_store_3d(tm0, stg + STG_BOX, row0, col, z);
         }
-        ptx::bulk_commit();
     }
+    if (lane == 0) ptx::bulk_commit();  // one group per chunk, an empty one where nothing is stored
 }
 
 template <int EPI, bool HEADS = false>
@@ -1064,6 +1085,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __shared__ __align__(8) uint64_t bar_tempty[2];
     __shared__ __align__(8) uint64_t bar_done;
     __shared__ __align__(8) uint64_t bar_aux[EPI_THREADS / 32];
+    __shared__ __align__(8) uint64_t bar_ns[is_ns_aux(EPI) ? 2 * (EPI_THREADS / 32) : 1];
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_sh;
 
@@ -1092,6 +1114,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         ptx::mbar_init(ptx::smem_u32(&bar_done), 1);
         for (int w = 0; w < EPI_THREADS / 32; ++w) ptx::mbar_init(ptx::smem_u32(&bar_aux[w]), 1);
+        if constexpr (is_ns_aux(EPI))
+            for (int w = 0; w < 2 * (EPI_THREADS / 32); ++w) ptx::mbar_init(ptx::smem_u32(&bar_ns[w]), 1);
         abort_sh = 0;
         ptx::fence_mbar_init();
     }
@@ -1609,6 +1633,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float sum[FOLD ? TILE_N / 2 : 1];
         (void)sum;
         AuxLoad aux{ptx::smem_u32(&bar_aux[ew]), 0u, false};
+        AuxLoad ns_aux[2] = {{ptx::smem_u32(&bar_ns[is_ns_aux(EPI) ? 2 * ew : 0]), 0u, false},
+                             {ptx::smem_u32(&bar_ns[is_ns_aux(EPI) ? 2 * ew + 1 : 0]), 0u, false}};
+        (void)ns_aux;
         // After every lane's tcgen05.ld of the buffer has completed, one arrival
         // per warp on the leader's accumulator-empty barrier.
         auto release = [&](uint32_t buf) {
@@ -1709,14 +1736,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             XentRow xr;
             if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, xr);
             (void)xr;
-            HalfPre h0, h1;  // the Newton-Schulz epilogues' inputs, one chunk ahead
-            auto ns_fetch = [&](int col) {
-                if constexpr (EPI == EPI_NS_POLY || EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST)
-                    half_fetch(p.aux, p, zb, row, col, h0);
-                if constexpr (EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST) half_fetch(p.aux2, p, zb, row, col, h1);
-            };
-            ns_fetch(col0);
-            (void)h0, (void)h1;
+            // The first two chunks' matrices come while the accumulator is still computed.
+            if constexpr (is_ns_aux(EPI)) {
+#pragma unroll
+                for (int c = 0; c < C::NS_SETS; ++c)
+                    ns_issue<EPI, false>(&tmO2, &tmB2, ns_aux[c], stg + c * 2 * STG_BOX, col0 + c * 32, row0, zb, lane);
+            }
             for (int s = 0; s < p.nshards; ++s, ++unit) {
                 const uint32_t buf = unit & 1u, use = unit >> 1;
                 bool got = ptx::mbar_wait_scoped<false>(ptx::smem_u32(&bar_tfull[buf]), use & 1u, p.wait_ns,
@@ -1830,10 +1855,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                         if constexpr (is_ns(EPI)) {
-                            const HalfPre c0 = h0, c1 = h1;
-                            if (c < CHUNKS - 1) ns_fetch(col0 + (c + 1) * 32);
-                            ns_chunk<EPI>(p, &tmO0, &tmO1, v, c0, c1, row, row0, col0 + c * 32, zb, mb != nb, lane,
-                                          stg + (C::SMALL ? (c & 1) * 2 * STG_BOX : 0), C::SMALL && (c & 1));
+                            const uint32_t box = stg + (C::NS ? (c & 1) * 2 * STG_BOX : 0);
+                            if constexpr (is_ns_aux(EPI)) {
+                                AuxLoad &a = ns_aux[c & (C::NS_SETS - 1)];
+                                const bool landed = ptx::mbar_wait(a.bar, a.phase, p.wait_ns, &abort_sh);
+                                a.phase ^= 1u;
+                                a.pending = false;
+                                if (!__all_sync(0xffffffffu, landed) && lane == 0) record_timeout(p, &abort_sh, 6);
+                            }
+                            // (a product that reads no matrix: on single CTAs the first chunk has
+                            // waited for the second's boxes too)
+                            ns_chunk<EPI>(p, &tmO0, &tmO1, v, row, row0, col0 + c * 32, zb, mb != nb, lane, box,
+                                          is_ns_aux(EPI) || (C::NS && (c & 1)));
+                            // Two pairs: the next chunk's matrices go into the other one, whose store
+                            // has had this chunk's time.  One pair: into this chunk's place.
+                            if constexpr (is_ns_aux(EPI)) {
+                                constexpr int SETS = C::NS_SETS;
+                                const int n = (c + 1) & (SETS - 1);
+                                if (c + 1 >= SETS && c + 1 < CHUNKS)
+                                    ns_issue<EPI, SETS == 2>(&tmO2, &tmB2, ns_aux[n], stg + n * 2 * STG_BOX,
+                                                             col0 + (c + 1) * 32, row0, zb, lane);
+                            }
                         } else if constexpr (EPI == EPI_XENT_STATS) {
                             xent_stats_chunk(v, row, col0 + c * 32, p.N, p, xr);
                             if ((c & 3) == 3) xent_stats_flush(p, row, (col0 + c * 32) >> 7, xr);
@@ -1852,6 +1894,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // an H or P load still in flight (only after an abort) must land before the CTA exits
         if (aux.pending && !ptx::mbar_wait(aux.bar, aux.phase, p.wait_ns, nullptr) && lane == 0)
             record_timeout(p, &abort_sh, 7);
+        for (int c = 0; c < 2; ++c)
+            if (ns_aux[c].pending && !ptx::mbar_wait(ns_aux[c].bar, ns_aux[c].phase, p.wait_ns, nullptr) && lane == 0)
+                record_timeout(p, &abort_sh, 7);
         // every TMA store of this warp must be complete before the CTA exits
         if (lane == 0) ptx::bulk_wait0();
         __syncwarp();
@@ -2082,6 +2127,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
                           : make_map(&mb, g.b, g.N, g.K, BK, any_n ? any_n / CG : C::B_ROWS, sw, nib, bf, g.ldb, g.b_part));
     if (WIDE && !B_MN && okb) okb = make_map(&mb2, g.b, g.N, g.K, BK, C::B_ROWS / 2, sw, ni, bf, g.ldb, g.b_part);
     if (!WIDE || (B_MN && !b4)) mb2 = mb;  // unused, or the per-block maps serve both widths
+    if constexpr (EPI == EPI_NS_UPDATE || EPI == EPI_NS_LAST) {
+        // X's low part, a 32 x 32 box per chunk like the output's
+        if (!make_map(&mb2, g.aux2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, nb)) return cudaErrorInvalidValue;
+    }
     if (!oka || !okb) return cudaErrorInvalidValue;
     // Output maps: [M, N] row-major, 32 x 32 boxes, 64-byte swizzle (matches stage_row).
     // Bias + GeLU writes H (optional) and Y; GeLU' reads H through the second map;
@@ -2096,6 +2145,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
                                             : ((EPI == EPI_DGELU || EPI == EPI_ATTN_DS) ? g.aux
                                                : (EPI == EPI_NS_UPDATE ? g.out1 : o0));
     const void *o2 = (EPI == EPI_DGELU && g.out1) ? g.out1 : o0;
+    constexpr bool NS_AUX = is_ns_aux(EPI);  // the third map is A's or X's high part
     const CUtensorMapDataType odt =
         EPI == EPI_ATTN_SCORE ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                               : (is_out32(EPI) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
@@ -2127,6 +2177,8 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
         if (o1 != o0 && !make_map(&mo1, o1, orows, ocols, obox, 32, so, no, odt, g.ldo)) return cudaErrorInvalidValue;
         if (bias_tile) {
             if (!make_map(&mo2, g.ones, 64, 64, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, 1)) return cudaErrorInvalidValue;
+        } else if (NS_AUX) {
+            if (!make_map(&mo2, g.aux, g.M, g.N, 32, 32, so, nb)) return cudaErrorInvalidValue;
         } else if (o2 != o0 && !make_map(&mo2, o2, orows, ocols, obox, 32, so, no, odt, g.ldo)) {
             return cudaErrorInvalidValue;
         }
