@@ -1111,7 +1111,8 @@ int64_t xent_piece(const tpmlp_xent_shape *s) {
 // rate.  fp32 operands also bound the range to 2048: the tensor core cuts off
 // (does not round) the accumulator at every 16-element step, 2^-24 on average,
 // and 128 such steps stay below the fp32 result's own 1e-6.
-// Measured at T = 1001, h = 1000, V = 30011 (dX): see the table of results.
+// Measured: dX of T = 1001, h = 1000, V = 30011 (16 tiles of 256 x 256) 173 us in one range,
+// 54 + 8 us split.
 struct Split {
     int n;
     int64_t len;
@@ -1173,7 +1174,7 @@ struct XentLayout {
 // path) | fp32 dX, per split | fp32 dW of one piece, per split.
 XentLayout xent_layout(const tpmlp_xent_shape *s) {
     XentLayout L;
-    const size_t T = static_cast<size_t>(s->tokens), h = static_cast<size_t>(s->hidden);
+    const size_t T = static_cast<size_t>(s->tokens);
     const size_t V = static_cast<size_t>(s->vocab);
     const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
     L.piece = xent_piece(s);
@@ -1210,7 +1211,6 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
     const bool dx_direct = tc ? L.dx.n == 1 && (f32 ? !odd : L.pieces == 1) : f32 || L.pieces == 1;
     L.acc = region(dx_direct && !f32 ? 0 : static_cast<size_t>(L.dx.n) * T * ldo * 4);
     L.dwacc = region(tc && (L.dw.n > 1 || f32) ? static_cast<size_t>(L.dw.n) * piece * ldo * 4 : 0);
-    (void)h;
     L.total = off;
     return L;
 }

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowAr
 // streams its share of W's rows, FEW_ROWS at a time, 512 bytes of each per load, and keeps its
 // own online softmax.  A product of so few rows would waste the tensor core's tile, and
 // its copies of 128-byte pieces of many rows read W at 3.2 to 3.6 TB/s (T = 1 to 8).
-// Bound by W's bytes.
+// Bound by W's bytes: h = 4096, V = 32768 in 47 us (5.7 TB/s) at T = 1, h = 8192, V = 50000
+// at 6.4 TB/s.
 constexpr int FEW_THREADS = 512, FEW_ROWS = 4;
 
 // EC consecutive elements as fp32 pairs.
@@ -249,6 +250,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, co
 // places; no shuffling, no staging of W.  The warps of a block share a group of 16
 // rows by slices of k and add their sums in order through shared memory, so that the
 // blocks' shares of the vocabulary stay even; two buffers let one barrier per group do.
+// 51 us (5.3 TB/s) for T = 8, h = 4096, V = 32768, where one FMA per weight and token took 78.
+// With 16 or 32 tokens the same kernel was no faster than the tcgen05 tiles.
 constexpr int SLIM_ROWS = 16;
 
 template <int SLIM_WARPS>
