@@ -1682,6 +1682,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 break;
             }
             ptx::tc_fence_after();
+            if constexpr (is_xent(EPI)) {
+                // A half's four chunks are taken into registers together, so that the next
+                // tile's MMAs wait for four loads and not for four finished chunks.
+                for (int hh = qa >> 2; hh < qb >> 2 && ok; ++hh) {
+                    const uint32_t taddr = tmem_base + lane_off + hh * MMA_N + half * 128;
+                    if (!dbg_ok(hh * MMA_N + half * 128 + 128 <= int(TMEM_COLS) && stg + C::STG_PER_WARP <= stg_end &&
+                                    row0 % 32 == 0,
+                                p, &abort_sh, 0x0A03u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t r[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(taddr + 32 * c, r[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) ptx::tmem_ld_wait(r[c]);
+                    release(static_cast<uint32_t>(hh));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = col0 + 128 * hh + 32 * c;
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[c][i]);
+                        if constexpr (EPI == EPI_XENT_STATS) {
+                            xent_stats_chunk(v, row, col, p.N, p, xr);
+                            if (c == 3) xent_stats_flush(p, row, col >> 7, xr);
+                        } else {
+                            finish_chunk<EPI, false>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col, zb, lane, stg, &aux, -1,
+                                                     row0, &abort_sh, nullptr, &xr);
+                        }
+                    }
+                }
+                continue;
+            }
             for (int q = qa; q < qb; ++q) {
                 const uint32_t taddr = tmem_base + lane_off + (q >> 2) * MMA_N + half * 128 + (q & 3) * 32;
                 if (!dbg_ok((q >> 2) * MMA_N + half * 128 + (q & 3) * 32 + 32 <= int(TMEM_COLS) &&
@@ -1708,14 +1742,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (rank == 0 && quarter == 0 && lane == 0) store_bias_grad(p, col0 + 32 * q, v);
                     continue;
                 }
-                if constexpr (EPI == EPI_XENT_STATS) {
-                    xent_stats_chunk(v, row, col0 + 32 * q, p.N, p, xr);
-                    if ((q & 3) == 3) xent_stats_flush(p, row, (col0 + 32 * q) >> 7, xr);
-                    continue;
-                }
                 finish_chunk<EPI, false>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + 32 * q, zb, lane, stg, &aux,
                                          q + 1 < qb ? col0 + 32 * (q + 1) : -1, row0, &abort_sh,
-                                         EPI == EPI_BIAS_GELU ? &bias_cur : nullptr, is_xent(EPI) ? &xr : nullptr);
+                                         EPI == EPI_BIAS_GELU ? &bias_cur : nullptr);
             }
         }
         } else {
