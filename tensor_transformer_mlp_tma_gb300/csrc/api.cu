@@ -1170,8 +1170,9 @@ struct XentLayout {
     size_t part, target_logit, xp, wp, ds, logits, acc, dwacc, total;
 };
 
-// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | three bf16 parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA
-// path) | fp32 dX, per split | fp32 dW of one piece, per split.
+// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | three bf16
+// parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA path) | fp32
+// dX, per split | fp32 dW of one piece, per split.
 XentLayout xent_layout(const tpmlp_xent_shape *s) {
     XentLayout L;
     const size_t T = static_cast<size_t>(s->tokens);

@@ -85,6 +85,20 @@ def test_against_64_bits(tp, batch, rows, cols, dtype):
     check(run(tp, G), reference(G))
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(tp, seed):
+    import math
+    import random
+    r = random.Random(2000 + seed)
+    size = lambda lo, hi: int(round(math.exp(r.uniform(math.log(lo), math.log(hi)))))
+    rows, cols, batch = size(1, 3000), size(1, 3000), size(1, 12)
+    while batch * rows * cols > 4_000_000:
+        rows, cols = (rows + 1) // 2, (cols + 1) // 2
+    G = rand(batch, rows, cols, r.choice((torch.float32, torch.bfloat16)), seed=seed,
+             kind=r.choice(("gauss", "lowrank", "mean")))
+    check(run(tp, G), reference(G))
+
+
 @pytest.mark.parametrize("kind", ["lowrank", "mean"])
 @pytest.mark.parametrize("rows,cols", [(256, 640), (640, 256), (384, 384)])
 def test_ill_conditioned(tp, rows, cols, kind):
