@@ -1549,6 +1549,13 @@ bool ortho_valid(const tpmlp_ortho_shape *s) {
     return tiles_fit(s->rows + 64, s->cols + 64, s->batch);
 }
 
+// K elements per accumulation of the Gram product that the chain starts from.  The tensor
+// core cuts its accumulator off at every step of 16 (three times for two parts): a relative
+// error of A_0 of about 2^-25 per step, which counts against the smallest eigenvalue's share
+// of the largest.  With 1024 at once, matrices with one singular value 200 times the others
+// came out with errors of 5e-3 to 8e-3; the ranges' sums are added in fp32.
+int64_t gram_range(const tpmlp_ortho_shape *s) { return s->dtype == TPMLP_F32 ? 128 : 256; }
+
 struct OrthoLayout {
     int64_t P, Q, p;
     bool wide;   // rows <= cols: A = X X^T, else A = X^T X
@@ -1582,9 +1589,9 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
     const size_t x = n * static_cast<size_t>(L.P) * L.Q * 2, a = n * static_cast<size_t>(L.p) * L.p * 2;
     if (L.chain) {
         // one tile per matrix: split K until the SMs have one each, 256 or more at a time
-        const int64_t K = L.wide ? L.Q : L.P;
+        const int64_t K = L.wide ? L.Q : L.P, range = gram_range(s);
         const int64_t want = std::min<int64_t>(152 / std::max<int64_t>(1, s->batch), (K + 255) / 256);
-        L.split_len = (K / std::max<int64_t>(1, want) + 63) / 64 * 64;
+        L.split_len = (K / std::max<int64_t>(1, want) + range - 1) / range * range;
         L.splits = static_cast<int>((K + L.split_len - 1) / L.split_len);
         const bool f32 = s->dtype == TPMLP_F32;  // bf16 values need no low part (see OrthoStart::rest)
         L.hi[0] = region(f32 ? 2 * x : x);
@@ -1693,7 +1700,8 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
     };
     if (L.chain) {
         GemmArgs g = product(ws + L.hi[0], !L.wide, ws + L.hi[0], !L.wide, L.p, L.p, L.wide ? L.Q : L.P, ws + L.A);
-        g.ksplit = L.splits, g.kshard = L.split_len;
+        g.ksplit = L.splits, g.kshard = gram_range(s);
+        g.nshards = static_cast<int>(L.split_len / g.kshard);
         g.x_single = single;
         e = launch("ortho_gram32", tpmlp::EPI_NS_GRAM32, g);
         if (e != cudaSuccess) return from_cuda(e);

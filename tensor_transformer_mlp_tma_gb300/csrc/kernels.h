@@ -37,7 +37,7 @@ enum Epi : int {
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
     EPI_STORE_UNIT = 19, // out = acc * unit (see xent_unit)                 -- dX and dW of bf16
     EPI_NS_GRAMS = 18,  // A in fp32, lower triangle, over K in ksplit ranges -- X X^T
-    EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts               -- X X^T
+    EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts, K in nshards ranges added up in fp32 -- X X^T
     EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
     EPI_XENT_FOLD = 17, // XENT_STATS over K in nshards ranges, added up in fp32
     EPI_XENT_GRAD3 = 14, // XENT_GRAD for fp32: dS as three bf16 parts      -- X W^T -> dS

@@ -1058,7 +1058,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const Params p) {
     using C = Cfg<CG, TILE_N, EPI>;
     constexpr bool PAIR = CG == 2;
-    constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD);
+    constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32);
     constexpr bool WIDE = TILE_N == 512;
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
     constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
@@ -2242,7 +2242,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.matrices = static_cast<int>(nb);
     p.kb_seg = p.kb_per_shard;
     p.pairs = SEG && g.parts > 1 ? 6 : 1;
-    if (EPI == EPI_XENT_FOLD)
+    if (EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32)
         p.kb_seg = p.nshards * p.kb_per_shard / p.pairs;
     else
         p.kb_per_shard *= p.pairs;
