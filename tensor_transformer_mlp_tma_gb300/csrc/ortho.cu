@@ -145,9 +145,10 @@ __device__ __forceinline__ float inverse_norm(const Blue &b, float eps, float sc
 }
 
 // hi and lo of 8 consecutive columns per thread; grid.y is the matrix.  Memory bound: G read
-// once more, 4 bytes written per element (4096 x 16384: 86 us, 4.7 TB/s), or 2: with POW2 (lo may then be null) X is scaled by the
-// power of two below the factor, which leaves bf16 values exact in fp16 and their
-// low part zero, and the rest of the factor goes to rest[matrix].
+// once more, 4 bytes written per element (4096 x 16384: 86 us, 4.7 TB/s), or 2: with POW2
+// (lo may then be null) X is scaled by the power of two below the factor, which leaves
+// bf16 values exact in fp16 and their low part zero, and the rest of the factor goes to
+// rest[matrix].
 template <typename T, bool VEC, bool POW2>
 __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                                         const Blue *part, int nparts, float eps, float scale,
