@@ -1358,8 +1358,11 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
         const StatsTile &t = c.L.stats;
         if (t.tile_n < 512) {
             g.tile_n = t.tile_n;
-            g.nshards = static_cast<int>(t.ranges * (c.parts() ? 6 : 1));
-            g.kshard = t.range;
+            // fp32: the six products one after the other, each in its ranges; where one range
+            // holds all of K, one accumulation takes the six (the five small ones first)
+            const int pairs = c.parts() ? 6 : 1;
+            g.nshards = t.ranges == 1 ? 1 : static_cast<int>(t.ranges) * pairs;
+            g.kshard = t.ranges == 1 ? t.range * pairs : t.range;
         }
         e = c.launch("xent_stats", t.tile_n < 512 ? tpmlp::EPI_XENT_FOLD : tpmlp::EPI_XENT_STATS, g);
         if (e != cudaSuccess) return from_cuda(e);
