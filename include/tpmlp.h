@@ -331,7 +331,8 @@ size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
 
 /* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
  * written for every token, ignored ones too.  bf16 runs on the tensor cores with
- * fp32 accumulation and statistics; the logits are not rounded.  A logit of NaN or
+ * fp32 accumulation and statistics; the logits are not rounded.  fp32 runs there too, each
+ * operand as the sum of three bf16 numbers (24 bits, and 2^-133 at the least).  A logit of NaN or
  * +inf makes its token's loss and lse non-finite, no other token's.  A target that
  * is neither ignore_index nor in [0, V) is reported as TPMLP_ERR_INVALID_ARG in the
  * status word (detail: the token) and treated as ignored.

@@ -384,32 +384,54 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int sp
 
 // x = p0 + p1 + p2 in bf16, each the rest before it rounded to eight bits, so that the
 // three together hold all 24 (the largest fp32 numbers, which would round up to
-// infinity, are cut off instead; an infinite one has parts inf, 0, 0).  Two matrices in one launch, four
-// columns per thread.  Memory bound: 4 bytes read, 6 written per element.
+// infinity, are cut off instead; an infinite one has parts inf, 0, 0).  Two matrices in one
+// launch, a warp per row, four columns per lane.  Memory bound: 4 bytes read, 6 written
+// per element.
+__device__ __forceinline__ void split3(const Split3 &m, int64_t r, int lane) {
+    const float *in = m.in + r * m.cols;
+    const bool vec = m.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(m.in) & 15) == 0;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(m.out) + r * m.ld;
+    const int64_t all = m.rows * m.ld;
+#pragma unroll 4
+    for (int64_t c = 4 * lane; c < m.ld; c += 128) {
+        float v[4];
+        if (vec && c < m.cols) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(in + c));
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = c + j < m.cols ? in[c + j] : 0.0f;
+        }
+        // numbers that no rounding makes infinite (all but the very largest, inf and NaN)
+        const bool ordinary = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))) < 0x1p127f &&
+                              v[0] == v[0] && v[1] == v[1] && v[2] == v[2] && v[3] == v[3];
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+            if (!ordinary) {
+                __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (__hisinf(p[j]) && !isinf(v[j])) p[j] = __float2bfloat16_rz(v[j]);
+            }
+            const float2 lo = __bfloat1622float2(h[0]), up = __bfloat1622float2(h[1]);
+            const float w[4] = {lo.x, lo.y, up.x, up.y};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = !ordinary && isinf(v[j]) ? 0.0f : v[j] - w[j];
+            *reinterpret_cast<uint2 *>(out + part * all + c) = *reinterpret_cast<const uint2 *>(h);
+        }
+    }
+}
 __global__ void __launch_bounds__(256) split3_kernel(const Split3 a, const Split3 b) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t na = a.rows * a.ld, n = na + b.rows * b.ld;
-    for (int64_t k = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; k < n;
-         k += static_cast<int64_t>(gridDim.x) * 1024) {
-        const Split3 &m = k < na ? a : b;
-        const int64_t i = k < na ? k : k - na, all = m.rows * m.ld;
-        const int64_t r = i / m.ld, c = i - r * m.ld;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = c + j < m.cols ? m.in[r * m.cols + c + j] : 0.0f;
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-            __nv_bfloat16 h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = __float2bfloat16_rn(v[j]);
-                if (__hisinf(h[j]) && !isinf(v[j])) h[j] = __float2bfloat16_rz(v[j]);
-                v[j] = isinf(v[j]) ? 0.0f : v[j] - __bfloat162float(h[j]);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(m.out) + part * all + i) =
-                *reinterpret_cast<const uint2 *>(h);
-        }
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows + b.rows;
+         r += static_cast<int64_t>(gridDim.x) * 8) {
+        if (r < a.rows)
+            split3(a, r, lane);
+        else
+            split3(b, r - a.rows, lane);
     }
 }
 
@@ -554,8 +576,8 @@ cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t
 }
 
 cudaError_t launch_split3(const Split3 &a, const Split3 &b, cudaStream_t st) {
-    const int64_t n = a.rows * a.ld + b.rows * b.ld;
-    return launch_pdl(xent::split3_kernel, dim3(static_cast<unsigned>(xent::blocks_for(n / 4))), 256, 0, st, a, b);
+    const int64_t blocks = xent::blocks_for((a.rows + b.rows) * 32);
+    return launch_pdl(xent::split3_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, st, a, b);
 }
 
 cudaError_t launch_xent_piece_stats(const RowArgs &a, const float *logits, int64_t n, int64_t col0, float2 *part,

@@ -5,6 +5,11 @@ Tolerances, per element and derived from the arithmetic:
   (h + 8) 2^-23 sum_k |x_k w_k| (2^-23, not 2^-24, allows an accumulator that truncates);
   call the largest of a token e.  loss and lse move by at most 2e and e, plus 2^-20 of
   their terms for the exponentials, the join and the logarithm;
+- an fp32 operand a is a sum of three bf16 numbers, whose steps are 2^-133 at the least: where
+  that cuts a short (below 2^-110) its sum is off by at most half a step, 2^-134.  With
+  x + d and w + f for x and w, x w moves by |d w| + |x f| + |d f|, so a logit by at most
+  2^-134 (sum |x_k| + sum |w_k| + h 2^-134), which e takes in (for sums up to 2^100 it is under
+  2^-33, nothing);
 - dS = (p - 1[y]) g: p moves by a factor of at most exp(2e) (1 + 2^-20), then one rounding
   to the dtype, u = eps/2 relative;
 - a probability below 2^-126, the smallest normal fp32 number, comes out of the exponential
@@ -61,6 +66,8 @@ def check(X, W, y, dl, loss, lse, grads, ref):
     u = torch.finfo(dt).eps / 2
     Xa, Wa = X.double().abs(), W.double().abs()
     e = (h + 8) * 2.0 ** -23 * (Xa @ Wa.t()).amax(1)
+    if dt == torch.float32:
+        e = e + 2.0 ** -134 * (Xa.sum(1) + Wa.sum(1).amax() + h * 2.0 ** -134)
     small = 2.0 ** -20 * (ref["S"].abs().amax(1) + math.log(V) + 1)
     assert bool(((lse.double() - ref["lse"]).abs() <= e + small).all())
     assert bool(((loss.double() - ref["loss"]).abs() <= 2 * e + 2 * small).all())
@@ -250,6 +257,17 @@ def test_captured_and_replayed(tp, T):
         g.replay()
     torch.cuda.synchronize()
     check(X, W, y, dl, out, ctx.lse, {"dX": dX, "dW": dW}, reference(X, W, y, dl))
+
+
+def test_f32_at_the_end_of_its_range(tp):
+    """The largest fp32 numbers do not become infinite in bf16 parts: X next to 2^128 times W small."""
+    X, W, y, dl = make(40, 64, 200, torch.float32, seed=14)
+    X[:, 0], W[:, 0] = torch.finfo(torch.float32).max, W[:, 0] * 1e-38
+    X[3, 5], W[:, 5] = -torch.finfo(torch.float32).max, 0.0
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    ref = reference(X, W, y, dl)
+    check(X, W, y, dl, loss, ctx.lse, {"dX": grads["dX"], "dW": None}, ref)
+    assert bool(torch.isfinite(grads["dW"][:, 1:5]).all())
 
 
 @pytest.mark.parametrize("T,h,V", [(3, 36, 500), (50, 36, 500), (50, 33, 70)])
