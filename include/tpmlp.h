@@ -336,8 +336,8 @@ size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
  * +inf makes its token's loss and lse non-finite, no other token's.  A target that
  * is neither ignore_index nor in [0, V) is reported as TPMLP_ERR_INVALID_ARG in the
  * status word (detail: the token) and treated as ignored.
- * Errors: INVALID_ARG for a bad shape or a NULL pointer (token arrays may be NULL
- * with T = 0); UNSUPPORTED for bf16 with h not a multiple of 8 or X or W not on 16
+ * Errors: INVALID_ARG for a bad shape, a NULL pointer (token arrays may be NULL
+ * with T = 0) or an output that overlaps an input or another output; UNSUPPORTED for bf16 with h not a multiple of 8 or X or W not on 16
  * bytes, and beyond 65535 * 64 tokens or vocabulary rows on the FFMA path; CUDA when
  * a launch fails. */
 tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
@@ -348,8 +348,7 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, co
  * frozen body).  In bf16 dS is rounded (in units of dloss[0] where that is a
  * number of ordinary size) before the two products, in fp32 it is not; dX is summed
  * over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
- * Results are bit-identical from call to call.  No output may overlap an input or the
- * other output (the same pointer is refused).  Errors as the forward. */
+ * Results are bit-identical from call to call.  Errors as the forward. */
 tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
                                  const float *lse, const float *dloss, void *dX, void *dW, void *workspace,
                                  void *stream);

@@ -1247,6 +1247,25 @@ tpmlp_status xent_check(const tpmlp_xent_shape *s, const char *who, std::initial
     return TPMLP_OK;
 }
 
+struct Buffer {
+    const void *p;
+    int64_t bytes;
+};
+// Whether an output's bytes are also an input's, or another output's.
+bool outputs_overlap(std::initializer_list<Buffer> outputs, std::initializer_list<Buffer> inputs) {
+    const auto shared = [](const Buffer &x, const Buffer &y) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+        return a && b && a < b + static_cast<uintptr_t>(y.bytes) && b < a + static_cast<uintptr_t>(x.bytes);
+    };
+    for (const Buffer *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Buffer &i : inputs)
+            if (shared(*o, i)) return true;
+        for (const Buffer *q = o + 1; q != outputs.end(); ++q)
+            if (shared(*o, *q)) return true;
+    }
+    return false;
+}
+
 // SMs of the current device, or the error to return.
 tpmlp_status device_ready(int &sms) {
     sms = num_sms_current();
@@ -1339,6 +1358,10 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
     if (!W || (!target && s->tokens > 0)) return invalid("tpmlp_xent_forward: NULL pointer");
     if (!aligned_elt(target, 8)) return TPMLP_ERR_UNSUPPORTED;
     if (s->tokens == 0) return TPMLP_OK;
+    const int64_t T = s->tokens, esz = s->dtype == TPMLP_BF16 ? 2 : 4;
+    if (outputs_overlap({{loss, 4 * T}, {lse, 4 * T}},
+                        {{X, T * s->hidden * esz}, {W, s->vocab * s->hidden * esz}, {target, 8 * T}}))
+        return invalid("tpmlp_xent_forward: an output overlaps an input or the other output");
     int sms;
     if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
     const XentCall c(s, target, workspace, sms, stream);
@@ -1391,22 +1414,22 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     if (rc != TPMLP_OK) return rc;
     if (!W || (!target && s->tokens > 0)) return invalid("tpmlp_xent_backward: NULL pointer");
     if (!aligned_elt(target, 8)) return TPMLP_ERR_UNSUPPORTED;
-    if (s->tokens > 0 && ((dX && (dX == X || dX == W || dX == dW)) || (dW && (dW == W || dW == X))))
-        return invalid("tpmlp_xent_backward: an output is an input's buffer, or the other output's");
+    const int64_t T = s->tokens, h = s->hidden, esz = s->dtype == TPMLP_BF16 ? 2 : 4;
+    if (T > 0 && outputs_overlap({{dX, T * h * esz}, {dW, s->vocab * h * esz}},
+                                 {{X, T * h * esz}, {W, s->vocab * h * esz}, {target, 8 * T}, {lse, 4 * T}, {dloss, 4 * T}}))
+        return invalid("tpmlp_xent_backward: an output overlaps an input or the other output");
     if (!dX && !dW) return TPMLP_OK;
     int sms;
     if ((rc = device_ready(sms)) != TPMLP_OK) return rc;
     cudaError_t e;
     if (s->tokens == 0) {
         if (!dW) return TPMLP_OK;
-        const size_t bytes = static_cast<size_t>(s->vocab) * s->hidden * (s->dtype == TPMLP_BF16 ? 2 : 4);
-        return from_cuda(cudaMemsetAsync(dW, 0, bytes, static_cast<cudaStream_t>(stream)));
+        return from_cuda(cudaMemsetAsync(dW, 0, static_cast<size_t>(s->vocab * h * esz), static_cast<cudaStream_t>(stream)));
     }
     const XentCall c(s, target, workspace, sms, stream);
     const bool tc = xent_tc(s), f32 = s->dtype == TPMLP_F32;
     if ((e = c.split_operands(X, W)) != cudaSuccess) return from_cuda(e);
     uint8_t *ds = c.ws + c.L.ds;
-    const int64_t T = s->tokens, h = s->hidden;
     // dX is summed over the pieces (and the splits of each) in fp32: in place for fp32,
     // in the workspace for bf16, and not at all when one piece and one range hold it all.
     const bool stores = !f32 || (h % 4 == 0 && aligned16(dX));  // fp32 rows that TMA can store

@@ -72,6 +72,24 @@ def test_xent_refusals(tp):
     assert xfwd(tp, xshape(tp, T=0), [None, FAKE, None, None, None]) == tp.OK
 
 
+def test_xent_outputs_overlap_nothing(tp):
+    """T = 64, h = 256, V = 1000 in bf16: X 32768 bytes, W 512000, targets 512, fp32 rows 256.  An
+    output one byte range into any other buffer is refused, from below and from above."""
+    good = xshape(tp)
+    size = {"X": 32768, "W": 512000, "target": 512, "loss": 256, "lse": 256, "dloss": 256, "dX": 32768, "dW": 512000}
+    at = {n: (k + 1) << 20 for k, n in enumerate(size)}
+    for call, names, outs in ((xfwd, ("X", "W", "target", "loss", "lse"), ("loss", "lse")),
+                              (xbwd, ("X", "W", "target", "lse", "dloss", "dX", "dW"), ("dX", "dW"))):
+        for out in outs:
+            for other in names:
+                if other == out:
+                    continue
+                for where in (at[other] + size[other] - 16, at[other] - size[out] + 16):
+                    p = [where if n == out else at[n] for n in names]
+                    assert call(tp, good, p) == tp.ERR_INVALID_ARG, (out, other)
+                    assert "overlaps" in tp.last_error()
+
+
 def oshape(tp, batch=2, rows=64, cols=128, steps=5, dtype=None, coef=(3.4445, -4.7750, 2.0315), eps=1e-7):
     return tp.OrthoShape(batch, rows, cols, steps, tp.BF16 if dtype is None else dtype, *coef, eps)
 
