@@ -1136,10 +1136,12 @@ Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
 
 // The forward product's tiles.  512: 256 x 512 with the whole K in one accumulator.
 // Otherwise 256 x tile_n with K in ranges that the epilogue adds up in fp32: the tensor
-// core cuts the accumulator off (does not round) at every step of 16 products, an error of
-// about 2.5e-10 h of the loss, so that beyond 4096 products it would pass 1e-6.
-// On 256 x 256 tiles and in ranges the product is 8 to 12% slower (T = 8192, h = 4096,
-// V = 65536: 2.10 against 2.27 ms).  Where there are few tiles the ranges cost nothing,
+// core cuts the accumulator off (does not round) at every step of 16 products; the mean of
+// that is put back (xent_regain), the rest grows with the range: a relative error of the loss
+// of 1e-7 at 1000 products, 2.1e-7 at 2048, 5.0e-7 at 4096 (T = 8192, V = 2500 to 3000; before
+// the mean was put back 4.6e-7, 8.0e-7, 1.4e-6), so that at 8192 it would pass 1e-6.
+// On 256 x 256 tiles and in ranges the product is 9% slower (T = 8192, h = 4096,
+// V = 65536: 2.38 against 2.59 ms, power-bound).  Where there are few tiles the ranges cost nothing,
 // and narrower tiles divide the vocabulary evenly among the 76 units; fp32 operands
 // want the precision and take short ranges always.
 struct StatsTile {
@@ -1158,7 +1160,7 @@ StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
         const int64_t waves = (tiles + units - 1) / units, per = std::max<int64_t>(1, waves * units / m);
         tile_n = std::min<int64_t>(256, ((V + per - 1) / per + 31) / 32 * 32);
     }
-    const int64_t longest = f32 ? 512 : (few ? 1024 : 2816);
+    const int64_t longest = f32 ? 512 : (few ? 1024 : 4096);
     const int64_t ranges = (h + longest - 1) / longest;
     return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64};
 }
@@ -1318,6 +1320,7 @@ struct XentCall {
             set_parts(g, s->tokens * L.hp, s->vocab * L.hp);
         }
         g.target = rows.target, g.ignore_index = s->ignore_index, g.col0 = v0;
+        g.regain = tpmlp::xent_regain(s->hidden);
         return g;
     }
     cudaError_t launch(const char *name, Epi epi, GemmArgs &g) const {
@@ -1381,6 +1384,7 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
         const StatsTile &t = c.L.stats;
         if (t.tile_n < 512) {
             g.tile_n = t.tile_n;
+            g.regain = tpmlp::xent_regain(t.range);
             // fp32: the six products one after the other, each in its ranges; where one range
             // holds all of K, one accumulation takes the six (the five small ones first)
             const int pairs = c.parts() ? 6 : 1;

@@ -181,6 +181,7 @@ struct Params {
     float2 *part;
     float *target_logit;
     const float *row_lse, *dloss;
+    float regain, regain_log2e;  // the logits' factor (xent_regain), and log2(e) of it
     long long vocab;
     int accumulate;  // EPI_ACC32
     // K of the cross entropy's products: kb_seg k-blocks per pair of operand parts (one
@@ -684,7 +685,8 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, Xent
 
 // One pass of the online softmax over 32 logits: the running maximum moves to m',
 // the running sum is scaled by exp(m - m') and the 32 exponentials are added, all
-// in fp32.  Columns from `end` on count as -inf.
+// in fp32.  Columns from `end` on count as -inf.  Logits and maximum are the accumulator's;
+// what leaves (flush, the target's logit) and the exponents have the factor `regain`.
 __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, int col, int end, const Params &p,
                                                  XentRow &x) {
     if (col >= end) return;
@@ -698,10 +700,10 @@ __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, in
     for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
     const float m = fmaxf(x.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
     // all logits so far -inf: exp(-inf - 0) = 0 instead of exp(-inf + inf)
-    const float base = m == -INFINITY ? 0.0f : m * kLog2e;
-    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
+    const float base = m == -INFINITY ? 0.0f : m * p.regain_log2e;
+    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, p.regain_log2e, -base)), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], kLog2e, -base));
+    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], p.regain_log2e, -base));
     x.m = m;
     x.s = (s[0] + s[1]) + (s[2] + s[3]);
     // the target's logit, where it is one of these columns (few warps at a time)
@@ -712,11 +714,11 @@ __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, in
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (at == i) z = v[i];
-        if (here && row < p.M) p.target_logit[row] = z;
+        if (here && row < p.M) p.target_logit[row] = z * p.regain;
     }
 }
 __device__ __forceinline__ void xent_stats_flush(const Params &p, int64_t row, int group, XentRow &x) {
-    if (row < p.M) p.part[static_cast<int64_t>(group) * p.M + row] = make_float2(x.m, x.s);
+    if (row < p.M) p.part[static_cast<int64_t>(group) * p.M + row] = make_float2(x.m * p.regain, x.s);
     x.m = -INFINITY, x.s = 0.0f;
 }
 
@@ -724,7 +726,7 @@ __device__ __forceinline__ void xent_stats_flush(const Params &p, int64_t row, i
 // the single rounding to bf16.  g = 0 gives exact zeros, whatever the logits.  The
 // difference S - lse is taken before the factor log2(e): where p is large it is
 // small, and its rounding too.
-__device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const XentRow &x) {
+__device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const Params &p, const XentRow &x) {
     const int at = x.tcol - col;
     if (x.g == 0.0f) {
 #pragma unroll
@@ -732,7 +734,7 @@ __device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const X
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float pr = ptx::ex2_approx((v[i] - x.lse) * kLog2e);
+            const float pr = ptx::ex2_approx(fmaf(v[i], p.regain, -x.lse) * kLog2e);
             v[i] = (at == i ? pr - 1.0f : pr) * x.g;
         }
     }
@@ -893,10 +895,10 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
         }
         return;
     }
-    if constexpr (EPI == EPI_XENT_GRAD) xent_grad_chunk(v, col, *xr);
+    if constexpr (EPI == EPI_XENT_GRAD) xent_grad_chunk(v, col, p, *xr);
     if constexpr (EPI == EPI_XENT_GRAD3) {
         // dS = d0 + d1 + d2, each the rest before it rounded to bf16.
-        xent_grad_chunk(v, col, *xr);
+        xent_grad_chunk(v, col, p, *xr);
         const bool inside = row0 < p.M && col < p.N;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
@@ -2285,6 +2287,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.part = g.part;
     p.target_logit = g.target_logit;
     p.row_lse = g.row_lse;
+    p.regain = g.regain, p.regain_log2e = g.regain * kLog2e;
     p.dloss = g.dloss;
     p.vocab = g.vocab;
     p.accumulate = g.accumulate ? 1 : 0;

@@ -338,6 +338,19 @@ def test_equal_weights_leave_no_bias(tp):
             assert abs(along - 1) < 2.0 ** -10, (n, along)
 
 
+@pytest.mark.parametrize("T,h,V", [(8192, 4096, 2560), (2048, 8192, 9000), (300, 4096, 2000)])
+def test_long_sums_leave_no_bias(tp, T, h, V):
+    """What is asked of the loss of bf16 inputs: within 1e-6 of itself, over all tokens, at lengths
+    where an accumulator that truncates at every 16 products shrinks a logit by about
+    2^-26 h / 16 of itself, 3.8e-6 for h = 4096."""
+    X, W, y, _ = make(T, h, V, seed=17)
+    X = (X.float() + torch.linspace(0, 4, T, device="cuda")[:, None] * W[y].float()).bfloat16()  # towards the target
+    ctx = tp.XentContext(T, h, V, torch.bfloat16)
+    loss = tp.xent_forward(ctx, X, W, y).double()
+    ref = reference(X, W, y, torch.zeros(T, device="cuda"))["loss"]
+    assert float((loss - ref).norm() / ref.norm()) <= 1e-6
+
+
 def test_workspace_is_left_ready_for_the_next_call(tp):
     """Calls of different kinds share one workspace, with other workspace contents between them."""
     X, W, y, dl = make(4, 128, 700, seed=12)
