@@ -1897,9 +1897,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             if constexpr (is_ns_aux(EPI)) {
                                 AuxLoad &a = ns_aux[c & (C::NS_SETS - 1)];
                                 const bool landed = ptx::mbar_wait(a.bar, a.phase, p.wait_ns, &abort_sh);
+                                if (!__all_sync(0xffffffffu, landed)) {
+                                    // an abort elsewhere also ends this wait: the copy in flight lands
+                                    // first, and no other is issued
+                                    if (lane == 0) record_timeout(p, &abort_sh, 6);
+                                    ok = false;
+                                    ptx::mbar_wait(a.bar, a.phase, p.wait_ns, nullptr);
+                                }
                                 a.phase ^= 1u;
                                 a.pending = false;
-                                if (!__all_sync(0xffffffffu, landed) && lane == 0) record_timeout(p, &abort_sh, 6);
                             }
                             // (a product that reads no matrix: on single CTAs the first chunk has
                             // waited for the second's boxes too)
@@ -1910,7 +1916,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             if constexpr (is_ns_aux(EPI)) {
                                 constexpr int SETS = C::NS_SETS;
                                 const int n = (c + 1) & (SETS - 1);
-                                if (c + 1 >= SETS && c + 1 < CHUNKS)
+                                if (c + 1 >= SETS && c + 1 < CHUNKS && ok)
                                     ns_issue<EPI, SETS == 2>(&tmO2, &tmB2, ns_aux[n], stg + n * 2 * STG_BOX,
                                                              col0 + (c + 1) * 32, row0, zb, lane);
                             }
