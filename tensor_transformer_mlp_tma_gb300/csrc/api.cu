@@ -1135,26 +1135,33 @@ Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
 }
 
 // The forward product's tiles.  512: 256 x 512 with the whole K in one accumulator.
-// Otherwise 256 x tile_n with K in ranges that the epilogue adds up in fp32: the tensor
+// Otherwise 256 (or 128) x tile_n with K in ranges that the epilogue adds up in fp32: the tensor
 // core cuts the accumulator off (does not round) at every step of 16 products; the mean of
 // that is put back (xent_regain), the rest grows with the range: a relative error of the loss
 // of 1e-7 at 1000 products, 2.1e-7 at 2048, 5.0e-7 at 4096 (T = 8192, V = 2500 to 3000; before
 // the mean was put back 4.6e-7, 8.0e-7, 1.4e-6), so that at 8192 it would pass 1e-6.
 // On 256 x 256 tiles and in ranges the product is 9% slower (T = 8192, h = 4096,
 // V = 65536: 2.38 against 2.59 ms, power-bound).  Where there are few tiles the ranges cost nothing,
-// and narrower tiles divide the vocabulary evenly among the 76 units; fp32 operands
+// and narrower tiles divide the vocabulary evenly among the units; fp32 operands
 // want the precision and take short ranges always.
+// Up to 128 bf16 tokens fill a single CTA's tile: pairs would multiply 128 empty rows, at which
+// rate W comes no faster than 6 TB/s (h = 4096, V = 32768: T = 64 62.0 against 54.3 us; T = 100,
+// h = 8192: 112 against 98.7; T = 128, h = 1536, V = 50000: 42.6 against 38.6; T = 16, h = 2048,
+// V = 50021, unevenly divided: 60.0 against 61.2).  fp32 stays on pairs (T = 20, h = 1024,
+// V = 16000: 79 against 96 us), and so do more tokens (T = 256: 64.4 against 74.0 us).
 struct StatsTile {
     int tile_n;  // 0: a pass over W without tiles, for few tokens
     int64_t ranges, range;
+    bool pair;  // on CTA pairs
 };
 StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
-    const int64_t T = s->tokens, V = s->vocab, h = s->hidden, units = 76;
-    const bool f32 = s->dtype == TPMLP_F32;
-    const int64_t m = (T + 255) / 256, tiles = m * ((V + 255) / 256);
-    if (tpmlp::xent_few(!f32, T, h)) return {0, 1, h};
+    const int64_t T = s->tokens, V = s->vocab, h = s->hidden;
+    const bool f32 = s->dtype == TPMLP_F32, pair = f32 || T > 128;
+    const int64_t units = pair ? 76 : 152, tile_m = pair ? 256 : 128;
+    const int64_t m = (T + tile_m - 1) / tile_m, tiles = m * ((V + 255) / 256);
+    if (tpmlp::xent_few(!f32, T, h)) return {0, 1, h, false};
     const bool few = m == 1 || tiles <= 4 * units;
-    if (!f32 && !few && h <= 4096) return {512, 1, h};
+    if (!f32 && !few && h <= 4096) return {512, 1, h, true};
     int64_t tile_n = 256;
     if (few) {  // as many waves as 256-wide tiles need, evenly filled
         const int64_t waves = (tiles + units - 1) / units, per = std::max<int64_t>(1, waves * units / m);
@@ -1162,7 +1169,7 @@ StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
     }
     const int64_t longest = f32 ? 512 : (few ? 1024 : 4096);
     const int64_t ranges = (h + longest - 1) / longest;
-    return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64};
+    return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64, pair};
 }
 
 struct XentLayout {
@@ -1383,7 +1390,7 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
         g.target_logit = c.rows.target_logit;
         const StatsTile &t = c.L.stats;
         if (t.tile_n < 512) {
-            g.tile_n = t.tile_n;
+            g.tile_n = t.tile_n, g.cta_pair = t.pair;
             g.regain = tpmlp::xent_regain(t.range);
             // fp32: the six products one after the other, each in its ranges; where one range
             // holds all of K, one accumulation takes the six (the five small ones first)

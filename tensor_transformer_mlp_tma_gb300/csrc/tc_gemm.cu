@@ -1588,6 +1588,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 if constexpr (ANY_N) {
                                     if constexpr (PAIR)
                                         ptx::umma_f16_ss_pair(d_tmem, ad, bd, p.idesc, acc);
+                                    else
+                                        ptx::umma_f16_ss(d_tmem, ad, bd, p.idesc, acc);
                                 } else if constexpr (EPI == EPI_NS_GRAM32) {
                                     // hi lo^T + lo hi^T + hi hi^T (both tiles are 128 x 64 in the
                                     // same layout, the high part in A's place)
@@ -2373,7 +2375,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
 template <int EPI, bool A_MN, bool B_MN>
 static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
     if constexpr (EPI == EPI_XENT_FOLD) {
-        return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
+        return g.cta_pair ? launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st) : launch_t<EPI, A_MN, B_MN, 1>(g, num_sms, st);
     } else if constexpr (EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS) {
         return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);  // small or split outputs
     } else if constexpr (EPI == EPI_NS_FINAL) {
