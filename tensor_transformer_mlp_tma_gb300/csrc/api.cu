@@ -1155,7 +1155,7 @@ struct StatsTile {
     bool pair;  // on CTA pairs
 };
 StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
-    const int64_t T = s->tokens, V = s->vocab, h = s->hidden;
+    const int64_t T = std::max<int64_t>(1, s->tokens), V = s->vocab, h = s->hidden;
     const bool f32 = s->dtype == TPMLP_F32, pair = f32 || T > 128;
     const int64_t units = pair ? 76 : 152, tile_m = pair ? 256 : 128;
     const int64_t m = (T + tile_m - 1) / tile_m, tiles = m * ((V + 255) / 256);

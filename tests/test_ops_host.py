@@ -200,3 +200,15 @@ def test_bindings(tp):
     ctx = tp.XentContext(4, 8, 16, torch.float32, device="cpu")  # buffers only; calls refuse CPU tensors
     with pytest.raises(ValueError):
         tp.xent_forward(ctx, torch.zeros(4, 8), torch.zeros(16, 8), torch.zeros(4, dtype=torch.int64))
+
+
+def test_no_tokens_at_any_hidden_size(tp):
+    """T = 0 is a valid shape whatever the hidden size: also past the 98304 (bf16), 49152 (fp32) and 12256
+    (bf16, more than one token) elements up to which X fits the few-token kernels' shared memory."""
+    for dtype in (tp.BF16, tp.F32):
+        for algo in (0, 1):
+            for h in (8, 12256, 12264, 49152, 49160, 98304, 98312, 1 << 20):
+                s = xshape(tp, T=0, h=h, V=100, dtype=dtype, algo=algo)
+                assert xws(tp, s) > 0
+                assert xfwd(tp, s, [None, FAKE, None, None, None]) == tp.OK
+                assert xbwd(tp, s, [None, FAKE, None, None, None, None, None]) == tp.OK
