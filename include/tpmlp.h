@@ -345,8 +345,9 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, co
 
 /* Backward: dX[T,h] and dW[V,h] from the forward pass's inputs and lse, and dloss[T]
  * (fp32).  Either output may be NULL and is then not computed (a frozen head, a
- * frozen body).  In bf16 dS is rounded (in units of dloss[0] where that is a
- * number of ordinary size) before the two products, in fp32 it is not; dX is summed
+ * frozen body).  In bf16 dS is rounded before the two products (on the tensor
+ * cores in units of the significand of the first dloss that takes part, so that equal
+ * weights are not rounded the same way in every token), in fp32 it is not; dX is summed
  * over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
  * Results are bit-identical from call to call.  Errors as the forward. */
 tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,

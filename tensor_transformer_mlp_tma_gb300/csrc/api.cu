@@ -1176,10 +1176,10 @@ struct XentLayout {
     int64_t piece, pieces, groups, hp, ldo;
     StatsTile stats;
     Split dx, dw;
-    size_t part, target_logit, xp, wp, ds, logits, acc, dwacc, total;
+    size_t unit, part, target_logit, xp, wp, ds, logits, acc, dwacc, total;
 };
 
-// Workspace, 1 KB-aligned regions: status | statistics | the targets' logits | three bf16
+// Workspace, 1 KB-aligned regions: status | the unit of dS | statistics | the targets' logits | three bf16
 // parts of X and W (fp32) | dS of one piece | fp32 logits of one piece (FFMA path) | fp32
 // dX, per split | fp32 dW of one piece, per split.
 XentLayout xent_layout(const tpmlp_xent_shape *s) {
@@ -1209,6 +1209,7 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
         return at;
     };
     const size_t piece = static_cast<size_t>(L.piece), hp = static_cast<size_t>(L.hp), ldo = static_cast<size_t>(L.ldo);
+    L.unit = region(sizeof(float));
     L.part = region(stored * T * sizeof(float2));
     L.target_logit = region(T * 4);
     L.xp = region(tc && f32 ? 3 * T * hp * 2 : 0);
@@ -1446,7 +1447,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     const bool stores = !f32 || (h % 4 == 0 && aligned16(dX));  // fp32 rows that TMA can store
     const bool one = !f32 && c.L.pieces == 1 && c.L.dx.n == 1;
     const bool dx_in_place = tc ? (f32 ? c.L.dx.n == 1 && stores : one) : f32 || c.L.pieces == 1;
-    float *acc = reinterpret_cast<float *>(c.ws + c.L.acc);
+    float *acc = reinterpret_cast<float *>(c.ws + c.L.acc), *unit = reinterpret_cast<float *>(c.ws + c.L.unit);
     for (int64_t k = 0; k < c.L.pieces; ++k) {
         const int64_t v0 = k * c.L.piece, n = std::min(c.L.piece, s->vocab - v0);
         GemmArgs g = c.logits(X, W, v0, n);
@@ -1454,7 +1455,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
         const int64_t ds_part = T * ld;
         if (tc) {
             g.out0 = ds, g.ldo = ld;
-            g.row_lse = lse, g.dloss = dloss, g.vocab = s->vocab;
+            g.row_lse = lse, g.dloss = dloss, g.vocab = s->vocab, g.unit = unit;
             e = c.launch("xent_ds", f32 ? tpmlp::EPI_XENT_GRAD3 : tpmlp::EPI_XENT_GRAD, g);
         } else {
             float *logits = reinterpret_cast<float *>(c.ws + c.L.logits);
@@ -1483,14 +1484,14 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
                     XentCall::set_parts(w, ds_part, T * c.L.hp);
                 }
             }
-            w.dloss = dloss;
+            w.unit = unit;
             e = c.launch("xent_dw", !tc                 ? tpmlp::EPI_STORE
                                     : f32 || !in_place ? tpmlp::EPI_ACC32
                                                        : tpmlp::EPI_STORE_UNIT, w);
             if (e == cudaSuccess && !in_place)
                 e = c.kernel("xent_dw_sum", [&] {
                     return tpmlp::launch_sum_splits(!f32, reinterpret_cast<float *>(c.ws + c.L.dwacc), c.L.dw.n, n, h,
-                                                    c.L.ldo, f32 ? nullptr : dloss, out, c.st);
+                                                    c.L.ldo, f32 ? nullptr : unit, out, c.st);
                 });
             if (e != cudaSuccess) return from_cuda(e);
         }
@@ -1510,7 +1511,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
                 }
             }
             const bool rounds = dx_in_place && !f32;  // one product gives the bf16 result
-            x.dloss = dloss;
+            x.unit = unit;
             e = c.launch("xent_dx", !rounds ? tpmlp::EPI_ACC32 : (tc ? tpmlp::EPI_STORE_UNIT : tpmlp::EPI_STORE), x);
             if (e != cudaSuccess) return from_cuda(e);
         }
@@ -1518,7 +1519,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
     if (dX && !dx_in_place)
         e = c.kernel("xent_dx_sum", [&] {
             return tpmlp::launch_sum_splits(!f32, acc, tc ? c.L.dx.n : 1, T, h, tc ? c.L.ldo : h,
-                                            tc && !f32 ? dloss : nullptr, dX, c.st);
+                                            tc && !f32 ? unit : nullptr, dX, c.st);
         });
     return from_cuda(e);
 }

@@ -8,14 +8,36 @@ namespace tpmlp {
 
 // The unit that dS of bf16 is taken in: dS / unit is rounded and multiplied, and the products
 // are multiplied by it in fp32.  The usual gradients of the losses are all the same (1 over
-// the tokens of a mean); in that unit dS at a target is p - 1, close to -1, where in the
-// plain unit it is the same rounding of 1/n in every token, up to 2^-9 of dX and dW that
-// does not average out.  The first token's gradient is as good as any where they differ;
-// one out of reach of fp32's middle range is not used.
+// the tokens of a mean); in units of their significand dS at a target is p - 1 times a power of
+// two, where in the plain unit it is the same rounding of 1/n in every token, up to 2^-9 of dX and
+// dW that does not average out.  The exponent stays with dS: only the significand rounds, and
+// a unit of 1 to 2 takes no gradient out of range.  It is the significand of the first
+// gradient that takes part: of a valid target, neither 0 nor subnormal, infinite or NaN.
+// Prompts come first, and have no part; a whole warp looks at 256 tokens at a time.
 #ifdef __CUDACC__
-__device__ __forceinline__ float xent_unit(const float *dloss) {
-    const float g = fabsf(dloss[0]);
-    return g >= 0x1p-20f && g <= 0x1p20f ? g : 1.0f;
+__device__ __forceinline__ float xent_find_unit(const int64_t *target, const float *dloss, int64_t tokens,
+                                                int64_t ignore_index, int64_t vocab) {
+    constexpr int UN = 8;  // loads in flight
+    const int lane = threadIdx.x & 31;
+    for (int64_t t0 = 0; t0 < tokens; t0 += 32 * UN) {
+        float g[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t t = t0 + 32 * u + lane;
+            const int64_t y = t < tokens ? target[t] : -1;
+            const float d = t < tokens ? fabsf(dloss[t]) : 0.0f;
+            g[u] = y != ignore_index && y >= 0 && y < vocab ? d : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const unsigned hit = __ballot_sync(0xffffffffu, g[u] >= 0x1p-126f && g[u] < INFINITY);
+            if (hit) {
+                const float first = __shfl_sync(0xffffffffu, g[u], __ffs(static_cast<int>(hit)) - 1);
+                return __uint_as_float((__float_as_uint(first) & 0x007FFFFFu) | 0x3F800000u);
+            }
+        }
+    }
+    return 1.0f;
 }
 #endif
 
@@ -35,7 +57,7 @@ enum Epi : int {
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
     EPI_NS_LAST = 13,   // the same X', bf16                                -- C X, last step
-    EPI_STORE_UNIT = 19, // out = acc * unit (see xent_unit)                 -- dX and dW of bf16
+    EPI_STORE_UNIT = 19, // out = acc * unit (see xent_find_unit)                 -- dX and dW of bf16
     EPI_NS_GRAMS = 18,  // A in fp32, lower triangle, over K in ksplit ranges -- X X^T
     EPI_NS_GRAM32 = 15, // A_0 in fp32 from X as two fp16 parts, K in nshards ranges added up in fp32 -- X X^T
     EPI_NS_FINAL = 16,  // bf16 out = scale * acc, both operands in two parts -- Q X
@@ -120,6 +142,7 @@ struct GemmArgs {
     float regain;            // factor of the logits, see xent_regain
     const float *row_lse;    // GRAD: [M]
     const float *dloss;      // GRAD: [M]; a target that is ignored or outside [0, vocab) has none
+    float *unit;             // GRAD: where its unit goes; EPI_STORE_UNIT: where it is read
     bool accumulate;         // EPI_ACC32: add to what out0 holds
     int tile_n;              // EPI_XENT_FOLD: columns per tile, a multiple of 32 up to 256 (0: 256)
     // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
@@ -225,9 +248,9 @@ int64_t xent_few_groups(int64_t vocab);
 cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden, float2 *part,
                             float *loss, float *lse, cudaStream_t st);
 // out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
-// With dloss the sums are multiplied by xent_unit(dloss).
+// With unit the sums are multiplied by *unit.
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
-                              const float *dloss, void *out, cudaStream_t st);
+                              const float *unit, void *out, cudaStream_t st);
 // fp32 [rows][cols] as three bf16 matrices [rows][ld], ld >= cols a multiple of 4, the rest zero.
 struct Split3 {
     const float *in;

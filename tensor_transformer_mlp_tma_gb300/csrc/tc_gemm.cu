@@ -183,6 +183,7 @@ struct Params {
     const float *row_lse, *dloss;
     float regain, regain_log2e;  // the logits' factor (xent_regain), and log2(e) of it
     long long vocab;
+    float *unit;     // EPI_XENT_GRAD writes it, EPI_STORE_UNIT reads it
     int accumulate;  // EPI_ACC32
     // K of the cross entropy's products: kb_seg k-blocks per pair of operand parts (one
     // pair, or six for fp32 operands in three parts); problem z starts at k-block
@@ -668,7 +669,7 @@ struct XentRow {
     float m, s;    // STATS: running maximum, sum of exp(logit - m)
 };
 template <int EPI>
-__device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, XentRow &x) {
+__device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, float unit, XentRow &x) {
     x.tcol = -1, x.lse = 0.0f, x.g = 0.0f;
     x.m = -INFINITY, x.s = 0.0f;
     if (row >= p.M) return;
@@ -679,7 +680,7 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, Xent
     if constexpr (is_grad(EPI)) {
         x.lse = p.row_lse[row];
         x.g = valid && t >= 0 && t < p.vocab ? p.dloss[row] : 0.0f;
-        if constexpr (EPI == EPI_XENT_GRAD) x.g = __fdiv_rn(x.g, xent_unit(p.dloss));
+        if constexpr (EPI == EPI_XENT_GRAD) x.g = __fdiv_rn(x.g, unit);
     }
 }
 
@@ -1003,7 +1004,7 @@ __device__ __forceinline__ void finish_chunk(const Params &p, const CUtensorMap 
         pack32(v, w0);
     } else {  // EPI_STORE, EPI_STORE_UNIT, EPI_FOLD
         if constexpr (EPI == EPI_STORE_UNIT) {
-            const float unit = xent_unit(p.dloss);
+            const float unit = *p.unit;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= unit;
         }
@@ -1647,6 +1648,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         AuxLoad ns_aux[2] = {{ptx::smem_u32(&bar_ns[is_ns_aux(EPI) ? 2 * ew : 0]), 0u, false},
                              {ptx::smem_u32(&bar_ns[is_ns_aux(EPI) ? 2 * ew + 1 : 0]), 0u, false}};
         (void)ns_aux;
+        float unit_of_ds = 1.0f;
+        if constexpr (EPI == EPI_XENT_GRAD) {
+            unit_of_ds = xent_find_unit(p.target, p.dloss, p.M, p.ignore_index, p.vocab);
+            if (blockIdx.x == 0 && ew == 0 && lane == 0) *p.unit = unit_of_ds;
+        }
+        (void)unit_of_ds;
         // After every lane's tcgen05.ld of the buffer has completed, one arrival
         // per warp on the leader's accumulator-empty barrier.
         auto release = [&](uint32_t buf) {
@@ -1684,7 +1691,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             BiasPre bias_next;
             if constexpr (EPI == EPI_BIAS_GELU) bias_fetch(p.bias, col0 + 32 * qa, p.N, bias_next);
             XentRow xr;
-            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, xr);
+            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, unit_of_ds, xr);
             bool got = ptx::mbar_wait_scoped<false>(ptx::smem_u32(&bar_tfull[0]), tcount & 1u, p.wait_ns, &abort_sh);
             ++tcount;
             got = __all_sync(0xffffffffu, got);
@@ -1774,7 +1781,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if constexpr (EPI == EPI_DGELU) aux_issue(&tmO1, aux, stg + STG_BOX, col0, row0, zb, lane);
             if constexpr (EPI == EPI_ATTN_DS) aux_issue(&tmO1, aux, stg + STG_BOX_WIDE, col0, row0, zb, lane, STG_BOX_WIDE);
             XentRow xr;
-            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, xr);
+            if constexpr (is_xent(EPI)) xent_row_load<EPI>(p, row, unit_of_ds, xr);
             (void)xr;
             // The first two chunks' matrices come while the accumulator is still computed.
             if constexpr (is_ns_aux(EPI)) {
@@ -2297,6 +2304,7 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.row_lse = g.row_lse;
     p.regain = g.regain, p.regain_log2e = g.regain * kLog2e;
     p.dloss = g.dloss;
+    p.unit = g.unit;
     p.vocab = g.vocab;
     p.accumulate = g.accumulate ? 1 : 0;
     p.aux2 = g.aux2;

@@ -345,10 +345,10 @@ __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(
 // output's type.  V columns per thread.  Memory bound: 4 bytes per split and element.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) sum_splits_kernel(const float *in, int splits, int64_t rows, int64_t cols,
-                                                         int64_t ld, const float *dloss, T *out) {
+                                                         int64_t ld, const float *unit_at, T *out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const float unit = dloss ? xent_unit(dloss) : 1.0f;
+    const float unit = unit_at ? *unit_at : 1.0f;
     const int64_t per_row = cols / V, n = rows * per_row, step = rows * ld;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -562,17 +562,17 @@ cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const
 }
 
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,
-                              const float *dloss, void *out, cudaStream_t st) {
+                              const float *unit, void *out, cudaStream_t st) {
     const bool vec = cols % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     const int64_t blocks = xent::blocks_for(rows * cols / (vec ? 4 : 1));
     if (is_bf16) {
         auto o = static_cast<__nv_bfloat16 *>(out);
-        return vec ? launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o)
-                   : launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o);
+        return vec ? launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, unit, o)
+                   : launch_pdl(xent::sum_splits_kernel<__nv_bfloat16, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, unit, o);
     }
     auto o = static_cast<float *>(out);
-    return vec ? launch_pdl(xent::sum_splits_kernel<float, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o)
-               : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, dloss, o);
+    return vec ? launch_pdl(xent::sum_splits_kernel<float, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, unit, o)
+               : launch_pdl(xent::sum_splits_kernel<float, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, in, splits, rows, cols, ld, unit, o);
 }
 
 cudaError_t launch_split3(const Split3 &a, const Split3 &b, cudaStream_t st) {

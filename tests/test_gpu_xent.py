@@ -405,3 +405,48 @@ def test_gradient_against_differences(tp):
         ana = float((grads["dX"].double() * dx).sum() + (grads["dW"].double() * dw).sum())
         scale = float((grads["dX"].double() * dx).abs().sum() + (grads["dW"].double() * dw).abs().sum())
         assert abs(num - ana) <= 1e-5 * scale + 1e-9
+
+
+@pytest.mark.parametrize("masked", ["ignored, dloss 0", "ignored, another dloss", "dloss 0", "outside", "nan dloss"])
+@pytest.mark.parametrize("n", [1, 100, 300])
+def test_equal_weights_after_masked_tokens_leave_no_bias(tp, masked, n):
+    """The bound of the test above where the first n tokens have no part in the loss: what their
+    dloss holds decides nothing.  Of 512 - n >= 212 tokens the mean error is at most
+    2^-8 / sqrt(3 * 212) in the mean of squares, 1.6e-4."""
+    X, W, y, _ = make(512, 256, 4000, seed=11)
+    dl = torch.full((512,), (1 + 2.0 ** -8) / 512, device="cuda")
+    if masked in ("dloss 0", "ignored, dloss 0"):
+        dl[:n] = 0
+    if masked == "ignored, another dloss":
+        dl[:n] = 1.3
+    if masked == "nan dloss":
+        dl[:n] = float("nan")
+    y[:n] = y[:n] if masked == "dloss 0" else IGN
+    y_in = y.clone()
+    if masked == "outside":
+        y_in[:n] = 4000
+    for piece in (0, 2048):
+        ctx = tp.XentContext(512, 256, 4000, X.dtype, piece=piece)
+        loss = tp.xent_forward(ctx, X, W, y_in)
+        grads = tp.xent_backward(ctx, dl)
+        assert tp.check_device_status(ctx) == (tp.ERR_INVALID_ARG if masked == "outside" else tp.OK)
+        ref = reference(X, W, y, dl)
+        check(X, W, y, torch.where(y == IGN, 0.0, dl), loss, ctx.lse, grads, ref)
+        for name in ("dX", "dW"):
+            along = float((grads[name].double() * ref[name]).sum() / (ref[name] * ref[name]).sum())
+            assert abs(along - 1) < 2.0 ** -10, (name, along)
+
+
+@pytest.mark.parametrize("first", [1e-30, 1e30, 3e38])
+def test_weights_far_apart(tp, first):
+    """The first token's weight next to ordinary ones: neither it nor they leave fp32's range."""
+    X, W, y, dl = make(40, 64, 300, seed=15)
+    dl[0] = first
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    ref = reference(X, W, y, dl)
+    if first > 1e31:  # dW adds terms of 3e38 up to more than fp32 holds
+        grads = {"dX": grads["dX"][1:], "dW": None}
+        X, y, dl, loss, lse = X[1:], y[1:], dl[1:], loss[1:], ctx.lse[1:]
+        check(X, W, y, dl, loss, lse, grads, reference(X, W, y, dl))
+    else:
+        check(X, W, y, dl, loss, ctx.lse, grads, ref)
