@@ -331,7 +331,9 @@ size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
 
 /* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
  * written for every token, ignored ones too.  bf16 runs on the tensor cores with
- * fp32 accumulation and statistics; the logits are not rounded.  fp32 runs there too, each
+ * fp32 accumulation and statistics; the logits are not rounded beyond that (the tensor core's
+ * accumulator cuts off rather than rounds: at most 2^-24 of the partial sum per 16 products,
+ * in ranges of at most 2048 products for bf16 and 256 for fp32, the ranges added in fp32).  fp32 runs there too, each
  * operand as the sum of three bf16 numbers (24 bits, and 2^-133 at the least).  A logit of NaN or
  * +inf makes its token's loss and lse non-finite, no other token's.  A target that
  * is neither ignore_index nor in [0, V) is reported as TPMLP_ERR_INVALID_ARG in the

@@ -1136,14 +1136,18 @@ Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
 
 // The forward product's tiles.  512: 256 x 512 with the whole K in one accumulator.
 // Otherwise 256 (or 128) x tile_n with K in ranges that the epilogue adds up in fp32: the tensor
-// core cuts the accumulator off (does not round) at every step of 16 products; the mean of
-// that is put back (xent_regain), the rest grows with the range: a relative error of the loss
-// of 1e-7 at 1000 products, 2.1e-7 at 2048, 5.0e-7 at 4096 (T = 8192, V = 2500 to 3000; before
-// the mean was put back 4.6e-7, 8.0e-7, 1.4e-6), so that at 8192 it would pass 1e-6.
-// On 256 x 256 tiles and in ranges the product is 9% slower (T = 8192, h = 4096,
-// V = 65536: 2.38 against 2.59 ms, power-bound).  Where there are few tiles the ranges cost nothing,
-// and narrower tiles divide the vocabulary evenly among the units; fp32 operands
-// want the precision and take short ranges always.
+// core cuts the accumulator off (towards zero, it does not round) at every step of 16 products,
+// which takes 2^-26 of a logit a step with independent terms, and up to 2^-24 a step with all
+// terms of one sign.  Relative error of the loss (T = 300 to 8192, V = 2500 to 50000, X
+// towards the target's row): 6e-8 in ranges of 256, 1.2e-7 of 512, 2.4 to 3.4e-7 of 1024, 5.0 to
+// 5.9e-7 of 2048, 1.0e-6 of 4096, 2.6e-6 of 8192; the plain fp32 form's is 2e-7.
+// Wide tiles take a quarter less from L2 per product, which bounds short products at full
+// clock (T = 333, h = 2048, V = 50021: 72 us against 81 in ranges of 1024), so that up to 2048
+// products go into one accumulation; longer rows go in ranges of 1024 (T = 8192, h = 4096,
+// V = 65536: 2.53 ms, ranges of 2048 2.50, one of 4096 on wide tiles 2.39).  Where there are few
+// tiles the ranges cost nothing, and narrower tiles divide the vocabulary evenly among the units;
+// fp32 operands want the precision and take ranges of 256 always (T = 512, h = 1024, V = 16384:
+// 8.4e-8 in 116 us, ranges of 512 1.8e-7 in 107).
 // Up to 128 bf16 tokens fill a single CTA's tile: pairs would multiply 128 empty rows, at which
 // rate W comes no faster than 6 TB/s (h = 4096, V = 32768: T = 64 62.0 against 54.3 us; T = 100,
 // h = 8192: 112 against 98.7; T = 128, h = 1536, V = 50000: 42.6 against 38.6; T = 16, h = 2048,
@@ -1161,13 +1165,13 @@ StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
     const int64_t m = (T + tile_m - 1) / tile_m, tiles = m * ((V + 255) / 256);
     if (tpmlp::xent_few(!f32, T, h)) return {0, 1, h, false};
     const bool few = m == 1 || tiles <= 4 * units;
-    if (!f32 && !few && h <= 4096) return {512, 1, h, true};
+    if (!f32 && !few && h <= 2048) return {512, 1, h, true};
     int64_t tile_n = 256;
     if (few) {  // as many waves as 256-wide tiles need, evenly filled
         const int64_t waves = (tiles + units - 1) / units, per = std::max<int64_t>(1, waves * units / m);
         tile_n = std::min<int64_t>(256, ((V + per - 1) / per + 31) / 32 * 32);
     }
-    const int64_t longest = f32 ? 512 : (few ? 1024 : 4096);
+    const int64_t longest = f32 ? 256 : 1024;
     const int64_t ranges = (h + longest - 1) / longest;
     return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64, pair};
 }
@@ -1328,7 +1332,6 @@ struct XentCall {
             set_parts(g, s->tokens * L.hp, s->vocab * L.hp);
         }
         g.target = rows.target, g.ignore_index = s->ignore_index, g.col0 = v0;
-        g.regain = tpmlp::xent_regain(s->hidden);
         return g;
     }
     cudaError_t launch(const char *name, Epi epi, GemmArgs &g) const {
@@ -1392,7 +1395,6 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
         const StatsTile &t = c.L.stats;
         if (t.tile_n < 512) {
             g.tile_n = t.tile_n, g.cta_pair = t.pair;
-            g.regain = tpmlp::xent_regain(t.range);
             // fp32: the six products one after the other, each in its ranges; where one range
             // holds all of K, one accumulation takes the six (the five small ones first)
             const int pairs = c.parts() ? 6 : 1;

@@ -139,7 +139,6 @@ struct GemmArgs {
     int64_t ignore_index, col0, vocab;
     float2 *part;            // STATS: (max, sum) of column group k, row m, at part[k * M + m]
     float *target_logit;     // STATS: [M], written where the target is one of the columns
-    float regain;            // factor of the logits, see xent_regain
     const float *row_lse;    // GRAD: [M]
     const float *dloss;      // GRAD: [M]; a target that is ignored or outside [0, vocab) has none
     float *unit;             // GRAD: where its unit goes; EPI_STORE_UNIT: where it is read
@@ -154,18 +153,6 @@ struct GemmArgs {
     float alpha, beta, diag;
     int64_t out_rows, out_cols;
 };
-
-// The tensor core cuts its accumulator off (towards zero) at every step of 16 products, which
-// makes a sum smaller than it is: by half an ulp a step on average, of a running sum that is
-// half the last one on average, is about 0.35 2^-24 of the sum per step.  Measured over logits
-// of 256 to 8192 products: 0.20 to 0.26 with independent terms, 0.26 to 0.31 where X leans
-// towards the row of W, 0.22 to 0.32 with one term ten times the others first or last, 0.4 to
-// 1.1 with all terms of one sign.  The logits are multiplied by 1 + 0.25 2^-24 a step, for
-// the products of one accumulation, which no such data wants less than 0.8 of: rms error of
-// a logit of 4096 independent terms 1.4e-5 -> 7e-6, of leaning ones 2.1e-4 -> 3e-5.
-inline float xent_regain(int64_t products) {
-    return 1.0f + 0x1p-26f / 16.0f * static_cast<float>(products);
-}
 
 // Column groups of the EPI_XENT_STATS partials: four per 512-wide tile (128 columns each), or
 // two per tile of EPI_XENT_FOLD.

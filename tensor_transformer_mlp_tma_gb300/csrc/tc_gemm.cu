@@ -181,7 +181,6 @@ struct Params {
     float2 *part;
     float *target_logit;
     const float *row_lse, *dloss;
-    float regain, regain_log2e;  // the logits' factor (xent_regain), and log2(e) of it
     long long vocab;
     float *unit;     // EPI_XENT_GRAD writes it, EPI_STORE_UNIT reads it
     int accumulate;  // EPI_ACC32
@@ -686,8 +685,7 @@ __device__ __forceinline__ void xent_row_load(const Params &p, int64_t row, floa
 
 // One pass of the online softmax over 32 logits: the running maximum moves to m',
 // the running sum is scaled by exp(m - m') and the 32 exponentials are added, all
-// in fp32.  Columns from `end` on count as -inf.  Logits and maximum are the accumulator's;
-// what leaves (flush, the target's logit) and the exponents have the factor `regain`.
+// in fp32.  Columns from `end` on count as -inf.
 __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, int col, int end, const Params &p,
                                                  XentRow &x) {
     if (col >= end) return;
@@ -701,10 +699,10 @@ __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, in
     for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
     const float m = fmaxf(x.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
     // all logits so far -inf: exp(-inf - 0) = 0 instead of exp(-inf + inf)
-    const float base = m == -INFINITY ? 0.0f : m * p.regain_log2e;
-    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, p.regain_log2e, -base)), 0.0f, 0.0f, 0.0f};
+    const float base = m == -INFINITY ? 0.0f : m * kLog2e;
+    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], p.regain_log2e, -base));
+    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], kLog2e, -base));
     x.m = m;
     x.s = (s[0] + s[1]) + (s[2] + s[3]);
     // the target's logit, where it is one of these columns (few warps at a time)
@@ -715,11 +713,11 @@ __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, in
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (at == i) z = v[i];
-        if (here && row < p.M) p.target_logit[row] = z * p.regain;
+        if (here && row < p.M) p.target_logit[row] = z;
     }
 }
 __device__ __forceinline__ void xent_stats_flush(const Params &p, int64_t row, int group, XentRow &x) {
-    if (row < p.M) p.part[static_cast<int64_t>(group) * p.M + row] = make_float2(x.m * p.regain, x.s);
+    if (row < p.M) p.part[static_cast<int64_t>(group) * p.M + row] = make_float2(x.m, x.s);
     x.m = -INFINITY, x.s = 0.0f;
 }
 
@@ -735,7 +733,7 @@ __device__ __forceinline__ void xent_grad_chunk(float (&v)[32], int col, const P
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float pr = ptx::ex2_approx(fmaf(v[i], p.regain, -x.lse) * kLog2e);
+            const float pr = ptx::ex2_approx((v[i] - x.lse) * kLog2e);
             v[i] = (at == i ? pr - 1.0f : pr) * x.g;
         }
     }
@@ -2302,7 +2300,6 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.part = g.part;
     p.target_logit = g.target_logit;
     p.row_lse = g.row_lse;
-    p.regain = g.regain, p.regain_log2e = g.regain * kLog2e;
     p.dloss = g.dloss;
     p.unit = g.unit;
     p.vocab = g.vocab;
@@ -2341,7 +2338,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // TPMLP_SERPENTINE=0 walks K upwards in every wave (a tuning knob, read per call).
     {
         const char *se = std::getenv("TPMLP_SERPENTINE");
-        p.serpentine = (WIDE || (!HEADS && g.causal_k == 0 && !g.skip_upper)) && !(se && se[0] == '0') ? 1 : 0;
+        // (Not the cross entropy's logits: a logit is summed in the same order in whichever wave its tile
+        // is, and one accumulation of fp32 parts takes the small products first.)
+        p.serpentine =
+            !is_xent(EPI) && (WIDE || (!HEADS && g.causal_k == 0 && !g.skip_upper)) && !(se && se[0] == '0') ? 1 : 0;
     }
     if (WIDE) {
         const char *tail_env = std::getenv("TPMLP_WIDE_TAIL");

@@ -450,3 +450,53 @@ def test_weights_far_apart(tp, first):
         check(X, W, y, dl, loss, lse, grads, reference(X, W, y, dl))
     else:
         check(X, W, y, dl, loss, ctx.lse, grads, ref)
+
+
+def rows_of_kind(kind, T, h, V, dtype, seed):
+    """X and W where the sum of a logit is exact, sparse, padded, or all of one sign."""
+    X, W, y, dl = make(T, h, V, torch.float32, seed=seed)
+    r = torch.arange(T, device="cuda")
+    if kind == "one-hot":
+        X = torch.zeros_like(X)
+        X[r, (r * 37 + 5) % h] = 64.0
+    elif kind == "sparse":
+        X = torch.where((r[:, None] * 7 + torch.arange(h, device="cuda")) % 97 == 0, 9 * X, 0.0)
+    elif kind == "padded":
+        X[:, 64:] = 0
+        X *= 8
+    elif kind == "one sign":
+        X, W = X.abs(), W.abs() / math.sqrt(h)
+    elif kind == "towards the target":
+        X = X + 4 * W[y]
+    return X.to(dtype), W.to(dtype), y, dl
+
+
+@pytest.mark.parametrize("dtype,h", [(torch.bfloat16, 2048), (torch.bfloat16, 4096), (torch.bfloat16, 8192),
+                                     (torch.float32, 256), (torch.float32, 4096)])
+@pytest.mark.parametrize("T,V", [(7, 1500), (100, 1500), (600, 2000), (2500, 9000)])
+@pytest.mark.parametrize("kind", ["dense", "one-hot", "sparse", "padded", "one sign", "towards the target"])
+def test_logits_of_every_kind_of_row(tp, kind, T, V, dtype, h):
+    """lse of every token, and the losses' error over all tokens, against 64 bits.
+
+    A logit S comes from accumulations of n products, 2048 (bf16) or 256 (fp32) at the most, that are
+    cut off at every step of 16 in which a product is not zero, by at most an ulp of the partial
+    sum, half of one on average: at most `steps` 2^-24 of sum |x w| for terms of one sign (the
+    partial sum is half the whole on average), and a quarter of `steps` 2^-24 of S for independent
+    terms, up to 1.3 times that where they lean one way (1.5 is taken).  The sum of the ranges, the
+    difference to the maximum and the logarithm round h / n + 4 times by 2^-24; fp32 leaves out
+    products of parts of 2^-22.  The exponentials, their sum and the logarithm leave 2^-21 of
+    their own (and of lse and log V in lse)."""
+    X, W, y, dl = rows_of_kind(kind, T, h, V, dtype, seed=T + h)
+    ctx = tp.XentContext(T, h, V, dtype)
+    loss = tp.xent_forward(ctx, X, W, y)
+    assert tp.check_device_status(ctx) == tp.OK
+    ref = reference(X, W, y, dl)
+    n = min(2048 if dtype == torch.bfloat16 else 256, h)
+    steps = {"one-hot": 0, "sparse": n / 97 + 1, "padded": 4}.get(kind, n / 16)
+    roundings = h / n + 4 + (4 if dtype == torch.float32 else 0)
+    size = (X.double().abs() @ W.double().abs().t()).amax(1)
+    tol = (steps + roundings) * 2.0 ** -24 * size + 2.0 ** -21 * (ref["lse"].abs() + math.log(V))
+    assert bool(((ctx.lse.double() - ref["lse"]).abs() <= tol).all())
+    both = ref["S"].abs().amax(1) + ref["S"].gather(1, y[:, None])[:, 0].abs()
+    tol = ((steps if kind == "one sign" else 1.5 * steps / 4) + roundings) * 2.0 ** -24 * both + 2.0 ** -21
+    assert float((loss.double() - ref["loss"]).norm()) <= float(tol.norm())
