@@ -699,10 +699,13 @@ __device__ __forceinline__ void xent_stats_chunk(float (&v)[32], int64_t row, in
     for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
     const float m = fmaxf(x.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
     // all logits so far -inf: exp(-inf - 0) = 0 instead of exp(-inf + inf)
-    const float base = m == -INFINITY ? 0.0f : m * kLog2e;
-    float s[4] = {x.s * ptx::ex2_approx(fmaf(x.m, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
+    const float base = m == -INFINITY ? 0.0f : m;
+    // The difference first and then the factor log2(e): the maximum's own term is exactly 1,
+    // and that of a logit near it as exact as the logit.  (One FMA with m log2(e) rounded leaves
+    // 2^-24 m in every term, and so in the loss of a token that is sure of its target.)
+    float s[4] = {x.s * ptx::ex2_approx((x.m - base) * kLog2e), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx(fmaf(v[i], kLog2e, -base));
+    for (int i = 0; i < 32; ++i) s[i & 3] += ptx::ex2_approx((v[i] - base) * kLog2e);
     x.m = m;
     x.s = (s[0] + s[1]) + (s[2] + s[3]);
     // the target's logit, where it is one of these columns (few warps at a time)

@@ -500,3 +500,42 @@ def test_logits_of_every_kind_of_row(tp, kind, T, V, dtype, h):
     both = ref["S"].abs().amax(1) + ref["S"].gather(1, y[:, None])[:, 0].abs()
     tol = ((steps if kind == "one sign" else 1.5 * steps / 4) + roundings) * 2.0 ** -24 * both + 2.0 ** -21
     assert float((loss.double() - ref["loss"]).norm()) <= float(tol.norm())
+
+
+def certain(T, h, V, dtype):
+    """Tokens whose target's logit (270) is more than 100 above every other, whose exponentials are
+    zero in fp32."""
+    X, W, y, dl = make(T, h, V, torch.float32, seed=T + h + V)
+    W = (W / W.norm(dim=1, keepdim=True)).to(dtype)
+    X = (270 * W[y].float()).to(dtype)
+    S = X.double() @ W.double().t()
+    others = S.scatter(1, y[:, None], -float("inf")).amax(1)
+    assert bool((S.gather(1, y[:, None])[:, 0] - others > 100).all())
+    return X, W, y, dl
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", [(1, 256, 300), (5, 1024, 3000), (9, 256, 300), (100, 1000, 2000), (333, 2056, 20000),
+                                   (2500, 2048, 9000), (2500, 4096, 9000)])
+def test_certain_tokens_have_no_loss(tp, T, h, V, dtype):
+    """The sum of exponentials is the maximum's own term, exactly 1, and lse the target's logit."""
+    X, W, y, dl = certain(T, h, V, dtype)
+    ctx = tp.XentContext(T, h, V, dtype)
+    assert not bool(tp.xent_forward(ctx, X, W, y).any())
+    assert tp.check_device_status(ctx) == tp.OK
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_logits_at_the_end_of_fp32(tp, T):
+    """Logits of either sign up to 2^127.5: 1.44 times the maximum would not be a number any more."""
+    h, V = 64, 600
+    X, W, y, dl = make(T, h, V, seed=16)
+    X[:, 0], W[:, 0] = 2.0 ** 100, 0.0
+    W[V // 2, 0], W[V // 2 + 1, 0] = 1.375 * 2.0 ** 27, -1.375 * 2.0 ** 27  # 2^127.46 and its negative
+    y[:] = V // 2
+    y[1::2] = V // 2 + 1
+    ctx = tp.XentContext(T, h, V, torch.bfloat16)
+    loss = tp.xent_forward(ctx, X, W, y)
+    top = 1.375 * 2.0 ** 127
+    assert bool((ctx.lse == top).all())
+    assert not bool(loss[::2].any()) and bool((loss[1::2] == float("inf")).all())  # 2^128.5 is past fp32
