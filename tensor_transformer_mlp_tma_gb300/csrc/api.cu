@@ -1155,7 +1155,7 @@ Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
 // V = 16000: 79 against 96 us), and so do more tokens (T = 256: 64.4 against 74.0 us).
 struct StatsTile {
     int tile_n;  // 0: a pass over W without tiles, for few tokens
-    int64_t ranges, range;
+    int64_t ranges, range;  // of K, in both passes: lse and the recomputed logits come from the same sums
     bool pair;  // on CTA pairs
 };
 StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
@@ -1163,7 +1163,6 @@ StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
     const bool f32 = s->dtype == TPMLP_F32, pair = f32 || T > 128;
     const int64_t units = pair ? 76 : 152, tile_m = pair ? 256 : 128;
     const int64_t m = (T + tile_m - 1) / tile_m, tiles = m * ((V + 255) / 256);
-    if (tpmlp::xent_few(!f32, T, h)) return {0, 1, h, false};
     const bool few = m == 1 || tiles <= 4 * units;
     if (!f32 && !few && h <= 2048) return {512, 1, h, true};
     int64_t tile_n = 256;
@@ -1172,8 +1171,9 @@ StatsTile xent_stats_tile(const tpmlp_xent_shape *s) {
         tile_n = std::min<int64_t>(256, ((V + per - 1) / per + 31) / 32 * 32);
     }
     const int64_t longest = f32 ? 256 : 1024;
-    const int64_t ranges = (h + longest - 1) / longest;
-    return {static_cast<int>(tile_n), ranges, ((h + ranges - 1) / ranges + 63) / 64 * 64, pair};
+    const int64_t ranges = (h + longest - 1) / longest, range = ((h + ranges - 1) / ranges + 63) / 64 * 64;
+    if (tpmlp::xent_few(!f32, T, h)) tile_n = 0;
+    return {static_cast<int>(tile_n), ranges, range, pair};
 }
 
 struct XentLayout {
@@ -1325,7 +1325,9 @@ struct XentCall {
         GemmArgs g = base_args(rows.status);
         g.a = X, g.a_mn = false;
         g.b = w_rows(W, v0), g.b_mn = false;
-        g.M = s->tokens, g.N = n, g.K = s->hidden, g.kshard = s->hidden;
+        g.M = s->tokens, g.N = n, g.K = s->hidden;
+        g.nshards = xent_tc(s) ? static_cast<int>(L.stats.ranges) : 1;
+        g.kshard = xent_tc(s) ? L.stats.range : s->hidden;
         if (parts()) {
             g.a = xp(), g.lda = L.hp;
             g.b = wp(v0), g.ldb = L.hp;
@@ -1393,14 +1395,7 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const 
         g.part = reinterpret_cast<float2 *>(c.ws + c.L.part);
         g.target_logit = c.rows.target_logit;
         const StatsTile &t = c.L.stats;
-        if (t.tile_n < 512) {
-            g.tile_n = t.tile_n, g.cta_pair = t.pair;
-            // fp32: the six products one after the other, each in its ranges; where one range
-            // holds all of K, one accumulation takes the six (the five small ones first)
-            const int pairs = c.parts() ? 6 : 1;
-            g.nshards = t.ranges == 1 ? 1 : static_cast<int>(t.ranges) * pairs;
-            g.kshard = t.ranges == 1 ? t.range * pairs : t.range;
-        }
+        if (t.tile_n < 512) g.tile_n = t.tile_n, g.cta_pair = t.pair;
         e = c.launch("xent_stats", t.tile_n < 512 ? tpmlp::EPI_XENT_FOLD : tpmlp::EPI_XENT_STATS, g);
         if (e != cudaSuccess) return from_cuda(e);
     } else {

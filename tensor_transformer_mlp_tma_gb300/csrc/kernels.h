@@ -128,7 +128,8 @@ struct GemmArgs {
     // three bf16 matrices, a_part / b_part elements apart, and each k-block is
     // multiplied six times (every pair of parts but those below 2^-24).  ksplit > 1 (ACC32):
     // the K range in ksplit parts of kshard elements, each an output [M, N] of its
-    // own, one after the other in out0.
+    // own, one after the other in out0.  XENT_FOLD and the XENT_GRADs take K in nshards ranges of
+    // kshard elements (all pairs of parts in one accumulation where there is one range).
     int parts;
     int64_t a_part, b_part;
     int ksplit;

@@ -1068,8 +1068,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const Params p) {
     using C = Cfg<CG, TILE_N, EPI>;
     constexpr bool PAIR = CG == 2;
-    constexpr bool FOLD = (EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32);
     constexpr bool WIDE = TILE_N == 512;
+    constexpr bool FOLD = EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32 ||
+                          (is_grad(EPI) && !WIDE);
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
     constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
                                           : ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
@@ -1833,7 +1834,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 if (c == CHUNKS - 1) xent_stats_flush(p, row, 2 * nb + half, xr);
                                 continue;
                             }
-                            finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg);
+                            finish_chunk<EPI, HEADS>(p, &tmO0, &tmO1, &tmO2, v, row, row0, col0 + c * 32, zb, lane, stg, nullptr,
+                                                     -1, 0, nullptr, nullptr, is_xent(EPI) ? &xr : nullptr);
                         }
                     }
                 } else {
@@ -2265,11 +2267,11 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     p.colsum_part = g.colsum_part;
     p.batch = static_cast<int>(nb * splits);
     p.matrices = static_cast<int>(nb);
-    p.kb_seg = p.kb_per_shard;
+    p.kb_seg = p.nshards * p.kb_per_shard;
     p.pairs = SEG && g.parts > 1 ? 6 : 1;
-    if (EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32)
-        p.kb_seg = p.nshards * p.kb_per_shard / p.pairs;
-    else
+    if (p.nshards > 1)  // the pairs one after the other, each in its ranges
+        p.nshards *= p.pairs;
+    else  // one accumulation takes them all, the small products first
         p.kb_per_shard *= p.pairs;
     if (EPI == EPI_NS_FINAL) {
         // Q's low part times X, (X's low part times Q,) then the high parts; in a wide matrix's

@@ -539,3 +539,58 @@ def test_logits_at_the_end_of_fp32(tp, T):
     top = 1.375 * 2.0 ** 127
     assert bool((ctx.lse == top).all())
     assert not bool(loss[::2].any()) and bool((loss[1::2] == float("inf")).all())  # 2^128.5 is past fp32
+
+
+def own_bits(tp, T, h, V, dtype, **kw):
+    """p - 1 of a token that is certain of its target is exactly 0 if the backward pass computes the
+    same bits for the target's logit, which is lse; else it is an ulp of 270 or more."""
+    X, W, y, dl = certain(T, h, V, dtype)
+    _, _, grads = run(tp, X, W, y, dl, **kw)
+    assert not bool(grads["dX"].any()) and not bool(grads["dW"].any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", [
+    (9, 256, 300), (100, 1000, 2000), (128, 2048, 12000), (200, 4096, 1500), (600, 8192, 2000), (1300, 1032, 9000),
+    (2500, 2048, 9000), (2500, 4096, 9000), (4000, 200, 70), (4000, 520, 3000), (333, 2056, 20000)])
+def test_both_passes_compute_the_same_logits(tp, T, h, V, dtype):
+    own_bits(tp, T, h, V, dtype)
+    own_bits(tp, T, h, V, dtype, piece=1024)
+
+
+def check_confident(tp, T, h, V, dtype, **kw):
+    """Tokens fairly sure of their target (1 - p from 1e-6 to 1e-2), every element.  The logits of
+    both passes are the same, with errors of at most e (see above) of the exact ones, so p
+    is a softmax of logits that are off by e: p moves by p (1 - p) (exp(2 e) - 1).  lse is rounded by
+    2^-24 of itself, and 2^-23 of the largest logit is taken, with 2^-21 for the exponentials and the
+    logarithm, which p - 1 moves by however small it is."""
+    X, W, y, dl = make(T, h, V, torch.float32, seed=T + h)
+    X = 0.3 * X + torch.linspace(9, 13, T, device="cuda")[:, None] * W[y]
+    X, W = X.to(dtype), W.to(dtype)
+    ctx, loss, grads = run(tp, X, W, y, dl, **kw)
+    ref = reference(X, W, y, dl)
+    Xa, Wa = X.double().abs(), W.double().abs()
+    e = (h + 8) * 2.0 ** -23 * (Xa @ Wa.t()).amax(1)
+    P = torch.exp(ref["S"] - ref["lse"][:, None])
+    rest = 1 - P
+    at = y[:, None]
+    sure = -torch.expm1(ref["S"].gather(1, at) - ref["lse"][:, None])  # 1 - p without cancellation
+    rest.scatter_(1, at, sure)
+    dS = P.scatter(1, at, -sure) * dl.double()[:, None]
+    small = 2.0 ** -23 * ref["S"].abs().amax(1) + 2.0 ** -21
+    u = torch.finfo(dtype).eps / 2
+    err = P * (rest * torch.expm1(2 * e)[:, None] + small[:, None]) * dl.double()[:, None]
+    err = err + (u + 2.0 ** -22) * (dS.abs() + err) + 2 * 2.0 ** -126
+    for name, got, want, a, s, other in (("dX", grads["dX"], dS @ W.double(), dS.abs(), err, Wa),
+                                         ("dW", grads["dW"], dS.t() @ X.double(), dS.abs().t(), err.t(), Xa)):
+        n = a.shape[1]
+        tol = s @ other + (n + 64) * 2.0 ** -23 * (a @ other)
+        tol = tol + u * (want.abs() + tol) + 2.0 ** -126
+        bad = (got.double() - want).abs() > tol
+        assert not bool(bad.any()), (name, int(bad.sum()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", [(20, 256, 3000), (64, 1024, 2000), (300, 4096, 2000), (600, 8192, 2000), (2500, 2048, 9000)])
+def test_confident_tokens(tp, T, h, V, dtype):
+    check_confident(tp, T, h, V, dtype)
