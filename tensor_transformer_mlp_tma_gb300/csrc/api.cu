@@ -1450,7 +1450,14 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
         GemmArgs g = c.logits(X, W, v0, n);
         const int64_t ld = tc ? c.L.piece : n;  // row pitch of dS, and between its parts
         const int64_t ds_part = T * ld;
-        if (tc) {
+        if (tc && c.L.stats.tile_n == 0) {  // few tokens: the logits of the forward pass's kernel
+            tpmlp::RowArgs rows = c.rows;
+            rows.vocab = n;
+            const tpmlp::FewGrad d = {lse, dloss, unit, ds, ld, ds_part, v0, s->vocab};
+            e = c.kernel("xent_few_ds", [&] {
+                return tpmlp::launch_xent_few_grad(!f32, rows, X, c.w_rows(W, v0), h, d, c.st);
+            });
+        } else if (tc) {
             g.out0 = ds, g.ldo = ld;
             g.row_lse = lse, g.dloss = dloss, g.vocab = s->vocab, g.unit = unit;
             e = c.launch("xent_ds", f32 ? tpmlp::EPI_XENT_GRAD3 : tpmlp::EPI_XENT_GRAD, g);

@@ -235,6 +235,17 @@ bool xent_few(bool is_bf16, int64_t tokens, int64_t hidden);
 int64_t xent_few_groups(int64_t vocab);
 cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden, float2 *part,
                             float *loss, float *lse, cudaStream_t st);
+// dS of few tokens over vocabulary rows col0 .. col0 + RowArgs::vocab - 1, W at the first of them, from
+// logits of the same bits as launch_xent_few's.  out: [tokens][ld] in bf16, in units of *unit, or
+// for fp32 three such matrices, `part` elements apart.
+struct FewGrad {
+    const float *lse, *dloss;
+    float *unit;
+    void *out;
+    int64_t ld, part, col0, all_vocab;
+};
+cudaError_t launch_xent_few_grad(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t hidden,
+                                 const FewGrad &d, cudaStream_t st);
 // out[r][c] = sum over the `splits` matrices [rows][ld] of in, in order, in the output's type.
 // With unit the sums are multiplied by *unit.
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,

@@ -107,7 +107,44 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const RowAr
 // its copies of 128-byte pieces of many rows read W at 3.2 to 3.6 TB/s (T = 1 to 8).
 // Bound by W's bytes: h = 4096, V = 32768 in 47 us (5.7 TB/s) at T = 1, h = 8192, V = 50000
 // at 6.4 TB/s.
+// The backward pass runs the same kernels (GRAD) for dS, so that its logits are those of lse to
+// the bit: 1 - p of a confident token is then as exact as the logits' differences.
 constexpr int FEW_THREADS = 512, FEW_ROWS = 4;
+
+// One token's row of dS, element by element.
+struct GradRow {
+    float lse, g;
+    int64_t tcol;  // the target's column of this piece
+};
+__device__ __forceinline__ GradRow grad_row(const RowArgs &a, const FewGrad &d, int64_t t, float unit) {
+    GradRow r = {0.0f, 0.0f, -1};
+    if (t >= a.tokens) return r;
+    const int64_t y = a.target[t];
+    r.lse = d.lse[t];
+    if (y != a.ignore_index && y >= 0 && y < d.all_vocab) r.g = __fdiv_rn(d.dloss[t], unit), r.tcol = y - d.col0;
+    return r;
+}
+__device__ __forceinline__ float grad_unit(const RowArgs &a, const FewGrad &d) {
+    const float unit = xent_find_unit(a.target, d.dloss, a.tokens, a.ignore_index, d.all_vocab);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *d.unit = unit;
+    return unit;
+}
+template <typename E>
+__device__ __forceinline__ void grad_put(const FewGrad &d, const GradRow &r, int64_t t, int64_t col, float z) {
+    const float p = __expf(z - r.lse);
+    float v = r.g == 0.0f ? 0.0f : (col == r.tcol ? p - 1.0f : p) * r.g;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(d.out) + t * d.ld + col;
+    if constexpr (sizeof(E) == 2) {
+        *out = __float2bfloat16_rn(v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k, out += d.part) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            *out = h;
+            v -= __bfloat162float(h);
+        }
+    }
+}
 
 // EC consecutive elements as fp32 pairs.
 template <typename E, int EC>
@@ -142,9 +179,9 @@ struct Chunk<float, 1> {  // rows that do not start on 16 bytes
     __device__ __forceinline__ float2 pair(int) const { return make_float2(w, 0.0f); }
 };
 
-template <typename E, int EC, int T>
+template <typename E, int EC, int T, bool GRAD>
 __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, const E *X, const E *W, int64_t h,
-                                                            float2 *part, float *loss, float *lse) {
+                                                            float2 *part, float *loss, float *lse, const FewGrad d) {
     extern __shared__ __align__(16) uint8_t few_smem[];
     E *xs = reinterpret_cast<E *>(few_smem);  // [T][h]
     __shared__ float2 sh[FEW_THREADS / 32][T];
@@ -168,7 +205,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, co
     // After the reduction below lane l holds sum number l >> (5 - LOG): row / T, token % T.
     const int mine = lane >> (5 - LOG), my_row = mine / T, my_t = mine % T;
     int64_t target = -1;
-    if (my_t < a.tokens) {
+    GradRow gr;
+    if constexpr (GRAD) {
+        // in fp32 dS keeps all its bits, and needs no unit
+        gr = grad_row(a, d, my_t, sizeof(E) == 2 ? grad_unit(a, d) : 1.0f);
+    } else if (my_t < a.tokens) {
         target = a.target[my_t];
         if (target == a.ignore_index) target = -1;
     }
@@ -222,11 +263,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, co
                 v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
             }
         }
-        if (my_row < n) {
+        if constexpr (GRAD) {
+            // 2^(5 - LOG) lanes hold each sum
+            if (my_row < n && my_t < a.tokens && (lane & (31 >> LOG)) == 0) grad_put<E>(d, gr, my_t, r0 + my_row, v[0]);
+        } else if (my_row < n) {
             join(m, s, v[0], 1.0f);
             if (target == r0 + my_row) a.target_logit[my_t] = v[0];
         }
     }
+    if constexpr (GRAD) return;
     // the rows of one token sit in lanes that differ in bits 4 and 3
 #pragma unroll
     for (int off = 16; off >= 8; off >>= 1) {
@@ -254,10 +299,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_kernel(const RowArgs a, co
 // With 16 or 32 tokens the same kernel was no faster than the tcgen05 tiles.
 constexpr int SLIM_ROWS = 16;
 
-template <int SLIM_WARPS>
+template <int SLIM_WARPS, bool GRAD>
 __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(const RowArgs a, const __nv_bfloat16 *X,
                                                               const __nv_bfloat16 *W, int64_t h, int hp,
-                                                              float2 *part, float *loss, float *lse) {
+                                                              float2 *part, float *loss, float *lse, const FewGrad fg) {
     extern __shared__ __align__(16) uint8_t slim_smem[];
     // [8][hp], hp = h rounded up to 32, and 8 more: a row's 16-byte pieces then start 4
     // banks after the row before, and the eight tokens that a load touches do not collide
@@ -276,11 +321,16 @@ __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(
     __syncthreads();
     int64_t target[2];
     float m[2], s[2];
+    GradRow gr[2];
+    float unit = 1.0f;
+    if constexpr (GRAD) unit = grad_unit(a, fg);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int t = 2 * q + j;
         target[j] = -1;
-        if (t < a.tokens && a.target[t] != a.ignore_index) target[j] = a.target[t];
+        if constexpr (GRAD)
+            gr[j] = grad_row(a, fg, t, unit);
+        else if (t < a.tokens && a.target[t] != a.ignore_index) target[j] = a.target[t];
         m[j] = -INFINITY, s[j] = 0.0f;
     }
     int it = 0;
@@ -313,13 +363,17 @@ __global__ void __launch_bounds__(32 * SLIM_WARPS, 16 / SLIM_WARPS) slim_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = r + 8 * (j >> 1);
-                if (row < rows) {
+                if constexpr (GRAD) {
+                    const int t = 2 * q + (j & 1);
+                    if (row < rows && t < a.tokens) grad_put<__nv_bfloat16>(fg, gr[j & 1], t, r0 + row, z[j]);
+                } else if (row < rows) {
                     join(m[j & 1], s[j & 1], z[j], 1.0f);
                     if (target[j & 1] == r0 + row) a.target_logit[2 * q + (j & 1)] = z[j];
                 }
             }
         }
     }
+    if constexpr (GRAD) return;
     // One token's rows: 8 lanes of every warp.
     float2 *all = reinterpret_cast<float2 *>(&sums[0][0][0]);  // [SLIM_WARPS][8]
     __syncthreads();
@@ -513,52 +567,75 @@ int64_t xent_few_groups(int64_t vocab) {
     return b < 304 ? b : 304;
 }
 
-template <int WARPS>
-static cudaError_t launch_slim(const RowArgs &a, const void *X, const void *W, int64_t h, int64_t smem, float2 *part,
-                               float *loss, float *lse, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(xent::slim_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(XENT_FEW_SMEM));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(xent::slim_kernel<WARPS>, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), 32 * WARPS,
-                      static_cast<size_t>(smem), st, a, static_cast<const __nv_bfloat16 *>(X),
-                      static_cast<const __nv_bfloat16 *>(W), h, static_cast<int>((h + 31) / 32 * 32), part, loss, lse);
-}
+namespace {
+// What the two passes' launches of a few-token kernel have in common, and what each adds.
+struct FewCall {
+    RowArgs a;
+    const void *X, *W;
+    int64_t h;
+    float2 *part;
+    float *loss, *lse;
+    FewGrad grad;
+    cudaStream_t st;
+};
 
-template <typename E, int EC, int T>
-static cudaError_t launch_few(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part, float *loss, float *lse,
-                              cudaStream_t st) {
-    auto kernel = xent::few_kernel<E, EC, T>;
-    const size_t smem = static_cast<size_t>(T) * h * sizeof(E);
+template <bool GRAD, int WARPS>
+cudaError_t launch_slim(const FewCall &c, int64_t smem) {
+    auto kernel = xent::slim_kernel<WARPS, GRAD>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(XENT_FEW_SMEM));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(xent_few_groups(a.vocab))), xent::FEW_THREADS, smem, st, a,
-                      static_cast<const E *>(X), static_cast<const E *>(W), h, part, loss, lse);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(xent_few_groups(c.a.vocab))), 32 * WARPS,
+                      static_cast<size_t>(smem), c.st, c.a, static_cast<const __nv_bfloat16 *>(c.X),
+                      static_cast<const __nv_bfloat16 *>(c.W), c.h, static_cast<int>((c.h + 31) / 32 * 32), c.part,
+                      c.loss, c.lse, c.grad);
 }
 
-template <typename E, int EC>
-static cudaError_t launch_few_t(const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
-                                float *loss, float *lse, cudaStream_t st) {
-    if (a.tokens <= 1) return launch_few<E, EC, 1>(a, X, W, h, part, loss, lse, st);
-    if (a.tokens <= 2) return launch_few<E, EC, 2>(a, X, W, h, part, loss, lse, st);
-    if (a.tokens <= 4) return launch_few<E, EC, 4>(a, X, W, h, part, loss, lse, st);
-    return launch_few<E, EC, 8>(a, X, W, h, part, loss, lse, st);
+template <bool GRAD, typename E, int EC, int T>
+cudaError_t launch_few(const FewCall &c) {
+    auto kernel = xent::few_kernel<E, EC, T, GRAD>;
+    const size_t smem = static_cast<size_t>(T) * c.h * sizeof(E);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(XENT_FEW_SMEM));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(xent_few_groups(c.a.vocab))), xent::FEW_THREADS, smem, c.st,
+                      c.a, static_cast<const E *>(c.X), static_cast<const E *>(c.W), c.h, c.part, c.loss, c.lse, c.grad);
 }
 
-cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
-                            float *loss, float *lse, cudaStream_t st) {
+template <bool GRAD, typename E, int EC>
+cudaError_t launch_few_t(const FewCall &c) {
+    if (c.a.tokens <= 1) return launch_few<GRAD, E, EC, 1>(c);
+    if (c.a.tokens <= 2) return launch_few<GRAD, E, EC, 2>(c);
+    if (c.a.tokens <= 4) return launch_few<GRAD, E, EC, 4>(c);
+    return launch_few<GRAD, E, EC, 8>(c);
+}
+
+// The choice depends on the tokens, h and the alignment alone, so that both passes and every
+// piece of W (whose rows of 16 bytes start on 16 bytes) take the same kernel.
+template <bool GRAD>
+cudaError_t launch_few_any(bool is_bf16, const FewCall &c) {
     if (is_bf16) {
-        if (a.tokens <= 1) return launch_few<__nv_bfloat16, 8, 1>(a, X, W, h, part, loss, lse, st);
+        if (c.a.tokens <= 1) return launch_few<GRAD, __nv_bfloat16, 8, 1>(c);
         // 16 warps per SM: two blocks, of which one computes while the other is at its barrier,
         // where two copies of X leave room for the loads in L1; one block of all 16 warps where
         // they do not (T = 4, V = 50000: h = 6144 4.4 TB/s with two blocks, h = 8192 5.8 with one).
-        const int64_t smem = few_smem(true, a.tokens, h);
-        return smem <= 72 * 1024 ? launch_slim<8>(a, X, W, h, smem, part, loss, lse, st)
-                                  : launch_slim<16>(a, X, W, h, smem, part, loss, lse, st);
+        const int64_t smem = few_smem(true, c.a.tokens, c.h);
+        return smem <= 72 * 1024 ? launch_slim<GRAD, 8>(c, smem) : launch_slim<GRAD, 16>(c, smem);
     }
-    const uintptr_t both = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W);
-    if (h % 4 == 0 && (both & 15) == 0) return launch_few_t<float, 4>(a, X, W, h, part, loss, lse, st);
-    return launch_few_t<float, 1>(a, X, W, h, part, loss, lse, st);
+    const uintptr_t both = reinterpret_cast<uintptr_t>(c.X) | reinterpret_cast<uintptr_t>(c.W);
+    if (c.h % 4 == 0 && (both & 15) == 0) return launch_few_t<GRAD, float, 4>(c);
+    return launch_few_t<GRAD, float, 1>(c);
+}
+}  // namespace
+
+cudaError_t launch_xent_few(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t h, float2 *part,
+                            float *loss, float *lse, cudaStream_t st) {
+    return launch_few_any<false>(is_bf16, {a, X, W, h, part, loss, lse, {}, st});
+}
+
+cudaError_t launch_xent_few_grad(bool is_bf16, const RowArgs &a, const void *X, const void *W, int64_t h,
+                                 const FewGrad &d, cudaStream_t st) {
+    return launch_few_any<true>(is_bf16, {a, X, W, h, nullptr, nullptr, nullptr, d, st});
 }
 
 cudaError_t launch_sum_splits(bool is_bf16, const float *in, int splits, int64_t rows, int64_t cols, int64_t ld,

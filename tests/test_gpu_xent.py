@@ -594,3 +594,41 @@ def check_confident(tp, T, h, V, dtype, **kw):
 @pytest.mark.parametrize("T,h,V", [(20, 256, 3000), (64, 1024, 2000), (300, 4096, 2000), (600, 8192, 2000), (2500, 2048, 9000)])
 def test_confident_tokens(tp, T, h, V, dtype):
     check_confident(tp, T, h, V, dtype)
+
+
+FEW = [(1, 8, 500), (1, 256, 300), (1, 4096, 9001), (2, 1000, 3000), (3, 4096, 2000), (5, 8192, 1500), (8, 264, 5003)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", [s for s in FEW if s[1] >= 256])
+def test_both_passes_compute_the_same_logits_of_few_tokens(tp, T, h, V, dtype):
+    own_bits(tp, T, h, V, dtype)
+    own_bits(tp, T, h, V, dtype, piece=136)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", FEW)
+def test_few_confident_tokens(tp, T, h, V, dtype):
+    check_confident(tp, T, h, V, dtype)
+    check_confident(tp, T, h, V, dtype, piece=64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [1, 2, 4, 6])
+def test_gradients_of_few_tokens(tp, T, dtype):
+    """Pieces that end inside a group of rows, ignored targets, a target outside the vocabulary, and
+    one gradient at a time."""
+    h, V = 72, 1003
+    for seed in range(4):
+        X, W, y, dl = make(T, h, V, dtype, seed=seed, ignored=0.3)
+        if seed == 3:
+            y[-1] = V
+        ctx = tp.XentContext(T, h, V, dtype, piece=(0, 8, 40, 512)[seed])
+        loss = tp.xent_forward(ctx, X, W, y)
+        assert tp.check_device_status(ctx) == (tp.ERR_INVALID_ARG if seed == 3 else tp.OK)
+        grads = tp.xent_backward(ctx, dl)
+        assert tp.check_device_status(ctx) == tp.OK
+        y = torch.where(y == V, IGN, y)
+        check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
+        assert torch.equal(tp.xent_backward(ctx, dl, need_dW=False)["dX"], grads["dX"])
+        assert torch.equal(tp.xent_backward(ctx, dl, need_dX=False)["dW"], grads["dW"])
