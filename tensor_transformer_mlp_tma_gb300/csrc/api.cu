@@ -1108,28 +1108,39 @@ int64_t xent_piece(const tpmlp_xent_shape *s) {
 // halves of such): S ranges run at once, each into an fp32 matrix of its own, which
 // sum_splits adds up.  The model counts waves of half tiles at the rate of a pair's
 // share of the tensor rate, and 8 bytes written and read per split output at the copy
-// rate.  fp32 operands also bound the range to 2048: the tensor core cuts off
-// (does not round) the accumulator at every 16-element step, 2^-24 on average,
-// and 128 such steps stay below the fp32 result's own 1e-6.
+// rate.
 // Measured: dX of T = 1001, h = 1000, V = 30011 (16 tiles of 256 x 256) 173 us in one range,
 // 54 + 8 us split.
+// fp32 operands also take each split in `ranges` ranges of at most 512, which the epilogue adds up
+// in fp32, however long K is (see xent_stats_tile): T = 2100, h = 8192, V = 2000, dX and dW to 6e-7
+// of themselves (the FFMA path 8e-7) in 1010 us, in ranges of 256 3.5e-7 in 1064, of 1024 1.2e-6 in 981.
 struct Split {
     int n;
-    int64_t len;
+    int64_t len;  // of a split: ranges * range
+    int ranges;
+    int64_t range;
+    void apply(GemmArgs &g) const {
+        if (n > 1)
+            g.ksplit = n, g.nshards = ranges, g.kshard = range;
+        else if (ranges > 1)  // of what there is: the last piece of a vocabulary may be short
+            g.nshards = static_cast<int>((g.K + range - 1) / range), g.kshard = range;
+    }
 };
 Split xent_split(int64_t M, int64_t N, int64_t K, bool f32) {
     const double pair_rate = 24e12 / (f32 ? 6 : 1), bytes_rate = 6e12;
     const int64_t halves = (M + 255) / 256 * ((N + 255) / 256), units = 76;
-    Split best{1, (K + 63) / 64 * 64};
+    Split best{1, 0, 1, 0};
     double best_t = 0.0;
-    const int64_t fewest = f32 ? std::min<int64_t>(64, (K + 2047) / 2048) : 1;
-    for (int64_t n = fewest; n < fewest + 16; ++n) {
-        const int64_t len = ((K + n - 1) / n + 63) / 64 * 64;
-        if (n > fewest && len < 256) break;
+    for (int64_t n = 1; n <= (f32 ? 80 : 16); ++n) {
+        int64_t len = ((K + n - 1) / n + 63) / 64 * 64;
+        if (n > 1 && len < 256) break;
+        const int64_t ranges = f32 ? (len + 511) / 512 : 1, range = ((len + ranges - 1) / ranges + 63) / 64 * 64;
+        len = ranges * range;
         const double waves = static_cast<double>((halves * n + units - 1) / units);
         const double t = waves * (static_cast<double>(len) * 2 * 256 * 256 / pair_rate + 1e-6) +
                          (n > 1 ? static_cast<double>(n) * M * N * 8 / bytes_rate + 4e-6 : 0.0);
-        if (best_t == 0.0 || t < best_t) best_t = t, best = {static_cast<int>((K + len - 1) / len), len};
+        if (best_t == 0.0 || t < best_t)
+            best_t = t, best = {static_cast<int>((K + len - 1) / len), len, static_cast<int>(ranges), range};
     }
     return best;
 }
@@ -1201,7 +1212,7 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
     L.groups = tc && L.stats.tile_n == 512 ? (s->vocab + 127) / 128 : static_cast<int64_t>(stored);
     L.hp = (s->hidden + 63) / 64 * 64;
     L.ldo = (s->hidden + 3) / 4 * 4;
-    L.dx = L.dw = {1, 0};
+    L.dx = L.dw = {1, 0, 1, 0};
     if (tc && s->tokens > 0) {
         L.dx = xent_split(s->tokens, s->hidden, L.piece, f32);
         L.dw = xent_split(L.piece, s->hidden, s->tokens, f32);
@@ -1481,7 +1492,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
             bool in_place = true;
             if (tc) {
                 in_place = c.L.dw.n == 1 && (!f32 || (h % 4 == 0 && aligned16(out)));
-                if (c.L.dw.n > 1) w.ksplit = c.L.dw.n, w.kshard = c.L.dw.len;
+                c.L.dw.apply(w);
                 if (!in_place) w.out0 = c.ws + c.L.dwacc, w.ldo = c.L.ldo;
                 if (f32) {
                     w.b = c.xp(), w.ldb = c.L.hp;
@@ -1489,9 +1500,10 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
                 }
             }
             w.unit = unit;
-            e = c.launch("xent_dw", !tc                 ? tpmlp::EPI_STORE
-                                    : f32 || !in_place ? tpmlp::EPI_ACC32
-                                                       : tpmlp::EPI_STORE_UNIT, w);
+            e = c.launch("xent_dw", !tc         ? tpmlp::EPI_STORE
+                                    : f32       ? tpmlp::EPI_FOLD32
+                                    : !in_place ? tpmlp::EPI_ACC32
+                                                : tpmlp::EPI_STORE_UNIT, w);
             if (e == cudaSuccess && !in_place)
                 e = c.kernel("xent_dw_sum", [&] {
                     return tpmlp::launch_sum_splits(!f32, reinterpret_cast<float *>(c.ws + c.L.dwacc), c.L.dw.n, n, h,
@@ -1507,7 +1519,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
             x.out0 = dx_in_place ? dX : static_cast<void *>(acc);
             x.accumulate = k > 0;
             if (tc) {
-                if (c.L.dx.n > 1) x.ksplit = c.L.dx.n, x.kshard = c.L.dx.len;
+                c.L.dx.apply(x);
                 if (!dx_in_place) x.ldo = c.L.ldo;
                 if (f32) {
                     x.b = c.wp(v0), x.ldb = c.L.hp;
@@ -1516,7 +1528,9 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *s, const void *X, const
             }
             const bool rounds = dx_in_place && !f32;  // one product gives the bf16 result
             x.unit = unit;
-            e = c.launch("xent_dx", !rounds ? tpmlp::EPI_ACC32 : (tc ? tpmlp::EPI_STORE_UNIT : tpmlp::EPI_STORE), x);
+            e = c.launch("xent_dx", tc && f32 ? tpmlp::EPI_FOLD32
+                                    : !rounds ? tpmlp::EPI_ACC32
+                                              : (tc ? tpmlp::EPI_STORE_UNIT : tpmlp::EPI_STORE), x);
             if (e != cudaSuccess) return from_cuda(e);
         }
     }

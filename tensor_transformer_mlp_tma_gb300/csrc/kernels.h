@@ -53,6 +53,7 @@ enum Epi : int {
     EPI_XENT_STATS = 7, // per row: max and sum of exponentials per 128 columns, the target's logit -- X W^T
     EPI_XENT_GRAD = 8,  // dS = (exp(acc - lse[row]) - [col = target]) * g[row]  -- X W^T -> dS
     EPI_ACC32 = 9,      // out (fp32) = acc, or out += acc                  -- dX and dW, piece by piece
+    EPI_FOLD32 = 20,    // ACC32 over K in nshards ranges, added up in fp32 -- dX and dW of fp32, from three parts
     EPI_NS_GRAM = 10,   // A = scale * acc, symmetric, fp16                 -- X X^T
     EPI_NS_POLY = 11,   // C = diag I + alpha A + scale * acc, symmetric, fp16 -- A A
     EPI_NS_UPDATE = 12, // X' = alpha hi + beta lo + scale * acc as hi' + lo', fp16 -- C X
@@ -124,16 +125,16 @@ struct GemmArgs {
     // Row pitches in elements of operand A and B and of the output (0: contiguous),
     // multiples of 8; batch must be 1 where one is set.
     int64_t lda, ldb, ldo;
-    // EPI_XENT_*, EPI_ACC32.  parts = 3: the operands are fp32 numbers given as the sum of
+    // EPI_XENT_*, EPI_FOLD32.  parts = 3: the operands are fp32 numbers given as the sum of
     // three bf16 matrices, a_part / b_part elements apart, and each k-block is
-    // multiplied six times (every pair of parts but those below 2^-24).  ksplit > 1 (ACC32):
-    // the K range in ksplit parts of kshard elements, each an output [M, N] of its
-    // own, one after the other in out0.  XENT_FOLD and the XENT_GRADs take K in nshards ranges of
-    // kshard elements (all pairs of parts in one accumulation where there is one range).
+    // multiplied six times (every pair of parts but those below 2^-22).  ksplit > 1 (ACC32, FOLD32):
+    // the K range in ksplit parts of nshards * kshard elements, each an output [M, N] of its
+    // own, one after the other in out0.  XENT_FOLD, FOLD32 and the XENT_GRADs take K (of a split) in
+    // nshards ranges of kshard elements (all pairs of parts in one accumulation where there is one range).
     int parts;
     int64_t a_part, b_part;
     int ksplit;
-    bool small_tile;  // 128 x 128 tiles on single CTAs (XENT_GRAD, XENT_GRAD3, ACC32, STORE)
+    bool small_tile;  // 128 x 128 tiles on single CTAs (XENT_GRAD, XENT_GRAD3, ACC32, FOLD32, STORE_UNIT)
     // EPI_XENT_STATS, EPI_XENT_GRAD: rows are tokens, columns vocabulary rows
     // col0 .. col0 + N - 1 of W.
     const int64_t *target;   // [M]
@@ -143,7 +144,7 @@ struct GemmArgs {
     const float *row_lse;    // GRAD: [M]
     const float *dloss;      // GRAD: [M]; a target that is ignored or outside [0, vocab) has none
     float *unit;             // GRAD: where its unit goes; EPI_STORE_UNIT: where it is read
-    bool accumulate;         // EPI_ACC32: add to what out0 holds
+    bool accumulate;         // EPI_ACC32, EPI_FOLD32: add to what out0 holds
     int tile_n;              // EPI_XENT_FOLD: columns per tile, a multiple of 32 up to 256 (0: 256)
     // EPI_NS_*: fp16 operands.  POLY reads A through aux; UPDATE and LAST read the
     // two parts of X through aux (high) and aux2 (low).  out0 / out1: X' high, low.

@@ -211,7 +211,7 @@ __host__ __device__ constexpr bool is_ns(int epi) {
 __host__ __device__ constexpr bool is_ns2(int epi) { return epi == EPI_NS_GRAM32 || epi == EPI_NS_FINAL; }
 __host__ __device__ constexpr bool is_f16(int epi) { return is_ns(epi) || is_ns2(epi) || epi == EPI_NS_GRAMS; }
 __host__ __device__ constexpr bool is_out32(int epi) {
-    return epi == EPI_ACC32 || epi == EPI_NS_GRAM32 || epi == EPI_NS_GRAMS;
+    return epi == EPI_ACC32 || epi == EPI_FOLD32 || epi == EPI_NS_GRAM32 || epi == EPI_NS_GRAMS;
 }
 __host__ __device__ constexpr bool is_sym(int epi) {
     return epi == EPI_NS_GRAM || epi == EPI_NS_POLY || epi == EPI_NS_GRAMS;
@@ -220,7 +220,7 @@ __host__ __device__ constexpr bool is_grad(int epi) { return epi == EPI_XENT_GRA
 __host__ __device__ constexpr bool is_stats(int epi) { return epi == EPI_XENT_STATS || epi == EPI_XENT_FOLD; }
 __host__ __device__ constexpr bool is_xent(int epi) { return is_stats(epi) || is_grad(epi); }
 // Products whose K range can run over pairs of operand parts, or be split.
-__host__ __device__ constexpr bool has_segments(int epi) { return is_xent(epi) || epi == EPI_ACC32; }
+__host__ __device__ constexpr bool has_segments(int epi) { return is_xent(epi) || epi == EPI_ACC32 || epi == EPI_FOLD32; }
 
 // The pairs of parts (a, b) of an fp32 product, two bits each, from the smallest:
 // (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).  Part i is at most 2^-8i of the number (each is
@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr bool PAIR = CG == 2;
     constexpr bool WIDE = TILE_N == 512;
     constexpr bool FOLD = EPI == EPI_FOLD_BIAS || EPI == EPI_FOLD || EPI == EPI_XENT_FOLD || EPI == EPI_NS_GRAM32 ||
-                          (is_grad(EPI) && !WIDE);
+                          EPI == EPI_FOLD32 || (is_grad(EPI) && !WIDE);
     constexpr int MMA_N = WIDE ? 256 : TILE_N;  // N of one MMA instruction
     constexpr uint32_t IDESC = is_f16(EPI) ? ptx::idesc_f16_f32(C::TILE_M, MMA_N, A_MN, B_MN)
                                           : ptx::idesc_bf16_f32(C::TILE_M, MMA_N, A_MN, B_MN);
@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // each epilogue warp finishes TILE_N / 2 columns of its 32 rows, in 32-column chunks
     constexpr int CHUNKS = TILE_N / 64;
     constexpr bool SMALL_TILE = EPI == EPI_NS_GRAM32 || EPI == EPI_NS_GRAMS || is_ns_tile(EPI) || is_grad(EPI) ||
-                                EPI == EPI_ACC32 || EPI == EPI_STORE_UNIT;
+                                EPI == EPI_ACC32 || EPI == EPI_FOLD32 || EPI == EPI_STORE_UNIT;
     static_assert(TILE_N == BN || TILE_N == 512 || (TILE_N == 128 && CG == 2 && EPI == EPI_STORE) ||
                       (TILE_N == 128 && CG == 1 && !HEADS && SMALL_TILE),
                   "narrow tile: CTA pairs and plain store, or single CTAs and the small products");
@@ -2343,10 +2343,10 @@ static cudaError_t launch_t(const GemmArgs &g, int num_sms, cudaStream_t st) {
     // TPMLP_SERPENTINE=0 walks K upwards in every wave (a tuning knob, read per call).
     {
         const char *se = std::getenv("TPMLP_SERPENTINE");
-        // (Not the cross entropy's logits: a logit is summed in the same order in whichever wave its tile
-        // is, and one accumulation of fp32 parts takes the small products first.)
+        // (Not the cross entropy's logits, which are summed in the same order in whichever wave their
+        // tile is, and not fp32 parts, of which one accumulation takes the small products first.)
         p.serpentine =
-            !is_xent(EPI) && (WIDE || (!HEADS && g.causal_k == 0 && !g.skip_upper)) && !(se && se[0] == '0') ? 1 : 0;
+            !is_xent(EPI) && p.pairs == 1 && (WIDE || (!HEADS && g.causal_k == 0 && !g.skip_upper)) && !(se && se[0] == '0') ? 1 : 0;
     }
     if (WIDE) {
         const char *tail_env = std::getenv("TPMLP_WIDE_TAIL");
@@ -2397,11 +2397,11 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
         if (!g.cta_pair) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
         return launch_t<EPI, A_MN, B_MN, 2>(g, num_sms, st);
     } else {
-    if constexpr (is_grad(EPI) || EPI == EPI_ACC32 || EPI == EPI_STORE_UNIT) {
+    if constexpr (is_grad(EPI) || EPI == EPI_ACC32 || EPI == EPI_FOLD32 || EPI == EPI_STORE_UNIT) {
         if (g.small_tile) return launch_t<EPI, A_MN, B_MN, 1, false, 128>(g, num_sms, st);
     }
     if constexpr (EPI == EPI_BIAS_GELU || EPI == EPI_DGELU || (EPI == EPI_STORE && A_MN == B_MN) ||
-                  EPI == EPI_STORE_UNIT || has_segments(EPI)) {
+                  EPI == EPI_STORE_UNIT || (has_segments(EPI) && EPI != EPI_FOLD32)) {
         if (tc_wide_tile(static_cast<Epi>(EPI), g)) return launch_t<EPI, A_MN, B_MN, 2, false, 512>(g, num_sms, st);
     }
     if constexpr (EPI == EPI_STORE && !A_MN && !B_MN) {
@@ -2432,7 +2432,7 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
     if (!(epi == EPI_BIAS_GELU || epi == EPI_DGELU || (epi == EPI_STORE && g.a_mn == g.b_mn) || epi == EPI_STORE_UNIT ||
-          (tc::has_segments(epi) && epi != EPI_XENT_FOLD)))
+          (tc::has_segments(epi) && epi != EPI_XENT_FOLD && epi != EPI_FOLD32)))
         return false;
     if (g.small_tile) return false;
     if (tc::has_segments(epi) || epi == EPI_STORE_UNIT) {
@@ -2489,6 +2489,10 @@ cudaError_t launch_tc_gemm(Epi epi, const GemmArgs &g, int num_sms, cudaStream_t
         case EPI_ACC32:  // dS[T,V'] (K-major) . W[V',h] (MN-major); dS^T . X[T,h] (both MN-major)
             if (!g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, false, true>(g, num_sms, st);
             if (g.a_mn && g.b_mn) return launch_cg<EPI_ACC32, true, true>(g, num_sms, st);
+            break;
+        case EPI_FOLD32:
+            if (!g.a_mn && g.b_mn) return launch_cg<EPI_FOLD32, false, true>(g, num_sms, st);
+            if (g.a_mn && g.b_mn) return launch_cg<EPI_FOLD32, true, true>(g, num_sms, st);
             break;
         case EPI_NS_GRAM:  // X X^T of a wide X (K-major), X^T X of a tall one (MN-major)
             if (!g.a_mn && !g.b_mn) return launch_cg<EPI_NS_GRAM, false, false>(g, num_sms, st);

@@ -632,3 +632,35 @@ def test_gradients_of_few_tokens(tp, T, dtype):
         check(X, W, y, dl, loss, ctx.lse, grads, reference(X, W, y, dl))
         assert torch.equal(tp.xent_backward(ctx, dl, need_dW=False)["dX"], grads["dX"])
         assert torch.equal(tp.xent_backward(ctx, dl, need_dX=False)["dW"], grads["dW"])
+
+
+@pytest.mark.parametrize("T,h,V", [(16, 256, 140000), (3, 64, 300000), (40, 4096, 3000), (2100, 1000, 2000),
+                                   (700, 8192, 2000), (9000, 512, 700)])
+def test_f32_gradients_are_fp32_whatever_the_length(tp, T, h, V):
+    """dX and dW as a whole against 64 bits, at K of 700 to 300000.  In units of 2^-24: a product of parts
+    is accumulated in ranges of at most 512, 32 steps that cut off a quarter of a unit of the sum on
+    average, taken as one and a half times that, 12; the products left out (2^-22) 4; the rounding of dS's
+    parts, the sums of ranges and splits 6; in p the logits, at most 3.5, with ranges of 256 (16 steps, 6) and
+    four roundings, 35, lse up to 12, 12, and the exponential 8.  They are independent: the root of
+    the sum of their squares is 41, and 2^-18 is 64."""
+    X, W, y, dl = make(T, h, V, torch.float32, seed=T + h)
+    X, W = 0.5 * X, W + 0.01
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    ref = reference(X, W, y, dl)
+    for name in ("dX", "dW"):
+        assert float((grads[name].double() - ref[name]).norm()) <= 2.0 ** -18 * float(ref[name].norm()), name
+
+
+def test_f32_gradients_near_the_ffma_path(tp):
+    """The tensor cores' fp32 against the FFMA kernels' on the same inputs: no more than 1.5 times as far
+    from 64 bits (both are dominated by sums of about a thousand terms; one accumulation of all of K was
+    3 to 9 times as far)."""
+    for T, h, V in ((2100, 1000, 2000), (600, 8192, 2000)):
+        X, W, y, dl = make(T, h, V, torch.float32, seed=T)
+        ref = reference(X, W, y, dl)
+        err = {}
+        for algo in (tp.ALGO_DEFAULT, tp.ALGO_SIMT):
+            _, _, grads = run(tp, X, W, y, dl, algo=algo)
+            err[algo] = [float((grads[n].double() - ref[n]).norm() / ref[n].norm()) for n in ("dX", "dW")]
+        for a, b in zip(err[tp.ALGO_DEFAULT], err[tp.ALGO_SIMT]):
+            assert a <= 1.5 * b, err
