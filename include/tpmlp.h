@@ -322,12 +322,16 @@ typedef struct {
 } tpmlp_xent_shape;
 
 /* Bytes of device workspace of both passes: status word, statistics (8 bytes per
- * token and 128 vocabulary rows, or per 16 at the fewest where there are few tokens), dS
- * of one piece (2 bytes per token and vocabulary row of it; fp32 6; the FFMA path also its
- * fp32 logits), fp32 sums of dX and dW where they are split, and for fp32 X and W in
- * three bf16 parts (6 bytes per element).  256-byte aligned, first 16 bytes zero
- * before first use; 0 for an invalid shape. */
+ * token and group of vocabulary rows), dS of one piece (2 bytes per token and vocabulary
+ * row of it; fp32 6; the FFMA path also its fp32 logits), fp32 sums of dX and dW where they
+ * are split or fp32, and for fp32 X and W in three bf16 parts (6 bytes per element).
+ * 256-byte aligned, first 16 bytes zero before first use; 0 for an invalid shape. */
 size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *shape);
+
+/* The same of the forward pass alone, for scoring: the statistics, beside them the parts of X
+ * and W for fp32 (with more tokens than eight, or than fit the kernels for few), or one piece
+ * of the FFMA path. */
+size_t tpmlp_xent_forward_workspace_bytes(const tpmlp_xent_shape *shape);
 
 /* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
  * written for every token, ignored ones too.  bf16 runs on the tensor cores with

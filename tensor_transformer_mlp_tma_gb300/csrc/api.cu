@@ -1192,6 +1192,7 @@ struct XentLayout {
     StatsTile stats;
     Split dx, dw;
     size_t unit, part, target_logit, xp, wp, ds, logits, acc, dwacc, total;
+    size_t forward;  // what the forward pass alone uses, from the start
 };
 
 // Workspace, 1 KB-aligned regions: status | the unit of dS | statistics | the targets' logits | three bf16
@@ -1227,11 +1228,14 @@ XentLayout xent_layout(const tpmlp_xent_shape *s) {
     L.unit = region(sizeof(float));
     L.part = region(stored * T * sizeof(float2));
     L.target_logit = region(T * 4);
+    L.forward = off;  // the statistics alone: bf16, and few tokens of either type
     L.xp = region(tc && f32 ? 3 * T * hp * 2 : 0);
     L.wp = region(tc && f32 ? 3 * V * hp * 2 : 0);
+    if (tc && f32 && L.stats.tile_n != 0) L.forward = off;
     L.ds = region(T * piece * (tc ? (f32 ? 6 : 2) : (f32 ? 4 : 2)));
     // FFMA path: in fp32 dS takes the place of the logits
     L.logits = tc || f32 ? L.ds : region(T * piece * 4);
+    if (!tc) L.forward = off;
     // dX and dW pass through fp32 where they are summed, or (fp32) cannot be stored by TMA
     const bool odd = f32 && s->hidden % 4 != 0;
     const bool dx_direct = tc ? L.dx.n == 1 && (f32 ? !odd : L.pieces == 1) : f32 || L.pieces == 1;
@@ -1376,6 +1380,10 @@ struct XentCall {
 extern "C" {
 
 size_t tpmlp_xent_workspace_bytes(const tpmlp_xent_shape *s) { return xent_valid(s) ? xent_layout(s).total : 0; }
+
+size_t tpmlp_xent_forward_workspace_bytes(const tpmlp_xent_shape *s) {
+    return xent_valid(s) ? xent_layout(s).forward : 0;
+}
 
 tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *s, const void *X, const void *W, const int64_t *target,
                                 float *loss, float *lse, void *workspace, void *stream) {

@@ -103,6 +103,7 @@ def _load():
         "tpmlp_attn_forward": (i32, [ctypes.POINTER(AttnShape)] + [vp] * 6 + [ctypes.POINTER(AttnSaved), vp, vp]),
         "tpmlp_attn_backward": (i32, [ctypes.POINTER(AttnShape), vp, ctypes.POINTER(AttnSaved)] + [vp] * 7),
         "tpmlp_xent_workspace_bytes": (sz, [ctypes.POINTER(XentShape)]),
+        "tpmlp_xent_forward_workspace_bytes": (sz, [ctypes.POINTER(XentShape)]),
         "tpmlp_xent_forward": (i32, [ctypes.POINTER(XentShape)] + [vp] * 7),
         "tpmlp_xent_backward": (i32, [ctypes.POINTER(XentShape)] + [vp] * 9),
         "tpmlp_ortho_workspace_bytes": (sz, [ctypes.POINTER(OrthoShape)]),
@@ -453,21 +454,25 @@ class XentContext:
     """Buffers of the vocabulary cross entropy between forward and backward: lse [T]
     (fp32) and the workspace.  W is [vocab, hidden], targets are int64; a target equal
     to ignore_index takes no part.  `piece` sets the vocabulary rows per piece of the
-    backward pass (a multiple of 8; 0: the library's choice).
+    backward pass (a multiple of 8; 0: the library's choice).  backward=False is for scoring
+    alone: the workspace then holds the forward pass only, and xent_backward is refused.
 
     One context serves one call at a time: its workspace is scratch of every call,
     also of captured graphs replayed at the same time."""
 
-    def __init__(self, tokens, hidden, vocab, dtype, ignore_index=-100, piece=0, algo=ALGO_DEFAULT, device=None):
+    def __init__(self, tokens, hidden, vocab, dtype, ignore_index=-100, piece=0, algo=ALGO_DEFAULT, device=None,
+                 backward=True):
         if dtype not in _DTYPES:
             raise ValueError("dtype %s: float32 or bfloat16" % (dtype,))
         self.shape = XentShape(int(tokens), int(hidden), int(vocab), int(ignore_index), int(piece), _DTYPES[dtype],
                                int(algo))
-        n = int(lib.tpmlp_xent_workspace_bytes(ctypes.byref(self.shape)))
+        size = lib.tpmlp_xent_workspace_bytes if backward else lib.tpmlp_xent_forward_workspace_bytes
+        n = int(size(ctypes.byref(self.shape)))
         if n == 0:
             raise ValueError("invalid cross entropy shape (tokens=%d hidden=%d vocab=%d piece=%d)"
                              % (tokens, hidden, vocab, piece))
         self.dtype = dtype
+        self.backward = bool(backward)
         self.workspace = _status_workspace(n, device)
         self.lse = torch.empty((int(tokens),), dtype=torch.float32, device=self.workspace.device)
         self._saved = None
@@ -496,6 +501,8 @@ def xent_backward(ctx: XentContext, dloss, dX=None, dW=None, need_dX=True, need_
     """dX[T,h] and dW[V,h] for the gradients dloss[T] (fp32) of the losses that the
     last xent_forward of this context returned; need_dX=False or need_dW=False leaves
     one out (its entry is None)."""
+    if not ctx.backward:
+        raise ValueError("xent_backward of a context made with backward=False")
     if ctx._saved is None:
         raise ValueError("xent_backward needs an xent_forward of the same context before it")
     X, W, target = ctx._saved

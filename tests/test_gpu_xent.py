@@ -664,3 +664,24 @@ def test_f32_gradients_near_the_ffma_path(tp):
             err[algo] = [float((grads[n].double() - ref[n]).norm() / ref[n].norm()) for n in ("dX", "dW")]
         for a, b in zip(err[tp.ALGO_DEFAULT], err[tp.ALGO_SIMT]):
             assert a <= 1.5 * b, err
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,h,V", [(1, 4096, 3000), (7, 200, 900), (100, 264, 2000), (700, 1000, 9001), (3, 70000, 40)])
+def test_scoring_workspace_is_all_the_forward_pass_needs(tp, T, h, V, dtype):
+    """The same bits from a workspace of the forward pass's size, and nothing written past it."""
+    X, W, y, dl = make(T, h, V, dtype, seed=T)
+    for algo in (tp.ALGO_DEFAULT, tp.ALGO_SIMT):
+        ctx = tp.XentContext(T, h, V, dtype, algo=algo)
+        want = tp.xent_forward(ctx, X, W, y)
+        score = tp.XentContext(T, h, V, dtype, algo=algo, backward=False)
+        n = score.workspace.numel()
+        room = torch.full((n + 65536,), 7, dtype=torch.uint8, device="cuda")
+        room[:1024] = 0
+        score.workspace = room[:n]
+        for _ in range(2):
+            assert torch.equal(tp.xent_forward(score, X, W, y), want) and torch.equal(score.lse, ctx.lse)
+        assert tp.check_device_status(score) == tp.OK
+        assert bool((room[n:] == 7).all())
+        with pytest.raises(ValueError):
+            tp.xent_backward(score, dl)

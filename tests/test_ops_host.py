@@ -212,3 +212,27 @@ def test_no_tokens_at_any_hidden_size(tp):
                 assert xws(tp, s) > 0
                 assert xfwd(tp, s, [None, FAKE, None, None, None]) == tp.OK
                 assert xbwd(tp, s, [None, FAKE, None, None, None, None, None]) == tp.OK
+
+
+def test_scoring_workspace(tp):
+    """The forward pass alone: no dS, no sums of dX and dW, and for few tokens no parts of W."""
+    fwd = lambda **k: tp.lib.tpmlp_xent_forward_workspace_bytes(ctypes.byref(xshape(tp, **k)))
+    for k in (dict(), dict(T=1, h=4096, V=32768), dict(T=4, h=4096, V=128256, dtype=tp.F32), dict(T=0),
+              dict(T=300, h=770, V=2500, dtype=tp.F32), dict(algo=1), dict(algo=1, dtype=tp.F32), dict(piece=64)):
+        assert 0 < fwd(**k) <= xws(tp, xshape(tp, **k)), k
+    for bad in (dict(T=-1), dict(h=0), dict(V=0), dict(piece=12), dict(dtype=7), dict(algo=5)):
+        assert fwd(**bad) == 0, bad
+    assert fwd(T=4, h=4096, V=128256, dtype=tp.F32) < 1 << 20
+    # two (max, sum) pairs of 8 bytes per token and at most 256 vocabulary rows
+    assert fwd(T=8192, h=4096, V=65536) <= 8192 * (65536 // 256) * 16 + (1 << 20)
+    # fp32 in three parts of 2 bytes
+    assert fwd(T=100, h=256, V=1000, dtype=tp.F32) >= 6 * 256 * 1100
+
+
+def test_scoring_context_refuses_the_backward_pass(tp):
+    import torch
+    ctx = tp.XentContext(4, 4096, 128256, torch.float32, device="cpu", backward=False)
+    assert ctx.workspace.numel() < 1 << 20
+    ctx._saved = (None, None, None)
+    with pytest.raises(ValueError, match="backward=False"):
+        tp.xent_backward(ctx, torch.zeros(4))
