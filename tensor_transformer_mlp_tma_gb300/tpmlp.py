@@ -478,9 +478,11 @@ class XentContext:
         self._saved = None
 
 
-def xent_forward(ctx: XentContext, X, W, target, loss=None, stream=None):
-    """loss[T] = log sum_v exp(X W^T)_v - (X W^T)_target, 0 for an ignored target; fills
-    ctx.lse.  X and W are kept for xent_backward."""
+def xent_forward(ctx: XentContext, X, W, target, loss=None, stream=None, lse=None):
+    """loss[T] = log sum_v exp(X W^T)_v - (X W^T)_target, 0 for an ignored target.  The log of
+    the sum goes to `lse` [T] (fp32), or without it to ctx.lse, which the next call overwrites.
+    X, W, target and the lse are kept, not copied, for xent_backward: they have to hold the same
+    values then."""
     s = ctx.shape
     T, h, V = s.tokens, s.hidden, s.vocab
     _need(X, "X", ctx.dtype, (T, h))
@@ -489,11 +491,15 @@ def xent_forward(ctx: XentContext, X, W, target, loss=None, stream=None):
     if loss is None:
         loss = torch.empty((T,), dtype=torch.float32, device=X.device)
     _need(loss, "loss", torch.float32, (T,))
-    _same_device(ctx, X, W, target, loss)
+    if lse is None:
+        lse = ctx.lse
+    else:
+        _need(lse, "lse", torch.float32, (T,))
+    _same_device(ctx, X, W, target, loss, lse)
     _call(ctx, lib.tpmlp_xent_forward, "tpmlp_xent_forward",
-          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(), ctx.lse.data_ptr(),
+          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(), lse.data_ptr(),
            ctx.workspace.data_ptr()), stream)
-    ctx._saved = (X, W, target)
+    ctx._saved = (X, W, target, lse)
     return loss
 
 
@@ -505,7 +511,7 @@ def xent_backward(ctx: XentContext, dloss, dX=None, dW=None, need_dX=True, need_
         raise ValueError("xent_backward of a context made with backward=False")
     if ctx._saved is None:
         raise ValueError("xent_backward needs an xent_forward of the same context before it")
-    X, W, target = ctx._saved
+    X, W, target, lse = ctx._saved
     s = ctx.shape
     T, h, V = s.tokens, s.hidden, s.vocab
     _need(dloss, "dloss", torch.float32, (T,))
@@ -519,7 +525,7 @@ def xent_backward(ctx: XentContext, dloss, dX=None, dW=None, need_dX=True, need_
             _need(x, n, ctx.dtype, shp)
     _same_device(ctx, dloss, dX, dW)
     _call(ctx, lib.tpmlp_xent_backward, "tpmlp_xent_backward",
-          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), ctx.lse.data_ptr(), dloss.data_ptr(),
+          (ctypes.byref(s), X.data_ptr(), W.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
            _ptr(dX), _ptr(dW), ctx.workspace.data_ptr()), stream)
     return {"dX": dX, "dW": dW}
 

@@ -685,3 +685,25 @@ def test_scoring_workspace_is_all_the_forward_pass_needs(tp, T, h, V, dtype):
         assert bool((room[n:] == 7).all())
         with pytest.raises(ValueError):
             tp.xent_backward(score, dl)
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_lse_of_the_callers_own(tp, T):
+    """It survives the context's next call, and the backward pass reads it."""
+    X, W, y, dl = make(T, 128, 900, seed=18)
+    X2, _, y2, _ = make(T, 128, 900, seed=19)
+    ctx, loss, grads = run(tp, X, W, y, dl)
+    want, kept = ctx.lse.clone(), torch.full((T + 2,), 7.0, device="cuda")
+    ctx2 = tp.XentContext(T, 128, 900, X.dtype)
+    ctx2.lse.fill_(5.0)
+    lse = kept[1:T + 1]
+    assert torch.equal(tp.xent_forward(ctx2, X, W, y, lse=lse), loss)
+    assert bool((ctx2.lse == 5.0).all())
+    again = tp.xent_backward(ctx2, dl)
+    assert torch.equal(again["dX"], grads["dX"]) and torch.equal(again["dW"], grads["dW"])
+    tp.xent_forward(ctx2, X2, W, y2)
+    assert torch.equal(lse, want) and float(kept[0]) == 7.0 and float(kept[-1]) == 7.0
+    for bad in (torch.empty(T + 1, device="cuda"), torch.empty(T, device="cuda", dtype=torch.bfloat16),
+                torch.empty(2 * T, device="cuda")[::2], torch.empty(T)):
+        with pytest.raises(ValueError):
+            tp.xent_forward(ctx2, X, W, y, lse=bad)
