@@ -371,7 +371,7 @@ tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, c
  * itself is carried as a sum of two fp16 numbers (about 22 bits), so that the
  * directions of small singular values, which only the term a X moves, keep their
  * precision whatever the matrix's condition.  The norm is exact to fp32 over the
- * whole range of the input's type. */
+ * whole range of the input's type, subnormal numbers and any number of the largest among them. */
 typedef struct {
     int64_t batch; /* matrices, 0..65535 */
     int64_t rows, cols; /* > 0, any number up to 2^20 */

@@ -22,10 +22,12 @@ constexpr int THREADS = 256;
 struct Blue {
     float big, mid, small;
 };
-constexpr float kBig = 0x1p48f, kSmall = 0x1p-48f;      // limits of the ordinary values
-constexpr float kBigScale = 0x1p-72f, kSmallScale = 0x1p72f;
+// The limits and scales leave room for 2^34 squares of the largest value of each kind (2^126, 2^122,
+// 2^106 in all), and the square of the smallest subnormal number is a normal one (2^-114).
+constexpr float kBig = 0x1p46f, kSmall = 0x1p-56f;      // limits of the ordinary values
+constexpr float kBigScale = 0x1p-84f, kSmallScale = 0x1p92f;
 // N values at once, all into the sum that the largest of them belongs to: beside a value of
-// 2^-48 or more, what underflows (below 2^-74) is too small to count.
+// 2^-56 or more, what underflows (below 2^-74) is too small to count.
 template <int N>
 __device__ __forceinline__ void add(Blue &b, const float (&x)[N]) {
     float m = 0.0f;
@@ -117,24 +119,24 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const T *G, int64_t n, in
     if (threadIdx.x == 0) part[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = b;
 }
 
-// scale / (|G| + eps) from the three sums.  The norm is sqrt(s) 2^h, s the sum in the
-// largest unit that has any (a sum two units down could not count): neither it nor the
-// factor then leaves fp32's range before the last step, where a factor beyond it
-// (|G| < 2^-113 with eps = 0) saturates.  fp32 throughout: 64-bit arithmetic here took
+// scale / (|G| + eps) from the three sums, as the product of f and the power of two `unit`.  The norm is
+// sqrt(s) / unit, s the sum in the largest unit that has any (a sum two units down could not
+// count); x unit f then neither overflows nor loses bits that count, whatever the norm: unit
+// moves all values towards the ordinary ones.  fp32 throughout: 64-bit arithmetic here took
 // longer than a block's share of the matrix.
-// With POW2 the result is the power of two below it, and `rest` (1 to 2) is what is left.
+// With POW2 f is the power of two below it, and `rest` (1 to 2) is what is left.
 template <bool POW2>
-__device__ __forceinline__ float inverse_norm(const Blue &b, float eps, float scale, float &rest) {
-    float s, down;  // 2^-h
+__device__ __forceinline__ float inverse_norm(const Blue &b, float eps, float scale, float &unit, float &rest) {
+    float s;
     if (b.big > 0.0f)
-        s = fmaf(b.mid, 0x1p-144f, b.big), down = 0x1p-72f;
+        s = b.big + b.mid * kBigScale * kBigScale, unit = kBigScale;
     else if (b.mid == 0.0f && b.small > 0.0f)
-        s = b.small, down = 0x1p72f;
+        s = b.small, unit = kSmallScale;
     else
-        s = fmaf(b.small, 0x1p-144f, b.mid), down = 1.0f;
+        s = b.mid + b.small * (1.0f / kSmallScale) * (1.0f / kSmallScale), unit = 1.0f;
     if (b.big != b.big || b.mid != b.mid || b.small != b.small) s = nanf("");
-    float f = __fdiv_rn(scale, __fsqrt_rn(s) + eps * down) * down;
-    if (f > 0x1p127f) f = 0x1p127f;  // not NaN
+    float f = __fdiv_rn(scale, __fsqrt_rn(s) + eps * unit);
+    if (f > 0x1p127f) f = 0x1p127f;  // a zero matrix with eps = 0; not NaN
     rest = 1.0f;
     if (POW2 && f >= 0x1p-126f) {
         const float p = __uint_as_float(__float_as_uint(f) & 0x7F800000u);
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
         const Blue p = part[z * nparts + i];
         b.big += p.big, b.mid += p.mid, b.small += p.small;
     }
-    float left;
-    const float f = inverse_norm<POW2>(block_sum(b), eps, scale, left);
+    float left, unit;
+    const float f = inverse_norm<POW2>(block_sum(b), eps, scale, unit, left);
     if (POW2 && blockIdx.x == 0 && threadIdx.x == 0) rest[z] = left;
     const T *g = G + z * rows * cols;
     // UN loads in flight per thread before the first is used
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(THREADS) scale_kernel(const T *G, int64_t rows
             alignas(16) __half l[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float x = v[u][j] * f;
+                const float x = v[u][j] * unit * f;
                 h[j] = __float2half_rn(x);
                 l[j] = __float2half_rn((x - __half2float(h[j])) * lo_scale);
             }

@@ -219,3 +219,39 @@ def test_a_batch_past_32_bits(tp):
 def test_empty_batch(tp):
     ctx = tp.OrthoContext(8, 8, 0)
     assert tp.orthogonalize(ctx, torch.empty(0, 8, 8, dtype=torch.bfloat16, device="cuda")).shape == (0, 8, 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(100, 3000), (1100, 1000)])
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** 100, 2.0 ** 47, 2.0 ** 45, 2.0 ** -55, 2.0 ** -57, 2.0 ** -115,
+                                   2.0 ** -130, 2.0 ** -143])
+def test_norms_at_the_ends_of_the_range(tp, rows, cols, scale, dtype):
+    """A million of the largest numbers (the sum of their squares is past fp32 in any one unit that also
+    holds the middle ones), and matrices wholly of subnormal ones, of which 2^-143 leaves fp32 six bits,
+    and bf16 none."""
+    G = rand(1, rows, cols, torch.float32, seed=11).clamp_(-3, 3)
+    if scale == 2.0 ** 126:
+        G = torch.sign(G) * (2 + G.abs() / 3)  # up to 3 * 2^126
+    G = (G.double() * scale).to(dtype)
+    assert bool(torch.isfinite(G).all())
+    if not bool(G.any()):
+        assert not bool(run(tp, G, eps=0.0).any())
+        return
+    check(run(tp, G, eps=0.0), reference(G, eps=0.0))
+
+
+def test_norm_of_all_kinds_of_values_at_once(tp):
+    """Large, ordinary and tiny values in one matrix, in every unit of the sum."""
+    for hi, lo in ((2.0 ** 60, 1.0), (2.0 ** 50, 2.0 ** 40), (1.0, 2.0 ** -60), (2.0 ** -50, 2.0 ** -58), (2.0 ** 120, 2.0 ** -140)):
+        for rows, cols in ((64, 600), (300, 200)):
+            G = rand(1, rows, cols, torch.float32, seed=12).double()
+            G[:, : rows // 2] *= hi
+            G[:, rows // 2:] *= lo
+            G = G.float()
+            keep = slice(0, rows // 2)
+            O, ref = run(tp, G, eps=0.0), reference(G, eps=0.0)
+            # (rows of the smaller scale are beyond the condition that the iterates hold)
+            if hi / lo <= 2.0 ** 10:
+                check(O, ref)
+            else:
+                check(O[:, keep], ref[:, keep])
