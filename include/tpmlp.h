@@ -308,14 +308,15 @@ tpmlp_status tpmlp_attn_backward(const tpmlp_attn_shape *shape, const void *dZ, 
  * mean):
  *   dS = (exp(S - lse) - onehot(target)) * dloss,   dX = dS W,   dW = dS^T X.
  * The forward pass keeps one (maximum, sum of exponentials) pair per token and 16 to
- * 128 vocabulary rows, in fp32, and joins them in a fixed order; the backward pass
- * recomputes the logits of one piece of the vocabulary at a time and holds that
- * piece's dS. */
+ * 128 vocabulary rows (few tokens: at most 304 in all; FFMA path: one per piece), in
+ * fp32, and joins them in a fixed order; the backward pass recomputes the logits of one
+ * piece of the vocabulary at a time, with the same sums, and holds that piece's dS. */
 typedef struct {
     int64_t tokens;       /* T >= 0 */
     int64_t hidden;       /* h > 0 */
     int64_t vocab;        /* V > 0, any number */
-    int64_t ignore_index; /* a token with this target has loss 0 and no gradient */
+    int64_t ignore_index; /* a token with this target has loss 0, a dX of 0 and no part in dW (0 times its
+                             row of X: a NaN or infinity there still makes dW NaN) */
     int64_t piece;        /* vocabulary rows per piece, a multiple of 8; 0: the library's choice */
     int32_t dtype;        /* tpmlp_dtype of X, W, dX, dW */
     int32_t algo;         /* tpmlp_algo */
@@ -336,8 +337,9 @@ size_t tpmlp_xent_forward_workspace_bytes(const tpmlp_xent_shape *shape);
 /* Forward: loss[T] and lse[T] (fp32) of X[T,h], W[V,h], target[T] (int64).  lse is
  * written for every token, ignored ones too.  bf16 runs on the tensor cores with
  * fp32 accumulation and statistics; the logits are not rounded beyond that (the tensor core's
- * accumulator cuts off rather than rounds: at most 2^-24 of the partial sum per 16 products,
- * in ranges of at most 2048 products for bf16 and 256 for fp32, the ranges added in fp32).  fp32 runs there too, each
+ * accumulator cuts off rather than rounds: up to 2^-23 of the partial sum per 16 products, a
+ * quarter of 2^-24 of the logit on average; ranges of at most 2048 products for bf16 and 256
+ * for fp32 are added in fp32).  fp32 runs there too, each
  * operand as the sum of three bf16 numbers (24 bits, and 2^-133 at the least).  A logit of NaN or
  * +inf makes its token's loss and lse non-finite, no other token's.  A target that
  * is neither ignore_index nor in [0, V) is reported as TPMLP_ERR_INVALID_ARG in the
@@ -355,6 +357,8 @@ tpmlp_status tpmlp_xent_forward(const tpmlp_xent_shape *shape, const void *X, co
  * cores in units of the significand of the first dloss that takes part, so that equal
  * weights are not rounded the same way in every token), in fp32 it is not; dX is summed
  * over the pieces in fp32 and rounded once.  With T = 0 dW is set to zero.
+ * X, W and target have to hold what they held in the forward pass.  lse is fp32: p - 1 of a token
+ * that is sure of its target carries 2^-24 |lse|.
  * Results are bit-identical from call to call.  Errors as the forward. */
 tpmlp_status tpmlp_xent_backward(const tpmlp_xent_shape *shape, const void *X, const void *W, const int64_t *target,
                                  const float *lse, const float *dloss, void *dX, void *dW, void *workspace,

@@ -707,3 +707,18 @@ def test_lse_of_the_callers_own(tp, T):
                 torch.empty(2 * T, device="cuda")[::2], torch.empty(T)):
         with pytest.raises(ValueError):
             tp.xent_forward(ctx2, X, W, y, lse=bad)
+
+
+@pytest.mark.parametrize("T,h,V,dtype,piece", [(1, 520, 4000, torch.bfloat16, 0), (6, 520, 4000, torch.bfloat16, 1000),
+                                               (3, 130, 4000, torch.float32, 0), (300, 770, 5000, torch.float32, 2048),
+                                               (20, 256, 150000, torch.float32, 0), (400, 4096, 3000, torch.bfloat16, 0)])
+def test_same_bits_on_every_path(tp, T, h, V, dtype, piece):
+    X, W, y, dl = make(T, h, V, dtype, seed=20, ignored=0.1)
+    ctx, loss, grads = run(tp, X, W, y, dl, piece=piece)
+    lse = ctx.lse.clone()
+    for _ in range(3):
+        ctx.workspace[1024:] = 255
+        assert torch.equal(tp.xent_forward(ctx, X, W, y), loss) and torch.equal(ctx.lse, lse)
+        ctx.workspace[1024:] = 255
+        again = tp.xent_backward(ctx, dl)
+        assert torch.equal(again["dX"], grads["dX"]) and torch.equal(again["dW"], grads["dW"])
