@@ -1638,9 +1638,12 @@ OrthoLayout ortho_layout(const tpmlp_ortho_shape *s) {
     L.P = (s->rows + 63) / 64 * 64, L.Q = (s->cols + 63) / 64 * 64;
     L.wide = s->rows <= s->cols;
     L.p = L.wide ? L.P : L.Q;
-    // The chain wants Q (times a factor of up to 2) in fp16's range.
+    // The chain holds A_0 to about 2^-23 of its largest eigenvalue, and the steps multiply what they
+    // do to the small ones by up to Q^2: errors (on matrices with some strong directions) of 3e-9 Q^2,
+    // 2e-3 in all up to Q = 485 (five steps of the usual coefficients), 3e-3 at 535, 4e-3 to 9e-3 at
+    // 1670 (six), 5e-2 at 5753.  Steps on X itself do not lose that (2e-3 to 4e-3 at 12 steps).
     double q_bound = 0.0;
-    L.chain = L.p <= tpmlp::NS_CHAIN_P && ortho_range_ok(s, q_bound) && q_bound < 32768.0;
+    L.chain = L.p <= tpmlp::NS_CHAIN_P && ortho_range_ok(s, q_bound) && q_bound <= 600.0;
     L.q_scale = L.chain ? static_cast<float>(std::exp2(std::floor(std::log2(30000.0 / std::max(q_bound, 1.0))))) : 1.0f;
     size_t off = STATUS_BYTES;
     auto region = [&](size_t bytes) {

@@ -9,7 +9,9 @@
 // small ones, so 11-bit operands would not do.  Every matrix is the sum of two fp16
 // matrices (22 bits) and a product is three: hi hi + hi lo + lo hi, in one fp32
 // accumulator.  Against 64 bits that leaves errors of 1e-6 (Gaussian matrices) to
-// 6e-4 (one singular value 1000 times the others), below the bf16 output's own.
+// 6e-4 (one singular value 1000 times the others), below the bf16 output's own, for five steps of
+// a = 3.4; they grow with the square of the largest factor in Q, which bounds the use of this kernel
+// (see ortho_layout).
 // All factors are polynomials of A_0 and commute, but their roundings do not: an error
 // that couples a large singular value i and a small one j is multiplied by
 // B_i B_j (at most about 2.4) in B A B and by B_j^2 (up to 11.8 a step) in A B B, and by

@@ -255,3 +255,21 @@ def test_norm_of_all_kinds_of_values_at_once(tp):
                 check(O, ref)
             else:
                 check(O[:, keep], ref[:, keep])
+
+
+@pytest.mark.parametrize("steps,coef", [(5, COEF), (6, COEF), (7, COEF), (8, COEF), (9, (3.0, -3.2, 1.2)), (6, (3.0, -3.2, 1.2)),
+                                        (9, (2.0, -1.5, 0.5)), (12, (2.0, -1.5, 0.5)), (10, (1.875, -1.25, 0.375)),
+                                        (13, (1.875, -1.25, 0.375))])
+@pytest.mark.parametrize("rows,cols", [(120, 706), (16, 300), (600, 50), (200, 300)])
+def test_many_steps_on_strong_directions_over_noise(tp, rows, cols, steps, coef):
+    """Small singular values grow by a factor of up to a^steps (500 to 40000 here) while the strong ones stay:
+    what a step does to the small ones may not be lost in the roundings of the large ones."""
+    for dtype in (torch.float32, torch.bfloat16):
+        for k, strong in ((1, 100.0), (4, 30.0)):
+            g = torch.Generator(device="cpu")
+            g.manual_seed(13)
+            G = torch.randn(2, rows, k, generator=g) @ torch.randn(2, k, cols, generator=g) * (strong / min(rows, cols) ** 0.5)
+            G = (G + 0.01 * torch.randn(2, rows, cols, generator=g)).to(dtype).cuda()
+            check(run(tp, G, steps=steps, coefficients=coef), reference(G, steps, coef))
+        G = rand(2, rows, cols, dtype, seed=14, kind="lowrank")
+        check(run(tp, G, steps=steps, coefficients=coef), reference(G, steps, coef))
