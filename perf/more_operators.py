@@ -374,11 +374,10 @@ def run(s):
     case, ctx = s["case"], s["ctx"]
     if op == "attend":
         return tpmlp.cache_attention(ctx, s["cache"], s["Q"], s["q_start"], s["kv_len"], s["table"], s["tree"])
-    Q, K, V = tpmlp.split_qkv(s["QKV"], case["heads"], case["kv"], case["d"], case.get("t", 1))
     if op == "append":
-        Q = tpmlp.kv_append(ctx, s["kv"], Q, K, V, s["position"], s["slot"], s["gq"], s["gk"])
+        Q = tpmlp.kv_append(ctx, s["kv"], s["QKV"], s["position"], s["slot"], s["gq"], s["gk"])
         return {"Q": Q, "K": s["cache"][0], "V": s["cache"][1]}
-    Q, K = tpmlp.qk_forward(ctx, Q, K, s["position"], s["gq"], s["gk"])
+    Q, K = tpmlp.qk_forward(ctx, s["QKV"], s["position"], s["gq"], s["gk"])
     out = {"Q": Q, "K": K}
     if case["train"]:
         grads = tpmlp.qk_backward(ctx, s["dQ"], s["dK"])
