@@ -400,6 +400,142 @@ size_t tpmlp_ortho_workspace_bytes(const tpmlp_ortho_shape *shape);
 tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *shape, const void *G, void *O, void *workspace,
                                  void *stream);
 
+/* ---- positions: norms of queries and keys per head, and their rotation --------------
+ * What the attention block's projection returns has no notion of position.  Per head of Q and K:
+ *   y = g x / sqrt(mean(x^2) + eps)                             (norm, gains g [dim])
+ *   (u, v) -> a (u cos f - v sin f, u sin f + v cos f),   f = position * theta_i
+ * for the pairs (i, i + rot/2) of its first `rot` components (TPMLP_ROPE_HALF) or (2i, 2i + 1)
+ * (TPMLP_ROPE_INTERLEAVED); the components behind them keep their normed values.  Computed in
+ * fp32, the angles to 2^-26 of a turn at any position, rounded once. */
+typedef enum { TPMLP_ROPE_HALF = 0, TPMLP_ROPE_INTERLEAVED = 1 } tpmlp_rope_layout;
+
+/* Contexts longer than the trained one.  LINEAR: every theta_i divided by `factor`.  PARTS: a pair
+ * that turns n = context theta_i / (2 pi) times within the trained context is kept where n >= high,
+ * divided by `factor` where n <= low, and in between theta_i (k + (1 - k) / factor) with
+ * k = (n - low) / (high - low). */
+typedef enum { TPMLP_ROPE_SCALE_NONE = 0, TPMLP_ROPE_SCALE_LINEAR = 1, TPMLP_ROPE_SCALE_PARTS = 2 } tpmlp_rope_scaling;
+
+typedef struct {
+    double base;     /* theta_i = base^(-2i/rot) before scaling; >= 1 */
+    double factor;   /* LINEAR, PARTS: > 0 */
+    double low, high; /* PARTS: low < high */
+    int64_t context; /* PARTS: > 0 */
+    int32_t rot;     /* rotating components of a head: even, 0..256 */
+    int32_t scaling; /* tpmlp_rope_scaling */
+} tpmlp_rope;
+
+/* turns[rot/2] (host memory): theta_i / (2 pi) in units of 2^-64.  The kernels read a copy of them in
+ * device memory.  INVALID_ARG for values out of range, or a theta_i that is not below 2 pi. */
+tpmlp_status tpmlp_rope_turns(const tpmlp_rope *rope, uint64_t *turns);
+
+typedef struct {
+    int64_t tokens;   /* T >= 0 */
+    int32_t heads;    /* query heads */
+    int32_t kv_heads; /* key (and value) heads */
+    int32_t dim;      /* components of a head: even, 2..256 */
+    int32_t t;        /* shards, 1..16; heads and kv_heads are multiples of it */
+    int32_t dtype;    /* tpmlp_dtype of heads and gains */
+    int32_t layout;   /* tpmlp_rope_layout */
+    int32_t rot;      /* even, 0..dim; 0: no rotation, positions and turns are not read */
+    int32_t norm;     /* 1: with the norm, 0: rotation alone, gains are not read */
+    float eps;        /* >= 0 */
+    float amplitude;  /* a, the factor of the rotated components */
+} tpmlp_qk_shape;
+
+/* Heads of T tokens: component e of head j of shard i of token r is p[r * row + i * shard + j * dim + e]
+ * (elements; each shard has heads/t, or kv_heads/t, of them).  Q inside the attention block's QKV [T, 3h]:
+ * {QKV, 3h, 3h/t}, K {QKV + h/t, 3h, 3h/t}; a dense [T, heads, dim] array: {Q, heads*dim, heads/t*dim}. */
+typedef struct {
+    void *p;
+    int64_t row;
+    int64_t shard;
+} tpmlp_heads;
+
+/* Bytes of device workspace of tpmlp_qk_backward and tpmlp_kv_append (status word, partial sums of the gains'
+ * gradients); 256-byte aligned, first 8 bytes zero before first use; 0 for an invalid shape. */
+size_t tpmlp_qk_workspace_bytes(const tpmlp_qk_shape *shape);
+
+/* Qr, Kr from Q, K; position[T], turns[rot/2] (tpmlp_rope_turns) and the gains in device memory.  Positions
+ * may be any int64 (taken modulo 2^64).  Qr may be Q and Kr K (in place; a backward pass with the norm
+ * needs Q and K as they were).  Rows are read 16 bytes at a time where bases, rows and shards
+ * are on 16 bytes and dim (TPMLP_ROPE_HALF: also rot) is a multiple of 16 (fp32: 8), else 8 bytes or one element.
+ * Errors: INVALID_ARG for a bad shape, a NULL pointer, rows that overlap one another or an output that overlaps an
+ * input in another place; UNSUPPORTED for a pointer that is not on its element; CUDA when a launch fails. */
+tpmlp_status tpmlp_qk_forward(const tpmlp_qk_shape *shape, const tpmlp_heads *Q, const tpmlp_heads *K, const void *gain_q,
+                              const void *gain_k, const int64_t *position, const uint64_t *turns, const tpmlp_heads *Qr,
+                              const tpmlp_heads *Kr, void *stream);
+
+/* Gradients dQ, dK, dgain_q[dim], dgain_k[dim] from those of Qr and Kr.  The gains are shared by all heads and
+ * tokens: their gradients are summed in fp32, in a fixed order.  Without the norm Q, K and the gains with their
+ * gradients may be NULL.  dQ may be dQr or Q, dK likewise.  With T = 0 the gains' gradients are zero.  Errors as the
+ * forward. */
+tpmlp_status tpmlp_qk_backward(const tpmlp_qk_shape *shape, const tpmlp_heads *Q, const tpmlp_heads *K, const void *gain_q,
+                               const void *gain_k, const int64_t *position, const uint64_t *turns, const tpmlp_heads *dQr,
+                               const tpmlp_heads *dKr, const tpmlp_heads *dQ, const tpmlp_heads *dK, void *dgain_q,
+                               void *dgain_k, void *workspace, void *stream);
+
+/* ---- paged key-value cache ----------------------------------------------------------
+ * Keys and values of many sequences in pages of page_size tokens: component e of key head j, row r of page p is
+ * K[p * page_stride + j * head_stride + r * token_stride + e] (elements), V alike. */
+typedef struct {
+    void *K;
+    void *V;
+    int64_t pages;     /* >= 1; pages * page_size < 2^40 */
+    int64_t page_size; /* >= 1 */
+    int64_t page_stride, head_stride, token_stride; /* no two rows may overlap */
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t dtype;
+} tpmlp_kv_cache;
+
+/* Appends T tokens: K normed and rotated as by tpmlp_qk_forward, and V as it is, go to row slot % page_size of page
+ * slot / page_size, Q normed and rotated to Qr (which may be Q).  slot[T] (int64, device): a negative one is of a
+ * token that is not kept (padding); one that is pages * page_size or more is reported as
+ * TPMLP_ERR_INVALID_ARG in the status word (detail: the token) and not kept.  Slots that are kept have to differ: of
+ * two tokens with the same slot, each head's row is one's or the other's.  All other rows of the cache stay as they are.
+ * Errors as tpmlp_qk_forward; INVALID_ARG also where heads, dim or type of shape and cache differ. */
+tpmlp_status tpmlp_kv_append(const tpmlp_qk_shape *shape, const tpmlp_kv_cache *cache, const tpmlp_heads *Q,
+                             const tpmlp_heads *K, const tpmlp_heads *V, const void *gain_q, const void *gain_k,
+                             const int64_t *position, const uint64_t *turns, const int64_t *slot, const tpmlp_heads *Qr,
+                             void *workspace, void *stream);
+
+/* Attention of new tokens over the cache, theirs in it already:
+ *   O = softmax(scale Q K^T over the visible keys) V   per head; query head g reads key head g / (heads/kv_heads).
+ * Sequence b has the tokens q_start[b] .. q_start[b+1] - 1 of Q[T, heads, dim] and kv_len[b] keys, key c in row
+ * c % page_size of page page_table[b][c / page_size].  Its new tokens are the last n = q_start[b+1] - q_start[b] of
+ * those keys.  Every new token sees all keys before them; of the new ones
+ *   tree NULL:  those up to itself (one token: decoding; more: a prompt's chunk, or the whole of it);
+ *   else:       those whose bit is set in tree[token][tree_words]: bit j % 64 of word j / 64 for the j-th new
+ *               token of the sequence (a tree of drafts: a token's own bit and those of the tokens above it).
+ * A row that sees nothing is zero.  What a row does not see has no part in it, whatever it holds (NaN, infinity).
+ * Rows of O behind q_start[batch] stay as they are. */
+typedef struct {
+    int64_t tokens;     /* T >= 0; tokens * heads < 2^31 */
+    int64_t batch;      /* sequences, 0..2^20 */
+    int64_t max_pages;  /* row length of page_table, max_pages * page_size < 2^31 - 1024 */
+    int32_t heads;      /* a multiple of the cache's kv_heads */
+    int32_t tree_words; /* with a tree: >= 1 */
+    int32_t algo;       /* tpmlp_algo */
+    float scale;        /* of the scores; finite */
+} tpmlp_cache_attn_shape;
+
+/* Bytes of device workspace (status word, block counters, pieces of sequences that several blocks share); 256-byte
+ * aligned, first 4096 bytes zero before first use; 0 for an invalid shape.  Depends on dim only. */
+size_t tpmlp_cache_attn_workspace_bytes(const tpmlp_cache_attn_shape *shape, const tpmlp_kv_cache *cache);
+
+/* Q, O[T, heads, dim] of the cache's type; q_start[batch + 1], kv_len[batch], page_table[batch][max_pages] are int32 in
+ * device memory, read by the kernel (a captured graph may be replayed with others).  Only the pages that hold a sequence's kv_len keys
+ * are looked up.  Reported as TPMLP_ERR_INVALID_ARG in the status word (detail: the sequence) are a kv_len that is below n or does
+ * not fit the table (the sequence's rows are zero), a q_start that decreases or leaves [0, T] (the sequence has no
+ * tokens) and a page that is not in the cache (its keys and values count as zeros).
+ * Both types run on FFMA kernels.
+ * Calls with the same lengths and inputs give the same bits on the same number of SMs.
+ * Errors: INVALID_ARG for a bad shape, a NULL pointer or an O that overlaps an input; UNSUPPORTED for dim not a multiple of 8
+ * or above 256, and for Q or O not on 16 bytes; CUDA when a launch fails. */
+tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *shape, const tpmlp_kv_cache *cache, const void *Q,
+                              const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, const int64_t *tree,
+                              void *O, void *workspace, void *stream);
+
 /* Synchronises the stream, reads the workspace status word, clears it and
  * returns it (TPMLP_OK when no device-side error was recorded). */
 tpmlp_status tpmlp_check_device_status(void *workspace, void *stream);

@@ -1850,3 +1850,404 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *s, const void *G, void
 }
 
 }  // extern "C"
+
+// ---- positions and the paged cache --------------------------------------------------------
+
+namespace {
+
+bool qk_valid(const tpmlp_qk_shape *s) {
+    if (!s || s->tokens < 0 || s->tokens > (1LL << 30)) return false;
+    if (s->heads < 1 || s->kv_heads < 1 || s->heads > 65536 || s->kv_heads > 65536) return false;
+    if (s->t < 1 || s->t > 16 || s->heads % s->t != 0 || s->kv_heads % s->t != 0) return false;
+    if (s->dim < 2 || s->dim > 256 || s->dim % 2 != 0) return false;
+    if (s->rot < 0 || s->rot > s->dim || s->rot % 2 != 0) return false;
+    if (s->dtype != TPMLP_F32 && s->dtype != TPMLP_BF16) return false;
+    if (s->layout != TPMLP_ROPE_HALF && s->layout != TPMLP_ROPE_INTERLEAVED) return false;
+    if (s->norm != 0 && s->norm != 1) return false;
+    return s->eps >= 0.0f && std::isfinite(s->eps) && std::isfinite(s->amplitude);
+}
+
+int64_t type_bytes(int32_t dtype) { return dtype == TPMLP_BF16 ? 2 : 4; }
+
+// The heads of one array and the bytes they lie in.
+struct HeadSpan {
+    const tpmlp_heads *h;
+    int64_t rows, shards, width;  // tokens, shards, elements of a shard's heads
+    int64_t esz;
+    int64_t elements() const { return rows > 0 ? (rows - 1) * h->row + (shards - 1) * h->shard + width : 0; }
+    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(h->p); }
+    uintptr_t end() const { return begin() + static_cast<uintptr_t>(elements() * esz); }
+    // No two heads share an element, and nothing wraps around.
+    bool sound() const {
+        if (shards > 1 && (h->shard < width || h->shard > (1LL << 40))) return false;
+        const int64_t row = (shards - 1) * (shards > 1 ? h->shard : 0) + width;
+        return rows <= 1 || (h->row >= row && h->row <= (1LL << 40));
+    }
+    bool same(const HeadSpan &o) const {
+        return begin() == o.begin() && width == o.width && (rows <= 1 || h->row == o.h->row) &&
+               (shards <= 1 || h->shard == o.h->shard);
+    }
+};
+
+HeadSpan span(const tpmlp_qk_shape *s, const tpmlp_heads *h, int32_t heads) {
+    return {h, s->tokens, s->t, static_cast<int64_t>(heads / s->t) * s->dim, type_bytes(s->dtype)};
+}
+
+// Whether two arrays share an element.  Inside one array of rows (Q, K and V of a QKV) columns are
+// compared; arrays with other rows must not meet at all.
+bool meet(const HeadSpan &x, const HeadSpan &y) {
+    if (x.rows <= 0 || y.rows <= 0 || x.begin() >= y.end() || y.begin() >= x.end()) return false;
+    const int64_t bytes = static_cast<int64_t>(x.begin() - y.begin());
+    if (x.rows <= 1 || y.rows <= 1 || x.h->row != y.h->row || bytes % x.esz != 0) {
+        if (x.rows > 1 || y.rows > 1 || bytes % x.esz != 0) return true;
+    }
+    const int64_t off = bytes / x.esz, row = x.rows > 1 ? x.h->row : (1LL << 60);
+    const auto mod = [row](int64_t v) { return ((v % row) + row) % row; };
+    for (int64_t i = 0; i < x.shards; ++i)
+        for (int64_t j = 0; j < y.shards; ++j) {
+            const int64_t a = off + i * x.h->shard, b = j * y.h->shard;
+            if (mod(a - b) < y.width || mod(b - a) < x.width) return true;
+        }
+    return false;
+}
+
+bool meets_buffer(const HeadSpan &x, const void *p, int64_t bytes) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return b && x.rows > 0 && x.begin() < b + static_cast<uintptr_t>(bytes) && b < x.end();
+}
+
+// Whether the cache's rows are apart: dimensions by growing stride, each past all that the ones below
+// it reach.  K and V inside one another (a page of both) are one more dimension of two.
+bool cache_valid(const tpmlp_kv_cache *c) {
+    if (!c || c->pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > 65536) return false;
+    if (c->dim < 2 || c->dim > 256 || c->dim % 2 != 0) return false;
+    if (c->dtype != TPMLP_F32 && c->dtype != TPMLP_BF16) return false;
+    if (c->pages > (1LL << 31) - 1 || c->page_size > (1LL << 31) - 1 || c->pages > ((1LL << 40) - 1) / c->page_size) return false;
+    for (int64_t stride : {c->page_stride, c->head_stride, c->token_stride})
+        if (stride < 0 || stride > (1LL << 39)) return false;
+    const int64_t esz = type_bytes(c->dtype);
+    std::pair<int64_t, int64_t> dims[4] = {{c->page_stride, c->pages}, {c->head_stride, c->kv_heads},
+                                           {c->token_stride, c->page_size}, {0, 1}};
+    if (c->K && c->V) {
+        const uintptr_t k = reinterpret_cast<uintptr_t>(c->K), v = reinterpret_cast<uintptr_t>(c->V);
+        const uintptr_t apart = k < v ? v - k : k - v;
+        if (apart == 0) return false;
+        double reach = c->dim;
+        for (int i = 0; i < 3; ++i) reach += static_cast<double>(dims[i].first) * (dims[i].second - 1);
+        if (static_cast<double>(apart) < reach * esz) {
+            if (apart % esz != 0) return false;
+            dims[3] = {static_cast<int64_t>(apart / esz), 2};
+        }
+    }
+    std::sort(dims, dims + 4);
+    double reach = c->dim;  // elements from a row's first on that the dimensions so far cover
+    for (const auto &d : dims) {
+        if (d.second == 1) continue;
+        if (static_cast<double>(d.first) < reach) return false;
+        reach += static_cast<double>(d.first) * (d.second - 1);
+    }
+    return true;
+}
+
+// Bytes from K's (or V's) first element to its last.
+int64_t cache_bytes(const tpmlp_kv_cache *c) {
+    return ((c->pages - 1) * c->page_stride + (c->kv_heads - 1) * c->head_stride + (c->page_size - 1) * c->token_stride + c->dim) *
+           type_bytes(c->dtype);
+}
+
+constexpr size_t QK_STATUS = 1024;
+
+struct QkCall {
+    const char *who;
+    const tpmlp_qk_shape *s;
+    tpmlp::QkArgs a;
+    tpmlp_status fail(tpmlp_status rc, const char *why) const {
+        tpmlp::set_last_error("%s: %s", who, why);
+        return rc;
+    }
+    QkCall(const char *who_, const tpmlp_qk_shape *s_) : who(who_), s(s_) { std::memset(&a, 0, sizeof(a)); }
+    // What all three entry points have in common.
+    tpmlp_status common(const void *gain_q, const void *gain_k, const int64_t *position, const uint64_t *turns) {
+        const bool some = s->tokens > 0;
+        if (some && s->rot > 0 && (!position || !turns)) return fail(TPMLP_ERR_INVALID_ARG, "NULL position or turns");
+        if (some && s->norm && (!gain_q || !gain_k)) return fail(TPMLP_ERR_INVALID_ARG, "NULL gain");
+        const size_t e = static_cast<size_t>(type_bytes(s->dtype));
+        if (!aligned_elt(gain_q, e) || !aligned_elt(gain_k, e) || !aligned_elt(position, 8) || !aligned_elt(turns, 8))
+            return fail(TPMLP_ERR_UNSUPPORTED, "a pointer is not on its element");
+        a.tokens = s->tokens, a.heads = s->heads, a.kv_heads = s->kv_heads, a.t = s->t, a.d = s->dim;
+        a.rot = s->rot, a.interleaved = s->layout == TPMLP_ROPE_INTERLEAVED, a.norm = s->norm != 0;
+        a.eps = s->eps, a.amplitude = s->amplitude;
+        a.gain_q = gain_q, a.gain_k = gain_k, a.position = position, a.turns = turns;
+        a.vec = !a.norm || (aligned16(gain_q) && aligned16(gain_k));
+        return TPMLP_OK;
+    }
+    tpmlp_status heads(tpmlp::HeadRows &to, const tpmlp_heads *h, int32_t n) {
+        if (!h || (!h->p && s->tokens > 0)) return fail(TPMLP_ERR_INVALID_ARG, "NULL heads");
+        if (h->row < 0 || h->shard < 0 || !span(s, h, n).sound()) return fail(TPMLP_ERR_INVALID_ARG, "rows or shards of heads overlap");
+        const int64_t e = type_bytes(s->dtype);
+        if (!aligned_elt(h->p, static_cast<size_t>(e))) return fail(TPMLP_ERR_UNSUPPORTED, "a pointer is not on its element");
+        to = {h->p, h->row, s->t > 1 ? h->shard : 0};
+        a.vec = a.vec && aligned16(h->p) && h->row * e % 16 == 0 && (s->t == 1 || h->shard * e % 16 == 0);
+        return TPMLP_OK;
+    }
+    // Whether an output meets what is read besides the heads.
+    bool over_inputs(const HeadSpan &o) const {
+        const int64_t e = type_bytes(s->dtype), g = s->norm ? s->dim * e : 0;
+        return meets_buffer(o, g ? a.gain_q : nullptr, g) || meets_buffer(o, g ? a.gain_k : nullptr, g) ||
+               (s->rot > 0 && (meets_buffer(o, a.position, 8 * s->tokens) || meets_buffer(o, a.turns, 4 * s->rot)));
+    }
+    template <typename F>
+    tpmlp_status launch(const char *name, void *stream, F f) const {
+        int sms;
+        const tpmlp_status rc = device_ready(sms);
+        if (rc != TPMLP_OK) return rc;
+        Timed timed(name, static_cast<cudaStream_t>(stream));
+        return from_cuda(f(static_cast<cudaStream_t>(stream)));
+    }
+};
+
+bool cache_attn_valid(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c) {
+    if (!s || !cache_valid(c) || s->tokens < 0 || s->batch < 0 || s->batch > (1LL << 20) || s->max_pages < 0) return false;
+    if (s->heads < 1 || s->heads % c->kv_heads != 0) return false;
+    if (s->tokens > (1LL << 31) - 1 || s->tokens * s->heads >= (1LL << 31)) return false;
+    if (s->max_pages > (1LL << 31) || s->max_pages * c->page_size >= (1LL << 31) - 1024) return false;
+    if (s->algo != TPMLP_ALGO_DEFAULT && s->algo != TPMLP_ALGO_SIMT) return false;
+    return s->tree_words >= 0 && std::isfinite(s->scale);
+}
+
+// status (1 KB) | counters | statistics | pieces.  Room for either kernel: which one runs depends on the
+// cache's alignment.
+struct CacheAttnLayout {
+    size_t ml, part, total;
+};
+constexpr int kCacheAttnBlocks = 160;  // tensor-core kernel: one per SM; the FFMA kernel two
+CacheAttnLayout cache_attn_layout(const tpmlp_kv_cache *c) {
+    const size_t rows = std::max<size_t>(2 * kCacheAttnBlocks * tpmlp::CACHE_ATTN_TC_ROWS,
+                                         4 * kCacheAttnBlocks * tpmlp::CACHE_ATTN_SIMT_ROWS);
+    CacheAttnLayout L;
+    L.ml = 4096;
+    L.part = L.ml + align_up(rows * 8, 1024);
+    L.total = L.part + align_up(rows * static_cast<size_t>(c->dim) * 4, 1024);
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+tpmlp_status tpmlp_rope_turns(const tpmlp_rope *r, uint64_t *turns) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!r || (!turns && r->rot > 0)) return invalid("tpmlp_rope_turns: NULL pointer");
+    if (r->rot < 0 || r->rot > 256 || r->rot % 2 != 0) return invalid("tpmlp_rope_turns: rot must be even, 0..256");
+    if (!(r->base >= 1.0) || !std::isfinite(r->base)) return invalid("tpmlp_rope_turns: base must be 1 or more");
+    const bool linear = r->scaling == TPMLP_ROPE_SCALE_LINEAR, parts = r->scaling == TPMLP_ROPE_SCALE_PARTS;
+    if (!linear && !parts && r->scaling != TPMLP_ROPE_SCALE_NONE) return invalid("tpmlp_rope_turns: unknown scaling");
+    if ((linear || parts) && (!(r->factor > 0.0) || !std::isfinite(r->factor)))
+        return invalid("tpmlp_rope_turns: factor must be positive");
+    if (parts && (!(r->low < r->high) || !std::isfinite(r->low) || !std::isfinite(r->high) || r->context <= 0))
+        return invalid("tpmlp_rope_turns: scaling by parts needs low < high and a context");
+    const double two_pi = 2.0 * std::acos(-1.0);
+    for (int i = 0; i < r->rot / 2; ++i) {
+        double f = std::pow(r->base, -2.0 * i / r->rot);
+        if (linear) f /= r->factor;
+        if (parts) {
+            const double n = static_cast<double>(r->context) * f / two_pi;
+            const double k = std::min(1.0, std::max(0.0, (n - r->low) / (r->high - r->low)));
+            f *= k + (1.0 - k) / r->factor;
+        }
+        if (!(f < two_pi)) return invalid("tpmlp_rope_turns: more than a turn per position");
+        const double t = std::ldexp(f / two_pi, 64);
+        turns[i] = t >= 18446744073709549568.0 ? ~uint64_t{0} : static_cast<uint64_t>(t);
+    }
+    return TPMLP_OK;
+}
+
+size_t tpmlp_qk_workspace_bytes(const tpmlp_qk_shape *s) {
+    if (!qk_valid(s)) return 0;
+    const int64_t n = s->norm ? tpmlp::qk_partial_floats(s->tokens, s->dim) : 0;
+    return QK_STATUS + align_up(static_cast<size_t>(n) * 4, 1024);
+}
+
+tpmlp_status tpmlp_qk_forward(const tpmlp_qk_shape *s, const tpmlp_heads *Q, const tpmlp_heads *K, const void *gain_q,
+                              const void *gain_k, const int64_t *position, const uint64_t *turns, const tpmlp_heads *Qr,
+                              const tpmlp_heads *Kr, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!qk_valid(s)) return invalid("tpmlp_qk_forward: invalid shape");
+    QkCall c("tpmlp_qk_forward", s);
+    tpmlp_status rc = c.common(gain_q, gain_k, position, turns);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.q, Q, s->heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.k, K, s->kv_heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.oq, Qr, s->heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.ok, Kr, s->kv_heads);
+    if (rc != TPMLP_OK) return rc;
+    if (s->tokens == 0) return TPMLP_OK;
+    const HeadSpan q = span(s, Q, s->heads), k = span(s, K, s->kv_heads), qr = span(s, Qr, s->heads),
+                   kr = span(s, Kr, s->kv_heads);
+    if ((!qr.same(q) && meet(qr, q)) || (!kr.same(k) && meet(kr, k)) || meet(qr, k) || meet(kr, q) || meet(qr, kr) ||
+        c.over_inputs(qr) || c.over_inputs(kr))
+        return c.fail(TPMLP_ERR_INVALID_ARG, "an output overlaps an input or the other output");
+    return c.launch("qk_forward", stream, [&](cudaStream_t st) {
+        const cudaError_t e = tpmlp::launch_qk_forward(s->dtype == TPMLP_BF16, c.a, false, st);
+        if (e == cudaSuccess) g_launches.fetch_add(1);
+        return e;
+    });
+}
+
+tpmlp_status tpmlp_qk_backward(const tpmlp_qk_shape *s, const tpmlp_heads *Q, const tpmlp_heads *K, const void *gain_q,
+                               const void *gain_k, const int64_t *position, const uint64_t *turns, const tpmlp_heads *dQr,
+                               const tpmlp_heads *dKr, const tpmlp_heads *dQ, const tpmlp_heads *dK, void *dgain_q,
+                               void *dgain_k, void *workspace, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!qk_valid(s)) return invalid("tpmlp_qk_backward: invalid shape");
+    QkCall c("tpmlp_qk_backward", s);
+    if (!workspace || (s->norm && (!dgain_q || !dgain_k))) return c.fail(TPMLP_ERR_INVALID_ARG, "NULL workspace or gain gradient");
+    tpmlp_status rc = c.common(gain_q, gain_k, position, turns);
+    if (rc == TPMLP_OK && s->norm) rc = c.heads(c.a.q, Q, s->heads);
+    if (rc == TPMLP_OK && s->norm) rc = c.heads(c.a.k, K, s->kv_heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.dq, dQr, s->heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.dk, dKr, s->kv_heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.oq, dQ, s->heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.ok, dK, s->kv_heads);
+    if (rc != TPMLP_OK) return rc;
+    const size_t e = static_cast<size_t>(type_bytes(s->dtype));
+    if (!aligned16(workspace) || (s->norm && (!aligned_elt(dgain_q, e) || !aligned_elt(dgain_k, e))))
+        return c.fail(TPMLP_ERR_UNSUPPORTED, "workspace not on 16 bytes, or a gain gradient not on its element");
+    const int64_t gain_bytes = s->dim * static_cast<int64_t>(e);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s->tokens == 0) {
+        if (!s->norm) return TPMLP_OK;
+        cudaError_t r = cudaMemsetAsync(dgain_q, 0, static_cast<size_t>(gain_bytes), st);
+        if (r == cudaSuccess) r = cudaMemsetAsync(dgain_k, 0, static_cast<size_t>(gain_bytes), st);
+        return from_cuda(r);
+    }
+    const HeadSpan gq = span(s, dQr, s->heads), gk = span(s, dKr, s->kv_heads), oq = span(s, dQ, s->heads),
+                   ok = span(s, dK, s->kv_heads);
+    bool bad = (!oq.same(gq) && meet(oq, gq)) || (!ok.same(gk) && meet(ok, gk)) || meet(oq, gk) || meet(ok, gq) ||
+               meet(oq, ok) || c.over_inputs(oq) || c.over_inputs(ok);
+    if (s->norm) {
+        const HeadSpan q = span(s, Q, s->heads), k = span(s, K, s->kv_heads);
+        bad = bad || (!oq.same(q) && meet(oq, q)) || (!ok.same(k) && meet(ok, k)) || meet(oq, k) || meet(ok, q);
+        for (const HeadSpan &x : {gq, gk, oq, ok, q, k})
+            bad = bad || meets_buffer(x, dgain_q, gain_bytes) || meets_buffer(x, dgain_k, gain_bytes);
+        bad = bad || outputs_overlap({{dgain_q, gain_bytes}, {dgain_k, gain_bytes}},
+                                     {{gain_q, gain_bytes}, {gain_k, gain_bytes}, {position, 8 * s->tokens}, {turns, 4 * s->rot}});
+    }
+    if (bad) return c.fail(TPMLP_ERR_INVALID_ARG, "an output overlaps an input or another output");
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    c.a.status = reinterpret_cast<uint32_t *>(ws);
+    c.a.part = reinterpret_cast<float *>(ws + QK_STATUS);
+    c.a.dgain_q = dgain_q, c.a.dgain_k = dgain_k;
+    return c.launch("qk_backward", stream, [&](cudaStream_t q) {
+        int n = 0;
+        const cudaError_t r = tpmlp::launch_qk_backward(s->dtype == TPMLP_BF16, c.a, q, &n);
+        g_launches.fetch_add(static_cast<uint64_t>(n));
+        return r;
+    });
+}
+
+tpmlp_status tpmlp_kv_append(const tpmlp_qk_shape *s, const tpmlp_kv_cache *cache, const tpmlp_heads *Q,
+                             const tpmlp_heads *K, const tpmlp_heads *V, const void *gain_q, const void *gain_k,
+                             const int64_t *position, const uint64_t *turns, const int64_t *slot, const tpmlp_heads *Qr,
+                             void *workspace, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!qk_valid(s) || !cache_valid(cache)) return invalid("tpmlp_kv_append: invalid shape or cache");
+    QkCall c("tpmlp_kv_append", s);
+    if (cache->kv_heads != s->kv_heads || cache->dim != s->dim || cache->dtype != s->dtype)
+        return c.fail(TPMLP_ERR_INVALID_ARG, "heads, dim or type of shape and cache differ");
+    if (!workspace || !cache->K || !cache->V || (!slot && s->tokens > 0)) return c.fail(TPMLP_ERR_INVALID_ARG, "NULL pointer");
+    tpmlp_status rc = c.common(gain_q, gain_k, position, turns);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.q, Q, s->heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.k, K, s->kv_heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.v, V, s->kv_heads);
+    if (rc == TPMLP_OK) rc = c.heads(c.a.oq, Qr, s->heads);
+    if (rc != TPMLP_OK) return rc;
+    const int64_t e = type_bytes(s->dtype);
+    if (!aligned16(workspace) || !aligned_elt(slot, 8) || !aligned_elt(cache->K, static_cast<size_t>(e)) ||
+        !aligned_elt(cache->V, static_cast<size_t>(e)))
+        return c.fail(TPMLP_ERR_UNSUPPORTED, "workspace not on 16 bytes, or a pointer not on its element");
+    if (s->tokens == 0) return TPMLP_OK;
+    const HeadSpan q = span(s, Q, s->heads), k = span(s, K, s->kv_heads), v = span(s, V, s->kv_heads),
+                   qr = span(s, Qr, s->heads);
+    bool bad = (!qr.same(q) && meet(qr, q)) || meet(qr, k) || meet(qr, v) || c.over_inputs(qr) ||
+               meets_buffer(qr, slot, 8 * s->tokens);
+    const int64_t bytes = cache_bytes(cache), gain = s->norm ? s->dim * e : 0;
+    for (const void *p : {cache->K, cache->V}) {
+        for (const HeadSpan &x : {q, k, v, qr}) bad = bad || meets_buffer(x, p, bytes);
+        bad = bad || outputs_overlap({{p, bytes}}, {{slot, 8 * s->tokens}, {s->rot > 0 ? position : nullptr, 8 * s->tokens},
+                                                    {s->rot > 0 ? turns : nullptr, 4 * s->rot},
+                                                    {gain ? gain_q : nullptr, gain}, {gain ? gain_k : nullptr, gain}});
+    }
+    if (bad) return c.fail(TPMLP_ERR_INVALID_ARG, "an output overlaps an input or another output");
+    c.a.slot = slot;
+    c.a.cache_k = cache->K, c.a.cache_v = cache->V;
+    c.a.page_size = cache->page_size, c.a.slots = cache->pages * cache->page_size;
+    c.a.page_stride = cache->page_stride, c.a.head_stride = cache->head_stride, c.a.token_stride = cache->token_stride;
+    c.a.status = static_cast<uint32_t *>(workspace);
+    c.a.vec = c.a.vec && aligned16(cache->K) && aligned16(cache->V) && cache->page_stride * e % 16 == 0 &&
+              cache->head_stride * e % 16 == 0 && cache->token_stride * e % 16 == 0;
+    return c.launch("kv_append", stream, [&](cudaStream_t st) {
+        const cudaError_t r = tpmlp::launch_qk_forward(s->dtype == TPMLP_BF16, c.a, true, st);
+        if (r == cudaSuccess) g_launches.fetch_add(1);
+        return r;
+    });
+}
+
+size_t tpmlp_cache_attn_workspace_bytes(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c) {
+    return cache_attn_valid(s, c) ? cache_attn_layout(c).total : 0;
+}
+
+tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c, const void *Q, const int32_t *q_start,
+                              const int32_t *kv_len, const int32_t *page_table, const int64_t *tree, void *O,
+                              void *workspace, void *stream) {
+    tpmlp::g_last_error[0] = '\0';
+    if (!cache_attn_valid(s, c)) return invalid("tpmlp_cache_attn: invalid shape or cache");
+    const bool some = s->tokens > 0 && s->batch > 0;
+    if (!workspace || !c->K || !c->V || (s->tokens > 0 && (!Q || !O)) || (s->batch > 0 && (!q_start || !kv_len)) ||
+        (s->batch > 0 && s->max_pages > 0 && !page_table))
+        return invalid("tpmlp_cache_attn: NULL pointer");
+    if (tree && s->tree_words < 1) return invalid("tpmlp_cache_attn: a tree needs tree_words");
+    const int64_t e = type_bytes(c->dtype);
+    if (c->dim % 8 != 0 || !aligned16(Q) || !aligned16(O) || !aligned16(workspace) || !aligned_elt(q_start, 4) ||
+        !aligned_elt(kv_len, 4) || !aligned_elt(page_table, 4) || !aligned_elt(tree, 8) ||
+        !aligned_elt(c->K, static_cast<size_t>(e)) || !aligned_elt(c->V, static_cast<size_t>(e))) {
+        tpmlp::set_last_error("tpmlp_cache_attn: dim must be a multiple of 8, Q, O and the workspace on 16 bytes, other "
+                              "pointers on their elements");
+        return TPMLP_ERR_UNSUPPORTED;
+    }
+    if (!some) return TPMLP_OK;
+    const int64_t rows = s->tokens * s->heads * c->dim * e;
+    if (outputs_overlap({{O, rows}}, {{Q, rows}, {c->K, cache_bytes(c)}, {c->V, cache_bytes(c)}, {q_start, 4 * (s->batch + 1)},
+                                      {kv_len, 4 * s->batch}, {page_table, 4 * s->batch * s->max_pages},
+                                      {tree, tree ? 8 * s->tokens * s->tree_words : 0}}))
+        return invalid("tpmlp_cache_attn: O overlaps an input");
+    int sms;
+    const tpmlp_status rc = device_ready(sms);
+    if (rc != TPMLP_OK) return rc;
+    const CacheAttnLayout L = cache_attn_layout(c);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    tpmlp::CacheAttnArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.tokens = s->tokens, a.batch = s->batch, a.max_pages = s->max_pages;
+    a.heads = s->heads, a.kv_heads = c->kv_heads, a.group = s->heads / c->kv_heads, a.d = c->dim;
+    a.q = Q, a.o = O, a.q_start = q_start, a.kv_len = kv_len, a.table = page_table;
+    a.tree = tree, a.tree_words = s->tree_words;
+    a.scale_log2 = static_cast<float>(static_cast<double>(s->scale) * 1.4426950408889634);
+    a.k = c->K, a.v = c->V;
+    a.pages = c->pages, a.page_size = c->page_size;
+    a.page_stride = c->page_stride, a.head_stride = c->head_stride, a.token_stride = c->token_stride;
+    a.vec = aligned16(c->K) && aligned16(c->V) && c->page_stride * e % 16 == 0 && c->head_stride * e % 16 == 0 &&
+            c->token_stride * e % 16 == 0;
+    a.status = reinterpret_cast<uint32_t *>(ws);
+    a.counters = reinterpret_cast<uint32_t *>(ws + STATUS_BYTES);
+    a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
+    a.part = reinterpret_cast<float *>(ws + L.part);
+    a.wait_ns = g_wait_ns.load();
+    sms = std::min(sms, kCacheAttnBlocks);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Timed timed("cache_attn", st);
+    const cudaError_t r = tpmlp::launch_cache_attn_simt(c->dtype == TPMLP_BF16, a, sms, st);
+    if (r == cudaSuccess) g_launches.fetch_add(1);
+    return from_cuda(r);
+}
+
+}  // extern "C"

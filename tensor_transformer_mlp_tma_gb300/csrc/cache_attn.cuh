@@ -1,0 +1,251 @@
+// How attention over a paged cache is divided among the blocks, and how its pieces are joined.
+//
+// The new tokens of a sequence and the `group` query heads that share a key head are the rows of
+// one product: row r is token r / group, head r % group of the group.  A unit is (sequence, key
+// head, ROWS consecutive rows); its work is its tiles of KEYS keys.  The lengths are known on the
+// device only (a captured graph is replayed with other lengths), so every block adds up the tiles
+// of all units itself and takes an equal share [c total / blocks, (c + 1) total / blocks) of them
+// in order: long sequences are cut wherever a share ends, short ones fill a block together, and
+// the shares differ by one tile at most.
+//
+// A unit that lies in one block is written by it.  The pieces of a cut one go to the workspace as
+// (maximum, sum, unnormalised output) in fp32, two places per block: [0] for a unit that began in
+// an earlier block, [1] for one that begins in this block and goes on.  The block that finds all other
+// pieces done joins them, in the order of the keys, so that results do not depend on which one it is.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace tpmlp {
+namespace cattn {
+
+constexpr uint32_t STATUS_INVALID = 1;  // TPMLP_ERR_INVALID_ARG
+
+__device__ __forceinline__ void report(const CacheAttnArgs &a, uint32_t status, uint32_t detail) {
+    if (atomicCAS(a.status, 0u, status) == 0u) a.status[1] = detail;
+}
+
+// One sequence's new tokens and keys.  What does not fit is reported (by one block): a sequence whose
+// q_start decreases or leaves the tokens has none (its rows may be another's), and with a length
+// that is too short for its tokens or too long for the table its rows see nothing.
+struct Seq {
+    int q0, n;         // first new token, their number
+    int len, prefix;   // keys in all, keys before the new tokens'
+};
+
+__device__ __forceinline__ Seq sequence(const CacheAttnArgs &a, int64_t b, bool tell) {
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], len = a.kv_len[b];
+    const bool starts = s0 >= 0 && s1 >= s0 && s1 <= a.tokens;
+    Seq s;
+    s.q0 = starts ? s0 : 0, s.n = starts ? s1 - s0 : 0;
+    const bool fits = len >= s.n && len <= a.max_pages * a.page_size;
+    s.len = fits ? len : 0;
+    s.prefix = fits ? len - s.n : 0;
+    if (!(starts && fits) && tell) report(a, STATUS_INVALID, static_cast<uint32_t>(b));
+    return s;
+}
+
+// Whether row `token` (counted in its sequence) sees the key.
+__device__ __forceinline__ bool visible(const CacheAttnArgs &a, const Seq &s, int token, int key) {
+    const int j = key - s.prefix;
+    if (j < 0) return true;
+    if (key >= s.len) return false;
+    if (!a.tree) return j <= token;
+    if (j >= 64 * a.tree_words) return false;
+    return (a.tree[static_cast<int64_t>(s.q0 + token) * a.tree_words + (j >> 6)] >> (j & 63)) & 1;
+}
+
+// The page of a key, or -1 where the table holds none.
+__device__ __forceinline__ int page_of(const CacheAttnArgs &a, int64_t b, int64_t page) {
+    const int p = a.table[b * a.max_pages + page];
+    if (p >= 0 && p < a.pages) return p;
+    report(a, STATUS_INVALID, static_cast<uint32_t>(b));
+    return -1;
+}
+
+template <int ROWS, int KEYS>
+struct Tiles {
+    static __device__ __forceinline__ int row_tiles(const CacheAttnArgs &a, const Seq &s) {
+        return (s.n * a.group + ROWS - 1) / ROWS;
+    }
+    // Tiles of one unit, one at least: rows that see nothing are written too.
+    static __device__ __forceinline__ int of(const CacheAttnArgs &a, const Seq &s, int rt) {
+        int keys = s.len;
+        if (!a.tree && s.len > 0) {
+            const int rows = min(s.n * a.group, (rt + 1) * ROWS);
+            keys = s.prefix + (rows - 1) / a.group + 1;
+        }
+        return max(1, (keys + KEYS - 1) / KEYS);
+    }
+    static __device__ __forceinline__ int64_t per_head(const CacheAttnArgs &a, const Seq &s) {
+        const int n = row_tiles(a, s);
+        if (a.tree || s.len == 0) return static_cast<int64_t>(n) * (n > 0 ? of(a, s, 0) : 0);
+        int64_t sum = 0;
+        for (int rt = 0; rt < n; ++rt) sum += of(a, s, rt);
+        return sum;
+    }
+};
+
+struct Unit {
+    Seq s;
+    int b, head;          // sequence, key head
+    int row0, rows;       // rows of the sequence
+    int tile0, tiles;     // this block's tiles of the unit
+    bool cut;             // the unit has tiles in other blocks
+    int place;            // of this block's piece
+    int first, last;      // blocks that hold pieces
+};
+
+// A block's share of the work.
+template <int ROWS, int KEYS>
+struct Walk {
+    using T = Tiles<ROWS, KEYS>;
+    int64_t total, pos, end;   // tiles of all, of this block
+    int blocks;
+    int b, head, rt, tile;     // where pos is
+    int count;                 // tiles of the unit
+
+    struct Shared {
+        int64_t warp_sum[8];
+        int64_t start_off;
+        int start_b;
+    };
+
+    // All threads (at least 256) of the block.
+    __device__ void begin(const CacheAttnArgs &a, Shared &sh) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const int per = static_cast<int>((a.batch + 255) / 256);
+        int64_t mine = 0;
+        if (tid < 256)
+            for (int i = 0; i < per; ++i) {
+                const int64_t s = static_cast<int64_t>(tid) * per + i;
+                if (s < a.batch) mine += a.kv_heads * T::per_head(a, sequence(a, s, blockIdx.x == 0));
+            }
+        int64_t scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += up;
+        }
+        if (tid < 256 && lane == 31) sh.warp_sum[tid >> 5] = scan;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w < (tid >> 5)) before += sh.warp_sum[w];
+            total += sh.warp_sum[w];
+        }
+        blocks = static_cast<int>(total < gridDim.x ? total : gridDim.x);
+        const int64_t c = blockIdx.x;
+        pos = end = 0;
+        if (c < blocks) pos = c * total / blocks, end = (c + 1) * total / blocks;
+        int64_t at = before + scan - mine;
+        if (tid < 256 && c < blocks && at <= pos && pos < at + mine) {
+            for (int i = 0; i < per; ++i) {
+                const int64_t s = static_cast<int64_t>(tid) * per + i;
+                const int64_t cost = s < a.batch ? a.kv_heads * T::per_head(a, sequence(a, s, false)) : 0;
+                if (pos < at + cost) {
+                    sh.start_b = static_cast<int>(s);
+                    sh.start_off = pos - at;
+                    break;
+                }
+                at += cost;
+            }
+        }
+        __syncthreads();
+        if (pos >= end) return;
+        b = sh.start_b;
+        const Seq s = sequence(a, b, false);
+        int64_t off = sh.start_off;
+        const int64_t ph = T::per_head(a, s);
+        head = static_cast<int>(off / ph);
+        off -= head * ph;
+        rt = 0;
+        while (off >= (count = T::of(a, s, rt))) off -= count, ++rt;
+        tile = static_cast<int>(off);
+    }
+
+    __device__ __forceinline__ bool next(const CacheAttnArgs &a, Unit &u) {
+        if (pos >= end) return false;
+        u.s = sequence(a, b, false);
+        u.b = b, u.head = head, u.row0 = rt * ROWS;
+        u.rows = min(ROWS, u.s.n * a.group - u.row0);
+        u.tile0 = tile;
+        u.tiles = static_cast<int>(min(static_cast<int64_t>(count - tile), end - pos));
+        const int64_t g0 = pos - tile;
+        u.cut = u.tiles != count;
+        u.place = tile == 0 ? 1 : 0;
+        u.first = u.last = blockIdx.x;
+        if (u.cut) {
+            // the block c with c total / blocks <= g < (c + 1) total / blocks, whole numbers
+            u.first = static_cast<int>(((g0 + 1) * blocks - 1) / total);
+            u.last = static_cast<int>(((g0 + count) * blocks - 1) / total);
+        }
+        pos += u.tiles;
+        if (pos < end) {  // the next unit
+            tile = 0;
+            Seq s = u.s;
+            if (++rt >= T::row_tiles(a, s)) {
+                rt = 0;
+                if (++head >= a.kv_heads) {
+                    head = 0;
+                    do s = sequence(a, ++b, false);
+                    while (s.n == 0);
+                }
+            }
+            count = T::of(a, s, rt);
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ float scale_of(float from, float to) { return from == to ? 1.0f : exp2f(from - to); }
+
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    uint2 w;
+    w.x = *reinterpret_cast<uint32_t *>(&lo);
+    w.y = *reinterpret_cast<uint32_t *>(&hi);
+    *reinterpret_cast<uint2 *>(p) = w;
+}
+
+// The output row of a unit's row.
+template <typename E>
+__device__ __forceinline__ E *out_row(const CacheAttnArgs &a, const Unit &u, int row) {
+    const int r = u.row0 + row, token = r / a.group;
+    return static_cast<E *>(a.o) +
+           (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
+}
+
+// Joins a cut unit's pieces; `threads` threads, `tid` of them.
+template <typename E, int ROWS>
+__device__ __forceinline__ void join(const CacheAttnArgs &a, const Unit &u, int tid, int threads) {
+    const int quads = a.d / 4;
+    for (int i = tid; i < u.rows * quads; i += threads) {
+        const int row = i / quads, e = (i - row * quads) * 4;
+        float m = -INFINITY, l = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int c = u.first; c <= u.last; ++c) {
+            const int64_t at = (2 * static_cast<int64_t>(c) + (c == u.first ? 1 : 0)) * ROWS + row;
+            const float2 ml = __ldcg(a.part_ml + at);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part + at * a.d + e));
+            const float top = fmaxf(m, ml.x), f = scale_of(m, top), g = scale_of(ml.x, top);
+            l = l * f + ml.y * g;
+            x.x = x.x * f + y.x * g;
+            x.y = x.y * f + y.y * g;
+            x.z = x.z * f + y.z * g;
+            x.w = x.w * f + y.w * g;
+            m = top;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing: zeros
+        put4(out_row<E>(a, u, row) + e, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    }
+}
+
+}  // namespace cattn
+}  // namespace tpmlp

@@ -1,0 +1,271 @@
+// Attention over a paged cache on FFMA kernels: fp32 caches, and bf16 ones whose layout the
+// tensor-core kernel does not take; any page size.
+//
+//   O = softmax(scale Q K^T over the visible keys) V,  one pass over the keys with the running
+//   maximum m and sum l of each row:  m' = max(m, max s),  l' = l 2^(m - m') + sum 2^(s - m'),
+//   O' = O 2^(m - m') + P V,  s in units of log2.
+//
+// A block takes 32 rows (tokens and the heads that share their keys) and 64 keys at a time, all
+// of them in shared memory in fp32.  Few rows are bound by reading the cache, many by the FFMA rate
+// and by shared memory: a thread forms up to 8 scores of one key, then 4 x 4 outputs.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "cache_attn.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace tpmlp {
+namespace cattn {
+
+constexpr int SR = CACHE_ATTN_SIMT_ROWS;
+constexpr int SK = 64;
+constexpr int STHREADS = 256;
+constexpr int P_LD = SR + 4;
+
+__device__ __forceinline__ float4 get4(const float *p, bool vec) {
+    return vec ? *reinterpret_cast<const float4 *>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ float4 get4(const __nv_bfloat16 *p, bool vec) {
+    if (!vec) return make_float4(__bfloat162float(p[0]), __bfloat162float(p[1]), __bfloat162float(p[2]), __bfloat162float(p[3]));
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162 *>(&w.x), hi = *reinterpret_cast<const __nv_bfloat162 *>(&w.y);
+    return make_float4(__low2float(lo), __high2float(lo), __low2float(hi), __high2float(hi));
+}
+
+inline size_t simt_smem(int d) {
+    return sizeof(float) * (static_cast<size_t>(SR) * d + SK * (d + 4) + SK * d + SK * P_LD + 3 * SR);
+}
+
+template <typename E>
+__global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
+    extern __shared__ float4 smem4[];
+    __shared__ typename Walk<SR, SK>::Shared wsh;
+    __shared__ int64_t where[SK];
+    __shared__ int last_sh;
+    const int d = a.d, quads = d / 4, kld = d + 4;
+    float *Q = reinterpret_cast<float *>(smem4), *K = Q + SR * d, *V = K + SK * kld, *P = V + SK * d;
+    float *m_sh = P + SK * P_LD, *l_sh = m_sh + SR, *f_sh = l_sh + SR;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    Walk<SR, SK> walk;
+    walk.begin(a, wsh);
+
+    // the output's threads: `cols` of four components each, `groups` of them; with fewer row quads
+    // than groups the keys are shared out too
+    int cols = 1;
+    while (cols < quads) cols *= 2;
+    // (at most 32 groups: their sums are added up in the space of K, V and P, 128 d floats and more)
+    const int groups = min(STHREADS / cols, 32), col = tid & (cols - 1), group = tid / cols;
+
+    Unit u;
+    while (walk.next(a, u)) {
+        const int rq = (u.rows + 3) / 4;
+        int rq2 = 1;
+        while (rq2 < rq) rq2 *= 2;
+        const int key_groups = rq2 < groups ? groups / rq2 : 1;
+        const int quad0 = rq2 < groups ? group % rq2 : group, kg = rq2 < groups ? group / rq2 : 0;
+        const bool mine = col < quads && group < groups;
+        float acc[2][4][4] = {};
+        __syncthreads();  // the unit before is done with shared memory
+        for (int i = tid; i < SR * quads; i += STHREADS) {
+            const int row = i / quads, e = (i - row * quads) * 4;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (row < u.rows) {
+                const int r = u.row0 + row, token = r / a.group;
+                const int64_t at = (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * d + e;
+                x = get4(static_cast<const E *>(a.q) + at, true);
+            }
+            *reinterpret_cast<float4 *>(Q + row * d + e) = x;
+        }
+        if (tid < SR) m_sh[tid] = -INFINITY, l_sh[tid] = 0.0f;
+        for (int t = u.tile0; t < u.tile0 + u.tiles; ++t) {
+            const int key0 = t * SK;
+            const bool masked = key0 + SK > u.s.prefix;
+            __syncthreads();
+            if (tid < SK) {
+                int64_t off = -1;  // no key: zeros
+                if (key0 + tid < u.s.len) {
+                    const int64_t at = (key0 + tid) / a.page_size;
+                    const int page = page_of(a, u.b, at);
+                    if (page >= 0)
+                        off = page * a.page_stride + u.head * a.head_stride + (key0 + tid - at * a.page_size) * a.token_stride;
+                }
+                where[tid] = off;
+            }
+            __syncthreads();
+            for (int i = tid; i < SK * quads; i += STHREADS) {
+                const int key = i / quads, e = (i - key * quads) * 4;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+                const int64_t off = where[key];
+                if (off >= 0) {
+                    x = get4(static_cast<const E *>(a.k) + off + e, a.vec);
+                    y = get4(static_cast<const E *>(a.v) + off + e, a.vec);
+                }
+                *reinterpret_cast<float4 *>(K + key * kld + e) = x;
+                *reinterpret_cast<float4 *>(V + key * d + e) = y;
+            }
+            __syncthreads();
+            {
+                // scores of one key and rows rg, rg + 4, ...
+                const int key = tid & (SK - 1), rg = tid / SK;
+                float s[SR / 4] = {};
+                const int nr = (u.rows + 3) / 4;
+                for (int e = 0; e < d; e += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(K + key * kld + e);
+#pragma unroll
+                    for (int i = 0; i < SR / 4; ++i)
+                        if (i < nr) {
+                            const float4 q = *reinterpret_cast<const float4 *>(Q + (rg + 4 * i) * d + e);
+                            s[i] += q.x * k.x + q.y * k.y + (q.z * k.z + q.w * k.w);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < SR / 4; ++i)
+                    if (i < nr) {
+                        const int row = rg + 4 * i;
+                        const bool seen = row < u.rows && (!masked || visible(a, u.s, (u.row0 + row) / a.group, key0 + key));
+                        // -inf marks what the row does not see: a score is raised to the lowest finite number
+                        const float x = s[i] * a.scale_log2;
+                        P[key * P_LD + row] = !seen ? -INFINITY : (x == -INFINITY ? -3.4e38f : x);
+                    }
+            }
+            __syncthreads();
+            for (int row = warp; row < u.rows; row += STHREADS / 32) {
+                const float s0 = P[lane * P_LD + row], s1 = P[(lane + 32) * P_LD + row];
+                float top = fmaxf(s0, s1);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float m = m_sh[row], mn = fmaxf(m, top);
+                // masked weights are marked by a negative number, not by zero: 0 x NaN would be NaN
+                const float p0 = s0 == -INFINITY ? -1.0f : exp2f(s0 - mn), p1 = s1 == -INFINITY ? -1.0f : exp2f(s1 - mn);
+                float sum = (s0 == -INFINITY ? 0.0f : p0) + (s1 == -INFINITY ? 0.0f : p1);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                P[lane * P_LD + row] = p0;
+                P[(lane + 32) * P_LD + row] = p1;
+                __syncwarp();
+                if (lane == 0) {
+                    const float f = scale_of(m, mn);
+                    f_sh[row] = f, m_sh[row] = mn, l_sh[row] = l_sh[row] * f + sum;
+                }
+            }
+            __syncthreads();
+            if (mine) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int quad = quad0 + h * groups;
+                    if (quad >= rq) continue;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float f = 4 * quad + r < u.rows ? f_sh[4 * quad + r] : 1.0f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[h][r][c] *= f;
+                    }
+                    for (int key = kg; key < SK; key += key_groups) {
+                        const float4 p = *reinterpret_cast<const float4 *>(P + key * P_LD + 4 * quad);
+                        const float4 v = *reinterpret_cast<const float4 *>(V + key * d + 4 * col);
+                        const float pr[4] = {p.x, p.y, p.z, p.w}, vc[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (!masked || !(pr[r] < 0.0f)) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) acc[h][r][c] += pr[r] * vc[c];
+                            }
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        // the key groups' sums, through the space of K
+        if (key_groups > 1) {
+            float *sums = K;
+            if (mine && kg > 0) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    put4(sums + (((kg - 1) * rq2 + quad0) * 4 + r) * d + 4 * col,
+                         make_float4(acc[0][r][0], acc[0][r][1], acc[0][r][2], acc[0][r][3]));
+            }
+            __syncthreads();
+            if (mine && kg == 0) {
+                for (int g = 1; g < key_groups; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float4 x = *reinterpret_cast<const float4 *>(sums + (((g - 1) * rq2 + quad0) * 4 + r) * d + 4 * col);
+                        acc[0][r][0] += x.x, acc[0][r][1] += x.y, acc[0][r][2] += x.z, acc[0][r][3] += x.w;
+                    }
+            }
+        }
+        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * SR;
+        if (mine && kg == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int quad = quad0 + h * groups;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 4 * quad + r;
+                    if (quad >= rq || row >= u.rows) continue;
+                    float4 x = make_float4(acc[h][r][0], acc[h][r][1], acc[h][r][2], acc[h][r][3]);
+                    if (u.cut) {
+                        __stcg(reinterpret_cast<float4 *>(a.part + (piece + row) * d + 4 * col), x);
+                    } else {
+                        const float l = l_sh[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
+                        put4(out_row<E>(a, u, row) + 4 * col, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+                    }
+                }
+            }
+        }
+        if (u.cut) {
+            if (tid < u.rows) __stcg(a.part_ml + piece + tid, make_float2(m_sh[tid], l_sh[tid]));
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t pieces = static_cast<uint32_t>(u.last - u.first + 1);
+                last_sh = atomicAdd(a.counters + u.first, 1u) == pieces - 1;
+                if (last_sh) a.counters[u.first] = 0u;
+                __threadfence();
+            }
+            __syncthreads();
+            if (last_sh) join<E, SR>(a, u, tid, STHREADS);
+        }
+    }
+}
+
+template <typename E>
+cudaError_t launch_simt(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
+    static std::mutex mu;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!set[dev]) {
+            e = cudaFuncSetAttribute(simt_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(simt_smem(256)));
+            if (e != cudaSuccess) return e;
+            set[dev] = true;
+        }
+    }
+    return launch_pdl(simt_kernel<E>, dim3(static_cast<unsigned>(blocks)), STHREADS, simt_smem(a.d), st, a);
+}
+
+}  // namespace cattn
+
+// Two blocks per SM where their shared memory fits (225 KB beside 1 KB each).
+int cache_attn_simt_blocks(bool, int d, int num_sms) {
+    const int per = 2 * (cattn::simt_smem(d) + 1024) <= 225 * 1024 ? 2 : 1;
+    const int n = per * num_sms;
+    return n < CACHE_ATTN_COUNTERS ? n : CACHE_ATTN_COUNTERS;
+}
+
+cudaError_t launch_cache_attn_simt(bool is_bf16, const CacheAttnArgs &a, int num_sms, cudaStream_t st) {
+    const int blocks = cache_attn_simt_blocks(is_bf16, a.d, num_sms);
+    return is_bf16 ? cattn::launch_simt<__nv_bfloat16>(a, blocks, st) : cattn::launch_simt<float>(a, blocks, st);
+}
+
+}  // namespace tpmlp

@@ -302,6 +302,65 @@ cudaError_t launch_ns_chain(const NsChain &c, cudaStream_t st);
 cudaError_t launch_ortho_unpad(const void *in, int64_t batch, int64_t rows, int64_t cols, int64_t P, int64_t Q,
                                void *out, cudaStream_t st);
 
+// Norms of queries and keys per head and the position rotation (qk.cu).  Head j of shard i of
+// token r is at p + r * row + i * shard + j * d, in elements.
+struct HeadRows {
+    const void *p;
+    int64_t row, shard;
+};
+struct QkArgs {
+    int64_t tokens;
+    int heads, kv_heads, t, d;
+    int rot;           // components that rotate
+    bool interleaved;  // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+    bool norm;
+    float eps, amplitude;
+    HeadRows q, k, v;       // inputs (v: append only)
+    HeadRows oq, ok;        // outputs: rotated (ok: not for append), or the gradients of q and k
+    const void *gain_q, *gain_k;  // [d]
+    const int64_t *position;      // [tokens]
+    const uint64_t *turns;        // [rot / 2]: turns per position, times 2^64
+    bool vec;               // every row start and stride on 16 bytes
+    // append: token r's K and V go to slot[r] of the cache
+    const int64_t *slot;
+    void *cache_k, *cache_v;
+    int64_t page_size, slots, page_stride, head_stride, token_stride;
+    uint32_t *status;
+    // backward: gradients of the rotated q and k
+    HeadRows dq, dk;
+    float *part;            // qk_partial_floats() floats
+    void *dgain_q, *dgain_k;
+};
+int64_t qk_partial_floats(int64_t tokens, int d);
+cudaError_t launch_qk_forward(bool is_bf16, const QkArgs &a, bool append, cudaStream_t st);
+cudaError_t launch_qk_backward(bool is_bf16, const QkArgs &a, cudaStream_t st, int *launches);
+
+// Attention of new tokens over a paged cache (cache_attn.cuh says how the work is divided).
+struct CacheAttnArgs {
+    int64_t tokens, batch, max_pages;
+    int heads, kv_heads, group, d;  // group = heads / kv_heads
+    const void *q;                  // [tokens][heads][d]
+    void *o;
+    const int32_t *q_start;         // [batch + 1]
+    const int32_t *kv_len;          // [batch]
+    const int32_t *table;           // [batch][max_pages]
+    const int64_t *tree;            // [tokens][tree_words], null: causal
+    int tree_words;
+    float scale_log2;               // the scores' factor times log2(e)
+    const void *k, *v;              // page p, head h, row r at p * page_stride + h * head_stride + r * token_stride
+    int64_t pages, page_size, page_stride, head_stride, token_stride;
+    bool vec;                       // rows start on 16 bytes
+    uint32_t *status, *counters;    // counters: one per block, zero between calls
+    float *part;                    // [2 blocks][rows per tile][d]
+    float2 *part_ml;                // [2 blocks][rows per tile]: maximum (log2), sum
+    uint64_t wait_ns;
+};
+constexpr int CACHE_ATTN_COUNTERS = 512;  // blocks at most
+constexpr int CACHE_ATTN_TC_ROWS = 128;   // rows (token, head) of a tile: tensor-core and FFMA kernel
+constexpr int CACHE_ATTN_SIMT_ROWS = 32;
+int cache_attn_simt_blocks(bool is_bf16, int d, int num_sms);
+cudaError_t launch_cache_attn_simt(bool is_bf16, const CacheAttnArgs &a, int num_sms, cudaStream_t st);
+
 // Records a description of the last failure of this host thread (read back by
 // tpmlp_last_error()).
 void set_last_error(const char *fmt, ...);

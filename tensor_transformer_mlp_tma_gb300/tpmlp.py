@@ -24,6 +24,8 @@ ALGO_DEFAULT, ALGO_SIMT = 0, 1
 WS_STATUS, WS_PARTIALS, WS_DY, WS_Y, WS_DXN = 0, 1, 2, 3, 4
 FLAG_RECOMPUTE, FLAG_LAYERNORM = 1, 2
 ATTN_P_UPPER_ZERO = 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_PARTS = 0, 1, 2
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -68,6 +70,36 @@ class OrthoShape(ctypes.Structure):
                 ("c", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("context", ctypes.c_int64), ("rot", ctypes.c_int32),
+                ("scaling", ctypes.c_int32)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("t", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("amplitude", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("row", ctypes.c_int64), ("shard", ctypes.c_int64)]
+
+
+class KvCacheShape(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class CacheAttnShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("batch", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("tree_words", ctypes.c_int32), ("algo", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 class TpmlpError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -108,6 +140,13 @@ def _load():
         "tpmlp_xent_backward": (i32, [ctypes.POINTER(XentShape)] + [vp] * 9),
         "tpmlp_ortho_workspace_bytes": (sz, [ctypes.POINTER(OrthoShape)]),
         "tpmlp_orthogonalize": (i32, [ctypes.POINTER(OrthoShape)] + [vp] * 4),
+        "tpmlp_rope_turns": (i32, [ctypes.POINTER(Rope), vp]),
+        "tpmlp_qk_workspace_bytes": (sz, [vp]),
+        "tpmlp_qk_forward": (i32, [vp] * 10),
+        "tpmlp_qk_backward": (i32, [vp] * 15),
+        "tpmlp_kv_append": (i32, [vp] * 13),
+        "tpmlp_cache_attn_workspace_bytes": (sz, [vp, vp]),
+        "tpmlp_cache_attn": (i32, [vp] * 10),
         "tpmlp_check_device_status": (i32, [vp, vp]),
         "tpmlp_set_wait_limit_ns": (None, [u64]),
         "tpmlp_debug_timeout_probe": (i32, [vp, u64, vp]),
@@ -567,8 +606,295 @@ def orthogonalize(ctx: OrthoContext, G, O=None, stream=None):
     return O
 
 
+class RopeTable:
+    """The rotation of positions: the first `rot` components of a head in pairs (i, i + rot/2) ("half") or
+    (2i, 2i + 1) ("interleaved"), pair i by position * base^(-2i/rot).
+
+    scaling stretches it to contexts longer than the trained one: ("linear", factor), or
+    ("parts", factor, context, low, high): pairs that turn `high` times or more within the trained context
+    keep their angles, those that turn `low` times or less are divided by factor, the others in between.
+    amplitude multiplies the rotated components."""
+
+    def __init__(self, rot, base=10000.0, layout="half", scaling=None, amplitude=1.0, device=None):
+        kinds = {"linear": ROPE_SCALE_LINEAR, "parts": ROPE_SCALE_PARTS}
+        layouts = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
+        if layout not in layouts:
+            raise ValueError("layout %r: 'half' or 'interleaved'" % (layout,))
+        if scaling is not None and (scaling[0] not in kinds or len(scaling) != (2 if scaling[0] == "linear" else 5)):
+            raise ValueError("scaling %r: ('linear', factor) or ('parts', factor, context, low, high)" % (scaling,))
+        kind, factor, context, low, high = (tuple(scaling or (None,)) + (1.0, 1, 0.0, 1.0)[len(scaling or (None,)) - 1:])
+        rope = Rope(float(base), float(factor), float(low), float(high), int(context), int(rot),
+                    kinds.get(kind, ROPE_SCALE_NONE))
+        turns = (ctypes.c_uint64 * max(rope.rot // 2, 1))()
+        _check(lib.tpmlp_rope_turns(ctypes.byref(rope), turns), "tpmlp_rope_turns")
+        self.rot, self.layout, self.amplitude = rope.rot, layouts[layout], float(amplitude)
+        self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns], dtype=torch.int64,
+                                  device=device or "cuda")
+
+
+class QkContext:
+    """Norms of queries and keys per head and their rotation, for `tokens` tokens of the attention block's
+    projection: `heads` query heads and `kv_heads` key and value heads of `dim` components, the columns of QKV
+    shard-major in t shards [Q_1 | K_1 | V_1 | Q_2 | ...].  rope: a RopeTable, or None for the norm alone;
+    norm=False: the rotation alone.  eps is the norm's.
+
+    QKV is [tokens, (heads + 2 kv_heads) dim] (its rows may be apart), or a tuple (Q, K) or (Q, K, V) of
+    [tokens, heads, dim] tensors, shards' heads one after another.
+
+    One context serves one call at a time (see XentContext)."""
+
+    def __init__(self, tokens, heads, kv_heads, dim, dtype, rope=None, norm=True, eps=1e-6, t=1, device=None):
+        if dtype not in _DTYPES:
+            raise ValueError("dtype %s: float32 or bfloat16" % (dtype,))
+        self.shape = QkShape(int(tokens), int(heads), int(kv_heads), int(dim), int(t), _DTYPES[dtype],
+                             rope.layout if rope else ROPE_HALF, rope.rot if rope else 0, 1 if norm else 0, float(eps),
+                             rope.amplitude if rope else 1.0)
+        n = int(lib.tpmlp_qk_workspace_bytes(ctypes.byref(self.shape)))
+        if n == 0:
+            raise ValueError("invalid shape (tokens=%d heads=%d kv_heads=%d dim=%d rot=%d t=%d eps=%g)"
+                             % (tokens, heads, kv_heads, dim, self.shape.rot, t, eps))
+        self.dtype = dtype
+        self.rope = rope
+        self.workspace = _status_workspace(n, device)
+        if rope is not None and rope.turns.device != self.workspace.device:
+            raise ValueError("rope table on %s, the context's workspace on %s" % (rope.turns.device, self.workspace.device))
+        self._turns = rope.turns.data_ptr() if rope else None
+        self._saved = None
+        # the C ABI's records, filled in at every call
+        self._records = [Heads() for _ in range(6)]
+        self._refs = [ctypes.byref(r) for r in self._records]
+        self._shape_ref = ctypes.byref(self.shape)
+
+
+def _dense_heads(ctx, record, x, heads, name):
+    """A [tokens, heads, dim] tensor whose heads follow one another; its rows may be apart."""
+    s = ctx.shape
+    if not x.is_cuda or x.dtype is not ctx.dtype:
+        raise ValueError("%s must be a CUDA tensor of %s" % (name, ctx.dtype))
+    if tuple(x.shape) != (s.tokens, heads, s.dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), (s.tokens, heads, s.dim)))
+    if x.numel() and ((s.dim > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != s.dim)):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    if x.device != ctx.workspace.device:
+        raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
+    record.p, record.row, record.shard = x.data_ptr(), x.stride(0), heads // s.t * s.dim
+
+
+def _qkv_heads(ctx, records, x, name):
+    """Q, K and V inside a projection's array, into three records."""
+    s = ctx.shape
+    n, m = s.heads // s.t * s.dim, s.kv_heads // s.t * s.dim
+    width = s.t * (n + 2 * m)
+    if not x.is_cuda or x.dtype is not ctx.dtype:
+        raise ValueError("%s must be a CUDA tensor of %s" % (name, ctx.dtype))
+    if tuple(x.shape) != (s.tokens, width):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), (s.tokens, width)))
+    if x.numel() and x.stride(1) != 1:
+        raise ValueError("%s: a token's columns must be contiguous" % name)
+    if x.device != ctx.workspace.device:
+        raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
+    p, row, e = x.data_ptr(), x.stride(0), x.element_size()
+    for r, off in zip(records, (0, n, n + m)):
+        r.p, r.row, r.shard = p + off * e, row, n + 2 * m
+
+
+def _qkv_input(ctx, QKV, values):
+    s = ctx.shape
+    if isinstance(QKV, torch.Tensor):
+        _qkv_heads(ctx, ctx._records[:3], QKV, "QKV")
+        return
+    if len(QKV) < (3 if values else 2):
+        raise ValueError("Q, K%s expected" % (" and V" if values else ""))
+    for r, x, n, name in zip(ctx._records, QKV, (s.heads, s.kv_heads, s.kv_heads), ("Q", "K", "V")):
+        _dense_heads(ctx, r, x, n, name)
+
+
+def _qk_inputs(ctx, position, gain_q, gain_k):
+    s = ctx.shape
+    if s.rot:
+        _need(position, "position", torch.int64, (s.tokens,))
+        _same_device(ctx, position)
+    if s.norm:
+        _need(gain_q, "gain_q", ctx.dtype, (s.dim,))
+        _need(gain_k, "gain_k", ctx.dtype, (s.dim,))
+        _same_device(ctx, gain_q, gain_k)
+    return (gain_q.data_ptr() if s.norm else None, gain_k.data_ptr() if s.norm else None,
+            position.data_ptr() if s.rot else None, ctx._turns)
+
+
+def _qk_out(ctx, out, records, names):
+    """The output's records; without one, dense tensors."""
+    s = ctx.shape
+    if isinstance(out, torch.Tensor):
+        _qkv_heads(ctx, records, out, "out")
+        return out
+    if out is None:
+        dev = ctx.workspace.device
+        out = (torch.empty((s.tokens, s.heads, s.dim), dtype=ctx.dtype, device=dev),
+               torch.empty((s.tokens, s.kv_heads, s.dim), dtype=ctx.dtype, device=dev))
+    for r, x, n, name in zip(records, out, (s.heads, s.kv_heads), names):
+        _dense_heads(ctx, r, x, n, name)
+    return tuple(out)
+
+
+def qk_forward(ctx: QkContext, QKV, position, gain_q=None, gain_k=None, out=None, stream=None):
+    """(Qr, Kr) from QKV's queries and keys: normed (gains [dim]) and rotated by position [tokens] (int64).
+    out: a tuple of [tokens, heads, dim] tensors, or an array laid out as QKV whose Q and K columns are
+    written (QKV itself: in place) and which is then returned.  QKV, position and gains are kept, not
+    copied, for qk_backward: they have to hold the same values then."""
+    records = ctx._records
+    _qkv_input(ctx, QKV, False)
+    given = _qk_inputs(ctx, position, gain_q, gain_k)
+    spare = Heads()
+    result = _qk_out(ctx, out, (records[3], records[4], spare), ("Qr", "Kr"))
+    r = ctx._refs
+    _call(ctx, lib.tpmlp_qk_forward, "tpmlp_qk_forward", (ctx._shape_ref, r[0], r[1], *given, r[3], r[4]), stream)
+    kept = not (ctx.shape.norm and ctx.shape.tokens) or (records[0].p != records[3].p and records[1].p != records[4].p)
+    ctx._saved = (QKV if kept else None, position, gain_q, gain_k)
+    return result
+
+
+def qk_backward(ctx: QkContext, dQr, dKr, out=None, dgain_q=None, dgain_k=None, stream=None):
+    """{"dQ", "dK", "dgain_q", "dgain_k"} from the gradients of what the last qk_forward of this context returned
+    ([tokens, heads, dim] each).  out: as for qk_forward (an array laid out as QKV is returned as "dQKV"); it may be
+    what holds dQr and dKr.  The gains' entries are None without the norm."""
+    if ctx._saved is None:
+        raise ValueError("qk_backward needs a qk_forward of the same context before it")
+    QKV, position, gain_q, gain_k = ctx._saved
+    if QKV is None:
+        raise ValueError("qk_backward after a qk_forward with the norm in place: its inputs are gone")
+    s = ctx.shape
+    records, r = ctx._records, ctx._refs
+    _qkv_input(ctx, QKV, False)
+    given = _qk_inputs(ctx, position, gain_q, gain_k)
+    grads = (Heads(), Heads())
+    _dense_heads(ctx, grads[0], dQr, s.heads, "dQr")
+    _dense_heads(ctx, grads[1], dKr, s.kv_heads, "dKr")
+    spare = Heads()
+    result = _qk_out(ctx, out, (records[3], records[4], spare), ("dQ", "dK"))
+    if s.norm:
+        if dgain_q is None:
+            dgain_q = torch.empty((s.dim,), dtype=ctx.dtype, device=dQr.device)
+        if dgain_k is None:
+            dgain_k = torch.empty((s.dim,), dtype=ctx.dtype, device=dQr.device)
+        _need(dgain_q, "dgain_q", ctx.dtype, (s.dim,))
+        _need(dgain_k, "dgain_k", ctx.dtype, (s.dim,))
+        _same_device(ctx, dgain_q, dgain_k)
+    else:
+        dgain_q = dgain_k = None
+    _call(ctx, lib.tpmlp_qk_backward, "tpmlp_qk_backward",
+          (ctx._shape_ref, r[0], r[1], *given, ctypes.byref(grads[0]), ctypes.byref(grads[1]), r[3], r[4],
+           _ptr(dgain_q), _ptr(dgain_k), ctx.workspace.data_ptr()), stream)
+    grads = {"dgain_q": dgain_q, "dgain_k": dgain_k}
+    if isinstance(result, torch.Tensor):
+        grads["dQKV"] = result
+    else:
+        grads["dQ"], grads["dK"] = result
+    return grads
+
+
+class KvCache:
+    """Keys and values of many sequences in pages of page_size tokens: K and V [pages, kv_heads, page_size, dim].
+    KvCache.of(K, V) takes existing tensors of that shape, of any strides that keep a row's components together
+    (a [pages, page_size, kv_heads, dim] cache is K.transpose(1, 2))."""
+
+    def __init__(self, pages, page_size, kv_heads, dim, dtype, device=None):
+        shape = (int(pages), int(kv_heads), int(page_size), int(dim))
+        self._set(*(torch.zeros(shape, dtype=dtype, device=device or "cuda") for _ in "kv"))
+
+    @classmethod
+    def of(cls, K, V):
+        self = cls.__new__(cls)
+        self._set(K, V)
+        return self
+
+    def _set(self, K, V):
+        if K.dtype not in _DTYPES or V.dtype is not K.dtype:
+            raise ValueError("K %s and V %s: float32 or bfloat16, the same" % (K.dtype, V.dtype))
+        if not (K.is_cuda and V.device == K.device) or K.dim() != 4 or V.shape != K.shape:
+            raise ValueError("K and V must be CUDA tensors [pages, kv_heads, page_size, dim] of one device")
+        if V.stride() != K.stride() or K.stride(3) != 1:
+            raise ValueError("K and V must have the same strides, and a row's components follow one another")
+        self.K, self.V, self.dtype = K, V, K.dtype
+        pages, kv_heads, page_size, dim = K.shape
+        self.shape = KvCacheShape(K.data_ptr(), V.data_ptr(), pages, page_size, K.stride(0), K.stride(1), K.stride(2),
+                                  kv_heads, dim, _DTYPES[K.dtype])
+        self._ref = ctypes.byref(self.shape)
+
+
+def kv_append(ctx: QkContext, cache: KvCache, QKV, position, slot, gain_q=None, gain_k=None, out=None, stream=None):
+    """Puts the tokens' keys (normed, rotated) and values at slot [tokens] (int64: page * page_size + row; negative: not
+    kept) of the cache, and returns their queries, normed and rotated, [tokens, heads, dim] (`out`, where given)."""
+    s = ctx.shape
+    records, r = ctx._records, ctx._refs
+    _qkv_input(ctx, QKV, True)
+    given = _qk_inputs(ctx, position, gain_q, gain_k)
+    _need(slot, "slot", torch.int64, (s.tokens,))
+    _same_device(ctx, slot, cache.K)
+    if out is None:
+        out = torch.empty((s.tokens, s.heads, s.dim), dtype=ctx.dtype, device=slot.device)
+    _dense_heads(ctx, records[3], out, s.heads, "out")
+    _call(ctx, lib.tpmlp_kv_append, "tpmlp_kv_append",
+          (ctx._shape_ref, cache._ref, r[0], r[1], r[2], *given, slot.data_ptr(), r[3], ctx.workspace.data_ptr()), stream)
+    return out
+
+
+class CacheAttnContext:
+    """Workspace of attention over a paged cache: `tokens` new tokens of `batch` sequences, `heads` query heads over the
+    cache's kv_heads.  scale: of the scores, 1/sqrt(dim) where it is None.  The number of pages per sequence and
+    of a tree's words may differ from call to call.
+
+    One context serves one call at a time (see XentContext)."""
+
+    def __init__(self, tokens, batch, heads, kv_heads, dim, dtype, scale=None, algo=ALGO_DEFAULT, device=None):
+        if dtype not in _DTYPES:
+            raise ValueError("dtype %s: float32 or bfloat16" % (dtype,))
+        self.shape = CacheAttnShape(int(tokens), int(batch), 0, int(heads), 0, int(algo),
+                                    float(dim) ** -0.5 if scale is None else float(scale))
+        sizes = KvCacheShape(None, None, 1, 1, int(dim) * int(kv_heads), int(dim), int(dim) * int(kv_heads), int(kv_heads),
+                             int(dim), _DTYPES[dtype])
+        n = int(lib.tpmlp_cache_attn_workspace_bytes(ctypes.byref(self.shape), ctypes.byref(sizes)))
+        if n == 0:
+            raise ValueError("invalid shape (tokens=%d batch=%d heads=%d kv_heads=%d dim=%d scale=%g)"
+                             % (tokens, batch, heads, kv_heads, dim, self.shape.scale))
+        self.dtype, self.kv_heads, self.dim = dtype, int(kv_heads), int(dim)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        self.workspace[:4096].zero_()
+        self._ref = ctypes.byref(self.shape)
+
+
+def cache_attention(ctx: CacheAttnContext, cache: KvCache, Q, q_start, kv_len, page_table, tree=None, O=None, stream=None):
+    """O [tokens, heads, dim]: attention of Q over the cache, which holds the new tokens' keys already.  Sequence b has
+    tokens q_start[b] .. q_start[b+1] - 1 and kv_len[b] keys in the pages page_table[b] (all int32); its new tokens are the
+    last of those keys, and each sees the keys before them, and of the new ones those up to itself, or with tree
+    [tokens, words] (int64) those whose bit is set."""
+    s = ctx.shape
+    if cache.dtype is not ctx.dtype or cache.shape.kv_heads != ctx.kv_heads or cache.shape.dim != ctx.dim:
+        raise ValueError("the cache has %s, %d heads of %d; the context %s, %d of %d"
+                         % (cache.dtype, cache.shape.kv_heads, cache.shape.dim, ctx.dtype, ctx.kv_heads, ctx.dim))
+    _need(Q, "Q", ctx.dtype, (s.tokens, s.heads, ctx.dim))
+    _need(q_start, "q_start", torch.int32, (s.batch + 1,))
+    _need(kv_len, "kv_len", torch.int32, (s.batch,))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, pages]")
+    _need(page_table, "page_table", torch.int32, (s.batch, page_table.shape[1]))
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[1] == 0:
+            raise ValueError("tree must be [tokens, words] with a word at least")
+        _need(tree, "tree", torch.int64, (s.tokens, tree.shape[1]))
+    if O is None:
+        O = torch.empty_like(Q)
+    _need(O, "O", ctx.dtype, (s.tokens, s.heads, ctx.dim))
+    _same_device(ctx, Q, q_start, kv_len, page_table, tree, O, cache.K)
+    s.max_pages, s.tree_words = page_table.shape[1], 0 if tree is None else tree.shape[1]
+    _call(ctx, lib.tpmlp_cache_attn, "tpmlp_cache_attn",
+          (ctx._ref, cache._ref, Q.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+           None if tree is None else tree.data_ptr(), O.data_ptr(), ctx.workspace.data_ptr()), stream)
+    return O
+
+
 def check_device_status(ctx_or_ws, stream=None) -> int:
-    known = (Context, AttnContext, XentContext, OrthoContext)
+    known = (Context, AttnContext, XentContext, OrthoContext, QkContext, CacheAttnContext)
     ws = ctx_or_ws.workspace if isinstance(ctx_or_ws, known) else ctx_or_ws
     return int(lib.tpmlp_check_device_status(_ptr(ws), _stream(stream)))
 
