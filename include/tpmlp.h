@@ -528,7 +528,8 @@ size_t tpmlp_cache_attn_workspace_bytes(const tpmlp_cache_attn_shape *shape, con
  * are looked up.  Reported as TPMLP_ERR_INVALID_ARG in the status word (detail: the sequence) are a kv_len that is below n or does
  * not fit the table (the sequence's rows are zero), a q_start that decreases or leaves [0, T] (the sequence has no
  * tokens) and a page that is not in the cache (its keys and values count as zeros).
- * Both types run on FFMA kernels.
+ * bf16 runs on the tensor cores (fp32 scores and sums, weights rounded to bf16) where page_size and dim are
+ * multiples of 8 and the cache's bases and strides are on 16 bytes, else, as fp32 and TPMLP_ALGO_SIMT, on FFMA kernels.
  * Calls with the same lengths and inputs give the same bits on the same number of SMs.
  * Errors: INVALID_ARG for a bad shape, a NULL pointer or an O that overlaps an input; UNSUPPORTED for dim not a multiple of 8
  * or above 256, and for Q or O not on 16 bytes; CUDA when a launch fails. */

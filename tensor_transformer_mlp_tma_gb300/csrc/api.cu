@@ -2245,7 +2245,9 @@ tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *s, const tpmlp_kv_ca
     sms = std::min(sms, kCacheAttnBlocks);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Timed timed("cache_attn", st);
-    const cudaError_t r = tpmlp::launch_cache_attn_simt(c->dtype == TPMLP_BF16, a, sms, st);
+    const bool tc = c->dtype == TPMLP_BF16 && s->algo == TPMLP_ALGO_DEFAULT && tpmlp::cache_attn_tc(a);
+    const cudaError_t r = tc ? tpmlp::launch_cache_attn_tc(a, sms, st)
+                             : tpmlp::launch_cache_attn_simt(c->dtype == TPMLP_BF16, a, sms, st);
     if (r == cudaSuccess) g_launches.fetch_add(1);
     return from_cuda(r);
 }

@@ -360,6 +360,9 @@ constexpr int CACHE_ATTN_TC_ROWS = 128;   // rows (token, head) of a tile: tenso
 constexpr int CACHE_ATTN_SIMT_ROWS = 32;
 int cache_attn_simt_blocks(bool is_bf16, int d, int num_sms);
 cudaError_t launch_cache_attn_simt(bool is_bf16, const CacheAttnArgs &a, int num_sms, cudaStream_t st);
+// bf16 on the tensor cores; cache_attn_tc says whether the cache's layout allows it.
+bool cache_attn_tc(const CacheAttnArgs &a);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs &a, int num_sms, cudaStream_t st);
 
 // Records a description of the last failure of this host thread (read back by
 // tpmlp_last_error()).

@@ -44,6 +44,7 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "tensormap.h"
 
 namespace tpmlp {
 namespace tc {
@@ -2428,6 +2429,8 @@ static cudaError_t launch_cg(const GemmArgs &g, int num_sms, cudaStream_t st) {
 }
 
 }  // namespace tc
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return tc::encode_fn(); }
 
 bool tc_wide_tile(Epi epi, const GemmArgs &g) {
     if (!g.cta_pair || g.heads_layout || g.nshards != 1 || g.causal_k != 0 || g.skip_upper) return false;
