@@ -2231,7 +2231,10 @@ tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *s, const tpmlp_kv_ca
     a.heads = s->heads, a.kv_heads = c->kv_heads, a.group = s->heads / c->kv_heads, a.d = c->dim;
     a.q = Q, a.o = O, a.q_start = q_start, a.kv_len = kv_len, a.table = page_table;
     a.tree = tree, a.tree_words = s->tree_words;
+    // (a scale of 0 is replaced by the least normal number: what a row does not see is an infinity that it
+    // multiplies)
     a.scale_log2 = static_cast<float>(static_cast<double>(s->scale) * 1.4426950408889634);
+    if (std::fabs(a.scale_log2) < 1.1754944e-38f) a.scale_log2 = 1.1754944e-38f;
     a.k = c->K, a.v = c->V;
     a.pages = c->pages, a.page_size = c->page_size;
     a.page_stride = c->page_stride, a.head_stride = c->head_stride, a.token_stride = c->token_stride;

@@ -66,25 +66,32 @@ __device__ __forceinline__ int page_of(const CacheAttnArgs &a, int64_t b, int64_
     return -1;
 }
 
+// Tokens that rows 0 .. rows - 1 reach into: rows / group, rounded up.
+__device__ __forceinline__ int tokens_of(const CacheAttnArgs &a, int rows) { return (rows + a.group - 1) / a.group; }
+
 template <int ROWS, int KEYS>
 struct Tiles {
     static __device__ __forceinline__ int row_tiles(const CacheAttnArgs &a, const Seq &s) {
         return (s.n * a.group + ROWS - 1) / ROWS;
     }
-    // Tiles of one unit, one at least: rows that see nothing are written too.
-    static __device__ __forceinline__ int of(const CacheAttnArgs &a, const Seq &s, int rt) {
-        int keys = s.len;
-        if (!a.tree && s.len > 0) {
-            const int rows = min(s.n * a.group, (rt + 1) * ROWS);
-            keys = s.prefix + (rows - 1) / a.group + 1;
-        }
+    // Tiles of the keys that the first `tokens` new tokens see, one at least: rows that see nothing are
+    // written too.
+    static __device__ __forceinline__ int to(const CacheAttnArgs &a, const Seq &s, int tokens) {
+        const int keys = a.tree || s.len == 0 ? s.len : s.prefix + tokens;
         return max(1, (keys + KEYS - 1) / KEYS);
+    }
+    static __device__ __forceinline__ int of(const CacheAttnArgs &a, const Seq &s, int rt) {
+        return to(a, s, min(s.n, tokens_of(a, (rt + 1) * ROWS)));
     }
     static __device__ __forceinline__ int64_t per_head(const CacheAttnArgs &a, const Seq &s) {
         const int n = row_tiles(a, s);
-        if (a.tree || s.len == 0) return static_cast<int64_t>(n) * (n > 0 ? of(a, s, 0) : 0);
-        int64_t sum = 0;
-        for (int rt = 0; rt < n; ++rt) sum += of(a, s, rt);
+        if (n == 0) return 0;
+        const int last = to(a, s, s.n);
+        if (a.tree || s.len == 0) return static_cast<int64_t>(n) * last;
+        int64_t sum = last;
+        const bool even = ROWS % a.group == 0;  // a tile's rows are whole tokens
+        const int step = ROWS / a.group;
+        for (int rt = 0; rt < n - 1; ++rt) sum += even ? to(a, s, (rt + 1) * step) : of(a, s, rt);
         return sum;
     }
 };
@@ -96,7 +103,12 @@ struct Unit {
     int tile0, tiles;     // this block's tiles of the unit
     bool cut;             // the unit has tiles in other blocks
     int place;            // of this block's piece
-    int first, last;      // blocks that hold pieces
+    int64_t begin, end;   // the unit's tiles, counted among all
+};
+
+// Blocks that hold a cut unit's pieces.
+struct Pieces {
+    int first, last;
 };
 
 // A block's share of the work.
@@ -110,20 +122,17 @@ struct Walk {
 
     struct Shared {
         int64_t warp_sum[8];
-        int64_t start_off;
-        int start_b;
+        int b, head, rt, tile, count;
     };
 
     // All threads (at least 256) of the block.
     __device__ void begin(const CacheAttnArgs &a, Shared &sh) {
         const int tid = threadIdx.x, lane = tid & 31;
         const int per = static_cast<int>((a.batch + 255) / 256);
+        const int s0 = tid * per, s1 = static_cast<int>(min(static_cast<int64_t>(s0) + per, a.batch));
         int64_t mine = 0;
         if (tid < 256)
-            for (int i = 0; i < per; ++i) {
-                const int64_t s = static_cast<int64_t>(tid) * per + i;
-                if (s < a.batch) mine += a.kv_heads * T::per_head(a, sequence(a, s, blockIdx.x == 0));
-            }
+            for (int i = s0; i < s1; ++i) mine += a.kv_heads * T::per_head(a, sequence(a, i, blockIdx.x == 0));
         int64_t scan = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -134,6 +143,7 @@ struct Walk {
         __syncthreads();
         int64_t before = 0;
         total = 0;
+#pragma unroll
         for (int w = 0; w < 8; ++w) {
             if (w < (tid >> 5)) before += sh.warp_sum[w];
             total += sh.warp_sum[w];
@@ -143,29 +153,26 @@ struct Walk {
         pos = end = 0;
         if (c < blocks) pos = c * total / blocks, end = (c + 1) * total / blocks;
         int64_t at = before + scan - mine;
-        if (tid < 256 && c < blocks && at <= pos && pos < at + mine) {
-            for (int i = 0; i < per; ++i) {
-                const int64_t s = static_cast<int64_t>(tid) * per + i;
-                const int64_t cost = s < a.batch ? a.kv_heads * T::per_head(a, sequence(a, s, false)) : 0;
+        if (tid < 256 && at <= pos && pos < at + mine && pos < end) {
+            // the sequence, key head, rows and tile at pos
+            for (int i = s0; i < s1; ++i) {
+                const Seq s = sequence(a, i, false);
+                const int64_t ph = T::per_head(a, s), cost = a.kv_heads * ph;
                 if (pos < at + cost) {
-                    sh.start_b = static_cast<int>(s);
-                    sh.start_off = pos - at;
+                    int64_t off = pos - at;
+                    sh.b = i;
+                    sh.head = static_cast<int>(off / ph);
+                    off -= sh.head * ph;
+                    int r = 0, n;
+                    while (off >= (n = T::of(a, s, r))) off -= n, ++r;
+                    sh.rt = r, sh.count = n, sh.tile = static_cast<int>(off);
                     break;
                 }
                 at += cost;
             }
         }
         __syncthreads();
-        if (pos >= end) return;
-        b = sh.start_b;
-        const Seq s = sequence(a, b, false);
-        int64_t off = sh.start_off;
-        const int64_t ph = T::per_head(a, s);
-        head = static_cast<int>(off / ph);
-        off -= head * ph;
-        rt = 0;
-        while (off >= (count = T::of(a, s, rt))) off -= count, ++rt;
-        tile = static_cast<int>(off);
+        b = sh.b, head = sh.head, rt = sh.rt, tile = sh.tile, count = sh.count;
     }
 
     __device__ __forceinline__ bool next(const CacheAttnArgs &a, Unit &u) {
@@ -175,15 +182,9 @@ struct Walk {
         u.rows = min(ROWS, u.s.n * a.group - u.row0);
         u.tile0 = tile;
         u.tiles = static_cast<int>(min(static_cast<int64_t>(count - tile), end - pos));
-        const int64_t g0 = pos - tile;
+        u.begin = pos - tile, u.end = u.begin + count;
         u.cut = u.tiles != count;
         u.place = tile == 0 ? 1 : 0;
-        u.first = u.last = blockIdx.x;
-        if (u.cut) {
-            // the block c with c total / blocks <= g < (c + 1) total / blocks, whole numbers
-            u.first = static_cast<int>(((g0 + 1) * blocks - 1) / total);
-            u.last = static_cast<int>(((g0 + count) * blocks - 1) / total);
-        }
         pos += u.tiles;
         if (pos < end) {  // the next unit
             tile = 0;
@@ -199,6 +200,12 @@ struct Walk {
             count = T::of(a, s, rt);
         }
         return true;
+    }
+
+    // The block c with c total / blocks <= g < (c + 1) total / blocks (whole numbers), of the first and
+    // the last tile.
+    __device__ Pieces pieces(const Unit &u) const {
+        return {static_cast<int>(((u.begin + 1) * blocks - 1) / total), static_cast<int>((u.end * blocks - 1) / total)};
     }
 };
 
@@ -223,15 +230,15 @@ __device__ __forceinline__ E *out_row(const CacheAttnArgs &a, const Unit &u, int
 
 // Joins a cut unit's pieces; `threads` threads, `tid` of them.
 template <typename E, int ROWS>
-__device__ __forceinline__ void join(const CacheAttnArgs &a, const Unit &u, int tid, int threads) {
+__device__ __forceinline__ void join(const CacheAttnArgs &a, const Unit &u, const Pieces &in, int tid, int threads) {
     const int quads = a.d / 4;
     for (int i = tid; i < u.rows * quads; i += threads) {
         const int row = i / quads, e = (i - row * quads) * 4;
         float m = -INFINITY, l = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int c = u.first; c <= u.last; ++c) {
-            const int64_t at = (2 * static_cast<int64_t>(c) + (c == u.first ? 1 : 0)) * ROWS + row;
+        for (int c = in.first; c <= in.last; ++c) {
+            const int64_t at = (2 * static_cast<int64_t>(c) + (c == in.first ? 1 : 0)) * ROWS + row;
             const float2 ml = __ldcg(a.part_ml + at);
             const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part + at * a.d + e));
             const float top = fmaxf(m, ml.x), f = scale_of(m, top), g = scale_of(ml.x, top);

@@ -222,14 +222,14 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
             if (tid < u.rows) __stcg(a.part_ml + piece + tid, make_float2(m_sh[tid], l_sh[tid]));
             __threadfence();
             __syncthreads();
+            const Pieces in = walk.pieces(u);
             if (tid == 0) {
-                const uint32_t pieces = static_cast<uint32_t>(u.last - u.first + 1);
-                last_sh = atomicAdd(a.counters + u.first, 1u) == pieces - 1;
-                if (last_sh) a.counters[u.first] = 0u;
+                last_sh = atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first);
+                if (last_sh) a.counters[in.first] = 0u;
                 __threadfence();
             }
             __syncthreads();
-            if (last_sh) join<E, SR>(a, u, tid, STHREADS);
+            if (last_sh) join<E, SR>(a, u, in, tid, STHREADS);
         }
     }
 }

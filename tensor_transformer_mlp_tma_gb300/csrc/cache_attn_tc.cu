@@ -40,14 +40,17 @@ namespace cattn {
 constexpr int TR = CACHE_ATTN_TC_ROWS;  // rows per tile of a unit
 constexpr int KEYS = 128;
 constexpr int COLS = 64;                // rows per stream
-// Two streams of a warpgroup each, and one whose first warp copies and second issues the products.
+// Two streams of a warpgroup each, and one whose warps copy K, issue the products and copy V.
 constexpr int TTHREADS = 384;
 // Registers per thread: a stream's hold 64 scores and 64 sums.  Launched with 168 (three warpgroups in
-// 65536), 224 + 224 + 56 = 3 x 168.
-constexpr int STREAM_REGISTERS = 224, OTHER_REGISTERS = 56;
+// 65536), 208 + 208 + 88 = 3 x 168.
+constexpr int STREAM_REGISTERS = 208, OTHER_REGISTERS = 88;
 constexpr uint32_t BLOCK_BYTES = KEYS * 128;    // 128 keys of 64 components
 constexpr uint32_t Q_BLOCK_BYTES = COLS * 128;  // 64 rows of 64 components
 constexpr uint32_t P_BYTES = KEYS * 128;
+// What else a stream's weights' space holds while no product reads it: per warp and row a maximum or a
+// sum; per row the factor of the outputs, that of the other stream's, and the output's row.
+constexpr uint32_t P_WARPS = 0, P_FACTOR = 1024, P_OTHER = 1280, P_ROW = 1536;
 constexpr float RENEW = 8.0f;           // log2 above the reference
 constexpr uint32_t STATUS_TIMEOUT = 4;  // TPMLP_ERR_TIMEOUT
 constexpr uint32_t SMALL_BYTES = 1536;
@@ -69,8 +72,8 @@ struct Shape {
 struct Small {
     uint64_t full[10], empty[10];
     uint64_t s_full[2], p_full[2], o_done[2], q_full[2], drain;
-    alignas(16) float m[2][COLS];  // references (log2), read four at a time
-    uint32_t top[2][COLS]; // the tile's maxima, ordered as integers; then the factors
+    float m[2][COLS];      // references (log2)
+    alignas(16) float ref[2][COLS];  // the same, 0 for a row that has seen nothing yet
     uint8_t token[2][COLS]; // of a row, counted from the first row's token
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
@@ -78,15 +81,8 @@ struct Small {
     int last;
     volatile int abort;
 };
-static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, m) % 16 == 0, "small arrays");
+static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
 static_assert(Shape<1, 1>::SLOTS == 10 && Shape<1, 2>::SLOTS == 5 && Shape<2, 2>::SLOTS == 4, "ring");
-
-// Order of floats as unsigned integers (all above 0).
-__device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t b = __float_as_uint(x);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o); }
 
 // Ring position of a unit's i-th K or V tile: K0 K1 V0 K2 V1 ... V(n-1), NB slots each.
 template <int NB>
@@ -109,6 +105,10 @@ struct Block {
     __device__ uint32_t full(int pos) const { return ptx::smem_u32(&sh->full[pos % S::SLOTS]); }
     __device__ uint32_t empty(int pos) const { return ptx::smem_u32(&sh->empty[pos % S::SLOTS]); }
     __device__ bool wait(uint32_t bar, uint32_t parity) const {
+        // the clock is looked at only after many tries
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
         if (ptx::mbar_wait(bar, parity, a.wait_ns, &sh->abort)) return true;
         sh->abort = 1;
         return false;
@@ -125,174 +125,183 @@ __device__ __forceinline__ int wrap(int pos) {
     return pos % (2 * SLOTS * 4096);
 }
 
-// ---- copies: one warp --------------------------------------------------------------------------
+// ---- copies: one warp for K, one for V -----------------------------------------------------------
 template <int NB, int BLK>
-__device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, const CUtensorMap *mk, const CUtensorMap *mv,
-                          int box) {
+__device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool values, const CUtensorMap *map, int box) {
     using S = Shape<NB, BLK>;
     const CacheAttnArgs &a = B.a;
     const int lane = threadIdx.x & 31;
     const int pieces = KEYS / box;
     const unsigned page_size = static_cast<unsigned>(a.page_size);
-    int pos = 0;
-    int64_t issued = 0;
+    const bool leader = ptx::elect_one();
+    int base = 0;
+    uint32_t copied = 0, phases = 0;  // per slot: this warp has copied to it, and in which phase last
     bool ok = true;
     Unit u = {};
-    // the page and row of this lane's piece of a tile; page -1: no keys there
+    // The page (as the table has it) and row of this lane's piece of a tile; row -1: no keys there.
     struct Piece {
         int page, row;
     };
     auto look = [&](int tile) {
-        Piece x = {-1, 0};
+        Piece x = {0, -1};
         const int key = tile * KEYS + lane * box;
         if (lane < pieces && key < u.s.len) {
             const unsigned at = static_cast<unsigned>(key) / page_size;
-            const int page = page_of(a, u.b, at);
-            x.page = page < 0 ? static_cast<int>(a.pages) : page;  // past the last page: zeros
+            x.page = a.table[u.b * a.max_pages + at];
             x.row = key - static_cast<int>(at * page_size);
         }
         return x;
     };
-    auto issue = [&](const CUtensorMap *map, const Piece &x) {
-        const int valid = __popc(__ballot_sync(0xffffffffu, x.page >= 0));
-        for (int nb = 0; nb < NB; ++nb) {
-            ok = __shfl_sync(0xffffffffu, lane == 0 ? B.wait_empty(pos) : true, 0) && ok;
-            if (!ok) return;
-            const int blocks = B.blocks(nb);
-            const uint32_t bar = B.full(pos), dst = B.slot(pos) + static_cast<uint32_t>(lane * box) * 128u;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
-            __syncwarp();
-            if (x.page >= 0)
-                for (int k = 0; k < blocks; ++k)
-                    ptx::tma_load_4d(dst + static_cast<uint32_t>(k) * BLOCK_BYTES, map, bar, nb * 128 + k * 64, x.row, u.head, x.page);
-            pos = wrap<S::SLOTS>(pos + 1);
-            ++issued;
-        }
-    };
     while (ok && walk.next(a, u)) {
-        Piece here = look(u.tile0), next = {-1, 0};
-        if (u.tiles > 1) next = look(u.tile0 + 1);
-        issue(mk, here);
+        Piece next = look(u.tile0);
         for (int i = 0; ok && i < u.tiles; ++i) {
-            Piece after = {-1, 0};
-            if (i + 2 < u.tiles) after = look(u.tile0 + i + 2);
-            if (i + 1 < u.tiles) issue(mk, next);
-            if (ok) issue(mv, here);
-            here = next, next = after;
+            Piece x = next;
+            if (i + 1 < u.tiles) next = look(u.tile0 + i + 1);
+            if (x.row >= 0 && (x.page < 0 || x.page >= a.pages)) {
+                report(a, STATUS_INVALID, static_cast<uint32_t>(u.b));
+                x.page = static_cast<int>(a.pages);  // past the last page: zeros
+            }
+            const int valid = __popc(__ballot_sync(0xffffffffu, x.row >= 0));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int pos = wrap<S::SLOTS>(base + (values ? v_pos<NB>(i, u.tiles) : k_pos<NB>(i)) + nb);
+                ok = __all_sync(0xffffffffu, ok && B.wait_empty(pos));
+                if (!ok) break;
+                const int blocks = B.blocks(nb);
+                const uint32_t bar = B.full(pos), dst = B.slot(pos);
+                if (leader) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
+                for (int p = 0; p < valid; ++p) {
+                    const int page = __shfl_sync(0xffffffffu, x.page, p), row = __shfl_sync(0xffffffffu, x.row, p);
+                    if (leader) {
+                        const uint32_t to = dst + static_cast<uint32_t>(p * box) * 128u;
+                        ptx::tma_load_4d(to, map, bar, nb * 128, row, u.head, page);
+                        if (BLK > 1 && blocks > 1) ptx::tma_load_4d(to + BLOCK_BYTES, map, bar, nb * 128 + 64, row, u.head, page);
+                    }
+                }
+                const uint32_t bit = 1u << (pos % S::SLOTS);
+                copied |= bit;
+                phases = (pos / S::SLOTS) & 1 ? phases | bit : phases & ~bit;
+            }
         }
+        base = wrap<S::SLOTS>(base + 2 * u.tiles * NB);
     }
     if (!ok) {
         if (lane == 0) report(a, STATUS_TIMEOUT, 1);
         // copies in flight land before anything goes on
-        const int back = static_cast<int>(issued < S::SLOTS ? issued : S::SLOTS);
-        for (int i = 1; i <= back; ++i) {
-            const int at = pos - i < 0 ? pos - i + 2 * S::SLOTS * 4096 : pos - i;
-            ptx::mbar_wait(B.full(at), static_cast<uint32_t>(at / S::SLOTS) & 1u, a.wait_ns, nullptr);
-        }
+        for (int i = 0; i < S::SLOTS; ++i)
+            if (copied >> i & 1u) ptx::mbar_wait(ptx::smem_u32(&B.sh->full[i]), phases >> i & 1u, a.wait_ns, nullptr);
     }
 }
 
-// ---- products: one thread ----------------------------------------------------------------------
+// ---- products: one warp --------------------------------------------------------------------------
 template <int NB, int BLK>
 __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint32_t tmem) {
     using S = Shape<NB, BLK>;
     const CacheAttnArgs &a = B.a;
     Small *sh = B.sh;
     const int steps = (a.d + 15) / 16;
+    const bool leader = ptx::elect_one();
     int base = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true;
     Unit u;
     auto bar = [&](uint64_t &x) { return ptx::smem_u32(&x); };
+    // all lanes wait, one issues
+    auto wait = [&](uint32_t b, uint32_t phase) { ok = __all_sync(0xffffffffu, ok && B.wait(b, phase)); };
     while (ok && walk.next(a, u)) {
         const int n = u.tiles;
         const bool both = u.rows > COLS;  // both streams take every tile
-        int width[2];
-        width[0] = both ? COLS : (u.rows + 15) & ~15;
-        width[1] = both ? (u.rows - COLS + 15) & ~15 : width[0];
-        auto scores = [&](int s, int i, bool first) {
+        const int width0 = both ? COLS : (u.rows + 15) & ~15, width1 = both ? (u.rows - COLS + 15) & ~15 : width0;
+        auto release = [&](int pos) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(B.empty(wrap<S::SLOTS>(base + pos + nb)));
+        };
+        auto arrived = [&](int pos) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int at = wrap<S::SLOTS>(base + pos + nb);
+                wait(B.full(at), static_cast<uint32_t>(at / S::SLOTS) & 1u);
+            }
+        };
+        // Descriptors count 16 bytes: 16 components on are 2, 64 a block; 16 keys on are 128.
+        auto scores = [&](int s, int i, bool first, bool free) {
             if (first) {
-                ok = ok && B.wait(bar(sh->q_full[s]), q_phase[s]);
+                wait(bar(sh->q_full[s]), q_phase[s]);
                 q_phase[s] ^= 1u;
             }
             if (!ok) return;
             ptx::tc_fence_after();
-            const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, width[s], false, false);
-            const uint32_t d = tmem + static_cast<uint32_t>(s * COLS), q = B.q + static_cast<uint32_t>(s) * S::Q_BYTES;
+            const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, s ? width1 : width0, false, false);
+            const uint32_t d = tmem + static_cast<uint32_t>(s * COLS);
+            const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * S::Q_BYTES, 16, 1024);
+#pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t tile = B.slot(wrap<S::SLOTS>(base + k_pos<NB>(i) + nb));
-                for (int k = 0; k < 8 && nb * 8 + k < steps; ++k) {
-                    const uint32_t ka = tile + static_cast<uint32_t>(k >> 2) * BLOCK_BYTES + (k & 3) * 32;
-                    const uint32_t qa = q + static_cast<uint32_t>(nb * 2 + (k >> 2)) * Q_BLOCK_BYTES + (k & 3) * 32;
-                    ptx::umma_f16_ss(d, ptx::sdesc_sw128(ka, 16, 1024), ptx::sdesc_sw128(qa, 16, 1024), idesc, nb + k > 0);
+                const uint64_t k0 = ptx::sdesc_sw128(B.slot(wrap<S::SLOTS>(base + k_pos<NB>(i) + nb)), 16, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 4 * BLK; ++k)
+                        if (nb * 8 + k < steps)
+                            ptx::umma_f16_ss(d, k0 + static_cast<uint64_t>((k >> 2) * (BLOCK_BYTES >> 4) + (k & 3) * 2),
+                                             q + static_cast<uint64_t>((nb * 2 + (k >> 2)) * (Q_BLOCK_BYTES >> 4) + (k & 3) * 2),
+                                             idesc, nb + k > 0);
                 }
+            }
+            if (leader) {
+                ptx::umma_commit(bar(sh->s_full[s]));
+                if (free) release(k_pos<NB>(i));
             }
         };
         // the stream's weights of a tile are formed, and its scores have been read
         auto weights = [&](int s) {
-            ok = ok && B.wait(bar(sh->p_full[s]), p_phase[s]);
+            wait(bar(sh->p_full[s]), p_phase[s]);
             p_phase[s] ^= 1u;
         };
-        auto outputs = [&](int s, int i, bool first) {
-            if (!ok || sh->skip[s]) return;
+        auto outputs = [&](int s, int i, bool first, bool free) {
+            if (!ok) return;
             ptx::tc_fence_after();
-            const uint32_t idesc = ptx::idesc_bf16_f32(128, width[s], true, true);
-            for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t d = tmem + static_cast<uint32_t>(2 * COLS + (s * NB + nb) * COLS);
-                const uint32_t va = B.slot(wrap<S::SLOTS>(base + v_pos<NB>(i, n) + nb)), pa = B.p + static_cast<uint32_t>(s) * P_BYTES;
-                // (64 components: the second half of the 128 rows is whatever lies behind, and is not read)
-                for (int k = 0; k < KEYS / 16; ++k)
-                    ptx::umma_f16_ss(d, ptx::sdesc_sw128(va + k * 2048, BLOCK_BYTES, 1024),
-                                     ptx::sdesc_sw128(pa + k * 2048, P_BYTES, 1024), idesc, !first || k > 0);
+            if (!sh->skip[s]) {
+                const uint32_t idesc = ptx::idesc_bf16_f32(128, s ? width1 : width0, true, true);
+                const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const uint32_t d = tmem + static_cast<uint32_t>(2 * COLS + (s * NB + nb) * COLS);
+                    // (64 components: the second half of the 128 rows is whatever lies behind, and is not read)
+                    const uint64_t v = ptx::sdesc_sw128(B.slot(wrap<S::SLOTS>(base + v_pos<NB>(i, n) + nb)), BLOCK_BYTES, 1024);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < KEYS / 16; ++k)
+                            ptx::umma_f16_ss(d, v + static_cast<uint64_t>(k * 128), p + static_cast<uint64_t>(k * 128), idesc, !first || k > 0);
+                    }
+                }
             }
-        };
-        auto release = [&](int pos) {
-            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(B.empty(wrap<S::SLOTS>(base + pos + nb)));
-        };
-        auto arrived = [&](int pos) {
-            for (int nb = 0; nb < NB; ++nb) ok = ok && B.wait_full(wrap<S::SLOTS>(base + pos + nb));
+            if (leader) {
+                ptx::umma_commit(bar(sh->o_done[s]));
+                if (free) release(v_pos<NB>(i, n));
+            }
         };
         for (int i = 0; ok && i <= n; ++i) {
             if (i < n) arrived(k_pos<NB>(i));
-            if (!both) {
-                if (ok && i < n) {
-                    scores(i & 1, i, i < 2);
-                    if (!ok) break;
-                    ptx::umma_commit(bar(sh->s_full[i & 1]));
-                    release(k_pos<NB>(i));
-                }
-                if (ok && i > 0) {
-                    arrived(v_pos<NB>(i - 1, n));
-                    weights((i - 1) & 1);
-                    outputs((i - 1) & 1, i - 1, i - 1 < 2);
-                    if (!ok) break;
-                    ptx::umma_commit(bar(sh->o_done[(i - 1) & 1]));
-                    release(v_pos<NB>(i - 1, n));
-                }
-            } else {
-                if (ok && i > 0) arrived(v_pos<NB>(i - 1, n));
-                for (int s = 0; ok && s < 2; ++s) {
-                    // the next scores first: the stream waits for them
-                    if (i > 0) weights(s);
-                    if (i < n) {
-                        scores(s, i, i == 0);
-                        if (!ok) break;
-                        ptx::umma_commit(bar(sh->s_full[s]));
+            if (both && i > 0) arrived(v_pos<NB>(i - 1, n));
+            const int turns = both ? 2 : 1;
+#pragma unroll 1
+            for (int j = 0; j < turns; ++j) {
+                // alternate tiles: scores of this tile for one stream, outputs of the one before for
+                // the other; both: the next scores of a stream first, it waits for them
+                const int s = both ? j : i & 1, so = both ? j : (i - 1) & 1;
+                if (both && i > 0) weights(s);
+                if (i < n) scores(s, i, i < 3 - turns, j == turns - 1);
+                if (i > 0) {
+                    if (!both) {
+                        arrived(v_pos<NB>(i - 1, n));
+                        weights(so);
                     }
-                    if (i > 0) {
-                        outputs(s, i - 1, i == 1);
-                        if (!ok) break;
-                        ptx::umma_commit(bar(sh->o_done[s]));
-                    }
+                    outputs(so, i - 1, i - 1 < 3 - turns, j == turns - 1);
                 }
-                if (!ok) break;
-                if (i > 0) release(v_pos<NB>(i - 1, n));
-                if (i < n) release(k_pos<NB>(i));
             }
         }
         base = wrap<S::SLOTS>(base + 2 * n * NB);
     }
-    if (!ok) {
+    if (!ok && leader) {
         report(a, STATUS_TIMEOUT, 2);
         // products in flight end before shared and tensor memory are given back
         ptx::umma_commit(bar(sh->drain));
@@ -301,6 +310,8 @@ __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
 }
 
 // ---- softmax: four warps per stream ------------------------------------------------------------
+// Code that runs once per unit or less is kept short, in loops: a line of instructions that is not in
+// the cache costs about as much as eight of them that are.
 template <int NB, int BLK>
 struct Stream {
     using S = Shape<NB, BLK>;
@@ -311,7 +322,7 @@ struct Stream {
     const uint32_t scores, out, q, p;
     uint32_t s_phase = 0, o_phase = 0;
     bool failed = false;
-    float l[4][16];                 // sums of this key's weights, per row
+    float2 l[COLS / 2];             // sums of this key's weights, per row
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
@@ -329,19 +340,35 @@ struct Stream {
 
     // Queries of rows row0 .. row0 + rows - 1 of the unit, zeros up to `width`, as the K-major operand.
     __device__ void load_q(const Unit &u, int row0, int rows, int width) {
-        const int chunks = (a.d + 15) / 16 * 2;
-        for (int i = key; i < width * chunks; i += 128) {
-            const int row = i / chunks, c = i - row * chunks;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows && c * 8 < a.d) {
-                const int r = u.row0 + row0 + row, token = r / a.group;
-                x = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(a.q) +
-                    (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d + c * 8);
+        const int chunks = (a.d + 15) / 16 * 2, n = width * chunks;
+        const uint32_t inv = (1u << 20) / static_cast<uint32_t>(chunks) + 1u;  // i / chunks of i < 2^11
+        const int r0 = u.row0 + row0;
+        const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(a.q) +
+                                    (static_cast<int64_t>(u.s.q0) * a.heads + u.head * a.group) * a.d;
+        constexpr int UN = 8;  // loads in flight
+#pragma unroll 1
+        for (int i0 = key; i0 < n; i0 += 128 * UN) {
+            uint4 x[UN];
+#pragma unroll
+            for (int j = 0; j < UN; ++j) {
+                const int i = i0 + 128 * j;
+                const int row = static_cast<int>((static_cast<uint32_t>(i) * inv) >> 20), c = i - row * chunks;
+                x[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n && row < rows && c * 8 < a.d) {
+                    const int token = (r0 + row) / a.group;
+                    x[j] = *reinterpret_cast<const uint4 *>(
+                        from + (static_cast<int64_t>(token) * a.heads + (r0 + row - token * a.group)) * a.d + c * 8);
+                }
             }
-            ptx::st_shared_v4(q + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + static_cast<uint32_t>(row) * 128u +
-                                  (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4),
-                              x.x, x.y, x.z, x.w);
+#pragma unroll
+            for (int j = 0; j < UN; ++j) {
+                const int i = i0 + 128 * j;
+                const int row = static_cast<int>((static_cast<uint32_t>(i) * inv) >> 20), c = i - row * chunks;
+                if (i < n)
+                    ptx::st_shared_v4(q + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + static_cast<uint32_t>(row) * 128u +
+                                          (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4),
+                                      x[j].x, x[j].y, x[j].z, x[j].w);
+            }
         }
         const int first = (u.row0 + row0) / a.group;
         if (key < COLS) {
@@ -352,18 +379,7 @@ struct Stream {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) l[c][j] = 0.0f;
-    }
-
-    __device__ void load_scores(uint32_t (&x)[4][16], int width) const {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (16 * c < width) ptx::tmem_ld_32x32b_x16(scores + 16 * c, x[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (16 * c < width) ptx::tmem_ld_wait(x[c]);
+        for (int i = 0; i < COLS / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
     }
 
     // Bit r: row r sees this thread's key.  Rows behind the last see everything (their scores are zero).
@@ -379,6 +395,7 @@ struct Stream {
         if (j >= 64 * a.tree_words) return past;
         const int64_t *words = a.tree + static_cast<int64_t>(u.s.q0 + (u.row0 + row0) / a.group) * a.tree_words + (j >> 6);
         uint64_t bits = past;
+#pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const uint64_t w = static_cast<uint64_t>(words[static_cast<int64_t>(sh->token[s][r]) * a.tree_words]);
             bits |= (w >> (j & 63) & 1ull) << r;
@@ -386,53 +403,145 @@ struct Stream {
         return bits;
     }
 
-    // Renews the references from the tile's maxima; the sums and outputs so far take the factors.
-    __device__ void renew(uint32_t (&x)[4][16], int width, bool masked, uint64_t sees, bool outputs) {
-        if (key < COLS) sh->top[s][key] = 0u;
-        vote(false);
-        load_scores(x, width);
+    // Scores that a row does not see: what the scale turns into -infinity.
+    __device__ void hide(uint64_t sees, int width) const {
+        const uint32_t none = a.scale_log2 > 0.0f ? 0xFF800000u : 0x7F800000u;
+#pragma unroll 1
+        for (int c = 0; c < width; c += 16) {
+            uint32_t x[16];
+            ptx::tmem_ld_32x32b_x16(scores + c, x);
+            ptx::tmem_ld_wait(x);
+            const uint32_t bits = static_cast<uint32_t>(sees >> c);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (16 * c < width) {
+            for (int j = 0; j < 16; ++j) x[j] = bits >> j & 1u ? x[j] : none;
+            ptx::tmem_st_32x32b_x16(scores + c, x);
+        }
+        ptx::tmem_st_wait();
+    }
+
+    // Scores of 16 rows in units of log2, less the references.
+    __device__ __forceinline__ void exponents(const uint32_t (&r)[16], int c, float2 (&x)[8]) const {
+        const float2 scale = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float v = __uint_as_float(x[c][j]) * a.scale_log2;
-                    if (masked && !(sees >> (16 * c + j) & 1ull)) v = -INFINITY;
-                    v = ptx::warp_max_f32(v);
-                    if (lane == ((16 * c + j) & 31)) atomicMax(&sh->top[s][16 * c + j], ordered(v));
-                }
+        for (int j = 0; j < 16; j += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&sh->ref[s][c + j]);
+            x[j / 2] = ptx::fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), scale, make_float2(-m.x, -m.y));
+            x[j / 2 + 1] = ptx::fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), scale, make_float2(-m.z, -m.w));
+        }
+    }
+
+    // The largest of them.
+    __device__ float highest(int width) const {
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (32 * h < width) {
+                uint32_t r[2][16];
+                ptx::tmem_ld_32x32b_x16(scores + 32 * h, r[0]);
+                if (32 * h + 16 < width) ptx::tmem_ld_32x32b_x16(scores + 32 * h + 16, r[1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (32 * h + 16 * c < width) {
+                        ptx::tmem_ld_wait(r[c]);
+                        float2 x[8];
+                        exponents(r[c], 32 * h + 16 * c, x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+                    }
             }
-        vote(false);
-        if (key < width) {
-            const float was = sh->m[s][key];
-            float now = unordered(sh->top[s][key]);
-            now = now > was ? now : was;  // NaN: as it was
-            sh->m[s][key] = now;
-            sh->top[s][key] = __float_as_uint(was == now ? 1.0f : exp2f(was - now));
+        return top;
+    }
+
+    // The weights, added to the sums and, rounded, to their place.  (The scores are read a second time: 64
+    // of them held over the vote beside the 64 sums do not fit the registers.)
+    __device__ void weigh(int width) {
+        const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (32 * h < width) {
+                uint32_t r[2][16];
+                ptx::tmem_ld_32x32b_x16(scores + 32 * h, r[0]);
+                if (32 * h + 16 < width) ptx::tmem_ld_32x32b_x16(scores + 32 * h + 16, r[1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (32 * h + 16 * c < width) {
+                        ptx::tmem_ld_wait(r[c]);
+                        float2 x[8];
+                        exponents(r[c], 32 * h + 16 * c, x);
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] = make_float2(ptx::ex2_approx(x[i].x), ptx::ex2_approx(x[i].y));
+                            float2 &sum = l[16 * h + 8 * c + i];
+                            sum = ptx::add2(sum, x[i]);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
+                            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        const int chunk = 4 * h + 2 * c;
+                        ptx::st_shared_v4(line + (static_cast<uint32_t>(chunk ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        ptx::st_shared_v4(line + (static_cast<uint32_t>((chunk + 1) ^ (key & 7)) << 4), w[4], w[5], w[6], w[7]);
+                    }
+            }
+    }
+
+    // Renews the references from the tile's maxima; the sums and outputs so far take the factors.
+    // Returns whether some row has seen nothing yet.
+    __device__ bool renew(int width, bool more) {
+#pragma unroll 1
+        for (int c = 0; c < width; c += 16) {
+            uint32_t x[16];
+            ptx::tmem_ld_32x32b_x16(scores + c, x);
+            ptx::tmem_ld_wait(x);
+            float top = 0.0f;  // lane j's: of row c + j
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float v = ptx::warp_max_f32(__uint_as_float(x[j]) * a.scale_log2);
+                if (lane == j) top = v;
+            }
+            if (lane < 16) ptx::st_shared_u32(p + P_WARPS + static_cast<uint32_t>(warp * COLS + c + lane) * 4u, __float_as_uint(top));
         }
         vote(false);
-        const uint32_t *factor = sh->top[s];
+        bool none = false;
+        if (key < width) {
+            const float was = sh->m[s][key];
+            float now = was;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (16 * c < width) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) l[c][j] *= __uint_as_float(factor[16 * c + j]);
+            for (int w = 0; w < 4; ++w) {
+                const float t = __uint_as_float(ptx::ld_shared_u32(p + P_WARPS + static_cast<uint32_t>(w * COLS + key) * 4u));
+                now = t > now ? t : now;  // NaN: passed over
             }
-        if (outputs) {
+            none = now == -INFINITY;
+            sh->m[s][key] = now;
+            sh->ref[s][key] = none ? 0.0f : now;
+            ptx::st_shared_u32(p + P_FACTOR + static_cast<uint32_t>(key) * 4u, __float_as_uint(was == now ? 1.0f : ptx::ex2_approx(was - now)));
+        }
+        const bool fresh = vote(none);
+        if (more) {
+#pragma unroll
+            for (int i = 0; i < COLS / 2; i += 2)
+                if (2 * i < width) {
+                    uint32_t f[4];
+                    ptx::ld_shared_v4(p + P_FACTOR + static_cast<uint32_t>(i) * 8u, f[0], f[1], f[2], f[3]);
+                    l[i] = ptx::mul2(l[i], make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])));
+                    l[i + 1] = ptx::mul2(l[i + 1], make_float2(__uint_as_float(f[2]), __uint_as_float(f[3])));
+                }
 #pragma unroll 1
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll 1
-                for (int c = 0; c * 16 < width; ++c) {
+                for (int c = 0; c < width; c += 16) {
                     uint32_t o[16];
-                    ptx::tmem_ld_32x32b_x16(out + nb * COLS + 16 * c, o);
+                    ptx::tmem_ld_32x32b_x16(out + nb * COLS + c, o);
                     ptx::tmem_ld_wait(o);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        o[j] = __float_as_uint(__uint_as_float(o[j]) * __uint_as_float(factor[16 * c + j]));
-                    ptx::tmem_st_32x32b_x16(out + nb * COLS + 16 * c, o);
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) *
+                                               __uint_as_float(ptx::ld_shared_u32(p + P_FACTOR + static_cast<uint32_t>(c + j) * 4u)));
+                    ptx::tmem_st_32x32b_x16(out + nb * COLS + c, o);
                 }
             ptx::tmem_st_wait();
+            vote(false);  // the factors have been read: the weights come to their place
         }
+        return fresh;
     }
 
     // Values that are not finite would reach rows that do not see them (0 x NaN).  Those behind the
@@ -445,7 +554,7 @@ struct Stream {
                 for (int b = 0; b < B.blocks(nb); ++b) {
                     const uint32_t line = B.slot(wrap<S::SLOTS>(pos + nb)) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
                     bool bad = false;
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
                         uint32_t w[4];
                         ptx::ld_shared_v4(line + static_cast<uint32_t>((c ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
@@ -454,7 +563,7 @@ struct Stream {
                             bad = bad || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
                     }
                     if (bad && at >= len) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 8; ++c) ptx::st_shared_v4(line + static_cast<uint32_t>(c << 4), 0u, 0u, 0u, 0u);
                     } else {
                         odd = odd || bad;
@@ -516,79 +625,18 @@ struct Stream {
         const int at = t * KEYS + key;
         const bool masked = (t + 1) * KEYS > u.s.prefix;
         uint64_t sees = ~0ull;
-        uint32_t x[4][16];
-        load_scores(x, width);
-        if (masked) sees = seen(u, row0, rows, at);
-        bool high = fresh;
-        if (!fresh) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (16 * c < width) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(&sh->m[s][16 * c + j]);
-                        const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float y = fmaf(__uint_as_float(x[c][j + i]), a.scale_log2, -mm[i]);
-                            x[c][j + i] = __float_as_uint(y);
-                        }
-                    }
-                }
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (!(sees >> (16 * c + j) & 1ull)) x[c][j] = 0xFF800000u;
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (16 * c < width) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) high = high || __uint_as_float(x[c][j]) > RENEW;
-                }
+        if (masked) {
+            sees = seen(u, row0, rows, at);
+            hide(sees, width);
         }
-        bool waited = false;
-        if (vote(high || failed)) {
+        if (fresh || vote(highest(width) > RENEW || failed)) {
             if (vote(failed)) return false;
-            if (k > 0) {
-                wait_out();
-                waited = true;
-            }
-            renew(x, width, masked, sees, k > 0);
-            fresh = false;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (16 * c < width) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float m = sh->m[s][16 * c + j];
-                        fresh = fresh || m == -INFINITY;
-                        float y = m == -INFINITY ? __uint_as_float(x[c][j]) : fmaf(__uint_as_float(x[c][j]), a.scale_log2, -m);
-                        if (masked && !(sees >> (16 * c + j) & 1ull)) y = -INFINITY;
-                        x[c][j] = __float_as_uint(y);
-                    }
-                }
+            if (k > 0) wait_out();
+            fresh = renew(width, k > 0);
+        } else if (k > 0) {
+            wait_out();  // the weights' space is read by the product of the tile before
         }
-        // the weights' space is read by the product of the tile before
-        if (k > 0 && !waited) wait_out();
-        const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (16 * c < width) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float p0 = ptx::ex2_approx(__uint_as_float(x[c][j])), p1 = ptx::ex2_approx(__uint_as_float(x[c][j + 1]));
-                    l[c][j] += p0;
-                    l[c][j + 1] += p1;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                    w[j >> 1] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                ptx::st_shared_v4(line + (static_cast<uint32_t>((2 * c) ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
-                ptx::st_shared_v4(line + (static_cast<uint32_t>((2 * c + 1) ^ (key & 7)) << 4), w[4], w[5], w[6], w[7]);
-            }
+        weigh(width);
         const bool own = masked && own_product(pos, at, u.s.len, sees, width, k == 0);
         if (key == 0) sh->skip[s] = own;
         ptx::fence_proxy_async_smem();
@@ -598,14 +646,12 @@ struct Stream {
         return true;
     }
 
-    // The warp's sums of l, into the weights' space (no product reads it any more): [warp][row].
-    __device__ void sum_l() {
+    // The warp's sums of l, into the weights' space (no product reads it any more).
+    __device__ void sum_l() const {
         float v[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[16 * c + j] = l[c][j];
-        // halves the values at every exchange: lane ends with rows 2 lane and 2 lane + 1, bits reversed below
+        for (int i = 0; i < COLS / 2; ++i) v[2 * i] = l[i].x, v[2 * i + 1] = l[i].y;
+        // halves the values at every exchange
 #pragma unroll
         for (int o = 16, n = 32; o > 0; o >>= 1, n >>= 1) {
             const bool up = lane & o;
@@ -616,30 +662,32 @@ struct Stream {
             }
         }
         const int row = (lane & 16 ? 32 : 0) + (lane & 8 ? 16 : 0) + (lane & 4 ? 8 : 0) + (lane & 2 ? 4 : 0) + (lane & 1 ? 2 : 0);
-        const uint32_t to = p + static_cast<uint32_t>(warp * COLS + row) * 4u;
+        const uint32_t to = p + P_WARPS + static_cast<uint32_t>(warp * COLS + row) * 4u;
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v[0]), "f"(v[1]) : "memory");
     }
 };
-
-__device__ __forceinline__ float ld_shared_f32(uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); }
 
 template <int NB, int BLK>
 __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint32_t tmem, int s) {
     const CacheAttnArgs &a = B.a;
     Small *sh = B.sh;
     Stream<NB, BLK> st(B, tmem, s);
+    const int key = st.key;
     int base = 0;
     Unit u;
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
+    auto shared = [&](uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); };
     while (walk.next(a, u)) {
         const int n = u.tiles;
         const bool both = u.rows > COLS;
         const int row0 = both ? s * COLS : 0, rows = both ? min(COLS, u.rows - row0) : u.rows;
         const int width = (rows + 15) & ~15;
         const int mine = both ? n : (n + 1 - s) / 2;
-        if (mine > 0) st.load_q(u, row0, rows, width);
+        if (mine > 0) {
+            st.load_q(u, row0, rows, width);
+            st.vote(false);  // references and tokens are written
+        }
         bool fresh = true, ok = true;
-        if (mine > 0) st.vote(false);  // m and token are written
         for (int k = 0; ok && k < mine; ++k) {
             const int i = both ? k : 2 * k + s;
             ok = st.tile(u, row0, rows, width, u.tile0 + i, k, wrap<Shape<NB, BLK>::SLOTS>(base + v_pos<NB>(i, n)), fresh);
@@ -655,60 +703,68 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
             if (threadIdx.x == 0) {
                 report(a, STATUS_TIMEOUT, 3);
                 do {
-                    if (u.cut && atomicAdd(a.counters + u.first, 1u) == static_cast<uint32_t>(u.last - u.first)) a.counters[u.first] = 0u;
+                    const Pieces in = walk.pieces(u);
+                    if (u.cut && atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first)) a.counters[in.first] = 0u;
                 } while (walk.next(a, u));
             }
             return;
         }
         ptx::tc_fence_after();
-        // Eight rows at a time: with the streams' tiles of the same rows, every other eight.
+        // Streams that shared the rows out by tiles are added up here.  A thread per row: factors of the
+        // outputs, and where the row goes.
         const bool two = !both && n > 1;
-        const int warp = st.warp, lane = st.lane;
-        const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-        auto l_of = [&](int stream, int r) {
-            const uint32_t at = B.p + static_cast<uint32_t>(stream) * P_BYTES + static_cast<uint32_t>(r) * 4u;
-            return (ld_shared_f32(at) + ld_shared_f32(at + COLS * 4)) + (ld_shared_f32(at + 2 * COLS * 4) + ld_shared_f32(at + 3 * COLS * 4));
-        };
-        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * TR;
-        for (int c = both ? 0 : s; 8 * c < rows; c += both ? 1 : 2) {
-            const int own = both ? s : 0;
-            float f0[8], f1[8], top[8], sum[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 8 * c + j;
-                top[j] = sh->m[own][r];
-                sum[j] = l_of(own, r);
-                f0[j] = 1.0f, f1[j] = 0.0f;
-                if (two) {
-                    const float m0 = top[j], m1 = sh->m[1][r], l1 = l_of(1, r);
-                    top[j] = fmaxf(m0, m1);
-                    f0[j] = scale_of(m0, top[j]), f1[j] = scale_of(m1, top[j]);
-                    sum[j] = sum[j] * f0[j] + l1 * f1[j];
-                }
+        const int own = both ? s : 0;
+        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * TR + row0;
+        if (key < rows) {
+            auto sum = [&](int stream) {
+                const uint32_t at = B.p + static_cast<uint32_t>(stream) * P_BYTES + P_WARPS + static_cast<uint32_t>(key) * 4u;
+                return (shared(at) + shared(at + COLS * 4)) + (shared(at + 2 * COLS * 4) + shared(at + 3 * COLS * 4));
+            };
+            float top = sh->m[own][key], total = sum(own), f0 = 1.0f, f1 = 0.0f;
+            if (two) {
+                const float m0 = top, m1 = sh->m[1][key];
+                top = fmaxf(m0, m1);
+                f0 = scale_of(m0, top), f1 = scale_of(m1, top);
+                total = total * f0 + sum(1) * f1;
             }
-            if (u.cut && warp == 0 && lane == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * c + j < rows) __stcg(a.part_ml + piece + row0 + 8 * c + j, make_float2(top[j], sum[j]));
+            const int r = u.row0 + row0 + key, token = r / a.group;
+            int to = token * a.heads + (r - token * a.group);
+            if (u.cut) {
+                if (both || s == 0) __stcg(a.part_ml + piece + key, make_float2(top, total));
+                to = key;
+            } else {
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a row that sees nothing: zeros
+                f0 *= inv, f1 *= inv;
             }
-            for (int nb = 0; nb < NB; ++nb) {
-                uint32_t o[8], o1[8];
-                ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (own * NB + nb) * COLS + 8 * c), o);
-                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (NB + nb) * COLS + 8 * c), o1);
-                ptx::tmem_ld_wait(o);
-                if (two) ptx::tmem_ld_wait(o1);
-                const int e = nb * 128 + 32 * warp + lane;
+            ptx::st_shared_u32(st.p + P_FACTOR + static_cast<uint32_t>(key) * 4u, __float_as_uint(f0));
+            ptx::st_shared_u32(st.p + P_OTHER + static_cast<uint32_t>(key) * 4u, __float_as_uint(f1));
+            ptx::st_shared_u32(st.p + P_ROW + static_cast<uint32_t>(key) * 4u, static_cast<uint32_t>(to));
+        }
+        st.vote(false);
+        float *part = a.part + piece * a.d;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (static_cast<int64_t>(u.s.q0) * a.heads + u.head * a.group) * a.d;
+        const uint32_t lanes = static_cast<uint32_t>(32 * st.warp) << 16;
+#pragma unroll 1
+        for (int nb = 0; nb < NB; ++nb) {
+            const int e = nb * 128 + key;
+#pragma unroll 1
+            for (int c = both ? 0 : 8 * s; c < rows; c += both ? 8 : 16) {
+                uint32_t x[8], y[8];
+                ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (own * NB + nb) * COLS + c), x);
+                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (NB + nb) * COLS + c), y);
+                ptx::tmem_ld_wait(x);
+                if (two) ptx::tmem_ld_wait(y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int r = 8 * c + j;
-                    if (r >= rows || e >= a.d) continue;
-                    float v = __uint_as_float(o[j]);
-                    if (two) v = v * f0[j] + __uint_as_float(o1[j]) * f1[j];
-                    if (u.cut) {
-                        __stcg(a.part + (piece + row0 + r) * a.d + e, v);
-                    } else {
-                        v = sum[j] == 0.0f ? 0.0f : v / sum[j];
-                        out_row<__nv_bfloat16>(a, u, row0 + r)[e] = __float2bfloat16_rn(v);
+                    const uint32_t at = st.p + P_FACTOR + static_cast<uint32_t>(c + j) * 4u;
+                    float v = __uint_as_float(x[j]) * shared(at);
+                    if (two) v += __uint_as_float(y[j]) * shared(at + (P_OTHER - P_FACTOR));
+                    const int64_t to = static_cast<int64_t>(static_cast<int>(ptx::ld_shared_u32(at + (P_ROW - P_FACTOR)))) * a.d + e;
+                    if (c + j < rows && e < a.d) {
+                        if (u.cut)
+                            __stcg(part + to, v);
+                        else
+                            o[to] = __float2bfloat16_rn(v);
                     }
                 }
             }
@@ -717,14 +773,14 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         if (u.cut) __threadfence();
         both_vote(false);  // outputs, references and sums have been read
         if (u.cut) {
+            const Pieces in = walk.pieces(u);
             if (threadIdx.x == 0) {
-                const uint32_t pieces = static_cast<uint32_t>(u.last - u.first + 1);
-                sh->last = atomicAdd(a.counters + u.first, 1u) == pieces - 1;
-                if (sh->last) a.counters[u.first] = 0u;
+                sh->last = atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first);
+                if (sh->last) a.counters[in.first] = 0u;
                 __threadfence();
             }
             both_vote(false);
-            if (sh->last) join<__nv_bfloat16, TR>(a, u, threadIdx.x, 256);
+            if (sh->last) join<__nv_bfloat16, TR>(a, u, in, threadIdx.x, 256);
         }
     }
 }
@@ -757,7 +813,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         ptx::prefetch_tensormap(&mk);
         ptx::prefetch_tensormap(&mv);
     }
-    if (warp == 9) {
+    if (warp == 8) {
         ptx::tmem_alloc(ptx::smem_u32(&sh->tmem), S::TMEM);
         ptx::tmem_relinquish();
     }
@@ -774,14 +830,14 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     } else {
         ptx::fewer_registers<OTHER_REGISTERS>();
         if (warp == 8)
-            copy_role<NB, BLK>(B, walk, &mk, &mv, box);
-        else if (warp == 9 && (threadIdx.x & 31) == 0)
             product_role<NB, BLK>(B, walk, tmem);
+        else if (warp < 11)
+            copy_role<NB, BLK>(B, walk, warp == 10, warp == 10 ? &mv : &mk, box);
     }
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 8) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, S::TMEM);
     }
