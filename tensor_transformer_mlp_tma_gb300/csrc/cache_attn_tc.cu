@@ -42,9 +42,6 @@ constexpr int KEYS = 128;
 constexpr int COLS = 64;                // rows per stream
 // Two streams of a warpgroup each, and one whose warps copy K, issue the products and copy V.
 constexpr int TTHREADS = 384;
-// Registers per thread: a stream's hold 64 scores and 64 sums.  Launched with 168 (three warpgroups in
-// 65536), 208 + 208 + 88 = 3 x 168.
-constexpr int STREAM_REGISTERS = 208, OTHER_REGISTERS = 88;
 constexpr uint32_t BLOCK_BYTES = KEYS * 128;    // 128 keys of 64 components
 constexpr uint32_t Q_BLOCK_BYTES = COLS * 128;  // 64 rows of 64 components
 constexpr uint32_t P_BYTES = KEYS * 128;
@@ -170,12 +167,21 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
                 const int blocks = B.blocks(nb);
                 const uint32_t bar = B.full(pos), dst = B.slot(pos);
                 if (leader) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
-                for (int p = 0; p < valid; ++p) {
-                    const int page = __shfl_sync(0xffffffffu, x.page, p), row = __shfl_sync(0xffffffffu, x.row, p);
+                for (int p = 0; p < valid; p += 4) {
+                    int page[4], row[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        page[j] = __shfl_sync(0xffffffffu, x.page, p + j);
+                        row[j] = __shfl_sync(0xffffffffu, x.row, p + j);
+                    }
                     if (leader) {
-                        const uint32_t to = dst + static_cast<uint32_t>(p * box) * 128u;
-                        ptx::tma_load_4d(to, map, bar, nb * 128, row, u.head, page);
-                        if (BLK > 1 && blocks > 1) ptx::tma_load_4d(to + BLOCK_BYTES, map, bar, nb * 128 + 64, row, u.head, page);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (p + j < valid) {
+                                const uint32_t to = dst + static_cast<uint32_t>((p + j) * box) * 128u;
+                                ptx::tma_load_4d(to, map, bar, nb * 128, row[j], u.head, page[j]);
+                                if (BLK > 1 && blocks > 1) ptx::tma_load_4d(to + BLOCK_BYTES, map, bar, nb * 128 + 64, row[j], u.head, page[j]);
+                            }
                     }
                 }
                 const uint32_t bit = 1u << (pos % S::SLOTS);
@@ -322,7 +328,7 @@ struct Stream {
     const uint32_t scores, out, q, p;
     uint32_t s_phase = 0, o_phase = 0;
     bool failed = false;
-    float2 l[COLS / 2];             // sums of this key's weights, per row
+    float2 l[4];                    // sums of the weights of 8 rows over some of the warp's keys (see add_up)
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
@@ -340,34 +346,29 @@ struct Stream {
 
     // Queries of rows row0 .. row0 + rows - 1 of the unit, zeros up to `width`, as the K-major operand.
     __device__ void load_q(const Unit &u, int row0, int rows, int width) {
-        const int chunks = (a.d + 15) / 16 * 2, n = width * chunks;
-        const uint32_t inv = (1u << 20) / static_cast<uint32_t>(chunks) + 1u;  // i / chunks of i < 2^11
-        const int r0 = u.row0 + row0;
+        // two threads per row, half of its chunks of 8 components each
+        const int row = key >> 1, chunks = (a.d + 15) / 16;
+        const int r = u.row0 + row0 + row, token = r / a.group;
         const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(a.q) +
-                                    (static_cast<int64_t>(u.s.q0) * a.heads + u.head * a.group) * a.d;
-        constexpr int UN = 8;  // loads in flight
+                                    (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
+        if (row < width) {
 #pragma unroll 1
-        for (int i0 = key; i0 < n; i0 += 128 * UN) {
-            uint4 x[UN];
+            for (int i0 = 0; i0 < chunks; i0 += 8) {
+                uint4 x[8];
 #pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                const int i = i0 + 128 * j;
-                const int row = static_cast<int>((static_cast<uint32_t>(i) * inv) >> 20), c = i - row * chunks;
-                x[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < n && row < rows && c * 8 < a.d) {
-                    const int token = (r0 + row) / a.group;
-                    x[j] = *reinterpret_cast<const uint4 *>(
-                        from + (static_cast<int64_t>(token) * a.heads + (r0 + row - token * a.group)) * a.d + c * 8);
+                for (int i = 0; i < 8; ++i) {
+                    const int c = 2 * (i0 + i) + (key & 1);
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i0 + i < chunks && row < rows && c * 8 < a.d) x[i] = *reinterpret_cast<const uint4 *>(from + c * 8);
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                const int i = i0 + 128 * j;
-                const int row = static_cast<int>((static_cast<uint32_t>(i) * inv) >> 20), c = i - row * chunks;
-                if (i < n)
-                    ptx::st_shared_v4(q + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + static_cast<uint32_t>(row) * 128u +
-                                          (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4),
-                                      x[j].x, x[j].y, x[j].z, x[j].w);
+                for (int i = 0; i < 8; ++i) {
+                    const int c = 2 * (i0 + i) + (key & 1);
+                    if (i0 + i < chunks)
+                        ptx::st_shared_v4(q + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + static_cast<uint32_t>(row) * 128u +
+                                              (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4),
+                                          x[i].x, x[i].y, x[i].z, x[i].w);
+                }
             }
         }
         const int first = (u.row0 + row0) / a.group;
@@ -379,7 +380,25 @@ struct Stream {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
 #pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < 4; ++i) l[i] = make_float2(0.0f, 0.0f);
+    }
+
+    // Lanes that share a key's line in add_up: eight rows each.
+    static __device__ __forceinline__ int line_lanes(int width) { return width <= 16 ? 2 : (width <= 32 ? 4 : 8); }
+
+    // Adds up the rounded weights, as the product does, from their place: a lane takes eight rows of every
+    // (32 / lanes)-th key of its warp.  (Sums of all rows for its own key would be 64 registers.)
+    __device__ void add_up(int width) {
+        const int lanes = line_lanes(width), chunk = lane & (lanes - 1), keys = 32 / lanes;
+        if (8 * chunk < width) {
+            for (int k = lane / lanes; k < 32; k += keys) {
+                uint32_t w[4];
+                ptx::ld_shared_v4(p + static_cast<uint32_t>(32 * warp + k) * 128u + (static_cast<uint32_t>(chunk ^ (k & 7)) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    l[i] = ptx::add2(l[i], make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+            }
+        }
     }
 
     // Bit r: row r sees this thread's key.  Rows behind the last see everything (their scores are zero).
@@ -419,69 +438,37 @@ struct Stream {
         ptx::tmem_st_wait();
     }
 
-    // Scores of 16 rows in units of log2, less the references.
-    __device__ __forceinline__ void exponents(const uint32_t (&r)[16], int c, float2 (&x)[8]) const {
+    // Weights of the rows, rounded to bf16, two to a word; returns the largest exponent.
+    __device__ float form(uint32_t (&w)[COLS / 2], int width) const {
         const float2 scale = make_float2(a.scale_log2, a.scale_log2);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(&sh->ref[s][c + j]);
-            x[j / 2] = ptx::fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), scale, make_float2(-m.x, -m.y));
-            x[j / 2 + 1] = ptx::fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), scale, make_float2(-m.z, -m.w));
-        }
-    }
-
-    // The largest of them.
-    __device__ float highest(int width) const {
         float top = -INFINITY;
+        // 32 rows at a time: with all 64 loaded at once the registers do not suffice
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (32 * h < width) {
-                uint32_t r[2][16];
-                ptx::tmem_ld_32x32b_x16(scores + 32 * h, r[0]);
-                if (32 * h + 16 < width) ptx::tmem_ld_32x32b_x16(scores + 32 * h + 16, r[1]);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[2][16];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (32 * h + 16 * c < width) {
-                        ptx::tmem_ld_wait(r[c]);
-                        float2 x[8];
-                        exponents(r[c], 32 * h + 16 * c, x);
+            for (int c = 0; c < 2; ++c)
+                if (32 * h + 16 * c < width) ptx::tmem_ld_32x32b_x16(scores + 32 * h + 16 * c, r[c]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+            for (int c = 0; c < 2; ++c)
+                if (32 * h + 16 * c < width) {
+                    ptx::tmem_ld_wait(r[c]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 m = *reinterpret_cast<const float4 *>(&sh->ref[s][32 * h + 16 * c + 4 * j]);
+                        const float2 lo = ptx::fma2(make_float2(__uint_as_float(r[c][4 * j]), __uint_as_float(r[c][4 * j + 1])), scale,
+                                                    make_float2(-m.x, -m.y));
+                        const float2 hi = ptx::fma2(make_float2(__uint_as_float(r[c][4 * j + 2]), __uint_as_float(r[c][4 * j + 3])), scale,
+                                                    make_float2(-m.z, -m.w));
+                        top = fmaxf(top, fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
+                        const __nv_bfloat162 e0 = __floats2bfloat162_rn(ptx::ex2_approx(lo.x), ptx::ex2_approx(lo.y)),
+                                             e1 = __floats2bfloat162_rn(ptx::ex2_approx(hi.x), ptx::ex2_approx(hi.y));
+                        w[16 * h + 8 * c + 2 * j] = *reinterpret_cast<const uint32_t *>(&e0);
+                        w[16 * h + 8 * c + 2 * j + 1] = *reinterpret_cast<const uint32_t *>(&e1);
                     }
-            }
+                }
+        }
         return top;
-    }
-
-    // The weights, added to the sums and, rounded, to their place.  (The scores are read a second time: 64
-    // of them held over the vote beside the 64 sums do not fit the registers.)
-    __device__ void weigh(int width) {
-        const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (32 * h < width) {
-                uint32_t r[2][16];
-                ptx::tmem_ld_32x32b_x16(scores + 32 * h, r[0]);
-                if (32 * h + 16 < width) ptx::tmem_ld_32x32b_x16(scores + 32 * h + 16, r[1]);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (32 * h + 16 * c < width) {
-                        ptx::tmem_ld_wait(r[c]);
-                        float2 x[8];
-                        exponents(r[c], 32 * h + 16 * c, x);
-                        uint32_t w[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x[i] = make_float2(ptx::ex2_approx(x[i].x), ptx::ex2_approx(x[i].y));
-                            float2 &sum = l[16 * h + 8 * c + i];
-                            sum = ptx::add2(sum, x[i]);
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
-                            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-                        }
-                        const int chunk = 4 * h + 2 * c;
-                        ptx::st_shared_v4(line + (static_cast<uint32_t>(chunk ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        ptx::st_shared_v4(line + (static_cast<uint32_t>((chunk + 1) ^ (key & 7)) << 4), w[4], w[5], w[6], w[7]);
-                    }
-            }
     }
 
     // Renews the references from the tile's maxima; the sums and outputs so far take the factors.
@@ -517,14 +504,13 @@ struct Stream {
         }
         const bool fresh = vote(none);
         if (more) {
+            const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & (line_lanes(width) - 1)) * 32u;
+            uint32_t f[8];
+            ptx::ld_shared_v4(rows8, f[0], f[1], f[2], f[3]);
+            ptx::ld_shared_v4(rows8 + 16, f[4], f[5], f[6], f[7]);
 #pragma unroll
-            for (int i = 0; i < COLS / 2; i += 2)
-                if (2 * i < width) {
-                    uint32_t f[4];
-                    ptx::ld_shared_v4(p + P_FACTOR + static_cast<uint32_t>(i) * 8u, f[0], f[1], f[2], f[3]);
-                    l[i] = ptx::mul2(l[i], make_float2(__uint_as_float(f[0]), __uint_as_float(f[1])));
-                    l[i + 1] = ptx::mul2(l[i + 1], make_float2(__uint_as_float(f[2]), __uint_as_float(f[3])));
-                }
+            for (int i = 0; i < 4; ++i)
+                l[i] = ptx::mul2(l[i], make_float2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1])));
 #pragma unroll 1
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll 1
@@ -629,41 +615,50 @@ struct Stream {
             sees = seen(u, row0, rows, at);
             hide(sees, width);
         }
-        if (fresh || vote(highest(width) > RENEW || failed)) {
-            if (vote(failed)) return false;
-            if (k > 0) wait_out();
-            fresh = renew(width, k > 0);
-        } else if (k > 0) {
-            wait_out();  // the weights' space is read by the product of the tile before
+        uint32_t w[COLS / 2];
+        int pass = fresh ? 1 : 0;
+#pragma unroll 1
+        for (;; ++pass) {
+            if (pass == 1) {
+                if (vote(failed)) return false;
+                if (k > 0) wait_out();
+                fresh = renew(width, k > 0);
+            }
+            const float top = form(w, width);
+            if (pass == 1 || !vote(top > RENEW || failed)) break;
         }
-        weigh(width);
+        if (k > 0 && pass == 0) wait_out();  // their place is read by the product of the tile before
+        const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (8 * c < width)
+                ptx::st_shared_v4(line + (static_cast<uint32_t>(c ^ (key & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         const bool own = masked && own_product(pos, at, u.s.len, sees, width, k == 0);
         if (key == 0) sh->skip[s] = own;
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->p_full[s]));
+        add_up(width);
         return true;
     }
 
-    // The warp's sums of l, into the weights' space (no product reads it any more).
-    __device__ void sum_l() const {
-        float v[64];
+    // The warp's sums, into the weights' space (which no product reads any more).
+    __device__ void sum_l(int width) {
+        const int lanes = line_lanes(width);
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) v[2 * i] = l[i].x, v[2 * i + 1] = l[i].y;
-        // halves the values at every exchange
-#pragma unroll
-        for (int o = 16, n = 32; o > 0; o >>= 1, n >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        for (int i = 0; i < 4; ++i)
+            for (int o = lanes; o < 32; o <<= 1) {
+                l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
+                l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
             }
+        vote(false);  // every warp has read its weights
+        if (lane < lanes) {
+            const uint32_t to = p + P_WARPS + static_cast<uint32_t>(warp * COLS + 8 * lane) * 4u;
+            ptx::st_shared_v4(to, __float_as_uint(l[0].x), __float_as_uint(l[0].y), __float_as_uint(l[1].x), __float_as_uint(l[1].y));
+            ptx::st_shared_v4(to + 16, __float_as_uint(l[2].x), __float_as_uint(l[2].y), __float_as_uint(l[3].x), __float_as_uint(l[3].y));
         }
-        const int row = (lane & 16 ? 32 : 0) + (lane & 8 ? 16 : 0) + (lane & 4 ? 8 : 0) + (lane & 2 ? 4 : 0) + (lane & 1 ? 2 : 0);
-        const uint32_t to = p + P_WARPS + static_cast<uint32_t>(warp * COLS + row) * 4u;
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v[0]), "f"(v[1]) : "memory");
     }
 };
 
@@ -694,7 +689,7 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         }
         if (ok && mine > 0) {
             st.wait_out();
-            st.sum_l();
+            st.sum_l(width);
         }
         base = wrap<Shape<NB, BLK>::SLOTS>(base + 2 * n * NB);
         if (both_vote(!ok || st.failed)) {
@@ -825,10 +820,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = sh->tmem;
     if (warp < 8) {
-        ptx::more_registers<STREAM_REGISTERS>();
         softmax_role<NB, BLK>(B, walk, tmem, warp >> 2);
     } else {
-        ptx::fewer_registers<OTHER_REGISTERS>();
         if (warp == 8)
             product_role<NB, BLK>(B, walk, tmem);
         else if (warp < 11)
