@@ -61,14 +61,17 @@ struct Shape {
     // 227 KB less the queries, the weights, the small arrays and 1 KB for alignment
     static constexpr int FIT = (232448 - 2 * static_cast<int>(Q_BYTES + P_BYTES) - static_cast<int>(SMALL_BYTES) - 1024) / static_cast<int>(SLOT);
     static constexpr int SLOTS = FIT < 10 ? FIT : 10;
+    // V waits for the weights of its tile, K for nothing
+    static constexpr int K_SLOTS = SLOTS / 2, V_SLOTS = SLOTS - K_SLOTS;
     static constexpr uint32_t RING = SLOTS * SLOT;
     static constexpr uint32_t SMEM = RING + 2 * (Q_BYTES + P_BYTES) + SMALL_BYTES + 1024;
-    static constexpr uint32_t TMEM = NB == 1 ? 256 : 512;  // columns: 2 x 64 of S, 2 x NB x 64 of O
 };
+constexpr uint32_t TMEM = 512;          // columns: 2 x 2 x 64 of S, 2 x NB x 64 of O
+constexpr uint32_t O_COLUMN = 4 * COLS;
 
 struct Small {
-    uint64_t full[10], empty[10];
-    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], drain;
+    uint64_t full[10], empty[10];  // of K's slots, then V's
+    uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
     float m[2][COLS];      // references (log2)
     alignas(16) float ref[2][COLS];  // the same, 0 for a row that has seen nothing yet
     uint8_t token[2][COLS]; // of a row, counted from the first row's token
@@ -81,16 +84,6 @@ struct Small {
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
 static_assert(Shape<1, 1>::SLOTS == 10 && Shape<1, 2>::SLOTS == 5 && Shape<2, 2>::SLOTS == 4, "ring");
 
-// Ring position of a unit's i-th K or V tile: K0 K1 V0 K2 V1 ... V(n-1), NB slots each.
-template <int NB>
-__device__ __forceinline__ int k_pos(int i) {
-    return NB * (i == 0 ? 0 : 2 * i - 1);
-}
-template <int NB>
-__device__ __forceinline__ int v_pos(int i, int n) {
-    return NB * (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
-}
-
 template <int NB, int BLK>
 struct Block {
     using S = Shape<NB, BLK>;
@@ -98,9 +91,7 @@ struct Block {
     Small *sh;
     uint32_t ring, q, p;   // shared-memory addresses
 
-    __device__ uint32_t slot(int pos) const { return ring + static_cast<uint32_t>(pos % S::SLOTS) * S::SLOT; }
-    __device__ uint32_t full(int pos) const { return ptx::smem_u32(&sh->full[pos % S::SLOTS]); }
-    __device__ uint32_t empty(int pos) const { return ptx::smem_u32(&sh->empty[pos % S::SLOTS]); }
+    __device__ uint32_t bar(const uint64_t &x) const { return ptx::smem_u32(&x); }
     __device__ bool wait(uint32_t bar, uint32_t parity) const {
         // the clock is looked at only after many tries
 #pragma unroll 1
@@ -110,17 +101,23 @@ struct Block {
         sh->abort = 1;
         return false;
     }
-    __device__ bool wait_full(int pos) const { return wait(full(pos), static_cast<uint32_t>(pos / S::SLOTS) & 1u); }
-    __device__ bool wait_empty(int pos) const { return wait(empty(pos), (static_cast<uint32_t>(pos / S::SLOTS) & 1u) ^ 1u); }
+    // The same for a whole warp.
+    __device__ bool warp_wait(uint32_t bar, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xffffffffu, wait(bar, parity));
+    }
     // Blocks of 64 components that block nb of a head has.
     __device__ int blocks(int nb) const { return min(BLK, (a.d - nb * 128 + 63) / 64); }
 };
 
-// Ring positions are counted modulo a multiple of the slots that keeps the phase.
-template <int SLOTS>
-__device__ __forceinline__ int wrap(int pos) {
-    return pos % (2 * SLOTS * 4096);
-}
+// A place in the ring of K or of V.
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) slot = 0, phase ^= 1u;
+    }
+};
 
 // ---- copies: one warp for K, one for V -----------------------------------------------------------
 template <int NB, int BLK>
@@ -131,8 +128,11 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
     const int pieces = KEYS / box;
     const unsigned page_size = static_cast<unsigned>(a.page_size);
     const bool leader = ptx::elect_one();
-    int base = 0;
-    uint32_t copied = 0, phases = 0;  // per slot: this warp has copied to it, and in which phase last
+    const int first = values ? S::K_SLOTS : 0, slots = values ? S::V_SLOTS : S::K_SLOTS;
+    const uint32_t ring = B.ring + static_cast<uint32_t>(first) * S::SLOT;
+    const uint32_t full0 = B.bar(B.sh->full[first]), empty0 = B.bar(B.sh->empty[first]);
+    Place at;
+    uint32_t copied = 0, phases = 0;  // per slot: whether it has been copied to, and in which phase last
     bool ok = true;
     Unit u = {};
     // The page (as the table has it) and row of this lane's piece of a tile; row -1: no keys there.
@@ -143,14 +143,15 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
         Piece x = {0, -1};
         const int key = tile * KEYS + lane * box;
         if (lane < pieces && key < u.s.len) {
-            const unsigned at = static_cast<unsigned>(key) / page_size;
-            x.page = a.table[u.b * a.max_pages + at];
-            x.row = key - static_cast<int>(at * page_size);
+            const unsigned n = static_cast<unsigned>(key) / page_size;
+            x.page = a.table[u.b * a.max_pages + n];
+            x.row = key - static_cast<int>(n * page_size);
         }
         return x;
     };
     while (ok && walk.next(a, u)) {
         Piece next = look(u.tile0);
+#pragma unroll 1
         for (int i = 0; ok && i < u.tiles; ++i) {
             Piece x = next;
             if (i + 1 < u.tiles) next = look(u.tile0 + i + 1);
@@ -159,14 +160,14 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
                 x.page = static_cast<int>(a.pages);  // past the last page: zeros
             }
             const int valid = __popc(__ballot_sync(0xffffffffu, x.row >= 0));
-#pragma unroll
+#pragma unroll 1
             for (int nb = 0; nb < NB; ++nb) {
-                const int pos = wrap<S::SLOTS>(base + (values ? v_pos<NB>(i, u.tiles) : k_pos<NB>(i)) + nb);
-                ok = __all_sync(0xffffffffu, ok && B.wait_empty(pos));
+                ok = B.warp_wait(empty0 + 8 * at.slot, at.phase ^ 1u);
                 if (!ok) break;
                 const int blocks = B.blocks(nb);
-                const uint32_t bar = B.full(pos), dst = B.slot(pos);
+                const uint32_t bar = full0 + 8 * at.slot, dst = ring + static_cast<uint32_t>(at.slot) * S::SLOT;
                 if (leader) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
+#pragma unroll 1
                 for (int p = 0; p < valid; p += 4) {
                     int page[4], row[4];
 #pragma unroll
@@ -184,18 +185,17 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
                             }
                     }
                 }
-                const uint32_t bit = 1u << (pos % S::SLOTS);
-                copied |= bit;
-                phases = (pos / S::SLOTS) & 1 ? phases | bit : phases & ~bit;
+                copied |= 1u << at.slot;
+                phases = (phases & ~(1u << at.slot)) | at.phase << at.slot;
+                at.next(slots);
             }
         }
-        base = wrap<S::SLOTS>(base + 2 * u.tiles * NB);
     }
     if (!ok) {
         if (lane == 0) report(a, STATUS_TIMEOUT, 1);
         // copies in flight land before anything goes on
-        for (int i = 0; i < S::SLOTS; ++i)
-            if (copied >> i & 1u) ptx::mbar_wait(ptx::smem_u32(&B.sh->full[i]), phases >> i & 1u, a.wait_ns, nullptr);
+        for (int i = 0; i < slots; ++i)
+            if (copied >> i & 1u) ptx::mbar_wait(full0 + 8 * i, phases >> i & 1u, a.wait_ns, nullptr);
     }
 }
 
@@ -207,111 +207,111 @@ __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
     Small *sh = B.sh;
     const int steps = (a.d + 15) / 16;
     const bool leader = ptx::elect_one();
-    int base = 0;
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    const uint32_t v_ring = B.ring + S::K_SLOTS * S::SLOT;
+    const uint32_t k_full = B.bar(sh->full[0]), v_full = B.bar(sh->full[S::K_SLOTS]);
+    const uint32_t to_empty = B.bar(sh->empty[0]) - k_full;
+    Place kp, vp;
+    uint32_t q_phase = 0, p_phase = 0;  // a bit per stream
     bool ok = true;
     Unit u;
-    auto bar = [&](uint64_t &x) { return ptx::smem_u32(&x); };
     // all lanes wait, one issues
-    auto wait = [&](uint32_t b, uint32_t phase) { ok = __all_sync(0xffffffffu, ok && B.wait(b, phase)); };
     while (ok && walk.next(a, u)) {
         const int n = u.tiles;
         const bool both = u.rows > COLS;  // both streams take every tile
         const int width0 = both ? COLS : (u.rows + 15) & ~15, width1 = both ? (u.rows - COLS + 15) & ~15 : width0;
-        auto release = [&](int pos) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(B.empty(wrap<S::SLOTS>(base + pos + nb)));
-        };
-        auto arrived = [&](int pos) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int at = wrap<S::SLOTS>(base + pos + nb);
-                wait(B.full(at), static_cast<uint32_t>(at / S::SLOTS) & 1u);
-            }
-        };
-        // Descriptors count 16 bytes: 16 components on are 2, 64 a block; 16 keys on are 128.
-        auto scores = [&](int s, int i, bool first, bool free) {
-            if (first) {
-                wait(bar(sh->q_full[s]), q_phase[s]);
-                q_phase[s] ^= 1u;
-            }
-            if (!ok) return;
-            ptx::tc_fence_after();
-            const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, s ? width1 : width0, false, false);
-            const uint32_t d = tmem + static_cast<uint32_t>(s * COLS);
-            const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * S::Q_BYTES, 16, 1024);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const uint64_t k0 = ptx::sdesc_sw128(B.slot(wrap<S::SLOTS>(base + k_pos<NB>(i) + nb)), 16, 1024);
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < 4 * BLK; ++k)
-                        if (nb * 8 + k < steps)
-                            ptx::umma_f16_ss(d, k0 + static_cast<uint64_t>((k >> 2) * (BLOCK_BYTES >> 4) + (k & 3) * 2),
-                                             q + static_cast<uint64_t>((nb * 2 + (k >> 2)) * (Q_BLOCK_BYTES >> 4) + (k & 3) * 2),
-                                             idesc, nb + k > 0);
-                }
-            }
-            if (leader) {
-                ptx::umma_commit(bar(sh->s_full[s]));
-                if (free) release(k_pos<NB>(i));
-            }
-        };
-        // the stream's weights of a tile are formed, and its scores have been read
-        auto weights = [&](int s) {
-            wait(bar(sh->p_full[s]), p_phase[s]);
-            p_phase[s] ^= 1u;
-        };
-        auto outputs = [&](int s, int i, bool first, bool free) {
-            if (!ok) return;
-            ptx::tc_fence_after();
-            if (!sh->skip[s]) {
-                const uint32_t idesc = ptx::idesc_bf16_f32(128, s ? width1 : width0, true, true);
-                const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
+        // Scores run ahead of outputs by a tile per stream: each has two places for them.
+        const int streams = both ? 2 : 1, lag = both ? 1 : 2;
+#pragma unroll 1
+        for (int i = 0; ok && i < n + lag; ++i) {
+            if (i < n) {
+                uint64_t kd[NB];
+                uint32_t free[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const uint32_t d = tmem + static_cast<uint32_t>(2 * COLS + (s * NB + nb) * COLS);
-                    // (64 components: the second half of the 128 rows is whatever lies behind, and is not read)
-                    const uint64_t v = ptx::sdesc_sw128(B.slot(wrap<S::SLOTS>(base + v_pos<NB>(i, n) + nb)), BLOCK_BYTES, 1024);
+                    ok = ok && B.warp_wait(k_full + 8 * kp.slot, kp.phase);
+                    kd[nb] = ptx::sdesc_sw128(B.ring + static_cast<uint32_t>(kp.slot) * S::SLOT, 16, 1024);
+                    free[nb] = k_full + to_empty + 8 * kp.slot;
+                    kp.next(S::K_SLOTS);
+                }
+#pragma unroll 1
+                for (int j = 0; ok && j < streams; ++j) {
+                    const int s = both ? j : i & 1, k = both ? i : i >> 1;
+                    if (k == 0) {
+                        ok = B.warp_wait(B.bar(sh->q_full[s]), q_phase >> s & 1u);
+                        q_phase ^= 1u << s;
+                        if (!ok) break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, s ? width1 : width0, false, false);
+                    const uint32_t d = tmem + static_cast<uint32_t>((2 * s + (k & 1)) * COLS);
+                    const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * S::Q_BYTES, 16, 1024);
                     if (leader) {
+                        // descriptors count 16 bytes: 16 components on are 2, 64 a block
 #pragma unroll
-                        for (int k = 0; k < KEYS / 16; ++k)
-                            ptx::umma_f16_ss(d, v + static_cast<uint64_t>(k * 128), p + static_cast<uint64_t>(k * 128), idesc, !first || k > 0);
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int c = 0; c < 4 * BLK; ++c)
+                                if (nb * 8 + c < steps)
+                                    ptx::umma_f16_ss(d, kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2),
+                                                     q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2),
+                                                     idesc, nb + c > 0);
+                        ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
+                        if (j == streams - 1) {
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
+                        }
                     }
                 }
             }
-            if (leader) {
-                ptx::umma_commit(bar(sh->o_done[s]));
-                if (free) release(v_pos<NB>(i, n));
-            }
-        };
-        for (int i = 0; ok && i <= n; ++i) {
-            if (i < n) arrived(k_pos<NB>(i));
-            if (both && i > 0) arrived(v_pos<NB>(i - 1, n));
-            const int turns = both ? 2 : 1;
+            const int o = i - lag;
+            if (ok && o >= 0) {
+                uint64_t vd[NB];
+                uint32_t free[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    ok = ok && B.warp_wait(v_full + 8 * vp.slot, vp.phase);
+                    // (64 components: the second half of the 128 rows is whatever lies behind, and is not read)
+                    vd[nb] = ptx::sdesc_sw128(v_ring + static_cast<uint32_t>(vp.slot) * S::SLOT, BLOCK_BYTES, 1024);
+                    free[nb] = v_full + to_empty + 8 * vp.slot;
+                    vp.next(S::V_SLOTS);
+                }
 #pragma unroll 1
-            for (int j = 0; j < turns; ++j) {
-                // alternate tiles: scores of this tile for one stream, outputs of the one before for
-                // the other; both: the next scores of a stream first, it waits for them
-                const int s = both ? j : i & 1, so = both ? j : (i - 1) & 1;
-                if (both && i > 0) weights(s);
-                if (i < n) scores(s, i, i < 3 - turns, j == turns - 1);
-                if (i > 0) {
-                    if (!both) {
-                        arrived(v_pos<NB>(i - 1, n));
-                        weights(so);
+                for (int j = 0; ok && j < streams; ++j) {
+                    const int s = both ? j : o & 1, k = both ? o : o >> 1;
+                    // the stream's weights of the tile are formed, and its scores have been read
+                    ok = B.warp_wait(B.bar(sh->p_full[s]), p_phase >> s & 1u);
+                    p_phase ^= 1u << s;
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t idesc = ptx::idesc_bf16_f32(128, s ? width1 : width0, true, true);
+                    const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s * NB * COLS);
+                    const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
+                    const bool skip = sh->skip[s] != 0;
+                    if (leader) {
+                        // 16 keys on are 128
+                        if (!skip) {
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int c = 0; c < KEYS / 16; ++c)
+                                    ptx::umma_f16_ss(d + nb * COLS, vd[nb] + static_cast<uint64_t>(c * 128), p + static_cast<uint64_t>(c * 128),
+                                                     idesc, k > 0 || c > 0);
+                        }
+                        ptx::umma_commit(B.bar(sh->o_done[s]));
+                        if (j == streams - 1) {
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
+                        }
                     }
-                    outputs(so, i - 1, i - 1 < 3 - turns, j == turns - 1);
                 }
             }
         }
-        base = wrap<S::SLOTS>(base + 2 * n * NB);
     }
     if (!ok && leader) {
         report(a, STATUS_TIMEOUT, 2);
         // products in flight end before shared and tensor memory are given back
-        ptx::umma_commit(bar(sh->drain));
-        ptx::mbar_wait(bar(sh->drain), 0, a.wait_ns, nullptr);
+        ptx::umma_commit(B.bar(sh->drain));
+        ptx::mbar_wait(B.bar(sh->drain), 0, a.wait_ns, nullptr);
     }
 }
 
@@ -325,15 +325,16 @@ struct Stream {
     const CacheAttnArgs &a;
     Small *sh;
     const int s, warp, lane, key;   // stream; warp of it; key of a tile (TMEM lane)
-    const uint32_t scores, out, q, p;
-    uint32_t s_phase = 0, o_phase = 0;
+    const uint32_t scores0, out, q, p;
+    uint32_t scores;                // of the tile at hand
+    uint32_t s_phase = 0, o_phase = 0;  // s_phase: a bit per place
     bool failed = false;
     float2 l[4];                    // sums of the weights of 8 rows over some of the warp's keys (see add_up)
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
-          scores(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(stream * COLS)),
-          out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(2 * COLS + stream * NB * COLS)),
+          scores0(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(2 * stream * COLS)),
+          out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + O_COLUMN + static_cast<uint32_t>(stream * NB * COLS)),
           q(b.q + static_cast<uint32_t>(stream) * S::Q_BYTES), p(b.p + static_cast<uint32_t>(stream) * P_BYTES) {}
 
     __device__ bool vote(bool x) const { return ptx::barrier_or(1 + s, 128, x); }
@@ -371,16 +372,20 @@ struct Stream {
                 }
             }
         }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
+    }
+
+    __device__ void start(const Unit &u, int row0, int rows) {
         const int first = (u.row0 + row0) / a.group;
         if (key < COLS) {
             sh->m[s][key] = -INFINITY;
             sh->token[s][key] = static_cast<uint8_t>((u.row0 + row0 + min(key, max(rows, 1) - 1)) / a.group - first);
         }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) l[i] = make_float2(0.0f, 0.0f);
+        vote(false);  // references and tokens are written
     }
 
     // Lanes that share a key's line in add_up: eight rows each.
@@ -391,13 +396,16 @@ struct Stream {
     __device__ void add_up(int width) {
         const int lanes = line_lanes(width), chunk = lane & (lanes - 1), keys = 32 / lanes;
         if (8 * chunk < width) {
-            for (int k = lane / lanes; k < 32; k += keys) {
-                uint32_t w[4];
-                ptx::ld_shared_v4(p + static_cast<uint32_t>(32 * warp + k) * 128u + (static_cast<uint32_t>(chunk ^ (k & 7)) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    l[i] = ptx::add2(l[i], make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
-            }
+            for (int i = 0; i < 8; ++i)
+                if (i < lanes) {
+                    const int k = lane / lanes + i * keys;
+                    uint32_t w[4];
+                    ptx::ld_shared_v4(p + static_cast<uint32_t>(32 * warp + k) * 128u + (static_cast<uint32_t>(chunk ^ (k & 7)) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        l[j] = ptx::add2(l[j], make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)));
+                }
         }
     }
 
@@ -532,13 +540,16 @@ struct Stream {
 
     // Values that are not finite would reach rows that do not see them (0 x NaN).  Those behind the
     // sequence's end are cleared; of a tile with others the stream forms the product itself, key by key.
-    __device__ bool own_product(int pos, int at, int len, uint64_t sees, int width, bool first) {
-        for (int nb = 0; nb < NB; ++nb) failed = !B.wait_full(wrap<S::SLOTS>(pos + nb)) || failed;
+    __device__ bool own_product(uint32_t pos, int at, int len, uint64_t sees, int width, bool first) {
+        auto v_slot = [&](int nb) { return B.ring + (S::K_SLOTS + (pos + nb) % S::V_SLOTS) * S::SLOT; };
+        for (int nb = 0; nb < NB; ++nb)
+            failed = !B.wait(B.bar(sh->full[S::K_SLOTS + (pos + nb) % S::V_SLOTS]), (pos + nb) / S::V_SLOTS & 1u) || failed;
+        __syncwarp();
         bool odd = false;
         if (!failed) {
             for (int nb = 0; nb < NB; ++nb)
                 for (int b = 0; b < B.blocks(nb); ++b) {
-                    const uint32_t line = B.slot(wrap<S::SLOTS>(pos + nb)) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
+                    const uint32_t line = v_slot(nb) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
                     bool bad = false;
 #pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
@@ -569,7 +580,7 @@ struct Stream {
         for (int nb = 0; nb < NB; ++nb) {
             const int e = key;  // component nb * 128 + key: this thread's TMEM lane
             const bool have = nb * 128 + e < a.d;
-            const uint32_t v0 = B.slot(wrap<S::SLOTS>(pos + nb)) + static_cast<uint32_t>(have ? e >> 6 : 0) * BLOCK_BYTES + (e & 7) * 2;
+            const uint32_t v0 = v_slot(nb) + static_cast<uint32_t>(have ? e >> 6 : 0) * BLOCK_BYTES + (e & 7) * 2;
 #pragma unroll 1
             for (int c = 0; c * 16 < width; ++c) {
                 uint32_t o[16];
@@ -602,10 +613,11 @@ struct Stream {
         return true;
     }
 
-    // One tile: scores to weights.  k: how many this stream has done of the unit; pos: ring position of its V.
-    __device__ bool tile(const Unit &u, int row0, int rows, int width, int t, int k, int pos, bool &fresh) {
-        failed = !B.wait(ptx::smem_u32(&sh->s_full[s]), s_phase) || failed;
-        s_phase ^= 1u;
+    // One tile: scores to weights.  k: how many this stream has done of the unit; pos: of its V, counted in slots.
+    __device__ bool tile(const Unit &u, int row0, int rows, int width, int t, int k, uint32_t pos, bool &fresh) {
+        failed = !B.wait(ptx::smem_u32(&sh->s_full[s][k & 1]), s_phase >> (k & 1) & 1u) || failed;
+        s_phase ^= 1u << (k & 1);
+        scores = scores0 + static_cast<uint32_t>((k & 1) * COLS);
         __syncwarp();
         ptx::tc_fence_after();
         const int at = t * KEYS + key;
@@ -668,39 +680,64 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
     Small *sh = B.sh;
     Stream<NB, BLK> st(B, tmem, s);
     const int key = st.key;
-    int base = 0;
-    Unit u;
+    uint32_t v_pos = 0;  // slots of V so far
+    Unit u, ahead;
+    bool more = walk.next(a, ahead);
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
     auto shared = [&](uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); };
-    while (walk.next(a, u)) {
-        const int n = u.tiles;
-        const bool both = u.rows > COLS;
-        const int row0 = both ? s * COLS : 0, rows = both ? min(COLS, u.rows - row0) : u.rows;
-        const int width = (rows + 15) & ~15;
-        const int mine = both ? n : (n + 1 - s) / 2;
-        if (mine > 0) {
-            st.load_q(u, row0, rows, width);
-            st.vote(false);  // references and tokens are written
-        }
+    // A unit's rows and tiles of this stream.
+    struct Part {
+        bool both;
+        int row0, rows, width, tiles;
+    };
+    auto part = [&](const Unit &x) {
+        Part y;
+        y.both = x.rows > COLS;
+        y.row0 = y.both ? s * COLS : 0, y.rows = y.both ? min(COLS, x.rows - y.row0) : x.rows;
+        y.width = (y.rows + 15) & ~15;
+        y.tiles = y.both ? x.tiles : (x.tiles + 1 - s) / 2;
+        return y;
+    };
+    // The queries of the next unit, as soon as the scores of the one before are complete.
+    auto queries = [&] {
+        const Part y = part(ahead);
+        if (y.tiles > 0) st.load_q(ahead, y.row0, y.rows, y.width);
+    };
+    bool loaded = false;
+    while (more) {
+        if (!loaded) queries();
+        loaded = false;
+        u = ahead;
+        more = walk.next(a, ahead);
+        const Part y = part(u);
+        const int n = u.tiles, row0 = y.row0, rows = y.rows, width = y.width;
+        const bool both = y.both;
+        st.start(u, row0, rows);
         bool fresh = true, ok = true;
-        for (int k = 0; ok && k < mine; ++k) {
+#pragma unroll 1
+        for (int k = 0; ok && k < y.tiles; ++k) {
             const int i = both ? k : 2 * k + s;
-            ok = st.tile(u, row0, rows, width, u.tile0 + i, k, wrap<Shape<NB, BLK>::SLOTS>(base + v_pos<NB>(i, n)), fresh);
+            ok = st.tile(u, row0, rows, width, u.tile0 + i, k, v_pos + i * NB, fresh);
         }
-        if (ok && mine > 0) {
-            st.wait_out();
-            st.sum_l(width);
+        v_pos += n * NB;
+        if (ok && y.tiles > 0) st.wait_out();
+        if (ok && more && !st.failed && y.tiles > 0) {
+            queries();
+            loaded = true;
         }
-        base = wrap<Shape<NB, BLK>::SLOTS>(base + 2 * n * NB);
+        if (ok && y.tiles > 0) st.sum_l(width);
         if (both_vote(!ok || st.failed)) {
             // what this block would have added to cut units is counted, so that the next call finds
             // the counters at zero
             if (threadIdx.x == 0) {
                 report(a, STATUS_TIMEOUT, 3);
-                do {
+                while (true) {
                     const Pieces in = walk.pieces(u);
                     if (u.cut && atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first)) a.counters[in.first] = 0u;
-                } while (walk.next(a, u));
+                    if (!more) break;
+                    u = ahead;
+                    more = walk.next(a, ahead);
+                }
             }
             return;
         }
@@ -745,8 +782,8 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
 #pragma unroll 1
             for (int c = both ? 0 : 8 * s; c < rows; c += both ? 8 : 16) {
                 uint32_t x[8], y[8];
-                ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (own * NB + nb) * COLS + c), x);
-                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + static_cast<uint32_t>(2 * COLS + (NB + nb) * COLS + c), y);
+                ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((own * NB + nb) * COLS + c), x);
+                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((NB + nb) * COLS + c), y);
                 ptx::tmem_ld_wait(x);
                 if (two) ptx::tmem_ld_wait(y);
 #pragma unroll
@@ -796,7 +833,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             ptx::mbar_init(ptx::smem_u32(&sh->empty[i]), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&sh->s_full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh->s_full[s][0]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh->s_full[s][1]), 1);
             ptx::mbar_init(ptx::smem_u32(&sh->p_full[s]), 4);
             ptx::mbar_init(ptx::smem_u32(&sh->o_done[s]), 1);
             ptx::mbar_init(ptx::smem_u32(&sh->q_full[s]), 4);
@@ -809,7 +847,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         ptx::prefetch_tensormap(&mv);
     }
     if (warp == 8) {
-        ptx::tmem_alloc(ptx::smem_u32(&sh->tmem), S::TMEM);
+        ptx::tmem_alloc(ptx::smem_u32(&sh->tmem), TMEM);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -832,7 +870,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     __syncthreads();
     if (warp == 8) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, S::TMEM);
+        ptx::tmem_dealloc(tmem, TMEM);
     }
 }
 
