@@ -221,16 +221,16 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
 }
 
 // The output row of a unit's row.
-template <typename E>
-__device__ __forceinline__ E *out_row(const CacheAttnArgs &a, const Unit &u, int row) {
+template <typename E, typename U>
+__device__ __forceinline__ E *out_row(const CacheAttnArgs &a, const U &u, int row) {
     const int r = u.row0 + row, token = r / a.group;
     return static_cast<E *>(a.o) +
            (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
 }
 
 // Joins a cut unit's pieces; `threads` threads, `tid` of them.
-template <typename E, int ROWS>
-__device__ __forceinline__ void join(const CacheAttnArgs &a, const Unit &u, const Pieces &in, int tid, int threads) {
+template <typename E, int ROWS, typename U>
+__device__ __forceinline__ void join(const CacheAttnArgs &a, const U &u, const Pieces &in, int tid, int threads) {
     const int quads = a.d / 4;
     for (int i = tid; i < u.rows * quads; i += threads) {
         const int row = i / quads, e = (i - row * quads) * 4;

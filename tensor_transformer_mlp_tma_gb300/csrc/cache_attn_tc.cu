@@ -40,36 +40,48 @@ namespace cattn {
 constexpr int TR = CACHE_ATTN_TC_ROWS;  // rows per tile of a unit
 constexpr int KEYS = 128;
 constexpr int COLS = 64;                // rows per stream
-// Two streams of a warpgroup each, and one whose warps copy K, issue the products and copy V.
+// Two streams of a warpgroup each, and one whose warps issue the products, copy K, copy V and plan.
 constexpr int TTHREADS = 384;
 constexpr uint32_t BLOCK_BYTES = KEYS * 128;    // 128 keys of 64 components
-constexpr uint32_t Q_BLOCK_BYTES = COLS * 128;  // 64 rows of 64 components
+constexpr uint32_t Q_BLOCK_BYTES = 2 * COLS * 128;  // 128 rows (64 of each stream) of 64 components
 constexpr uint32_t P_BYTES = KEYS * 128;
 // What else a stream's weights' space holds while no product reads it: per warp and row a maximum or a
 // sum; per row the factor of the outputs, that of the other stream's, and the output's row.
 constexpr uint32_t P_WARPS = 0, P_FACTOR = 1024, P_OTHER = 1280, P_ROW = 1536;
 constexpr float RENEW = 8.0f;           // log2 above the reference
 constexpr uint32_t STATUS_TIMEOUT = 4;  // TPMLP_ERR_TIMEOUT
-constexpr uint32_t SMALL_BYTES = 1536;
+constexpr uint32_t SMALL_BYTES = 2048;
 
 // NB blocks of 128 components of a head, each a slot of BLK blocks of 64.
 template <int NB, int BLK>
 struct Shape {
     static constexpr uint32_t SLOT = BLK * BLOCK_BYTES;
     static constexpr int Q_BLOCKS = NB * BLK;
-    static constexpr uint32_t Q_BYTES = Q_BLOCKS * Q_BLOCK_BYTES;
+    static constexpr uint32_t Q_BYTES = Q_BLOCKS * Q_BLOCK_BYTES;  // of both streams
     // 227 KB less the queries, the weights, the small arrays and 1 KB for alignment
-    static constexpr int FIT = (232448 - 2 * static_cast<int>(Q_BYTES + P_BYTES) - static_cast<int>(SMALL_BYTES) - 1024) / static_cast<int>(SLOT);
+    static constexpr int FIT = (232448 - static_cast<int>(Q_BYTES + 2 * P_BYTES) - static_cast<int>(SMALL_BYTES) - 1024) / static_cast<int>(SLOT);
     static constexpr int SLOTS = FIT < 10 ? FIT : 10;
     // V waits for the weights of its tile, K for nothing
     static constexpr int K_SLOTS = SLOTS / 2, V_SLOTS = SLOTS - K_SLOTS;
     static constexpr uint32_t RING = SLOTS * SLOT;
-    static constexpr uint32_t SMEM = RING + 2 * (Q_BYTES + P_BYTES) + SMALL_BYTES + 1024;
+    static constexpr uint32_t SMEM = RING + Q_BYTES + 2 * P_BYTES + SMALL_BYTES + 1024;
 };
 constexpr uint32_t TMEM = 512;          // columns: 2 x 2 x 64 of S, 2 x NB x 64 of O
 constexpr uint32_t O_COLUMN = 4 * COLS;
 
+// A unit as the planning warp hands it to the others.  tiles = 0: there are no more.
+struct alignas(16) Job {
+    Seq s;
+    int b, head, row0, rows;
+    int tile0, tiles, cut, place;
+    int first, last, unused[2];
+};
+constexpr int JOBS = 4;
+constexpr int JOB_READERS = 11;  // warps: the streams' eight, products, copies of K and of V
+
 struct Small {
+    Job job[JOBS];
+    uint64_t job_full[JOBS], job_empty[JOBS];
     uint64_t full[10], empty[10];  // of K's slots, then V's
     uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
     float m[2][COLS];      // references (log2)
@@ -79,6 +91,7 @@ struct Small {
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
     int last;
+    int joined;            // bit per place: this block's piece of a cut unit has been counted
     volatile int abort;
 };
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
@@ -110,7 +123,7 @@ struct Block {
     __device__ int blocks(int nb) const { return min(BLK, (a.d - nb * 128 + 63) / 64); }
 };
 
-// A place in the ring of K or of V.
+// A place in a ring.
 struct Place {
     int slot = 0;
     uint32_t phase = 0;
@@ -119,9 +132,69 @@ struct Place {
     }
 };
 
+// Takes the jobs in order; all lanes of the warp.
+template <int NB, int BLK>
+struct Jobs {
+    const Block<NB, BLK> &B;
+    Place at;
+    __device__ bool get(Job &j) {
+        if (!B.warp_wait(B.bar(B.sh->job_full[at.slot]), at.phase)) return false;
+        const uint32_t from = ptx::smem_u32(&B.sh->job[at.slot]);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) ptx::ld_shared_v4(from + 4 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+        memcpy(&j, w, sizeof(j));
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(B.bar(B.sh->job_empty[at.slot]));
+        at.next(JOBS);
+        return true;
+    }
+};
+
+// ---- planning: one warp ------------------------------------------------------------------------
+// Reads the lengths and hands out the units ahead of time, so that no other warp waits for them, and
+// brings the units' queries near.
+template <int NB, int BLK>
+__device__ void plan_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk) {
+    const CacheAttnArgs &a = B.a;
+    const int lane = threadIdx.x & 31;
+    Place at;
+    Unit u = {};
+    bool more = true;
+    while (more) {
+        more = walk.next(a, u);
+        Job j = {};
+        if (more) {
+            j.s = u.s, j.b = u.b, j.head = u.head, j.row0 = u.row0, j.rows = u.rows;
+            j.tile0 = u.tile0, j.tiles = u.tiles, j.cut = u.cut, j.place = u.place;
+            if (u.cut) {
+                const Pieces in = walk.pieces(u);
+                j.first = in.first, j.last = in.last;
+            }
+            // a line for every 64 components of every row
+            const int per = (a.d + 63) / 64;
+#pragma unroll 1
+            for (int i = lane; i < u.rows * per; i += 32) {
+                const int row = i / per, r = u.row0 + row, token = r / a.group;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                         (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d +
+                                         (i - row * per) * 64;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            }
+        }
+        if (!B.warp_wait(B.bar(B.sh->job_empty[at.slot]), at.phase ^ 1u)) return;
+        if (lane == 0) {
+            B.sh->job[at.slot] = j;
+            ptx::mbar_arrive(B.bar(B.sh->job_full[at.slot]));
+        }
+        __syncwarp();
+        at.next(JOBS);
+    }
+}
+
 // ---- copies: one warp for K, one for V -----------------------------------------------------------
 template <int NB, int BLK>
-__device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool values, const CUtensorMap *map, int box) {
+__device__ void copy_role(const Block<NB, BLK> &B, bool values, const CUtensorMap *map, int box) {
     using S = Shape<NB, BLK>;
     const CacheAttnArgs &a = B.a;
     const int lane = threadIdx.x & 31;
@@ -134,62 +207,81 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
     Place at;
     uint32_t copied = 0, phases = 0;  // per slot: whether it has been copied to, and in which phase last
     bool ok = true;
-    Unit u = {};
-    // The page (as the table has it) and row of this lane's piece of a tile; row -1: no keys there.
+    Jobs<NB, BLK> jobs = {B, {}};
+    Job job = {};
+    int tile = 0;
+    // A tile: key head and sequence (none: -1), and the page (as the table has it) and row of this lane's
+    // piece; row -1: no keys there.  Looked up two tiles ahead: under load a word of the table takes as
+    // long as a tile.
     struct Piece {
-        int page, row;
+        int head, b, page, row;
     };
-    auto look = [&](int tile) {
-        Piece x = {0, -1};
-        const int key = tile * KEYS + lane * box;
-        if (lane < pieces && key < u.s.len) {
+    auto look = [&] {
+        Piece x = {-1, 0, 0, -1};
+        if (tile == job.tiles) {
+            tile = 0;
+            if (job.head >= 0 && !jobs.get(job)) {
+                ok = false;
+                job.tiles = 0;
+            }
+            if (job.tiles == 0) {
+                job.head = -1;
+                return x;
+            }
+        }
+        x.head = job.head, x.b = job.b;
+        const int key = (job.tile0 + tile) * KEYS + lane * box;
+        if (lane < pieces && key < job.s.len) {
             const unsigned n = static_cast<unsigned>(key) / page_size;
-            x.page = a.table[u.b * a.max_pages + n];
+            x.page = a.table[job.b * a.max_pages + n];
             x.row = key - static_cast<int>(n * page_size);
         }
+        ++tile;
         return x;
     };
-    while (ok && walk.next(a, u)) {
-        Piece next = look(u.tile0);
+    Piece next = {-1, 0, 0, -1}, after = next;
 #pragma unroll 1
-        for (int i = 0; ok && i < u.tiles; ++i) {
-            Piece x = next;
-            if (i + 1 < u.tiles) next = look(u.tile0 + i + 1);
-            if (x.row >= 0 && (x.page < 0 || x.page >= a.pages)) {
-                report(a, STATUS_INVALID, static_cast<uint32_t>(u.b));
-                x.page = static_cast<int>(a.pages);  // past the last page: zeros
-            }
-            const int valid = __popc(__ballot_sync(0xffffffffu, x.row >= 0));
-#pragma unroll 1
-            for (int nb = 0; nb < NB; ++nb) {
-                ok = B.warp_wait(empty0 + 8 * at.slot, at.phase ^ 1u);
-                if (!ok) break;
-                const int blocks = B.blocks(nb);
-                const uint32_t bar = full0 + 8 * at.slot, dst = ring + static_cast<uint32_t>(at.slot) * S::SLOT;
-                if (leader) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
-#pragma unroll 1
-                for (int p = 0; p < valid; p += 4) {
-                    int page[4], row[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        page[j] = __shfl_sync(0xffffffffu, x.page, p + j);
-                        row[j] = __shfl_sync(0xffffffffu, x.row, p + j);
-                    }
-                    if (leader) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (p + j < valid) {
-                                const uint32_t to = dst + static_cast<uint32_t>((p + j) * box) * 128u;
-                                ptx::tma_load_4d(to, map, bar, nb * 128, row[j], u.head, page[j]);
-                                if (BLK > 1 && blocks > 1) ptx::tma_load_4d(to + BLOCK_BYTES, map, bar, nb * 128 + 64, row[j], u.head, page[j]);
-                            }
-                    }
-                }
-                copied |= 1u << at.slot;
-                phases = (phases & ~(1u << at.slot)) | at.phase << at.slot;
-                at.next(slots);
-            }
+    for (int t = -2;; ++t) {
+        Piece x = next;
+        next = after;
+        after = look();
+        if (t < 0) continue;
+        if (!ok || x.head < 0) break;
+        if (x.row >= 0 && (x.page < 0 || x.page >= a.pages)) {
+            report(a, STATUS_INVALID, static_cast<uint32_t>(x.b));
+            x.page = static_cast<int>(a.pages);  // past the last page: zeros
         }
+        const int valid = __popc(__ballot_sync(0xffffffffu, x.row >= 0));
+#pragma unroll 1
+        for (int nb = 0; nb < NB; ++nb) {
+            ok = B.warp_wait(empty0 + 8 * at.slot, at.phase ^ 1u);
+            if (!ok) break;
+            const int blocks = B.blocks(nb);
+            const uint32_t bar = full0 + 8 * at.slot, dst = ring + static_cast<uint32_t>(at.slot) * S::SLOT;
+            if (leader) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(valid * box * blocks) * 128u);
+#pragma unroll 1
+            for (int p = 0; p < valid; p += 4) {
+                int page[4], row[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    page[j] = __shfl_sync(0xffffffffu, x.page, p + j);
+                    row[j] = __shfl_sync(0xffffffffu, x.row, p + j);
+                }
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (p + j < valid) {
+                            const uint32_t to = dst + static_cast<uint32_t>((p + j) * box) * 128u;
+                            ptx::tma_load_4d(to, map, bar, nb * 128, row[j], x.head, page[j]);
+                            if (BLK > 1 && blocks > 1) ptx::tma_load_4d(to + BLOCK_BYTES, map, bar, nb * 128 + 64, row[j], x.head, page[j]);
+                        }
+                }
+            }
+            copied |= 1u << at.slot;
+            phases = (phases & ~(1u << at.slot)) | at.phase << at.slot;
+            at.next(slots);
+        }
+        if (!ok) break;
     }
     if (!ok) {
         if (lane == 0) report(a, STATUS_TIMEOUT, 1);
@@ -200,8 +292,11 @@ __device__ void copy_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, bool val
 }
 
 // ---- products: one warp --------------------------------------------------------------------------
+// Scores run ahead of outputs, by a tile per stream: each has two places for them.  Units that both streams
+// take tile by tile have their 128 rows in one product: the tile of K or V, which is the larger
+// operand, is read from shared memory once for both.
 template <int NB, int BLK>
-__device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint32_t tmem) {
+__device__ void product_role(const Block<NB, BLK> &B, uint32_t tmem) {
     using S = Shape<NB, BLK>;
     const CacheAttnArgs &a = B.a;
     Small *sh = B.sh;
@@ -213,17 +308,26 @@ __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
     Place kp, vp;
     uint32_t q_phase = 0, p_phase = 0;  // a bit per stream
     bool ok = true;
-    Unit u;
-    // all lanes wait, one issues
-    while (ok && walk.next(a, u)) {
+    Jobs<NB, BLK> jobs = {B, {}};
+    Job u;
+    auto queries = [&](int s) {
+        ok = ok && B.warp_wait(B.bar(sh->q_full[s]), q_phase >> s & 1u);
+        q_phase ^= 1u << s;
+    };
+    // the stream's weights of a tile are formed, and its scores have been read
+    auto weights = [&](int s) {
+        ok = ok && B.warp_wait(B.bar(sh->p_full[s]), p_phase >> s & 1u);
+        p_phase ^= 1u << s;
+    };
+    while (ok && (ok = jobs.get(u)) && u.tiles > 0) {
         const int n = u.tiles;
         const bool both = u.rows > COLS;  // both streams take every tile
-        const int width0 = both ? COLS : (u.rows + 15) & ~15, width1 = both ? (u.rows - COLS + 15) & ~15 : width0;
-        // Scores run ahead of outputs by a tile per stream: each has two places for them.
-        const int streams = both ? 2 : 1, lag = both ? 1 : 2;
+        const int width = (u.rows + 15) & ~15;
+        const int lag = both ? 1 : 2;
 #pragma unroll 1
         for (int i = 0; ok && i < n + lag; ++i) {
             if (i < n) {
+                const int s = both ? 0 : i & 1, k = both ? i : i >> 1;
                 uint64_t kd[NB];
                 uint32_t free[NB];
 #pragma unroll
@@ -233,38 +337,34 @@ __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
                     free[nb] = k_full + to_empty + 8 * kp.slot;
                     kp.next(S::K_SLOTS);
                 }
-#pragma unroll 1
-                for (int j = 0; ok && j < streams; ++j) {
-                    const int s = both ? j : i & 1, k = both ? i : i >> 1;
-                    if (k == 0) {
-                        ok = B.warp_wait(B.bar(sh->q_full[s]), q_phase >> s & 1u);
-                        q_phase ^= 1u << s;
-                        if (!ok) break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, s ? width1 : width0, false, false);
-                    const uint32_t d = tmem + static_cast<uint32_t>((2 * s + (k & 1)) * COLS);
-                    const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * S::Q_BYTES, 16, 1024);
-                    if (leader) {
-                        // descriptors count 16 bytes: 16 components on are 2, 64 a block
+                if (k == 0) {
+                    queries(s);
+                    if (both) queries(1);
+                }
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, width, false, false);
+                    const uint32_t d = tmem + static_cast<uint32_t>((2 * (k & 1) + s) * COLS);
+                    const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * COLS * 128u, 16, 1024);
+                    // descriptors count 16 bytes: 16 components on are 2, 64 a block
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int c = 0; c < 4 * BLK; ++c)
-                                if (nb * 8 + c < steps)
-                                    ptx::umma_f16_ss(d, kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2),
-                                                     q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2),
-                                                     idesc, nb + c > 0);
-                        ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
-                        if (j == streams - 1) {
+                        for (int c = 0; c < 4 * BLK; ++c)
+                            if (nb * 8 + c < steps)
+                                ptx::umma_f16_ss(d, kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2),
+                                                 q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2),
+                                                 idesc, nb + c > 0);
+                    ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
+                    if (both) ptx::umma_commit(B.bar(sh->s_full[1][k & 1]));
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
-                        }
-                    }
+                    for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
                 }
             }
             const int o = i - lag;
-            if (ok && o >= 0) {
+            if (o >= 0) {
+                const int s = both ? 0 : o & 1, k = both ? o : o >> 1;
                 uint64_t vd[NB];
                 uint32_t free[NB];
 #pragma unroll
@@ -275,34 +375,30 @@ __device__ void product_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
                     free[nb] = v_full + to_empty + 8 * vp.slot;
                     vp.next(S::V_SLOTS);
                 }
-#pragma unroll 1
-                for (int j = 0; ok && j < streams; ++j) {
-                    const int s = both ? j : o & 1, k = both ? o : o >> 1;
-                    // the stream's weights of the tile are formed, and its scores have been read
-                    ok = B.warp_wait(B.bar(sh->p_full[s]), p_phase >> s & 1u);
-                    p_phase ^= 1u << s;
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t idesc = ptx::idesc_bf16_f32(128, s ? width1 : width0, true, true);
-                    const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s * NB * COLS);
-                    const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
-                    const bool skip = sh->skip[s] != 0;
-                    if (leader) {
+                weights(s);
+                if (both) weights(1);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                // streams that have formed the product themselves are left out
+                const bool skip0 = sh->skip[s] != 0, skip1 = both && sh->skip[1] != 0;
+                if (leader) {
+                    const int from = both && skip0 ? 1 : s, columns = both ? (skip0 ? width - COLS : (skip1 ? COLS : width)) : width;
+                    if (!(skip0 && (skip1 || !both))) {
+                        const uint32_t idesc = ptx::idesc_bf16_f32(128, columns, true, true);
+                        const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(from * COLS);
+                        const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(from) * P_BYTES, P_BYTES, 1024);
                         // 16 keys on are 128
-                        if (!skip) {
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
+                        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                                for (int c = 0; c < KEYS / 16; ++c)
-                                    ptx::umma_f16_ss(d + nb * COLS, vd[nb] + static_cast<uint64_t>(c * 128), p + static_cast<uint64_t>(c * 128),
-                                                     idesc, k > 0 || c > 0);
-                        }
-                        ptx::umma_commit(B.bar(sh->o_done[s]));
-                        if (j == streams - 1) {
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
-                        }
+                            for (int c = 0; c < KEYS / 16; ++c)
+                                ptx::umma_f16_ss(d + nb * 2 * COLS, vd[nb] + static_cast<uint64_t>(c * 128), p + static_cast<uint64_t>(c * 128),
+                                                 idesc, k > 0 || c > 0);
                     }
+                    ptx::umma_commit(B.bar(sh->o_done[s]));
+                    if (both) ptx::umma_commit(B.bar(sh->o_done[1]));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
                 }
             }
         }
@@ -333,9 +429,9 @@ struct Stream {
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
-          scores0(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(2 * stream * COLS)),
-          out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + O_COLUMN + static_cast<uint32_t>(stream * NB * COLS)),
-          q(b.q + static_cast<uint32_t>(stream) * S::Q_BYTES), p(b.p + static_cast<uint32_t>(stream) * P_BYTES) {}
+          scores0(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(stream * COLS)),
+          out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + O_COLUMN + static_cast<uint32_t>(stream * COLS)),
+          q(b.q + static_cast<uint32_t>(stream) * COLS * 128u), p(b.p + static_cast<uint32_t>(stream) * P_BYTES) {}
 
     __device__ bool vote(bool x) const { return ptx::barrier_or(1 + s, 128, x); }
     __device__ void wait_out() {
@@ -346,7 +442,7 @@ struct Stream {
     }
 
     // Queries of rows row0 .. row0 + rows - 1 of the unit, zeros up to `width`, as the K-major operand.
-    __device__ void load_q(const Unit &u, int row0, int rows, int width) {
+    __device__ void load_q(const Job &u, int row0, int rows, int width) {
         // two threads per row, half of its chunks of 8 components each
         const int row = key >> 1, chunks = (a.d + 15) / 16;
         const int r = u.row0 + row0 + row, token = r / a.group;
@@ -377,7 +473,7 @@ struct Stream {
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
     }
 
-    __device__ void start(const Unit &u, int row0, int rows) {
+    __device__ void start(const Job &u, int row0, int rows) {
         const int first = (u.row0 + row0) / a.group;
         if (key < COLS) {
             sh->m[s][key] = -INFINITY;
@@ -410,7 +506,7 @@ struct Stream {
     }
 
     // Bit r: row r sees this thread's key.  Rows behind the last see everything (their scores are zero).
-    __device__ uint64_t seen(const Unit &u, int row0, int rows, int at) const {
+    __device__ uint64_t seen(const Job &u, int row0, int rows, int at) const {
         const uint64_t past = rows >= 64 ? 0ull : ~0ull << rows;
         const int j = at - u.s.prefix;
         if (j < 0) return ~0ull;
@@ -524,13 +620,13 @@ struct Stream {
 #pragma unroll 1
                 for (int c = 0; c < width; c += 16) {
                     uint32_t o[16];
-                    ptx::tmem_ld_32x32b_x16(out + nb * COLS + c, o);
+                    ptx::tmem_ld_32x32b_x16(out + nb * 2 * COLS + c, o);
                     ptx::tmem_ld_wait(o);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         o[j] = __float_as_uint(__uint_as_float(o[j]) *
                                                __uint_as_float(ptx::ld_shared_u32(p + P_FACTOR + static_cast<uint32_t>(c + j) * 4u)));
-                    ptx::tmem_st_32x32b_x16(out + nb * COLS + c, o);
+                    ptx::tmem_st_32x32b_x16(out + nb * 2 * COLS + c, o);
                 }
             ptx::tmem_st_wait();
             vote(false);  // the factors have been read: the weights come to their place
@@ -588,7 +684,7 @@ struct Stream {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = 0u;
                 } else {
-                    ptx::tmem_ld_32x32b_x16(out + nb * COLS + 16 * c, o);
+                    ptx::tmem_ld_32x32b_x16(out + nb * 2 * COLS + 16 * c, o);
                     ptx::tmem_ld_wait(o);
                 }
 #pragma unroll 1
@@ -606,7 +702,7 @@ struct Stream {
                             o[j] = __float_as_uint(__uint_as_float(o[j]) + __uint_as_float(half << 16) * v);
                     }
                 }
-                ptx::tmem_st_32x32b_x16(out + nb * COLS + 16 * c, o);
+                ptx::tmem_st_32x32b_x16(out + nb * 2 * COLS + 16 * c, o);
             }
         }
         ptx::tmem_st_wait();
@@ -614,10 +710,10 @@ struct Stream {
     }
 
     // One tile: scores to weights.  k: how many this stream has done of the unit; pos: of its V, counted in slots.
-    __device__ bool tile(const Unit &u, int row0, int rows, int width, int t, int k, uint32_t pos, bool &fresh) {
+    __device__ bool tile(const Job &u, int row0, int rows, int width, int t, int k, uint32_t pos, bool &fresh) {
         failed = !B.wait(ptx::smem_u32(&sh->s_full[s][k & 1]), s_phase >> (k & 1) & 1u) || failed;
         s_phase ^= 1u << (k & 1);
-        scores = scores0 + static_cast<uint32_t>((k & 1) * COLS);
+        scores = scores0 + static_cast<uint32_t>((k & 1) * 2 * COLS);
         __syncwarp();
         ptx::tc_fence_after();
         const int at = t * KEYS + key;
@@ -675,14 +771,14 @@ struct Stream {
 };
 
 template <int NB, int BLK>
-__device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint32_t tmem, int s) {
+__device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
     const CacheAttnArgs &a = B.a;
     Small *sh = B.sh;
     Stream<NB, BLK> st(B, tmem, s);
     const int key = st.key;
     uint32_t v_pos = 0;  // slots of V so far
-    Unit u, ahead;
-    bool more = walk.next(a, ahead);
+    Jobs<NB, BLK> jobs = {B, {}};
+    Job u, ahead;
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
     auto shared = [&](uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); };
     // A unit's rows and tiles of this stream.
@@ -690,7 +786,7 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         bool both;
         int row0, rows, width, tiles;
     };
-    auto part = [&](const Unit &x) {
+    auto part = [&](const Job &x) {
         Part y;
         y.both = x.rows > COLS;
         y.row0 = y.both ? s * COLS : 0, y.rows = y.both ? min(COLS, x.rows - y.row0) : x.rows;
@@ -704,11 +800,13 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         if (y.tiles > 0) st.load_q(ahead, y.row0, y.rows, y.width);
     };
     bool loaded = false;
-    while (more) {
+    // (both streams leave together: a barrier that only one of them comes to would wait forever)
+    if (both_vote(!jobs.get(ahead))) return;
+    while (ahead.tiles > 0) {
         if (!loaded) queries();
         loaded = false;
         u = ahead;
-        more = walk.next(a, ahead);
+        st.failed = !jobs.get(ahead) || st.failed;
         const Part y = part(u);
         const int n = u.tiles, row0 = y.row0, rows = y.rows, width = y.width;
         const bool both = y.both;
@@ -721,26 +819,12 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         }
         v_pos += n * NB;
         if (ok && y.tiles > 0) st.wait_out();
-        if (ok && more && !st.failed && y.tiles > 0) {
+        if (ok && !st.failed && ahead.tiles > 0 && y.tiles > 0) {
             queries();
             loaded = true;
         }
         if (ok && y.tiles > 0) st.sum_l(width);
-        if (both_vote(!ok || st.failed)) {
-            // what this block would have added to cut units is counted, so that the next call finds
-            // the counters at zero
-            if (threadIdx.x == 0) {
-                report(a, STATUS_TIMEOUT, 3);
-                while (true) {
-                    const Pieces in = walk.pieces(u);
-                    if (u.cut && atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first)) a.counters[in.first] = 0u;
-                    if (!more) break;
-                    u = ahead;
-                    more = walk.next(a, ahead);
-                }
-            }
-            return;
-        }
+        if (both_vote(!ok || st.failed)) return;
         ptx::tc_fence_after();
         // Streams that shared the rows out by tiles are added up here.  A thread per row: factors of the
         // outputs, and where the row goes.
@@ -782,8 +866,8 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
 #pragma unroll 1
             for (int c = both ? 0 : 8 * s; c < rows; c += both ? 8 : 16) {
                 uint32_t x[8], y[8];
-                ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((own * NB + nb) * COLS + c), x);
-                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((NB + nb) * COLS + c), y);
+                ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + own) * COLS + c), x);
+                if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + 1) * COLS + c), y);
                 ptx::tmem_ld_wait(x);
                 if (two) ptx::tmem_ld_wait(y);
 #pragma unroll
@@ -805,14 +889,14 @@ __device__ void softmax_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk, uint3
         if (u.cut) __threadfence();
         both_vote(false);  // outputs, references and sums have been read
         if (u.cut) {
-            const Pieces in = walk.pieces(u);
             if (threadIdx.x == 0) {
-                sh->last = atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first);
-                if (sh->last) a.counters[in.first] = 0u;
+                sh->last = atomicAdd(a.counters + u.first, 1u) == static_cast<uint32_t>(u.last - u.first);
+                if (sh->last) a.counters[u.first] = 0u;
+                sh->joined |= 1 << u.place;
                 __threadfence();
             }
             both_vote(false);
-            if (sh->last) join<__nv_bfloat16, TR>(a, u, in, threadIdx.x, 256);
+            if (sh->last) join<__nv_bfloat16, TR>(a, u, {u.first, u.last}, threadIdx.x, 256);
         }
     }
 }
@@ -823,9 +907,9 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     using S = Shape<NB, BLK>;
     extern __shared__ uint8_t raw[];
     const uint32_t start = (ptx::smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t small_at = S::RING + 2 * (S::Q_BYTES + P_BYTES);
+    const uint32_t small_at = S::RING + S::Q_BYTES + 2 * P_BYTES;
     Small *sh = reinterpret_cast<Small *>(raw + (start - ptx::smem_u32(raw)) + small_at);
-    const Block<NB, BLK> B = {a, sh, start, start + S::RING, start + S::RING + 2 * S::Q_BYTES};
+    const Block<NB, BLK> B = {a, sh, start, start + S::RING, start + S::RING + S::Q_BYTES};
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::SLOTS; ++i) {
@@ -840,7 +924,12 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             ptx::mbar_init(ptx::smem_u32(&sh->q_full[s]), 4);
             sh->skip[s] = 0;
         }
+        for (int i = 0; i < JOBS; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sh->job_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh->job_empty[i]), JOB_READERS);
+        }
         ptx::mbar_init(ptx::smem_u32(&sh->drain), 1);
+        sh->joined = 0;
         sh->abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&mk);
@@ -857,20 +946,31 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     walk.begin(a, sh->walk);  // with a __syncthreads
     ptx::tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    if (warp < 8) {
-        softmax_role<NB, BLK>(B, walk, tmem, warp >> 2);
-    } else {
-        if (warp == 8)
-            product_role<NB, BLK>(B, walk, tmem);
-        else if (warp < 11)
-            copy_role<NB, BLK>(B, walk, warp == 10, warp == 10 ? &mv : &mk, box);
-    }
+    if (warp < 8)
+        softmax_role<NB, BLK>(B, tmem, warp >> 2);
+    else if (warp == 8)
+        product_role<NB, BLK>(B, tmem);
+    else if (warp < 11)
+        copy_role<NB, BLK>(B, warp == 10, warp == 10 ? &mv : &mk, box);
+    else
+        plan_role<NB, BLK>(B, walk);
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 8) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TMEM);
+    }
+    if (sh->abort && threadIdx.x == 0) {
+        // what this block would have added to cut units is counted, so that the next call finds the
+        // counters at zero
+        report(a, STATUS_TIMEOUT, 3);
+        Unit u;
+        while (walk.next(a, u))
+            if (u.cut && !(sh->joined >> u.place & 1)) {
+                const Pieces in = walk.pieces(u);
+                if (atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first)) a.counters[in.first] = 0u;
+            }
     }
 }
 
