@@ -25,7 +25,7 @@ namespace tpmlp {
 namespace qk {
 
 constexpr int THREADS = 256;
-constexpr int MAX_TOKENS = 4;      // tokens per block
+constexpr int WARPS = THREADS / 32;
 constexpr int MAX_D = 256;
 constexpr uint32_t STATUS_INVALID = 1;  // TPMLP_ERR_INVALID_ARG
 
@@ -195,32 +195,60 @@ __device__ __forceinline__ void store_raw(typename L::E *row, const Place &at, i
     }
 }
 
-// Amplitude times cosine and sine of every pair's angle, for `n` tokens from t0 on.
-__device__ __forceinline__ void angles(const QkArgs &a, int64_t t0, int n, float *cosines, float *sines) {
-    const int nf = a.rot / 2;
-    for (int i = threadIdx.x; i < n * nf; i += THREADS) {
-        const int tok = i / nf, f = i - tok * nf;
-        const uint64_t turn = static_cast<uint64_t>(a.position[t0 + tok]) * a.turns[f];
+// Amplitude times cosine and sine of every pair's angle at one token, by one warp.
+__device__ __forceinline__ void angles(const QkArgs &a, int64_t token, float *cosines, float *sines) {
+    const uint64_t position = static_cast<uint64_t>(a.position[token]);
+    for (int f = threadIdx.x & 31; f < a.rot / 2; f += 32) {
+        const uint64_t turn = position * a.turns[f];
         // half turns in [-1, 1)
         const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
         float s, c;
         sincospif(half, &s, &c);
-        cosines[i] = a.amplitude * c;
-        sines[i] = a.amplitude * s;
+        cosines[f] = a.amplitude * c;
+        sines[f] = a.amplitude * s;
     }
 }
 
+// What a lane's pairs are multiplied by: (u, v) -> (uu u + uv v, vu u + vv v), two pairs to a float2.
 template <int P>
-__device__ __forceinline__ void turn(float (&u)[P], float (&v)[P], const float *c, const float *s, int rotated, float sign) {
+struct Factors {
+    float2 uu[P / 2], uv[P / 2], vu[P / 2], vv[P / 2];
+};
+
+template <typename L>
+__device__ __forceinline__ bool turns_pair(const Place &at, int i) {
+    return L::VEC ? at.rotated > 0 : i < at.rotated;  // vector lanes rotate as a whole
+}
+
+template <int P>
+__device__ __forceinline__ void table_row(const float *t, float (&x)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(t + i);
+        x[i] = q.x, x[i + 1] = q.y, x[i + 2] = q.z, x[i + 3] = q.w;
+    }
+}
+
+template <typename L>
+__device__ __forceinline__ Factors<L::P> factors(const QkArgs &a, const void *gain, const Place &at, int p0, const float *cosines,
+                                                 const float *sines) {
+    constexpr int P = L::P;
+    float gu[P], gv[P], c[P], s[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) gu[i] = gv[i] = 1.0f, c[i] = 1.0f, s[i] = 0.0f;
+    if (a.norm) unpack<L>(load<L>(static_cast<const typename L::E *>(gain), at, p0, a.rot, a.interleaved), at, gu, gv);
+    if (at.rotated > 0) table_row<P>(cosines + p0, c), table_row<P>(sines + p0, s);
+    Factors<P> f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        if (i < rotated) {
-            const float ci = c[i], si = sign * s[i];
-            const float x = u[i] * ci - v[i] * si;
-            v[i] = u[i] * si + v[i] * ci;
-            u[i] = x;
-        }
+        const bool r = turns_pair<L>(at, i);
+        const float ci = r ? c[i] : 1.0f, si = r ? s[i] : 0.0f;
+        (i & 1 ? f.uu[i / 2].y : f.uu[i / 2].x) = gu[i] * ci;
+        (i & 1 ? f.uv[i / 2].y : f.uv[i / 2].x) = -gv[i] * si;
+        (i & 1 ? f.vu[i / 2].y : f.vu[i / 2].x) = gu[i] * si;
+        (i & 1 ? f.vv[i / 2].y : f.vv[i / 2].x) = gv[i] * ci;
     }
+    return f;
 }
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
@@ -228,216 +256,249 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
     return x;
 }
 
-template <typename E>
-__device__ __forceinline__ const E *head_row(const HeadRows &h, int64_t token, int head, int per_shard, int d) {
-    const int shard = head / per_shard;
-    return static_cast<const E *>(h.p) + token * h.row + shard * h.shard + static_cast<int64_t>(head - shard * per_shard) * d;
+// Heads of one array: the shard of a head by a multiplication.  inverse = ceil(2^32 / per) gives the
+// quotient of heads below 2^32 / per; there are 2^16 at most, 2^15 per shard where there are several.
+struct Shards {
+    uint32_t per, inverse;
+};
+inline Shards shards_of(int heads, int t) {
+    const uint32_t per = static_cast<uint32_t>(heads / t);
+    return {per, t == 1 || per == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + per - 1) / per)};
 }
 
-// blockIdx.x: a group of `toks` tokens; blockIdx.y: a range of `rows` head rows of each.
+template <typename E>
+__device__ __forceinline__ const E *head_row(const HeadRows &h, int64_t token, int head, const Shards &s, int d) {
+    const int shard = s.inverse == 0u ? (s.per == 1u ? head : 0) : static_cast<int>(__umulhi(static_cast<uint32_t>(head), s.inverse));
+    return static_cast<const E *>(h.p) + token * h.row + shard * h.shard + static_cast<int64_t>(head - shard * static_cast<int>(s.per)) * d;
+}
+
+// A warp takes one token's heads, 32 / lanes at a time, or with few tokens a `split`-th of them; its
+// factors stay in registers.
+struct Split {
+    int lanes;   // per head
+    int split;   // warps per token
+    Shards q, k;
+};
+
 template <typename L, bool APPEND>
-__global__ void __launch_bounds__(THREADS)
-    forward_kernel(const QkArgs a, int toks, int rows_per_block, int lanes) {
+__global__ void __launch_bounds__(THREADS) forward_kernel(const QkArgs a, const Split w) {
     using E = typename L::E;
-    extern __shared__ float table[];
-    __shared__ int64_t dst[MAX_TOKENS];
+    constexpr int P = L::P;
+    __shared__ alignas(16) float cosines[WARPS][MAX_D / 2], sines[WARPS][MAX_D / 2];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * toks;
-    const int n = static_cast<int>(min(static_cast<int64_t>(toks), a.tokens - t0));
-    const int total = a.heads + (APPEND ? 2 : 1) * a.kv_heads;
-    const int r0 = static_cast<int>(blockIdx.y) * rows_per_block, rows = min(rows_per_block, total - r0);
-    const int nf = a.rot / 2, hq = a.heads / a.t, hk = a.kv_heads / a.t;
-    const int lane = static_cast<int>(threadIdx.x) & (lanes - 1), p0 = lane * L::P;
-    const int sub = static_cast<int>(threadIdx.x) / lanes, subs = THREADS / lanes;
-    const Place at = place<L::P>(lane, a.d, a.rot, a.interleaved);
-    const int items = n * rows;
-    float *sines = table + toks * nf;
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
+    // (tokens times split is below 2^31, see split_of)
+    const uint32_t work = blockIdx.x * WARPS + warp;
+    const int64_t token = work / static_cast<uint32_t>(w.split);
+    if (token >= a.tokens) return;
+    const int part = static_cast<int>(work) - static_cast<int>(token) * w.split;
+    const int rows = a.heads + (APPEND ? 2 : 1) * a.kv_heads;
+    const int lane = static_cast<int>(threadIdx.x) & (w.lanes - 1), p0 = lane * P;
+    const int each = 32 / w.lanes, sub = (static_cast<int>(threadIdx.x) & 31) / w.lanes, step = each * w.split;
+    const Place at = place<P>(lane, a.d, a.rot, a.interleaved);
 
-    struct Item {
-        int tok, row;
-        Raw<L> x;
+    auto fetch = [&](int row) {
+        if (row < a.heads) return load<L>(head_row<E>(a.q, token, row, w.q, a.d), at, p0, a.rot, a.interleaved);
+        row -= a.heads;
+        if (!APPEND || row < a.kv_heads) return load<L>(head_row<E>(a.k, token, row, w.k, a.d), at, p0, a.rot, a.interleaved);
+        return load<L>(head_row<E>(a.v, token, row - a.kv_heads, w.k, a.d), at, p0, a.rot, a.interleaved);
     };
-    auto fetch = [&](int i, Item &it) {
-        it.tok = i / rows, it.row = r0 + i - it.tok * rows;
-        const int64_t t = t0 + it.tok;
-        const E *p = it.row < a.heads ? head_row<E>(a.q, t, it.row, hq, a.d)
-                     : !APPEND || it.row < a.heads + a.kv_heads
-                         ? head_row<E>(a.k, t, it.row - a.heads, hk, a.d)
-                         : head_row<E>(a.v, t, it.row - a.heads - a.kv_heads, hk, a.d);
-        it.x = load<L>(p, at, p0, a.rot, a.interleaved);
-    };
-    Item cur;
-    if (sub < items) fetch(sub, cur);
-    angles(a, t0, n, table, sines);
-    if (APPEND && static_cast<int>(threadIdx.x) < n) {
-        const int64_t slot = a.slot[t0 + threadIdx.x];
-        int64_t where = -1;
+    int row = part * each + sub;
+    Raw<L> x = {}, next = {};
+    if (row < rows) x = fetch(row);
+    if (row + step < rows) next = fetch(row + step);
+    if (a.rot > 0) angles(a, token, cosines[warp], sines[warp]);
+    int64_t where = -1;
+    if (APPEND) {
+        const int64_t slot = a.slot[token];
         if (slot >= a.slots) {
-            if (atomicCAS(a.status, 0u, STATUS_INVALID) == 0u) a.status[1] = static_cast<uint32_t>(t0 + threadIdx.x);
+            if (atomicCAS(a.status, 0u, STATUS_INVALID) == 0u) a.status[1] = static_cast<uint32_t>(token);
         } else if (slot >= 0) {
             where = slot / a.page_size * a.page_stride + slot % a.page_size * a.token_stride;
         }
-        dst[threadIdx.x] = where;
     }
-    __syncthreads();
-    // every lane of a warp takes part in the shuffles; `live` says whether it has a row
-    for (int i0 = 0; i0 < items; i0 += subs) {
-        const int i = i0 + sub;
-        const bool live = i < items;
-        Item next;
-        if (i + subs < items) fetch(i + subs, next);
-        const bool value = APPEND && live && cur.row >= a.heads + a.kv_heads;
-        const bool key = live && !value && cur.row >= a.heads;
-        float u[L::P], v[L::P];
-        if (live) unpack<L>(cur.x, at, u, v);
+    __syncwarp();
+    int kind = -1;  // of the factors at hand: 0 queries, 1 keys
+    Factors<P> f;
+    const float inv_d = 1.0f / static_cast<float>(a.d);
+    for (int r0 = part * each; r0 < rows; r0 += step, row += step) {
+        // two rows ahead in flight; every lane of the warp takes part in the shuffles
+        Raw<L> after = {};
+        if (row + 2 * step < rows) after = fetch(row + 2 * step);
+        const int of = row < a.heads ? 0 : (!APPEND || row < a.heads + a.kv_heads ? 1 : 2);
+        if (of < 2 && of != kind) {
+            f = factors<L>(a, of ? a.gain_k : a.gain_q, at, p0, cosines[warp], sines[warp]);
+            kind = of;
+        }
+        float u[P], v[P];
+        unpack<L>(x, at, u, v);
+        float r = 1.0f;
         if (a.norm) {
-            float sum = 0.0f;
-            if (live) {
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int j = 0; j < L::P; ++j) sum += u[j] * u[j] + v[j] * v[j];
-            }
-            const float r = rsqrtf(group_sum(sum, lanes) / static_cast<float>(a.d) + a.eps);
-            if (live && !value) {
-                float gu[L::P], gv[L::P];
-                const E *gain = static_cast<const E *>(key ? a.gain_k : a.gain_q);
-                unpack<L>(load<L>(gain, at, p0, a.rot, a.interleaved), at, gu, gv);
+            for (int i = 0; i < P; ++i) sum = ptx::fma2(make_float2(u[i], v[i]), make_float2(u[i], v[i]), sum);
+            r = rsqrtf(group_sum(sum.x + sum.y, w.lanes) * inv_d + a.eps);
+        }
+        if (row < rows) {
+            if (of == 2) {
+                if (where >= 0)
+                    store_raw<L>(static_cast<E *>(a.cache_v) + where + (row - a.heads - a.kv_heads) * a.head_stride, at, p0,
+                                 a.rot, a.interleaved, x);
+            } else {
+                const float2 rr = make_float2(r, r);
 #pragma unroll
-                for (int j = 0; j < L::P; ++j) u[j] *= r * gu[j], v[j] *= r * gv[j];
+                for (int i = 0; i < P; i += 2) {
+                    const float2 ui = make_float2(u[i], u[i + 1]), vi = make_float2(v[i], v[i + 1]);
+                    float2 x0, x1;
+                    if (L::VEC && at.rotated == 0) {  // not mixed: infinities stay where they are
+                        x0 = ptx::mul2(ptx::mul2(ui, f.uu[i / 2]), rr);
+                        x1 = ptx::mul2(ptx::mul2(vi, f.vv[i / 2]), rr);
+                    } else {
+                        x0 = ptx::mul2(ptx::fma2(ui, f.uu[i / 2], ptx::mul2(vi, f.uv[i / 2])), rr);
+                        x1 = ptx::mul2(ptx::fma2(vi, f.vv[i / 2], ptx::mul2(ui, f.vu[i / 2])), rr);
+                        if (!L::VEC) {
+                            if (i >= at.rotated) x0.x = ui.x * f.uu[i / 2].x * r, x1.x = vi.x * f.vv[i / 2].x * r;
+                            if (i + 1 >= at.rotated) x0.y = ui.y * f.uu[i / 2].y * r, x1.y = vi.y * f.vv[i / 2].y * r;
+                        }
+                    }
+                    u[i] = x0.x, u[i + 1] = x0.y, v[i] = x1.x, v[i + 1] = x1.y;
+                }
+                if (of == 0)
+                    store<L>(const_cast<E *>(head_row<E>(a.oq, token, row, w.q, a.d)), at, p0, a.rot, a.interleaved, u, v);
+                else if (!APPEND)
+                    store<L>(const_cast<E *>(head_row<E>(a.ok, token, row - a.heads, w.k, a.d)), at, p0, a.rot, a.interleaved, u, v);
+                else if (where >= 0)
+                    store<L>(static_cast<E *>(a.cache_k) + where + (row - a.heads) * a.head_stride, at, p0, a.rot, a.interleaved, u, v);
             }
         }
-        if (live) {
-            if (!value) turn<L::P>(u, v, table + cur.tok * nf + p0, sines + cur.tok * nf + p0, at.rotated, 1.0f);
-            const int64_t t = t0 + cur.tok;
-            if (!key && !value) {
-                E *o = const_cast<E *>(head_row<E>(a.oq, t, cur.row, hq, a.d));
-                store<L>(o, at, p0, a.rot, a.interleaved, u, v);
-            } else if (!APPEND) {
-                E *o = const_cast<E *>(head_row<E>(a.ok, t, cur.row - a.heads, hk, a.d));
-                store<L>(o, at, p0, a.rot, a.interleaved, u, v);
-            } else if (dst[cur.tok] >= 0) {
-                if (key)
-                    store<L>(static_cast<E *>(a.cache_k) + dst[cur.tok] + (cur.row - a.heads) * a.head_stride, at, p0,
-                             a.rot, a.interleaved, u, v);
-                else
-                    store_raw<L>(static_cast<E *>(a.cache_v) + dst[cur.tok] +
-                                     (cur.row - a.heads - a.kv_heads) * a.head_stride,
-                                 at, p0, a.rot, a.interleaved, cur.x);
-            }
-        }
-        cur = next;
+        x = next, next = after;
     }
 }
 
-// Blocks [0, q_blocks) take the queries' rows, the others the keys'; each takes groups of `toks`
-// tokens in turn, and leaves its sums of the gains' gradient in part[blockIdx.x][d].
+// Blocks [0, q_blocks) take the queries, the others the keys; each warp takes tokens in turn (or
+// parts of them) and leaves the block's sums of the gains' gradient in part[blockIdx.x][d].
 template <typename L>
-__global__ void __launch_bounds__(THREADS)
-    backward_kernel(const QkArgs a, int toks, int q_blocks, int lanes) {
+__global__ void __launch_bounds__(THREADS, 2) backward_kernel(const QkArgs a, const Split w, int q_blocks) {
     using E = typename L::E;
-    extern __shared__ float table[];
-    __shared__ float sums[THREADS / 32][MAX_D];
+    constexpr int P = L::P;
+    __shared__ alignas(16) float cosines[WARPS][MAX_D / 2], sines[WARPS][MAX_D / 2];
+    __shared__ float sums[WARPS][MAX_D];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
     const bool key = static_cast<int>(blockIdx.x) >= q_blocks;
     const int block = static_cast<int>(blockIdx.x) - (key ? q_blocks : 0);
     const int blocks = key ? static_cast<int>(gridDim.x) - q_blocks : q_blocks;
-    const int heads = key ? a.kv_heads : a.heads, per_shard = heads / a.t;
+    const int heads = key ? a.kv_heads : a.heads;
+    const Shards sh = key ? w.k : w.q;
     const HeadRows &hx = key ? a.k : a.q, &hg = key ? a.dk : a.dq, &ho = key ? a.ok : a.oq;
-    const int nf = a.rot / 2;
-    const int lane = static_cast<int>(threadIdx.x) & (lanes - 1), p0 = lane * L::P;
-    const int sub = static_cast<int>(threadIdx.x) / lanes, subs = THREADS / lanes;
-    const Place at = place<L::P>(lane, a.d, a.rot, a.interleaved);
-    float *sines = table + toks * nf;
-    float gu[L::P], gv[L::P], su[L::P], sv[L::P];
+    const int lane = static_cast<int>(threadIdx.x) & (w.lanes - 1), p0 = lane * P;
+    const int each = 32 / w.lanes, sub = (static_cast<int>(threadIdx.x) & 31) / w.lanes, step = each * w.split;
+    const Place at = place<P>(lane, a.d, a.rot, a.interleaved);
+    float gu[P], gv[P];
+    float2 su[P / 2], sv[P / 2];
 #pragma unroll
-    for (int j = 0; j < L::P; ++j) gu[j] = gv[j] = 1.0f, su[j] = sv[j] = 0.0f;
+    for (int i = 0; i < P; ++i) gu[i] = gv[i] = 1.0f;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) su[i] = sv[i] = make_float2(0.0f, 0.0f);
     if (a.norm)
         unpack<L>(load<L>(static_cast<const E *>(key ? a.gain_k : a.gain_q), at, p0, a.rot, a.interleaved), at, gu, gv);
-    const int64_t groups = (a.tokens + toks - 1) / toks;
-    for (int64_t group = block; group < groups; group += blocks) {
-        const int64_t t0 = group * toks;
-        const int n = static_cast<int>(min(static_cast<int64_t>(toks), a.tokens - t0));
-        const int items = n * heads;
-        struct Item {
-            int tok, head;
-            Raw<L> x, g;
+    const float inv_d = 1.0f / static_cast<float>(a.d);
+    struct Item {
+        Raw<L> x, g;
+    };
+    const uint32_t all = static_cast<uint32_t>(a.tokens) * w.split;
+    for (uint32_t work = block * WARPS + warp; work < all; work += blocks * WARPS) {
+        const int64_t token = work / static_cast<uint32_t>(w.split);
+        const int part = static_cast<int>(work) - static_cast<int>(token) * w.split;
+        auto fetch = [&](int row) {
+            Item it = {};
+            if (row < heads) {
+                it.g = load<L>(head_row<E>(hg, token, row, sh, a.d), at, p0, a.rot, a.interleaved);
+                if (a.norm) it.x = load<L>(head_row<E>(hx, token, row, sh, a.d), at, p0, a.rot, a.interleaved);
+            }
+            return it;
         };
-        auto fetch = [&](int i, Item &it) {
-            it.tok = i / heads, it.head = i - it.tok * heads;
-            it.g = load<L>(head_row<E>(hg, t0 + it.tok, it.head, per_shard, a.d), at, p0, a.rot, a.interleaved);
-            if (a.norm)
-                it.x = load<L>(head_row<E>(hx, t0 + it.tok, it.head, per_shard, a.d), at, p0, a.rot, a.interleaved);
-        };
-        Item cur;
-        if (sub < items) fetch(sub, cur);
-        __syncthreads();  // the table of the group before has been read
-        angles(a, t0, n, table, sines);
-        __syncthreads();
-        for (int i0 = 0; i0 < items; i0 += subs) {
-            const bool live = i0 + sub < items;
-            Item next;
-            if (i0 + sub + subs < items) fetch(i0 + sub + subs, next);
-            float u[L::P], v[L::P];
-            if (live) {
-                unpack<L>(cur.g, at, u, v);
-                turn<L::P>(u, v, table + cur.tok * nf + p0, sines + cur.tok * nf + p0, at.rotated, -1.0f);
+        int row = part * each + sub;
+        Item cur = fetch(row);
+        __syncwarp();  // the table of the token before has been read
+        if (a.rot > 0) angles(a, token, cosines[warp], sines[warp]);
+        __syncwarp();
+        float c[P], s[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) c[i] = 1.0f, s[i] = 0.0f;
+        if (at.rotated > 0) table_row<P>(cosines[warp] + p0, c), table_row<P>(sines[warp] + p0, s);
+        for (int r0 = part * each; r0 < heads; r0 += step, row += step) {
+            const Item next = fetch(row + step);
+            float u[P], v[P];
+            unpack<L>(cur.g, at, u, v);
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                if (L::VEC && at.rotated == 0) continue;
+                const float2 ui = make_float2(u[i], u[i + 1]), vi = make_float2(v[i], v[i + 1]);
+                const float2 ci = make_float2(c[i], c[i + 1]), si = make_float2(s[i], s[i + 1]);
+                const float2 x0 = ptx::fma2(ui, ci, ptx::mul2(vi, si));
+                const float2 x1 = ptx::fma2(vi, ci, ptx::mul2(ui, make_float2(-si.x, -si.y)));
+                if (L::VEC || i < at.rotated) u[i] = x0.x, v[i] = x1.x;
+                if (L::VEC || i + 1 < at.rotated) u[i + 1] = x0.y, v[i + 1] = x1.y;
             }
             if (a.norm) {
-                float xu[L::P], xv[L::P], square = 0.0f, dot = 0.0f;
-                if (live) {
-                    unpack<L>(cur.x, at, xu, xv);
+                float xu[P], xv[P];
+                unpack<L>(cur.x, at, xu, xv);
+                float2 square = make_float2(0.0f, 0.0f), dot = square;
 #pragma unroll
-                    for (int j = 0; j < L::P; ++j) {
-                        square += xu[j] * xu[j] + xv[j] * xv[j];
-                        dot += gu[j] * u[j] * xu[j] + gv[j] * v[j] * xv[j];
-                    }
+                for (int i = 0; i < P; ++i) {
+                    const float2 xi = make_float2(xu[i], xv[i]);
+                    square = ptx::fma2(xi, xi, square);
+                    dot = ptx::fma2(ptx::mul2(make_float2(u[i], v[i]), xi), make_float2(gu[i], gv[i]), dot);
                 }
-                for (int o = lanes / 2; o > 0; o >>= 1) {
-                    square += __shfl_xor_sync(0xffffffffu, square, o);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                float sq = square.x + square.y, dt = dot.x + dot.y;
+                for (int o = w.lanes / 2; o > 0; o >>= 1) {
+                    sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    dt += __shfl_xor_sync(0xffffffffu, dt, o);
                 }
-                const float inv_d = 1.0f / static_cast<float>(a.d);
-                const float r = rsqrtf(square / static_cast<float>(a.d) + a.eps);
-                const float m = r * dot * inv_d;  // mean of dy g x r
-                if (live) {
+                const float r = rsqrtf(sq * inv_d + a.eps);
+                // r (dy g - x r mean(dy g x r)) = r dy g - (r^3 mean(dy g x)) x
+                const float m = -(r * r) * (r * (dt * inv_d));
+                const float2 rr = make_float2(r, r), mm = make_float2(m, m);
+                const bool live = row < heads;
 #pragma unroll
-                    for (int j = 0; j < L::P; ++j) {
-                        const float hu = xu[j] * r, hv = xv[j] * r;
-                        su[j] += u[j] * hu, sv[j] += v[j] * hv;
-                        u[j] = r * (u[j] * gu[j] - hu * m);
-                        v[j] = r * (v[j] * gv[j] - hv * m);
+                for (int i = 0; i < P; i += 2) {
+                    const float2 ui = make_float2(u[i], u[i + 1]), vi = make_float2(v[i], v[i + 1]);
+                    const float2 xi = make_float2(xu[i], xu[i + 1]), yi = make_float2(xv[i], xv[i + 1]);
+                    if (live) {
+                        su[i / 2] = ptx::fma2(ui, ptx::mul2(xi, rr), su[i / 2]);
+                        sv[i / 2] = ptx::fma2(vi, ptx::mul2(yi, rr), sv[i / 2]);
                     }
+                    const float2 x0 = ptx::fma2(ptx::mul2(ui, make_float2(gu[i], gu[i + 1])), rr, ptx::mul2(xi, mm));
+                    const float2 x1 = ptx::fma2(ptx::mul2(vi, make_float2(gv[i], gv[i + 1])), rr, ptx::mul2(yi, mm));
+                    u[i] = x0.x, u[i + 1] = x0.y, v[i] = x1.x, v[i + 1] = x1.y;
                 }
             }
-            if (live) {
-                E *o = const_cast<E *>(head_row<E>(ho, t0 + cur.tok, cur.head, per_shard, a.d));
-                store<L>(o, at, p0, a.rot, a.interleaved, u, v);
-            }
+            if (row < heads) store<L>(const_cast<E *>(head_row<E>(ho, token, row, sh, a.d)), at, p0, a.rot, a.interleaved, u, v);
             cur = next;
         }
     }
     if (!a.norm) return;
     // lanes of a warp that hold the same components, then the block's warps in order
 #pragma unroll
-    for (int j = 0; j < L::P; ++j) {
-        for (int o = lanes; o < 32; o <<= 1) {
-            su[j] += __shfl_xor_sync(0xffffffffu, su[j], o);
-            sv[j] += __shfl_xor_sync(0xffffffffu, sv[j], o);
+    for (int i = 0; i < P / 2; ++i) {
+        for (int o = w.lanes; o < 32; o <<= 1) {
+            su[i].x += __shfl_xor_sync(0xffffffffu, su[i].x, o);
+            su[i].y += __shfl_xor_sync(0xffffffffu, su[i].y, o);
+            sv[i].x += __shfl_xor_sync(0xffffffffu, sv[i].x, o);
+            sv[i].y += __shfl_xor_sync(0xffffffffu, sv[i].y, o);
         }
     }
-    const int warp = static_cast<int>(threadIdx.x) >> 5;
-    if ((static_cast<int>(threadIdx.x) & 31) < lanes) {
+    if ((static_cast<int>(threadIdx.x) & 31) < w.lanes) {
 #pragma unroll
-        for (int j = 0; j < L::P; ++j) {
-            if (j < at.pairs) {
+        for (int i = 0; i < P; ++i) {
+            if (i < at.pairs) {
                 int ia, ib;
-                if (L::VEC && at.step == 2)
-                    ia = at.a + 2 * j, ib = ia + 1;
-                else
-                    straddle(at, j, p0, a.rot, a.interleaved, ia, ib);
-                sums[warp][ia] = su[j];
-                sums[warp][ib] = sv[j];
+                straddle(at, i, p0, a.rot, a.interleaved, ia, ib);
+                sums[warp][ia] = i & 1 ? su[i / 2].y : su[i / 2].x;
+                sums[warp][ib] = i & 1 ? sv[i / 2].y : sv[i / 2].x;
             }
         }
     }
@@ -445,7 +506,7 @@ __global__ void __launch_bounds__(THREADS)
     for (int c = threadIdx.x; c < a.d; c += THREADS) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) s += sums[w][c];
+        for (int i = 0; i < WARPS; ++i) s += sums[i][c];
         a.part[static_cast<int64_t>(blockIdx.x) * a.d + c] = s;
     }
 }
@@ -474,13 +535,14 @@ __global__ void __launch_bounds__(32 * GAIN_ROWS) gain_kernel(const QkArgs a, in
     }
 }
 
-// Blocks of the backward pass: four per SM of the 152, and no more than groups of tokens.
-constexpr int BACKWARD_BLOCKS = 608;
+// Blocks of the backward pass: two per SM of the 152, and no more than there is work for.
+constexpr int BACKWARD_BLOCKS = 304;
 
 template <typename F>
 cudaError_t dispatch(bool is_bf16, const QkArgs &a, F f) {
-    // sixteen-byte pieces of first and second members (bf16: 8 elements), eight-byte ones, or elements
-    auto fits = [&](int p) { return a.vec && a.d % (2 * p) == 0 && (a.interleaved || a.rot % (2 * p) == 0) && a.rot % 2 == 0; };
+    // Sixteen-byte pieces of first and second members (bf16: 8 elements), eight-byte ones, or elements.
+    // 8192 tokens of 64 heads of 128: 63 us with the first, 106 with the second.
+    auto fits = [&](int p) { return a.vec && a.d % (2 * p) == 0 && a.rot % (2 * p) == 0; };
     if (is_bf16) {
         if (fits(8)) return f(Lanes<__nv_bfloat16, 8, true>());
         if (fits(4)) return f(Lanes<__nv_bfloat16, 4, true>());
@@ -490,10 +552,17 @@ cudaError_t dispatch(bool is_bf16, const QkArgs &a, F f) {
     return f(Lanes<float, 4, false>());
 }
 
-int lanes_of(int d, int p) {
-    int n = 1;
-    while (n * 2 * p < d) n *= 2;
-    return n;
+// `rows` heads of each token, of which a warp takes 32 / lanes at once.  A warp per token where
+// there are 16 warps for every SM, else as many as that takes, up to a step each.
+Split split_of(const QkArgs &a, int pairs, int rows) {
+    Split w;
+    w.lanes = 1;
+    while (w.lanes * 2 * pairs < a.d) w.lanes *= 2;
+    const int each = 32 / w.lanes;
+    const int64_t steps = (rows + each - 1) / each, want = (152 * 16 + a.tokens - 1) / a.tokens;
+    w.split = static_cast<int>(want < steps ? want : steps);
+    w.q = shards_of(a.heads, a.t), w.k = shards_of(a.kv_heads, a.t);
+    return w;
 }
 
 }  // namespace qk
@@ -505,16 +574,10 @@ int64_t qk_partial_floats(int64_t tokens, int d) {
 cudaError_t launch_qk_forward(bool is_bf16, const QkArgs &a, bool append, cudaStream_t st) {
     return qk::dispatch(is_bf16, a, [&](auto L) {
         using Ln = decltype(L);
-        const int lanes = qk::lanes_of(a.d, Ln::P), subs = qk::THREADS / lanes;
-        const int rows = a.heads + (append ? 2 : 1) * a.kv_heads;
-        // Many tokens: four per block, so that a thread computes about one sine; few: a row per
-        // group of lanes, over as many blocks as that takes.
-        const int toks = a.tokens * rows >= 152LL * 8 * subs ? qk::MAX_TOKENS : 1;
-        const int per = toks > 1 ? rows : (rows < subs ? rows : subs);
-        const dim3 grid(static_cast<unsigned>((a.tokens + toks - 1) / toks), static_cast<unsigned>((rows + per - 1) / per));
-        const size_t smem = static_cast<size_t>(toks) * a.rot * sizeof(float);
-        return append ? launch_pdl(qk::forward_kernel<Ln, true>, grid, qk::THREADS, smem, st, a, toks, per, lanes)
-                      : launch_pdl(qk::forward_kernel<Ln, false>, grid, qk::THREADS, smem, st, a, toks, per, lanes);
+        const qk::Split w = qk::split_of(a, Ln::P, a.heads + (append ? 2 : 1) * a.kv_heads);
+        const dim3 grid(static_cast<unsigned>((a.tokens * w.split + qk::WARPS - 1) / qk::WARPS));
+        return append ? launch_pdl(qk::forward_kernel<Ln, true>, grid, qk::THREADS, 0, st, a, w)
+                      : launch_pdl(qk::forward_kernel<Ln, false>, grid, qk::THREADS, 0, st, a, w);
     });
 }
 
@@ -522,17 +585,17 @@ cudaError_t launch_qk_backward(bool is_bf16, const QkArgs &a, cudaStream_t st, i
     *launches = 0;
     return qk::dispatch(is_bf16, a, [&](auto L) {
         using Ln = decltype(L);
-        const int lanes = qk::lanes_of(a.d, Ln::P), subs = qk::THREADS / lanes;
-        const int rows = a.heads + a.kv_heads;
-        const int toks = a.tokens * rows >= 152LL * 8 * subs ? qk::MAX_TOKENS : 1;
-        const int64_t groups = (a.tokens + toks - 1) / toks;
+        // queries and keys have warps of their own
+        const qk::Split w = qk::split_of(a, Ln::P, a.heads > a.kv_heads ? a.heads : a.kv_heads);
+        const int64_t most = (a.tokens * w.split + qk::WARPS - 1) / qk::WARPS;
         // blocks in proportion to the rows
-        int64_t nq = qk::BACKWARD_BLOCKS * static_cast<int64_t>(a.heads) / rows, nk = qk::BACKWARD_BLOCKS - nq;
-        nq = nq < groups ? nq : groups;
-        nk = nk < groups ? nk : groups;
-        const size_t smem = static_cast<size_t>(toks) * a.rot * sizeof(float);
-        cudaError_t e = launch_pdl(qk::backward_kernel<Ln>, dim3(static_cast<unsigned>(nq + nk)), qk::THREADS, smem, st, a,
-                                   toks, static_cast<int>(nq), lanes);
+        int64_t nq = qk::BACKWARD_BLOCKS * static_cast<int64_t>(a.heads) / (a.heads + a.kv_heads);
+        nq = nq < 1 ? 1 : (nq > qk::BACKWARD_BLOCKS - 1 ? qk::BACKWARD_BLOCKS - 1 : nq);
+        int64_t nk = qk::BACKWARD_BLOCKS - nq;
+        nq = nq < most ? nq : most;
+        nk = nk < most ? nk : most;
+        cudaError_t e = launch_pdl(qk::backward_kernel<Ln>, dim3(static_cast<unsigned>(nq + nk)), qk::THREADS, 0, st, a, w,
+                                   static_cast<int>(nq));
         if (e != cudaSuccess) return e;
         ++*launches;
         if (!a.norm) return e;
