@@ -443,7 +443,7 @@ typedef struct {
 } tpmlp_qk_shape;
 
 /* Heads of T tokens: component e of head j of shard i of token r is p[r * row + i * shard + j * dim + e]
- * (elements; each shard has heads/t, or kv_heads/t, of them).  Q inside the attention block's QKV [T, 3h]:
+ * (elements; each shard has heads/t, or kv_heads/t, of them; shards are at most 2^27 apart).  Q inside the attention block's QKV [T, 3h]:
  * {QKV, 3h, 3h/t}, K {QKV + h/t, 3h, 3h/t}; a dense [T, heads, dim] array: {Q, heads*dim, heads/t*dim}. */
 typedef struct {
     void *p;

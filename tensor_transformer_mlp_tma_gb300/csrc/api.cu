@@ -1879,7 +1879,7 @@ struct HeadSpan {
     uintptr_t end() const { return begin() + static_cast<uintptr_t>(elements() * esz); }
     // No two heads share an element, and nothing wraps around.
     bool sound() const {
-        if (shards > 1 && (h->shard < width || h->shard > (1LL << 40))) return false;
+        if (shards > 1 && (h->shard < width || h->shard > (1LL << 27))) return false;
         const int64_t row = (shards - 1) * (shards > 1 ? h->shard : 0) + width;
         return rows <= 1 || (h->row >= row && h->row <= (1LL << 40));
     }
