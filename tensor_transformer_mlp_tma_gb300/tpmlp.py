@@ -475,12 +475,14 @@ def _same_device(ctx, *tensors):
 # The current stream's handle without a Stream object around it, where this PyTorch has it
 # (a tenth of the time, and calls on small inputs are bound by the host).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# A context's workspace exists, so CUDA is up: the current device without a check for that.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(ctx, fn, name, args, stream):
     """fn(*args, stream) with the context's device as the current one."""
     index = ctx.workspace.device.index
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             _check(fn(*args, _stream(stream)), name)
     elif stream is None and _raw_stream is not None:
@@ -660,79 +662,91 @@ class QkContext:
             raise ValueError("rope table on %s, the context's workspace on %s" % (rope.turns.device, self.workspace.device))
         self._turns = rope.turns.data_ptr() if rope else None
         self._saved = None
-        # the C ABI's records, filled in at every call
-        self._records = [Heads() for _ in range(6)]
+        # the C ABI's records, filled in at every call: Q, K, V, two outputs, two gradients
+        self._records = [Heads() for _ in range(7)]
         self._refs = [ctypes.byref(r) for r in self._records]
         self._shape_ref = ctypes.byref(self.shape)
+        s = self.shape
+        self._tokens, self._heads, self._kv_heads, self._dim = s.tokens, s.heads, s.kv_heads, s.dim
+        self._q_width, self._k_width = s.heads // s.t * s.dim, s.kv_heads // s.t * s.dim  # of a shard
+        self._qkv_shape = (s.tokens, s.t * (self._q_width + 2 * self._k_width))
+        self._rot, self._norm, self._device = s.rot, s.norm, self.workspace.device
+
+
+def _on_device(ctx, x, name):
+    if x.dtype is not ctx.dtype or not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor of %s" % (name, ctx.dtype))
+    if x.device != ctx._device:
+        raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx._device))
 
 
 def _dense_heads(ctx, record, x, heads, name):
     """A [tokens, heads, dim] tensor whose heads follow one another; its rows may be apart."""
-    s = ctx.shape
-    if not x.is_cuda or x.dtype is not ctx.dtype:
-        raise ValueError("%s must be a CUDA tensor of %s" % (name, ctx.dtype))
-    if tuple(x.shape) != (s.tokens, heads, s.dim):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), (s.tokens, heads, s.dim)))
-    if x.numel() and ((s.dim > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != s.dim)):
+    _on_device(ctx, x, name)
+    if x.shape != (ctx._tokens, heads, ctx._dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), (ctx._tokens, heads, ctx._dim)))
+    row, head, one = x.stride()
+    if (one != 1 or (heads > 1 and head != ctx._dim)) and x.numel():
         raise ValueError("%s: a token's heads must be contiguous" % name)
-    if x.device != ctx.workspace.device:
-        raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
-    record.p, record.row, record.shard = x.data_ptr(), x.stride(0), heads // s.t * s.dim
+    record.p, record.row = x.data_ptr(), row
+    record.shard = ctx._q_width if heads == ctx._heads else ctx._k_width
 
 
 def _qkv_heads(ctx, records, x, name):
-    """Q, K and V inside a projection's array, into three records."""
-    s = ctx.shape
-    n, m = s.heads // s.t * s.dim, s.kv_heads // s.t * s.dim
-    width = s.t * (n + 2 * m)
-    if not x.is_cuda or x.dtype is not ctx.dtype:
-        raise ValueError("%s must be a CUDA tensor of %s" % (name, ctx.dtype))
-    if tuple(x.shape) != (s.tokens, width):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), (s.tokens, width)))
-    if x.numel() and x.stride(1) != 1:
+    """Q, K and V (three records) or Q and K (two) inside a projection's array."""
+    _on_device(ctx, x, name)
+    if x.shape != ctx._qkv_shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(x.shape), ctx._qkv_shape))
+    row, one = x.stride()
+    if one != 1 and x.numel():
         raise ValueError("%s: a token's columns must be contiguous" % name)
-    if x.device != ctx.workspace.device:
-        raise ValueError("tensor on %s, the context's workspace on %s" % (x.device, ctx.workspace.device))
-    p, row, e = x.data_ptr(), x.stride(0), x.element_size()
-    for r, off in zip(records, (0, n, n + m)):
-        r.p, r.row, r.shard = p + off * e, row, n + 2 * m
+    p, e, n, m = x.data_ptr(), 2 if ctx.dtype is torch.bfloat16 else 4, ctx._q_width, ctx._k_width
+    shard, off = n + 2 * m, 0
+    for r in records:
+        r.p, r.row, r.shard = p + off * e, row, shard
+        off = off + m if off else n
 
 
 def _qkv_input(ctx, QKV, values):
-    s = ctx.shape
     if isinstance(QKV, torch.Tensor):
-        _qkv_heads(ctx, ctx._records[:3], QKV, "QKV")
+        _qkv_heads(ctx, ctx._records[:3 if values else 2], QKV, "QKV")
         return
     if len(QKV) < (3 if values else 2):
         raise ValueError("Q, K%s expected" % (" and V" if values else ""))
-    for r, x, n, name in zip(ctx._records, QKV, (s.heads, s.kv_heads, s.kv_heads), ("Q", "K", "V")):
+    for r, x, n, name in zip(ctx._records, QKV, (ctx._heads, ctx._kv_heads, ctx._kv_heads), ("Q", "K", "V")):
         _dense_heads(ctx, r, x, n, name)
 
 
 def _qk_inputs(ctx, position, gain_q, gain_k):
-    s = ctx.shape
-    if s.rot:
-        _need(position, "position", torch.int64, (s.tokens,))
+    p = q = k = None
+    if ctx._rot:
+        _need(position, "position", torch.int64, (ctx._tokens,))
         _same_device(ctx, position)
-    if s.norm:
-        _need(gain_q, "gain_q", ctx.dtype, (s.dim,))
-        _need(gain_k, "gain_k", ctx.dtype, (s.dim,))
+        p = position.data_ptr()
+    if ctx._norm:
+        _need(gain_q, "gain_q", ctx.dtype, (ctx._dim,))
+        _need(gain_k, "gain_k", ctx.dtype, (ctx._dim,))
         _same_device(ctx, gain_q, gain_k)
-    return (gain_q.data_ptr() if s.norm else None, gain_k.data_ptr() if s.norm else None,
-            position.data_ptr() if s.rot else None, ctx._turns)
+        q, k = gain_q.data_ptr(), gain_k.data_ptr()
+    return q, k, p, ctx._turns
 
 
-def _qk_out(ctx, out, records, names):
+def _new_heads(ctx, record, heads):
+    x = torch.empty((ctx._tokens, heads, ctx._dim), dtype=ctx.dtype, device=ctx._device)
+    record.p, record.row = x.data_ptr(), heads * ctx._dim
+    record.shard = ctx._q_width if heads == ctx._heads else ctx._k_width
+    return x
+
+
+def _qk_out(ctx, out, names):
     """The output's records; without one, dense tensors."""
-    s = ctx.shape
-    if isinstance(out, torch.Tensor):
-        _qkv_heads(ctx, records, out, "out")
-        return out
+    records = ctx._records
     if out is None:
-        dev = ctx.workspace.device
-        out = (torch.empty((s.tokens, s.heads, s.dim), dtype=ctx.dtype, device=dev),
-               torch.empty((s.tokens, s.kv_heads, s.dim), dtype=ctx.dtype, device=dev))
-    for r, x, n, name in zip(records, out, (s.heads, s.kv_heads), names):
+        return _new_heads(ctx, records[3], ctx._heads), _new_heads(ctx, records[4], ctx._kv_heads)
+    if isinstance(out, torch.Tensor):
+        _qkv_heads(ctx, records[3:5], out, "out")
+        return out
+    for r, x, n, name in zip(records[3:5], out, (ctx._heads, ctx._kv_heads), names):
         _dense_heads(ctx, r, x, n, name)
     return tuple(out)
 
@@ -742,15 +756,15 @@ def qk_forward(ctx: QkContext, QKV, position, gain_q=None, gain_k=None, out=None
     out: a tuple of [tokens, heads, dim] tensors, or an array laid out as QKV whose Q and K columns are
     written (QKV itself: in place) and which is then returned.  QKV, position and gains are kept, not
     copied, for qk_backward: they have to hold the same values then."""
-    records = ctx._records
     _qkv_input(ctx, QKV, False)
     given = _qk_inputs(ctx, position, gain_q, gain_k)
-    spare = Heads()
-    result = _qk_out(ctx, out, (records[3], records[4], spare), ("Qr", "Kr"))
-    r = ctx._refs
+    result = _qk_out(ctx, out, ("Qr", "Kr"))
+    r, records = ctx._refs, ctx._records
     _call(ctx, lib.tpmlp_qk_forward, "tpmlp_qk_forward", (ctx._shape_ref, r[0], r[1], *given, r[3], r[4]), stream)
-    kept = not (ctx.shape.norm and ctx.shape.tokens) or (records[0].p != records[3].p and records[1].p != records[4].p)
-    ctx._saved = (QKV if kept else None, position, gain_q, gain_k)
+    q, k = records[0], records[1]
+    kept = not (ctx._norm and ctx._tokens) or (q.p != records[3].p and k.p != records[4].p)
+    # the tensors are kept so that what the records point to stays
+    ctx._saved = ((QKV, position, gain_q, gain_k), (q.p, q.row, q.shard), (k.p, k.row, k.shard), given) if kept else ()
     return result
 
 
@@ -760,31 +774,31 @@ def qk_backward(ctx: QkContext, dQr, dKr, out=None, dgain_q=None, dgain_k=None, 
     what holds dQr and dKr.  The gains' entries are None without the norm."""
     if ctx._saved is None:
         raise ValueError("qk_backward needs a qk_forward of the same context before it")
-    QKV, position, gain_q, gain_k = ctx._saved
-    if QKV is None:
+    if not ctx._saved:
         raise ValueError("qk_backward after a qk_forward with the norm in place: its inputs are gone")
-    s = ctx.shape
+    _, q, k, given = ctx._saved
     records, r = ctx._records, ctx._refs
-    _qkv_input(ctx, QKV, False)
-    given = _qk_inputs(ctx, position, gain_q, gain_k)
-    grads = (Heads(), Heads())
-    _dense_heads(ctx, grads[0], dQr, s.heads, "dQr")
-    _dense_heads(ctx, grads[1], dKr, s.kv_heads, "dKr")
-    spare = Heads()
-    result = _qk_out(ctx, out, (records[3], records[4], spare), ("dQ", "dK"))
-    if s.norm:
+    records[0].p, records[0].row, records[0].shard = q
+    records[1].p, records[1].row, records[1].shard = k
+    _dense_heads(ctx, records[5], dQr, ctx._heads, "dQr")
+    _dense_heads(ctx, records[6], dKr, ctx._kv_heads, "dKr")
+    result = _qk_out(ctx, out, ("dQ", "dK"))
+    to_q = to_k = None
+    if ctx._norm:
         if dgain_q is None:
-            dgain_q = torch.empty((s.dim,), dtype=ctx.dtype, device=dQr.device)
+            dgain_q = torch.empty((ctx._dim,), dtype=ctx.dtype, device=ctx._device)
+        else:
+            _need(dgain_q, "dgain_q", ctx.dtype, (ctx._dim,))
         if dgain_k is None:
-            dgain_k = torch.empty((s.dim,), dtype=ctx.dtype, device=dQr.device)
-        _need(dgain_q, "dgain_q", ctx.dtype, (s.dim,))
-        _need(dgain_k, "dgain_k", ctx.dtype, (s.dim,))
+            dgain_k = torch.empty((ctx._dim,), dtype=ctx.dtype, device=ctx._device)
+        else:
+            _need(dgain_k, "dgain_k", ctx.dtype, (ctx._dim,))
         _same_device(ctx, dgain_q, dgain_k)
+        to_q, to_k = dgain_q.data_ptr(), dgain_k.data_ptr()
     else:
         dgain_q = dgain_k = None
     _call(ctx, lib.tpmlp_qk_backward, "tpmlp_qk_backward",
-          (ctx._shape_ref, r[0], r[1], *given, ctypes.byref(grads[0]), ctypes.byref(grads[1]), r[3], r[4],
-           _ptr(dgain_q), _ptr(dgain_k), ctx.workspace.data_ptr()), stream)
+          (ctx._shape_ref, r[0], r[1], *given, r[5], r[6], r[3], r[4], to_q, to_k, ctx.workspace.data_ptr()), stream)
     grads = {"dgain_q": dgain_q, "dgain_k": dgain_k}
     if isinstance(result, torch.Tensor):
         grads["dQKV"] = result
@@ -819,21 +833,22 @@ class KvCache:
         pages, kv_heads, page_size, dim = K.shape
         self.shape = KvCacheShape(K.data_ptr(), V.data_ptr(), pages, page_size, K.stride(0), K.stride(1), K.stride(2),
                                   kv_heads, dim, _DTYPES[K.dtype])
+        self.kv_heads, self.dim = kv_heads, dim
         self._ref = ctypes.byref(self.shape)
 
 
 def kv_append(ctx: QkContext, cache: KvCache, QKV, position, slot, gain_q=None, gain_k=None, out=None, stream=None):
     """Puts the tokens' keys (normed, rotated) and values at slot [tokens] (int64: page * page_size + row; negative: not
     kept) of the cache, and returns their queries, normed and rotated, [tokens, heads, dim] (`out`, where given)."""
-    s = ctx.shape
-    records, r = ctx._records, ctx._refs
     _qkv_input(ctx, QKV, True)
     given = _qk_inputs(ctx, position, gain_q, gain_k)
-    _need(slot, "slot", torch.int64, (s.tokens,))
+    _need(slot, "slot", torch.int64, (ctx._tokens,))
     _same_device(ctx, slot, cache.K)
     if out is None:
-        out = torch.empty((s.tokens, s.heads, s.dim), dtype=ctx.dtype, device=slot.device)
-    _dense_heads(ctx, records[3], out, s.heads, "out")
+        out = _new_heads(ctx, ctx._records[3], ctx._heads)
+    else:
+        _dense_heads(ctx, ctx._records[3], out, ctx._heads, "out")
+    r = ctx._refs
     _call(ctx, lib.tpmlp_kv_append, "tpmlp_kv_append",
           (ctx._shape_ref, cache._ref, r[0], r[1], r[2], *given, slot.data_ptr(), r[3], ctx.workspace.data_ptr()), stream)
     return out
@@ -858,6 +873,7 @@ class CacheAttnContext:
             raise ValueError("invalid shape (tokens=%d batch=%d heads=%d kv_heads=%d dim=%d scale=%g)"
                              % (tokens, batch, heads, kv_heads, dim, self.shape.scale))
         self.dtype, self.kv_heads, self.dim = dtype, int(kv_heads), int(dim)
+        self._tokens, self._batch, self._heads = int(tokens), int(batch), int(heads)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         self.workspace[:4096].zero_()
         self._ref = ctypes.byref(self.shape)
@@ -868,23 +884,24 @@ def cache_attention(ctx: CacheAttnContext, cache: KvCache, Q, q_start, kv_len, p
     tokens q_start[b] .. q_start[b+1] - 1 and kv_len[b] keys in the pages page_table[b] (all int32); its new tokens are the
     last of those keys, and each sees the keys before them, and of the new ones those up to itself, or with tree
     [tokens, words] (int64) those whose bit is set."""
-    s = ctx.shape
-    if cache.dtype is not ctx.dtype or cache.shape.kv_heads != ctx.kv_heads or cache.shape.dim != ctx.dim:
+    if cache.dtype is not ctx.dtype or cache.kv_heads != ctx.kv_heads or cache.dim != ctx.dim:
         raise ValueError("the cache has %s, %d heads of %d; the context %s, %d of %d"
-                         % (cache.dtype, cache.shape.kv_heads, cache.shape.dim, ctx.dtype, ctx.kv_heads, ctx.dim))
-    _need(Q, "Q", ctx.dtype, (s.tokens, s.heads, ctx.dim))
-    _need(q_start, "q_start", torch.int32, (s.batch + 1,))
-    _need(kv_len, "kv_len", torch.int32, (s.batch,))
+                         % (cache.dtype, cache.kv_heads, cache.dim, ctx.dtype, ctx.kv_heads, ctx.dim))
+    s, T, batch, shape = ctx.shape, ctx._tokens, ctx._batch, (ctx._tokens, ctx._heads, ctx.dim)
+    _need(Q, "Q", ctx.dtype, shape)
+    _need(q_start, "q_start", torch.int32, (batch + 1,))
+    _need(kv_len, "kv_len", torch.int32, (batch,))
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, pages]")
-    _need(page_table, "page_table", torch.int32, (s.batch, page_table.shape[1]))
+    _need(page_table, "page_table", torch.int32, (batch, page_table.shape[1]))
     if tree is not None:
         if tree.dim() != 2 or tree.shape[1] == 0:
             raise ValueError("tree must be [tokens, words] with a word at least")
-        _need(tree, "tree", torch.int64, (s.tokens, tree.shape[1]))
+        _need(tree, "tree", torch.int64, (T, tree.shape[1]))
     if O is None:
         O = torch.empty_like(Q)
-    _need(O, "O", ctx.dtype, (s.tokens, s.heads, ctx.dim))
+    else:
+        _need(O, "O", ctx.dtype, shape)
     _same_device(ctx, Q, q_start, kv_len, page_table, tree, O, cache.K)
     s.max_pages, s.tree_words = page_table.shape[1], 0 if tree is None else tree.shape[1]
     _call(ctx, lib.tpmlp_cache_attn, "tpmlp_cache_attn",
