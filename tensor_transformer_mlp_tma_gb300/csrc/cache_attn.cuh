@@ -111,6 +111,13 @@ struct Pieces {
     int first, last;
 };
 
+// x y / z for z > 0: most work has fewer than 2^32 / blocks tiles, for which 32 bits do.
+__device__ __forceinline__ int64_t share(int64_t x, int64_t y, int64_t z) {
+    const uint64_t product = static_cast<uint64_t>(x) * static_cast<uint64_t>(y);
+    if ((product >> 32) == 0 && (z >> 32) == 0) return static_cast<uint32_t>(product) / static_cast<uint32_t>(z);
+    return static_cast<int64_t>(product / static_cast<uint64_t>(z));
+}
+
 // A block's share of the work.
 template <int ROWS, int KEYS>
 struct Walk {
@@ -151,7 +158,7 @@ struct Walk {
         blocks = static_cast<int>(total < gridDim.x ? total : gridDim.x);
         const int64_t c = blockIdx.x;
         pos = end = 0;
-        if (c < blocks) pos = c * total / blocks, end = (c + 1) * total / blocks;
+        if (c < blocks) pos = share(c, total, blocks), end = share(c + 1, total, blocks);
         int64_t at = before + scan - mine;
         if (tid < 256 && at <= pos && pos < at + mine && pos < end) {
             // the sequence, key head, rows and tile at pos
@@ -161,7 +168,7 @@ struct Walk {
                 if (pos < at + cost) {
                     int64_t off = pos - at;
                     sh.b = i;
-                    sh.head = static_cast<int>(off / ph);
+                    sh.head = static_cast<int>(share(off, 1, ph));
                     off -= sh.head * ph;
                     int r = 0, n;
                     while (off >= (n = T::of(a, s, r))) off -= n, ++r;
@@ -205,7 +212,12 @@ struct Walk {
     // The block c with c total / blocks <= g < (c + 1) total / blocks (whole numbers), of the first and
     // the last tile.
     __device__ Pieces pieces(const Unit &u) const {
-        return {static_cast<int>(((u.begin + 1) * blocks - 1) / total), static_cast<int>((u.end * blocks - 1) / total)};
+        // ((g + 1) blocks - 1) / total of the first tile and of the last
+        const auto of = [&](int64_t n) {
+            const int64_t x = n * blocks - 1;
+            return static_cast<int>(share(x, 1, total));
+        };
+        return {of(u.begin + 1), of(u.end)};
     }
 };
 

@@ -81,6 +81,7 @@ constexpr int JOB_READERS = 11;  // warps: the streams' eight, products, copies 
 
 struct Small {
     Job job[JOBS];
+    Job cut[2];            // units with pieces in other blocks, by place (tiles = 0: none)
     uint64_t job_full[JOBS], job_empty[JOBS];
     uint64_t full[10], empty[10];  // of K's slots, then V's
     uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
@@ -90,8 +91,8 @@ struct Small {
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
-    int last;
-    int joined;            // bit per place: this block's piece of a cut unit has been counted
+    int last[2];           // per place: this block's piece of a cut unit is the last to be counted
+    int joined;            // bit per place: it has been counted
     volatile int abort;
 };
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
@@ -137,13 +138,18 @@ template <int NB, int BLK>
 struct Jobs {
     const Block<NB, BLK> &B;
     Place at;
-    __device__ bool get(Job &j) {
+    // The next job, without taking it.
+    __device__ bool peek(Job &j) const {
         if (!B.warp_wait(B.bar(B.sh->job_full[at.slot]), at.phase)) return false;
         const uint32_t from = ptx::smem_u32(&B.sh->job[at.slot]);
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) ptx::ld_shared_v4(from + 4 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
         memcpy(&j, w, sizeof(j));
+        return true;
+    }
+    __device__ bool get(Job &j) {
+        if (!peek(j)) return false;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(B.bar(B.sh->job_empty[at.slot]));
         at.next(JOBS);
@@ -171,6 +177,15 @@ __device__ void plan_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk) {
                 const Pieces in = walk.pieces(u);
                 j.first = in.first, j.last = in.last;
             }
+        }
+        if (!B.warp_wait(B.bar(B.sh->job_empty[at.slot]), at.phase ^ 1u)) return;
+        if (lane == 0) {
+            B.sh->job[at.slot] = j;
+            ptx::mbar_arrive(B.bar(B.sh->job_full[at.slot]));
+        }
+        __syncwarp();
+        at.next(JOBS);
+        if (more) {
             // a line for every 64 components of every row
             const int per = (a.d + 63) / 64;
 #pragma unroll 1
@@ -182,13 +197,6 @@ __device__ void plan_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk) {
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
             }
         }
-        if (!B.warp_wait(B.bar(B.sh->job_empty[at.slot]), at.phase ^ 1u)) return;
-        if (lane == 0) {
-            B.sh->job[at.slot] = j;
-            ptx::mbar_arrive(B.bar(B.sh->job_full[at.slot]));
-        }
-        __syncwarp();
-        at.next(JOBS);
     }
 }
 
@@ -484,18 +492,18 @@ struct Stream {
         vote(false);  // references and tokens are written
     }
 
-    // Lanes that share a key's line in add_up: eight rows each.
-    static __device__ __forceinline__ int line_lanes(int width) { return width <= 16 ? 2 : (width <= 32 ? 4 : 8); }
+    // Lanes that share a key's line in add_up, eight rows each: 2, 4 or 8, as a power of two.
+    static __device__ __forceinline__ int line_bits(int width) { return width <= 16 ? 1 : (width <= 32 ? 2 : 3); }
 
     // Adds up the rounded weights, as the product does, from their place: a lane takes eight rows of every
     // (32 / lanes)-th key of its warp.  (Sums of all rows for its own key would be 64 registers.)
     __device__ void add_up(int width) {
-        const int lanes = line_lanes(width), chunk = lane & (lanes - 1), keys = 32 / lanes;
+        const int bits = line_bits(width), lanes = 1 << bits, chunk = lane & (lanes - 1);
         if (8 * chunk < width) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < lanes) {
-                    const int k = lane / lanes + i * keys;
+                    const int k = (lane >> bits) + (i << (5 - bits));
                     uint32_t w[4];
                     ptx::ld_shared_v4(p + static_cast<uint32_t>(32 * warp + k) * 128u + (static_cast<uint32_t>(chunk ^ (k & 7)) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
@@ -608,7 +616,7 @@ struct Stream {
         }
         const bool fresh = vote(none);
         if (more) {
-            const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & (line_lanes(width) - 1)) * 32u;
+            const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & ((1 << line_bits(width)) - 1)) * 32u;
             uint32_t f[8];
             ptx::ld_shared_v4(rows8, f[0], f[1], f[2], f[3]);
             ptx::ld_shared_v4(rows8 + 16, f[4], f[5], f[6], f[7]);
@@ -753,7 +761,7 @@ struct Stream {
 
     // The warp's sums, into the weights' space (which no product reads any more).
     __device__ void sum_l(int width) {
-        const int lanes = line_lanes(width);
+        const int lanes = (1 << line_bits(width));
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -778,7 +786,7 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
     const int key = st.key;
     uint32_t v_pos = 0;  // slots of V so far
     Jobs<NB, BLK> jobs = {B, {}};
-    Job u, ahead;
+    Job u;
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
     auto shared = [&](uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); };
     // A unit's rows and tiles of this stream.
@@ -795,18 +803,16 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         return y;
     };
     // The queries of the next unit, as soon as the scores of the one before are complete.
-    auto queries = [&] {
-        const Part y = part(ahead);
-        if (y.tiles > 0) st.load_q(ahead, y.row0, y.rows, y.width);
+    auto queries = [&](const Job &x) {
+        const Part y = part(x);
+        if (y.tiles > 0) st.load_q(x, y.row0, y.rows, y.width);
     };
-    bool loaded = false;
+    bool loaded = false, any_cut = false;
     // (both streams leave together: a barrier that only one of them comes to would wait forever)
-    if (both_vote(!jobs.get(ahead))) return;
-    while (ahead.tiles > 0) {
-        if (!loaded) queries();
+    if (both_vote(!jobs.get(u))) return;
+    while (u.tiles > 0) {
+        if (!loaded) queries(u);
         loaded = false;
-        u = ahead;
-        st.failed = !jobs.get(ahead) || st.failed;
         const Part y = part(u);
         const int n = u.tiles, row0 = y.row0, rows = y.rows, width = y.width;
         const bool both = y.both;
@@ -818,12 +824,18 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             ok = st.tile(u, row0, rows, width, u.tile0 + i, k, v_pos + i * NB, fresh);
         }
         v_pos += n * NB;
-        if (ok && y.tiles > 0) st.wait_out();
-        if (ok && !st.failed && ahead.tiles > 0 && y.tiles > 0) {
-            queries();
-            loaded = true;
+        if (ok && !st.failed && y.tiles > 0) {
+            Job ahead;
+            st.failed = !jobs.peek(ahead);
+            if (!st.failed && ahead.tiles > 0) {
+                queries(ahead);
+                loaded = true;
+            }
         }
-        if (ok && y.tiles > 0) st.sum_l(width);
+        if (ok && y.tiles > 0) {
+            st.wait_out();
+            st.sum_l(width);
+        }
         if (both_vote(!ok || st.failed)) return;
         ptx::tc_fence_after();
         // Streams that shared the rows out by tiles are added up here.  A thread per row: factors of the
@@ -886,18 +898,32 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             }
         }
         ptx::tc_fence_before();
-        if (u.cut) __threadfence();
-        both_vote(false);  // outputs, references and sums have been read
         if (u.cut) {
-            if (threadIdx.x == 0) {
-                sh->last = atomicAdd(a.counters + u.first, 1u) == static_cast<uint32_t>(u.last - u.first);
-                if (sh->last) a.counters[u.first] = 0u;
-                sh->joined |= 1 << u.place;
-                __threadfence();
-            }
-            both_vote(false);
-            if (sh->last) join<__nv_bfloat16, TR>(a, u, {u.first, u.last}, threadIdx.x, 256);
+            // at most two per block, the first unit and the last: counted together at the end, since a fence
+            // under load takes as long as several tiles
+            if (threadIdx.x == 0) sh->cut[u.place] = u;
+            any_cut = true;
         }
+        if (both_vote(!jobs.get(u))) return;  // (and outputs, references and sums have been read)
+    }
+    if (!any_cut) return;
+    if (threadIdx.x == 0) {
+        __threadfence();  // (the others' pieces are behind the barrier)
+        for (int i = 0; i < 2; ++i) {
+            const Job &c = sh->cut[i];
+            sh->last[i] = 0;
+            if (c.tiles == 0) continue;
+            sh->last[i] = atomicAdd(a.counters + c.first, 1u) == static_cast<uint32_t>(c.last - c.first);
+            if (sh->last[i]) a.counters[c.first] = 0u;
+            sh->joined |= 1 << i;
+        }
+        __threadfence();
+    }
+    both_vote(false);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const Job &c = sh->cut[i];
+        if (sh->last[i]) join<__nv_bfloat16, TR>(a, c, {c.first, c.last}, threadIdx.x, 256);
     }
 }
 
@@ -929,7 +955,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             ptx::mbar_init(ptx::smem_u32(&sh->job_empty[i]), JOB_READERS);
         }
         ptx::mbar_init(ptx::smem_u32(&sh->drain), 1);
-        sh->joined = 0;
+        sh->joined = sh->cut[0].tiles = sh->cut[1].tiles = 0;
         sh->abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&mk);
