@@ -87,7 +87,6 @@ struct Small {
     uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
     float m[2][COLS];      // references (log2)
     alignas(16) float ref[2][COLS];  // the same, 0 for a row that has seen nothing yet
-    uint8_t token[2][COLS]; // of a row, counted from the first row's token
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
@@ -138,21 +137,34 @@ template <int NB, int BLK>
 struct Jobs {
     const Block<NB, BLK> &B;
     Place at;
-    // The next job, without taking it.
-    __device__ bool peek(Job &j) const {
-        if (!B.warp_wait(B.bar(B.sh->job_full[at.slot]), at.phase)) return false;
-        const uint32_t from = ptx::smem_u32(&B.sh->job[at.slot]);
+    __device__ void read(Job &j, int slot) const {
+        const uint32_t from = ptx::smem_u32(&B.sh->job[slot]);
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) ptx::ld_shared_v4(from + 4 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
         memcpy(&j, w, sizeof(j));
+    }
+    // The job at hand (waiting for it the first time), and the one behind it.
+    __device__ bool peek(Job &j) const {
+        if (!B.warp_wait(B.bar(B.sh->job_full[at.slot]), at.phase)) return false;
+        read(j, at.slot);
         return true;
     }
-    __device__ bool get(Job &j) {
-        if (!peek(j)) return false;
+    __device__ bool peek_next(Job &j) const {
+        Place next = at;
+        next.next(JOBS);
+        if (!B.warp_wait(B.bar(B.sh->job_full[next.slot]), next.phase)) return false;
+        read(j, next.slot);
+        return true;
+    }
+    __device__ void release() {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(B.bar(B.sh->job_empty[at.slot]));
         at.next(JOBS);
+    }
+    __device__ bool get(Job &j) {
+        if (!peek(j)) return false;
+        release();
         return true;
     }
 };
@@ -454,42 +466,37 @@ struct Stream {
         // two threads per row, half of its chunks of 8 components each
         const int row = key >> 1, chunks = (a.d + 15) / 16;
         const int r = u.row0 + row0 + row, token = r / a.group;
-        const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(a.q) +
+        const __nv_bfloat16 *const from0 = static_cast<const __nv_bfloat16 *>(a.q);
+        const __nv_bfloat16 *from = from0 +
                                     (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
         if (row < width) {
-#pragma unroll 1
-            for (int i0 = 0; i0 < chunks; i0 += 8) {
-                uint4 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = 2 * (i0 + i) + (key & 1);
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (i0 + i < chunks && row < rows && c * 8 < a.d) x[i] = *reinterpret_cast<const uint4 *>(from + c * 8);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = 2 * (i0 + i) + (key & 1);
-                    if (i0 + i < chunks)
-                        ptx::st_shared_v4(q + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + static_cast<uint32_t>(row) * 128u +
-                                              (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4),
-                                          x[i].x, x[i].y, x[i].z, x[i].w);
-                }
+            const uint32_t line = q + static_cast<uint32_t>(row) * 128u;
+            const int odd = key & 1;
+#pragma unroll 4
+            for (int i = 0; i < chunks; ++i) {
+                const int c = 2 * i + odd;
+                const uint32_t have = row < rows && c * 8 < a.d ? 16u : 0u;  // 0: zeros are written
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 line + static_cast<uint32_t>(c >> 3) * Q_BLOCK_BYTES + (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4)),
+                             "l"(have ? from + c * 8 : from0), "r"(have)
+                             : "memory");
             }
         }
+    }
+
+    // They have landed.
+    __device__ void have_q() {
+        asm volatile("cp.async.wait_all;" ::: "memory");
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->q_full[s]));
     }
 
-    __device__ void start(const Job &u, int row0, int rows) {
-        const int first = (u.row0 + row0) / a.group;
-        if (key < COLS) {
-            sh->m[s][key] = -INFINITY;
-            sh->token[s][key] = static_cast<uint8_t>((u.row0 + row0 + min(key, max(rows, 1) - 1)) / a.group - first);
-        }
+    __device__ void start() {
+        if (key < COLS) sh->m[s][key] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 4; ++i) l[i] = make_float2(0.0f, 0.0f);
-        vote(false);  // references and tokens are written
+        vote(false);
     }
 
     // Lanes that share a key's line in add_up, eight rows each: 2, 4 or 8, as a power of two.
@@ -524,12 +531,17 @@ struct Stream {
             return (from <= 0 ? ~0ull : (from >= 64 ? 0ull : ~0ull << from)) | past;
         }
         if (j >= 64 * a.tree_words) return past;
-        const int64_t *words = a.tree + static_cast<int64_t>(u.s.q0 + (u.row0 + row0) / a.group) * a.tree_words + (j >> 6);
+        // token by token: `group` rows each, the first one's perhaps fewer
+        const int r0 = u.row0 + row0, first = r0 / a.group, tokens = (r0 + rows - 1) / a.group - first + 1;
+        const int64_t *words = a.tree + static_cast<int64_t>(u.s.q0 + first) * a.tree_words + (j >> 6);
         uint64_t bits = past;
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-            const uint64_t w = static_cast<uint64_t>(words[static_cast<int64_t>(sh->token[s][r]) * a.tree_words]);
-            bits |= (w >> (j & 63) & 1ull) << r;
+        int begin = first * a.group - r0;
+#pragma unroll 8
+        for (int t = 0; t < tokens; ++t, begin += a.group) {
+            const uint64_t w = static_cast<uint64_t>(words[static_cast<int64_t>(t) * a.tree_words]);
+            const int b = max(begin, 0), e = min(begin + a.group, rows);
+            const uint64_t span = (e >= 64 ? ~0ull : (1ull << e) - 1ull) & ~((1ull << b) - 1ull);
+            if (w >> (j & 63) & 1ull) bits |= span;
         }
         return bits;
     }
@@ -651,18 +663,22 @@ struct Stream {
         __syncwarp();
         bool odd = false;
         if (!failed) {
+#pragma unroll 1
             for (int nb = 0; nb < NB; ++nb)
+#pragma unroll 1
                 for (int b = 0; b < B.blocks(nb); ++b) {
                     const uint32_t line = v_slot(nb) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
-                    bool bad = false;
-#pragma unroll 2
+                    // the largest size, NaN above all
+                    __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint32_t w[4];
                         ptx::ld_shared_v4(line + static_cast<uint32_t>((c ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            bad = bad || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+                        for (int i = 0; i < 4; ++i) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
                     }
+                    const uint32_t t = *reinterpret_cast<const uint32_t *>(&top);
+                    const bool bad = (t & 0x7F80u) == 0x7F80u || (t & 0x7F800000u) == 0x7F800000u;
                     if (bad && at >= len) {
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) ptx::st_shared_v4(line + static_cast<uint32_t>(c << 4), 0u, 0u, 0u, 0u);
@@ -729,6 +745,7 @@ struct Stream {
         uint64_t sees = ~0ull;
         if (masked) {
             sees = seen(u, row0, rows, at);
+            __syncwarp();
             hide(sees, width);
         }
         uint32_t w[COLS / 2];
@@ -806,17 +823,18 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
     auto queries = [&](const Job &x) {
         const Part y = part(x);
         if (y.tiles > 0) st.load_q(x, y.row0, y.rows, y.width);
+        return y.tiles > 0;
     };
     bool loaded = false, any_cut = false;
     // (both streams leave together: a barrier that only one of them comes to would wait forever)
-    if (both_vote(!jobs.get(u))) return;
+    if (both_vote(!jobs.peek(u))) return;
     while (u.tiles > 0) {
-        if (!loaded) queries(u);
+        if (!loaded && queries(u)) st.have_q();
         loaded = false;
         const Part y = part(u);
         const int n = u.tiles, row0 = y.row0, rows = y.rows, width = y.width;
         const bool both = y.both;
-        st.start(u, row0, rows);
+        st.start();
         bool fresh = true, ok = true;
 #pragma unroll 1
         for (int k = 0; ok && k < y.tiles; ++k) {
@@ -824,11 +842,12 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             ok = st.tile(u, row0, rows, width, u.tile0 + i, k, v_pos + i * NB, fresh);
         }
         v_pos += n * NB;
+        bool coming = false;
         if (ok && !st.failed && y.tiles > 0) {
             Job ahead;
-            st.failed = !jobs.peek(ahead);
+            st.failed = !jobs.peek_next(ahead);
             if (!st.failed && ahead.tiles > 0) {
-                queries(ahead);
+                coming = queries(ahead);
                 loaded = true;
             }
         }
@@ -836,8 +855,10 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             st.wait_out();
             st.sum_l(width);
         }
+        if (coming) st.have_q();
         if (both_vote(!ok || st.failed)) return;
         ptx::tc_fence_after();
+        jobs.read(u, jobs.at.slot);  // (not kept in registers over the tiles)
         // Streams that shared the rows out by tiles are added up here.  A thread per row: factors of the
         // outputs, and where the row goes.
         const bool two = !both && n > 1;
@@ -877,22 +898,35 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             const int e = nb * 128 + key;
 #pragma unroll 1
             for (int c = both ? 0 : 8 * s; c < rows; c += both ? 8 : 16) {
-                uint32_t x[8], y[8];
+                uint32_t x[8], y[8], f[8], g[8], to[8];
                 ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + own) * COLS + c), x);
                 if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + 1) * COLS + c), y);
+                const uint32_t at = st.p + P_FACTOR + static_cast<uint32_t>(c) * 4u;
+                ptx::ld_shared_v4(at, f[0], f[1], f[2], f[3]);
+                ptx::ld_shared_v4(at + 16, f[4], f[5], f[6], f[7]);
+                ptx::ld_shared_v4(at + (P_ROW - P_FACTOR), to[0], to[1], to[2], to[3]);
+                ptx::ld_shared_v4(at + (P_ROW - P_FACTOR) + 16, to[4], to[5], to[6], to[7]);
+                if (two) {
+                    ptx::ld_shared_v4(at + (P_OTHER - P_FACTOR), g[0], g[1], g[2], g[3]);
+                    ptx::ld_shared_v4(at + (P_OTHER - P_FACTOR) + 16, g[4], g[5], g[6], g[7]);
+                }
                 ptx::tmem_ld_wait(x);
                 if (two) ptx::tmem_ld_wait(y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t at = st.p + P_FACTOR + static_cast<uint32_t>(c + j) * 4u;
-                    float v = __uint_as_float(x[j]) * shared(at);
-                    if (two) v += __uint_as_float(y[j]) * shared(at + (P_OTHER - P_FACTOR));
-                    const int64_t to = static_cast<int64_t>(static_cast<int>(ptx::ld_shared_u32(at + (P_ROW - P_FACTOR)))) * a.d + e;
-                    if (c + j < rows && e < a.d) {
-                        if (u.cut)
-                            __stcg(part + to, v);
-                        else
-                            o[to] = __float2bfloat16_rn(v);
+                    float v = __uint_as_float(x[j]) * __uint_as_float(f[j]);
+                    if (two) v += __uint_as_float(y[j]) * __uint_as_float(g[j]);
+                    x[j] = __float_as_uint(v);
+                }
+                if (e < a.d) {
+                    if (u.cut) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c + j < rows) __stcg(part + static_cast<int64_t>(static_cast<int>(to[j])) * a.d + e, __uint_as_float(x[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c + j < rows) o[static_cast<int64_t>(static_cast<int>(to[j])) * a.d + e] = __float2bfloat16_rn(__uint_as_float(x[j]));
                     }
                 }
             }
@@ -904,7 +938,8 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             if (threadIdx.x == 0) sh->cut[u.place] = u;
             any_cut = true;
         }
-        if (both_vote(!jobs.get(u))) return;  // (and outputs, references and sums have been read)
+        jobs.release();
+        if (both_vote(!jobs.peek(u))) return;  // (and outputs, references and sums have been read)
     }
     if (!any_cut) return;
     if (threadIdx.x == 0) {
