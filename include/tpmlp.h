@@ -519,8 +519,8 @@ typedef struct {
     float scale;        /* of the scores; finite */
 } tpmlp_cache_attn_shape;
 
-/* Bytes of device workspace (status word, block counters, pieces of sequences that several blocks share); 256-byte
- * aligned, first 4096 bytes zero before first use; 0 for an invalid shape.  Depends on dim only. */
+/* Bytes of device workspace (status word, pieces of sequences that several blocks share); 256-byte aligned,
+ * first 8 bytes zero before first use; 0 for an invalid shape.  Depends on dim only. */
 size_t tpmlp_cache_attn_workspace_bytes(const tpmlp_cache_attn_shape *shape, const tpmlp_kv_cache *cache);
 
 /* Q, O[T, heads, dim] of the cache's type; q_start[batch + 1], kv_len[batch], page_table[batch][max_pages] are int32 in

@@ -2015,17 +2015,18 @@ bool cache_attn_valid(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c) 
     return s->tree_words >= 0 && std::isfinite(s->scale);
 }
 
-// status (1 KB) | counters | statistics | pieces.  Room for either kernel: which one runs depends on the
+// status (1 KB) | cut units | statistics | pieces.  Room for either kernel: which one runs depends on the
 // cache's alignment.
 struct CacheAttnLayout {
-    size_t ml, part, total;
+    size_t cuts, ml, part, total;
 };
 constexpr int kCacheAttnBlocks = 160;  // tensor-core kernel: one per SM; the FFMA kernel two
 CacheAttnLayout cache_attn_layout(const tpmlp_kv_cache *c) {
     const size_t rows = std::max<size_t>(2 * kCacheAttnBlocks * tpmlp::CACHE_ATTN_TC_ROWS,
                                          4 * kCacheAttnBlocks * tpmlp::CACHE_ATTN_SIMT_ROWS);
     CacheAttnLayout L;
-    L.ml = 4096;
+    L.cuts = STATUS_BYTES;
+    L.ml = L.cuts + align_up(tpmlp::CACHE_ATTN_BLOCKS * 32, 1024);
     L.part = L.ml + align_up(rows * 8, 1024);
     L.total = L.part + align_up(rows * static_cast<size_t>(c->dim) * 4, 1024);
     return L;
@@ -2241,7 +2242,7 @@ tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *s, const tpmlp_kv_ca
     a.vec = aligned16(c->K) && aligned16(c->V) && c->page_stride * e % 16 == 0 && c->head_stride * e % 16 == 0 &&
             c->token_stride * e % 16 == 0;
     a.status = reinterpret_cast<uint32_t *>(ws);
-    a.counters = reinterpret_cast<uint32_t *>(ws + STATUS_BYTES);
+    a.cuts = ws + L.cuts;
     a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.wait_ns = g_wait_ns.load();
@@ -2251,7 +2252,7 @@ tpmlp_status tpmlp_cache_attn(const tpmlp_cache_attn_shape *s, const tpmlp_kv_ca
     const bool tc = c->dtype == TPMLP_BF16 && s->algo == TPMLP_ALGO_DEFAULT && tpmlp::cache_attn_tc(a);
     const cudaError_t r = tc ? tpmlp::launch_cache_attn_tc(a, sms, st)
                              : tpmlp::launch_cache_attn_simt(c->dtype == TPMLP_BF16, a, sms, st);
-    if (r == cudaSuccess) g_launches.fetch_add(1);
+    if (r == cudaSuccess) g_launches.fetch_add(2);
     return from_cuda(r);
 }
 

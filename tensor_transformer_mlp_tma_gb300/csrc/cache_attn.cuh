@@ -10,14 +10,17 @@
 //
 // A unit that lies in one block is written by it.  The pieces of a cut one go to the workspace as
 // (maximum, sum, unnormalised output) in fp32, two places per block: [0] for a unit that began in
-// an earlier block, [1] for one that begins in this block and goes on.  The block that finds all other
-// pieces done joins them, in the order of the keys, so that results do not depend on which one it is.
+// an earlier block, [1] for one that begins in this block and goes on.  A second kernel joins them in the order of
+// the keys, eight rows to a block: left to the
+// block that finishes last, the join of 20 pieces of 64 rows (8 sequences of 16 to 32 thousand keys) made 96 us 124.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace tpmlp {
 namespace cattn {
@@ -106,10 +109,6 @@ struct Unit {
     int64_t begin, end;   // the unit's tiles, counted among all
 };
 
-// Blocks that hold a cut unit's pieces.
-struct Pieces {
-    int first, last;
-};
 
 // x y / z for z > 0: most work has fewer than 2^32 / blocks tiles, for which 32 bits do.
 __device__ __forceinline__ int64_t share(int64_t x, int64_t y, int64_t z) {
@@ -209,16 +208,8 @@ struct Walk {
         return true;
     }
 
-    // The block c with c total / blocks <= g < (c + 1) total / blocks (whole numbers), of the first and
-    // the last tile.
-    __device__ Pieces pieces(const Unit &u) const {
-        // ((g + 1) blocks - 1) / total of the first tile and of the last
-        const auto of = [&](int64_t n) {
-            const int64_t x = n * blocks - 1;
-            return static_cast<int>(share(x, 1, total));
-        };
-        return {of(u.begin + 1), of(u.end)};
-    }
+    // The block of a cut unit's last tile: c with c total / blocks <= g < (c + 1) total / blocks (whole numbers).
+    __device__ int last_block(const Unit &u) const { return static_cast<int>(share(u.end * blocks - 1, 1, total)); }
 };
 
 __device__ __forceinline__ float scale_of(float from, float to) { return from == to ? 1.0f : exp2f(from - to); }
@@ -240,30 +231,65 @@ __device__ __forceinline__ E *out_row(const CacheAttnArgs &a, const U &u, int ro
            (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
 }
 
-// Joins a cut unit's pieces; `threads` threads, `tid` of them.
-template <typename E, int ROWS, typename U>
-__device__ __forceinline__ void join(const CacheAttnArgs &a, const U &u, const Pieces &in, int tid, int threads) {
+// A unit that begins in a block and goes on, for the kernel that joins its pieces; rows = 0: none.
+__device__ __forceinline__ void post_cut(const CacheAttnArgs &a, int q0, int head, int row0, int rows, int last) {
+    int4 *to = reinterpret_cast<int4 *>(a.cuts) + 2 * blockIdx.x;
+    to[0] = make_int4(rows, last, q0, head);
+    to[1] = make_int4(row0, 0, 0, 0);
+}
+
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 8;
+
+// blockIdx.x: the block that a unit begins in; blockIdx.y: eight of its rows.
+template <typename E, int ROWS>
+__global__ void __launch_bounds__(JOIN_THREADS, 4) join_kernel(const CacheAttnArgs a) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int4 *cut = reinterpret_cast<const int4 *>(a.cuts) + 2 * blockIdx.x;
+    const int4 c0 = __ldcg(cut);
+    const int rows = c0.x, first = blockIdx.x, last = c0.y, from = JOIN_ROWS * blockIdx.y;
+    if (from >= rows) return;
+    const int row0 = __ldcg(cut + 1).x;
     const int quads = a.d / 4;
-    for (int i = tid; i < u.rows * quads; i += threads) {
-        const int row = i / quads, e = (i - row * quads) * 4;
+    for (int i = threadIdx.x; i < min(JOIN_ROWS, rows - from) * quads; i += JOIN_THREADS) {
+        const int row = from + i / quads, e = (i % quads) * 4;
         float m = -INFINITY, l = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int c = in.first; c <= in.last; ++c) {
-            const int64_t at = (2 * static_cast<int64_t>(c) + (c == in.first ? 1 : 0)) * ROWS + row;
-            const float2 ml = __ldcg(a.part_ml + at);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part + at * a.d + e));
-            const float top = fmaxf(m, ml.x), f = scale_of(m, top), g = scale_of(ml.x, top);
-            l = l * f + ml.y * g;
-            x.x = x.x * f + y.x * g;
-            x.y = x.y * f + y.y * g;
-            x.z = x.z * f + y.z * g;
-            x.w = x.w * f + y.w * g;
-            m = top;
+        // four pieces under way at a time
+        for (int c = first; c <= last; c += 4) {
+            float2 ml[4];
+            float4 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from_block = min(c + k, last);
+                const int64_t at = (2 * static_cast<int64_t>(from_block) + (from_block == first ? 1 : 0)) * ROWS + row;
+                ml[k] = __ldcg(a.part_ml + at);
+                y[k] = __ldcg(reinterpret_cast<const float4 *>(a.part + at * a.d + e));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (c + k > last) break;
+                const float top = fmaxf(m, ml[k].x), f = scale_of(m, top), g = scale_of(ml[k].x, top);
+                l = l * f + ml[k].y * g;
+                x.x = x.x * f + y[k].x * g;
+                x.y = x.y * f + y[k].y * g;
+                x.z = x.z * f + y[k].z * g;
+                x.w = x.w * f + y[k].w * g;
+                m = top;
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing: zeros
-        put4(out_row<E>(a, u, row) + e, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+        const int r = row0 + row, token = r / a.group;
+        E *o = static_cast<E *>(a.o) + (static_cast<int64_t>(c0.z + token) * a.heads + c0.w * a.group + (r - token * a.group)) * a.d + e;
+        put4(o, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
     }
+}
+
+template <typename E, int ROWS>
+cudaError_t launch_join(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
+    const int64_t all = a.tokens * a.group, rows = all < ROWS ? all : ROWS;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((rows + JOIN_ROWS - 1) / JOIN_ROWS));
+    return launch_pdl(join_kernel<E, ROWS>, grid, JOIN_THREADS, 0, st, a);
 }
 
 }  // namespace cattn

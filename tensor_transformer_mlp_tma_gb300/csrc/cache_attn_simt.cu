@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
     extern __shared__ float4 smem4[];
     __shared__ typename Walk<SR, SK>::Shared wsh;
     __shared__ int64_t where[SK];
-    __shared__ int last_sh;
     const int d = a.d, quads = d / 4, kld = d + 4;
     float *Q = reinterpret_cast<float *>(smem4), *K = Q + SR * d, *V = K + SK * kld, *P = V + SK * d;
     float *m_sh = P + SK * P_LD, *l_sh = m_sh + SR, *f_sh = l_sh + SR;
@@ -61,6 +60,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
     // (at most 32 groups: their sums are added up in the space of K, V and P, 128 d floats and more)
     const int groups = min(STHREADS / cols, 32), col = tid & (cols - 1), group = tid / cols;
 
+    bool posted = false;
     Unit u;
     while (walk.next(a, u)) {
         const int rq = (u.rows + 3) / 4;
@@ -218,20 +218,13 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                 }
             }
         }
-        if (u.cut) {
-            if (tid < u.rows) __stcg(a.part_ml + piece + tid, make_float2(m_sh[tid], l_sh[tid]));
-            __threadfence();
-            __syncthreads();
-            const Pieces in = walk.pieces(u);
-            if (tid == 0) {
-                last_sh = atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first);
-                if (last_sh) a.counters[in.first] = 0u;
-                __threadfence();
-            }
-            __syncthreads();
-            if (last_sh) join<E, SR>(a, u, in, tid, STHREADS);
+        if (u.cut && tid < u.rows) __stcg(a.part_ml + piece + tid, make_float2(m_sh[tid], l_sh[tid]));
+        if (u.cut && u.place == 1) {
+            if (tid == 0) post_cut(a, u.s.q0, u.head, u.row0, u.rows, walk.last_block(u));
+            posted = true;
         }
     }
+    if (!posted && tid == 0) post_cut(a, 0, 0, 0, 0, 0);
 }
 
 template <typename E>
@@ -251,7 +244,8 @@ cudaError_t launch_simt(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
             set[dev] = true;
         }
     }
-    return launch_pdl(simt_kernel<E>, dim3(static_cast<unsigned>(blocks)), STHREADS, simt_smem(a.d), st, a);
+    e = launch_pdl(simt_kernel<E>, dim3(static_cast<unsigned>(blocks)), STHREADS, simt_smem(a.d), st, a);
+    return e == cudaSuccess ? launch_join<E, SR>(a, blocks, st) : e;
 }
 
 }  // namespace cattn
@@ -260,7 +254,7 @@ cudaError_t launch_simt(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
 int cache_attn_simt_blocks(bool, int d, int num_sms) {
     const int per = 2 * (cattn::simt_smem(d) + 1024) <= 225 * 1024 ? 2 : 1;
     const int n = per * num_sms;
-    return n < CACHE_ATTN_COUNTERS ? n : CACHE_ATTN_COUNTERS;
+    return n < CACHE_ATTN_BLOCKS ? n : CACHE_ATTN_BLOCKS;
 }
 
 cudaError_t launch_cache_attn_simt(bool is_bf16, const CacheAttnArgs &a, int num_sms, cudaStream_t st) {

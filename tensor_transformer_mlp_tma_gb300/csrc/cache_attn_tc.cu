@@ -74,14 +74,13 @@ struct alignas(16) Job {
     Seq s;
     int b, head, row0, rows;
     int tile0, tiles, cut, place;
-    int first, last, unused[2];
+    int last, unused[3];   // last block of a unit that begins here and is cut
 };
 constexpr int JOBS = 4;
 constexpr int JOB_READERS = 11;  // warps: the streams' eight, products, copies of K and of V
 
 struct Small {
     Job job[JOBS];
-    Job cut[2];            // units with pieces in other blocks, by place (tiles = 0: none)
     uint64_t job_full[JOBS], job_empty[JOBS];
     uint64_t full[10], empty[10];  // of K's slots, then V's
     uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
@@ -90,8 +89,6 @@ struct Small {
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
-    int last[2];           // per place: this block's piece of a cut unit is the last to be counted
-    int joined;            // bit per place: it has been counted
     volatile int abort;
 };
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
@@ -185,10 +182,7 @@ __device__ void plan_role(const Block<NB, BLK> &B, Walk<TR, KEYS> walk) {
         if (more) {
             j.s = u.s, j.b = u.b, j.head = u.head, j.row0 = u.row0, j.rows = u.rows;
             j.tile0 = u.tile0, j.tiles = u.tiles, j.cut = u.cut, j.place = u.place;
-            if (u.cut) {
-                const Pieces in = walk.pieces(u);
-                j.first = in.first, j.last = in.last;
-            }
+            if (u.cut && u.place == 1) j.last = walk.last_block(u);
         }
         if (!B.warp_wait(B.bar(B.sh->job_empty[at.slot]), at.phase ^ 1u)) return;
         if (lane == 0) {
@@ -825,7 +819,7 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         if (y.tiles > 0) st.load_q(x, y.row0, y.rows, y.width);
         return y.tiles > 0;
     };
-    bool loaded = false, any_cut = false;
+    bool loaded = false, posted = false;
     // (both streams leave together: a barrier that only one of them comes to would wait forever)
     if (both_vote(!jobs.peek(u))) return;
     while (u.tiles > 0) {
@@ -932,34 +926,14 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
             }
         }
         ptx::tc_fence_before();
-        if (u.cut) {
-            // at most two per block, the first unit and the last: counted together at the end, since a fence
-            // under load takes as long as several tiles
-            if (threadIdx.x == 0) sh->cut[u.place] = u;
-            any_cut = true;
+        if (u.cut && u.place == 1) {
+            if (threadIdx.x == 0) post_cut(a, u.s.q0, u.head, u.row0, u.rows, u.last);
+            posted = true;
         }
         jobs.release();
         if (both_vote(!jobs.peek(u))) return;  // (and outputs, references and sums have been read)
     }
-    if (!any_cut) return;
-    if (threadIdx.x == 0) {
-        __threadfence();  // (the others' pieces are behind the barrier)
-        for (int i = 0; i < 2; ++i) {
-            const Job &c = sh->cut[i];
-            sh->last[i] = 0;
-            if (c.tiles == 0) continue;
-            sh->last[i] = atomicAdd(a.counters + c.first, 1u) == static_cast<uint32_t>(c.last - c.first);
-            if (sh->last[i]) a.counters[c.first] = 0u;
-            sh->joined |= 1 << i;
-        }
-        __threadfence();
-    }
-    both_vote(false);
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        const Job &c = sh->cut[i];
-        if (sh->last[i]) join<__nv_bfloat16, TR>(a, c, {c.first, c.last}, threadIdx.x, 256);
-    }
+    if (!posted && threadIdx.x == 0) post_cut(a, 0, 0, 0, 0, 0);
 }
 
 template <int NB, int BLK>
@@ -990,7 +964,6 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             ptx::mbar_init(ptx::smem_u32(&sh->job_empty[i]), JOB_READERS);
         }
         ptx::mbar_init(ptx::smem_u32(&sh->drain), 1);
-        sh->joined = sh->cut[0].tiles = sh->cut[1].tiles = 0;
         sh->abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&mk);
@@ -1023,15 +996,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         ptx::tmem_dealloc(tmem, TMEM);
     }
     if (sh->abort && threadIdx.x == 0) {
-        // what this block would have added to cut units is counted, so that the next call finds the
-        // counters at zero
         report(a, STATUS_TIMEOUT, 3);
-        Unit u;
-        while (walk.next(a, u))
-            if (u.cut && !(sh->joined >> u.place & 1)) {
-                const Pieces in = walk.pieces(u);
-                if (atomicAdd(a.counters + in.first, 1u) == static_cast<uint32_t>(in.last - in.first)) a.counters[in.first] = 0u;
-            }
+        post_cut(a, 0, 0, 0, 0, 0);
     }
 }
 
@@ -1079,7 +1045,8 @@ cudaError_t launch_tc(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
     while (a.page_size % box != 0) box /= 2;
     CUtensorMap mk, mv;
     if (!cache_map(&mk, a, a.k, box) || !cache_map(&mv, a, a.v, box)) return cudaErrorInvalidValue;
-    return launch_pdl(tc_kernel<NB, BLK>, dim3(static_cast<unsigned>(blocks)), TTHREADS, S::SMEM, st, a, mk, mv, box);
+    e = launch_pdl(tc_kernel<NB, BLK>, dim3(static_cast<unsigned>(blocks)), TTHREADS, S::SMEM, st, a, mk, mv, box);
+    return e == cudaSuccess ? launch_join<__nv_bfloat16, TR>(a, blocks, st) : e;
 }
 
 }  // namespace cattn

@@ -350,12 +350,13 @@ struct CacheAttnArgs {
     const void *k, *v;              // page p, head h, row r at p * page_stride + h * head_stride + r * token_stride
     int64_t pages, page_size, page_stride, head_stride, token_stride;
     bool vec;                       // rows start on 16 bytes
-    uint32_t *status, *counters;    // counters: one per block, zero between calls
+    uint32_t *status;
+    void *cuts;                     // [blocks] of 32 bytes: the unit that begins in a block and goes on
     float *part;                    // [2 blocks][rows per tile][d]
     float2 *part_ml;                // [2 blocks][rows per tile]: maximum (log2), sum
     uint64_t wait_ns;
 };
-constexpr int CACHE_ATTN_COUNTERS = 512;  // blocks at most
+constexpr int CACHE_ATTN_BLOCKS = 320;    // at most
 constexpr int CACHE_ATTN_TC_ROWS = 128;   // rows (token, head) of a tile: tensor-core and FFMA kernel
 constexpr int CACHE_ATTN_SIMT_ROWS = 32;
 int cache_attn_simt_blocks(bool is_bf16, int d, int num_sms);

@@ -874,8 +874,7 @@ class CacheAttnContext:
                              % (tokens, batch, heads, kv_heads, dim, self.shape.scale))
         self.dtype, self.kv_heads, self.dim = dtype, int(kv_heads), int(dim)
         self._tokens, self._batch, self._heads = int(tokens), int(batch), int(heads)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        self.workspace[:4096].zero_()
+        self.workspace = _status_workspace(n, device)
         self._ref = ctypes.byref(self.shape)
 
 
