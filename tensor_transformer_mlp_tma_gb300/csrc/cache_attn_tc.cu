@@ -66,8 +66,8 @@ struct Shape {
     static constexpr uint32_t RING = SLOTS * SLOT;
     static constexpr uint32_t SMEM = RING + Q_BYTES + 2 * P_BYTES + SMALL_BYTES + 1024;
 };
-constexpr uint32_t TMEM = 512;          // columns: 2 x 2 x 64 of S, 2 x NB x 64 of O
-constexpr uint32_t O_COLUMN = 4 * COLS;
+constexpr uint32_t TMEM = 512;          // columns: 2 x 2 x 64 of S, 2 x NB x 64 of O, for NB = 1 2 x 64 of sums
+constexpr uint32_t O_COLUMN = 4 * COLS, L_COLUMN = 6 * COLS;
 
 // A unit as the planning warp hands it to the others.  tiles = 0: there are no more.
 struct alignas(16) Job {
@@ -76,7 +76,7 @@ struct alignas(16) Job {
     int tile0, tiles, cut, place;
     int last, unused[3];   // last block of a unit that begins here and is cut
 };
-constexpr int JOBS = 4;
+constexpr int JOBS = 3;
 constexpr int JOB_READERS = 11;  // warps: the streams' eight, products, copies of K and of V
 
 struct Small {
@@ -89,6 +89,7 @@ struct Small {
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
+    alignas(16) uint32_t ones[96];  // in bf16: 128 x 16 of them, whose groups of 8 x 8 (128 bytes) begin 16 bytes apart
     volatile int abort;
 };
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
@@ -320,6 +321,7 @@ __device__ void product_role(const Block<NB, BLK> &B, uint32_t tmem) {
     const uint32_t k_full = B.bar(sh->full[0]), v_full = B.bar(sh->full[S::K_SLOTS]);
     const uint32_t to_empty = B.bar(sh->empty[0]) - k_full;
     Place kp, vp;
+    const uint64_t ones = ptx::sdesc_plain(ptx::smem_u32(sh->ones), 16, 16);
     uint32_t q_phase = 0, p_phase = 0;  // a bit per stream
     bool ok = true;
     Jobs<NB, BLK> jobs = {B, {}};
@@ -409,6 +411,15 @@ __device__ void product_role(const Block<NB, BLK> &B, uint32_t tmem) {
                                 ptx::umma_f16_ss(d + nb * 2 * COLS, vd[nb] + static_cast<uint64_t>(c * 128), p + static_cast<uint64_t>(c * 128),
                                                  idesc, k > 0 || c > 0);
                     }
+                    if (NB == 1) {
+                        // sums of the weights: one more product, with ones for V (each lane has all of them)
+                        const uint32_t idesc = ptx::idesc_bf16_f32(128, width, false, true);
+                        const uint32_t d = tmem + L_COLUMN + static_cast<uint32_t>(s * COLS);
+                        const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
+#pragma unroll
+                        for (int c = 0; c < KEYS / 16; ++c)
+                            ptx::umma_f16_ss(d, ones, p + static_cast<uint64_t>(c * 128), idesc, k > 0 || c > 0);
+                    }
                     ptx::umma_commit(B.bar(sh->o_done[s]));
                     if (both) ptx::umma_commit(B.bar(sh->o_done[1]));
 #pragma unroll
@@ -439,7 +450,7 @@ struct Stream {
     uint32_t scores;                // of the tile at hand
     uint32_t s_phase = 0, o_phase = 0;  // s_phase: a bit per place
     bool failed = false;
-    float2 l[4];                    // sums of the weights of 8 rows over some of the warp's keys (see add_up)
+    float2 l[4];                    // NB = 2: sums of the weights of 8 rows over some of the warp's keys (see add_up)
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
@@ -488,15 +499,17 @@ struct Stream {
 
     __device__ void start() {
         if (key < COLS) sh->m[s][key] = -INFINITY;
+        if (NB > 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i) l[i] = make_float2(0.0f, 0.0f);
+        }
         vote(false);
     }
 
     // Lanes that share a key's line in add_up, eight rows each: 2, 4 or 8, as a power of two.
     static __device__ __forceinline__ int line_bits(int width) { return width <= 16 ? 1 : (width <= 32 ? 2 : 3); }
 
-    // Adds up the rounded weights, as the product does, from their place: a lane takes eight rows of every
+    // Where tensor memory is full of outputs (NB = 2), a stream adds up the rounded weights itself, from their place: a lane takes eight rows of every
     // (32 / lanes)-th key of its warp.  (Sums of all rows for its own key would be 64 registers.)
     __device__ void add_up(int width) {
         const int bits = line_bits(width), lanes = 1 << bits, chunk = lane & (lanes - 1);
@@ -622,15 +635,18 @@ struct Stream {
         }
         const bool fresh = vote(none);
         if (more) {
-            const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & ((1 << line_bits(width)) - 1)) * 32u;
-            uint32_t f[8];
-            ptx::ld_shared_v4(rows8, f[0], f[1], f[2], f[3]);
-            ptx::ld_shared_v4(rows8 + 16, f[4], f[5], f[6], f[7]);
+            if (NB > 1) {
+                const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & ((1 << line_bits(width)) - 1)) * 32u;
+                uint32_t f[8];
+                ptx::ld_shared_v4(rows8, f[0], f[1], f[2], f[3]);
+                ptx::ld_shared_v4(rows8 + 16, f[4], f[5], f[6], f[7]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                l[i] = ptx::mul2(l[i], make_float2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1])));
+                for (int i = 0; i < 4; ++i)
+                    l[i] = ptx::mul2(l[i], make_float2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1])));
+            }
+            // (NB = 1: behind the outputs are the sums)
 #pragma unroll 1
-            for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < 2; ++nb)
 #pragma unroll 1
                 for (int c = 0; c < width; c += 16) {
                     uint32_t o[16];
@@ -766,12 +782,26 @@ struct Stream {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->p_full[s]));
-        add_up(width);
+        if (NB > 1) add_up(width);
         return true;
     }
 
-    // The warp's sums, into the weights' space (which no product reads any more).
+    // The sums (NB = 2: each warp's), into the weights' space, which no product reads any more.
     __device__ void sum_l(int width) {
+        if (NB == 1) {
+            if (warp == 0)
+#pragma unroll 1
+                for (int c = 0; c < width; c += 16) {
+                    uint32_t x[16];
+                    ptx::tmem_ld_32x32b_x16(out + (L_COLUMN - O_COLUMN) + c, x);
+                    ptx::tmem_ld_wait(x);
+                    if (lane == 0)
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            ptx::st_shared_v4(p + P_WARPS + static_cast<uint32_t>(c + j) * 4u, x[j], x[j + 1], x[j + 2], x[j + 3]);
+                }
+            return;
+        }
         const int lanes = (1 << line_bits(width));
         __syncwarp();
 #pragma unroll
@@ -861,7 +891,8 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         if (key < rows) {
             auto sum = [&](int stream) {
                 const uint32_t at = B.p + static_cast<uint32_t>(stream) * P_BYTES + P_WARPS + static_cast<uint32_t>(key) * 4u;
-                return (shared(at) + shared(at + COLS * 4)) + (shared(at + 2 * COLS * 4) + shared(at + 3 * COLS * 4));
+                return NB == 1 ? shared(at)
+                               : (shared(at) + shared(at + COLS * 4)) + (shared(at + 2 * COLS * 4) + shared(at + 3 * COLS * 4));
             };
             float top = sh->m[own][key], total = sum(own), f0 = 1.0f, f1 = 0.0f;
             if (two) {
@@ -968,6 +999,10 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&mk);
         ptx::prefetch_tensormap(&mv);
+    }
+    if (threadIdx.x < 96) {
+        sh->ones[threadIdx.x] = 0x3F803F80u;
+        ptx::fence_proxy_async_smem();
     }
     if (warp == 8) {
         ptx::tmem_alloc(ptx::smem_u32(&sh->tmem), TMEM);

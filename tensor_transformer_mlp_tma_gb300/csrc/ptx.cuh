@@ -399,6 +399,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return d;
 }
 
+// The same without swizzling: groups of 8 rows of 16 bytes (128 bytes in a row), lbo bytes apart along K and sbo bytes
+// along the rows of a K-major tile.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61);
+}
+
 // ---- TMEM <-> registers -------------------------------------------------------------
 // 32x32b shape, 32 repetitions: thread i of the warp gets TMEM lane (lane_base + i),
 // registers j = columns col .. col+31.  The warp may only address its own quarter
