@@ -85,7 +85,7 @@ struct Small {
     uint64_t full[10], empty[10];  // of K's slots, then V's
     uint64_t s_full[2][2], p_full[2], o_done[2], q_full[2], drain;
     float m[2][COLS];      // references (log2)
-    alignas(16) float ref[2][COLS];  // the same, 0 for a row that has seen nothing yet
+    alignas(16) float ref[2][COLS];  // their negatives, 0 for a row that has seen nothing yet
     Walk<TR, KEYS>::Shared walk;
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
@@ -335,95 +335,128 @@ __device__ void product_role(const Block<NB, BLK> &B, uint32_t tmem) {
         ok = ok && B.warp_wait(B.bar(sh->p_full[s]), p_phase >> s & 1u);
         p_phase ^= 1u << s;
     };
+    // The next tile of a ring: its descriptors, and the barriers that give its slots back.
+    auto take = [&](Place &at, int slots, uint32_t full, uint32_t ring, uint32_t lbo, uint64_t (&desc)[NB], uint32_t (&free)[NB]) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            ok = ok && B.warp_wait(full + 8 * at.slot, at.phase);
+            desc[nb] = ptx::sdesc_sw128(ring + static_cast<uint32_t>(at.slot) * S::SLOT, lbo, 1024);
+            free[nb] = full + to_empty + 8 * at.slot;
+            at.next(slots);
+        }
+    };
+    uint64_t kd[NB], vd[NB];
+    uint32_t free[NB];
+    auto take_k = [&] { take(kp, S::K_SLOTS, k_full, B.ring, 16, kd, free); };
+    // (64 components: the second half of the 128 is whatever lies behind, and is not read)
+    auto take_v = [&] { take(vp, S::V_SLOTS, v_full, v_ring, BLOCK_BYTES, vd, free); };
+    // Scores of a tile: `keys` and `rows` are the operands as the mode has them.
+    auto scores = [&](uint32_t d, uint32_t q0, bool wide, uint32_t idesc) {
+        const uint64_t q = ptx::sdesc_sw128(q0, 16, 1024);
+        // descriptors count 16 bytes: 16 components on are 2, 64 a block
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4 * BLK; ++c)
+                if (nb * 8 + c < steps) {
+                    const uint64_t kc = kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2);
+                    const uint64_t qc = q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2);
+                    ptx::umma_f16_ss(d, wide ? qc : kc, wide ? kc : qc, idesc, nb + c > 0);
+                }
+    };
+    auto give_back = [&] {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
+    };
     while (ok && (ok = jobs.get(u)) && u.tiles > 0) {
         const int n = u.tiles;
-        const bool both = u.rows > COLS;  // both streams take every tile
-        const int width = (u.rows + 15) & ~15;
-        const int lag = both ? 1 : 2;
+        if (u.rows > COLS) {
+            // a scale below zero: the products with -Q
+            const uint32_t s_desc = ptx::idesc_bf16_f32(128, KEYS, false, false) | (a.scale_log2 < 0.0f ? ptx::IDESC_NEGATE_A : 0u);
+            const uint32_t o_desc = ptx::idesc_bf16_f32(128, 128, false, true);
 #pragma unroll 1
-        for (int i = 0; ok && i < n + lag; ++i) {
-            if (i < n) {
-                const int s = both ? 0 : i & 1, k = both ? i : i >> 1;
-                uint64_t kd[NB];
-                uint32_t free[NB];
+            for (int i = 0; ok && i < n + 2; ++i) {
+                const int o = i - 2;
+                if (o >= 0) {
+                    const int s = NB == 1 ? o & 1 : 0;
+                    take_v();
+                    weights(s);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        if (sh->skip[s] == 0) {
+                            const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s) * 128u, p = tmem + static_cast<uint32_t>(o & 1) * 128u;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    ok = ok && B.warp_wait(k_full + 8 * kp.slot, kp.phase);
-                    kd[nb] = ptx::sdesc_sw128(B.ring + static_cast<uint32_t>(kp.slot) * S::SLOT, 16, 1024);
-                    free[nb] = k_full + to_empty + 8 * kp.slot;
-                    kp.next(S::K_SLOTS);
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int c = 0; c < KEYS / 16; ++c)  // 16 keys on are 8 columns of weights
+                                    ptx::umma_f16_ts(d + nb * 128, p + 8 * c, vd[nb] + static_cast<uint64_t>(c * 128), o_desc,
+                                                     o >= (NB == 1 ? 2 : 1) || c > 0);
+                        }
+                        if (NB > 1 || o + 2 >= n) ptx::umma_commit(B.bar(sh->o_done[s]));
+                        give_back();
+                    }
                 }
-                if (k == 0) {
-                    queries(s);
-                    if (both) queries(1);
-                }
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (leader) {
-                    const uint32_t idesc = ptx::idesc_bf16_f32(KEYS, width, false, false);
-                    const uint32_t d = tmem + static_cast<uint32_t>((2 * (k & 1) + s) * COLS);
-                    const uint64_t q = ptx::sdesc_sw128(B.q + static_cast<uint32_t>(s) * COLS * 128u, 16, 1024);
-                    // descriptors count 16 bytes: 16 components on are 2, 64 a block
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int c = 0; c < 4 * BLK; ++c)
-                            if (nb * 8 + c < steps)
-                                ptx::umma_f16_ss(d, kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2),
-                                                 q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2),
-                                                 idesc, nb + c > 0);
-                    ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
-                    if (both) ptx::umma_commit(B.bar(sh->s_full[1][k & 1]));
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
+                if (i < n) {
+                    const int s = NB == 1 ? i & 1 : 0;
+                    take_k();
+                    if (i == 0) queries(0), queries(1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        scores(tmem + static_cast<uint32_t>(i & 1) * 128u, B.q, true, s_desc);
+                        ptx::umma_commit(B.bar(sh->s_full[s][NB == 1 ? 0 : i & 1]));
+                        give_back();
+                    }
                 }
             }
-            const int o = i - lag;
-            if (o >= 0) {
-                const int s = both ? 0 : o & 1, k = both ? o : o >> 1;
-                uint64_t vd[NB];
-                uint32_t free[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    ok = ok && B.warp_wait(v_full + 8 * vp.slot, vp.phase);
-                    // (64 components: the second half of the 128 rows is whatever lies behind, and is not read)
-                    vd[nb] = ptx::sdesc_sw128(v_ring + static_cast<uint32_t>(vp.slot) * S::SLOT, BLOCK_BYTES, 1024);
-                    free[nb] = v_full + to_empty + 8 * vp.slot;
-                    vp.next(S::V_SLOTS);
-                }
-                weights(s);
-                if (both) weights(1);
+            continue;
+        }
+        const int width = (u.rows + 15) & ~15;
+        const uint32_t s_desc = ptx::idesc_bf16_f32(KEYS, width, false, false), o_desc = ptx::idesc_bf16_f32(128, width, true, true);
+#pragma unroll 1
+        for (int i = 0; ok && i < n + 2; ++i) {
+            if (i < n) {
+                const int s = i & 1, k = i >> 1;
+                take_k();
+                if (k == 0) queries(s);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                // streams that have formed the product themselves are left out
-                const bool skip0 = sh->skip[s] != 0, skip1 = both && sh->skip[1] != 0;
                 if (leader) {
-                    const int from = both && skip0 ? 1 : s, columns = both ? (skip0 ? width - COLS : (skip1 ? COLS : width)) : width;
-                    if (!(skip0 && (skip1 || !both))) {
-                        const uint32_t idesc = ptx::idesc_bf16_f32(128, columns, true, true);
-                        const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(from * COLS);
-                        const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(from) * P_BYTES, P_BYTES, 1024);
+                    scores(tmem + static_cast<uint32_t>((2 * (k & 1) + s) * COLS), B.q + static_cast<uint32_t>(s) * COLS * 128u, false, s_desc);
+                    ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
+                    give_back();
+                }
+            }
+            const int o = i - 2;
+            if (o >= 0) {
+                const int s = o & 1, k = o >> 1;
+                take_v();
+                weights(s);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
+                    if (sh->skip[s] == 0) {
+                        const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s * COLS);
                         // 16 keys on are 128
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int c = 0; c < KEYS / 16; ++c)
                                 ptx::umma_f16_ss(d + nb * 2 * COLS, vd[nb] + static_cast<uint64_t>(c * 128), p + static_cast<uint64_t>(c * 128),
-                                                 idesc, k > 0 || c > 0);
+                                                 o_desc, k > 0 || c > 0);
                     }
                     if (NB == 1) {
                         // sums of the weights: one more product, with ones for V (each lane has all of them)
-                        const uint32_t idesc = ptx::idesc_bf16_f32(128, width, false, true);
+                        const uint32_t l_desc = ptx::idesc_bf16_f32(128, width, false, true);
                         const uint32_t d = tmem + L_COLUMN + static_cast<uint32_t>(s * COLS);
-                        const uint64_t p = ptx::sdesc_sw128(B.p + static_cast<uint32_t>(s) * P_BYTES, P_BYTES, 1024);
 #pragma unroll
                         for (int c = 0; c < KEYS / 16; ++c)
-                            ptx::umma_f16_ss(d, ones, p + static_cast<uint64_t>(c * 128), idesc, k > 0 || c > 0);
+                            ptx::umma_f16_ss(d, ones, p + static_cast<uint64_t>(c * 128), l_desc, k > 0 || c > 0);
                     }
                     ptx::umma_commit(B.bar(sh->o_done[s]));
-                    if (both) ptx::umma_commit(B.bar(sh->o_done[1]));
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(free[nb]);
+                    give_back();
                 }
             }
         }
@@ -446,16 +479,22 @@ struct Stream {
     const CacheAttnArgs &a;
     Small *sh;
     const int s, warp, lane, key;   // stream; warp of it; key of a tile (TMEM lane)
-    const uint32_t scores0, out, q, p;
+    const uint32_t scores0, out;
+    const uint32_t wide_scores, wide_out;  // the same of units of more than 64 rows
+    const uint32_t q, p;
     uint32_t scores;                // of the tile at hand
     uint32_t s_phase = 0, o_phase = 0;  // s_phase: a bit per place
     bool failed = false;
+    float m;                        // its reference (log2)
+    float2 wl[2];                   // its sum, in four parts
     float2 l[4];                    // NB = 2: sums of the weights of 8 rows over some of the warp's keys (see add_up)
 
     __device__ Stream(const Block<NB, BLK> &b, uint32_t tmem, int stream)
         : B(b), a(b.a), sh(b.sh), s(stream), warp((threadIdx.x >> 5) & 3), lane(threadIdx.x & 31), key(threadIdx.x & 127),
           scores0(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + static_cast<uint32_t>(stream * COLS)),
           out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + O_COLUMN + static_cast<uint32_t>(stream * COLS)),
+          wide_scores(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16)),
+          wide_out(tmem + (static_cast<uint32_t>(32 * ((threadIdx.x >> 5) & 3)) << 16) + O_COLUMN + static_cast<uint32_t>(stream) * 128u),
           q(b.q + static_cast<uint32_t>(stream) * COLS * 128u), p(b.p + static_cast<uint32_t>(stream) * P_BYTES) {}
 
     __device__ bool vote(bool x) const { return ptx::barrier_or(1 + s, 128, x); }
@@ -528,18 +567,18 @@ struct Stream {
     }
 
     // Bit r: row r sees this thread's key.  Rows behind the last see everything (their scores are zero).
-    __device__ uint64_t seen(const Job &u, int row0, int rows, int at) const {
+    __device__ uint64_t seen(const Job &u, int rows, int at) const {
         const uint64_t past = rows >= 64 ? 0ull : ~0ull << rows;
         const int j = at - u.s.prefix;
         if (j < 0) return ~0ull;
         if (at >= u.s.len) return past;
         if (!a.tree) {
-            const int64_t from = static_cast<int64_t>(j) * a.group - (u.row0 + row0);  // rows of token j and later
+            const int64_t from = static_cast<int64_t>(j) * a.group - u.row0;  // rows of token j and later
             return (from <= 0 ? ~0ull : (from >= 64 ? 0ull : ~0ull << from)) | past;
         }
         if (j >= 64 * a.tree_words) return past;
         // token by token: `group` rows each, the first one's perhaps fewer
-        const int r0 = u.row0 + row0, first = r0 / a.group, tokens = (r0 + rows - 1) / a.group - first + 1;
+        const int r0 = u.row0, first = r0 / a.group, tokens = (r0 + rows - 1) / a.group - first + 1;
         const int64_t *words = a.tree + static_cast<int64_t>(u.s.q0 + first) * a.tree_words + (j >> 6);
         uint64_t bits = past;
         int begin = first * a.group - r0;
@@ -588,9 +627,9 @@ struct Stream {
                     for (int j = 0; j < 4; ++j) {
                         const float4 m = *reinterpret_cast<const float4 *>(&sh->ref[s][32 * h + 16 * c + 4 * j]);
                         const float2 lo = ptx::fma2(make_float2(__uint_as_float(r[c][4 * j]), __uint_as_float(r[c][4 * j + 1])), scale,
-                                                    make_float2(-m.x, -m.y));
+                                                    make_float2(m.x, m.y));
                         const float2 hi = ptx::fma2(make_float2(__uint_as_float(r[c][4 * j + 2]), __uint_as_float(r[c][4 * j + 3])), scale,
-                                                    make_float2(-m.z, -m.w));
+                                                    make_float2(m.z, m.w));
                         top = fmaxf(top, fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
                         const __nv_bfloat162 e0 = __floats2bfloat162_rn(ptx::ex2_approx(lo.x), ptx::ex2_approx(lo.y)),
                                              e1 = __floats2bfloat162_rn(ptx::ex2_approx(hi.x), ptx::ex2_approx(hi.y));
@@ -630,7 +669,7 @@ struct Stream {
             }
             none = now == -INFINITY;
             sh->m[s][key] = now;
-            sh->ref[s][key] = none ? 0.0f : now;
+            sh->ref[s][key] = none ? 0.0f : -now;
             ptx::st_shared_u32(p + P_FACTOR + static_cast<uint32_t>(key) * 4u, __float_as_uint(was == now ? 1.0f : ptx::ex2_approx(was - now)));
         }
         const bool fresh = vote(none);
@@ -664,10 +703,12 @@ struct Stream {
         return fresh;
     }
 
+    __device__ uint32_t v_slot(uint32_t pos) const { return B.ring + (S::K_SLOTS + pos % S::V_SLOTS) * S::SLOT; }
+
     // Values that are not finite would reach rows that do not see them (0 x NaN).  Those behind the
     // sequence's end are cleared; of a tile with others the stream forms the product itself, key by key.
-    __device__ bool own_product(uint32_t pos, int at, int len, uint64_t sees, int width, bool first) {
-        auto v_slot = [&](int nb) { return B.ring + (S::K_SLOTS + (pos + nb) % S::V_SLOTS) * S::SLOT; };
+    // Whether this thread's key (at) has such values.
+    __device__ bool odd_values(uint32_t pos, int at, int len) {
         for (int nb = 0; nb < NB; ++nb)
             failed = !B.wait(B.bar(sh->full[S::K_SLOTS + (pos + nb) % S::V_SLOTS]), (pos + nb) / S::V_SLOTS & 1u) || failed;
         __syncwarp();
@@ -677,7 +718,7 @@ struct Stream {
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll 1
                 for (int b = 0; b < B.blocks(nb); ++b) {
-                    const uint32_t line = v_slot(nb) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
+                    const uint32_t line = v_slot(pos + nb) + static_cast<uint32_t>(b) * BLOCK_BYTES + static_cast<uint32_t>(key) * 128u;
                     // the largest size, NaN above all
                     __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
@@ -697,6 +738,11 @@ struct Stream {
                     }
                 }
         }
+        return odd;
+    }
+
+    __device__ bool own_product(uint32_t pos, int at, int len, uint64_t sees, int width, bool first) {
+        const bool odd = odd_values(pos, at, len);
         if (!vote(odd && sees != ~0ull)) return false;
         // -0 marks a weight that is none
         const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
@@ -710,7 +756,7 @@ struct Stream {
         for (int nb = 0; nb < NB; ++nb) {
             const int e = key;  // component nb * 128 + key: this thread's TMEM lane
             const bool have = nb * 128 + e < a.d;
-            const uint32_t v0 = v_slot(nb) + static_cast<uint32_t>(have ? e >> 6 : 0) * BLOCK_BYTES + (e & 7) * 2;
+            const uint32_t v0 = v_slot(pos + nb) + static_cast<uint32_t>(have ? e >> 6 : 0) * BLOCK_BYTES + (e & 7) * 2;
 #pragma unroll 1
             for (int c = 0; c * 16 < width; ++c) {
                 uint32_t o[16];
@@ -744,7 +790,7 @@ struct Stream {
     }
 
     // One tile: scores to weights.  k: how many this stream has done of the unit; pos: of its V, counted in slots.
-    __device__ bool tile(const Job &u, int row0, int rows, int width, int t, int k, uint32_t pos, bool &fresh) {
+    __device__ bool tile(const Job &u, int rows, int width, int t, int k, uint32_t pos, bool &fresh) {
         failed = !B.wait(ptx::smem_u32(&sh->s_full[s][k & 1]), s_phase >> (k & 1) & 1u) || failed;
         s_phase ^= 1u << (k & 1);
         scores = scores0 + static_cast<uint32_t>((k & 1) * 2 * COLS);
@@ -754,7 +800,7 @@ struct Stream {
         const bool masked = (t + 1) * KEYS > u.s.prefix;
         uint64_t sees = ~0ull;
         if (masked) {
-            sees = seen(u, row0, rows, at);
+            sees = seen(u, rows, at);
             __syncwarp();
             hide(sees, width);
         }
@@ -784,6 +830,179 @@ struct Stream {
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->p_full[s]));
         if (NB > 1) add_up(width);
         return true;
+    }
+
+    // ---- units of more than 64 rows: a thread per row ----
+
+    // Bit i: row `token` sees key at + i.
+    __device__ uint32_t sees_of(const Job &u, int token, int at) const {
+        const int left = u.s.len - at, j = at - u.s.prefix;
+        const uint32_t bits = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+        if (j + 32 <= 0) return bits;
+        if (!a.tree) {
+            const int n = token + 1 - j;
+            return n >= 32 ? bits : (n <= 0 ? 0u : bits & ((1u << n) - 1u));
+        }
+        const int64_t *words = a.tree + static_cast<int64_t>(u.s.q0 + token) * a.tree_words;
+        auto word = [&](int i) { return i < a.tree_words ? static_cast<uint64_t>(words[i]) : 0ull; };
+        uint64_t w;
+        if (j < 0) {
+            w = word(0) << -j | ((1ull << -j) - 1ull);
+        } else {
+            w = word(j >> 6) >> (j & 63);
+            if ((j & 63) > 32) w |= word((j >> 6) + 1) << (64 - (j & 63));
+        }
+        return bits & static_cast<uint32_t>(w);
+    }
+
+    __device__ void wide_hide(const Job &u, int token, int at) const {
+#pragma unroll 1
+        for (int h = 0; h < KEYS; h += 32) {
+            const uint32_t bits = sees_of(u, token, at + h);
+            if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+                uint32_t x[16];
+                ptx::tmem_ld_32x32b_x16(scores + h + c, x);
+                ptx::tmem_ld_wait(x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = bits >> (c + j) & 1u ? x[j] : 0xFF800000u;
+                ptx::tmem_st_32x32b_x16(scores + h + c, x);
+            }
+        }
+        ptx::tmem_st_wait();
+    }
+
+    // The reference becomes the row's maximum so far (top: of this tile); its sum and outputs take the factor.
+    __device__ void wide_renew(float top, bool more) {
+        const float now = top > m ? top : m;  // NaN: passed over
+        const float f = m == now ? 1.0f : ptx::ex2_approx(m - now);
+        m = now;
+        wl[0] = ptx::mul2(wl[0], make_float2(f, f));
+        wl[1] = ptx::mul2(wl[1], make_float2(f, f));
+        if (more) {
+#pragma unroll 1
+            for (int c = 0; c < a.d; c += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld_32x32b_x16(wide_out + c, o);
+                ptx::tmem_ld_wait(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                ptx::tmem_st_32x32b_x16(wide_out + c, o);
+            }
+            ptx::tmem_st_wait();
+        }
+    }
+
+    // Weights (in place of the scores: two to a word) and their sums.
+    __device__ void wide_form() {
+        const float scale = fabsf(a.scale_log2), ref = m == -INFINITY ? 0.0f : -m;
+        const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+        uint32_t x[2][32];
+        ptx::tmem_ld_32x32b_x32(scores, x[0]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t (&r)[32] = x[h & 1];
+            ptx::tmem_ld_wait(r);
+            if (h < 3) ptx::tmem_ld_32x32b_x32(scores + 32 * (h + 1), x[(h + 1) & 1]);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float2 e = ptx::fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), scale2, ref2);
+                const float2 p2 = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+                wl[j & 1] = ptx::add2(wl[j & 1], p2);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(p2.x, p2.y);
+                w[j] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            ptx::tmem_st_32x32b_x16(scores + 16 * h, w);
+        }
+        ptx::tmem_st_wait();
+    }
+
+    // The product of a tile with values that are not finite, from the weights as they were rounded.
+    __device__ bool wide_product(const Job &u, int token, uint32_t pos, int at, bool first) {
+        if (!vote(odd_values(pos, at + key, u.s.len))) return false;
+#pragma unroll 1
+        for (int c = 0; c < a.d; c += 16) {
+            const uint32_t v0 = v_slot(pos + (c >> 7)) + static_cast<uint32_t>((c >> 6) & 1) * BLOCK_BYTES;
+            const uint32_t chunk = static_cast<uint32_t>(c >> 3) & 7u;
+            uint32_t o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = 0u;
+            if (!first) {
+                ptx::tmem_ld_32x32b_x16(wide_out + c, o);
+                ptx::tmem_ld_wait(o);
+            }
+#pragma unroll 1
+            for (int h = 0; h < KEYS; h += 16) {
+                const uint32_t bits = sees_of(u, token, at + (h & ~31)) >> (h & 16);
+                uint32_t w[8];
+                ptx::tmem_ld_32x32b_x8(scores + h / 2, w);
+                ptx::tmem_ld_wait(w);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const uint32_t line = v0 + static_cast<uint32_t>(h + k) * 128u;
+                    uint32_t v[8];
+                    ptx::ld_shared_v4(line + ((chunk ^ (k & 7)) << 4), v[0], v[1], v[2], v[3]);
+                    ptx::ld_shared_v4(line + (((chunk + 1) ^ (k & 7)) << 4), v[4], v[5], v[6], v[7]);
+                    if (bits >> k & 1u) {
+                        const float p1 = __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) +
+                                                   p1 * __uint_as_float(j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16));
+                    }
+                }
+            }
+            __syncwarp();
+            ptx::tmem_st_32x32b_x16(wide_out + c, o);
+        }
+        ptx::tmem_st_wait();
+        return true;
+    }
+
+    __device__ void wide_start() {
+        m = -INFINITY;
+        wl[0] = wl[1] = make_float2(0.0f, 0.0f);
+    }
+
+    // One tile, the unit's i-th and this stream's k-th.  A wait that failed makes the rest of them end at once.
+    __device__ void wide_tile(const Job &u, int i, int k, uint32_t pos) {
+        const int place = NB == 1 ? 0 : k & 1;
+        failed = !B.wait(ptx::smem_u32(&sh->s_full[s][place]), s_phase >> place & 1u) || failed;
+        s_phase ^= 1u << place;
+        scores = wide_scores + static_cast<uint32_t>(i & 1) * 128u;
+        __syncwarp();
+        ptx::tc_fence_after();
+        const int at = (u.tile0 + i) * KEYS, token = (u.row0 + min(key, u.rows - 1)) / a.group;
+        // keys that every row of the unit sees
+        const int all = min(u.s.len, a.tree ? u.s.prefix : u.s.prefix + u.row0 / a.group + 1);
+        const bool masked = at + KEYS > all;
+        if (masked) wide_hide(u, token, at);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+            uint32_t x[2][32];
+            ptx::tmem_ld_32x32b_x32(scores, x[0]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                ptx::tmem_ld_wait(x[h & 1]);
+                if (h < 3) ptx::tmem_ld_32x32b_x32(scores + 32 * (h + 1), x[(h + 1) & 1]);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    top[(j >> 1) & 3] = fmaxf(top[(j >> 1) & 3], fmaxf(__uint_as_float(x[h & 1][j]), __uint_as_float(x[h & 1][j + 1])));
+            }
+        }
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(a.scale_log2);
+        // (NB = 1: these scores were issued behind the stream's product before them, and are there with it)
+        if (NB > 1 && k > 0) wait_out();
+        if (__any_sync(0xffffffffu, most > m + RENEW)) wide_renew(most, k > 0);
+        wide_form();
+        const bool own = masked && wide_product(u, token, pos, at, k == 0);
+        if (key == 0) sh->skip[s] = own;
+        if (masked) ptx::fence_proxy_async_smem();  // values that were cleared
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->p_full[s]));
     }
 
     // The sums (NB = 2: each warp's), into the weights' space, which no product reads any more.
@@ -830,24 +1049,25 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
     Job u;
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
     auto shared = [&](uint32_t at) { return __uint_as_float(ptx::ld_shared_u32(at)); };
-    // A unit's rows and tiles of this stream.
+    // A unit's queries and tiles of this stream.
     struct Part {
-        bool both;
+        bool wide;
         int row0, rows, width, tiles;
     };
     auto part = [&](const Job &x) {
         Part y;
-        y.both = x.rows > COLS;
-        y.row0 = y.both ? s * COLS : 0, y.rows = y.both ? min(COLS, x.rows - y.row0) : x.rows;
-        y.width = (y.rows + 15) & ~15;
-        y.tiles = y.both ? x.tiles : (x.tiles + 1 - s) / 2;
+        y.wide = x.rows > COLS;
+        y.row0 = y.wide ? s * COLS : 0, y.rows = y.wide ? min(COLS, x.rows - y.row0) : x.rows;
+        y.width = y.wide ? COLS : (y.rows + 15) & ~15;
+        y.tiles = y.wide && NB > 1 ? (s == 0 ? x.tiles : 0) : (x.tiles + 1 - s) / 2;
         return y;
     };
     // The queries of the next unit, as soon as the scores of the one before are complete.
     auto queries = [&](const Job &x) {
         const Part y = part(x);
-        if (y.tiles > 0) st.load_q(x, y.row0, y.rows, y.width);
-        return y.tiles > 0;
+        const bool some = x.tiles > 0 && (y.wide || y.tiles > 0);
+        if (some) st.load_q(x, y.row0, y.rows, y.width);
+        return some;
     };
     bool loaded = false, posted = false;
     // (both streams leave together: a barrier that only one of them comes to would wait forever)
@@ -856,14 +1076,89 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         if (!loaded && queries(u)) st.have_q();
         loaded = false;
         const Part y = part(u);
-        const int n = u.tiles, row0 = y.row0, rows = y.rows, width = y.width;
-        const bool both = y.both;
+        const int n = u.tiles, rows = u.rows, width = y.width;
+        if (y.wide) {
+            st.wide_start();
+#pragma unroll 1
+            for (int k = 0; k < y.tiles; ++k) {
+                const int i = NB == 1 ? 2 * k + s : k;
+                st.wide_tile(u, i, k, v_pos + i * NB);
+            }
+            v_pos += n * NB;
+            if (y.tiles > 0) st.wait_out();
+            const uint32_t ml = B.p + static_cast<uint32_t>(key) * 8u;
+            ptx::st_shared_u32(ml + static_cast<uint32_t>(s) * P_BYTES, __float_as_uint(st.m));
+            ptx::st_shared_u32(ml + static_cast<uint32_t>(s) * P_BYTES + 4, __float_as_uint((st.wl[0].x + st.wl[0].y) + (st.wl[1].x + st.wl[1].y)));
+            if (both_vote(st.failed)) return;
+            ptx::tc_fence_after();
+            // both streams' scores are complete: the next unit's queries
+            Job ahead;
+            if (both_vote(!jobs.peek_next(ahead))) return;
+            const bool coming = queries(ahead);
+            loaded = true;
+            jobs.read(u, jobs.at.slot);
+            // streams that shared the tiles out are added up; each writes half of the components
+            const bool two = NB == 1 && n > 1;
+            const float m0 = shared(ml), m1 = shared(ml + P_BYTES), top = two ? fmaxf(m0, m1) : m0;
+            float f0 = two ? scale_of(m0, top) : 1.0f, f1 = two ? scale_of(m1, top) : 0.0f;
+            const float total = two ? shared(ml + 4) * f0 + shared(ml + P_BYTES + 4) * f1 : shared(ml + 4);
+            const bool have = key < rows;
+            const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * TR + key;
+            const int r = u.row0 + key, token = r / a.group;
+            float *part_row = a.part + piece * a.d;
+            __nv_bfloat16 *o_row = static_cast<__nv_bfloat16 *>(a.o) +
+                                   (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
+            if (u.cut) {
+                if (have && s == 0) __stcg(a.part_ml + piece, make_float2(top, total));
+            } else {
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a row that sees nothing: zeros
+                f0 *= inv, f1 *= inv;
+            }
+            constexpr int HALF = 32 * BLK * NB;
+            const uint32_t outs = st.wide_scores + O_COLUMN;
+#pragma unroll 1
+            for (int c = s * HALF; c < min(a.d, (s + 1) * HALF); c += 8) {
+                uint32_t x[8], x1[8];
+                ptx::tmem_ld_32x32b_x8(outs + c, x);
+                if (two) ptx::tmem_ld_32x32b_x8(outs + 128 + c, x1);
+                ptx::tmem_ld_wait(x);
+                if (two) ptx::tmem_ld_wait(x1);
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = __uint_as_float(x[j]) * f0;
+                    if (two) v[j] += __uint_as_float(x1[j]) * f1;
+                }
+                if (have && u.cut) {
+                    __stcg(reinterpret_cast<float4 *>(part_row + c), make_float4(v[0], v[1], v[2], v[3]));
+                    __stcg(reinterpret_cast<float4 *>(part_row + c + 4), make_float4(v[4], v[5], v[6], v[7]));
+                } else if (have) {
+                    uint4 w;
+                    uint32_t *to = &w.x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                        to[j] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    *reinterpret_cast<uint4 *>(o_row + c) = w;
+                }
+            }
+            ptx::tc_fence_before();
+            if (coming) st.have_q();
+            if (u.cut && u.place == 1) {
+                if (threadIdx.x == 0) post_cut(a, u.s.q0, u.head, u.row0, u.rows, u.last);
+                posted = true;
+            }
+            jobs.release();
+            if (both_vote(!jobs.peek(u))) return;
+            continue;
+        }
         st.start();
         bool fresh = true, ok = true;
 #pragma unroll 1
         for (int k = 0; ok && k < y.tiles; ++k) {
-            const int i = both ? k : 2 * k + s;
-            ok = st.tile(u, row0, rows, width, u.tile0 + i, k, v_pos + i * NB, fresh);
+            const int i = 2 * k + s;
+            ok = st.tile(u, rows, width, u.tile0 + i, k, v_pos + i * NB, fresh);
         }
         v_pos += n * NB;
         bool coming = false;
@@ -885,26 +1180,25 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         jobs.read(u, jobs.at.slot);  // (not kept in registers over the tiles)
         // Streams that shared the rows out by tiles are added up here.  A thread per row: factors of the
         // outputs, and where the row goes.
-        const bool two = !both && n > 1;
-        const int own = both ? s : 0;
-        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * TR + row0;
+        const bool two = n > 1;
+        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * TR;
         if (key < rows) {
             auto sum = [&](int stream) {
                 const uint32_t at = B.p + static_cast<uint32_t>(stream) * P_BYTES + P_WARPS + static_cast<uint32_t>(key) * 4u;
                 return NB == 1 ? shared(at)
                                : (shared(at) + shared(at + COLS * 4)) + (shared(at + 2 * COLS * 4) + shared(at + 3 * COLS * 4));
             };
-            float top = sh->m[own][key], total = sum(own), f0 = 1.0f, f1 = 0.0f;
+            float top = sh->m[0][key], total = sum(0), f0 = 1.0f, f1 = 0.0f;
             if (two) {
                 const float m0 = top, m1 = sh->m[1][key];
                 top = fmaxf(m0, m1);
                 f0 = scale_of(m0, top), f1 = scale_of(m1, top);
                 total = total * f0 + sum(1) * f1;
             }
-            const int r = u.row0 + row0 + key, token = r / a.group;
+            const int r = u.row0 + key, token = r / a.group;
             int to = token * a.heads + (r - token * a.group);
             if (u.cut) {
-                if (both || s == 0) __stcg(a.part_ml + piece + key, make_float2(top, total));
+                if (s == 0) __stcg(a.part_ml + piece + key, make_float2(top, total));
                 to = key;
             } else {
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a row that sees nothing: zeros
@@ -922,9 +1216,9 @@ __device__ void softmax_role(const Block<NB, BLK> &B, uint32_t tmem, int s) {
         for (int nb = 0; nb < NB; ++nb) {
             const int e = nb * 128 + key;
 #pragma unroll 1
-            for (int c = both ? 0 : 8 * s; c < rows; c += both ? 8 : 16) {
+            for (int c = 8 * s; c < rows; c += 16) {
                 uint32_t x[8], y[8], f[8], g[8], to[8];
-                ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + own) * COLS + c), x);
+                ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>(2 * nb * COLS + c), x);
                 if (two) ptx::tmem_ld_32x32b_x8(tmem + lanes + O_COLUMN + static_cast<uint32_t>((2 * nb + 1) * COLS + c), y);
                 const uint32_t at = st.p + P_FACTOR + static_cast<uint32_t>(c) * 4u;
                 ptx::ld_shared_v4(at, f[0], f[1], f[2], f[3]);
