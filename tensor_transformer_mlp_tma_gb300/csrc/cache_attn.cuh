@@ -117,6 +117,11 @@ __device__ __forceinline__ int64_t share(int64_t x, int64_t y, int64_t z) {
     return static_cast<int64_t>(product / static_cast<uint64_t>(z));
 }
 
+struct WalkShared {
+    int64_t warp_sum[8];
+    int b, head, rt, tile, count;
+};
+
 // A block's share of the work.
 template <int ROWS, int KEYS>
 struct Walk {
@@ -126,10 +131,7 @@ struct Walk {
     int b, head, rt, tile;     // where pos is
     int count;                 // tiles of the unit
 
-    struct Shared {
-        int64_t warp_sum[8];
-        int b, head, rt, tile, count;
-    };
+    using Shared = WalkShared;
 
     // All threads (at least 256) of the block.
     __device__ void begin(const CacheAttnArgs &a, Shared &sh) {
