@@ -360,18 +360,18 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
     auto take_k = [&] { take(kp, S::K_SLOTS, k_full, B.ring, 16, kd, free); };
     // (64 components: the second half of the 128 is whatever lies behind, and is not read)
     auto take_v = [&] { take(vp, S::V_SLOTS, v_full, v_ring, BLOCK_BYTES, vd, free); };
-    // Scores of a tile: `keys` and `rows` are the operands as the mode has them.
-    auto scores = [&](uint32_t d, uint32_t q0, bool wide, uint32_t idesc) {
+    // Scores of a tile, or a half of their products (steps of 16 components `from` to `to` of every block of 128).
+    auto scores = [&](uint32_t d, uint32_t q0, uint32_t idesc, int from = 0, int to = 4 * BLK) {
         const uint64_t q = ptx::sdesc_sw128(q0, 16, 1024);
         // descriptors count 16 bytes: 16 components on are 2, 64 a block
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int c = 0; c < 4 * BLK; ++c)
+            for (int c = from; c < to; ++c)
                 if (nb * 8 + c < steps) {
                     const uint64_t kc = kd[nb] + static_cast<uint64_t>((c >> 2) * (BLOCK_BYTES >> 4) + (c & 3) * 2);
                     const uint64_t qc = q + static_cast<uint64_t>((nb * 2 + (c >> 2)) * (Q_BLOCK_BYTES >> 4) + (c & 3) * 2);
-                    ptx::umma_f16_ss(d, wide ? qc : kc, wide ? kc : qc, idesc, nb + c > 0);
+                    ptx::umma_f16_ss(d, WIDE ? qc : kc, WIDE ? kc : qc, idesc, nb + c > 0);
                 }
     };
     auto give_back = [&] {
@@ -384,41 +384,70 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
             // a scale below zero: the products with -Q
             const uint32_t s_desc = ptx::idesc_bf16_f32(128, KEYS, false, false) | (a.scale_log2 < 0.0f ? ptx::IDESC_NEGATE_A : 0u);
             const uint32_t o_desc = ptx::idesc_bf16_f32(128, 128, false, true);
+            // Waits stand between products: the queue holds a few of them, and an open barrier too
+            // takes 150 cycles and more to be seen, with shared memory as busy as it is.
+            auto place = [&](int i) { return tmem + static_cast<uint32_t>(i & 1) * 128u; };
+            auto have_scores = [&](int i, const uint32_t (&slots)[NB]) {
+                ptx::umma_commit(B.bar(sh->s_full[NB == 1 ? i & 1 : 0][NB == 1 ? 0 : i & 1]));
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(slots[nb]);
+            };
+            queries(0), queries(1);
+            for (int i = 0; ok && i < 2 && i < n; ++i) {
+                take_k();
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    scores(place(i), B.q, s_desc);
+                    have_scores(i, free);
+                }
+            }
+            uint64_t v[NB];
+            uint32_t v_free[NB];
+            auto next_v = [&] {
+                take_v();
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) v[nb] = vd[nb], v_free[nb] = free[nb];
+            };
+            if (ok) next_v();
 #pragma unroll 1
-            for (int i = 0; ok && i < n + 2; ++i) {
-                const int o = i - 2;
-                if (o >= 0) {
-                    const int s = NB == 1 ? o & 1 : 0;
-                    take_v();
-                    weights(s);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    if (leader) {
-                        if (sh->skip[s] == 0) {
-                            const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s) * 128u, p = tmem + static_cast<uint32_t>(o & 1) * 128u;
+            for (int o = 0; ok && o < n; ++o) {
+                const int s = NB == 1 ? o & 1 : 0;
+                weights(s);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const bool skip = sh->skip[s] != 0, more = o + 2 < n;
+                const uint32_t d = tmem + O_COLUMN + static_cast<uint32_t>(s) * 128u;
+                auto outputs = [&](int from, int to) {
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                                for (int c = 0; c < KEYS / 16; ++c)  // 16 keys on are 8 columns of weights
-                                    ptx::umma_f16_ts(d + nb * 128, p + 8 * c, vd[nb] + static_cast<uint64_t>(c * 128), o_desc,
-                                                     o >= (NB == 1 ? 2 : 1) || c > 0);
-                        }
-                        if (NB > 1 || o + 2 >= n) ptx::umma_commit(B.bar(sh->o_done[s]));
-                        give_back();
-                    }
+                        for (int c = from; c < to; ++c)  // 16 keys on are 8 columns of weights
+                            ptx::umma_f16_ts(d + nb * 128, place(o) + 8 * c, v[nb] + static_cast<uint64_t>(c * 128), o_desc,
+                                             o >= (NB == 1 ? 2 : 1) || c > 0);
+                };
+                if (leader && !skip) outputs(0, KEYS / 32);
+                if (more) take_k();
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    if (!skip) outputs(KEYS / 32, KEYS / 16);
+                    if (NB > 1 || o + 2 >= n) ptx::umma_commit(B.bar(sh->o_done[s]));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) ptx::umma_commit(v_free[nb]);
+                    if (more) scores(place(o), B.q, s_desc, 0, 2 * BLK);
                 }
-                if (i < n) {
-                    const int s = NB == 1 ? i & 1 : 0;
-                    take_k();
-                    if (i == 0) queries(0), queries(1);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    if (leader) {
-                        scores(tmem + static_cast<uint32_t>(i & 1) * 128u, B.q, true, s_desc);
-                        ptx::umma_commit(B.bar(sh->s_full[s][NB == 1 ? 0 : i & 1]));
-                        give_back();
-                    }
+                uint32_t k_free[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) k_free[nb] = free[nb];
+                // (NB = 2: the slots hold V of a tile and a half, and the next one comes late)
+                if (NB == 1 && o + 1 < n) next_v();
+                if (!ok) break;
+                if (leader && more) {
+                    scores(place(o), B.q, s_desc, 2 * BLK, 4 * BLK);
+                    have_scores(o, k_free);
                 }
+                if (NB > 1 && o + 1 < n) next_v();
             }
         } else {
             const int width = (u.rows + 15) & ~15;
@@ -432,7 +461,7 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (leader) {
-                        scores(tmem + static_cast<uint32_t>((2 * (k & 1) + s) * COLS), B.q + static_cast<uint32_t>(s) * COLS * 128u, false, s_desc);
+                        scores(tmem + static_cast<uint32_t>((2 * (k & 1) + s) * COLS), B.q + static_cast<uint32_t>(s) * COLS * 128u, s_desc);
                         ptx::umma_commit(B.bar(sh->s_full[s][k & 1]));
                         give_back();
                     }
