@@ -942,12 +942,14 @@ struct Wide : Stream<NB, BLK, true> {
     const uint32_t out;
     float m;                        // the row's reference (log2)
     float2 l[2];                    // its sum, in four parts
+    int token;                      // its token
+    int all;                        // keys that every row of the unit sees
 
     __device__ Wide(const Block<NB, BLK, WIDE> &b, uint32_t tmem0, int stream)
         : Base(b, tmem0, stream), out(tmem + O_COLUMN + static_cast<uint32_t>(stream) * 128u) {}
 
-    // Bit i: row `token` sees key at + i.
-    __device__ uint32_t sees_of(const Job &u, int token, int at) const {
+    // Bit i: the row sees key at + i.
+    __device__ uint32_t sees_of(const Job &u, int at) const {
         const int left = u.s.len - at, j = at - u.s.prefix;
         const uint32_t bits = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
         if (j + 32 <= 0) return bits;
@@ -967,10 +969,10 @@ struct Wide : Stream<NB, BLK, true> {
         return bits & static_cast<uint32_t>(w);
     }
 
-    __device__ void hide(const Job &u, int token, int at) const {
+    __device__ void hide(const Job &u, int at) const {
 #pragma unroll 1
         for (int h = 0; h < KEYS; h += 32) {
-            const uint32_t bits = sees_of(u, token, at + h);
+            const uint32_t bits = sees_of(u, at + h);
             if (__all_sync(0xffffffffu, bits == ~0u)) continue;
 #pragma unroll
             for (int c = 0; c < 32; c += 16) {
@@ -1032,7 +1034,7 @@ struct Wide : Stream<NB, BLK, true> {
     }
 
     // The product of a tile with values that are not finite, from the weights as they were rounded.
-    __device__ bool product(const Job &u, int token, uint32_t pos, int at, bool first) {
+    __device__ bool product(const Job &u, uint32_t pos, int at, bool first) {
         if (!vote(odd_values(pos, at + key, u.s.len))) return false;
 #pragma unroll 1
         for (int c = 0; c < a.d; c += 16) {
@@ -1047,7 +1049,7 @@ struct Wide : Stream<NB, BLK, true> {
             }
 #pragma unroll 1
             for (int h = 0; h < KEYS; h += 16) {
-                const uint32_t bits = sees_of(u, token, at + (h & ~31)) >> (h & 16);
+                const uint32_t bits = sees_of(u, at + (h & ~31)) >> (h & 16);
                 uint32_t w[8];
                 ptx::tmem_ld_32x32b_x8(scores + h / 2, w);
                 ptx::tmem_ld_wait(w);
@@ -1073,7 +1075,9 @@ struct Wide : Stream<NB, BLK, true> {
         return true;
     }
 
-    __device__ void start() {
+    __device__ void start(const Job &u) {
+        token = (u.row0 + min(key, u.rows - 1)) / a.group;
+        all = min(u.s.len, a.tree ? u.s.prefix : u.s.prefix + u.row0 / a.group + 1);
         m = -INFINITY;
         l[0] = l[1] = make_float2(0.0f, 0.0f);
     }
@@ -1086,11 +1090,9 @@ struct Wide : Stream<NB, BLK, true> {
         scores = tmem + static_cast<uint32_t>(i & 1) * 128u;
         __syncwarp();
         ptx::tc_fence_after();
-        const int at = (u.tile0 + i) * KEYS, token = (u.row0 + min(key, u.rows - 1)) / a.group;
-        // keys that every row of the unit sees
-        const int all = min(u.s.len, a.tree ? u.s.prefix : u.s.prefix + u.row0 / a.group + 1);
+        const int at = (u.tile0 + i) * KEYS;
         const bool masked = at + KEYS > all;
-        if (masked) hide(u, token, at);
+        if (masked) hide(u, at);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         {
             uint32_t x[2][32];
@@ -1109,7 +1111,7 @@ struct Wide : Stream<NB, BLK, true> {
         if (NB > 1 && k > 0) wait_out();
         if (__any_sync(0xffffffffu, most > m + RENEW)) renew(most, k > 0);
         form();
-        const bool own = masked && product(u, token, pos, at, k == 0);
+        const bool own = masked && product(u, pos, at, k == 0);
         if (key == 0) sh->skip[s] = own;
         if (masked) ptx::fence_proxy_async_smem();  // values that were cleared
         ptx::tc_fence_before();
@@ -1260,7 +1262,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
     while (u.tiles > 0) {
         if (!loaded && st.queries(u)) st.have_q();
         const int n = u.tiles, rows = u.rows, tiles = st.part(u).tiles;
-        st.start();
+        st.start(u);
 #pragma unroll 1
         for (int k = 0; k < tiles; ++k) {
             const int i = NB == 1 ? 2 * k + s : k;
@@ -1296,7 +1298,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
         if (two) total = total * f0 + __uint_as_float(ml1[1]) * f1;
         const bool have = key < rows;
         const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + u.place) * (2 * COLS) + key;
-        const int r = u.row0 + key, token = r / a.group;
+        const int r = u.row0 + key, token = st.token;  // (of rows that there are)
         float *part_row = a.part + piece * a.d;
         __nv_bfloat16 *o_row = static_cast<__nv_bfloat16 *>(a.o) +
                                (static_cast<int64_t>(u.s.q0 + token) * a.heads + u.head * a.group + (r - token * a.group)) * a.d;
