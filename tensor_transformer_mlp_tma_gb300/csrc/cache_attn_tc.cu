@@ -1253,6 +1253,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
     Wide<NB, BLK> st(B, tmem, s);
     const int key = st.key;
     uint32_t v_pos = 0;  // slots of V so far
+    uint32_t other = 0;  // NB = 1: phase of the other stream's scores
     Jobs<NB, BLK, true> jobs = {B, {}};
     Job u;
     auto both_vote = [&](bool x) { return ptx::barrier_or(3, 256, x); };
@@ -1269,6 +1270,20 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
             st.tile(u, i, k, v_pos + i * NB);
         }
         v_pos += n * NB;
+        // The next unit's queries are on their way as soon as the last scores, this stream's or the other's, are complete.
+        Job ahead;
+        bool coming = false;
+        if (NB == 1) {
+            const int count = s == 0 ? n / 2 : (n + 1) / 2;  // tiles of the other stream
+            if (((n - 1) & 1) != s) st.failed = !B.wait(B.bar(B.sh->s_full[1 - s][0]), (other + count - 1) & 1u) || st.failed;
+            other = (other + count) & 1u;
+            if (__all_sync(0xffffffffu, !st.failed)) {
+                if (jobs.peek_next(ahead))
+                    coming = st.queries(ahead);
+                else
+                    st.failed = true;
+            }
+        }
         if (tiles > 0) st.wait_out();
         // the row's reference and sum, to both streams (in place of scores)
         {
@@ -1279,10 +1294,10 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
         }
         if (both_vote(st.failed)) return;
         ptx::tc_fence_after();
-        // both streams' scores are complete: the next unit's queries
-        Job ahead;
-        if (both_vote(!jobs.peek_next(ahead))) return;
-        const bool coming = st.queries(ahead);
+        if (NB > 1) {
+            if (both_vote(!jobs.peek_next(ahead))) return;
+            coming = st.queries(ahead);
+        }
         loaded = true;
         jobs.read(u, jobs.at.slot);
         // streams that shared the tiles out are added up; each writes half of the components
@@ -1292,6 +1307,8 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
         if (two) ptx::tmem_ld_32x32b_x8(st.tmem + 128, ml1);
         ptx::tmem_ld_wait(ml0);
         if (two) ptx::tmem_ld_wait(ml1);
+        ptx::tc_fence_before();
+        if (NB == 1 && coming) st.have_q();  // (the next scores come while the outputs are written)
         const float m0 = __uint_as_float(ml0[0]), m1 = two ? __uint_as_float(ml1[0]) : m0, top = two ? fmaxf(m0, m1) : m0;
         float f0 = two ? scale_of(m0, top) : 1.0f, f1 = two ? scale_of(m1, top) : 0.0f;
         float total = __uint_as_float(ml0[1]);
@@ -1338,7 +1355,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
             }
         }
         ptx::tc_fence_before();
-        if (coming) st.have_q();
+        if (NB > 1 && coming) st.have_q();
         if (u.cut && u.place == 1) {
             if (threadIdx.x == 0) post_cut(a, u.s.q0, u.head, u.row0, u.rows, u.last);
             posted = true;
@@ -1408,6 +1425,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         copy_role<NB, BLK, WIDE>(B, warp == 10, warp == 10 ? &mv : &mk, box);
     else
         plan_role<NB, BLK, WIDE>(B, walk);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
