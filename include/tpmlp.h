@@ -516,7 +516,7 @@ typedef struct {
     int32_t heads;      /* a multiple of the cache's kv_heads */
     int32_t tree_words; /* with a tree: >= 1 */
     int32_t algo;       /* tpmlp_algo */
-    float scale;        /* of the scores; finite */
+    float scale;        /* of the scores; finite, times log2(e) too */
 } tpmlp_cache_attn_shape;
 
 /* Bytes of device workspace (status word, pieces of sequences that several blocks share); 256-byte aligned,

@@ -1881,7 +1881,7 @@ struct HeadSpan {
     bool sound() const {
         if (shards > 1 && (h->shard < width || h->shard > (1LL << 27))) return false;
         const int64_t row = (shards - 1) * (shards > 1 ? h->shard : 0) + width;
-        return rows <= 1 || (h->row >= row && h->row <= (1LL << 40));
+        return rows <= 1 || (h->row >= row && h->row <= (1LL << 40) && rows <= (1LL << 60) / h->row);
     }
     bool same(const HeadSpan &o) const {
         return begin() == o.begin() && width == o.width && (rows <= 1 || h->row == o.h->row) &&
@@ -2012,7 +2012,8 @@ bool cache_attn_valid(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c) 
     if (s->tokens > (1LL << 31) - 1 || s->tokens * s->heads >= (1LL << 31)) return false;
     if (s->max_pages > (1LL << 31) || s->max_pages * c->page_size >= (1LL << 31) - 1024) return false;
     if (s->algo != TPMLP_ALGO_DEFAULT && s->algo != TPMLP_ALGO_SIMT) return false;
-    return s->tree_words >= 0 && std::isfinite(s->scale);
+    // (the kernels multiply by scale log2(e))
+    return s->tree_words >= 0 && std::isfinite(s->scale) && std::isfinite(s->scale * 1.44269504f);
 }
 
 // status (1 KB) | cut units | statistics | pieces.  Room for either kernel: which one runs depends on the
