@@ -20,15 +20,17 @@
 // More rows (Wide): S [rows, keys] = Q K^T, O [rows, d] += P V, a thread holding a row: maximum and sum are
 // its own, masks are a row's 32 bits at a time, and the weights go back to tensor memory in place of the
 // scores, as the second product's first operand: shared memory, which the products' operands keep busy,
-// carries half as much as with the weights in it (128 rows and 8192 keys: 376 us instead of 622 for
-// 4 prompt chunks of 300 to 512 tokens, 1.18 PFLOP/s).
+// carries half as much as with the weights in it.  4 prompt chunks of 300 to 512 tokens over 3000 to 8192 keys,
+// 64 heads on 8 of 128 components: 352 us, 1.26 PFLOP/s; with the weights in shared memory 622.
 //
 // In both the weights are 2^(s - m) with a reference m that is only renewed when some score of the tile is
 // above it by more than 2^8: bf16 weights and fp32 sums hold 2^8 as well as 1, and outputs are
 // scaled a few times per row instead of once per tile.
 //
-// Narrow is bound by reading the cache (64 sequences of one token, 1.19 GB: 185 us, 6.4 TB/s); Wide by the turns of
-// a stream between its products and its exponentials: 1.18 PFLOP/s, 61 % of a large library product.
+// Narrow is bound by reading the cache: 64 sequences of one token, 1.19 GB: 185 us, 6.4 TB/s.  Wide is bound by the
+// turns of a stream between its products and its exponentials, of about 1700 cycles each for a tile (the products of
+// both streams' tiles alone are 1060), and at the units' ends by the outputs' way to memory.
+// The kernel's start, until the first scores, is 4 us: one sequence of one token takes 16 us with the join.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1107,7 +1109,7 @@ struct Wide : Stream<NB, BLK, true> {
             }
         }
         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(a.scale_log2);
-        // (NB = 1: these scores were issued behind the stream's product before them, whose end they come with)
+        // (NB = 1: the scores come with the end of the stream's product before them, which was issued before)
         if (NB > 1 && k > 0) wait_out();
         if (__any_sync(0xffffffffu, most > m + RENEW)) renew(most, k > 0);
         form();
