@@ -62,14 +62,6 @@ __device__ __forceinline__ bool visible(const CacheAttnArgs &a, const Seq &s, in
     return (a.tree[static_cast<int64_t>(s.q0 + token) * a.tree_words + (j >> 6)] >> (j & 63)) & 1;
 }
 
-// The page of a key, or -1 where the table holds none.
-__device__ __forceinline__ int page_of(const CacheAttnArgs &a, int64_t b, int64_t page) {
-    const int p = a.table[b * a.max_pages + page];
-    if (p >= 0 && p < a.pages) return p;
-    report(a, STATUS_INVALID, static_cast<uint32_t>(b));
-    return -1;
-}
-
 // Tokens that rows 0 .. rows - 1 reach into: rows / group, rounded up.
 __device__ __forceinline__ int tokens_of(const CacheAttnArgs &a, int rows) { return (rows + a.group - 1) / a.group; }
 

@@ -5,6 +5,9 @@
 //   maximum m and sum l of each row:  m' = max(m, max s),  l' = l 2^(m - m') + sum 2^(s - m'),
 //   O' = O 2^(m - m') + P V,  s in units of log2.
 //
+// K of the next tile is on its way while the weights and outputs of one are formed, V while the scores are
+// (fp32 rows on 16 bytes: by asynchronous copies; two blocks per SM hide the rest).
+//
 // A block takes 32 rows (tokens and the heads that share their keys) and 64 keys at a time, all
 // of them in shared memory in fp32.  Many rows are bound by the FFMA rate and by shared memory: a thread
 // forms up to 8 scores of one key, then 4 x 4 outputs (prompt chunks in fp32: 11 TFLOP/s); few by the latency
@@ -14,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "cache_attn.cuh"
 #include "launch.cuh"
@@ -45,7 +49,7 @@ template <typename E>
 __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
     extern __shared__ float4 smem4[];
     __shared__ typename Walk<SR, SK>::Shared wsh;
-    __shared__ int64_t where[SK];
+    __shared__ int64_t where_sh[2][SK];
     const int d = a.d, quads = d / 4, kld = d + 4;
     float *Q = reinterpret_cast<float *>(smem4), *K = Q + SR * d, *V = K + SK * kld, *P = V + SK * d;
     float *m_sh = P + SK * P_LD, *l_sh = m_sh + SR, *f_sh = l_sh + SR;
@@ -61,6 +65,26 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
     while (cols < quads) cols *= 2;
     // (at most 32 groups: their sums are added up in the space of K, V and P, 128 d floats and more)
     const int groups = min(STHREADS / cols, 32), col = tid & (cols - 1), group = tid / cols;
+
+    // K or V of a tile into shared memory, rows `ld` apart
+    auto copy = [&](float *to, int ld, const void *base, const int64_t *where) {
+        if (col < quads)
+#pragma unroll 4
+            for (int key = tid / cols; key < SK; key += STHREADS / cols) {
+                const int64_t off = where[key];
+                const E *from = static_cast<const E *>(base) + (off >= 0 ? off + 4 * col : 0);
+                float *at = to + key * ld + 4 * col;
+                if constexpr (std::is_same<E, float>::value) {
+                    if (a.vec) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(at)), "l"(from), "r"(off >= 0 ? 16u : 0u)
+                                     : "memory");
+                        continue;
+                    }
+                }
+                *reinterpret_cast<float4 *>(at) = off >= 0 ? get4(from, a.vec) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 
     bool posted = false;
     Unit u;
@@ -84,32 +108,33 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
             *reinterpret_cast<float4 *>(Q + row * d + e) = x;
         }
         if (tid < SR) m_sh[tid] = -INFINITY, l_sh[tid] = 0.0f;
+        // where a tile's keys lie: the page is looked up early, and used after the scores of the tile before
+        auto look = [&](int t) {
+            const int key = t * SK + tid;
+            return tid < SK && key < u.s.len ? a.table[u.b * a.max_pages + static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size)] : -1;
+        };
+        auto place = [&](int t, int page) {
+            const int key = t * SK + tid;
+            if (tid >= SK) return;
+            int64_t off = -1;  // no key: zeros
+            if (key < u.s.len) {
+                if (page >= 0 && page < a.pages)
+                    off = page * a.page_stride + u.head * a.head_stride +
+                          static_cast<uint32_t>(key) % static_cast<uint32_t>(a.page_size) * a.token_stride;
+                else
+                    report(a, STATUS_INVALID, static_cast<uint32_t>(u.b));
+            }
+            where_sh[t & 1][tid] = off;
+        };
+        place(u.tile0, look(u.tile0));
+        __syncthreads();
+        copy(K, kld, a.k, where_sh[u.tile0 & 1]);
+        copy(V, d, a.v, where_sh[u.tile0 & 1]);
         for (int t = u.tile0; t < u.tile0 + u.tiles; ++t) {
             const int key0 = t * SK;
-            const bool masked = key0 + SK > u.s.prefix;
-            __syncthreads();
-            if (tid < SK) {
-                int64_t off = -1;  // no key: zeros
-                if (key0 + tid < u.s.len) {
-                    const int64_t at = (key0 + tid) / a.page_size;
-                    const int page = page_of(a, u.b, at);
-                    if (page >= 0)
-                        off = page * a.page_stride + u.head * a.head_stride + (key0 + tid - at * a.page_size) * a.token_stride;
-                }
-                where[tid] = off;
-            }
-            __syncthreads();
-            for (int i = tid; i < SK * quads; i += STHREADS) {
-                const int key = i / quads, e = (i - key * quads) * 4;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
-                const int64_t off = where[key];
-                if (off >= 0) {
-                    x = get4(static_cast<const E *>(a.k) + off + e, a.vec);
-                    y = get4(static_cast<const E *>(a.v) + off + e, a.vec);
-                }
-                *reinterpret_cast<float4 *>(K + key * kld + e) = x;
-                *reinterpret_cast<float4 *>(V + key * d + e) = y;
-            }
+            const bool masked = key0 + SK > u.s.prefix, more = t + 1 < u.tile0 + u.tiles;
+            const int page = more ? look(t + 1) : -1;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
             __syncthreads();
             {
                 // scores of one key and rows rg, rg + 4, ...
@@ -135,7 +160,10 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                         P[key * P_LD + row] = !seen ? -INFINITY : (x == -INFINITY ? -3.4e38f : x);
                     }
             }
+            if (more) place(t + 1, page);
             __syncthreads();
+            if (more) copy(K, kld, a.k, where_sh[(t + 1) & 1]);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
             for (int row = warp; row < u.rows; row += STHREADS / 32) {
                 const float s0 = P[lane * P_LD + row], s1 = P[(lane + 32) * P_LD + row];
                 float top = fmaxf(s0, s1);
@@ -155,22 +183,29 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                     f_sh[row] = f, m_sh[row] = mn, l_sh[row] = l_sh[row] * f + sum;
                 }
             }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
             __syncthreads();
-            if (mine) {
+            if (mine && quad0 < rq) {
+                const int quad1 = quad0 + groups < rq ? quad0 + groups : quad0;
+                const bool two = quad1 != quad0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int quad = quad0 + h * groups;
-                    if (quad >= rq) continue;
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float f = 4 * quad + r < u.rows ? f_sh[4 * quad + r] : 1.0f;
+                        const int row = 4 * (h == 0 ? quad0 : quad1) + r;
+                        const float f = row < u.rows ? f_sh[row] : 1.0f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) acc[h][r][c] *= f;
                     }
-                    for (int key = kg; key < SK; key += key_groups) {
-                        const float4 p = *reinterpret_cast<const float4 *>(P + key * P_LD + 4 * quad);
-                        const float4 v = *reinterpret_cast<const float4 *>(V + key * d + 4 * col);
-                        const float pr[4] = {p.x, p.y, p.z, p.w}, vc[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 4
+                for (int key = kg; key < SK; key += key_groups) {
+                    const float4 v = *reinterpret_cast<const float4 *>(V + key * d + 4 * col);
+                    const float vc[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1 && !two) continue;
+                        const float4 p = *reinterpret_cast<const float4 *>(P + key * P_LD + 4 * (h == 0 ? quad0 : quad1));
+                        const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             if (!masked || !(pr[r] < 0.0f)) {
@@ -180,6 +215,8 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                     }
                 }
             }
+            __syncthreads();  // V is free
+            if (more) copy(V, d, a.v, where_sh[(t + 1) & 1]);
         }
         __syncthreads();
         // the key groups' sums, through the space of K
