@@ -29,7 +29,7 @@ namespace cattn {
 constexpr int SR = CACHE_ATTN_SIMT_ROWS;
 constexpr int SK = 64;
 constexpr int STHREADS = 256;
-constexpr int P_LD = SR + 4;
+constexpr int P_LD = SK + 4;
 
 __device__ __forceinline__ float4 get4(const float *p, bool vec) {
     return vec ? *reinterpret_cast<const float4 *>(p) : make_float4(p[0], p[1], p[2], p[3]);
@@ -42,7 +42,22 @@ __device__ __forceinline__ float4 get4(const __nv_bfloat16 *p, bool vec) {
 }
 
 inline size_t simt_smem(int d) {
-    return sizeof(float) * (static_cast<size_t>(SR) * d + SK * (d + 4) + SK * d + SK * P_LD + 3 * SR);
+    return sizeof(float) * (static_cast<size_t>(SR) * d + SK * (d + 4) + SK * d + SR * P_LD + 3 * SR);
+}
+
+// Scores of a key and NR rows, four apart from q on.  (A constant number of them: with a test per row the rows' loads
+// wait for one another.)
+template <int NR>
+__device__ __forceinline__ void scores(float (&s)[SR / 4], const float *q, const float *k, int d) {
+#pragma unroll 2
+    for (int e = 0; e < d; e += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(k + e);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(q + 4 * i * d + e);
+            s[i] += y.x * x.x + y.y * x.y + (y.z * x.z + y.w * x.w);
+        }
+    }
 }
 
 template <typename E>
@@ -52,7 +67,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
     __shared__ int64_t where_sh[2][SK];
     const int d = a.d, quads = d / 4, kld = d + 4;
     float *Q = reinterpret_cast<float *>(smem4), *K = Q + SR * d, *V = K + SK * kld, *P = V + SK * d;
-    float *m_sh = P + SK * P_LD, *l_sh = m_sh + SR, *f_sh = l_sh + SR;
+    float *m_sh = P + SR * P_LD, *l_sh = m_sh + SR, *f_sh = l_sh + SR;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -141,15 +156,14 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                 const int key = tid & (SK - 1), rg = tid / SK;
                 float s[SR / 4] = {};
                 const int nr = (u.rows + 3) / 4;
-                for (int e = 0; e < d; e += 4) {
-                    const float4 k = *reinterpret_cast<const float4 *>(K + key * kld + e);
-#pragma unroll
-                    for (int i = 0; i < SR / 4; ++i)
-                        if (i < nr) {
-                            const float4 q = *reinterpret_cast<const float4 *>(Q + (rg + 4 * i) * d + e);
-                            s[i] += q.x * k.x + q.y * k.y + (q.z * k.z + q.w * k.w);
-                        }
-                }
+                if (nr == 1)
+                    scores<1>(s, Q + rg * d, K + key * kld, d);
+                else if (nr == 2)
+                    scores<2>(s, Q + rg * d, K + key * kld, d);
+                else if (nr <= 4)
+                    scores<4>(s, Q + rg * d, K + key * kld, d);
+                else
+                    scores<8>(s, Q + rg * d, K + key * kld, d);
 #pragma unroll
                 for (int i = 0; i < SR / 4; ++i)
                     if (i < nr) {
@@ -157,7 +171,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                         const bool seen = row < u.rows && (!masked || visible(a, u.s, (u.row0 + row) / a.group, key0 + key));
                         // -inf marks what the row does not see: a score is raised to the lowest finite number
                         const float x = s[i] * a.scale_log2;
-                        P[key * P_LD + row] = !seen ? -INFINITY : (x == -INFINITY ? -3.4e38f : x);
+                        P[row * P_LD + key] = !seen ? -INFINITY : (x == -INFINITY ? -3.4e38f : x);
                     }
             }
             if (more) place(t + 1, page);
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
             if (more) copy(K, kld, a.k, where_sh[(t + 1) & 1]);
             else asm volatile("cp.async.commit_group;" ::: "memory");
             for (int row = warp; row < u.rows; row += STHREADS / 32) {
-                const float s0 = P[lane * P_LD + row], s1 = P[(lane + 32) * P_LD + row];
+                const float s0 = P[row * P_LD + lane], s1 = P[row * P_LD + lane + 32];
                 float top = fmaxf(s0, s1);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -175,8 +189,8 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                 float sum = (s0 == -INFINITY ? 0.0f : p0) + (s1 == -INFINITY ? 0.0f : p1);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                P[lane * P_LD + row] = p0;
-                P[(lane + 32) * P_LD + row] = p1;
+                P[row * P_LD + lane] = p0;
+                P[row * P_LD + lane + 32] = p1;
                 __syncwarp();
                 if (lane == 0) {
                     const float f = scale_of(m, mn);
@@ -197,21 +211,26 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) acc[h][r][c] *= f;
                     }
-#pragma unroll 4
-                for (int key = kg; key < SK; key += key_groups) {
-                    const float4 v = *reinterpret_cast<const float4 *>(V + key * d + 4 * col);
-                    const float vc[4] = {v.x, v.y, v.z, v.w};
+                for (int key = 4 * kg; key < SK; key += 4 * key_groups) {
+                    float4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(V + (key + k) * d + 4 * col);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h == 1 && !two) continue;
-                        const float4 p = *reinterpret_cast<const float4 *>(P + key * P_LD + 4 * (h == 0 ? quad0 : quad1));
-                        const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (!masked || !(pr[r] < 0.0f)) {
+                        for (int r = 0; r < 4; ++r) {
+                            const float4 p = *reinterpret_cast<const float4 *>(P + (4 * (h == 0 ? quad0 : quad1) + r) * P_LD + key);
+                            const float pk[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) acc[h][r][c] += pr[r] * vc[c];
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                if (!masked || !(pk[k] < 0.0f)) {
+                                    acc[h][r][0] += pk[k] * v[k].x;
+                                    acc[h][r][1] += pk[k] * v[k].y;
+                                    acc[h][r][2] += pk[k] * v[k].z;
+                                    acc[h][r][3] += pk[k] * v[k].w;
+                                }
+                        }
                     }
                 }
             }
