@@ -28,7 +28,7 @@ namespace cattn {
 
 constexpr int SR = CACHE_ATTN_SIMT_ROWS;
 constexpr int SK = 64;
-constexpr int STHREADS = 256;
+constexpr int STHREADS = 256, WARPS = STHREADS / 32;
 constexpr int P_LD = SK + 4;
 
 __device__ __forceinline__ float4 get4(const float *p, bool vec) {
@@ -57,6 +57,77 @@ __device__ __forceinline__ void scores(float (&s)[SR / 4], const float *q, const
             const float4 y = *reinterpret_cast<const float4 *>(q + 4 * i * d + e);
             s[i] += y.x * x.x + y.y * x.y + (y.z * x.z + y.w * x.w);
         }
+    }
+}
+
+// Weights of a tile in place of its scores, and the rows' new maxima, sums and factors; a warp takes NR rows, eight apart,
+// side by side.
+template <int NR>
+__device__ __forceinline__ void weights(float *P, float *m_sh, float *l_sh, float *f_sh, int warp, int lane, int rows) {
+    float s[NR][2], top[NR], sum[NR], m[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int row = warp + WARPS * i;
+        const bool have = row < rows;
+        s[i][0] = have ? P[row * P_LD + lane] : -INFINITY;
+        s[i][1] = have ? P[row * P_LD + lane + 32] : -INFINITY;
+        m[i] = have ? m_sh[row] : -INFINITY;
+        top[i] = fmaxf(s[i][0], s[i][1]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int row = warp + WARPS * i;
+        top[i] = fmaxf(m[i], top[i]);
+        // masked weights are marked by a negative number, not by zero: 0 x NaN would be NaN
+        const float p0 = s[i][0] == -INFINITY ? -1.0f : exp2f(s[i][0] - top[i]), p1 = s[i][1] == -INFINITY ? -1.0f : exp2f(s[i][1] - top[i]);
+        sum[i] = (s[i][0] == -INFINITY ? 0.0f : p0) + (s[i][1] == -INFINITY ? 0.0f : p1);
+        if (row < rows) {
+            P[row * P_LD + lane] = p0;
+            P[row * P_LD + lane + 32] = p1;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    __syncwarp();
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int row = warp + WARPS * i;
+            if (row < rows) {
+                const float f = scale_of(m[i], top[i]);
+                f_sh[row] = f, m_sh[row] = top[i], l_sh[row] = l_sh[row] * f + sum[i];
+            }
+        }
+}
+
+// Outputs of row quads quad0 and (TWO) quad1 from the keys of a group, four at a time.
+template <bool TWO, bool MASKED>
+__device__ __forceinline__ void outputs(float (&acc)[2][4][4], const float *P, const float *V, int d, int quad0, int quad1, int kg, int key_groups) {
+    for (int key = 4 * kg; key < SK; key += 4 * key_groups) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(V + (key + k) * d);
+#pragma unroll
+        for (int h = 0; h < (TWO ? 2 : 1); ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 p = *reinterpret_cast<const float4 *>(P + (4 * (h == 0 ? quad0 : quad1) + r) * P_LD + key);
+                const float pk[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (!MASKED || !(pk[k] < 0.0f)) {
+                        acc[h][r][0] += pk[k] * v[k].x;
+                        acc[h][r][1] += pk[k] * v[k].y;
+                        acc[h][r][2] += pk[k] * v[k].z;
+                        acc[h][r][3] += pk[k] * v[k].w;
+                    }
+            }
     }
 }
 
@@ -178,25 +249,10 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
             __syncthreads();
             if (more) copy(K, kld, a.k, where_sh[(t + 1) & 1]);
             else asm volatile("cp.async.commit_group;" ::: "memory");
-            for (int row = warp; row < u.rows; row += STHREADS / 32) {
-                const float s0 = P[row * P_LD + lane], s1 = P[row * P_LD + lane + 32];
-                float top = fmaxf(s0, s1);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m = m_sh[row], mn = fmaxf(m, top);
-                // masked weights are marked by a negative number, not by zero: 0 x NaN would be NaN
-                const float p0 = s0 == -INFINITY ? -1.0f : exp2f(s0 - mn), p1 = s1 == -INFINITY ? -1.0f : exp2f(s1 - mn);
-                float sum = (s0 == -INFINITY ? 0.0f : p0) + (s1 == -INFINITY ? 0.0f : p1);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                P[row * P_LD + lane] = p0;
-                P[row * P_LD + lane + 32] = p1;
-                __syncwarp();
-                if (lane == 0) {
-                    const float f = scale_of(m, mn);
-                    f_sh[row] = f, m_sh[row] = mn, l_sh[row] = l_sh[row] * f + sum;
-                }
-            }
+            if (u.rows <= WARPS)
+                weights<1>(P, m_sh, l_sh, f_sh, warp, lane, u.rows);
+            else
+                weights<SR / WARPS>(P, m_sh, l_sh, f_sh, warp, lane, u.rows);
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
             __syncthreads();
             if (mine && quad0 < rq) {
@@ -211,28 +267,13 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) acc[h][r][c] *= f;
                     }
-                for (int key = 4 * kg; key < SK; key += 4 * key_groups) {
-                    float4 v[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(V + (key + k) * d + 4 * col);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h == 1 && !two) continue;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float4 p = *reinterpret_cast<const float4 *>(P + (4 * (h == 0 ? quad0 : quad1) + r) * P_LD + key);
-                            const float pk[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (!masked || !(pk[k] < 0.0f)) {
-                                    acc[h][r][0] += pk[k] * v[k].x;
-                                    acc[h][r][1] += pk[k] * v[k].y;
-                                    acc[h][r][2] += pk[k] * v[k].z;
-                                    acc[h][r][3] += pk[k] * v[k].w;
-                                }
-                        }
-                    }
-                }
+                const float *v = V + 4 * col;
+                if (two)
+                    masked ? outputs<true, true>(acc, P, v, d, quad0, quad1, kg, key_groups)
+                           : outputs<true, false>(acc, P, v, d, quad0, quad1, kg, key_groups);
+                else
+                    masked ? outputs<false, true>(acc, P, v, d, quad0, quad1, kg, key_groups)
+                           : outputs<false, false>(acc, P, v, d, quad0, quad1, kg, key_groups);
             }
             __syncthreads();  // V is free
             if (more) copy(V, d, a.v, where_sh[(t + 1) & 1]);
