@@ -9,10 +9,10 @@
 // (fp32 rows on 16 bytes: by asynchronous copies; two blocks per SM hide the rest).
 //
 // A block takes 32 rows (tokens and the heads that share their keys) and 64 keys at a time, all
-// of them in shared memory in fp32.  Many rows are bound by the FFMA rate and by shared memory: a thread
-// forms up to 8 scores of one key, then 4 x 4 outputs (prompt chunks in fp32: 11 TFLOP/s); few by the latency
-// of a tile's copy, its barriers and its sums, one after another (64 sequences of one token, 2.4 GB: 1.55 ms,
-// 1.5 TB/s).
+// of them in shared memory in fp32.  Many rows are bound by shared memory's rate and the FFMA rate: a thread
+// forms up to 8 scores of one key, then 4 x 4 outputs (4 prompt chunks of 300 to 512 tokens in fp32: 18.1 ms,
+// 25 TFLOP/s); few by the turns of a tile's copies, barriers and sums (64 sequences of one token, 2.4 GB: 545 us,
+// 4.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +46,7 @@ inline size_t simt_smem(int d) {
 }
 
 // Scores of a key and NR rows, four apart from q on.  (A constant number of them: with a test per row the rows' loads
-// wait for one another.)
+// waited for one another, and everything took twice as long.)
 template <int NR>
 __device__ __forceinline__ void scores(float (&s)[SR / 4], const float *q, const float *k, int d) {
 #pragma unroll 2
