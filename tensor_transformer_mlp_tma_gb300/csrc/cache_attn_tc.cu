@@ -850,6 +850,7 @@ struct Narrow : Stream<NB, BLK, false> {
                             o[j] = __float_as_uint(__uint_as_float(o[j]) + __uint_as_float(half << 16) * v);
                     }
                 }
+                __syncwarp();
                 ptx::tmem_st_32x32b_x16(out + nb * 2 * COLS + 16 * c, o);
             }
         }
@@ -1053,6 +1054,7 @@ struct Wide : Stream<NB, BLK, true> {
             for (int h = 0; h < KEYS; h += 16) {
                 const uint32_t bits = sees_of(u, at + (h & ~31)) >> (h & 16);
                 uint32_t w[8];
+                __syncwarp();
                 ptx::tmem_ld_32x32b_x8(scores + h / 2, w);
                 ptx::tmem_ld_wait(w);
 #pragma unroll
@@ -1236,6 +1238,7 @@ __device__ void narrow_role(const Block<NB, BLK, false> &B, uint32_t tmem, int s
                             if (c + j < rows) o[static_cast<int64_t>(static_cast<int>(to[j])) * a.d + e] = __float2bfloat16_rn(__uint_as_float(x[j]));
                     }
                 }
+                __syncwarp();  // (lanes without a component; tensor memory is read by whole warps)
             }
         }
         ptx::tc_fence_before();
@@ -1355,6 +1358,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
                 }
                 *reinterpret_cast<uint4 *>(o_row + c) = w;
             }
+            __syncwarp();  // (lanes without a row)
         }
         ptx::tc_fence_before();
         if (NB > 1 && coming) st.have_q();
