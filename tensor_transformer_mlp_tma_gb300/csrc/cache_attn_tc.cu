@@ -116,6 +116,8 @@ struct Block {
 
     __device__ uint32_t bar(const uint64_t &x) const { return ptx::smem_u32(&x); }
     __device__ bool wait(uint32_t bar, uint32_t parity) const {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (sh->abort) return false;
         // the clock is looked at only after many tries
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
@@ -124,7 +126,9 @@ struct Block {
         sh->abort = 1;
         return false;
     }
-    // The same for a whole warp.
+    // For copies and products under way when a wait has run out: 0.1 s at least, whatever the limit of waits.
+    __device__ uint64_t drain_ns() const { return a.wait_ns > 100000000ull ? a.wait_ns : 100000000ull; }
+    // `wait` for a whole warp.
     __device__ bool warp_wait(uint32_t bar, uint32_t parity) const {
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
         return __all_sync(0xffffffffu, wait(bar, parity));
@@ -314,7 +318,7 @@ __device__ void copy_role(const Block<NB, BLK, WIDE> &B, bool values, const CUte
         if (lane == 0) report(a, STATUS_TIMEOUT, 1);
         // copies in flight land before anything goes on
         for (int i = 0; i < slots; ++i)
-            if (copied >> i & 1u) ptx::mbar_wait(full0 + 8 * i, phases >> i & 1u, a.wait_ns, nullptr);
+            if (copied >> i & 1u) ptx::mbar_wait(full0 + 8 * i, phases >> i & 1u, B.drain_ns(), nullptr);
     }
 }
 
@@ -506,7 +510,7 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
         report(a, STATUS_TIMEOUT, 2);
         // products in flight end before shared and tensor memory are given back
         ptx::umma_commit(B.bar(sh->drain));
-        ptx::mbar_wait(B.bar(sh->drain), 0, a.wait_ns, nullptr);
+        ptx::mbar_wait(B.bar(sh->drain), 0, B.drain_ns(), nullptr);
     }
 }
 
