@@ -523,7 +523,7 @@ struct Stream {
     const Block<NB, BLK, WIDE> &B;
     const CacheAttnArgs &a;
     Small *sh;
-    const int s, warp, lane, key;   // stream; warp of it; key of a tile (TMEM lane)
+    const int s, warp, lane, key;   // stream; warp of it; TMEM lane: Narrow's key of a tile, Wide's row of the unit
     const uint32_t tmem, q;         // tensor memory from this warp's lanes on; this stream's queries
     uint32_t scores;                // of the tile at hand
     uint32_t s_phase = 0, o_phase = 0;  // s_phase: a bit per place
@@ -658,8 +658,9 @@ struct Narrow : Stream<NB, BLK, false> {
     // Lanes that share a key's line in add_up, eight rows each: 2, 4 or 8, as a power of two.
     static __device__ __forceinline__ int line_bits(int width) { return width <= 16 ? 1 : (width <= 32 ? 2 : 3); }
 
-    // Where tensor memory is full of outputs (NB = 2), a stream adds up the rounded weights itself, from their place: a lane takes eight rows of every
-    // (32 / lanes)-th key of its warp.  (Sums of all rows for its own key would be 64 registers.)
+    // Where tensor memory is full of outputs (NB = 2), a stream adds up the rounded weights itself, from their
+    // place: a lane takes eight rows of every (32 / lanes)-th key of its warp.  (Sums of all rows for its own
+    // key would be 64 registers.)
     __device__ void add_up(int width) {
         const int bits = line_bits(width), lanes = 1 << bits, chunk = lane & (lanes - 1);
         if (8 * chunk < width) {
