@@ -49,15 +49,19 @@ inline size_t simt_smem(int d) {
 // waited for one another, and everything took twice as long.)
 template <int NR>
 __device__ __forceinline__ void scores(float (&s)[SR / 4], const float *q, const float *k, int d) {
+    float2 t[NR] = {};  // sums of even and odd components: two products to an instruction
 #pragma unroll 2
     for (int e = 0; e < d; e += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(k + e);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const float4 y = *reinterpret_cast<const float4 *>(q + 4 * i * d + e);
-            s[i] += y.x * x.x + y.y * x.y + (y.z * x.z + y.w * x.w);
+            t[i] = ptx::fma2(make_float2(y.x, y.y), make_float2(x.x, x.y), t[i]);
+            t[i] = ptx::fma2(make_float2(y.z, y.w), make_float2(x.z, x.w), t[i]);
         }
     }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) s[i] = t[i].x + t[i].y;
 }
 
 // Weights of a tile in place of its scores, and the rows' new maxima, sums and factors; a warp takes NR rows, eight apart,
@@ -108,7 +112,7 @@ __device__ __forceinline__ void weights(float *P, float *m_sh, float *l_sh, floa
 
 // Outputs of row quads quad0 and (TWO) quad1 from the keys of a group, four at a time.
 template <bool TWO, bool MASKED>
-__device__ __forceinline__ void outputs(float (&acc)[2][4][4], const float *P, const float *V, int d, int quad0, int quad1, int kg, int key_groups) {
+__device__ __forceinline__ void outputs(float2 (&acc)[2][4][2], const float *P, const float *V, int d, int quad0, int quad1, int kg, int key_groups) {
     for (int key = 4 * kg; key < SK; key += 4 * key_groups) {
         float4 v[4];
 #pragma unroll
@@ -122,10 +126,9 @@ __device__ __forceinline__ void outputs(float (&acc)[2][4][4], const float *P, c
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (!MASKED || !(pk[k] < 0.0f)) {
-                        acc[h][r][0] += pk[k] * v[k].x;
-                        acc[h][r][1] += pk[k] * v[k].y;
-                        acc[h][r][2] += pk[k] * v[k].z;
-                        acc[h][r][3] += pk[k] * v[k].w;
+                        const float2 p2 = make_float2(pk[k], pk[k]);
+                        acc[h][r][0] = ptx::fma2(p2, make_float2(v[k].x, v[k].y), acc[h][r][0]);
+                        acc[h][r][1] = ptx::fma2(p2, make_float2(v[k].z, v[k].w), acc[h][r][1]);
                     }
             }
     }
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
         const int key_groups = rq2 < groups ? groups / rq2 : 1;
         const int quad0 = rq2 < groups ? group % rq2 : group, kg = rq2 < groups ? group / rq2 : 0;
         const bool mine = col < quads && group < groups;
-        float acc[2][4][4] = {};
+        float2 acc[2][4][2] = {};
         __syncthreads();  // the unit before is done with shared memory
         for (int i = tid; i < SR * quads; i += STHREADS) {
             const int row = i / quads, e = (i - row * quads) * 4;
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                         const int row = 4 * (h == 0 ? quad0 : quad1) + r;
                         const float f = row < u.rows ? f_sh[row] : 1.0f;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[h][r][c] *= f;
+                        for (int c = 0; c < 2; ++c) acc[h][r][c] = ptx::mul2(acc[h][r][c], make_float2(f, f));
                     }
                 const float *v = V + 4 * col;
                 if (two)
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     put4(sums + (((kg - 1) * rq2 + quad0) * 4 + r) * d + 4 * col,
-                         make_float4(acc[0][r][0], acc[0][r][1], acc[0][r][2], acc[0][r][3]));
+                         make_float4(acc[0][r][0].x, acc[0][r][0].y, acc[0][r][1].x, acc[0][r][1].y));
             }
             __syncthreads();
             if (mine && kg == 0) {
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float4 x = *reinterpret_cast<const float4 *>(sums + (((g - 1) * rq2 + quad0) * 4 + r) * d + 4 * col);
-                        acc[0][r][0] += x.x, acc[0][r][1] += x.y, acc[0][r][2] += x.z, acc[0][r][3] += x.w;
+                        acc[0][r][0] = ptx::add2(acc[0][r][0], make_float2(x.x, x.y)), acc[0][r][1] = ptx::add2(acc[0][r][1], make_float2(x.z, x.w));
                     }
             }
         }
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                 for (int r = 0; r < 4; ++r) {
                     const int row = 4 * quad + r;
                     if (quad >= rq || row >= u.rows) continue;
-                    float4 x = make_float4(acc[h][r][0], acc[h][r][1], acc[h][r][2], acc[h][r][3]);
+                    float4 x = make_float4(acc[h][r][0].x, acc[h][r][0].y, acc[h][r][1].x, acc[h][r][1].y);
                     if (u.cut) {
                         __stcg(reinterpret_cast<float4 *>(a.part + (piece + row) * d + 4 * col), x);
                     } else {
