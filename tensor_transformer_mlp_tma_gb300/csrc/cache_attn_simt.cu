@@ -9,10 +9,10 @@
 // (fp32 rows on 16 bytes: by asynchronous copies; two blocks per SM hide the rest).
 //
 // A block takes 32 rows (tokens and the heads that share their keys) and 64 keys at a time, all
-// of them in shared memory in fp32.  Many rows are bound by shared memory's rate and the FFMA rate: a thread
-// forms up to 8 scores of one key, then 4 x 4 outputs (4 prompt chunks of 300 to 512 tokens in fp32: 18.1 ms,
-// 25 TFLOP/s); few by the turns of a tile's copies, barriers and sums (64 sequences of one token, 2.4 GB: 545 us,
-// 4.4 TB/s).
+// of them in shared memory in fp32.  Many rows are bound by instructions and shared memory's rate (56 and 50 %
+// of the cycles before two products went to an instruction): a thread forms up to 8 scores of one key, then 4 x 4
+// outputs (4 prompt chunks of 300 to 512 tokens in fp32: 16.2 ms, 27 TFLOP/s); few by the turns of a tile's
+// copies, barriers and sums (64 sequences of one token, 2.4 GB: 515 us, 4.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
