@@ -756,6 +756,7 @@ def qk_forward(ctx: QkContext, QKV, position, gain_q=None, gain_k=None, out=None
     out: a tuple of [tokens, heads, dim] tensors, or an array laid out as QKV whose Q and K columns are
     written (QKV itself: in place) and which is then returned.  QKV, position and gains are kept, not
     copied, for qk_backward: they have to hold the same values then."""
+    ctx._saved = None  # (a call that is refused leaves no earlier pass to go back from)
     _qkv_input(ctx, QKV, False)
     given = _qk_inputs(ctx, position, gain_q, gain_k)
     result = _qk_out(ctx, out, ("Qr", "Kr"))
@@ -768,14 +769,24 @@ def qk_forward(ctx: QkContext, QKV, position, gain_q=None, gain_k=None, out=None
     return result
 
 
+def _written_over(ctx, *outputs):
+    """An output in the place of the saved Q or K, which a backward pass with the norm reads: there is no other one."""
+    if ctx._saved and ctx._norm and ctx._tokens:
+        for r, saved in zip(outputs, ctx._saved[1:3]):
+            if r.p == saved[0]:
+                ctx._saved = ()
+                return
+
+
 def qk_backward(ctx: QkContext, dQr, dKr, out=None, dgain_q=None, dgain_k=None, stream=None):
     """{"dQ", "dK", "dgain_q", "dgain_k"} from the gradients of what the last qk_forward of this context returned
     ([tokens, heads, dim] each).  out: as for qk_forward (an array laid out as QKV is returned as "dQKV"); it may be
-    what holds dQr and dKr.  The gains' entries are None without the norm."""
+    what holds dQr and dKr, or the QKV of the forward pass: with the norm there is no second backward pass then.  The
+    gains' entries are None without the norm."""
     if ctx._saved is None:
         raise ValueError("qk_backward needs a qk_forward of the same context before it")
     if not ctx._saved:
-        raise ValueError("qk_backward after a qk_forward with the norm in place: its inputs are gone")
+        raise ValueError("qk_backward after a pass with the norm that wrote in place of its inputs: they are gone")
     _, q, k, given = ctx._saved
     records, r = ctx._records, ctx._refs
     records[0].p, records[0].row, records[0].shard = q
@@ -799,6 +810,7 @@ def qk_backward(ctx: QkContext, dQr, dKr, out=None, dgain_q=None, dgain_k=None, 
         dgain_q = dgain_k = None
     _call(ctx, lib.tpmlp_qk_backward, "tpmlp_qk_backward",
           (ctx._shape_ref, r[0], r[1], *given, r[5], r[6], r[3], r[4], to_q, to_k, ctx.workspace.data_ptr()), stream)
+    _written_over(ctx, records[3], records[4])
     grads = {"dgain_q": dgain_q, "dgain_k": dgain_k}
     if isinstance(result, torch.Tensor):
         grads["dQKV"] = result
@@ -851,6 +863,7 @@ def kv_append(ctx: QkContext, cache: KvCache, QKV, position, slot, gain_q=None, 
     r = ctx._refs
     _call(ctx, lib.tpmlp_kv_append, "tpmlp_kv_append",
           (ctx._shape_ref, cache._ref, r[0], r[1], r[2], *given, slot.data_ptr(), r[3], ctx.workspace.data_ptr()), stream)
+    _written_over(ctx, ctx._records[3])
     return out
 
 
