@@ -508,6 +508,8 @@ tpmlp_status tpmlp_kv_append(const tpmlp_qk_shape *shape, const tpmlp_kv_cache *
  *   else:       those whose bit is set in tree[token][tree_words]: bit j % 64 of word j / 64 for the j-th new
  *               token of the sequence (a tree of drafts: a token's own bit and those of the tokens above it).
  * A row that sees nothing is zero.  What a row does not see has no part in it, whatever it holds (NaN, infinity).
+ * A visible score of minus infinity (of an infinite key, or past fp32's range) is a weight of zero, and a row all of whose
+ * visible scores are that is zero too.
  * Rows of O behind q_start[batch] stay as they are. */
 typedef struct {
     int64_t tokens;     /* T >= 0; tokens * heads < 2^31 */

@@ -30,6 +30,9 @@ constexpr int SR = CACHE_ATTN_SIMT_ROWS;
 constexpr int SK = 64;
 constexpr int STHREADS = 256, WARPS = STHREADS / 32;
 constexpr int P_LD = SK + 4;
+// Minus infinity in the place of a score says that the row does not see the key.  A visible score of minus infinity becomes
+// LOWEST; a row's maximum begins at the next number above it, 2^104 away: the weight is zero, whatever else the row sees.
+constexpr float LOWEST = -0x1.fffffep+127f, LEAST_MAXIMUM = -0x1.fffffcp+127f;
 
 __device__ __forceinline__ float4 get4(const float *p, bool vec) {
     return vec ? *reinterpret_cast<const float4 *>(p) : make_float4(p[0], p[1], p[2], p[3]);
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
             }
             *reinterpret_cast<float4 *>(Q + row * d + e) = x;
         }
-        if (tid < SR) m_sh[tid] = -INFINITY, l_sh[tid] = 0.0f;
+        if (tid < SR) m_sh[tid] = LEAST_MAXIMUM, l_sh[tid] = 0.0f;
         // where a tile's keys lie: the page is looked up early, and used after the scores of the tile before
         auto look = [&](int t) {
             const int key = t * SK + tid;
@@ -243,9 +246,8 @@ __global__ void __launch_bounds__(STHREADS) simt_kernel(const CacheAttnArgs a) {
                     if (i < nr) {
                         const int row = rg + 4 * i;
                         const bool seen = row < u.rows && (!masked || visible(a, u.s, (u.row0 + row) / a.group, key0 + key));
-                        // -inf marks what the row does not see: a score is raised to the lowest finite number
                         const float x = s[i] * a.scale_log2;
-                        P[row * P_LD + key] = !seen ? -INFINITY : (x == -INFINITY ? -3.4e38f : x);
+                        P[row * P_LD + key] = !seen ? -INFINITY : (x == -INFINITY ? LOWEST : x);
                     }
             }
             if (more) place(t + 1, page);
