@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(THREADS, 2) backward_kernel(const QkArgs a, co
                     dt += __shfl_xor_sync(0xffffffffu, dt, o);
                 }
                 const float r = rsqrtf(sq * inv_d + a.eps);
-                // r (dy g - x r mean(dy g x r)) = r dy g - (r^3 mean(dy g x)) x
-                const float m = -(r * r) * (r * (dt * inv_d));
+                // r (dy g - x r mean(dy g x r)), with no power of r above the first: r may be 1e20, or 1e-19
+                const float m = -r * (r * (dt * inv_d));
                 const float2 rr = make_float2(r, r), mm = make_float2(m, m);
 #pragma unroll
                 for (int i = 0; i < P; i += 2) {
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(THREADS, 2) backward_kernel(const QkArgs a, co
                         su[i / 2] = ptx::fma2(ui, ptx::mul2(xi, rr), su[i / 2]);
                         sv[i / 2] = ptx::fma2(vi, ptx::mul2(yi, rr), sv[i / 2]);
                     }
-                    const float2 x0 = ptx::fma2(ptx::mul2(ui, make_float2(gu[i], gu[i + 1])), rr, ptx::mul2(xi, mm));
-                    const float2 x1 = ptx::fma2(ptx::mul2(vi, make_float2(gv[i], gv[i + 1])), rr, ptx::mul2(yi, mm));
+                    const float2 x0 = ptx::mul2(ptx::fma2(ui, make_float2(gu[i], gu[i + 1]), ptx::mul2(xi, mm)), rr);
+                    const float2 x1 = ptx::mul2(ptx::fma2(vi, make_float2(gv[i], gv[i + 1]), ptx::mul2(yi, mm)), rr);
                     u[i] = x0.x, u[i + 1] = x0.y, v[i] = x1.x, v[i + 1] = x1.y;
                 }
             }
