@@ -406,7 +406,7 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *shape, const void *G, 
  *   (u, v) -> a (u cos f - v sin f, u sin f + v cos f),   f = position * theta_i
  * for the pairs (i, i + rot/2) of its first `rot` components (TPMLP_ROPE_HALF) or (2i, 2i + 1)
  * (TPMLP_ROPE_INTERLEAVED); the components behind them keep their normed values.  Computed in
- * fp32, the angles to 2^-26 of a turn at any position, rounded once. */
+ * fp32, rounded once; an angle is off by 2^-26 + 2^-32 + |position| 2^-65 of a turn at most: 2^-25 up to position 2^38. */
 typedef enum { TPMLP_ROPE_HALF = 0, TPMLP_ROPE_INTERLEAVED = 1 } tpmlp_rope_layout;
 
 /* Contexts longer than the trained one.  LINEAR: every theta_i divided by `factor`.  PARTS: a pair
@@ -424,7 +424,7 @@ typedef struct {
     int32_t scaling; /* tpmlp_rope_scaling */
 } tpmlp_rope;
 
-/* turns[rot/2] (host memory): theta_i / (2 pi) in units of 2^-64.  The kernels read a copy of them in
+/* turns[rot/2] (host memory): theta_i / (2 pi) in units of 2^-64, rounded to the nearest.  The kernels read a copy of them in
  * device memory.  INVALID_ARG for values out of range, or a theta_i that is not below 2 pi. */
 tpmlp_status tpmlp_rope_turns(const tpmlp_rope *rope, uint64_t *turns);
 

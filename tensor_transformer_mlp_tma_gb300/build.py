@@ -25,7 +25,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 VARIANTS = {LIB: [], LIB_DEBUG: ["-DTPMLP_DEBUG=1"]}
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# -ffp-contract=off: host arithmetic is the same on machines with and without fused multiply-add by default.
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+              "-Xcompiler", "-ffp-contract=off",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 

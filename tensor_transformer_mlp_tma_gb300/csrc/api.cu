@@ -18,6 +18,7 @@
 
 #include "kernels.h"
 #include "tpmlp.h"
+#include "twofold.h"
 
 namespace tpmlp {
 
@@ -2033,6 +2034,16 @@ CacheAttnLayout cache_attn_layout(const tpmlp_kv_cache *c) {
     return L;
 }
 
+// A fraction of a turn, 0 <= t < 1, in units of 2^-64, rounded.
+uint64_t units(tpmlp::Twofold t) {
+    const double hi = std::ldexp(t.hi, 64), whole = std::floor(hi);
+    const int64_t rest = std::llrint((hi - whole) + std::ldexp(t.lo, 64));
+    // (the leading part may be a whole turn that the other takes something from)
+    if (whole >= 18446744073709551616.0) return rest < 0 ? static_cast<uint64_t>(rest) : ~uint64_t{0};
+    const uint64_t n = static_cast<uint64_t>(whole), sum = n + static_cast<uint64_t>(rest);
+    return rest > 0 && sum < n ? ~uint64_t{0} : sum;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2048,18 +2059,21 @@ tpmlp_status tpmlp_rope_turns(const tpmlp_rope *r, uint64_t *turns) {
         return invalid("tpmlp_rope_turns: factor must be positive");
     if (parts && (!(r->low < r->high) || !std::isfinite(r->low) || !std::isfinite(r->high) || r->context <= 0))
         return invalid("tpmlp_rope_turns: scaling by parts needs low < high and a context");
-    const double two_pi = 2.0 * std::acos(-1.0);
+    // With doubles alone a position of 2^40 would be off by 2^-16 of a turn.
+    using tpmlp::Twofold;
+    const Twofold pi = tpmlp::pi_of(), two_pi = {2.0 * pi.hi, 2.0 * pi.lo}, one = {1.0, 0.0}, factor = {r->factor, 0.0};
+    const Twofold log_base = tpmlp::log_of(r->base);
     for (int i = 0; i < r->rot / 2; ++i) {
-        double f = std::pow(r->base, -2.0 * i / r->rot);
-        if (linear) f /= r->factor;
+        Twofold f = tpmlp::exp_of(log_base * Twofold{-2.0 * i, 0.0} / Twofold{static_cast<double>(r->rot), 0.0});
+        if (linear) f = f / factor;
         if (parts) {
-            const double n = static_cast<double>(r->context) * f / two_pi;
-            const double k = std::min(1.0, std::max(0.0, (n - r->low) / (r->high - r->low)));
-            f *= k + (1.0 - k) / r->factor;
+            const Twofold low = {r->low, 0.0}, n = Twofold{static_cast<double>(r->context), 0.0} * f / two_pi;
+            Twofold k = (n + -low) / (Twofold{r->high, 0.0} + -low);
+            k = k < Twofold{0.0, 0.0} ? Twofold{0.0, 0.0} : (one < k ? one : k);
+            f = f * (k + (one + -k) / factor);
         }
         if (!(f < two_pi)) return invalid("tpmlp_rope_turns: more than a turn per position");
-        const double t = std::ldexp(f / two_pi, 64);
-        turns[i] = t >= 18446744073709549568.0 ? ~uint64_t{0} : static_cast<uint64_t>(t);
+        turns[i] = units(f / two_pi);
     }
     return TPMLP_OK;
 }

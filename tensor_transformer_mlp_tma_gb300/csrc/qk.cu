@@ -7,8 +7,8 @@
 //              dg = sum dy x r,  dx = r (dy g - x r mean(dy g x r))
 //
 // Angles.  position * theta_i in fp32 is off by 2^-24 of itself: 0.06 radians at position 10^6.
-// theta_i is kept as turns in units of 2^-64, so that the product modulo 2^64 is the fraction of
-// a turn, exact to position * 2^-65; its upper 32 bits go to sincospif.
+// theta_i is kept as turns in units of 2^-64, rounded, so that the product modulo 2^64 is the fraction of
+// a turn, off by position * 2^-65 at most; its upper 32 bits go to sincospif.
 //
 // Bound by memory: 8192 tokens of 32 heads of 128 with as many key heads (bf16, norm and rotation) take 45 us forward
 // (0.27 GB, 6.0 TB/s) and 79 us backward (0.40 GB, 5.1 TB/s, with the gains' sums).  Each element is read once and
