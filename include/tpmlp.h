@@ -406,7 +406,7 @@ tpmlp_status tpmlp_orthogonalize(const tpmlp_ortho_shape *shape, const void *G, 
  *   (u, v) -> a (u cos f - v sin f, u sin f + v cos f),   f = position * theta_i
  * for the pairs (i, i + rot/2) of its first `rot` components (TPMLP_ROPE_HALF) or (2i, 2i + 1)
  * (TPMLP_ROPE_INTERLEAVED); the components behind them keep their normed values.  Computed in
- * fp32, rounded once; an angle is off by 2^-26 + 2^-32 + |position| 2^-65 of a turn at most: 2^-25 up to position 2^38. */
+ * fp32, rounded once; an angle is off by 2^-28 + 2^-34 + |position| 2^-65 of a turn at most: 2^-27 up to position 2^36. */
 typedef enum { TPMLP_ROPE_HALF = 0, TPMLP_ROPE_INTERLEAVED = 1 } tpmlp_rope_layout;
 
 /* Contexts longer than the trained one.  LINEAR: every theta_i divided by `factor`.  PARTS: a pair

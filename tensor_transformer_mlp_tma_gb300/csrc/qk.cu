@@ -8,7 +8,7 @@
 //
 // Angles.  position * theta_i in fp32 is off by 2^-24 of itself: 0.06 radians at position 10^6.
 // theta_i is kept as turns in units of 2^-64, rounded, so that the product modulo 2^64 is the fraction of
-// a turn, off by position * 2^-65 at most; its upper 32 bits go to sincospif.
+// a turn, off by position * 2^-65 at most; what it has beyond the nearest quarter goes to sincospif.
 //
 // Bound by memory: 8192 tokens of 32 heads of 128 with as many key heads (bf16, norm and rotation) take 45 us forward
 // (0.27 GB, 6.0 TB/s) and 79 us backward (0.40 GB, 5.1 TB/s, with the gains' sums).  Each element is read once and
@@ -269,12 +269,15 @@ __device__ __forceinline__ void angles(const QkArgs &a, int64_t token, float *co
     const uint64_t position = static_cast<uint64_t>(a.position[token]);
     for (int f = threadIdx.x & 31; f < a.rot / 2; f += 32) {
         const uint64_t turn = position * a.turns[f];
-        // half turns in [-1, 1)
-        const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+        // The nearest quarter, and the rest of at most an eighth of a turn: rounded to 24 bits, the rest is off by 2^-28
+        // of a turn, where half turns from -1 to 1 would be by 2^-26 (an error of the sine of 1.6 steps of 2^-24).
+        const uint32_t quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+        const int32_t rest = static_cast<int32_t>((turn - (static_cast<uint64_t>(quarter) << 62)) >> 30);
+        const float ac = (quarter + 1u) & 2u ? -a.amplitude : a.amplitude, as = quarter & 2u ? -a.amplitude : a.amplitude;
         float s, c;
-        sincospif(half, &s, &c);
-        cosines[f] = a.amplitude * c;
-        sines[f] = a.amplitude * s;
+        sincospif(static_cast<float>(rest) * 0x1p-33f, &s, &c);
+        cosines[f] = ac * (quarter & 1u ? s : c);
+        sines[f] = as * (quarter & 1u ? c : s);
     }
 }
 
