@@ -515,6 +515,8 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
 }
 
 // ---- softmax: four warps per stream ------------------------------------------------------------
+// Loads and stores of tensor memory are instructions of whole warps: where lanes may have taken different ways before one (a wait,
+// lanes without a row or a component, a vote, which brings the warps together but not their lanes), a __syncwarp stands before it.
 // Code that runs once per unit or less is kept short, in loops: a line of instructions that is not in
 // the cache costs about as much as eight of them that are.
 template <int NB, int BLK, bool WIDE>
@@ -758,6 +760,7 @@ struct Narrow : Stream<NB, BLK, false> {
 #pragma unroll 1
         for (int c = 0; c < width; c += 16) {
             uint32_t x[16];
+            __syncwarp();
             ptx::tmem_ld_32x32b_x16(scores + c, x);
             ptx::tmem_ld_wait(x);
             float top = 0.0f;  // lane j's: of row c + j
@@ -784,6 +787,7 @@ struct Narrow : Stream<NB, BLK, false> {
             ptx::st_shared_u32(p + P_FACTOR + static_cast<uint32_t>(key) * 4u, __float_as_uint(was == now ? 1.0f : ptx::ex2_approx(was - now)));
         }
         const bool fresh = vote(none);
+        __syncwarp();
         if (more) {
             if (NB > 1) {
                 const uint32_t rows8 = p + P_FACTOR + static_cast<uint32_t>(lane & ((1 << line_bits(width)) - 1)) * 32u;
@@ -816,7 +820,9 @@ struct Narrow : Stream<NB, BLK, false> {
 
     __device__ bool own_product(uint32_t pos, int at, int len, uint64_t sees, int width, bool first) {
         const bool odd = odd_values(pos, at, len);
-        if (!vote(odd && sees != ~0ull)) return false;
+        const bool own = vote(odd && sees != ~0ull);
+        __syncwarp();
+        if (!own) return false;
         // -0 marks a weight that is none
         const uint32_t line = p + static_cast<uint32_t>(key) * 128u;
         for (int r = 0; r < width; ++r)
@@ -825,6 +831,7 @@ struct Narrow : Stream<NB, BLK, false> {
                              "h"(static_cast<uint16_t>(0x8000))
                              : "memory");
         vote(false);
+        __syncwarp();
 #pragma unroll 1
         for (int nb = 0; nb < NB; ++nb) {
             const int e = key;  // component nb * 128 + key: this thread's TMEM lane
@@ -913,6 +920,7 @@ struct Narrow : Stream<NB, BLK, false> {
 #pragma unroll 1
                 for (int c = 0; c < width; c += 16) {
                     uint32_t x[16];
+                    __syncwarp();
                     ptx::tmem_ld_32x32b_x16(out + (L_COLUMN - O_COLUMN) + c, x);
                     ptx::tmem_ld_wait(x);
                     if (lane == 0)
@@ -1043,7 +1051,9 @@ struct Wide : Stream<NB, BLK, true> {
 
     // The product of a tile with values that are not finite, from the weights as they were rounded.
     __device__ bool product(const Job &u, uint32_t pos, int at, bool first) {
-        if (!vote(odd_values(pos, at + key, u.s.len))) return false;
+        const bool own = vote(odd_values(pos, at + key, u.s.len));
+        __syncwarp();
+        if (!own) return false;
 #pragma unroll 1
         for (int c = 0; c < a.d; c += 16) {
             const uint32_t v0 = v_slot(pos + (c >> 7)) + static_cast<uint32_t>((c >> 6) & 1) * BLOCK_BYTES;
@@ -1204,6 +1214,7 @@ __device__ void narrow_role(const Block<NB, BLK, false> &B, uint32_t tmem, int s
             ptx::st_shared_u32(st.p + P_ROW + static_cast<uint32_t>(key) * 4u, static_cast<uint32_t>(to));
         }
         st.vote(false);
+        __syncwarp();
         float *part = a.part + piece * a.d;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (static_cast<int64_t>(u.s.q0) * a.heads + u.head * a.group) * a.d;
         const uint32_t lanes = static_cast<uint32_t>(32 * st.warp) << 16;
@@ -1295,6 +1306,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
             }
         }
         if (tiles > 0) st.wait_out();
+        __syncwarp();
         // the row's reference and sum, to both streams (in place of scores)
         {
             uint32_t ml[8] = {__float_as_uint(st.m), __float_as_uint((st.l[0].x + st.l[0].y) + (st.l[1].x + st.l[1].y))};
@@ -1313,6 +1325,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
         // streams that shared the tiles out are added up; each writes half of the components
         const bool two = NB == 1 && n > 1;
         uint32_t ml0[8], ml1[8];
+        __syncwarp();
         ptx::tmem_ld_32x32b_x8(st.tmem, ml0);
         if (two) ptx::tmem_ld_32x32b_x8(st.tmem + 128, ml1);
         ptx::tmem_ld_wait(ml0);
@@ -1335,6 +1348,7 @@ __device__ void wide_role(const Block<NB, BLK, true> &B, uint32_t tmem, int s) {
             const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a row that sees nothing: zeros
             f0 *= inv, f1 *= inv;
         }
+        __syncwarp();  // (lanes without a row)
         constexpr int HALF = 32 * BLK * NB;
         const uint32_t outs = st.tmem + O_COLUMN;
 #pragma unroll 1
