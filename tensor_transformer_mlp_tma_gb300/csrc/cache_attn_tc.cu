@@ -90,6 +90,11 @@ struct alignas(16) Job {
 constexpr int JOBS = 3;
 constexpr int JOB_READERS = 11;  // warps: the streams' eight, products, copies of K and of V
 
+// Slots of a ring that have been copied to (a bit each), and the phase of the last copy into each.
+struct Copied {
+    uint32_t slots, phases;
+};
+
 struct Small {
     Job job[JOBS];
     uint64_t job_full[JOBS], job_empty[JOBS];
@@ -101,6 +106,7 @@ struct Small {
     uint32_t tmem;
     int skip[2];           // the weights' product has been done by the stream itself
     alignas(16) uint32_t ones[96];  // in bf16: 128 x 16 of them, whose groups of 8 x 8 (128 bytes) begin 16 bytes apart
+    Copied copied[2];      // K's and V's, when their roles have ended
     volatile int abort;
 };
 static_assert(sizeof(Small) <= SMALL_BYTES && offsetof(Small, ref) % 16 == 0, "small arrays");
@@ -126,7 +132,7 @@ struct Block {
         sh->abort = 1;
         return false;
     }
-    // For copies and products under way when a wait has run out: 0.1 s at least, whatever the limit of waits.
+    // For copies and products under way after a wait has run out: 0.1 s at least, whatever the limit of waits.
     __device__ uint64_t drain_ns() const { return a.wait_ns > 100000000ull ? a.wait_ns : 100000000ull; }
     // `wait` for a whole warp.
     __device__ bool warp_wait(uint32_t bar, uint32_t parity) const {
@@ -236,7 +242,7 @@ __device__ void copy_role(const Block<NB, BLK, WIDE> &B, bool values, const CUte
     const uint32_t ring = B.ring + static_cast<uint32_t>(first) * S::SLOT;
     const uint32_t full0 = B.bar(B.sh->full[first]), empty0 = B.bar(B.sh->empty[first]);
     Place at;
-    uint32_t copied = 0, phases = 0;  // per slot: whether it has been copied to, and in which phase last
+    Copied copied = {0, 0};
     bool ok = true;
     Jobs<NB, BLK, WIDE> jobs = {B, {}};
     Job job = {};
@@ -308,18 +314,22 @@ __device__ void copy_role(const Block<NB, BLK, WIDE> &B, bool values, const CUte
                         }
                 }
             }
-            copied |= 1u << at.slot;
-            phases = (phases & ~(1u << at.slot)) | at.phase << at.slot;
+            copied.slots |= 1u << at.slot;
+            copied.phases = (copied.phases & ~(1u << at.slot)) | at.phase << at.slot;
             at.next(slots);
         }
         if (!ok) break;
     }
-    if (!ok) {
-        if (lane == 0) report(a, STATUS_TIMEOUT, 1);
-        // copies in flight land before anything goes on
-        for (int i = 0; i < slots; ++i)
-            if (copied >> i & 1u) ptx::mbar_wait(full0 + 8 * i, phases >> i & 1u, B.drain_ns(), nullptr);
+    if (lane == 0) {
+        B.sh->copied[values] = copied;
+        if (!ok) report(a, STATUS_TIMEOUT, 1);
     }
+}
+// After a timeout: copies in flight land.  (Functions of their own: inlined they cost the drafts 1 us of 60.)
+__device__ __noinline__ void drain_copies(uint32_t full0, Copied copied, uint64_t limit_ns) {
+#pragma unroll 1
+    for (int i = 0; copied.slots >> i != 0; ++i)
+        if (copied.slots >> i & 1u) ptx::mbar_wait(full0 + 8 * i, copied.phases >> i & 1u, limit_ns, nullptr);
 }
 
 // ---- products: one warp --------------------------------------------------------------------------
@@ -506,11 +516,13 @@ __device__ void product_role(const Block<NB, BLK, WIDE> &B, uint32_t tmem) {
             }
         }
     }
-    if (!ok && leader) {
-        report(a, STATUS_TIMEOUT, 2);
-        // products in flight end before shared and tensor memory are given back
-        ptx::umma_commit(B.bar(sh->drain));
-        ptx::mbar_wait(B.bar(sh->drain), 0, B.drain_ns(), nullptr);
+    if (!ok && leader) report(a, STATUS_TIMEOUT, 2);
+}
+// After a timeout: products in flight end.  (By the lane that issued them: elect_one's is always the same.)
+__device__ __noinline__ void drain_products(uint32_t drain, uint64_t limit_ns) {
+    if (ptx::elect_one()) {
+        ptx::umma_commit(drain);
+        ptx::mbar_wait(drain, 0, limit_ns, nullptr);
     }
 }
 
@@ -1454,13 +1466,20 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
+    if (sh->abort) {
+        // A wait has run out.  A role that was done before that, its copies or products still under way, does not know of it:
+        // only here have all roles ended.  What is in flight ends before shared and tensor memory are given back.
+        if (warp == 8) drain_products(B.bar(sh->drain), B.drain_ns());
+        if (warp == 9 || warp == 10) drain_copies(B.bar(sh->full[warp == 10 ? S::K_SLOTS : 0]), sh->copied[warp == 10], B.drain_ns());
+        if (threadIdx.x == 0) {
+            report(a, STATUS_TIMEOUT, 3);
+            post_cut(a, 0, 0, 0, 0, 0);
+        }
+        __syncthreads();
+    }
     if (warp == 8) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TMEM);
-    }
-    if (sh->abort && threadIdx.x == 0) {
-        report(a, STATUS_TIMEOUT, 3);
-        post_cut(a, 0, 0, 0, 0, 0);
     }
 }
 
