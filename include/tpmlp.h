@@ -491,8 +491,9 @@ typedef struct {
 /* Appends T tokens: K normed and rotated as by tpmlp_qk_forward, and V as it is, go to row slot % page_size of page
  * slot / page_size, Q normed and rotated to Qr (which may be Q).  slot[T] (int64, device): a negative one is of a
  * token that is not kept (padding); one that is pages * page_size or more is reported as
- * TPMLP_ERR_INVALID_ARG in the status word (detail: the token) and not kept.  Slots that are kept have to differ: of
- * two tokens with the same slot, each head's row is one's or the other's.  All other rows of the cache stay as they are.
+ * TPMLP_ERR_INVALID_ARG in the status word (detail: the token) and not kept.  Slots that are kept have to differ: where
+ * two tokens have the same one, each element of its rows is one token's or the other's, and a row may be a mixture.  All
+ * other rows of the cache stay as they are.
  * Errors as tpmlp_qk_forward; INVALID_ARG also where heads, dim or type of shape and cache differ. */
 tpmlp_status tpmlp_kv_append(const tpmlp_qk_shape *shape, const tpmlp_kv_cache *cache, const tpmlp_heads *Q,
                              const tpmlp_heads *K, const tpmlp_heads *V, const void *gain_q, const void *gain_k,

@@ -850,8 +850,8 @@ class KvCache:
 
 
 def kv_append(ctx: QkContext, cache: KvCache, QKV, position, slot, gain_q=None, gain_k=None, out=None, stream=None):
-    """Puts the tokens' keys (normed, rotated) and values at slot [tokens] (int64: page * page_size + row; negative: not
-    kept) of the cache, and returns their queries, normed and rotated, [tokens, heads, dim] (`out`, where given)."""
+    """Puts the tokens' keys (normed, rotated) and values at slot [tokens] (int64: page * page_size + row, each
+    once; negative: not kept) of the cache, and returns their queries, normed and rotated, [tokens, heads, dim] (`out`, where given)."""
     _qkv_input(ctx, QKV, True)
     given = _qk_inputs(ctx, position, gain_q, gain_k)
     _need(slot, "slot", torch.int64, (ctx._tokens,))
