@@ -513,7 +513,7 @@ tpmlp_status tpmlp_kv_append(const tpmlp_qk_shape *shape, const tpmlp_kv_cache *
  * visible scores are that is zero too.
  * Rows of O behind q_start[batch] stay as they are. */
 typedef struct {
-    int64_t tokens;     /* T >= 0; tokens * heads < 2^31 */
+    int64_t tokens;     /* T >= 0; (tokens + 1) * heads < 2^31 - 1024 */
     int64_t batch;      /* sequences, 0..2^20 */
     int64_t max_pages;  /* row length of page_table, max_pages * page_size < 2^31 - 1024 */
     int32_t heads;      /* a multiple of the cache's kv_heads */

@@ -2010,7 +2010,8 @@ struct QkCall {
 bool cache_attn_valid(const tpmlp_cache_attn_shape *s, const tpmlp_kv_cache *c) {
     if (!s || !cache_valid(c) || s->tokens < 0 || s->batch < 0 || s->batch > (1LL << 20) || s->max_pages < 0) return false;
     if (s->heads < 1 || s->heads % c->kv_heads != 0) return false;
-    if (s->tokens > (1LL << 31) - 1 || s->tokens * s->heads >= (1LL << 31)) return false;
+    // (the kernels count rows in 32 bits, rounded up to whole tiles and whole tokens)
+    if (s->tokens > (1LL << 31) - 1 || (s->tokens + 1) * s->heads >= (1LL << 31) - 1024) return false;
     if (s->max_pages > (1LL << 31) || s->max_pages * c->page_size >= (1LL << 31) - 1024) return false;
     if (s->algo != TPMLP_ALGO_DEFAULT && s->algo != TPMLP_ALGO_SIMT) return false;
     // (the kernels multiply by scale log2(e))
