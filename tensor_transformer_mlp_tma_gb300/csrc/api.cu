@@ -1998,9 +1998,8 @@ struct QkCall {
                (s->rot > 0 && (meets_buffer(o, a.position, 8 * s->tokens) || meets_buffer(o, a.turns, 4 * s->rot)));
     }
     template <typename F>
-    tpmlp_status launch(const char *name, void *stream, F f) const {
-        int sms;
-        const tpmlp_status rc = device_ready(sms);
+    tpmlp_status launch(const char *name, void *stream, F f) {
+        const tpmlp_status rc = device_ready(a.sms);
         if (rc != TPMLP_OK) return rc;
         Timed timed(name, static_cast<cudaStream_t>(stream));
         return from_cuda(f(static_cast<cudaStream_t>(stream)));

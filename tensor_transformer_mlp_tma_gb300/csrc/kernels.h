@@ -309,6 +309,7 @@ struct HeadRows {
     int64_t row, shard;
 };
 struct QkArgs {
+    int sms;           // of the device
     int64_t tokens;
     int heads, kv_heads, t, d;
     int rot;           // components that rotate

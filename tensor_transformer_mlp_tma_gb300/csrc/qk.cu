@@ -662,8 +662,8 @@ __global__ void __launch_bounds__(32 * GAIN_ROWS) gain_kernel(const QkArgs a, in
     }
 }
 
-// Blocks of the backward pass: two per SM of the 152, and no more than there is work for.
-constexpr int BACKWARD_BLOCKS = 304;
+// Blocks of the backward pass: two per SM, and no more than there is work for; at most as many as the workspace has room for.
+constexpr int MOST_BACKWARD_BLOCKS = 304;
 
 template <typename F>
 cudaError_t dispatch(bool is_bf16, const QkArgs &a, F f) {
@@ -714,7 +714,7 @@ Split split_of(const QkArgs &a, int pairs, int rows, int warps) {
     w.lanes = 1;
     while (w.lanes * 2 * pairs < a.d) w.lanes *= 2;
     const int each = 32 / w.lanes;
-    const int64_t steps = (rows + each - 1) / each, want = (152LL * warps + a.tokens - 1) / a.tokens;
+    const int64_t steps = (rows + each - 1) / each, want = (static_cast<int64_t>(a.sms) * warps + a.tokens - 1) / a.tokens;
     w.split = static_cast<int>(want < steps ? want : steps);
     w.q = map_of(a.q, a.heads, a.t, a.d), w.oq = map_of(a.oq, a.heads, a.t, a.d), w.dq = map_of(a.dq, a.heads, a.t, a.d);
     w.k = map_of(a.k, a.kv_heads, a.t, a.d), w.ok = map_of(a.ok, a.kv_heads, a.t, a.d), w.dk = map_of(a.dk, a.kv_heads, a.t, a.d);
@@ -725,7 +725,7 @@ Split split_of(const QkArgs &a, int pairs, int rows, int warps) {
 }  // namespace qk
 
 int64_t qk_partial_floats(int64_t tokens, int d) {
-    return (tokens > 0 ? qk::BACKWARD_BLOCKS : 1) * static_cast<int64_t>(d);
+    return (tokens > 0 ? qk::MOST_BACKWARD_BLOCKS : 1) * static_cast<int64_t>(d);
 }
 
 cudaError_t launch_qk_forward(bool is_bf16, const QkArgs &a, bool append, cudaStream_t st) {
@@ -747,9 +747,10 @@ cudaError_t launch_qk_backward(bool is_bf16, const QkArgs &a, cudaStream_t st, i
         const qk::Split w = qk::split_of(a, Ln::P, a.heads > a.kv_heads ? a.heads : a.kv_heads, 16);
         const int64_t most = (a.tokens * w.split + qk::WARPS - 1) / qk::WARPS;
         // blocks in proportion to the rows
-        int64_t nq = qk::BACKWARD_BLOCKS * static_cast<int64_t>(a.heads) / (a.heads + a.kv_heads);
-        nq = nq < 1 ? 1 : (nq > qk::BACKWARD_BLOCKS - 1 ? qk::BACKWARD_BLOCKS - 1 : nq);
-        int64_t nk = qk::BACKWARD_BLOCKS - nq;
+        const int64_t blocks = 2 * a.sms < qk::MOST_BACKWARD_BLOCKS ? 2 * a.sms : qk::MOST_BACKWARD_BLOCKS;
+        int64_t nq = blocks * a.heads / (a.heads + a.kv_heads);
+        nq = nq < 1 ? 1 : (nq > blocks - 1 ? blocks - 1 : nq);
+        int64_t nk = blocks - nq;
         nq = nq < most ? nq : most;
         nk = nk < most ? nk : most;
         constexpr int smem = Ln::VEC ? 2 * qk::Queue<Ln, qk::BACKWARD_DEPTH>::BYTES : 0;
