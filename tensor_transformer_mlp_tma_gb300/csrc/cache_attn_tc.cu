@@ -21,16 +21,23 @@
 // its own, masks are a row's 32 bits at a time, and the weights go back to tensor memory in place of the
 // scores, as the second product's first operand: shared memory, which the products' operands keep busy,
 // carries half as much as with the weights in it.  4 prompt chunks of 300 to 512 tokens over 3000 to 8192 keys,
-// 64 heads on 8 of 128 components: 352 us, 1.26 PFLOP/s; with the weights in shared memory 622.
+// 64 heads on 8 of 128 components: 352 to 359 us, 1.25 PFLOP/s, in bursts of a few ms, and 380 to 400 (1.15) one after another
+// for longer, when the power limit lowers the clock; with the weights in shared memory 622.
 //
 // In both the weights are 2^(s - m) with a reference m that is only renewed when some score of the tile is
 // above it by more than 2^8: bf16 weights and fp32 sums hold 2^8 as well as 1, and outputs are
 // scaled a few times per row instead of once per tile.
 //
+// The weights are rounded to bf16, because they are operands of a bf16 product whose other one is the cache as it is: at most
+// 2^-8 of each, next to the 2^-8 of the rounded output (against 64 bits an output of the decoding batch is off by 2.3e-3, with
+// weights in fp32 by 1.7e-3).  Two parts per weight would be two products of V instead of one.  Scores, references, sums and
+// outputs are fp32; Narrow's sums are of the rounded weights (one more product), Wide's of the unrounded ones, which it has
+// in registers when it adds them up.
+//
 // Narrow is bound by reading the cache: 64 sequences of one token, 1.19 GB: 185 us, 6.4 TB/s.  Wide is bound by the
 // turns of a stream between its products and its exponentials, of about 1700 cycles each for a tile (the products of
 // both streams' tiles alone are 1060), and at the units' ends by the outputs' way to memory.
-// The kernel's start, until the first scores, is 4 us: one sequence of one token takes 16 us with the join.
+// One sequence of one token over 2048 keys takes 16.4 us with the join, over a single key 9.9.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1536,9 +1543,11 @@ cudaError_t launch_tc(const CacheAttnArgs &a, int blocks, cudaStream_t st) {
 bool cache_attn_tc(const CacheAttnArgs &a) { return a.vec && a.page_size % 8 == 0 && a.d % 8 == 0 && a.d <= 256; }
 
 cudaError_t launch_cache_attn_tc(const CacheAttnArgs &a, int num_sms, cudaStream_t st) {
-    // Rows in lanes from 32 rows per sequence on (the lengths themselves are known on the device only).  Measured with
-    // rows in lanes and in columns: 64 sequences of 4 rows 205 and 185 us, one of 64 rows 94 and 94 us, 16 of 68 to 256
-    // rows 65 and 85 us.
+    // Rows in lanes above 32 rows per sequence (the lengths themselves are known on the device only).  Measured with
+    // rows in lanes and in columns, us: 64 sequences of 128 components over 100 to 8192 keys with 4 rows 196 and 189, 16 rows
+    // 220 and 199, 32 196 and 192, 40 193 and 193, 48 195 and 194, 64 189 and 199; 8 of them with 32 rows 39.3 and 38.5, 40 rows
+    // 42.8 and 43.5, 64 43 and 47; 16 of 68 to 256 rows 65 and 85; one of 131072 keys the same within 1% from 8 to 64 rows.
+    // The border moves with the components: with 64 of them 32 rows 141 and 150, with 256 of them 48 rows 451 and 401.
     const bool wide = a.tokens * a.group > 32 * a.batch;
     if (a.d <= 64) return wide ? cattn::launch_tc<1, 1, true>(a, num_sms, st) : cattn::launch_tc<1, 1, false>(a, num_sms, st);
     if (a.d <= 128) return wide ? cattn::launch_tc<1, 2, true>(a, num_sms, st) : cattn::launch_tc<1, 2, false>(a, num_sms, st);

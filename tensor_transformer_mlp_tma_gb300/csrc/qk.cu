@@ -11,7 +11,7 @@
 // a turn, off by position * 2^-65 at most; what it has beyond the nearest quarter goes to sincospif.
 //
 // Bound by memory: 8192 tokens of 32 heads of 128 with as many key heads (bf16, norm and rotation) take 45 us forward
-// (0.27 GB, 6.0 TB/s) and 79 us backward (0.40 GB, 5.1 TB/s, with the gains' sums).  Each element is read once and
+// (0.27 GB, 5.9 TB/s) and 80 us backward (0.40 GB, 5.1 TB/s, with the gains' sums); fp32 86 us (6.3 TB/s) and 142 (5.7).  Each element is read once and
 // written once.  A warp takes a token: its angles' factors stay in registers over the token's heads, and a head
 // is held by d / 16 (bf16) or d / 8 (fp32) lanes, sixteen bytes of first members and sixteen of second members of the
 // pairs each, so that the rotation needs no exchange and the norm a few shuffles.  Rows come by a queue of
@@ -668,8 +668,9 @@ constexpr int MOST_BACKWARD_BLOCKS = 304;
 template <typename F>
 cudaError_t dispatch(bool is_bf16, const QkArgs &a, F f) {
     // Sixteen-byte pieces of first and second members (bf16: 8 elements), eight-byte ones, or elements.
-    // Forward, 8192 tokens of 32 + 32 heads of 128: 45 us with the first, 57 with the second (120 of 128 rotate), 122
-    // element by element (116 rotate).
+    // 8192 tokens of 32 + 32 heads of 128 in bf16, forward and backward: 45 and 80 us with the first, 56 and 104 with the second
+    // (120 of 128 rotate), 123 and 212 element by element (116 rotate; rows on 2 bytes 123 and 256).  fp32: 86 and 142 us
+    // with sixteen-byte pieces, 139 and 227 element by element.
     auto fits = [&](int p) { return a.vec && a.d % (2 * p) == 0 && a.rot % (a.interleaved ? p : 2 * p) == 0; };
     if (is_bf16) {
         if (fits(8)) return f(Lanes<__nv_bfloat16, 8, true>());
