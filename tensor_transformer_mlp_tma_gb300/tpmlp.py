@@ -772,10 +772,9 @@ def qk_forward(ctx: QkContext, QKV, position, gain_q=None, gain_k=None, out=None
 def _written_over(ctx, *outputs):
     """An output in the place of the saved Q or K, which a backward pass with the norm reads: there is no other one."""
     if ctx._saved and ctx._norm and ctx._tokens:
-        for r, saved in zip(outputs, ctx._saved[1:3]):
-            if r.p == saved[0]:
-                ctx._saved = ()
-                return
+        q, k = ctx._saved[1][0], ctx._saved[2][0]
+        if any(r.p == q or r.p == k for r in outputs):
+            ctx._saved = ()
 
 
 def qk_backward(ctx: QkContext, dQr, dKr, out=None, dgain_q=None, dgain_k=None, stream=None):

@@ -76,6 +76,16 @@ def test_queries_of_an_append_over_the_saved_ones(tp):
         tp.qk_backward(ctx, dQ, dK)
 
 
+def test_queries_of_another_append_over_the_saved_keys(tp):
+    QKV, gq, gk, pos, dQ, dK = make(T, KV, KV, D, torch.bfloat16, 22)
+    ctx = tp.QkContext(T, KV, KV, D, torch.bfloat16, tp.RopeTable(D))
+    tp.qk_forward(ctx, QKV, pos, gq, gk)
+    cache = tp.KvCache(4, 16, KV, D, torch.bfloat16)
+    tp.kv_append(ctx, cache, QKV.clone(), pos, torch.arange(T, device="cuda"), gq, gk, out=QKV[:, KV * D:2 * KV * D].view(T, KV, D))
+    with pytest.raises(ValueError, match="gone"):
+        tp.qk_backward(ctx, dQ, dK)
+
+
 def test_a_refused_forward_pass(tp):
     ctx, QKV, pos, gq, gk, dQ, dK = forward(tp, torch.bfloat16)
     with pytest.raises(ValueError):
