@@ -2067,8 +2067,9 @@ tpmlp_status tpmlp_rope_turns(const tpmlp_rope *r, uint64_t *turns) {
         Twofold f = tpmlp::exp_of(log_base * Twofold{-2.0 * i, 0.0} / Twofold{static_cast<double>(r->rot), 0.0});
         if (linear) f = f / factor;
         if (parts) {
-            const Twofold low = {r->low, 0.0}, n = Twofold{static_cast<double>(r->context), 0.0} * f / two_pi;
-            Twofold k = (n + -low) / (Twofold{r->high, 0.0} + -low);
+            // (halves, so that high - low is finite)
+            const Twofold low = {0.5 * r->low, 0.0}, n = Twofold{0.5 * static_cast<double>(r->context), 0.0} * f / two_pi;
+            Twofold k = (n + -low) / (Twofold{0.5 * r->high, 0.0} + -low);
             k = k < Twofold{0.0, 0.0} ? Twofold{0.0, 0.0} : (one < k ? one : k);
             f = f * (k + (one + -k) / factor);
         }
