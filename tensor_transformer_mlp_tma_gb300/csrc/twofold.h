@@ -48,10 +48,10 @@ inline Twofold exp_of(Twofold x) {
     for (int i = 0; i < 20; ++i) sum = sum * sum;
     return sum;
 }
-// The double's logarithm and one step of Newton's method: x e^-y = 1 + d.
+// The double's logarithm and one step of Newton's method: x e^-y = 1 + d (in two halves, so that e^-y does not underflow).
 inline Twofold log_of(double x) {
     const double y = std::log(x);
-    const Twofold d = Twofold{x, 0.0} * exp_of({-y, 0.0}) + Twofold{-1.0, 0.0};
+    const Twofold half = exp_of({-0.5 * y, 0.0}), d = Twofold{x, 0.0} * half * half + Twofold{-1.0, 0.0};
     return Twofold{y, 0.0} + d;
 }
 // pi: the sine of its leading part is what is missing, up to the cube of that.

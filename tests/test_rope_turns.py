@@ -48,7 +48,7 @@ def turns_of(base, rot, scaling=None):
 
 
 @pytest.mark.parametrize("rot", [2, 48, 64, 96, 128, 256])
-@pytest.mark.parametrize("base", [1.0, 1.0 + 2.0 ** -30, 1.5, 10000.0, 500000.0, 1e300])
+@pytest.mark.parametrize("base", [1.0, 1.0 + 2.0 ** -30, 1.5, 10000.0, 500000.0, 1e300, 1.7e308])
 @pytest.mark.parametrize("scaling", [None, ("linear", 3.7), ("parts", 8.0, 2048, 1.0, 32.0), ("parts", 40.0, 4096, 0.3, 17.1),
                                      ("parts", 4.0, 1 << 40, -1.7e308, 1.7e308), ("parts", 4.0, 1, 5.0, 5.0 + 2.0 ** -50)])
 def test_turns(tp, base, rot, scaling):
